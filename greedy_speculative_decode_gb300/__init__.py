@@ -17,6 +17,8 @@ SV_LIN_O, SV_LIN_GATE_UP, SV_LIN_DOWN, SV_LIN_LM_HEAD = 1, 2, 3, 4
 PAGE_SIZE = 16
 MAX_K = 32
 MAX_PREFILL_ROWS = 128
+SV_KV_BF16, SV_KV_E4M3 = 0, 1
+ATTEND_MAX_SEQ = 1024
 _ERRNAMES = {SV_E_INVAL: "SV_E_INVAL", SV_E_NOMEM: "SV_E_NOMEM", SV_E_CUDA: "SV_E_CUDA",
              SV_E_STATE: "SV_E_STATE"}
 
@@ -38,6 +40,16 @@ LAYER_KEYS = ("attn_norm", "wqkv", "q_norm", "k_norm", "wo", "ffn_norm", "w_gate
 
 class SvWeights(ctypes.Structure):
     _fields_ = [("embed", _P), ("lm_head", _P), ("final_norm", _P)] + [(k, _PP) for k in LAYER_KEYS]
+
+
+class SvKvPool(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("format", "n_pages", "n_kv_heads", "head_dim", "scale_block")] + [
+        (n, _P) for n in ("k", "v", "k_exp", "v_exp")]
+
+
+class SvRowBatch(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("n_seq", "n_rows", "max_rows", "table_stride")] + [
+        (n, _P) for n in ("block_table", "first", "row_start")]
 
 
 class SvError(RuntimeError):
@@ -70,12 +82,17 @@ def _load():
     L.sv_time_linear.argtypes = [_P, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_float),
                                  ctypes.POINTER(ctypes.c_double)]
     L.sv_lm_head_noalloc.argtypes = [_P, _P, _P, _i32, _i32, _i32, ctypes.c_float, _P, _P, _P, _P]
+    i64 = ctypes.c_int64
+    L.sv_kv_write.argtypes = L.sv_kv_fetch.argtypes = [_P, _P, _P, i64, _P, i64, _P, _P]
+    L.sv_attend_workspace.argtypes = [_P, _P, _i32, ctypes.POINTER(i64)]
+    L.sv_attend.argtypes = [_P, _P, _i32, _P, i64, _P, i64, _P, _i32, _i32, ctypes.c_float, _P, i64, _P, _P]
     L.sv_last_error.argtypes = [_P]
     L.sv_last_error.restype = ctypes.c_char_p
     for name in ("sv_create", "sv_prefill", "sv_decode", "sv_verify", "sv_verify_async",
                  "sv_reserve", "sv_sync", "sv_truncate", "sv_seq_len", "sv_kv_read",
                  "sv_shuffle_pages", "sv_trace_hidden", "sv_step_kernel_count", "sv_time_linear",
-                 "sv_lm_head_noalloc", "sv_prefill_blocks"):
+                 "sv_lm_head_noalloc", "sv_prefill_blocks", "sv_kv_write", "sv_kv_fetch",
+                 "sv_attend_workspace", "sv_attend"):
         getattr(L, name).restype = _i32
     return L
 
@@ -154,6 +171,204 @@ def lm_head_noalloc(x, gain, w, logits, argmax=None, status=None, eps=1e-6, stre
     if rc != SV_OK:
         raise SvError(rc, "sv_lm_head_noalloc rejected the shapes (scratch limit 8 MiB, "
                           "1 <= M <= 32, hidden % 128 == 0) or a CUDA call failed")
+
+
+class PagedKv:
+    """A paged K/V cache of the caller's tensors (sv_kv_pool in include/sv.h).
+
+    k, v: codes [n_pages, n_kv_heads, 16, head_dim], bf16, or uint8 holding
+    e4m3 codes; then k_exp, v_exp: uint8 exponent bytes [n_pages, n_kv_heads,
+    16 / scale_block], scale_block 1 or 16. All contiguous on one CUDA device,
+    kept alive by this object. PagedKv.empty allocates them."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        if getattr(k, "dim", lambda: 0)() != 4:
+            raise ValueError("k: must be a 4-D tensor [n_pages, n_kv_heads, 16, head_dim]")
+        n_pages, n_kv, page, d = (int(x) for x in k.shape)
+        if page != PAGE_SIZE or d not in (64, 128, 256) or n_pages < 1 or n_kv < 1:
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected [n_pages, n_kv_heads, 16, 64 | 128 | 256]")
+        kind = str(k.dtype)
+        if kind not in ("torch.bfloat16", "torch.uint8"):
+            raise ValueError(f"k: dtype {k.dtype}, expected torch.bfloat16 or torch.uint8 (e4m3 codes)")
+        self.format = SV_KV_BF16 if kind == "torch.bfloat16" else SV_KV_E4M3
+        _check_tensor(k, "k", kind, k.shape)
+        _check_tensor(v, "v", kind, k.shape)
+        self.scale_block = 1
+        if self.format == SV_KV_E4M3:
+            if k_exp is None or v_exp is None:
+                raise ValueError("an 8-bit cache needs k_exp and v_exp")
+            per = int(k_exp.shape[-1]) if k_exp.dim() == 3 else 0
+            if per not in (1, PAGE_SIZE):
+                raise ValueError(f"k_exp: shape {tuple(k_exp.shape)}, expected [n_pages, n_kv_heads, 16 or 1]")
+            self.scale_block = PAGE_SIZE // per
+            _check_tensor(k_exp, "k_exp", "torch.uint8", (n_pages, n_kv, per))
+            _check_tensor(v_exp, "v_exp", "torch.uint8", (n_pages, n_kv, per))
+        elif k_exp is not None or v_exp is not None:
+            raise ValueError("a bf16 cache takes no exponents")
+        self.tensors = tuple(t for t in (k, v, k_exp, v_exp) if t is not None)
+        for t in self.tensors:
+            if t.device != k.device:
+                raise ValueError("the cache's tensors lie on different devices")
+            if t.data_ptr() % 16:
+                raise ValueError("the cache's tensors must be aligned to 16 bytes")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, d, k.device
+        self._c = SvKvPool(self.format, n_pages, n_kv, d, self.scale_block, _ptr(k), _ptr(v), _ptr(k_exp),
+                           _ptr(v_exp))
+        self._p = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, *, fmt: str = "e4m3", scale_block: int = 1,
+              device="cuda"):
+        """A zeroed cache; fmt "e4m3" or "bf16"."""
+        import torch
+        if fmt not in ("e4m3", "bf16"):
+            raise ValueError(f"fmt {fmt!r}, expected 'e4m3' or 'bf16'")
+        if scale_block not in (1, PAGE_SIZE):
+            raise ValueError(f"scale_block {scale_block}, expected 1 or 16")
+        shape = (n_pages, n_kv_heads, PAGE_SIZE, head_dim)
+        if fmt == "bf16":
+            return cls(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        return cls(*(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.zeros((n_pages, n_kv_heads, PAGE_SIZE // scale_block), dtype=torch.uint8, device=device)
+                     for _ in range(2)))
+
+
+class RowBatch:
+    """The rows of a call on a PagedKv (sv_row_batch in include/sv.h).
+
+    block_table: int32 [n_seq, pages]; first: int32 [n_seq], the position of
+    each sequence's first row; n_rows: rows of the call's buffers; row_start:
+    int32 [n_seq + 1], or None for n_rows / n_seq rows each; max_rows: the most
+    rows of a sequence, where known (only speed depends on it). The tensors
+    are read when the kernels run, so a program may change their contents
+    between calls (and replays of a captured graph)."""
+
+    def __init__(self, block_table, first, n_rows: int, *, row_start=None, max_rows: int = 0):
+        if getattr(block_table, "dim", lambda: 0)() != 2 or min(block_table.shape) < 1:
+            raise ValueError("block_table: must be a 2-D tensor [n_seq, pages]")
+        n_seq, pages = (int(x) for x in block_table.shape)
+        _check_tensor(block_table, "block_table", "torch.int32", (n_seq, pages))
+        _check_tensor(first, "first", "torch.int32", (n_seq,))
+        _check_tensor(row_start, "row_start", "torch.int32", (n_seq + 1,))
+        if n_rows < 1 or (row_start is None and n_rows % n_seq):
+            raise ValueError(f"n_rows {n_rows}: must be positive, and a multiple of {n_seq} without row_start")
+        if max_rows < 0:
+            raise ValueError(f"max_rows {max_rows}: must not be negative")
+        if first.device != block_table.device or (row_start is not None and row_start.device != first.device):
+            raise ValueError("the batch's tensors lie on different devices")
+        self.n_seq, self.n_rows, self.device = n_seq, int(n_rows), block_table.device
+        self.tensors = (block_table, first, row_start)
+        self._c = SvRowBatch(n_seq, int(n_rows), int(max_rows), pages, _ptr(block_table), _ptr(first),
+                             _ptr(row_start))
+        self._p = ctypes.byref(self._c)
+
+
+def _check_rows(t, name, cache, n_rows, heads):
+    """Rows of heads side by side: [n_rows, heads, head_dim] bf16 whose rows may
+    lie apart (a slice of a fused projection). Returns the row stride."""
+    d = cache.head_dim
+    if t.device != cache.device:
+        raise ValueError(f"{name}: on {t.device}, the cache on {cache.device}")
+    if str(t.dtype) != "torch.bfloat16":
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.shape != (n_rows, heads, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n_rows, heads, d)}")
+    row, head, one = t.stride()
+    if n_rows == 1:  # a lone row's stride says nothing
+        row = heads * d
+    if one != 1 or (head != d and heads > 1) or row < heads * d or row % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: needs heads side by side in rows a multiple of 8 elements apart, 16-byte "
+                         f"aligned; strides {t.stride()}")
+    return row
+
+
+def _run_on(cache, rows, stream, status, call):
+    """call(stream handle) on the cache's device; None: torch's current stream there."""
+    import torch
+    if rows.device != cache.device:
+        raise ValueError(f"the rows' tables lie on {rows.device}, the cache on {cache.device}")
+    if status is not None:
+        _check_tensor(status, "status", "torch.int32", (1,))
+        if status.device != cache.device:
+            raise ValueError(f"status: on {status.device}, the cache on {cache.device}")
+    index = cache.device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _run_on(cache, rows, stream, None, call)
+    s = torch.cuda.current_stream() if stream is None else stream
+    rc = call(_P(s.cuda_stream))
+    if rc != SV_OK:
+        raise SvError(rc, "rejected the arguments or a CUDA call failed")
+
+
+def kv_write(cache: PagedKv, rows: RowBatch, k, v, *, status=None, stream=None):
+    """sv_kv_write: put the rows' K and V (bf16 [n_rows, n_kv_heads, head_dim],
+    rows may lie apart) into the cache. status: int32 [1], failure bits are
+    ORed into it. stream: None for torch's current one. Asynchronous."""
+    ks = _check_rows(k, "k", cache, rows.n_rows, cache.n_kv_heads)
+    vs = _check_rows(v, "v", cache, rows.n_rows, cache.n_kv_heads)
+    _run_on(cache, rows, stream, status, lambda s: _lib.sv_kv_write(
+        cache._p, rows._p, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(status), s))
+
+
+def kv_fetch(cache: PagedKv, rows: RowBatch, k_out, v_out, *, status=None, stream=None):
+    """sv_kv_fetch: K and V of the rows' positions, as bf16, into k_out, v_out
+    ([n_rows, n_kv_heads, head_dim]). Asynchronous."""
+    ks = _check_rows(k_out, "k_out", cache, rows.n_rows, cache.n_kv_heads)
+    vs = _check_rows(v_out, "v_out", cache, rows.n_rows, cache.n_kv_heads)
+    _run_on(cache, rows, stream, status, lambda s: _lib.sv_kv_fetch(
+        cache._p, rows._p, k_out.data_ptr(), ks, v_out.data_ptr(), vs, _ptr(status), s))
+
+
+def attend_workspace(cache: PagedKv, rows: RowBatch, n_q_heads: int) -> int:
+    """sv_attend_workspace: bytes that attend needs besides its arguments."""
+    n = ctypes.c_int64(0)
+    rc = _lib.sv_attend_workspace(cache._p, rows._p, int(n_q_heads), ctypes.byref(n))
+    if rc != SV_OK:
+        raise SvError(rc, f"attend_workspace({n_q_heads} query heads)")
+    return n.value
+
+
+def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: int = 0, scale=None, lse=None,
+           workspace=None, status=None, stream=None):
+    """sv_attend: attention of the rows over the cache. q, out: bf16 [n_rows,
+    n_q_heads, head_dim] (rows may lie apart); the row at position t sees p <=
+    t, or with a window only p > t - window or p < sinks. scale: None for
+    1 / sqrt(head_dim). lse: fp32 [n_rows, n_q_heads] for the log-sum-exp, or
+    None. workspace: uint8 tensor of attend_workspace bytes; None takes one
+    from torch's allocator for this call, on torch's current stream (then
+    `stream`, if given, must be that one). Asynchronous."""
+    if getattr(q, "dim", lambda: 0)() != 3:
+        raise ValueError("q: must be a 3-D tensor [n_rows, n_q_heads, head_dim]")
+    heads = int(q.shape[1])
+    if heads < 1 or heads % cache.n_kv_heads:
+        raise ValueError(f"q: {heads} heads, not a multiple of the cache's {cache.n_kv_heads}")
+    qs = _check_rows(q, "q", cache, rows.n_rows, heads)
+    os_ = _check_rows(out, "out", cache, rows.n_rows, heads)
+    if window < 0 or sinks < 0:
+        raise ValueError(f"window {window}, sinks {sinks}: must not be negative")
+    if rows.n_seq > ATTEND_MAX_SEQ:
+        raise ValueError(f"{rows.n_seq} sequences, at most {ATTEND_MAX_SEQ}")
+    if lse is not None:
+        _check_tensor(lse, "lse", "torch.float32", (rows.n_rows, heads))
+        if lse.device != cache.device:
+            raise ValueError(f"lse: on {lse.device}, the cache on {cache.device}")
+    need = attend_workspace(cache, rows, heads)
+    if workspace is None:
+        import torch
+        if stream is not None and stream != torch.cuda.current_stream(cache.device):
+            raise ValueError("a stream that is not torch's current one needs a workspace of the caller's")
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    else:
+        _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
+        if workspace.device != cache.device:
+            raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    _run_on(cache, rows, stream, status, lambda s: _lib.sv_attend(
+        cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse), int(window), int(sinks),
+        float(scale), workspace.data_ptr(), workspace.numel(), _ptr(status), s))
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):

@@ -1,0 +1,67 @@
+// paged.h -- the paged-cache operators: writing rows into a cache, fetching
+// them back, and attention of rows over it (launch interface).
+#pragma once
+#include "sv_internal.h"
+
+namespace sv {
+
+// A pool of pages: codes [n_pages, n_kv_heads, 16, head_dim] (bf16 or e4m3)
+// and, for e4m3, exponent bytes [n_pages, n_kv_heads, 16 / block].
+struct KvPool {
+  int fmt, n_pages, n_kv_heads, head_dim, block;
+  uint8_t *k, *v, *k_exp, *v_exp;
+  int row_bytes() const { return head_dim * (fmt == SV_KV_BF16 ? 2 : 1); }
+};
+
+// The rows of a call: sequence s brings rows row_start[s] .. row_start[s + 1]
+// - 1 (or, with no row_start, rows_each rows), at positions first[s] onward.
+// Rows at negative positions are padding.
+struct RowBatch {
+  int n_seq, n_rows, rows_each, max_rows, table_stride;
+  const int* table;      // [n_seq, table_stride]
+  const int* first;      // [n_seq]
+  const int* row_start;  // [n_seq + 1] or null
+  __host__ __device__ int limit() const { return table_stride * kPage; }  // positions the table reaches
+};
+
+// Where new rows' K and V come from: dense rows (stride elements apart, heads
+// side by side), or the pages of a bf16 staging pool of src_pages pages in
+// which position p of the (single) sequence lies in page (p / 16) % src_pages.
+struct KvSource {
+  const bf16 *k, *v;
+  int64_t k_stride, v_stride;
+  int src_pages;
+};
+
+cudaError_t launch_kv_write(const KvPool& c, const RowBatch& b, const KvSource& src, int* status, cudaStream_t s,
+                            bool pdl);
+cudaError_t launch_kv_fetch(const KvPool& c, const RowBatch& b, bf16* k, int64_t k_stride, bf16* v,
+                            int64_t v_stride, int* status, cudaStream_t s);
+
+// Most sequences of an attention call: each CTA keeps three words per
+// sequence in shared memory.
+constexpr int kAttendMaxSeq = 1024;
+
+struct AttendParams {
+  RowBatch rows;
+  const bf16* q;  // [n_rows, n_q_heads, head_dim], rows q_stride elements apart
+  bf16* out;
+  int64_t q_stride, out_stride;
+  float* lse;  // [n_rows, n_q_heads] natural-log sum of exponentials, or null
+  const uint8_t *k_exp, *v_exp;
+  int n_q_heads, n_kv_heads, n_pages, block, window, sinks;
+  int page0;         // page of the tensor maps that is page 0 of this pool
+  float scale_log2;  // softmax scale * log2(e)
+  int max_splits;
+  float2* part_ml;  // [n_rows, n_q_heads, max_splits] (running max in log2 units, sum)
+  float* part_o;    // [n_rows, n_q_heads, max_splits, head_dim]
+  int* status;      // or null
+};
+
+// Tensor map of a pool's codes as the attention kernel loads them.
+bool make_kv_map(CUtensorMap* m, const void* codes, int row_bytes, uint64_t rows);
+cudaError_t prepare_attend_kernels();
+cudaError_t launch_attend(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttendParams& p, int fmt,
+                          int head_dim, int num_sms, cudaStream_t s, bool pdl);
+
+}  // namespace sv

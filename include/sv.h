@@ -333,6 +333,99 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
                        int vocab, float eps, float* logits_dev, int32_t* argmax_dev,
                        int32_t* status_dev, void* cuda_stream);
 
+/* ---------------------------------------------------------------- paged caches
+ * Operators on a paged K/V cache of the caller's, for a batch of sequences:
+ * write rows of K and V, fetch them back, and attend to them.  The contexts
+ * above run the same kernels on their own pools (sv_config.kv_format, window).
+ *
+ * A pool holds codes k, v [n_pages, n_kv_heads, 16, head_dim], device memory
+ * aligned to 16 bytes.  head_dim is 64, 128 or 256.  format:
+ *   SV_KV_BF16  the codes are the bf16 values (k_exp, v_exp, scale_block unused);
+ *   SV_KV_E4M3  8 bits: e4m3 codes, and for each kv head and block of
+ *     scale_block = 1 or 16 positions one e8m0 exponent byte b, the value
+ *     2^(b - 127), in k_exp, v_exp [n_pages, n_kv_heads, 16 / scale_block]
+ *     (16-byte aligned).  A block whose largest magnitude is a has the smallest
+ *     exponent e >= -100 with a <= 448 * 2^e; its values are rounded to the
+ *     nearest code, ties to even.  So a value x of a block comes back within
+ *     2^-4 |x| (half a step of e4m3's four significant bits) or within
+ *     2^-10 * 2^e near zero (e > -100: a > 224 * 2^e, so 2^-17.8 a).  A block with an
+ *     infinity or NaN has byte 255 and codes of zero: it reads back as NaN
+ *     throughout.  (A value that rounds up to 2^128 comes back as infinity.)
+ *   scale_block 1: an append never touches what is stored, so the cache's
+ *     bytes do not depend on how the positions were cut into calls.
+ *   scale_block 16: one exponent a page.  A write that begins inside a page
+ *     keeps the page's exponent or raises it; when it rises the page's
+ *     earlier codes are rounded again.  A page whose first position is
+ *     written starts anew.
+ * The NaN codes 0x7f, 0xff are not written; where a caller's own pool holds
+ * them at positions a row sees, that row's result is not defined (NaN or a
+ * number), other rows' are not affected.
+ *
+ * The rows of a call: sequence s brings rows row_start[s] .. row_start[s+1] - 1
+ * (device int32 [n_seq + 1], not decreasing; NULL: n_rows / n_seq rows each),
+ * which stand at positions first[s], first[s] + 1, ... (device int32 [n_seq]).
+ * Position p lies in page block_table[s * table_stride + p / 16] at slot p % 16
+ * (device int32 [n_seq, table_stride]).  n_rows: rows of the buffers; those
+ * behind the last sequence's are not touched.  max_rows: the most rows of a
+ * sequence where the caller knows it (0: n_rows); only speed depends on it.
+ * The device arrays are read when the kernels run: a captured graph may be
+ * replayed with other lengths, tables and rows.
+ *   Rows at negative positions are padding: not written, fetched as zeros,
+ * and attending to nothing.  A page that the table does not reach or that is
+ * not of the pool is passed over (nothing written, zeros fetched, its
+ * positions unseen) and status bit 2 raised.
+ *   In one sv_kv_write call no two rows may lie at the same place of the pool.
+ * Pages may be shared between sequences otherwise (a common prefix).
+ *
+ * Conventions: device pointers of the current device; strides in elements,
+ * multiples of 8, between rows whose heads lie side by side (rows of a fused
+ * projection will do); row buffers 16-byte aligned.  status_dev: int32 the
+ * kernels OR their failure bits into (1 timeout, 2 bad page), or NULL.
+ * cuda_stream: the stream to run on (NULL = legacy stream).  Asynchronous, no
+ * allocation, no synchronisation: may be captured into a graph (the first
+ * sv_attend of a process on a device sets kernel attributes).  Returns SV_OK,
+ * SV_E_INVAL (nothing launched), SV_E_NOMEM (workspace too small, nothing
+ * launched) or SV_E_CUDA. */
+#define SV_KV_BF16 0
+#define SV_KV_E4M3 1
+typedef struct {
+  int32_t format, n_pages, n_kv_heads, head_dim, scale_block;
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+} sv_kv_pool;
+typedef struct {
+  int32_t n_seq, n_rows, max_rows, table_stride;
+  const int32_t *block_table, *first, *row_start;
+} sv_row_batch;
+
+/* Put the rows' K and V (bf16 [n_rows, n_kv_heads, head_dim]) into their places. */
+int sv_kv_write(const sv_kv_pool* pool, const sv_row_batch* rows, const void* k_dev, int64_t k_stride,
+                const void* v_dev, int64_t v_stride, int32_t* status_dev, void* cuda_stream);
+
+/* The reverse: K and V of the rows' positions as bf16. */
+int sv_kv_fetch(const sv_kv_pool* pool, const sv_row_batch* rows, void* k_dev, int64_t k_stride, void* v_dev,
+                int64_t v_stride, int32_t* status_dev, void* cuda_stream);
+
+/* Attention of the rows over the pool: the row at position t sees positions
+ * p <= t, or with window > 0 those with p > t - window or p < sinks, and
+ *   out = softmax(scale * q . k) v,  lse = ln(sum exp(scale * q . k)).
+ * The rows' own K and V are taken from the pool: write them first.
+ *   q, out: bf16 [n_rows, n_q_heads, head_dim], query head h reads kv head
+ *   h / (n_q_heads / n_kv_heads) (n_q_heads a multiple of n_kv_heads);
+ *   lse_dev: fp32 [n_rows, n_q_heads] or NULL.  A row that sees nothing gives
+ *   zeros and -infinity.  What lies in places a row does not see has no effect on it.
+ * Softmax sums and accumulators are fp32.  A row's result depends on its own
+ * query, position, window and cache alone, bit for bit: not on the other
+ * rows or sequences of the call, nor on the pages that hold the cache.
+ * n_seq is at most 1024.
+ *   workspace_dev: sv_attend_workspace bytes (256-byte aligned) that the call
+ *   may overwrite; calls that may run at the same time (other streams,
+ *   captured graphs replayed beside one another) need one each. */
+int sv_attend_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, int64_t* bytes);
+int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, const void* q_dev, int64_t q_stride,
+              void* out_dev, int64_t out_stride, float* lse_dev, int window, int sinks, float scale,
+              void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
 const char* sv_last_error(const sv_ctx* ctx);
 
 #ifdef __cplusplus
