@@ -211,6 +211,8 @@ class PagedKv:
                 raise ValueError("the cache's tensors lie on different devices")
             if t.data_ptr() % 16:
                 raise ValueError("the cache's tensors must be aligned to 16 bytes")
+        import torch
+        self._bf16 = torch.bfloat16
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, d, k.device
         self._c = SvKvPool(self.format, n_pages, n_kv, d, self.scale_block, _ptr(k), _ptr(v), _ptr(k_exp),
@@ -259,6 +261,7 @@ class RowBatch:
             raise ValueError("the batch's tensors lie on different devices")
         self.n_seq, self.n_rows, self.device = n_seq, int(n_rows), block_table.device
         self.tensors = (block_table, first, row_start)
+        self._workspace = {}  # bytes by (query heads, head_dim): the sizes of a batch do not change
         self._c = SvRowBatch(n_seq, int(n_rows), int(max_rows), pages, _ptr(block_table), _ptr(first),
                              _ptr(row_start))
         self._p = ctypes.byref(self._c)
@@ -268,10 +271,10 @@ def _check_rows(t, name, cache, n_rows, heads):
     """Rows of heads side by side: [n_rows, heads, head_dim] bf16 whose rows may
     lie apart (a slice of a fused projection). Returns the row stride."""
     d = cache.head_dim
+    if t.dtype is not cache._bf16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
     if t.device != cache.device:
         raise ValueError(f"{name}: on {t.device}, the cache on {cache.device}")
-    if str(t.dtype) != "torch.bfloat16":
-        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
     if t.shape != (n_rows, heads, d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n_rows, heads, d)}")
     row, head, one = t.stride()
@@ -283,23 +286,28 @@ def _check_rows(t, name, cache, n_rows, heads):
     return row
 
 
-def _run_on(cache, rows, stream, status, call):
-    """call(stream handle) on the cache's device; None: torch's current stream there."""
-    import torch
+def _check_call(cache, rows, status):
     if rows.device != cache.device:
         raise ValueError(f"the rows' tables lie on {rows.device}, the cache on {cache.device}")
     if status is not None:
         _check_tensor(status, "status", "torch.int32", (1,))
         if status.device != cache.device:
             raise ValueError(f"status: on {status.device}, the cache on {cache.device}")
-    index = cache.device.index
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _run_on(cache, rows, stream, None, call)
-    s = torch.cuda.current_stream() if stream is None else stream
-    rc = call(_P(s.cuda_stream))
+
+
+def _launch(cache, stream, call, *args):
+    """call(*args, stream handle) on the cache's device; stream None: torch's current one there."""
+    import torch
+    dev = cache.device.index
+    # (the current stream's handle without the Stream object around it: 2 us less a call)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = call(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, handle)
     if rc != SV_OK:
-        raise SvError(rc, "rejected the arguments or a CUDA call failed")
+        raise SvError(rc, f"{call.__name__} rejected the arguments or a CUDA call failed")
 
 
 def kv_write(cache: PagedKv, rows: RowBatch, k, v, *, status=None, stream=None):
@@ -308,8 +316,8 @@ def kv_write(cache: PagedKv, rows: RowBatch, k, v, *, status=None, stream=None):
     ORed into it. stream: None for torch's current one. Asynchronous."""
     ks = _check_rows(k, "k", cache, rows.n_rows, cache.n_kv_heads)
     vs = _check_rows(v, "v", cache, rows.n_rows, cache.n_kv_heads)
-    _run_on(cache, rows, stream, status, lambda s: _lib.sv_kv_write(
-        cache._p, rows._p, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(status), s))
+    _check_call(cache, rows, status)
+    _launch(cache, stream, _lib.sv_kv_write, cache._p, rows._p, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(status))
 
 
 def kv_fetch(cache: PagedKv, rows: RowBatch, k_out, v_out, *, status=None, stream=None):
@@ -317,17 +325,22 @@ def kv_fetch(cache: PagedKv, rows: RowBatch, k_out, v_out, *, status=None, strea
     ([n_rows, n_kv_heads, head_dim]). Asynchronous."""
     ks = _check_rows(k_out, "k_out", cache, rows.n_rows, cache.n_kv_heads)
     vs = _check_rows(v_out, "v_out", cache, rows.n_rows, cache.n_kv_heads)
-    _run_on(cache, rows, stream, status, lambda s: _lib.sv_kv_fetch(
-        cache._p, rows._p, k_out.data_ptr(), ks, v_out.data_ptr(), vs, _ptr(status), s))
+    _check_call(cache, rows, status)
+    _launch(cache, stream, _lib.sv_kv_fetch, cache._p, rows._p, k_out.data_ptr(), ks, v_out.data_ptr(), vs,
+            _ptr(status))
 
 
 def attend_workspace(cache: PagedKv, rows: RowBatch, n_q_heads: int) -> int:
     """sv_attend_workspace: bytes that attend needs besides its arguments."""
-    n = ctypes.c_int64(0)
-    rc = _lib.sv_attend_workspace(cache._p, rows._p, int(n_q_heads), ctypes.byref(n))
-    if rc != SV_OK:
-        raise SvError(rc, f"attend_workspace({n_q_heads} query heads)")
-    return n.value
+    key = (n_q_heads, cache.head_dim)
+    need = rows._workspace.get(key)
+    if need is None:
+        n = ctypes.c_int64(0)
+        rc = _lib.sv_attend_workspace(cache._p, rows._p, int(n_q_heads), ctypes.byref(n))
+        if rc != SV_OK:
+            raise SvError(rc, f"attend_workspace({n_q_heads} query heads)")
+        need = rows._workspace[key] = n.value
+    return need
 
 
 def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: int = 0, scale=None, lse=None,
@@ -341,11 +354,12 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     `stream`, if given, must be that one). Asynchronous."""
     if getattr(q, "dim", lambda: 0)() != 3:
         raise ValueError("q: must be a 3-D tensor [n_rows, n_q_heads, head_dim]")
-    heads = int(q.shape[1])
+    heads = q.shape[1]
     if heads < 1 or heads % cache.n_kv_heads:
         raise ValueError(f"q: {heads} heads, not a multiple of the cache's {cache.n_kv_heads}")
     qs = _check_rows(q, "q", cache, rows.n_rows, heads)
     os_ = _check_rows(out, "out", cache, rows.n_rows, heads)
+    _check_call(cache, rows, status)
     if window < 0 or sinks < 0:
         raise ValueError(f"window {window}, sinks {sinks}: must not be negative")
     if rows.n_seq > ATTEND_MAX_SEQ:
@@ -360,15 +374,16 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
         if stream is not None and stream != torch.cuda.current_stream(cache.device):
             raise ValueError("a stream that is not torch's current one needs a workspace of the caller's")
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        given = need
     else:
         _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
         if workspace.device != cache.device:
             raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
+        given = workspace.numel()
     if scale is None:
         scale = cache.head_dim ** -0.5
-    _run_on(cache, rows, stream, status, lambda s: _lib.sv_attend(
-        cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse), int(window), int(sinks),
-        float(scale), workspace.data_ptr(), workspace.numel(), _ptr(status), s))
+    _launch(cache, stream, _lib.sv_attend, cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse),
+            window, sinks, scale, workspace.data_ptr(), given, _ptr(status))
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):

@@ -36,12 +36,26 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace sv {
 namespace {
 
 constexpr int kAttendWarps = 8;
 constexpr int kAttendThreads = (kAttendWarps + 1) * 32;  // consumers, then the producer warp
+
+// What the producer tells the consumers of a chunk (and, with an item's last
+// chunk, of the item after it, whose queries they fetch meanwhile).
+struct AttendTile {
+  int row0, f0, nf, kvh;  // the sequence's first row, the tile's first query row, the sequence's query rows
+  int first;              // position of the sequence's first row
+};
+struct alignas(16) AttendDesc {
+  int base, loaded, flags, split;  // first position; pages in the ring; kDesc*
+  AttendTile now, next;
+  int pad[2];
+};
+enum : int { kDescLast = 1, kDescNext = 2, kDescEdge = 4, kDescEnd = 8 };
 
 template <int D_, int FMT_, int MT_>
 struct AttendCfg {
@@ -54,6 +68,7 @@ struct AttendCfg {
   static constexpr int kStageBytes = 2 * CP * kPageBytes;
   // ring depth: 96 KB a CTA (64 KB at the smallest rows; 128 KB for rows of 512 bytes)
   static constexpr int kStages = RB == 64 ? 4 : RB == 512 ? 2 : 3;
+  static constexpr int kPerSm = RB == 512 || MT == 4 ? 1 : 2;  // CTAs per SM the registers are cut for
   static constexpr int NT = CP / 4;               // 8-position score tiles per warp
   static constexpr int NK = D / 16;               // k16 steps of a score
   static constexpr int DW = D / kAttendWarps;     // output columns per warp
@@ -68,9 +83,9 @@ struct AttendCfg {
   static constexpr int kPBytes = MT * CP * 512 * (kBf16 ? 2 : 1);
   static constexpr int kOffMax = kOffP + kPBytes;                    // [QR][8] row maxima
   static constexpr int kOffSum = kOffMax + QR * 32;                  // [QR][8] row sums
-  static constexpr int kOffRow = kOffSum + QR * 32;                  // [2][QR] score factors, [QR] maxima
-  static constexpr int kOffMask = kOffRow + 3 * QR * 4;              // [stages] loaded pages
-  static constexpr int kOffBar = (kOffMask + kStages * 4 + 7) & ~7;
+  static constexpr int kOffRow = kOffSum + QR * 32;                  // [2][QR] score factors, [2][QR] positions, [QR] maxima
+  static constexpr int kOffDesc = kOffRow + 5 * QR * 4;              // [stages] chunk descriptors
+  static constexpr int kOffBar = kOffDesc + kStages * (int)sizeof(AttendDesc);
   static constexpr int kOffSeq = kOffBar + 2 * kStages * 8;          // [n_seq + 1] items before, first, row start
   static constexpr int smem_bytes(int n_seq) { return 1024 + kOffSeq + 4 * (3 * n_seq + 2); }
   static_assert(1024 + kOffSeq + 4 * (3 * kAttendMaxSeq + 2) <= 227 * 1024, "shared memory of a CTA");
@@ -151,10 +166,9 @@ __device__ __forceinline__ SplitRange splits_seen(int t0, int t1, int window, in
 
 // One unit of work: a split of a kv head for a tile of query rows.
 struct AttendItem {
-  int seq, kvh, split, f0;   // f0: the tile's first query row of its sequence
-  int row0, nf;              // the sequence's first row; its query rows
-  int t0, t1;                // positions of the tile's first and last token row
-  int first;
+  AttendTile tile;
+  int seq, split;
+  int t0, t1;  // positions of the tile's first and last token row
 };
 
 template <class C>
@@ -172,21 +186,22 @@ struct AttendWork {
       if (before[mid] <= w) lo = mid; else hi = mid;
     }
     it.seq = lo;
-    it.first = first[lo];
-    it.row0 = start[lo];
-    const int n = start[lo + 1] - it.row0;
-    it.nf = n * G;
-    const int tiles = (it.nf + C::QR - 1) / C::QR;
+    AttendTile& tl = it.tile;
+    tl.first = first[lo];
+    tl.row0 = start[lo];
+    const int n = start[lo + 1] - tl.row0;
+    tl.nf = n * G;
+    const int tiles = (tl.nf + C::QR - 1) / C::QR;
     int x = w - before[lo];
     const int tile = x % tiles;
     x /= tiles;
-    it.kvh = x % p.n_kv_heads;
+    tl.kvh = x % p.n_kv_heads;
     x /= p.n_kv_heads;
-    const SplitRange sr = splits_seen(it.first, it.first + n - 1, p.window, p.sinks, p.rows.limit(), C::D);
+    const SplitRange sr = splits_seen(tl.first, tl.first + n - 1, p.window, p.sinks, p.rows.limit(), C::D);
     it.split = sr.at(sr.n - 1 - x);
-    it.f0 = tile * C::QR;
-    it.t0 = it.first + it.f0 / G;
-    it.t1 = it.first + (min(it.f0 + C::QR, it.nf) - 1) / G;
+    tl.f0 = tile * C::QR;
+    it.t0 = tl.first + tl.f0 / G;
+    it.t1 = tl.first + (min(tl.f0 + C::QR, tl.nf) - 1) / G;
   }
   // Pages of chunk c of the item that some row of the tile sees, as a mask.
   __device__ __forceinline__ uint32_t seen(const AttendItem& it, int base) const {
@@ -206,7 +221,6 @@ struct AttendWork {
 
 // Walks the CTA's chunks in order: items w, w + step, ..., each from the start
 // of its split; chunks and items of which nothing is seen are passed over.
-// Producer and consumers walk the same sequence.
 template <class C>
 struct AttendWalk {
   AttendItem it;
@@ -290,7 +304,8 @@ __device__ int attend_plan(const AttendParams& p, int G, int* before, int* first
 // ------------------------------------------------------------------ producer
 // One warp: lane l < CP takes page l of K, lane 16 + l that of V.  The next
 // chunk's page numbers and exponents are requested while the current one waits
-// for its place in the ring.
+// for its place in the ring.  A descriptor goes with each chunk; the last one
+// says that there are no more.
 template <class C>
 __device__ void attend_produce(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const AttendWork<C>& wk, uint8_t* smem, uint64_t* full, uint64_t* empty) {
@@ -299,7 +314,7 @@ __device__ void attend_produce(const AttendParams& p, const CUtensorMap& kmap, c
   const CUtensorMap* map = is_v ? &vmap : &kmap;
   const uint8_t* exps = is_v ? p.v_exp : p.k_exp;
   const uint64_t pol = policy_evict_first();
-  int* mask_s = reinterpret_cast<int*>(smem + C::kOffMask);
+  AttendDesc* desc = reinterpret_cast<AttendDesc*>(smem + C::kOffDesc);
   auto page_of = [&](const AttendWalk<C>& k) {
     if (!k.valid || j >= C::CP || !((k.mask >> j) & 1)) return -1;
     return find_page(p.rows, p.n_pages, k.it.seq, k.base + j * kPage, p.status);
@@ -307,7 +322,7 @@ __device__ void attend_produce(const AttendParams& p, const CUtensorMap& kmap, c
   auto exps_of = [&](const AttendWalk<C>& k, int page) {
     uint4 e = make_uint4(0u, 0u, 0u, 0u);
     if (C::kBf16 || page < 0) return e;
-    const size_t ph = (size_t)page * p.n_kv_heads + k.it.kvh;
+    const size_t ph = (size_t)page * p.n_kv_heads + k.it.tile.kvh;
     if (p.block == 1) return __ldcg(reinterpret_cast<const uint4*>(exps + ph * kPage));
     e.x = e.y = e.z = e.w = 0x01010101u * __ldcg(exps + ph);
     return e;
@@ -316,30 +331,48 @@ __device__ void attend_produce(const AttendParams& p, const CUtensorMap& kmap, c
   cur.start(wk, blockIdx.x);
   int page = page_of(cur);
   uint4 ex = exps_of(cur, page);
-  bool ok = true;
   int n = 0;
-  for (; cur.valid; ++n) {
+  for (;; ++n) {
     const int st = n % C::kStages, use = n / C::kStages;
     AttendWalk<C> nxt = cur;
-    nxt.next(wk);
-    const int npage = page_of(nxt);
-    if (ok && use > 0 && !mbar_wait(&empty[st], (use - 1) & 1)) ok = false;
+    int npage = -1;
+    if (cur.valid) {
+      nxt.next(wk);
+      npage = page_of(nxt);
+    }
+    const bool ok = use == 0 || mbar_wait(&empty[st], (use - 1) & 1);
     if (!__all_sync(0xffffffffu, ok)) {
-      ok = false;
+      if (p.status && lane == 0) atomicOr(p.status, ST_TIMEOUT);
       break;
     }
     const uint32_t got = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
     if (lane == 0) {
-      mask_s[st] = (int)got;
+      AttendDesc& d = desc[st];
+      d.base = cur.base;
+      d.loaded = (int)got;
+      if (cur.valid) {
+        const bool last = !nxt.valid || nxt.w != cur.w;
+        // whether every row of the tile sees every position of the chunk
+        const int cend = cur.base + C::kChunk - 1;
+        const bool all = got == (1u << C::CP) - 1u && cend <= cur.it.t0 &&
+                         (p.window <= 0 || cur.base > cur.it.t1 - p.window || cend < p.sinks);
+        d.flags = (last ? kDescLast : 0) | (last && nxt.valid ? kDescNext : 0) | (all ? 0 : kDescEdge);
+        d.split = cur.it.split;
+        d.now = cur.it.tile;
+        if (last && nxt.valid) d.next = nxt.it.tile;
+      } else {
+        d.flags = kDescEnd;
+      }
       mbar_arrive_expect_tx(&full[st], 2 * __popc(got) * C::kPageBytes);
     }
     if (!C::kBf16 && j < C::CP)
       *reinterpret_cast<uint4*>(smem + C::kOffScale + st * C::kScaleBytes + (is_v ? C::CP * kPage : 0) + j * kPage) = ex;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&full[st]);  // after the mask and the exponents
+    if (lane == 0) mbar_arrive(&full[st]);  // after the descriptor and the exponents
+    if (!cur.valid) return;
     if (page >= 0) {
       uint8_t* dst = smem + st * C::kStageBytes + ((is_v ? C::CP : 0) + j) * C::kPageBytes;
-      const int ph = (p.page0 + page) * p.n_kv_heads + cur.it.kvh;
+      const int ph = (p.page0 + page) * p.n_kv_heads + cur.it.tile.kvh;
       if (C::RB == 64) {
         tma_load_2d(dst, map, 0, ph * 8, &full[st], pol);
       } else {
@@ -351,12 +384,9 @@ __device__ void attend_produce(const AttendParams& p, const CUtensorMap& kmap, c
     page = npage;
     cur = nxt;
   }
-  if (!ok) {
-    if (p.status && lane == 0) atomicOr(p.status, ST_TIMEOUT);
-    // what is still on its way into the ring lands before the CTA ends
-    for (int k = n > C::kStages ? n - C::kStages : 0; k < n && lane == 0; ++k)
-      mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
-  }
+  // (after a timeout) what is still on its way into the ring lands before the CTA ends
+  for (int k = n > C::kStages ? n - C::kStages : 0; k < n && lane == 0; ++k)
+    mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
 }
 
 // ------------------------------------------------------------------ consumers
@@ -369,7 +399,7 @@ struct QueryTile {
   static constexpr int kPer = (kPieces + kAttendWarps * 32 - 1) / (kAttendWarps * 32);
   uint4 x[kPer];
 
-  __device__ __forceinline__ void load(const AttendParams& p, const AttendItem& it, int G) {
+  __device__ __forceinline__ void load(const AttendParams& p, const AttendTile& it, int G) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int v = threadIdx.x + u * kAttendWarps * 32, qi = v / (C::D / 8), c8 = v % (C::D / 8);
@@ -381,8 +411,9 @@ struct QueryTile {
       }
     }
   }
-  // to shared memory: fragments [MT][NK][32 lanes] and the rows' score factors
-  __device__ __forceinline__ void stage(const AttendParams& p, uint8_t* frag, float* factor) const {
+  // to shared memory: fragments [MT][NK][32 lanes], the rows' score factors and positions
+  __device__ __forceinline__ void stage(const AttendParams& p, const AttendTile& it, int G, uint8_t* frag,
+                                        float* factor, int* tpos) const {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int v = threadIdx.x + u * kAttendWarps * 32, qi = v / (C::D / 8), c8 = v % (C::D / 8);
@@ -424,92 +455,92 @@ struct QueryTile {
         dst[hi] = w[2 * i];
         dst[2 + hi] = w[2 * i + 1];
       }
-      if (c8 == 0) factor[qi] = f;
+      if (c8 == 0) {
+        factor[qi] = f;
+        tpos[qi] = it.first + (it.f0 + qi) / G;
+      }
     }
   }
 };
 
+// Named barrier over `count` threads; whether any of them says `v`.
+__device__ __forceinline__ bool sync_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// The sums, maxima and accumulators of a tile in the course of an item, and
+// what a chunk does to them.
 template <class C>
-__device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, uint8_t* smem, uint64_t* full,
-                               uint64_t* empty) {
-  constexpr int MT = C::MT, CP = C::CP, NT = C::NT, NO = C::NO, W = kAttendWarps;
-  constexpr bool kBf16 = C::kBf16;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
-  const int G = wk.G;
-  float* s_max = reinterpret_cast<float*>(smem + C::kOffMax);
-  float* s_sum = reinterpret_cast<float*>(smem + C::kOffSum);
-  float* s_fac = reinterpret_cast<float*>(smem + C::kOffRow);
-  float* s_m = s_fac + 2 * C::QR;
-  const int* mask_s = reinterpret_cast<const int*>(smem + C::kOffMask);
-  uint4* s_p = reinterpret_cast<uint4*>(smem + C::kOffP);
+struct AttendRows {
+  static constexpr int MT = C::MT, CP = C::CP, NT = C::NT, NO = C::NO, W = kAttendWarps;
+  static constexpr bool kBf16 = C::kBf16;
+  const AttendParams& p;
+  uint8_t* smem;
+  int warp, lane, g, q4, my_page, my_nt;
+  float o[MT][NO][4], m_run[MT][2], l_run[MT][2];
 
-  AttendWalk<C> cur;
-  cur.start(wk, blockIdx.x);
-  if (!cur.valid) return;
-  QueryTile<C> qt;
-  qt.load(p, cur.it, G);
-  int qb = 0;
-  qt.stage(p, smem + C::kOffQ, s_fac);
-  named_sync(2, W * 32);
+  __device__ __forceinline__ AttendRows(const AttendParams& p_, uint8_t* smem_) : p(p_), smem(smem_) {
+    warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+    g = lane >> 2;
+    q4 = lane & 3;
+    my_page = NT == 2 ? warp : warp >> 1;
+    my_nt = NT == 2 ? 0 : warp & 1;
+  }
+  __device__ __forceinline__ float* s_max() const { return reinterpret_cast<float*>(smem + C::kOffMax); }
+  __device__ __forceinline__ float* s_sum() const { return reinterpret_cast<float*>(smem + C::kOffSum); }
+  __device__ __forceinline__ float* s_fac(int qb) const { return reinterpret_cast<float*>(smem + C::kOffRow) + qb * C::QR; }
+  __device__ __forceinline__ int* s_t(int qb) const { return reinterpret_cast<int*>(smem + C::kOffRow) + (2 + qb) * C::QR; }
+  __device__ __forceinline__ float* s_m() const { return reinterpret_cast<float*>(smem + C::kOffRow) + 4 * C::QR; }
+  __device__ __forceinline__ uint4* s_p() const { return reinterpret_cast<uint4*>(smem + C::kOffP); }
+  __device__ __forceinline__ bool sees(int t, int pos) const {
+    return pos <= t && (p.window <= 0 || pos > t - p.window || pos < p.sinks);
+  }
 
-  float o[MT][NO][4], m_run[MT][2], l_run[MT][2], fac[MT][2];
-  int tpos[MT][2];  // position of the lane's rows (g and g + 8 of each tile)
-  bool ok = true, opens = true;
-  const int my_page = NT == 2 ? warp : warp >> 1, my_nt = NT == 2 ? 0 : warp & 1;
-
-  for (int n = 0; cur.valid; ++n) {
-    const int st = n % C::kStages;
-    AttendWalk<C> nxt = cur;
-    nxt.next(wk);
-    const bool last = !nxt.valid || nxt.w != cur.w;
-    if (opens) {
-      opens = false;
+  __device__ __forceinline__ void open() {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          m_run[mt][r] = -INFINITY;
-          l_run[mt][r] = 0.0f;
-          const int qi = mt * 16 + g + 8 * r;
-          fac[mt][r] = s_fac[qb * C::QR + qi];
-          tpos[mt][r] = cur.it.first + (cur.it.f0 + qi) / G;
+      for (int r = 0; r < 2; ++r) {
+        m_run[mt][r] = -INFINITY;
+        l_run[mt][r] = 0.0f;
 #pragma unroll
-          for (int x = 0; x < NO; ++x) o[mt][x][2 * r] = o[mt][x][2 * r + 1] = 0.0f;
-        }
-    }
-    // (the next item's queries, if this is the item's last chunk)
-    if (last && nxt.valid) qt.load(p, nxt.it, G);
+        for (int x = 0; x < NO; ++x) o[mt][x][2 * r] = o[mt][x][2 * r + 1] = 0.0f;
+      }
+  }
 
-    if (ok && !mbar_wait(&full[st], (n / C::kStages) & 1)) ok = false;
-    const uint32_t loaded = ok ? (uint32_t)mask_s[st] : 0u;
-    const uint32_t kbase = smem_u32(smem + st * C::kStageBytes);
-    const uint32_t vbase = kbase + CP * C::kPageBytes;
-    // whether every row of the tile sees every position of the chunk
-    const int cend = cur.base + C::kChunk - 1;
-    const bool all_seen = cend <= cur.it.t0 &&
-                          (p.window <= 0 || cur.base > cur.it.t1 - p.window || cend < p.sinks);
-
-    // ---- scores of this warp's positions
-    float s[MT][NT][4];
+  // Scores of this warp's positions of the chunk, in log2 units with the
+  // value's exponent added, -inf where a row does not see them.
+  // kEdge: some row does not see some position, or a page is not there.
+  template <bool kEdge>
+  __device__ __forceinline__ void scores(uint32_t kbase, const uint8_t* sc, int base, uint32_t loaded, int qb,
+                                         float (&s)[MT][NT][4], float (&iv)[NT][2]) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
-    const bool have = (loaded >> my_page) & 1;
+    const bool have = !kEdge || ((loaded >> my_page) & 1);
     if (have) {
       const uint32_t kp = kbase + my_page * C::kPageBytes;
-      const uint4* qf = reinterpret_cast<const uint4*>(smem + C::kOffQ + qb * C::kQBytes);
+      const uint4* qf = reinterpret_cast<const uint4*>(smem + C::kOffQ + qb * C::kQBytes) + lane;
       constexpr int kUnits = C::RB / 64;               // 16-byte units of a key row per lane
       constexpr int kSteps = C::NK / kUnits;           // k16 steps per unit
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        uint4 kx[NT];
+        uint32_t kx[NT][4];
         const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint32_t a = kp + page_off<C::RB>(pos_of_col<kBf16>((my_nt + nt) * 8 + g), c);
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(kx[nt].x), "=r"(kx[nt].y), "=r"(kx[nt].z), "=r"(kx[nt].w)
+                       : "=r"(kx[nt][0]), "=r"(kx[nt][1]), "=r"(kx[nt][2]), "=r"(kx[nt][3])
                        : "r"(a));
         }
 #pragma unroll
@@ -517,18 +548,17 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t w[4] = {kx[nt].x, kx[nt].y, kx[nt].z, kx[nt].w};
             if (kBf16) {
-              b0[nt] = w[(2 * k) & 3];
-              b1[nt] = w[(2 * k + 1) & 3];
+              b0[nt] = kx[nt][(2 * k) & 3];
+              b1[nt] = kx[nt][(2 * k + 1) & 3];
             } else {
-              b0[nt] = f16x2_of_lo(w[k & 3]);
-              b1[nt] = f16x2_of_hi(w[k & 3]);
+              b0[nt] = f16x2_of_lo(kx[nt][k & 3]);
+              b1[nt] = f16x2_of_hi(kx[nt][k & 3]);
             }
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const uint4 av = qf[(mt * C::NK + u * kSteps + k) * 32 + lane];
+            const uint4 av = qf[(mt * C::NK + u * kSteps + k) * 32];
             const uint32_t a[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_16<kBf16>(s[mt][nt], a, b0[nt], b1[nt]);
@@ -536,63 +566,65 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
         }
       }
     }
-    // ---- exponents: key scale, value exponent and its inverse of the lane's columns
-    float ks[NT][2], ev[NT][2], iv[NT][2];
-    if (!kBf16) {
-      const uint8_t* sc = smem + C::kOffScale + st * C::kScaleBytes + my_page * kPage;
-      const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + 4 * q4);
-      const uint32_t vw = *reinterpret_cast<const uint32_t*>(sc + CP * kPage + 4 * q4);
+    float ks[NT][2], ev[NT][2];
+    if (!kBf16) {  // columns 2 q4 + e of tile nt are position 4 q4 + 2 nt + e: four bytes of the page's exponents
+      const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + my_page * kPage + 4 * q4);
+      const uint32_t vw = *reinterpret_cast<const uint32_t*>(sc + (CP + my_page) * kPage + 4 * q4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int sh = 8 * (2 * (my_nt + nt) + e);  // columns 2 q4 + e of tile nt: position 4 q4 + 2 nt + e
+          const int sh = 8 * (2 * (my_nt + nt) + e);
           const uint32_t bk = (kw >> sh) & 255u, bv = (vw >> sh) & 255u;
           ks[nt][e] = __uint_as_float(bk << 23);  // (255: infinity, times a score of zero codes: NaN)
           ev[nt][e] = bv == kExpNaN ? __uint_as_float(0x7fffffffu) : (float)((int)bv - 127);
           iv[nt][e] = exp_byte_inverse((int)bv);
         }
     }
-    // ---- scores in log2 units (with the value's exponent), masked, and the rows' maxima
+    const float* fac = s_fac(qb);
+    const int* tp = s_t(qb);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        const int qi = mt * 16 + g + 8 * r;
+        const float f = fac[qi];
+        const int t = kEdge ? tp[qi] : 0;
         float mx = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float& x = s[mt][nt][2 * r + e];
-            x = kBf16 ? __fmul_rn(x, fac[mt][r]) : __fmaf_rn(x, __fmul_rn(fac[mt][r], ks[nt][e]), ev[nt][e]);
-            if (!all_seen || !have) {
-              const int pp = cur.base + my_page * kPage + pos_of_col<kBf16>((my_nt + nt) * 8 + 2 * q4 + e);
-              const bool vis = have && pp <= tpos[mt][r] &&
-                               (p.window <= 0 || pp > tpos[mt][r] - p.window || pp < p.sinks);
-              x = vis ? x : -INFINITY;
-            }
+            x = kBf16 ? __fmul_rn(x, f) : __fmaf_rn(x, __fmul_rn(f, ks[nt][e]), ev[nt][e]);
+            if (kEdge)
+              x = have && sees(t, base + my_page * kPage + pos_of_col<kBf16>((my_nt + nt) * 8 + 2 * q4 + e)) ? x
+                                                                                                            : -INFINITY;
             mx = fmaxf(mx, x);
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (q4 == 0) s_max[(mt * 16 + g + 8 * r) * W + warp] = mx;
+        if (q4 == 0) s_max()[qi * W + warp] = mx;
       }
-    named_sync(2, W * 32);
-    // ---- weights
-    float alpha[MT][2];
+  }
+
+  // The scores' weights against the rows' running maxima, to shared memory as
+  // A fragments; accumulators and sums are scaled to the new maxima.
+  template <bool kEdge>
+  __device__ __forceinline__ void weights(const float (&s)[MT][NT][4], const float (&iv)[NT][2], bool last) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       uint32_t hi[2][NT], lo[2][NT];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float4* mr = reinterpret_cast<const float4*>(s_max + (mt * 16 + g + 8 * r) * W);
+        const int qi = mt * 16 + g + 8 * r;
+        const float4* mr = reinterpret_cast<const float4*>(s_max() + qi * W);
         const float4 a = mr[0], b = mr[1];
         float m = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
         m = fmaxf(m, m_run[mt][r]);
         // a row that has seen nothing yet: every weight is 2^-inf = 0
         const float ref = m == -INFINITY ? 0.0f : m;
-        alpha[mt][r] = ex2(__fsub_rn(m_run[mt][r], ref));
-        if (m == m_run[mt][r]) alpha[mt][r] = 1.0f;
+        const float alpha = m == m_run[mt][r] ? 1.0f : ex2(__fsub_rn(m_run[mt][r], ref));
         m_run[mt][r] = m;
         float sum = 0.0f;
 #pragma unroll
@@ -604,8 +636,10 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
             pv[e] = ex2(__fsub_rn(x, ref));
             if (kBf16)
               sum = __fadd_rn(sum, pv[e]);
-            else  // (a masked place's exponent may be anything)
+            else if (kEdge)  // (the exponent of a masked place may be anything)
               sum = x == -INFINITY ? sum : __fmaf_rn(pv[e], iv[nt][e], sum);
+            else
+              sum = __fmaf_rn(pv[e], iv[nt][e], sum);
           }
           if (kBf16) {
             hi[r][nt] = pack_bf16x2(pv[0], pv[1]);
@@ -614,10 +648,24 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
             hi[r][nt] = pack_f16x2(pv[0], pv[1]);
           }
         }
-        l_run[mt][r] = __fmaf_rn(l_run[mt][r], alpha[mt][r], sum);
+        l_run[mt][r] = __fmaf_rn(l_run[mt][r], alpha, sum);
+#pragma unroll
+        for (int x = 0; x < NO; ++x) {
+          o[mt][x][2 * r] = __fmul_rn(o[mt][x][2 * r], alpha);
+          o[mt][x][2 * r + 1] = __fmul_rn(o[mt][x][2 * r + 1], alpha);
+        }
+        if (last) {
+          float l = l_run[mt][r];
+          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 1));
+          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 2));
+          if (q4 == 0) {
+            s_sum()[qi * W + warp] = l;
+            if (warp == 0) s_m()[qi] = m;
+          }
+        }
       }
-      // A fragment of the page's 16 positions: (g, g + 8) x (columns of tile 0, of tile 1)
-      uint4* dst = s_p + (mt * CP + my_page) * 32 + lane;
+      // A fragment of the page's 16 positions: rows (g, g + 8) x columns of (tile 0, tile 1)
+      uint4* dst = s_p() + (mt * CP + my_page) * 32 + lane;
       if (NT == 2) {
         *dst = make_uint4(hi[0][0], hi[1][0], hi[0][NT - 1], hi[1][NT - 1]);
         if (kBf16) dst[MT * CP * 32] = make_uint4(lo[0][0], lo[1][0], lo[0][NT - 1], lo[1][NT - 1]);
@@ -625,122 +673,103 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
         reinterpret_cast<uint2*>(dst)[my_nt] = make_uint2(hi[0][0], hi[1][0]);
         if (kBf16) reinterpret_cast<uint2*>(dst + MT * CP * 32)[my_nt] = make_uint2(lo[0][0], lo[1][0]);
       }
-      if (last) {
+    }
+  }
+
+  // O += P V for page j and column tile x, whose values the lane holds as (b0, b1).
+  __device__ __forceinline__ void times(int j, int x, uint32_t b0, uint32_t b1) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float l = l_run[mt][r];
-          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 1));
-          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 2));
-          if (q4 == 0) {
-            s_sum[(mt * 16 + g + 8 * r) * W + warp] = l;
-            if (warp == 0) s_m[mt * 16 + g + 8 * r] = m_run[mt][r];
-          }
-        }
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint4 av = s_p()[(mt * CP + j) * 32 + lane];
+      const uint32_t a[4] = {av.x, av.y, av.z, av.w};
+      mma_16<kBf16>(o[mt][x], a, b0, b1);
+      if (kBf16) {
+        const uint4 lv = s_p()[((MT + mt) * CP + j) * 32 + lane];
+        const uint32_t al[4] = {lv.x, lv.y, lv.z, lv.w};
+        mma_16<kBf16>(o[mt][x], al, b0, b1);
       }
     }
-    if (last && nxt.valid) qt.stage(p, smem + C::kOffQ + (qb ^ 1) * C::kQBytes, s_fac + (qb ^ 1) * C::QR);
-    named_sync(2, W * 32);
-    // ---- O = alpha O + P V on this warp's columns
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int x = 0; x < NO; ++x) {
-        o[mt][x][0] = __fmul_rn(o[mt][x][0], alpha[mt][0]);
-        o[mt][x][1] = __fmul_rn(o[mt][x][1], alpha[mt][0]);
-        o[mt][x][2] = __fmul_rn(o[mt][x][2], alpha[mt][1]);
-        o[mt][x][3] = __fmul_rn(o[mt][x][3], alpha[mt][1]);
-      }
-    // values of page j, column tile x, as (b0, b1): into every query tile
-    auto times = [&](int j, int x, uint32_t b0, uint32_t b1) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const uint4 av = s_p[(mt * CP + j) * 32 + lane];
-        const uint32_t a[4] = {av.x, av.y, av.z, av.w};
-        mma_16<kBf16>(o[mt][x], a, b0, b1);
-        if (kBf16) {
-          const uint4 lv = s_p[((MT + mt) * CP + j) * 32 + lane];
-          const uint32_t al[4] = {lv.x, lv.y, lv.z, lv.w};
-          mma_16<kBf16>(o[mt][x], al, b0, b1);
-        }
-      }
+  }
+
+  // An infinity or NaN of a bf16 page in a place that some row does not see
+  // must not meet that row's weight of zero: it is taken out here and added to
+  // the rows that see it.  (The lane's words: positions 2 q4, 2 q4 + 1 and 8
+  // more of page j, column g of tile x.)
+  __device__ __forceinline__ void set_apart(int base, int j, int x, int qb, uint32_t& b0, uint32_t& b1) {
+    auto bad2 = [](uint32_t w) {
+      return ((w & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
     };
+    const uint32_t bad = bad2(b0) | (bad2(b1) << 2);
+    uint32_t who = __ballot_sync(0xffffffffu, bad != 0);
+    while (who) {
+      const int src = __ffs(who) - 1;
+      who &= who - 1;
+      const uint32_t w0 = __shfl_sync(0xffffffffu, b0, src), w1 = __shfl_sync(0xffffffffu, b1, src);
+      const uint32_t bb = __shfl_sync(0xffffffffu, bad, src);
+      const int col = src >> 2, pos0 = base + j * kPage + 2 * (src & 3);
+      for (int k = 0; k < 4; ++k) {
+        if (!((bb >> k) & 1u) || q4 != col >> 1) continue;
+        const uint32_t w = k < 2 ? w0 : w1;
+        const float v = __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
+        const int pos = pos0 + (k >> 1) * 8 + (k & 1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (sees(s_t(qb)[mt * 16 + g + 8 * r], pos)) {
+              if (col & 1) o[mt][x][2 * r + 1] = __fadd_rn(o[mt][x][2 * r + 1], v);
+              else o[mt][x][2 * r] = __fadd_rn(o[mt][x][2 * r], v);
+            }
+      }
+    }
+    if (bad & 1u) b0 &= 0xffff0000u;
+    if (bad & 2u) b0 &= 0x0000ffffu;
+    if (bad & 4u) b1 &= 0xffff0000u;
+    if (bad & 8u) b1 &= 0x0000ffffu;
+  }
+
+  // O += P V on this warp's columns.
+  template <bool kEdge>
+  __device__ __forceinline__ void values(uint32_t vbase, int base, uint32_t loaded, int qb) {
     if constexpr (!kBf16) {
 #pragma unroll
       for (int j = 0; j < CP; j += 2) {
-        if (!((loaded >> j) & 3u)) continue;
+        if (kEdge && !((loaded >> j) & 3u)) continue;
 #pragma unroll
-        for (int x = 0; x < (NO + 1) / 2; ++x) {
-          const int c = warp * C::DW / 16 + x;  // 16-column unit
+        for (int u = 0; u < (NO + 1) / 2; ++u) {
           uint32_t r[4];
-          ldsm_b8_x2_trans(vbase + (j + (lane >> 4)) * C::kPageBytes + page_off<C::RB>(lane & 15, c), r);
+          ldsm_b8_x2_trans(vbase + (j + (lane >> 4)) * C::kPageBytes + page_off<C::RB>(lane & 15, warp * C::DW / 16 + u), r);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // page j + h
-            if (!((loaded >> (j + h)) & 1u)) continue;
+            if (kEdge && !((loaded >> (j + h)) & 1u)) continue;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {  // columns 8 y .. of the unit
-              if (NO == 1 && y == 1) continue;
+            for (int y = 0; y < (NO == 1 ? 1 : 2); ++y) {  // columns 8 y .. of the 16-column unit
               const uint32_t w = NO == 1 ? ((warp & 1) ? r[2 * h + 1] : r[2 * h]) : r[2 * h + y];
               uint32_t b0 = f16x2_of_lo(w), b1 = f16x2_of_hi(w);
-              if (!all_seen) {
+              if (kEdge) {
                 // what lies in places that a row does not see may be any byte:
                 // a NaN code must not meet its weight of zero
                 const uint32_t top = 0x5f005f00u;  // 448
                 asm("min.f16x2 %0, %0, %1;" : "+r"(b0) : "r"(top));
                 asm("min.f16x2 %0, %0, %1;" : "+r"(b1) : "r"(top));
               }
-              times(j + h, NO == 1 ? 0 : 2 * x + y, b0, b1);
+              times(j + h, NO == 1 ? 0 : 2 * u + y, b0, b1);
             }
           }
         }
       }
     } else {
-      // a lane's two words of a column tile and page: positions 2 q4, 2 q4 + 1 and 8 more, column g
       auto one = [&](int j, int x, uint32_t b0, uint32_t b1) {
-        if (!((loaded >> j) & 1u)) return;
-        if (!all_seen) {
-          // An infinity or NaN in a place that some row does not see must not
-          // meet that row's weight of zero: it is taken out here and added to
-          // the rows that see it.
-          auto bad2 = [](uint32_t w) {
-            return ((w & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
-          };
-          uint32_t bad = bad2(b0) | (bad2(b1) << 2);
-          uint32_t who = __ballot_sync(0xffffffffu, bad != 0);
-          while (who) {
-            const int src = __ffs(who) - 1;
-            who &= who - 1;
-            const uint32_t w0 = __shfl_sync(0xffffffffu, b0, src), w1 = __shfl_sync(0xffffffffu, b1, src);
-            const uint32_t bb = __shfl_sync(0xffffffffu, bad, src);
-            const int col = src >> 2, pos0 = cur.base + j * kPage + 2 * (src & 3);
-            for (int k = 0; k < 4; ++k) {
-              if (!((bb >> k) & 1u) || q4 != col >> 1) continue;
-              const uint32_t w = k < 2 ? w0 : w1;
-              const float v = __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
-              const int pp = pos0 + (k >> 1) * 8 + (k & 1);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const bool vis = pp <= tpos[mt][r] &&
-                                   (p.window <= 0 || pp > tpos[mt][r] - p.window || pp < p.sinks);
-                  if (vis) {
-                    if (col & 1) o[mt][x][2 * r + 1] = __fadd_rn(o[mt][x][2 * r + 1], v);
-                    else o[mt][x][2 * r] = __fadd_rn(o[mt][x][2 * r], v);
-                  }
-                }
-            }
-          }
-          if (bad & 1u) b0 &= 0xffff0000u;
-          if (bad & 2u) b0 &= 0x0000ffffu;
-          if (bad & 4u) b1 &= 0xffff0000u;
-          if (bad & 8u) b1 &= 0x0000ffffu;
+        if (kEdge) {
+          if (!((loaded >> j) & 1u)) return;
+          set_apart(base, j, x, qb, b0, b1);
         }
         times(j, x, b0, b1);
       };
       if constexpr (NO == 1) {  // one 8-column unit, two pages a load
 #pragma unroll
         for (int j = 0; j < CP; j += 2) {
-          if (!((loaded >> j) & 3u)) continue;
+          if (kEdge && !((loaded >> j) & 3u)) continue;
           uint32_t r0, r1, r2, r3;
           ldsm_x4_trans(vbase + (j + (lane >> 4)) * C::kPageBytes + page_off<C::RB>(lane & 15, warp), r0, r1, r2, r3);
           one(j, 0, r0, r1);
@@ -749,7 +778,7 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
       } else {
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
-          if (!((loaded >> j) & 1u)) continue;
+          if (kEdge && !((loaded >> j) & 1u)) continue;
 #pragma unroll
           for (int x = 0; x < NO; x += 2) {
             uint32_t r0, r1, r2, r3;
@@ -761,45 +790,96 @@ __device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, u
         }
       }
     }
+  }
+
+  // The item's partial: accumulators from every warp, (max, sum) from the first threads.
+  __device__ __forceinline__ void partial(const AttendTile& it, int split, int G) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int f = it.f0 + mt * 16 + g + 8 * r;
+        if (f >= it.nf) continue;
+        const size_t slot = ((size_t)(it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G) * p.max_splits + split;
+        float* dst = p.part_o + slot * C::D + warp * C::DW + 2 * q4;
+#pragma unroll
+        for (int x = 0; x < NO; ++x)
+          *reinterpret_cast<float2*>(dst + 8 * x) = make_float2(o[mt][x][2 * r], o[mt][x][2 * r + 1]);
+      }
+    const int tid = threadIdx.x, f = it.f0 + tid;
+    if (tid < C::QR && f < it.nf) {
+      const float* sr = s_sum() + tid * W;
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) l = __fadd_rn(l, sr[w]);
+      const size_t slot = ((size_t)(it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G) * p.max_splits + split;
+      p.part_ml[slot] = make_float2(s_m()[tid], l);
+    }
+  }
+};
+
+template <class C>
+__device__ void attend_consume(const AttendParams& p, const AttendWork<C>& wk, uint8_t* smem, uint64_t* full,
+                               uint64_t* empty) {
+  AttendRows<C> rows(p, smem);
+  QueryTile<C> qt;
+  const AttendDesc* desc = reinterpret_cast<const AttendDesc*>(smem + C::kOffDesc);
+  int qb = 0;
+  {  // the first item's queries
+    AttendWalk<C> w;
+    w.start(wk, blockIdx.x);
+    if (!w.valid) return;
+    qt.load(p, w.it.tile, wk.G);
+    qt.stage(p, w.it.tile, wk.G, smem + C::kOffQ, rows.s_fac(0), rows.s_t(0));
+  }
+  rows.open();
+  named_sync(2, kAttendWarps * 32);
+  for (int n = 0;; ++n) {
+    const int st = n % C::kStages;
+    // A warp whose wait ran out says so at the chunk's first barrier, where all
+    // of them then leave.
+    const bool ok = mbar_wait(&full[st], (n / C::kStages) & 1);
+    const AttendDesc& d = desc[st];
+    const int flags = ok ? d.flags : kDescEnd;
+    if (flags & kDescEnd) {
+      if (sync_or(2, kAttendWarps * 32, !ok) && p.status && threadIdx.x == 0) atomicOr(p.status, ST_TIMEOUT);
+      return;
+    }
+    const int base = d.base;
+    const uint32_t loaded = (uint32_t)d.loaded;
+    const bool last = flags & kDescLast;
+    if (flags & kDescNext) qt.load(p, d.next, wk.G);
+    const uint32_t kbase = smem_u32(smem + st * C::kStageBytes), vbase = kbase + C::CP * C::kPageBytes;
+    const uint8_t* sc = smem + C::kOffScale + st * C::kScaleBytes;
+    auto chunk = [&](auto edge) {
+      constexpr bool kEdge = decltype(edge)::value;
+      float s[C::MT][C::NT][4], iv[C::NT][2];
+      rows.template scores<kEdge>(kbase, sc, base, loaded, qb, s, iv);
+      if (sync_or(2, kAttendWarps * 32, false)) return false;
+      rows.template weights<kEdge>(s, iv, last);
+      if (flags & kDescNext)
+        qt.stage(p, d.next, wk.G, smem + C::kOffQ + (qb ^ 1) * C::kQBytes, rows.s_fac(qb ^ 1), rows.s_t(qb ^ 1));
+      named_sync(2, kAttendWarps * 32);
+      rows.template values<kEdge>(vbase, base, loaded, qb);
+      return true;
+    };
+    if (!((flags & kDescEdge) ? chunk(std::true_type{}) : chunk(std::false_type{}))) {
+      if (p.status && threadIdx.x == 0) atomicOr(p.status, ST_TIMEOUT);
+      return;
+    }
+    if (last) {
+      rows.partial(d.now, d.split, wk.G);
+      rows.open();
+      qb ^= 1;
+    }
     fence_proxy_async_smem();  // reads of the stage precede its next TMA write
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
-    // ---- the item's partial
-    if (last) {
-      const AttendItem& it = cur.it;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int f = it.f0 + mt * 16 + g + 8 * r;
-          if (f >= it.nf) continue;
-          const size_t slot =
-              ((size_t)(it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G) * p.max_splits + it.split;
-          float* dst = p.part_o + slot * C::D + warp * C::DW + 2 * q4;
-#pragma unroll
-          for (int x = 0; x < NO; ++x)
-            *reinterpret_cast<float2*>(dst + 8 * x) = make_float2(o[mt][x][2 * r], o[mt][x][2 * r + 1]);
-        }
-      if (tid < C::QR && it.f0 + tid < it.nf) {
-        const int f = it.f0 + tid;
-        const float* sr = s_sum + tid * W;
-        float l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) l = __fadd_rn(l, sr[w]);
-        const size_t slot =
-            ((size_t)(it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G) * p.max_splits + it.split;
-        p.part_ml[slot] = make_float2(s_m[tid], l);
-      }
-      qb ^= 1;
-      opens = true;
-    }
-    cur = nxt;
+    if (rows.lane == 0) mbar_arrive(&empty[st]);
   }
-  if (!ok && p.status && lane == 0) atomicOr(p.status, ST_TIMEOUT);
 }
 
 template <int D, int FMT, int MT>
-__global__ void __launch_bounds__(kAttendThreads)
+__global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, MT>::kPerSm)
     k_attend(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p) {
   using C = AttendCfg<D, FMT, MT>;
   extern __shared__ uint8_t smem_raw[];
