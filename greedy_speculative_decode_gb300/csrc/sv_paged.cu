@@ -173,9 +173,10 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
   if (sv_attend_workspace(pool, rows, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
   if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev) return SV_E_INVAL;
   if (workspace_bytes < need) return SV_E_NOMEM;
-  // 32-bit counts on the device: query rows, merge blocks and work items
+  // 32-bit counts on the device: query rows, and chunks of 64 positions for
+  // every kv head and tile of at least 8 query rows
   const int64_t f = (int64_t)b.n_rows * n_q_heads;
-  if (f > INT32_MAX || (f / 16 + (int64_t)b.n_seq * c.n_kv_heads) * max_splits(b, c.head_dim) > INT32_MAX)
+  if (f > INT32_MAX || (f / 8 + (int64_t)b.n_seq * c.n_kv_heads) * (b.limit() / 64 + 1) > INT32_MAX)
     return SV_E_INVAL;
   int num_sms = 0;
   const int rc = device_setup(&num_sms);
