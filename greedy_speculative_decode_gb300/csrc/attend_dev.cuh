@@ -5,17 +5,19 @@
 //   s_p = scale * q . k_p,  o = sum_p softmax(s)_p v_p,  lse = ln sum_p exp(s_p).
 // The cache is read once per tile of 8 N query rows (token rows x the query
 // heads of a kv head, packed one behind the other whatever the group size), so
-// few rows are bound by its bytes: a CTA streams chunks of four pages by TMA
-// into a ring, and four warps share each chunk.
-//   Scores, transposed: S^T = K Q^T.  Warp w takes page w: its 16 positions
-//     are the 16 rows of an mma, eight query rows its columns, so single-token
-//     decode with a group of up to eight heads wastes none of it.  K goes from
-//     8 to 16 bits in registers.
-//   The query rows' maxima over the chunk meet in shared memory, and each warp
-//     leaves its weights there, transposed on the way (stmatrix).
-//   O^T += V^T P^T: warp w takes D / 4 columns of every position, so the
-//     accumulators need no merge between warps.  A transposing load of bytes
-//     makes V's operand (four consecutive positions of a column in a word).
+// few rows are bound by its bytes.  A CTA of four warps walks a split's chunks
+// of four pages, warp w its page w, each warp by itself: its own ring of
+// asynchronous copies and its own softmax statistics and accumulators, no barrier.
+//   Scores, transposed: S^T = K Q^T.  The page's 16 positions are the 16 rows
+//     of an mma, eight query rows its columns, so single-token decode with a
+//     group of up to eight heads wastes none of it.  K goes from 8 to 16 bits
+//     in registers.
+//   Online softmax over pages; the weights are transposed in registers
+//     (movmatrix).
+//   O^T += V^T P^T, all columns.  A transposing load of bytes makes V's operand
+//     (four consecutive positions of a column in a word).
+// At the split's end the four warps' results meet in shared memory and go out
+// as the split's partial; a second kernel merges the splits.
 //
 // An 8-bit cache's exponents cost an addition each.  The key's scales its
 // score; the value's, ev, is added to the score in log2 units, t' = log2(e) s +
@@ -28,9 +30,9 @@
 // bf16 queries, and the weights are taken as the sum of two bf16 values
 // (about 2^-16), since one would shift outputs by up to half a bf16 step.
 //
-// Splits are ranges of absolute positions (attn_split_start), and a row's
+// Splits are ranges of absolute positions (attend_split_start), and a row's
 // arithmetic does not depend on the rows, sequences or tiles beside it: a
-// chunk a row does not see leaves its maximum, sum and accumulators as they
+// page a row does not see leaves its maximum, sum and accumulators as they
 // are, bit for bit.  So each row's result is the same in every batch.
 #pragma once
 #include "paged_dev.cuh"
@@ -45,23 +47,21 @@ namespace sv {
 namespace {
 
 constexpr int kAttendWarps = 4;
-constexpr int kAttendThreads = (kAttendWarps + 1) * 32;  // consumers, then the producer warp
+constexpr int kAttendThreads = kAttendWarps * 32;
 
 // A tile of query rows.
 struct AttendTile {
   int row0, f0, nf, kvh;  // the sequence's first row, the tile's first query row, the sequence's query rows
   int first;              // position of the sequence's first row
 };
-// What the producer tells the consumers of a chunk.
-struct alignas(16) AttendDesc {
-  int base, loaded, flags, split;  // first position; pages in the ring; kDesc*
-  AttendTile tile;
-  int pad[3];
-};
-// kDescTile: the first chunk of another tile; kDescLast: the split's last
-// chunk; kDescEdge: some row does not see some position, or a page is not
-// there; kDescEnd: no chunk, there are no more
-enum : int { kDescTile = 1, kDescLast = 2, kDescEdge = 4, kDescEnd = 8 };
+// (by what the rings and 32 N D / 128 accumulators a lane leave room for)
+__host__ __device__ constexpr int kAttendPerSm(int d, bool bf16, int n) {
+  const int rb = d * (bf16 ? 2 : 1);
+  if (rb == 512) return 1;
+  if (n * d >= 512) return 2;
+  if (rb == 256) return 2;
+  return n * d >= 256 ? 3 : n * d >= 128 ? 4 : 5;
+}
 
 template <int D_, int FMT_, int N_>
 struct AttendCfg {
@@ -69,36 +69,34 @@ struct AttendCfg {
   static constexpr bool kBf16 = FMT == SV_KV_BF16;
   static constexpr int RB = D * (kBf16 ? 2 : 1);  // bytes of a position's row
   static constexpr int kPageBytes = kPage * RB;
-  static constexpr int CP = kAttendWarps;         // pages per chunk: one a warp
-  static constexpr int kChunk = CP * kPage;
-  static constexpr int kStageBytes = 2 * CP * kPageBytes;
-  static constexpr int kStages = RB == 64 ? 4 : RB == 512 ? 2 : 3;
-  // CTAs per SM that registers are cut for (the rings allow 4 at rows of 64
-  // and 128 bytes, 2 at 256, 1 at 512)
-  static constexpr int kRingSm = RB <= 128 ? 4 : RB == 256 ? 2 : 1;
-  static constexpr int kRegSm = N <= 2 ? 4 : N == 4 ? 3 : 2;
-  static constexpr int kPerSm = kRingSm < kRegSm ? kRingSm : kRegSm;
+  static constexpr int kChunk = kAttendWarps * kPage;
+  static constexpr int kStageBytes = 2 * kPageBytes;
+  // pages of K and V in a warp's ring: one at hand, the others on their way.
+  // The warps of an SM together keep about 80 KB on the way.
+  static constexpr int kStages = N == 4 || RB == 512 ? 2 : RB == 256 ? 3 : 2;
+  static constexpr int kPerSm = kAttendPerSm(D, kBf16, N);  // CTAs per SM that registers are cut for
   static constexpr int NK = D / 16;               // k16 steps of a score
-  static constexpr int DW = D / kAttendWarps;     // output columns per warp
-  static constexpr int U = DW / 16;               // their 16-column units
+  static constexpr int U = D / 16;                // 16-column units of the output
   static constexpr int QR = 8 * N;                // query rows of a tile
-  static constexpr bool kQRegs = N * NK <= 8;     // query fragments stay in registers
+  static constexpr bool kQRegs = N * NK <= 16;    // query fragments stay in registers
+  // the meeting of the warps, a part of the columns at a time (8 KB of accumulators)
+  static constexpr int kColsMax = 64 / N;
+  static constexpr int kCols = kColsMax < D ? kColsMax : D;
+  static constexpr int kRounds = D / kCols;
+  static constexpr int kColStride = kCols + 4;    // floats of a query row (4 mod 16: no bank conflicts)
+  static_assert(kCols % 16 == 0 && kColStride % 16 == 4, "columns of a round");
   // shared memory
-  static constexpr int kScaleBytes = kBf16 ? 0 : 2 * CP * kPage;
-  static constexpr int kOffScale = kStages * kStageBytes;
-  static constexpr int kOffQ = kOffScale + kStages * kScaleBytes;  // query fragments [N][NK][32 lanes][2 words]
+  static constexpr int kScaleBytes = kBf16 ? 0 : 2 * kPage;        // exponents of a stage (one a position)
+  static constexpr int kRing = kAttendWarps * kStages;             // stages of all warps
+  static constexpr int kOffScale = kRing * kStageBytes;
+  static constexpr int kOffQ = kOffScale + kRing * kScaleBytes;    // query fragments [N][NK][32 lanes][2 words]
   static constexpr int kQBytes = N * NK * 256;
-  static constexpr int kPStride = kChunk * 2 + 16;                 // bytes of a query row's weights, padded against
-  static constexpr int kOffP = kOffQ + kQBytes;                    // bank conflicts
-  static constexpr int kPBytes = QR * kPStride;                    // (bf16: twice, high and low parts)
-  static constexpr int kOffMax = kOffP + kPBytes * (kBf16 ? 2 : 1);  // [QR][4] maxima of the warps
-  static constexpr int kOffSum = kOffMax + QR * 16;                // [QR][4] sums
-  static constexpr int kOffRow = kOffSum + QR * 16;                // [QR] score factors, positions, slots, maxima
-  static constexpr int kOffDesc = kOffRow + 4 * QR * 4;            // [stages] chunk descriptors
-  static constexpr int kOffBar = kOffDesc + kStages * (int)sizeof(AttendDesc);
-  static constexpr int kOffSeq = kOffBar + 2 * kStages * 8;        // [n_seq + 1] chunks before, first, row start
-  static constexpr int smem_bytes(int n_seq) { return 1024 + kOffSeq + 4 * (3 * n_seq + 2); }
-  static_assert(1024 + kOffSeq + 4 * (3 * kAttendMaxSeq + 2) <= 227 * 1024, "shared memory of a CTA");
+  static constexpr int kOffO = kOffQ + kQBytes;                    // [4 warps][QR][kColStride] accumulators
+  static constexpr int kOffMl = kOffO + kAttendWarps * QR * kColStride * 4;  // [QR][4 warps] (max, sum)
+  static constexpr int kOffRow = kOffMl + QR * 32;                 // [QR] score factors, positions, slots
+  static constexpr int kOffSeq = kOffRow + 3 * QR * 4;             // [n_seq + 1] chunks before, first, row start
+  static constexpr int smem_bytes(int n_seq) { return 128 + kOffSeq + 4 * (3 * n_seq + 2); }
+  static_assert(128 + kOffSeq + 4 * (3 * kAttendMaxSeq + 2) <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Position within a page of score row n (0 .. 15).  A value fragment's
@@ -149,19 +147,11 @@ __device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t (&r)[4]
                : "r"(addr));
 }
 
-// Two / four 8 x 8 matrices of 16-bit values, stored transposed.
-__device__ __forceinline__ void stsm_x2_trans(uint32_t addr, uint32_t r0, uint32_t r1) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0), "r"(r1)
-               : "memory");
-}
-__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0),
-               "r"(r1), "r"(r2), "r"(r3)
-               : "memory");
-}
-
-__device__ __forceinline__ int split_of(int pos, int d) {
-  return pos < kAttnRegionA ? pos / kAttnSplitA : kAttnSplitsA + (pos - kAttnRegionA) / attn_split_b(d);
+// An 8 x 8 matrix of 16-bit values, transposed across the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t r) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(r));
+  return d;
 }
 
 // The splits a range of rows t0 .. t1 of one sequence sees some position of:
@@ -171,15 +161,15 @@ struct SplitRange {
   __device__ __forceinline__ int at(int j) const { return j < n_sink ? j : lo + j - n_sink; }
 };
 // (limit: positions the block table reaches; those beyond are unseen)
-__device__ __forceinline__ SplitRange splits_seen(int t0, int t1, int window, int sinks, int limit, int d) {
+__device__ __forceinline__ SplitRange splits_seen(int t0, int t1, int window, int sinks, int limit) {
   SplitRange r = {0, 0, 0};
   t1 = min(t1, limit - 1);
   if (t1 < 0) return r;
-  const int hi = split_of(t1, d);
+  const int hi = attend_split_of(t1);
   const int64_t w0 = (int64_t)t0 - window + 1;
   if (window > 0 && w0 > 0) {
-    r.lo = w0 > t1 ? hi + 1 : split_of((int)w0, d);
-    if (sinks > 0) r.n_sink = min(r.lo, split_of(min(sinks - 1, t1), d) + 1);
+    r.lo = w0 > t1 ? hi + 1 : attend_split_of((int)w0);
+    if (sinks > 0) r.n_sink = min(r.lo, attend_split_of(min(sinks - 1, t1)) + 1);
   }
   r.n = r.n_sink + hi - r.lo + 1;
   return r;
@@ -217,24 +207,20 @@ struct AttendWork {
   int total, G;
 };
 
-// Walks a CTA's chunks in order, past chunks of which the tile sees nothing.
+// Where a CTA is in its run: a list (sequence, and x = kv head * tiles + tile),
+// the place i in it, and the number u of that chunk in the call.
 template <class C>
-struct AttendWalk {
+struct AttendPlace {
   AttendTile tile;
   ChunkList list;
-  int seq, tiles, x, i;   // x: kv head * tiles + tile of the list; i: place in the list
-  int t0, t1;             // positions of the tile's first and last token row
-  int u, end;             // the chunk's number; the CTA's last + 1
-  int base, split;
-  uint32_t mask;          // pages that some row of the tile sees
-  bool valid, fresh;      // fresh: the first chunk since the tile changed
+  int seq, tiles, x, i, u, end;
+  int t0, t1;           // positions of the tile's first and last token row
+  int vis_lo, vis_end;  // positions that some row of the tile reaches, sinks apart
 
-  __device__ __forceinline__ void start(const AttendWork<C>& wk) {
-    valid = false;
-    fresh = true;
+  __device__ __forceinline__ bool start(const AttendWork<C>& wk) {
     u = (int)((int64_t)wk.total * blockIdx.x / gridDim.x);
     end = (int)((int64_t)wk.total * (blockIdx.x + 1) / gridDim.x);
-    if (u >= end) return;
+    if (u >= end) return false;
     int lo = 0, hi = wk.p.rows.n_seq;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -244,16 +230,16 @@ struct AttendWalk {
     open_seq(wk);
     x = (u - wk.before[seq]) / list.n;
     i = (u - wk.before[seq]) % list.n;
-    open_tile(wk);
     // to the first item that begins here
-    if (i > 0)
-      while (split_of(list.at(i) * C::kChunk, C::D) == split_of(list.at(i - 1) * C::kChunk, C::D)) {
-        ++u;
-        if (++i == list.n && !next_list(wk)) return;
-        if (i == 0) break;
-      }
-    settle(wk);
+    while (i > 0 && i < list.n && split_at(i) == split_at(i - 1)) {
+      ++u;
+      ++i;
+    }
+    if (i == list.n) return next_list(wk);
+    open_tile(wk);
+    return u < end;
   }
+  __device__ __forceinline__ int split_at(int k) const { return attend_split_of(list.at(k) * C::kChunk); }
   __device__ __forceinline__ void open_seq(const AttendWork<C>& wk) {
     tile.first = wk.first[seq];
     tile.row0 = wk.start[seq];
@@ -267,9 +253,22 @@ struct AttendWalk {
     tile.f0 = x % tiles * C::QR;
     t0 = tile.first + tile.f0 / wk.G;
     t1 = tile.first + (min(tile.f0 + C::QR, tile.nf) - 1) / wk.G;
-    fresh = true;
+    vis_lo = wk.p.window > 0 ? max(t0 - wk.p.window + 1, 0) : 0;
+    vis_end = min(t1 + 1, wk.p.rows.limit());
   }
-  // the next list's first chunk (u is its number); false: the CTA's work is done
+  // The list's last place of this CTA's run + 1: the items that begin before `end`.
+  __device__ __forceinline__ int run_end() const {
+    if (list.n - i <= end - u) return list.n;
+    int e = i + (end - u);
+    while (e < list.n && split_at(e) == split_at(e - 1)) ++e;
+    return e;
+  }
+  // Behind the places i .. e - 1; false: the CTA's work is done.
+  __device__ __forceinline__ bool past(const AttendWork<C>& wk, int e) {
+    u += e - i;
+    i = e;
+    return i == list.n && next_list(wk);
+  }
   __device__ __forceinline__ bool next_list(const AttendWork<C>& wk) {
     if (u >= end) return false;
     i = 0;
@@ -281,38 +280,9 @@ struct AttendWalk {
     open_tile(wk);
     return true;
   }
-  // from the chunk at u to the next one with a page that is seen
-  __device__ __forceinline__ void settle(const AttendWork<C>& wk) {
-    valid = false;
-    for (;;) {
-      base = list.at(i) * C::kChunk;
-      const int s = split_of(base, C::D);
-      // (past the CTA's share only an item that it has begun is carried on)
-      if (u >= end && (i == 0 || split_of(list.at(i - 1) * C::kChunk, C::D) != s)) return;
-      split = s;
-      mask = 0;
-#pragma unroll
-      for (int j = 0; j < C::CP; ++j) {
-        const int a = base + j * kPage;
-        const bool vis = a <= t1 && a < wk.p.rows.limit() &&
-                         (wk.p.window <= 0 || a + kPage - 1 > t0 - wk.p.window || a < wk.p.sinks);
-        mask |= (vis ? 1u : 0u) << j;
-      }
-      if (mask) {
-        valid = true;
-        return;
-      }
-      if (!step(wk)) return;
-    }
-  }
-  __device__ __forceinline__ bool step(const AttendWork<C>& wk) {
-    ++u;
-    return ++i < list.n || next_list(wk);
-  }
-  __device__ __forceinline__ void next(const AttendWork<C>& wk) {
-    fresh = false;
-    valid = false;
-    if (step(wk)) settle(wk);
+  // Whether positions a .. a + n - 1 hold one that some row of the tile sees.
+  __device__ __forceinline__ bool sees(int a, int n, int sinks) const {
+    return a < vis_end && (a + n > vis_lo || a < sinks);
   }
 };
 
@@ -352,113 +322,38 @@ __device__ int attend_plan(const AttendParams& p, int G, int* before, int* first
   return before[S];
 }
 
-// ------------------------------------------------------------------ producer
-// One warp: lane l < CP takes page l of K, lane 16 + l that of V.  The next
-// chunk's page numbers and exponents are requested while the current one waits
-// for its place in the ring.  A descriptor goes with each chunk; the last one
-// says that there are no more.
+// ------------------------------------------------------------------ a warp's loads
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Page `page` of a kv head into a stage: 2 RB / 64 copies of 16 bytes a lane,
+// swizzled as page_off says, and an 8-bit page's exponents (one a position).
 template <class C>
-__device__ void attend_produce(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                               const AttendWork<C>& wk, uint8_t* smem, uint64_t* full, uint64_t* empty) {
-  const int lane = threadIdx.x & 31, j = lane & 15;
-  const bool is_v = lane >= 16;
-  const CUtensorMap* map = is_v ? &vmap : &kmap;
-  const uint8_t* exps = is_v ? p.v_exp : p.k_exp;
-  const uint64_t pol = policy_evict_first();
-  AttendDesc* desc = reinterpret_cast<AttendDesc*>(smem + C::kOffDesc);
-  auto page_of = [&](const AttendWalk<C>& k) {
-    if (!k.valid || j >= C::CP || !((k.mask >> j) & 1)) return -1;
-    return find_page(p.rows, p.n_pages, k.seq, k.base + j * kPage, p.status);
-  };
-  auto exps_of = [&](const AttendWalk<C>& k, int page) {
-    uint4 e = make_uint4(0u, 0u, 0u, 0u);
-    if (C::kBf16 || page < 0) return e;
-    const size_t ph = (size_t)page * p.n_kv_heads + k.tile.kvh;
-    if (p.block == 1) return __ldcg(reinterpret_cast<const uint4*>(exps + ph * kPage));
-    e.x = e.y = e.z = e.w = 0x01010101u * __ldcg(exps + ph);
-    return e;
-  };
-  AttendWalk<C> cur;
-  cur.start(wk);
-  int page = page_of(cur);
-  uint4 ex = exps_of(cur, page);
-  int n = 0;
-  for (;; ++n) {
-    const int st = n % C::kStages, use = n / C::kStages;
-    AttendWalk<C> nxt = cur;
-    int npage = -1;
-    if (cur.valid) {
-      nxt.next(wk);
-      npage = page_of(nxt);
-    }
-    const bool ok = use == 0 || mbar_wait(&empty[st], (use - 1) & 1);
-    if (!__all_sync(0xffffffffu, ok)) {
-      if (p.status && lane == 0) atomicOr(p.status, ST_TIMEOUT);
-      break;
-    }
-    const uint32_t got = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-    if (lane == 0) {
-      AttendDesc& d = desc[st];
-      d.base = cur.base;
-      d.loaded = (int)got;
-      if (cur.valid) {
-        const bool last = !nxt.valid || nxt.fresh || nxt.split != cur.split;
-        // whether every row of the tile sees every position of the chunk
-        const int cend = cur.base + C::kChunk - 1;
-        const bool all = got == (1u << C::CP) - 1u && cend <= cur.t0 &&
-                         (p.window <= 0 || cur.base > cur.t1 - p.window || cend < p.sinks);
-        d.flags = (cur.fresh ? kDescTile : 0) | (last ? kDescLast : 0) | (all ? 0 : kDescEdge);
-        d.split = cur.split;
-        if (cur.fresh || last) d.tile = cur.tile;
-      } else {
-        d.flags = kDescEnd;
-      }
-      mbar_arrive_expect_tx(&full[st], 2 * __popc(got) * C::kPageBytes);
-    }
-    if (!C::kBf16 && j < C::CP)
-      *reinterpret_cast<uint4*>(smem + C::kOffScale + st * C::kScaleBytes + (is_v ? C::CP * kPage : 0) + j * kPage) = ex;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&full[st]);  // after the descriptor and the exponents
-    if (!cur.valid) return;
-    if (page >= 0) {
-      uint8_t* dst = smem + st * C::kStageBytes + ((is_v ? C::CP : 0) + j) * C::kPageBytes;
-      const int ph = (p.page0 + page) * p.n_kv_heads + cur.tile.kvh;
-      if (C::RB == 64) {
-        tma_load_2d(dst, map, 0, ph * 8, &full[st], pol);
-      } else {
+__device__ __forceinline__ void fetch_page(const AttendParams& p, int page, int kvh, int lane, uint32_t stage,
+                                           uint32_t scale) {
+  constexpr int kUnitsRow = C::RB / 16, kPer = C::kPageBytes / 512;  // units of a row; copies of a lane
+  const size_t ph = (size_t)page * p.n_kv_heads + kvh;
+  const uint8_t* k = p.k + ph * C::kPageBytes + lane * 16;
+  const uint8_t* v = p.v + ph * C::kPageBytes + lane * 16;
 #pragma unroll
-        for (int c = 0; c < C::RB / 128; ++c) tma_load_2d(dst + c * 2048, map, c * 128, ph * kPage, &full[st], pol);
-      }
-    }
-    ex = exps_of(nxt, npage);
-    page = npage;
-    cur = nxt;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 32 * i;
+    const uint32_t dst = stage + page_off<C::RB>(e / kUnitsRow, e % kUnitsRow);
+    copy16(dst, k + 512 * i);
+    copy16(dst + C::kPageBytes, v + 512 * i);
   }
-  // (after a timeout) what is still on its way into the ring lands before the CTA ends
-  for (int k = n > C::kStages ? n - C::kStages : 0; k < n && lane == 0; ++k)
-    mbar_wait(&full[k % C::kStages], (k / C::kStages) & 1);
+  if (!C::kBf16 && p.block == 1 && lane < 2) copy16(scale + lane * kPage, (lane ? p.v_exp : p.k_exp) + ph * kPage);
 }
 
-// ------------------------------------------------------------------ consumers
-// Named barrier over `count` threads; whether any of them says `v`.
-__device__ __forceinline__ bool sync_or(int id, int count, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
-
-// The sums, maxima and accumulators of a tile in the course of an item, and
-// what a chunk does to them.  A lane (g, q4) holds positions g and g + 8 of its
-// warp's page (in pos_of_row's order) against query rows 2 q4, 2 q4 + 1 of
-// each query tile, then columns g and g + 8 of its warp's units against them.
+// ------------------------------------------------------------------ the arithmetic
+// The statistics and accumulators of a warp in the course of a split.  A lane
+// (g, q4) holds positions g and g + 8 of a page (in pos_of_row's order)
+// against query rows 2 q4, 2 q4 + 1 of each query tile, then columns g and
+// g + 8 of each unit against them.
 template <class C>
 struct AttendRows {
-  static constexpr int N = C::N, CP = C::CP, U = C::U, W = kAttendWarps;
+  static constexpr int N = C::N, U = C::U, W = kAttendWarps;
   static constexpr bool kBf16 = C::kBf16;
   const AttendParams& p;
   uint8_t* smem;
@@ -472,23 +367,22 @@ struct AttendRows {
     g = lane >> 2;
     q4 = lane & 3;
   }
-  __device__ __forceinline__ float* s_max() const { return reinterpret_cast<float*>(smem + C::kOffMax); }
-  __device__ __forceinline__ float* s_sum() const { return reinterpret_cast<float*>(smem + C::kOffSum); }
+  __device__ __forceinline__ float* s_o() const { return reinterpret_cast<float*>(smem + C::kOffO); }
+  __device__ __forceinline__ float2* s_ml() const { return reinterpret_cast<float2*>(smem + C::kOffMl); }
   __device__ __forceinline__ float* s_fac() const { return reinterpret_cast<float*>(smem + C::kOffRow); }
   __device__ __forceinline__ int* s_t() const { return reinterpret_cast<int*>(smem + C::kOffRow) + C::QR; }
   __device__ __forceinline__ int* s_slot() const { return reinterpret_cast<int*>(smem + C::kOffRow) + 2 * C::QR; }
-  __device__ __forceinline__ float* s_m() const { return reinterpret_cast<float*>(smem + C::kOffRow) + 3 * C::QR; }
   __device__ __forceinline__ const uint2* s_q() const { return reinterpret_cast<const uint2*>(smem + C::kOffQ) + lane; }
   __device__ __forceinline__ bool sees(int t, int pos) const {
     return pos <= t && (p.window <= 0 || pos > t - p.window || pos < p.sinks);
   }
 
   // A tile's queries as B fragments, the rows' score factors, positions and
-  // output slots.  A piece is 8 elements of one query row; they go to the
-  // lanes and k16 steps that meet the same elements of K (a lane's 16-byte
-  // unit of a key row, four elements a step).
+  // output slots (all warps).  A piece is 8 elements of one query row; they go
+  // to the lanes and k16 steps that meet the same elements of K (a lane's
+  // 16-byte unit of a key row, four elements a step).
   __device__ __forceinline__ void queries(const AttendTile& it, int G) {
-    constexpr int kPieces = C::QR * C::D / 8, T = W * 32;
+    constexpr int kPieces = C::QR * C::D / 8, T = kAttendThreads;
     constexpr int kPer = (kPieces + T - 1) / T, kBatch = kPer < 4 ? kPer : 4;
 #pragma unroll 1
     for (int u0 = 0; u0 < kPer; u0 += kBatch) {
@@ -540,16 +434,6 @@ struct AttendRows {
       }
     }
   }
-
-  __device__ __forceinline__ void open() {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      m_run[n][0] = m_run[n][1] = -INFINITY;
-      l_run[n][0] = l_run[n][1] = 0.0f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) o[u][n][0] = o[u][n][1] = o[u][n][2] = o[u][n][3] = 0.0f;
-    }
-  }
   __device__ __forceinline__ void keep_queries() {
     if constexpr (C::kQRegs) {
 #pragma unroll
@@ -561,162 +445,22 @@ struct AttendRows {
     }
   }
 
-  // Scores of this warp's page, in log2 units with the value's exponent added,
-  // -inf where a row does not see them, and their maxima.  iv: 2^-ev.
-  template <bool kEdge>
-  __device__ __forceinline__ void scores(uint32_t kbase, const uint8_t* sc, int base, uint32_t loaded,
-                                         float (&s)[N][4], float (&iv)[2]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-    const bool have = !kEdge || ((loaded >> warp) & 1);
-    const int pos = pos_of_row<kBf16>(g), pos8 = pos_of_row<kBf16>(g + 8);
-    if (have) {
-      const uint32_t kp = kbase + warp * C::kPageBytes;
-      constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
-      constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        uint32_t x[2][4];
-        const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[h][0]), "=r"(x[h][1]), "=r"(x[h][2]), "=r"(x[h][3])
-                       : "r"(kp + page_off<C::RB>(h ? pos8 : pos, c)));
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            a[h] = kBf16 ? x[h][(2 * k) & 3] : f16x2_of_lo(x[h][k & 3]);
-            a[2 + h] = kBf16 ? x[h][(2 * k + 1) & 3] : f16x2_of_hi(x[h][k & 3]);
-          }
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int f = n * C::NK + u * kSteps + k;
-            if constexpr (C::kQRegs) {
-              mma_16<kBf16>(s[n], a, qr[f][0], qr[f][1]);
-            } else {
-              const uint2 b = s_q()[f * 32];
-              mma_16<kBf16>(s[n], a, b.x, b.y);
-            }
-          }
-        }
-      }
-    }
-    float ks[2], ev[2];
-    if (!kBf16) {  // positions pos and pos + 2: two bytes of a word of the page's exponents
-      const int sh = 8 * (pos & 3);
-      const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + warp * kPage + (pos & ~3)) >> sh;
-      const uint32_t vw = *reinterpret_cast<const uint32_t*>(sc + (CP + warp) * kPage + (pos & ~3)) >> sh;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t bk = (kw >> (16 * h)) & 255u, bv = (vw >> (16 * h)) & 255u;
-        ks[h] = __uint_as_float(bk << 23);  // (255: infinity, times a score of zero codes: NaN)
-        ev[h] = bv == kExpNaN ? __uint_as_float(0x7fffffffu) : (float)((int)bv - 127);
-        iv[h] = exp_byte_inverse((int)bv);
-      }
-    }
+  __device__ __forceinline__ void open() {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const float2 f = reinterpret_cast<const float2*>(s_fac())[n * 4 + q4];
-      const int2 t = kEdge ? reinterpret_cast<const int2*>(s_t())[n * 4 + q4] : make_int2(0, 0);
+      m_run[n][0] = m_run[n][1] = -INFINITY;
+      l_run[n][0] = l_run[n][1] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& x = s[n][2 * h + c];
-          const float fc = c ? f.y : f.x;
-          x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[h]), ev[h]);
-          if (kEdge) x = have && sees(c ? t.y : t.x, base + warp * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
-        }
-        float mx = fmaxf(s[n][c], s[n][2 + c]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        if (g == 0) s_max()[(n * 8 + 2 * q4 + c) * W + warp] = mx;
-      }
-    }
-  }
-
-  // The scores' weights against the rows' running maxima, to shared memory
-  // ([query row][position]); accumulators and sums are scaled to the new maxima.
-  template <bool kEdge>
-  __device__ __forceinline__ void weights(const float (&s)[N][4], const float (&iv)[2], bool last) {
-    uint32_t hi[N][2], lo[N][2];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float pv[4];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int qi = n * 8 + 2 * q4 + c;
-        const float4 a = reinterpret_cast<const float4*>(s_max())[qi];
-        const float m = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), m_run[n][c]);
-        // a row that has seen nothing yet: every weight is 2^-inf = 0
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const float alpha = m == m_run[n][c] ? 1.0f : ex2(__fsub_rn(m_run[n][c], ref));
-        m_run[n][c] = m;
-        float sum = 0.0f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = s[n][2 * h + c], e = ex2(__fsub_rn(x, ref));
-          pv[2 * h + c] = e;
-          if (kBf16)
-            sum = __fadd_rn(sum, e);
-          else if (kEdge)  // (the exponent of a masked place may be anything)
-            sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[h], sum);
-          else
-            sum = __fmaf_rn(e, iv[h], sum);
-        }
-        l_run[n][c] = __fmaf_rn(l_run[n][c], alpha, sum);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          o[u][n][c] = __fmul_rn(o[u][n][c], alpha);
-          o[u][n][2 + c] = __fmul_rn(o[u][n][2 + c], alpha);
-        }
-        if (last) {
-          float l = l_run[n][c];
-          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 4));
-          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 8));
-          l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 16));
-          if (g == 0) {
-            s_sum()[qi * W + warp] = l;
-            if (warp == 0) s_m()[qi] = m;
-          }
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (kBf16) {
-          hi[n][h] = pack_bf16x2(pv[2 * h], pv[2 * h + 1]);
-          lo[n][h] = pack_bf16x2(__fsub_rn(pv[2 * h], bf16r(pv[2 * h])), __fsub_rn(pv[2 * h + 1], bf16r(pv[2 * h + 1])));
-        } else {
-          hi[n][h] = pack_f16x2(pv[2 * h], pv[2 * h + 1]);
-        }
-      }
-    }
-    // matrix h: score rows 8 h .. of the page; lane l gives the row address of
-    // query row l mod 8, matrix l / 8 (and the next query tile's above 16)
-    const uint32_t at = smem_u32(smem + C::kOffP) + (uint32_t)((lane & 7) * C::kPStride + (warp * kPage + ((lane >> 3) & 1) * 8) * 2);
-    if constexpr (N == 1) {
-      stsm_x2_trans(at, hi[0][0], hi[0][1]);
-      if (kBf16) stsm_x2_trans(at + C::kPBytes, lo[0][0], lo[0][1]);
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; n += 2) {
-        const uint32_t a2 = at + (uint32_t)((n + (lane >> 4)) * 8 * C::kPStride);
-        stsm_x4_trans(a2, hi[n][0], hi[n][1], hi[n + 1][0], hi[n + 1][1]);
-        if (kBf16) stsm_x4_trans(a2 + C::kPBytes, lo[n][0], lo[n][1], lo[n + 1][0], lo[n + 1][1]);
-      }
+      for (int u = 0; u < U; ++u) o[u][n][0] = o[u][n][1] = o[u][n][2] = o[u][n][3] = 0.0f;
     }
   }
 
   // An infinity or NaN of a bf16 page in a place that some row does not see
   // must not meet that row's weight of zero: it is taken out here and added to
   // the rows that see it.  (a: columns g, g + 8 of unit u, positions 2 q4, 2 q4
-  // + 1 and 8 more of page j; the accumulators of these columns are held by
+  // + 1 and 8 more of the page; the accumulators of these columns are held by
   // the same quad of lanes.)
-  __device__ __forceinline__ void set_apart(int base, int j, int u, uint32_t (&a)[4]) {
+  __device__ __forceinline__ void set_apart(int base, int u, uint32_t (&a)[4]) {
     auto bad = [](uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; };
     if (!__any_sync(0xffffffffu, bad(a[0]) || bad(a[1]) || bad(a[2]) || bad(a[3]))) return;
     for (int src = 0; src < 4; ++src)
@@ -726,7 +470,7 @@ struct AttendRows {
         for (int e = 0; e < 2; ++e) {
           const uint32_t b = e ? w & 0xffff0000u : w << 16;
           if ((b & 0x7f800000u) != 0x7f800000u) continue;
-          const int pos = base + j * kPage + (k >> 1) * 8 + 2 * src + e;
+          const int pos = base + (k >> 1) * 8 + 2 * src + e;
 #pragma unroll
           for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -744,164 +488,320 @@ struct AttendRows {
     }
   }
 
-  // O^T += V^T P^T on this warp's columns.
+  // One page: scores in log2 units with the value's exponent added, -inf where
+  // a row does not see the position; the running maxima and sums; O^T.
+  // kEdge: some row does not see some position.
   template <bool kEdge>
-  __device__ __forceinline__ void values(uint32_t vbase, int base, uint32_t loaded) {
-    const uint32_t pt = smem_u32(smem + C::kOffP) + (uint32_t)((lane & 7) * C::kPStride + (lane >> 3) * 16);
+  __device__ __forceinline__ void page(uint32_t kp, uint32_t vp, const uint8_t* sc, int base, uint32_t exps) {
+    float s[N][4];
 #pragma unroll
-    for (int j = 0; j < CP; j += 2) {
-      if (kEdge && !((loaded >> j) & 3u)) continue;
-      // the weights of pages j and j + 1: (b0, b1) of each, for every query tile
-      uint32_t b[N][4], bl[kBf16 ? N : 1][4];
+    for (int n = 0; n < N; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    const int pos = pos_of_row<kBf16>(g), pos8 = pos_of_row<kBf16>(g + 8);
+    constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
+    constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const uint32_t at = pt + (uint32_t)(n * 8 * C::kPStride + j * kPage * 2);
-        ldsm_x4(at, b[n][0], b[n][1], b[n][2], b[n][3]);
-        if (kBf16) ldsm_x4(at + C::kPBytes, bl[kBf16 ? n : 0][0], bl[kBf16 ? n : 0][1], bl[kBf16 ? n : 0][2], bl[kBf16 ? n : 0][3]);
+    for (int u = 0; u < kUnits; ++u) {
+      uint32_t x[2][4];
+      const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[h][0]), "=r"(x[h][1]), "=r"(x[h][2]), "=r"(x[h][3])
+                     : "r"(kp + page_off<C::RB>(h ? pos8 : pos, c)));
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t a[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[h] = kBf16 ? x[h][(2 * k) & 3] : f16x2_of_lo(x[h][k & 3]);
+          a[2 + h] = kBf16 ? x[h][(2 * k + 1) & 3] : f16x2_of_hi(x[h][k & 3]);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int f = n * C::NK + u * kSteps + k;
+          if constexpr (C::kQRegs) {
+            mma_16<kBf16>(s[n], a, qr[f][0], qr[f][1]);
+          } else {
+            const uint2 b = s_q()[f * 32];
+            mma_16<kBf16>(s[n], a, b.x, b.y);
+          }
+        }
+      }
+    }
+    float ks[2], ev[2], iv[2];
+    if (!kBf16) {  // positions pos and pos + 2: two bytes of a word of the page's exponents
+      uint32_t kw, vw;
+      if (p.block == 1) {
+        kw = *reinterpret_cast<const uint32_t*>(sc + (pos & ~3)) >> (8 * (pos & 3));
+        vw = *reinterpret_cast<const uint32_t*>(sc + kPage + (pos & ~3)) >> (8 * (pos & 3));
+      } else {
+        kw = (exps & 255u) * 0x00010001u;
+        vw = (exps >> 8) * 0x00010001u;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t r[4];
-        if constexpr (!kBf16)
-          ldsm_b8_x2_trans(vbase + (j + (lane >> 4)) * C::kPageBytes + page_off<C::RB>(lane & 15, warp * U + u), r);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t bk = (kw >> (16 * h)) & 255u, bv = (vw >> (16 * h)) & 255u;
+        ks[h] = __uint_as_float(bk << 23);  // (255: infinity, times a score of zero codes: NaN)
+        ev[h] = bv == kExpNaN ? __uint_as_float(0x7fffffffu) : (float)((int)bv - 127);
+        iv[h] = exp_byte_inverse((int)bv);
+      }
+    }
+    uint32_t hi[N][2], lo[kBf16 ? N : 1][2];
+    bool moved = false;
+    float alpha[N][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // page j + h
-          if (kEdge && !((loaded >> (j + h)) & 1u)) continue;
-          uint32_t a[4];
-          if constexpr (!kBf16) {
-            a[0] = f16x2_of_lo(r[2 * h]);
-            a[1] = f16x2_of_lo(r[2 * h + 1]);
-            a[2] = f16x2_of_hi(r[2 * h]);
-            a[3] = f16x2_of_hi(r[2 * h + 1]);
-            if (kEdge) {
-              // what lies in places that a row does not see may be any byte: a
-              // NaN code must not meet its weight of zero
-              const uint32_t top = 0x5f005f00u;  // 448
+    for (int n = 0; n < N; ++n) {
+      const float2 f = reinterpret_cast<const float2*>(s_fac())[n * 4 + q4];
+      const int2 t = kEdge ? reinterpret_cast<const int2*>(s_t())[n * 4 + q4] : make_int2(0, 0);
+      float pv[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) asm("min.f16x2 %0, %0, %1;" : "+r"(a[k]) : "r"(top));
-            }
-          } else {
-            ldsm_x4_trans(vbase + (j + h) * C::kPageBytes + page_off<C::RB>(lane & 15, (warp * U + u) * 2 + (lane >> 4)),
-                          a[0], a[2], a[1], a[3]);
-            if (kEdge) set_apart(base, j + h, u, a);
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float& x = s[n][2 * h + c];
+          const float fc = c ? f.y : f.x;
+          x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[h]), ev[h]);
+          if (kEdge) x = sees(c ? t.y : t.x, base + (h ? pos8 : pos)) ? x : -INFINITY;
+        }
+        float m = fmaxf(s[n][c], s[n][2 + c]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        m = fmaxf(m, m_run[n][c]);
+        // a row that has seen nothing yet: every weight is 2^-inf = 0
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const bool same = m == m_run[n][c];
+        alpha[n][c] = same ? 1.0f : ex2(__fsub_rn(m_run[n][c], ref));
+        moved |= !same;
+        m_run[n][c] = m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = s[n][2 * h + c], e = ex2(__fsub_rn(x, ref));
+          pv[2 * h + c] = e;
+          if (kBf16)
+            sum = __fadd_rn(sum, e);
+          else if (kEdge)  // (the exponent of a masked place may be anything)
+            sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[h], sum);
+          else
+            sum = __fmaf_rn(e, iv[h], sum);
+        }
+        l_run[n][c] = __fmaf_rn(l_run[n][c], alpha[n][c], sum);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (kBf16) {
+          hi[n][h] = transposed(pack_bf16x2(pv[2 * h], pv[2 * h + 1]));
+          lo[kBf16 ? n : 0][h] = transposed(pack_bf16x2(__fsub_rn(pv[2 * h], bf16r(pv[2 * h])),
+                                                        __fsub_rn(pv[2 * h + 1], bf16r(pv[2 * h + 1]))));
+        } else {
+          hi[n][h] = transposed(pack_f16x2(pv[2 * h], pv[2 * h + 1]));
+        }
+      }
+    }
+    // (a maximum seldom moves after a split's first pages; times one is skipped)
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[u][n][e] = __fmul_rn(o[u][n][e], alpha[n][e & 1]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u += 2) {
+      uint32_t r[4];
+      if constexpr (!kBf16) ldsm_b8_x2_trans(vp + page_off<C::RB>(lane & 15, u + (lane >> 4)), r);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t a[4];
+        if constexpr (!kBf16) {
+          a[0] = f16x2_of_lo(r[2 * y]);
+          a[1] = f16x2_of_lo(r[2 * y + 1]);
+          a[2] = f16x2_of_hi(r[2 * y]);
+          a[3] = f16x2_of_hi(r[2 * y + 1]);
+          if (kEdge) {
+            // what lies in places that a row does not see may be any byte: a
+            // NaN code must not meet its weight of zero
+            const uint32_t top = 0x5f005f00u;  // 448
+#pragma unroll
+            for (int k = 0; k < 4; ++k) asm("min.f16x2 %0, %0, %1;" : "+r"(a[k]) : "r"(top));
           }
+        } else {
+          ldsm_x4_trans(vp + page_off<C::RB>(lane & 15, (u + y) * 2 + (lane >> 4)), a[0], a[2], a[1], a[3]);
+          if (kEdge) set_apart(base, u + y, a);
+        }
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            mma_16<kBf16>(o[u][n], a, b[n][2 * h], b[n][2 * h + 1]);
-            if (kBf16) mma_16<kBf16>(o[u][n], a, bl[kBf16 ? n : 0][2 * h], bl[kBf16 ? n : 0][2 * h + 1]);
-          }
+        for (int n = 0; n < N; ++n) {
+          mma_16<kBf16>(o[u + y][n], a, hi[n][0], hi[n][1]);
+          if (kBf16) mma_16<kBf16>(o[u + y][n], a, lo[kBf16 ? n : 0][0], lo[kBf16 ? n : 0][1]);
         }
       }
     }
   }
 
-  // The item's partial: accumulators from every warp, (max, sum) from the first threads.
+  // The split's partial: (max, sum) and accumulators of the four warps merged
+  // in warp order, a part of the columns at a time.
   __device__ __forceinline__ void partial(int split) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int slot = s_slot()[n * 8 + 2 * q4 + c];
-        if (slot < 0) continue;
-        float* dst = p.part_o + ((size_t)slot * p.max_splits + split) * C::D + warp * C::DW + g;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          dst[16 * u] = o[u][n][c];
-          dst[16 * u + 8] = o[u][n][2 + c];
-        }
+        float l = l_run[n][c];
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 4));
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 8));
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 16));
+        if (g == 0) s_ml()[(n * 8 + 2 * q4 + c) * W + warp] = make_float2(m_run[n][c], l);
       }
+    constexpr int kUR = U / C::kRounds;            // units a round
+    constexpr int kV = C::kCols / 4;               // float4 columns of a query row
     const int tid = threadIdx.x;
-    if (tid < C::QR && s_slot()[tid] >= 0) {
-      const float4 l = reinterpret_cast<const float4*>(s_sum())[tid];
-      p.part_ml[(size_t)s_slot()[tid] * p.max_splits + split] =
-          make_float2(s_m()[tid], __fadd_rn(__fadd_rn(l.x, l.y), __fadd_rn(l.z, l.w)));
+#pragma unroll
+    for (int rd = 0; rd < C::kRounds; ++rd) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float* dst = s_o() + (warp * C::QR + n * 8 + 2 * q4 + c) * C::kColStride + g;
+#pragma unroll
+          for (int u = 0; u < kUR; ++u) {
+            dst[16 * u] = o[rd * kUR + u][n][c];
+            dst[16 * u + 8] = o[rd * kUR + u][n][2 + c];
+          }
+        }
+      named_sync(2, kAttendThreads);
+      for (int e = tid; e < C::QR * kV; e += kAttendThreads) {
+        const int qi = e / kV, v = e % kV, slot = s_slot()[qi];
+        if (slot < 0) continue;
+        const float2* ml = s_ml() + qi * W;
+        float M = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w].x);
+        const float ref = M == -INFINITY ? 0.0f : M;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float f = ex2(__fsub_rn(ml[w].x, ref));
+          const float4 x = *reinterpret_cast<const float4*>(s_o() + (w * C::QR + qi) * C::kColStride + 4 * v);
+          l = __fmaf_rn(ml[w].y, f, l);
+          a.x = __fmaf_rn(x.x, f, a.x);
+          a.y = __fmaf_rn(x.y, f, a.y);
+          a.z = __fmaf_rn(x.z, f, a.z);
+          a.w = __fmaf_rn(x.w, f, a.w);
+        }
+        const size_t at = (size_t)slot * p.max_splits + split;
+        if (rd == 0 && v == 0) p.part_ml[at] = make_float2(M, l);
+        *reinterpret_cast<float4*>(p.part_o + at * C::D + rd * C::kCols + 4 * v) = a;
+      }
+      named_sync(2, kAttendThreads);
     }
   }
 };
 
+// A CTA's run, list by list.
 template <class C>
-__device__ void attend_consume(const AttendParams& p, int G, uint8_t* smem, uint64_t* full, uint64_t* empty) {
+__device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8_t* smem) {
+  constexpr int S = C::kStages;
+  AttendPlace<C> at;
+  if (!at.start(wk)) return;
   AttendRows<C> rows(p, smem);
-  const AttendDesc* desc = reinterpret_cast<const AttendDesc*>(smem + C::kOffDesc);
-  constexpr int T = kAttendWarps * 32;
-  for (int i = 0;; ++i) {
-    const int st = i % C::kStages;
-    // A warp whose wait ran out says so at the chunk's first barrier, where all
-    // of them then leave.
-    const bool ok = mbar_wait(&full[st], (i / C::kStages) & 1);
-    const AttendDesc& d = desc[st];
-    const int flags = ok ? d.flags : kDescEnd;
-    auto timed_out = [&](bool mine) {
-      const bool any = sync_or(2, T, mine);
-      if (any && p.status && threadIdx.x == 0) atomicOr(p.status, ST_TIMEOUT);
-      return any;
+  const int warp = rows.warp, lane = rows.lane;
+  const uint32_t ring = smem_u32(smem) + warp * S * C::kStageBytes;
+  const uint8_t* scales = smem + C::kOffScale + warp * S * C::kScaleBytes;
+  const uint32_t scales_at = smem_u32(scales);
+  for (;;) {
+    const int run = at.run_end();
+    const int* table = p.rows.table + (size_t)at.seq * p.rows.table_stride;
+    // This warp's page of place j of the list: its number, -1 where the tile
+    // sees nothing of it (or there is none)
+    auto page_of = [&](int j) {
+      if (j >= run) return -1;
+      const int a = at.list.at(j) * C::kChunk + warp * kPage;
+      if (!at.sees(a, kPage, p.sinks)) return -1;
+      const int pg = __ldg(table + a / kPage);
+      if ((uint32_t)pg < (uint32_t)p.n_pages) return pg;
+      if (p.status && lane == 0) atomicOr(p.status, ST_BAD_PAGE);
+      return -1;
     };
-    if (flags & kDescEnd) {
-      timed_out(!ok);
-      return;
-    }
-    const int base = d.base;
-    const uint32_t loaded = (uint32_t)d.loaded;
-    const bool last = flags & kDescLast, tile = flags & kDescTile;
-    if (tile) {
-      if (timed_out(false)) return;  // and every warp is done with the last tile's queries
-      rows.queries(d.tile, G);
-      named_sync(2, T);
-      rows.keep_queries();
-      rows.open();
-    }
-    const uint32_t kbase = smem_u32(smem + st * C::kStageBytes), vbase = kbase + C::CP * C::kPageBytes;
-    const uint8_t* sc = smem + C::kOffScale + st * C::kScaleBytes;
-    auto chunk = [&](auto edge) {
-      constexpr bool kEdge = decltype(edge)::value;
-      float s[C::N][4], iv[2];
-      rows.template scores<kEdge>(kbase, sc, base, loaded, s, iv);
-      if (tile) named_sync(2, T); else if (timed_out(false)) return false;
-      rows.template weights<kEdge>(s, iv, last);
-      named_sync(2, T);
-      rows.template values<kEdge>(vbase, base, loaded);
-      return true;
+    uint32_t have = 0, exps[S];  // bit k, exps[k]: of place i + k
+    int issued = 0;
+    auto request = [&](int j, int pg, uint32_t& ex) {
+      if (pg >= 0) {
+        const int st = issued % S;
+        fetch_page<C>(p, pg, at.tile.kvh, lane, ring + st * C::kStageBytes, scales_at + st * C::kScaleBytes);
+        if (!C::kBf16 && p.block != 1) {
+          const size_t ph = (size_t)pg * p.n_kv_heads + at.tile.kvh;
+          ex = (uint32_t)__ldg(p.k_exp + ph) | (uint32_t)__ldg(p.v_exp + ph) << 8;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++issued;
     };
-    if (!((flags & kDescEdge) ? chunk(std::true_type{}) : chunk(std::false_type{}))) return;
-    fence_proxy_async_smem();  // reads of the stage precede its next TMA write
-    __syncwarp();
-    const int split = d.split;
-    if (rows.lane == 0) mbar_arrive(&empty[st]);
-    if (last) {
-      rows.partial(split);
-      rows.open();
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) {
+      const int pg = page_of(at.i + k);
+      have |= (pg >= 0 ? 1u : 0u) << k;
+      request(at.i + k, pg, exps[k]);
     }
+    int ahead = page_of(at.i + S - 1);
+    rows.queries(at.tile, wk.G);
+    named_sync(2, kAttendThreads);
+    rows.keep_queries();
+    rows.open();
+    bool any = false;  // the item has a chunk that the tile sees
+    int st = 0;
+    for (int i = at.i; i < run; ++i) {
+      // the page S - 1 places on, into the stage that place i - 1 had (every lane has done with it)
+      __syncwarp();
+      have |= (ahead >= 0 ? 1u : 0u) << (S - 1);
+      request(i + S - 1, ahead, exps[S - 1]);
+      ahead = page_of(i + S);
+      const int chunk = at.list.at(i) * C::kChunk, base = chunk + warp * kPage;
+      any |= at.sees(chunk, C::kChunk, p.sinks);
+      if (have & 1u) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();
+        const uint32_t kp = ring + st * C::kStageBytes;
+        const uint8_t* sc = scales + st * C::kScaleBytes;
+        // whether every row of the tile sees every position of the page
+        const bool all = base + kPage - 1 <= at.t0 &&
+                         (p.window <= 0 || base > at.t1 - p.window || base + kPage - 1 < p.sinks);
+        if (all) rows.template page<false>(kp, kp + C::kPageBytes, sc, base, exps[0]);
+        else rows.template page<true>(kp, kp + C::kPageBytes, sc, base, exps[0]);
+      }
+      have >>= 1;
+#pragma unroll
+      for (int k = 0; k < S - 1; ++k) exps[k] = exps[k + 1];
+      st = st + 1 == S ? 0 : st + 1;
+      const int split = attend_split_of(chunk);
+      if (i + 1 == run || attend_split_of(at.list.at(i + 1) * C::kChunk) != split) {
+        if (any) {
+          rows.partial(split);
+          rows.open();
+        }
+        any = false;
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!at.past(wk, run)) return;
+    named_sync(2, kAttendThreads);  // every warp is done with this tile's queries
   }
 }
 
 template <int D, int FMT, int N>
-__global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm)
-    k_attend(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttendParams p) {
+__global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) k_attend(const AttendParams p) {
   using C = AttendCfg<D, FMT, N>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* empty = full + C::kStages;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  // (an offset, not a rounded address: the compiler keeps knowing that this is shared memory)
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 127u);
   int* before = reinterpret_cast<int*>(smem + C::kOffSeq);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 2);  // the bytes' announcement, and the mask and exponents
-      mbar_init(&empty[i], kAttendWarps);
-    }
-    fence_barrier_init();
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
-  }
   pdl_trigger();
   pdl_wait();
   const int S = p.rows.n_seq, G = p.n_q_heads / p.n_kv_heads;
   int *first = before + S + 1, *start = first + S;  // (S + 1 starts)
   AttendWork<C> wk{p, before, first, start, 0, G};
   wk.total = attend_plan<C>(p, G, before, first, start);
-  if (threadIdx.x >= kAttendWarps * 32)
-    attend_produce<C>(p, kmap, vmap, wk, smem, full, empty);
-  else
-    attend_consume<C>(p, G, smem, full, empty);
+  attend_cta<C>(p, wk, smem);
 }
 
 // The splits of one (row, query head) merged: out = sum_s o_s 2^(m_s - M) /
@@ -920,7 +820,7 @@ __global__ void __launch_bounds__(128) k_attend_merge(const AttendParams p) {
   int seq, i;
   if (!find_row(p.rows, r, seq, i)) return;
   const int t = first_of(p.rows, seq) + i;
-  const SplitRange sr = splits_seen(t, t, p.window, p.sinks, p.rows.limit(), D);
+  const SplitRange sr = splits_seen(t, t, p.window, p.sinks, p.rows.limit());
   const size_t base = ((size_t)r * p.n_q_heads + hq) * p.max_splits;
   float M = -INFINITY;
   for (int j = threadIdx.x; j < sr.n; j += 128) M = fmaxf(M, __ldcg(&p.part_ml[base + sr.at(j)].x));
@@ -972,7 +872,7 @@ __global__ void __launch_bounds__(128) k_attend_merge(const AttendParams p) {
 }
 
 template <int D, int FMT, int N>
-cudaError_t attend_launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttendParams& p, int num_sms,
+cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
                             cudaStream_t s, bool pdl) {
   using C = AttendCfg<D, FMT, N>;
   const int smem = C::smem_bytes(p.rows.n_seq);
@@ -1004,7 +904,7 @@ cudaError_t attend_launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, k_attend<D, FMT, N>, kmap, vmap, p);
+  e = cudaLaunchKernelEx(&cfg, k_attend<D, FMT, N>, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)((int64_t)p.rows.n_rows * p.n_q_heads));
   cfg.blockDim = dim3(128);
@@ -1013,18 +913,17 @@ cudaError_t attend_launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   return cudaLaunchKernelEx(&cfg, k_attend_merge<D>, p);
 }
 
-// Query tiles of 8, 16, 32 or 64 rows (32 at most for heads of 256): the
-// smallest that hold a sequence's rows at once, so that its pages are read and
-// widened once.  A row's result is the same in each (the columns of an mma do
-// not meet).
+// Query tiles of 8, 16 or 32 rows (16 at most for heads of 256): the smallest
+// that hold a sequence's rows at once, so that its pages are read and widened
+// as seldom as accumulators in registers allow.  A row's result is the same in
+// each (the columns of an mma do not meet).
 template <int D, int FMT>
-cudaError_t attend_launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttendParams& p, int num_sms,
+cudaError_t attend_launch(const AttendParams& p, int num_sms,
                           cudaStream_t s, bool pdl) {
   const int64_t f = (int64_t)p.rows.max_rows * (p.n_q_heads / p.n_kv_heads);
-  if (f <= 8) return attend_launch_t<D, FMT, 1>(kmap, vmap, p, num_sms, s, pdl);
-  if (f <= 16) return attend_launch_t<D, FMT, 2>(kmap, vmap, p, num_sms, s, pdl);
-  if (f <= 32 || D == 256) return attend_launch_t<D, FMT, 4>(kmap, vmap, p, num_sms, s, pdl);
-  return attend_launch_t<D, FMT, D == 256 ? 4 : 8>(kmap, vmap, p, num_sms, s, pdl);
+  if (f <= 8) return attend_launch_t<D, FMT, 1>(p, num_sms, s, pdl);
+  if (f <= 16 || D == 256) return attend_launch_t<D, FMT, 2>(p, num_sms, s, pdl);
+  return attend_launch_t<D, FMT, D == 256 ? 2 : 4>(p, num_sms, s, pdl);
 }
 
 template <int D, int FMT, int N>
@@ -1036,10 +935,8 @@ cudaError_t attend_prepare_t() {
 template <int D, int FMT>
 cudaError_t attend_prepare() {
   cudaError_t e;
-  if ((e = attend_prepare_t<D, FMT, 1>()) != cudaSuccess || (e = attend_prepare_t<D, FMT, 2>()) != cudaSuccess ||
-      (e = attend_prepare_t<D, FMT, 4>()) != cudaSuccess)
-    return e;
-  return attend_prepare_t<D, FMT, D == 256 ? 4 : 8>();
+  if ((e = attend_prepare_t<D, FMT, 1>()) != cudaSuccess || (e = attend_prepare_t<D, FMT, 2>()) != cudaSuccess) return e;
+  return attend_prepare_t<D, FMT, D == 256 ? 2 : 4>();
 }
 
 }  // namespace

@@ -8,10 +8,9 @@ cudaError_t prepare_attend_128() {
   return e != cudaSuccess ? e : attend_prepare<128, SV_KV_E4M3>();
 }
 
-cudaError_t launch_attend_128(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttendParams& p, int fmt,
-                             int num_sms, cudaStream_t s, bool pdl) {
-  return fmt == SV_KV_BF16 ? attend_launch<128, SV_KV_BF16>(kmap, vmap, p, num_sms, s, pdl)
-                           : attend_launch<128, SV_KV_E4M3>(kmap, vmap, p, num_sms, s, pdl);
+cudaError_t launch_attend_128(const AttendParams& p, int fmt, int num_sms, cudaStream_t s, bool pdl) {
+  return fmt == SV_KV_BF16 ? attend_launch<128, SV_KV_BF16>(p, num_sms, s, pdl)
+                           : attend_launch<128, SV_KV_E4M3>(p, num_sms, s, pdl);
 }
 
 }  // namespace sv

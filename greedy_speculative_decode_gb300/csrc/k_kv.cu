@@ -103,7 +103,6 @@ __global__ void __launch_bounds__(256) k_kv_write(const KvPool c, const RowBatch
       c.v_exp[row] = (uint8_t)bv;
     }
   }
-  asm volatile("fence.proxy.async.global;" ::: "memory");  // attention reads the pages through TMA
 }
 
 // One exponent for each page.  A block of 16 x D / 8 threads takes a page of
@@ -180,7 +179,6 @@ __global__ void __launch_bounds__(2 * D) k_kv_write_page(const KvPool c, const R
     }
     __syncthreads();  // every thread has read the old exponent and s_max
     if (tid == 0) exps[ph] = (uint8_t)bn;
-    asm volatile("fence.proxy.async.global;" ::: "memory");  // attention reads the pages through TMA
   }
 }
 

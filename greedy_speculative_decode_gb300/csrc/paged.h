@@ -42,15 +42,27 @@ cudaError_t launch_kv_fetch(const KvPool& c, const RowBatch& b, bf16* k, int64_t
 // sequence in shared memory.
 constexpr int kAttendMaxSeq = 1024;
 
+// Splits of the attention's work: ranges of absolute positions, 256 each below
+// position 4096 and 512 beyond.
+constexpr int kAttendSplitA = 256, kAttendRegionA = 4096, kAttendSplitB = 512;
+__host__ __device__ inline int attend_split_of(int pos) {
+  return pos < kAttendRegionA ? pos / kAttendSplitA
+                              : kAttendRegionA / kAttendSplitA + (pos - kAttendRegionA) / kAttendSplitB;
+}
+
+__host__ __device__ inline int attend_split_end(int split) {  // first position behind it
+  constexpr int n = kAttendRegionA / kAttendSplitA;
+  return split < n ? (split + 1) * kAttendSplitA : kAttendRegionA + (split + 1 - n) * kAttendSplitB;
+}
+
 struct AttendParams {
   RowBatch rows;
   const bf16* q;  // [n_rows, n_q_heads, head_dim], rows q_stride elements apart
   bf16* out;
   int64_t q_stride, out_stride;
   float* lse;  // [n_rows, n_q_heads] natural-log sum of exponentials, or null
-  const uint8_t *k_exp, *v_exp;
+  const uint8_t *k, *v, *k_exp, *v_exp;
   int n_q_heads, n_kv_heads, n_pages, block, window, sinks;
-  int page0;         // page of the tensor maps that is page 0 of this pool
   float scale_log2;  // softmax scale * log2(e)
   int max_splits;
   float2* part_ml;  // [n_rows, n_q_heads, max_splits] (running max in log2 units, sum)
@@ -58,10 +70,7 @@ struct AttendParams {
   int* status;      // or null
 };
 
-// Tensor map of a pool's codes as the attention kernel loads them.
-bool make_kv_map(CUtensorMap* m, const void* codes, int row_bytes, uint64_t rows);
 cudaError_t prepare_attend_kernels();
-cudaError_t launch_attend(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttendParams& p, int fmt,
-                          int head_dim, int num_sms, cudaStream_t s, bool pdl);
+cudaError_t launch_attend(const AttendParams& p, int fmt, int head_dim, int num_sms, cudaStream_t s, bool pdl);
 
 }  // namespace sv

@@ -247,7 +247,5 @@ cudaError_t launch_set_len(SvState* st, int len, int cap_len, int pending, cudaS
 // 2D bf16 tensor map [rows, cols] row-major, boxes of box_rows x 64 columns,
 // 128B swizzle (the driver's encoder is looked up once per process).
 bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
-// The same of bytes: boxes of box_rows x 128 columns.
-bool make_u8_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 }  // namespace sv

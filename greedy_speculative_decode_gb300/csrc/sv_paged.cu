@@ -1,5 +1,5 @@
 // sv_paged.cu -- C entry points of the paged-cache operators: argument
-// checks, tensor maps, and the launches.
+// checks and the launches.
 #include <cmath>
 #include <mutex>
 
@@ -10,9 +10,9 @@ namespace sv {
 cudaError_t prepare_attend_64();
 cudaError_t prepare_attend_128();
 cudaError_t prepare_attend_256();
-cudaError_t launch_attend_64(const CUtensorMap&, const CUtensorMap&, const AttendParams&, int, int, cudaStream_t, bool);
-cudaError_t launch_attend_128(const CUtensorMap&, const CUtensorMap&, const AttendParams&, int, int, cudaStream_t, bool);
-cudaError_t launch_attend_256(const CUtensorMap&, const CUtensorMap&, const AttendParams&, int, int, cudaStream_t, bool);
+cudaError_t launch_attend_64(const AttendParams&, int, int, cudaStream_t, bool);
+cudaError_t launch_attend_128(const AttendParams&, int, int, cudaStream_t, bool);
+cudaError_t launch_attend_256(const AttendParams&, int, int, cudaStream_t, bool);
 
 cudaError_t prepare_attend_kernels() {
   cudaError_t e;
@@ -20,12 +20,11 @@ cudaError_t prepare_attend_kernels() {
   return prepare_attend_256();
 }
 
-cudaError_t launch_attend(const CUtensorMap& kmap, const CUtensorMap& vmap, const AttendParams& p, int fmt,
-                          int head_dim, int num_sms, cudaStream_t s, bool pdl) {
+cudaError_t launch_attend(const AttendParams& p, int fmt, int head_dim, int num_sms, cudaStream_t s, bool pdl) {
   switch (head_dim) {
-    case 64: return launch_attend_64(kmap, vmap, p, fmt, num_sms, s, pdl);
-    case 128: return launch_attend_128(kmap, vmap, p, fmt, num_sms, s, pdl);
-    case 256: return launch_attend_256(kmap, vmap, p, fmt, num_sms, s, pdl);
+    case 64: return launch_attend_64(p, fmt, num_sms, s, pdl);
+    case 128: return launch_attend_128(p, fmt, num_sms, s, pdl);
+    case 256: return launch_attend_256(p, fmt, num_sms, s, pdl);
   }
   return cudaErrorInvalidValue;
 }
@@ -106,14 +105,9 @@ bool bad_stride(int64_t stride, int width) { return stride < width || stride % 8
 
 int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
 
-int max_splits(const RowBatch& b, int head_dim) { return attn_n_splits(b.table_stride * kPage, head_dim); }
+int max_splits(const RowBatch& b) { return attend_split_of(b.limit() - 1) + 1; }
 
 }  // namespace
-
-bool make_kv_map(CUtensorMap* m, const void* codes, int row_bytes, uint64_t rows) {
-  if (row_bytes == 64) return make_u8_map(m, codes, rows / 2, 128, kPage / 2);
-  return make_u8_map(m, codes, rows, (uint64_t)row_bytes, kPage);
-}
 
 }  // namespace sv
 
@@ -154,7 +148,7 @@ int sv_attend_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, int n_
   RowBatch b;
   if (!pool || !bytes || n_q_heads < 1 || !read_rows(rows, b)) return SV_E_INVAL;
   if (pool->head_dim != 64 && pool->head_dim != 128 && pool->head_dim != 256) return SV_E_INVAL;
-  const int64_t slots = (int64_t)b.n_rows * n_q_heads * max_splits(b, pool->head_dim);
+  const int64_t slots = (int64_t)b.n_rows * n_q_heads * max_splits(b);
   *bytes = round256(slots * (int64_t)sizeof(float2)) + slots * pool->head_dim * (int64_t)sizeof(float);
   return SV_OK;
 }
@@ -181,9 +175,6 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
   int num_sms = 0;
   const int rc = device_setup(&num_sms);
   if (rc != SV_OK) return rc;
-  CUtensorMap kmap, vmap;
-  const uint64_t n = (uint64_t)c.n_pages * c.n_kv_heads * kPage;
-  if (!make_kv_map(&kmap, c.k, c.row_bytes(), n) || !make_kv_map(&vmap, c.v, c.row_bytes(), n)) return SV_E_CUDA;
   AttendParams p = {};
   p.rows = b;
   p.q = static_cast<const bf16*>(q_dev);
@@ -191,6 +182,8 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
   p.q_stride = q_stride;
   p.out_stride = out_stride;
   p.lse = lse_dev;
+  p.k = c.k;
+  p.v = c.v;
   p.k_exp = c.k_exp;
   p.v_exp = c.v_exp;
   p.n_q_heads = n_q_heads;
@@ -200,13 +193,12 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.max_splits = max_splits(b, c.head_dim);
+  p.max_splits = max_splits(b);
   p.part_ml = static_cast<float2*>(workspace_dev);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) +
                                       round256(f * p.max_splits * (int64_t)sizeof(float2)));
   p.status = status_dev;
-  return launch_attend(kmap, vmap, p, c.fmt, c.head_dim, num_sms, static_cast<cudaStream_t>(cuda_stream), false) ==
-                 cudaSuccess
+  return launch_attend(p, c.fmt, c.head_dim, num_sms, static_cast<cudaStream_t>(cuda_stream), false) == cudaSuccess
              ? SV_OK
              : SV_E_CUDA;
 }
