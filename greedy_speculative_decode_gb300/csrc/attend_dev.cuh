@@ -5,24 +5,28 @@
 //   s_p = scale * q . k_p,  o = sum_p softmax(s)_p v_p,  lse = ln sum_p exp(s_p).
 // The cache is read once per tile of 8 N query rows (token rows x the query
 // heads of a kv head, packed one behind the other whatever the group size), so
-// few rows are bound by its bytes.  A CTA of four warps walks a split's chunks
-// of four pages, warp w its page w, each warp by itself: its own ring of
-// asynchronous copies and its own softmax statistics and accumulators, no barrier.
-//   Scores, transposed: S^T = K Q^T.  The page's 16 positions are the 16 rows
+// few rows are bound by its bytes.  A CTA of four warps takes a split (a range
+// of positions) for a kv head and a tile; each warp works by itself on its
+// share of the positions, with its own ring of asynchronous copies and its own
+// softmax statistics and accumulators, no barrier.  Two pages (one where a
+// position's row has 256 bytes or more) at a time:
+//   Scores, transposed: S^T = K Q^T.  A page's 16 positions are the 16 rows
 //     of an mma, eight query rows its columns, so single-token decode with a
 //     group of up to eight heads wastes none of it.  K goes from 8 to 16 bits
 //     in registers.
-//   Online softmax over pages; the weights are transposed in registers
-//     (movmatrix).
+//   Online softmax; the weights are transposed in registers (movmatrix).  The
+//     reference that weights are taken against moves only when a row's maximum
+//     has risen by more than 2^8 over it (weights reach 2^8, which f16 and fp32
+//     hold as exactly as those below one), so accumulators are seldom rescaled.
 //   O^T += V^T P^T, all columns.  A transposing load of bytes makes V's operand
 //     (four consecutive positions of a column in a word).
-// At the split's end the four warps' results meet in shared memory and go out
-// as the split's partial; a second kernel merges the splits.
+// At the split's end the warps' results meet in shared memory and go out as its
+// partial; a second kernel merges the splits.
 //
 // An 8-bit cache's exponents cost an addition each.  The key's scales its
 // score; the value's, ev, is added to the score in log2 units, t' = log2(e) s +
-// ev, and the weights are p' = 2^(t' - max t'): they already carry the value's
-// scale, the largest is 1, and f16 (11 bits, the tensor cores' type that holds
+// ev, and the weights are p' = 2^(t' - ref): they already carry the value's
+// scale, the largest is between 2^-8 and 2^8, and f16 (11 bits, the tensor cores' type that holds
 // every e4m3 code) rounds them relative to the largest contribution.  The
 // denominator takes p' 2^-ev, unrounded, in fp32.  Queries go to f16 divided
 // by a power of two near their row's largest value: exact for elements within
@@ -46,21 +50,21 @@
 namespace sv {
 namespace {
 
-constexpr int kAttendWarps = 4;
+constexpr int kAttendWarps = 4;  // of a CTA
 constexpr int kAttendThreads = kAttendWarps * 32;
+constexpr float kAttendSlack = 8.0f;  // log2 of what a row's maximum may exceed its reference by
 
 // A tile of query rows.
 struct AttendTile {
   int row0, f0, nf, kvh;  // the sequence's first row, the tile's first query row, the sequence's query rows
   int first;              // position of the sequence's first row
 };
-// (by what the rings and 32 N D / 128 accumulators a lane leave room for)
-__host__ __device__ constexpr int kAttendPerSm(int d, bool bf16, int n) {
+
+// CTAs per SM: what the rings (64 KB at rows of 128 bytes) and N D / 4
+// accumulators a lane leave room for.
+__host__ __device__ constexpr int attend_per_sm(int d, bool bf16, int n) {
   const int rb = d * (bf16 ? 2 : 1);
-  if (rb == 512) return 1;
-  if (n * d >= 512) return 2;
-  if (rb == 256) return 2;
-  return n * d >= 256 ? 3 : n * d >= 128 ? 4 : 5;
+  return rb == 512 ? 1 : n * d >= 256 ? (rb == 256 ? 1 : 2) : rb == 256 ? 2 : n * d <= 64 ? 4 : 3;
 }
 
 template <int D_, int FMT_, int N_>
@@ -69,32 +73,30 @@ struct AttendCfg {
   static constexpr bool kBf16 = FMT == SV_KV_BF16;
   static constexpr int RB = D * (kBf16 ? 2 : 1);  // bytes of a position's row
   static constexpr int kPageBytes = kPage * RB;
-  static constexpr int kChunk = kAttendWarps * kPage;
-  static constexpr int kStageBytes = 2 * kPageBytes;
-  // pages of K and V in a warp's ring: one at hand, the others on their way.
-  // The warps of an SM together keep about 80 KB on the way.
-  static constexpr int kStages = N == 4 || RB == 512 ? 2 : RB == 256 ? 3 : 2;
-  static constexpr int kPerSm = kAttendPerSm(D, kBf16, N);  // CTAs per SM that registers are cut for
+  static constexpr int PW = RB <= 128 ? 2 : 1;    // pages a warp takes at a time
+  static constexpr int kWarpPos = PW * kPage;     // their positions
+  static constexpr int kChunk = kAttendWarps * kWarpPos;
+  static constexpr int kStageBytes = 2 * PW * kPageBytes;  // pages of K, pages of V
+  static constexpr int kStages = RB == 256 ? 3 : 2;  // of a warp's ring: one at hand, the others on their way
+  static constexpr int kPerSm = attend_per_sm(D, kBf16, N);  // CTAs per SM that registers are cut for
   static constexpr int NK = D / 16;               // k16 steps of a score
   static constexpr int U = D / 16;                // 16-column units of the output
   static constexpr int QR = 8 * N;                // query rows of a tile
   static constexpr bool kQRegs = N * NK <= 16;    // query fragments stay in registers
-  // the meeting of the warps, a part of the columns at a time (8 KB of accumulators)
-  static constexpr int kColsMax = 64 / N;
-  static constexpr int kCols = kColsMax < D ? kColsMax : D;
-  static constexpr int kRounds = D / kCols;
-  static constexpr int kColStride = kCols + 4;    // floats of a query row (4 mod 16: no bank conflicts)
-  static_assert(kCols % 16 == 0 && kColStride % 16 == 4, "columns of a round");
+  // the warps' meeting: each leaves its accumulators in the stage it has done
+  // with, all columns or a part of them at a time
+  static constexpr int kRounds = QR * D * 4 > kStageBytes ? QR * D * 4 / kStageBytes : 1;
+  static constexpr int kCols = D / kRounds;
+  static_assert(kCols % 32 == 0, "columns of a round");
   // shared memory
-  static constexpr int kScaleBytes = kBf16 ? 0 : 2 * kPage;        // exponents of a stage (one a position)
+  static constexpr int kScaleBytes = kBf16 ? 0 : 2 * PW * kPage;   // exponents of a stage (one a position)
   static constexpr int kRing = kAttendWarps * kStages;             // stages of all warps
   static constexpr int kOffScale = kRing * kStageBytes;
-  static constexpr int kOffQ = kOffScale + kRing * kScaleBytes;    // query fragments [N][NK][32 lanes][2 words]
-  static constexpr int kQBytes = N * NK * 256;
-  static constexpr int kOffO = kOffQ + kQBytes;                    // [4 warps][QR][kColStride] accumulators
-  static constexpr int kOffMl = kOffO + kAttendWarps * QR * kColStride * 4;  // [QR][4 warps] (max, sum)
-  static constexpr int kOffRow = kOffMl + QR * 32;                 // [QR] score factors, positions, slots
-  static constexpr int kOffSeq = kOffRow + 3 * QR * 4;             // [n_seq + 1] chunks before, first, row start
+  static constexpr int kOffQ = kOffScale + kRing * kScaleBytes;    // query fragments of a warp [N][NK][32 lanes][2 words]
+  static constexpr int kQBytes = kQRegs ? 0 : N * NK * 256;
+  static constexpr int kOffMl = kOffQ + kAttendWarps * kQBytes;    // [QR][4 warps] (reference, sum)
+  static constexpr int kOffSlot = kOffMl + QR * 32;                // [QR] places of the query rows in the output
+  static constexpr int kOffSeq = kOffSlot + QR * 4;                // [n_seq + 1] chunks before, first, row start
   static constexpr int smem_bytes(int n_seq) { return 128 + kOffSeq + 4 * (3 * n_seq + 2); }
   static_assert(128 + kOffSeq + 4 * (3 * kAttendMaxSeq + 2) <= 227 * 1024, "shared memory of a CTA");
 };
@@ -327,10 +329,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Page `page` of a kv head into a stage: 2 RB / 64 copies of 16 bytes a lane,
-// swizzled as page_off says, and an 8-bit page's exponents (one a position).
+// Page `page` of a kv head as a stage's h-th: 2 RB / 64 copies of 16 bytes
+// a lane, swizzled as page_off says, and an 8-bit page's exponents (one a
+// position).
 template <class C>
-__device__ __forceinline__ void fetch_page(const AttendParams& p, int page, int kvh, int lane, uint32_t stage,
+__device__ __forceinline__ void fetch_page(const AttendParams& p, int page, int kvh, int lane, int h, uint32_t stage,
                                            uint32_t scale) {
   constexpr int kUnitsRow = C::RB / 16, kPer = C::kPageBytes / 512;  // units of a row; copies of a lane
   const size_t ph = (size_t)page * p.n_kv_heads + kvh;
@@ -339,11 +342,12 @@ __device__ __forceinline__ void fetch_page(const AttendParams& p, int page, int 
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
-    const uint32_t dst = stage + page_off<C::RB>(e / kUnitsRow, e % kUnitsRow);
+    const uint32_t dst = stage + h * C::kPageBytes + page_off<C::RB>(e / kUnitsRow, e % kUnitsRow);
     copy16(dst, k + 512 * i);
-    copy16(dst + C::kPageBytes, v + 512 * i);
+    copy16(dst + C::PW * C::kPageBytes, v + 512 * i);
   }
-  if (!C::kBf16 && p.block == 1 && lane < 2) copy16(scale + lane * kPage, (lane ? p.v_exp : p.k_exp) + ph * kPage);
+  if (!C::kBf16 && p.block == 1 && lane < 2)
+    copy16(scale + (C::PW * lane + h) * kPage, (lane ? p.v_exp : p.k_exp) + ph * kPage);
 }
 
 // ------------------------------------------------------------------ the arithmetic
@@ -353,95 +357,93 @@ __device__ __forceinline__ void fetch_page(const AttendParams& p, int page, int 
 // g + 8 of each unit against them.
 template <class C>
 struct AttendRows {
-  static constexpr int N = C::N, U = C::U, W = kAttendWarps;
+  static constexpr int N = C::N, U = C::U, PW = C::PW;
   static constexpr bool kBf16 = C::kBf16;
   const AttendParams& p;
+  uint2* s_q;  // query fragments in shared memory, where they do not stay in registers
   uint8_t* smem;
   int warp, lane, g, q4;
-  float o[U][N][4], m_run[N][2], l_run[N][2];
-  uint32_t qr[C::kQRegs ? N * C::NK : 1][2];  // query fragments, where they stay in registers
+  float o[U][N][4], m_run[N][2], l_run[N][2], fac[N][2];
+  int tpos[N][2];  // positions of the lane's query rows
+  uint32_t qr[C::kQRegs ? N * C::NK : 1][2];
 
   __device__ __forceinline__ AttendRows(const AttendParams& p_, uint8_t* smem_) : p(p_), smem(smem_) {
     warp = threadIdx.x >> 5;
     lane = threadIdx.x & 31;
     g = lane >> 2;
     q4 = lane & 3;
+    s_q = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQBytes) + lane;
   }
-  __device__ __forceinline__ float* s_o() const { return reinterpret_cast<float*>(smem + C::kOffO); }
-  __device__ __forceinline__ float2* s_ml() const { return reinterpret_cast<float2*>(smem + C::kOffMl); }
-  __device__ __forceinline__ float* s_fac() const { return reinterpret_cast<float*>(smem + C::kOffRow); }
-  __device__ __forceinline__ int* s_t() const { return reinterpret_cast<int*>(smem + C::kOffRow) + C::QR; }
-  __device__ __forceinline__ int* s_slot() const { return reinterpret_cast<int*>(smem + C::kOffRow) + 2 * C::QR; }
-  __device__ __forceinline__ const uint2* s_q() const { return reinterpret_cast<const uint2*>(smem + C::kOffQ) + lane; }
   __device__ __forceinline__ bool sees(int t, int pos) const {
     return pos <= t && (p.window <= 0 || pos > t - p.window || pos < p.sinks);
   }
 
-  // A tile's queries as B fragments, the rows' score factors, positions and
-  // output slots (all warps).  A piece is 8 elements of one query row; they go
-  // to the lanes and k16 steps that meet the same elements of K (a lane's
-  // 16-byte unit of a key row, four elements a step).
+  // A tile's queries as B fragments.  Lane (g, q4) takes row g of each query
+  // tile, the elements it meets in K: its 16-byte units of a key row, four
+  // elements a k16 step.
   __device__ __forceinline__ void queries(const AttendTile& it, int G) {
-    constexpr int kPieces = C::QR * C::D / 8, T = kAttendThreads;
-    constexpr int kPer = (kPieces + T - 1) / T, kBatch = kPer < 4 ? kPer : 4;
-#pragma unroll 1
-    for (int u0 = 0; u0 < kPer; u0 += kBatch) {
-      uint4 x[kBatch];
+    constexpr int kUnits = C::RB / 64, kV = kBf16 ? 1 : 2, kSteps = C::NK / kUnits;  // kV: 16-byte loads a unit
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int v = threadIdx.x + (u0 + u) * T, qi = v / (C::D / 8), c8 = v % (C::D / 8), f = it.f0 + qi;
-        x[u] = make_uint4(0u, 0u, 0u, 0u);
-        if ((kPieces % T == 0 || v < kPieces) && f < it.nf)
-          x[u] = __ldcg(reinterpret_cast<const uint4*>(p.q + (int64_t)(it.row0 + f / G) * p.q_stride +
-                                                       (it.kvh * G + f % G) * C::D + c8 * 8));
+    for (int n = 0; n < N; ++n) {
+      const int f = it.f0 + n * 8 + g;
+      const bf16* row = p.q + (int64_t)(it.row0 + f / G) * p.q_stride + (it.kvh * G + f % G) * C::D;
+      uint4 x[kUnits][kV];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+          x[u][v] = f < it.nf ? __ldcg(reinterpret_cast<const uint4*>(row) + c * kV + v) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      float down = 1.0f, up = p.scale_log2;
+      if (!kBf16) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+          for (int v = 0; v < kV; ++v)
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[u][v].x & 0x7fff7fffu, x[u][v].y & 0x7fff7fffu),
+                                     __vmaxu2(x[u][v].z & 0x7fff7fffu, x[u][v].w & 0x7fff7fffu)));
+        m = max(m & 0xffffu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // the row's largest exponent E: q / 2^(E - 127) is below 2 (E = 0, and
+        // rows of zeros, count as E = 1; an infinity or NaN makes the row NaN)
+        const int E = min(max((int)(m >> 7), 1), 253);
+        down = __uint_as_float((uint32_t)(254 - E) << 23);
+        up = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __fmul_rn(p.scale_log2, __uint_as_float((uint32_t)E << 23));
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int v = threadIdx.x + (u0 + u) * T, qi = v / (C::D / 8), c8 = v % (C::D / 8), f = it.f0 + qi;
-        float fac = p.scale_log2;
-        uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        if (!kBf16) {
-          uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-          m = max(m & 0xffffu, m >> 16);
+      for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-          for (int o = C::D / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // the row's largest exponent E: q / 2^(E - 127) is below 2 (E = 0, and
-          // rows of zeros, count as E = 1; an infinity or NaN makes the row NaN)
-          const int E = min(max((int)(m >> 7), 1), 253);
-          const float down = __uint_as_float((uint32_t)(254 - E) << 23);
-          fac = m >= 0x7f80u ? __uint_as_float(0x7fffffffu)
-                             : __fmul_rn(p.scale_log2, __uint_as_float((uint32_t)E << 23));
+        for (int k = 0; k < kSteps; ++k) {
+          const uint4 w = x[u][kBf16 ? 0 : k >> 1];
+          uint32_t b0 = (k & 1) ? w.z : w.x, b1 = (k & 1) ? w.w : w.y;
+          if (!kBf16) {
+            b0 = pack_f16x2(__fmul_rn(__uint_as_float(b0 << 16), down), __fmul_rn(__uint_as_float(b0 & 0xffff0000u), down));
+            b1 = pack_f16x2(__fmul_rn(__uint_as_float(b1 << 16), down), __fmul_rn(__uint_as_float(b1 & 0xffff0000u), down));
+          }
+          const int at = n * C::NK + u * kSteps + k;
+          if constexpr (C::kQRegs) {
+            qr[at][0] = b0;
+            qr[at][1] = b1;
+          } else {
+            s_q[at * 32] = make_uint2(b0, b1);
+          }
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack_f16x2(__fmul_rn(__uint_as_float(w[i] << 16), down),
-                              __fmul_rn(__uint_as_float(w[i] & 0xffff0000u), down));
-        }
-        if (kPieces % T != 0 && v >= kPieces) continue;
-        // the 16-byte unit of a key row that holds these elements: its lane and steps
-        const int c = kBf16 ? c8 : c8 >> 1;
-        const int lane_q = C::RB == 64 ? c : (c & 7) >> 1;
-        int k0 = C::RB == 64 ? 0 : (c >> 3) * 2 + (c & 1);
-        k0 = kBf16 ? k0 * 2 : k0 * 4 + (c8 & 1) * 2;
-        uint2* dst = reinterpret_cast<uint2*>(smem + C::kOffQ) + ((qi >> 3) * C::NK + k0) * 32 + (qi & 7) * 4 + lane_q;
-        dst[0] = make_uint2(w[0], w[1]);
-        dst[32] = make_uint2(w[2], w[3]);
-        if (c8 == 0) {
-          s_fac()[qi] = fac;
-          s_t()[qi] = it.first + f / G;
-          s_slot()[qi] = f < it.nf ? (it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G : -1;
-        }
+      for (int c = 0; c < 2; ++c) {
+        fac[n][c] = __shfl_sync(0xffffffffu, up, (2 * q4 + c) * 4);
+        const int fq = it.f0 + n * 8 + 2 * q4 + c;
+        tpos[n][c] = it.first + fq / G;
       }
     }
-  }
-  __device__ __forceinline__ void keep_queries() {
-    if constexpr (C::kQRegs) {
-#pragma unroll
-      for (int k = 0; k < N * C::NK; ++k) {
-        const uint2 v = s_q()[k * 32];
-        qr[k][0] = v.x;
-        qr[k][1] = v.y;
-      }
+    // (fragments in shared memory: a lane reads its own)
+    // places in the output, -1: no row (a barrier comes before they are read, at the warps' meeting)
+    if (threadIdx.x < C::QR) {
+      const int fq = it.f0 + threadIdx.x;
+      reinterpret_cast<int*>(smem + C::kOffSlot)[threadIdx.x] =
+          fq < it.nf ? (it.row0 + fq / G) * p.n_q_heads + it.kvh * G + fq % G : -1;
     }
   }
 
@@ -460,7 +462,7 @@ struct AttendRows {
   // the rows that see it.  (a: columns g, g + 8 of unit u, positions 2 q4, 2 q4
   // + 1 and 8 more of the page; the accumulators of these columns are held by
   // the same quad of lanes.)
-  __device__ __forceinline__ void set_apart(int base, int u, uint32_t (&a)[4]) {
+  __device__ __forceinline__ void set_apart(int base, bool have, int u, uint32_t (&a)[4]) {
     auto bad = [](uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; };
     if (!__any_sync(0xffffffffu, bad(a[0]) || bad(a[1]) || bad(a[2]) || bad(a[3]))) return;
     for (int src = 0; src < 4; ++src)
@@ -475,7 +477,7 @@ struct AttendRows {
           for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              if (sees(s_t()[n * 8 + 2 * q4 + c], pos)) {
+              if (have && sees(tpos[n][c], pos)) {
                 float& x = o[u][n][2 * (k & 1) + c];
                 x = __fadd_rn(x, __uint_as_float(b));
               }
@@ -488,118 +490,149 @@ struct AttendRows {
     }
   }
 
-  // One page: scores in log2 units with the value's exponent added, -inf where
-  // a row does not see the position; the running maxima and sums; O^T.
-  // kEdge: some row does not see some position.
+  // The warp's pages of a chunk: scores in log2 units with the value's exponent added, -inf
+  // where a row does not see the position; the references and sums; O^T.
+  // kEdge: some row does not see some position, or a page is not there (have).
   template <bool kEdge>
-  __device__ __forceinline__ void page(uint32_t kp, uint32_t vp, const uint8_t* sc, int base, uint32_t exps) {
-    float s[N][4];
+  __device__ __forceinline__ void pages(uint32_t kp, const uint8_t* sc, int base, uint32_t have, const uint32_t (&ke)[PW],
+                                        const uint32_t (&ve)[PW]) {
+    const uint32_t vp = kp + PW * C::kPageBytes;
+    float s[PW][N][4];
 #pragma unroll
-    for (int n = 0; n < N; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < PW; ++j) s[j][n][e] = 0.0f;
     const int pos = pos_of_row<kBf16>(g), pos8 = pos_of_row<kBf16>(g + 8);
     constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
     constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      uint32_t x[2][4];
+      uint32_t x[PW][2][4];
       const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x[h][0]), "=r"(x[h][1]), "=r"(x[h][2]), "=r"(x[h][3])
-                     : "r"(kp + page_off<C::RB>(h ? pos8 : pos, c)));
+      for (int j = 0; j < PW; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[j][h][0]), "=r"(x[j][h][1]), "=r"(x[j][h][2]), "=r"(x[j][h][3])
+                       : "r"(kp + j * C::kPageBytes + page_off<C::RB>(h ? pos8 : pos, c)));
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        uint32_t a[4];
+        uint32_t a[PW][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          a[h] = kBf16 ? x[h][(2 * k) & 3] : f16x2_of_lo(x[h][k & 3]);
-          a[2 + h] = kBf16 ? x[h][(2 * k + 1) & 3] : f16x2_of_hi(x[h][k & 3]);
-        }
+        for (int j = 0; j < PW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            a[j][h] = kBf16 ? x[j][h][(2 * k) & 3] : f16x2_of_lo(x[j][h][k & 3]);
+            a[j][2 + h] = kBf16 ? x[j][h][(2 * k + 1) & 3] : f16x2_of_hi(x[j][h][k & 3]);
+          }
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const int f = n * C::NK + u * kSteps + k;
+          uint32_t b0, b1;
           if constexpr (C::kQRegs) {
-            mma_16<kBf16>(s[n], a, qr[f][0], qr[f][1]);
+            b0 = qr[f][0];
+            b1 = qr[f][1];
           } else {
-            const uint2 b = s_q()[f * 32];
-            mma_16<kBf16>(s[n], a, b.x, b.y);
+            const uint2 b = s_q[f * 32];
+            b0 = b.x;
+            b1 = b.y;
           }
+#pragma unroll
+          for (int j = 0; j < PW; ++j) mma_16<kBf16>(s[j][n], a[j], b0, b1);
         }
       }
     }
-    float ks[2], ev[2], iv[2];
-    if (!kBf16) {  // positions pos and pos + 2: two bytes of a word of the page's exponents
-      uint32_t kw, vw;
-      if (p.block == 1) {
-        kw = *reinterpret_cast<const uint32_t*>(sc + (pos & ~3)) >> (8 * (pos & 3));
-        vw = *reinterpret_cast<const uint32_t*>(sc + kPage + (pos & ~3)) >> (8 * (pos & 3));
-      } else {
-        kw = (exps & 255u) * 0x00010001u;
-        vw = (exps >> 8) * 0x00010001u;
-      }
+    // The lane's positions, two a page: key scale, value exponent ev and 2^-ev.  A byte
+    // of 255 makes the score 0 * inf and ev inf * 0: NaN.
+    float ks[PW][2], ev[PW][2], iv[PW][2];
+    if (!kBf16) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t bk = (kw >> (16 * h)) & 255u, bv = (vw >> (16 * h)) & 255u;
-        ks[h] = __uint_as_float(bk << 23);  // (255: infinity, times a score of zero codes: NaN)
-        ev[h] = bv == kExpNaN ? __uint_as_float(0x7fffffffu) : (float)((int)bv - 127);
-        iv[h] = exp_byte_inverse((int)bv);
+      for (int j = 0; j < PW; ++j) {
+        uint32_t kw, vw;
+        if (p.block == 1) {  // positions pos and pos + 2: two bytes of a word of the page's exponents
+          const uint8_t* w = sc + j * kPage + (pos & ~3);
+          kw = *reinterpret_cast<const uint32_t*>(w) >> (8 * (pos & 3));
+          vw = *reinterpret_cast<const uint32_t*>(w + PW * kPage) >> (8 * (pos & 3));
+        } else {
+          kw = ke[j] * 0x00010001u;
+          vw = ve[j] * 0x00010001u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t bk = (kw >> (16 * h)) & 255u, bv = (vw >> (16 * h)) & 255u;
+          ks[j][h] = __uint_as_float(bk << 23);
+          iv[j][h] = __uint_as_float((254u - bv) << 23);
+          // 2^23 + bv as a float, less 2^23 + 127
+          ev[j][h] = __fmaf_rn(__uint_as_float(bv << 23), 0.0f, __fsub_rn(__uint_as_float(0x4b000000u | bv), 8388735.0f));
+        }
       }
     }
-    uint32_t hi[N][2], lo[kBf16 ? N : 1][2];
+    uint32_t hi[PW][N][2], lo[kBf16 ? PW : 1][N][2];
     bool moved = false;
     float alpha[N][2];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const float2 f = reinterpret_cast<const float2*>(s_fac())[n * 4 + q4];
-      const int2 t = kEdge ? reinterpret_cast<const int2*>(s_t())[n * 4 + q4] : make_int2(0, 0);
-      float pv[4];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const float fc = fac[n][c];
+        float m = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& x = s[n][2 * h + c];
-          const float fc = c ? f.y : f.x;
-          x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[h]), ev[h]);
-          if (kEdge) x = sees(c ? t.y : t.x, base + (h ? pos8 : pos)) ? x : -INFINITY;
-        }
-        float m = fmaxf(s[n][c], s[n][2 + c]);
+        for (int j = 0; j < PW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[j][n][2 * h + c];
+            x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[j][h]), ev[j][h]);
+            if (kEdge)
+              x = ((have >> j) & 1u) && sees(tpos[n][c], base + j * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
+            m = fmaxf(m, x);
+          }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        m = fmaxf(m, m_run[n][c]);
+        float a = 1.0f;
+        if (m > __fadd_rn(m_run[n][c], kAttendSlack)) {  // (of a row's first pages: -inf, and nothing to scale)
+          if (m_run[n][c] != -INFINITY) {
+            a = ex2(__fsub_rn(m_run[n][c], m));
+            moved = true;
+          }
+          m_run[n][c] = m;
+        }
         // a row that has seen nothing yet: every weight is 2^-inf = 0
-        const float ref = m == -INFINITY ? 0.0f : m;
-        const bool same = m == m_run[n][c];
-        alpha[n][c] = same ? 1.0f : ex2(__fsub_rn(m_run[n][c], ref));
-        moved |= !same;
-        m_run[n][c] = m;
+        const float ref = m_run[n][c] == -INFINITY ? 0.0f : m_run[n][c];
         float sum = 0.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = s[n][2 * h + c], e = ex2(__fsub_rn(x, ref));
-          pv[2 * h + c] = e;
-          if (kBf16)
-            sum = __fadd_rn(sum, e);
-          else if (kEdge)  // (the exponent of a masked place may be anything)
-            sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[h], sum);
-          else
-            sum = __fmaf_rn(e, iv[h], sum);
-        }
-        l_run[n][c] = __fmaf_rn(l_run[n][c], alpha[n][c], sum);
+        for (int j = 0; j < PW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[j][n][2 * h + c];
+            const float e = ex2(__fsub_rn(x, ref));
+            if (kBf16)
+              sum = __fadd_rn(sum, e);
+            else if (kEdge)  // (the exponent of a masked place may be anything)
+              sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[j][h], sum);
+            else
+              sum = __fmaf_rn(e, iv[j][h], sum);
+            x = e;
+          }
+        l_run[n][c] = __fmaf_rn(l_run[n][c], a, sum);
+        alpha[n][c] = a;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (kBf16) {
-          hi[n][h] = transposed(pack_bf16x2(pv[2 * h], pv[2 * h + 1]));
-          lo[kBf16 ? n : 0][h] = transposed(pack_bf16x2(__fsub_rn(pv[2 * h], bf16r(pv[2 * h])),
-                                                        __fsub_rn(pv[2 * h + 1], bf16r(pv[2 * h + 1]))));
-        } else {
-          hi[n][h] = transposed(pack_f16x2(pv[2 * h], pv[2 * h + 1]));
+      for (int j = 0; j < PW; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = s[j][n][2 * h], y = s[j][n][2 * h + 1];
+          if (kBf16) {
+            hi[j][n][h] = transposed(pack_bf16x2(x, y));
+            lo[kBf16 ? j : 0][n][h] = transposed(pack_bf16x2(__fsub_rn(x, bf16r(x)), __fsub_rn(y, bf16r(y))));
+          } else {
+            hi[j][n][h] = transposed(pack_f16x2(x, y));
+          }
         }
-      }
     }
-    // (a maximum seldom moves after a split's first pages; times one is skipped)
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -610,39 +643,47 @@ struct AttendRows {
     }
 #pragma unroll
     for (int u = 0; u < U; u += 2) {
-      uint32_t r[4];
-      if constexpr (!kBf16) ldsm_b8_x2_trans(vp + page_off<C::RB>(lane & 15, u + (lane >> 4)), r);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t a[4];
-        if constexpr (!kBf16) {
-          a[0] = f16x2_of_lo(r[2 * y]);
-          a[1] = f16x2_of_lo(r[2 * y + 1]);
-          a[2] = f16x2_of_hi(r[2 * y]);
-          a[3] = f16x2_of_hi(r[2 * y + 1]);
-          if (kEdge) {
-            // what lies in places that a row does not see may be any byte: a
-            // NaN code must not meet its weight of zero
-            const uint32_t top = 0x5f005f00u;  // 448
+      for (int j = 0; j < PW; ++j) {
+        const uint32_t vj = vp + j * C::kPageBytes;
+        uint32_t r[4];
+        if constexpr (!kBf16) ldsm_b8_x2_trans(vj + page_off<C::RB>(lane & 15, u + (lane >> 4)), r);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) asm("min.f16x2 %0, %0, %1;" : "+r"(a[k]) : "r"(top));
+        for (int y = 0; y < 2; ++y) {
+          uint32_t a[4];
+          if constexpr (!kBf16) {
+            a[0] = f16x2_of_lo(r[2 * y]);
+            a[1] = f16x2_of_lo(r[2 * y + 1]);
+            a[2] = f16x2_of_hi(r[2 * y]);
+            a[3] = f16x2_of_hi(r[2 * y + 1]);
+            if (kEdge) {
+              // what lies in places that a row does not see may be any byte: a
+              // NaN code must not meet its weight of zero
+              const uint32_t top = 0x5f005f00u;  // 448
+#pragma unroll
+              for (int k = 0; k < 4; ++k) asm("min.f16x2 %0, %0, %1;" : "+r"(a[k]) : "r"(top));
+            }
+          } else {
+            ldsm_x4_trans(vj + page_off<C::RB>(lane & 15, (u + y) * 2 + (lane >> 4)), a[0], a[2], a[1], a[3]);
+            if (kEdge) set_apart(base + j * kPage, (have >> j) & 1u, u + y, a);
           }
-        } else {
-          ldsm_x4_trans(vp + page_off<C::RB>(lane & 15, (u + y) * 2 + (lane >> 4)), a[0], a[2], a[1], a[3]);
-          if (kEdge) set_apart(base, u + y, a);
-        }
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          mma_16<kBf16>(o[u + y][n], a, hi[n][0], hi[n][1]);
-          if (kBf16) mma_16<kBf16>(o[u + y][n], a, lo[kBf16 ? n : 0][0], lo[kBf16 ? n : 0][1]);
+          for (int n = 0; n < N; ++n) {
+            mma_16<kBf16>(o[u + y][n], a, hi[j][n][0], hi[j][n][1]);
+            if (kBf16) mma_16<kBf16>(o[u + y][n], a, lo[kBf16 ? j : 0][n][0], lo[kBf16 ? j : 0][n][1]);
+          }
         }
       }
     }
   }
 
-  // The split's partial: (max, sum) and accumulators of the four warps merged
-  // in warp order, a part of the columns at a time.
-  __device__ __forceinline__ void partial(int split) {
+  // The split's partial: the four warps' results merged in warp order.  `left`:
+  // the stage each warp has done with, kRing / 4 stages apart.  (Columns are
+  // stored at c ^ 8 (row / 2 mod 4): the lanes of a store meet 32 banks.)
+  __device__ __forceinline__ void partial(int split, uint8_t* left) {
+    constexpr int W = kAttendWarps, T = kAttendThreads, kStride = C::kStages * C::kStageBytes;
+    float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+    const int* s_slot = reinterpret_cast<const int*>(smem + C::kOffSlot);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -651,38 +692,41 @@ struct AttendRows {
         l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 4));
         l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 8));
         l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 16));
-        if (g == 0) s_ml()[(n * 8 + 2 * q4 + c) * W + warp] = make_float2(m_run[n][c], l);
+        if (g == 0) s_ml[(n * 8 + 2 * q4 + c) * W + warp] = make_float2(m_run[n][c], l);
       }
-    constexpr int kUR = U / C::kRounds;            // units a round
-    constexpr int kV = C::kCols / 4;               // float4 columns of a query row
-    const int tid = threadIdx.x;
+    constexpr int kUR = U / C::kRounds, kV = C::kCols / 4;  // units and float4 columns of a round
+    __syncwarp();                                           // every lane has read its pages
 #pragma unroll
     for (int rd = 0; rd < C::kRounds; ++rd) {
+      float* mine = reinterpret_cast<float*>(left + warp * kStride);
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float* dst = s_o() + (warp * C::QR + n * 8 + 2 * q4 + c) * C::kColStride + g;
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int u = 0; u < kUR; ++u) {
-            dst[16 * u] = o[rd * kUR + u][n][c];
-            dst[16 * u + 8] = o[rd * kUR + u][n][2 + c];
+            float* dst = mine + (n * 8 + 2 * q4 + c) * C::kCols;
+            dst[(16 * u + g) ^ (8 * q4)] = o[rd * kUR + u][n][c];
+            dst[(16 * u + 8 + g) ^ (8 * q4)] = o[rd * kUR + u][n][2 + c];
           }
-        }
-      named_sync(2, kAttendThreads);
-      for (int e = tid; e < C::QR * kV; e += kAttendThreads) {
-        const int qi = e / kV, v = e % kV, slot = s_slot()[qi];
+      named_sync(2, T);
+      for (int e = threadIdx.x; e < C::QR * kV; e += T) {
+        const int qi = e / kV, v = e % kV, slot = s_slot[qi];
         if (slot < 0) continue;
-        const float2* ml = s_ml() + qi * W;
+        float2 ml[W];
         float M = -INFINITY, l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w].x);
+        for (int w = 0; w < W; ++w) {
+          ml[w] = s_ml[qi * W + w];
+          M = fmaxf(M, ml[w].x);
+        }
         const float ref = M == -INFINITY ? 0.0f : M;
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float f = ex2(__fsub_rn(ml[w].x, ref));
-          const float4 x = *reinterpret_cast<const float4*>(s_o() + (w * C::QR + qi) * C::kColStride + 4 * v);
+          const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(left + w * kStride) +
+                                                            qi * C::kCols + ((4 * v) ^ (8 * ((qi >> 1) & 3))));
           l = __fmaf_rn(ml[w].y, f, l);
           a.x = __fmaf_rn(x.x, f, a.x);
           a.y = __fmaf_rn(x.y, f, a.y);
@@ -693,7 +737,7 @@ struct AttendRows {
         if (rd == 0 && v == 0) p.part_ml[at] = make_float2(M, l);
         *reinterpret_cast<float4*>(p.part_o + at * C::D + rd * C::kCols + 4 * v) = a;
       }
-      named_sync(2, kAttendThreads);
+      named_sync(2, T);  // the stages, and s_ml, are free again
     }
   }
 };
@@ -701,7 +745,7 @@ struct AttendRows {
 // A CTA's run, list by list.
 template <class C>
 __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8_t* smem) {
-  constexpr int S = C::kStages;
+  constexpr int S = C::kStages, PW = C::PW;
   AttendPlace<C> at;
   if (!at.start(wk)) return;
   AttendRows<C> rows(p, smem);
@@ -712,71 +756,88 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
   for (;;) {
     const int run = at.run_end();
     const int* table = p.rows.table + (size_t)at.seq * p.rows.table_stride;
-    // This warp's page of place j of the list: its number, -1 where the tile
-    // sees nothing of it (or there is none)
-    auto page_of = [&](int j) {
-      if (j >= run) return -1;
-      const int a = at.list.at(j) * C::kChunk + warp * kPage;
-      if (!at.sees(a, kPage, p.sinks)) return -1;
-      const int pg = __ldg(table + a / kPage);
-      if ((uint32_t)pg < (uint32_t)p.n_pages) return pg;
-      if (p.status && lane == 0) atomicOr(p.status, ST_BAD_PAGE);
-      return -1;
+    // This warp's pages of place j of the list that the tile sees something of
+    // (a mask), and their numbers.  (Loaded a place ahead of their use, and
+    // looked at only then: nothing here waits for the load.)
+    auto pages_of = [&](int j, int (&pg)[PW]) {
+      const int a = at.list.at(j) * C::kChunk + warp * C::kWarpPos;
+      uint32_t seen = 0;
+#pragma unroll
+      for (int h = 0; h < PW; ++h) {
+        if (j >= run || !at.sees(a + h * kPage, kPage, p.sinks)) continue;
+        seen |= 1u << h;
+        pg[h] = __ldg(table + a / kPage + h);
+      }
+      return seen;
     };
-    uint32_t have = 0, exps[S];  // bit k, exps[k]: of place i + k
-    int issued = 0;
-    auto request = [&](int j, int pg, uint32_t& ex) {
-      if (pg >= 0) {
-        const int st = issued % S;
-        fetch_page<C>(p, pg, at.tile.kvh, lane, ring + st * C::kStageBytes, scales_at + st * C::kScaleBytes);
+    auto request = [&](int st, uint32_t seen, const int (&pg)[PW], uint32_t& have, uint32_t (&ke)[PW], uint32_t (&ve)[PW]) {
+      have = 0;
+#pragma unroll
+      for (int h = 0; h < PW; ++h) {
+        ke[h] = ve[h] = 0;
+        if (!((seen >> h) & 1u)) continue;
+        if ((uint32_t)pg[h] >= (uint32_t)p.n_pages) {
+          if (p.status && lane == 0) atomicOr(p.status, ST_BAD_PAGE);
+          continue;
+        }
+        have |= 1u << h;
+        fetch_page<C>(p, pg[h], at.tile.kvh, lane, h, ring + st * C::kStageBytes, scales_at + st * C::kScaleBytes);
         if (!C::kBf16 && p.block != 1) {
-          const size_t ph = (size_t)pg * p.n_kv_heads + at.tile.kvh;
-          ex = (uint32_t)__ldg(p.k_exp + ph) | (uint32_t)__ldg(p.v_exp + ph) << 8;
+          const size_t ph = (size_t)pg[h] * p.n_kv_heads + at.tile.kvh;
+          ke[h] = __ldg(p.k_exp + ph);
+          ve[h] = __ldg(p.v_exp + ph);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      ++issued;
     };
+    // of places i, i + 1, ..: pages that are there, and a page's one exponent
+    uint32_t have[S], ke[S][PW], ve[S][PW];
+    int ahead[PW] = {};
+    uint32_t seen;
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-      const int pg = page_of(at.i + k);
-      have |= (pg >= 0 ? 1u : 0u) << k;
-      request(at.i + k, pg, exps[k]);
+      seen = pages_of(at.i + k, ahead);
+      request(k, seen, ahead, have[k], ke[k], ve[k]);
     }
-    int ahead = page_of(at.i + S - 1);
+    seen = pages_of(at.i + S - 1, ahead);
     rows.queries(at.tile, wk.G);
-    named_sync(2, kAttendThreads);
-    rows.keep_queries();
     rows.open();
     bool any = false;  // the item has a chunk that the tile sees
     int st = 0;
     for (int i = at.i; i < run; ++i) {
-      // the page S - 1 places on, into the stage that place i - 1 had (every lane has done with it)
+      // the pages S - 1 places on, into the stage that place i - 1 had (every lane has done with it)
       __syncwarp();
-      have |= (ahead >= 0 ? 1u : 0u) << (S - 1);
-      request(i + S - 1, ahead, exps[S - 1]);
-      ahead = page_of(i + S);
-      const int chunk = at.list.at(i) * C::kChunk, base = chunk + warp * kPage;
-      any |= at.sees(chunk, C::kChunk, p.sinks);
-      if (have & 1u) {
+      request(st == 0 ? S - 1 : st - 1, seen, ahead, have[S - 1], ke[S - 1], ve[S - 1]);
+      seen = pages_of(i + S, ahead);
+      const int chunk = at.list.at(i) * C::kChunk, base = chunk + warp * C::kWarpPos;
+      if (at.sees(chunk, C::kChunk, p.sinks)) any = true;
+      if (have[0]) {
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
         __syncwarp();
         const uint32_t kp = ring + st * C::kStageBytes;
         const uint8_t* sc = scales + st * C::kScaleBytes;
-        // whether every row of the tile sees every position of the page
-        const bool all = base + kPage - 1 <= at.t0 &&
-                         (p.window <= 0 || base > at.t1 - p.window || base + kPage - 1 < p.sinks);
-        if (all) rows.template page<false>(kp, kp + C::kPageBytes, sc, base, exps[0]);
-        else rows.template page<true>(kp, kp + C::kPageBytes, sc, base, exps[0]);
+        // whether every row of the tile sees every position of the pages
+        const int e = base + C::kWarpPos - 1;
+        const bool all = have[0] == (1u << PW) - 1u && e <= at.t0 &&
+                         (p.window <= 0 || base > at.t1 - p.window || e < p.sinks);
+        if (all) rows.template pages<false>(kp, sc, base, have[0], ke[0], ve[0]);
+        else rows.template pages<true>(kp, sc, base, have[0], ke[0], ve[0]);
       }
-      have >>= 1;
 #pragma unroll
-      for (int k = 0; k < S - 1; ++k) exps[k] = exps[k + 1];
+      for (int k = 0; k < S - 1; ++k) {
+        have[k] = have[k + 1];
+#pragma unroll
+        for (int h = 0; h < PW; ++h) {
+          ke[k][h] = ke[k + 1][h];
+          ve[k][h] = ve[k + 1][h];
+        }
+      }
+      uint8_t* left = smem + st * C::kStageBytes;
       st = st + 1 == S ? 0 : st + 1;
       const int split = attend_split_of(chunk);
       if (i + 1 == run || attend_split_of(at.list.at(i + 1) * C::kChunk) != split) {
         if (any) {
-          rows.partial(split);
+          rows.partial(split, left);
           rows.open();
         }
         any = false;
@@ -784,7 +845,7 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!at.past(wk, run)) return;
-    named_sync(2, kAttendThreads);  // every warp is done with this tile's queries
+    __syncwarp();  // every lane is done with this tile's stages (and the CTA, by its last meeting, with the slots)
   }
 }
 
@@ -805,40 +866,61 @@ __global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) 
 }
 
 // The splits of one (row, query head) merged: out = sum_s o_s 2^(m_s - M) /
-// sum_s l_s 2^(m_s - M).  Four warps, warp w adding every fourth split from w
-// in order, then the warps in order: a fixed order for the splits that the
-// row sees, whatever else is in the call.
-template <int D>
-__global__ void __launch_bounds__(128) k_attend_merge(const AttendParams p) {
-  constexpr int V = D / 32;  // elements per lane: columns V * lane ..
-  __shared__ float s_m[4], s_l[4];
-  __shared__ float s_o[4][D];
+// sum_s l_s 2^(m_s - M), in a fixed order for the splits that the row sees,
+// whatever else is in the call: the j-th of them belongs to strand j mod 8, each
+// strand is added up in order and then the strands; the denominators of 32
+// splits are added as a tree, and the groups of 32 in order.
+//   kWide: a block for each, a warp a strand (few rows, many splits: the
+// partials are requested side by side).  Else a warp does all of it.
+constexpr int kStrands = 8;
+template <int D, bool kWide>
+__global__ void __launch_bounds__(256) k_attend_merge(const AttendParams p) {
+  constexpr int V = D / 32, W = kStrands, B = 8;  // V: elements a lane, columns V * lane ..
+  extern __shared__ float s_dyn[];                // factors [max_splits], denominators [max_splits / 32] of a unit
+  __shared__ float s_red[W], s_o[kWide ? W : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x / p.n_q_heads, hq = blockIdx.x % p.n_q_heads;
+  const int unit = kWide ? blockIdx.x : blockIdx.x * W + warp;  // row * n_q_heads + head
+  const int groups = (p.max_splits + 31) / 32;
+  float* s_f = s_dyn + (kWide ? 0 : warp * groups * 33);
+  float* s_l = s_f + groups * 32;
+  const int r = unit / p.n_q_heads, hq = unit % p.n_q_heads;
   pdl_trigger();
-  pdl_wait();
-  int seq, i;
-  if (!find_row(p.rows, r, seq, i)) return;
-  const int t = first_of(p.rows, seq) + i;
+  int seq, i, t = 0;
+  const bool row = r < p.rows.n_rows && find_row(p.rows, r, seq, i);
+  if (row) t = first_of(p.rows, seq) + i;
   const SplitRange sr = splits_seen(t, t, p.window, p.sinks, p.rows.limit());
-  const size_t base = ((size_t)r * p.n_q_heads + hq) * p.max_splits;
+  pdl_wait();
+  if (!row) return;  // (a whole block, or a warp that meets no other)
+  auto meet = [] { if (kWide) __syncthreads(); else __syncwarp(); };
+  const int first = kWide ? threadIdx.x : lane, step = kWide ? 256 : 32;
+  const size_t base = (size_t)unit * p.max_splits;
   float M = -INFINITY;
-  for (int j = threadIdx.x; j < sr.n; j += 128) M = fmaxf(M, __ldcg(&p.part_ml[base + sr.at(j)].x));
+  for (int j = first; j < sr.n; j += step) M = fmaxf(M, __ldcg(&p.part_ml[base + sr.at(j)].x));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float ref = M == -INFINITY ? 0.0f : M;
-  float l = 0.0f, acc[V];
+  if (kWide) {
+    if (lane == 0) s_red[warp] = M;
+    __syncthreads();
 #pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int j = warp; j < sr.n; j += 4) {
-    const size_t slot = base + sr.at(j);
-    const float2 ml = __ldcg(&p.part_ml[slot]);
-    const float* src = p.part_o + slot * D + lane * V;
-    float x[V];
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_red[w]);
+  }
+  const float ref = M == -INFINITY ? 0.0f : M;
+  for (int j0 = first - lane; j0 < sr.n; j0 += step) {
+    const int j = j0 + lane;
+    float l = 0.0f, f = 0.0f;
+    if (j < sr.n) {
+      const float2 ml = __ldcg(&p.part_ml[base + sr.at(j)]);
+      f = ex2(__fsub_rn(ml.x, ref));
+      l = __fmul_rn(ml.y, f);
+    }
+    s_f[j] = f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, o));
+    if (lane == 0) s_l[j0 / 32] = l;
+  }
+  meet();
+  auto load = [&](int j, float (&x)[V]) {
+    const float* src = p.part_o + (base + sr.at(j)) * D + lane * V;
     if constexpr (V == 2) {
       const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
       x[0] = v.x; x[1] = v.y;
@@ -849,25 +931,69 @@ __global__ void __launch_bounds__(128) k_attend_merge(const AttendParams p) {
         x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
       }
     }
-    const float f = ex2(__fsub_rn(ml.x, ref));
-    l = __fmaf_rn(ml.y, f, l);
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(x[e], f, acc[e]);
-  }
-  if (lane == 0) s_l[warp] = l;
-#pragma unroll
-  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
-  __syncthreads();
-  l = __fadd_rn(__fadd_rn(s_l[0], s_l[1]), __fadd_rn(s_l[2], s_l[3]));
+  };
+  float l = 0.0f;
+  for (int k = 0; k < (sr.n + 31) / 32; ++k) l = __fadd_rn(l, s_l[k]);
   const bool none = l == 0.0f;  // a row that sees nothing: zeros
   bf16* out = p.out + (int64_t)r * p.out_stride + hq * D;
-  for (int c = threadIdx.x; c < D; c += 128) {
-    const float a = __fadd_rn(__fadd_rn(s_o[0][c], s_o[1][c]), __fadd_rn(s_o[2][c], s_o[3][c]));
-    out[c] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(a, l));
+  if constexpr (kWide) {  // this warp's strand, eight of its splits at a time
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+    for (int j0 = warp; j0 < sr.n; j0 += W * B) {
+      float x[B][V];
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (j0 + W * b < sr.n) load(j0 + W * b, x[b]);
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (j0 + W * b < sr.n) {
+          const float f = s_f[j0 + W * b];
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(x[b][e], f, acc[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += 256) {
+      float a = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) a = __fadd_rn(a, s_o[w][c]);
+      out[c] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(a, l));
+    }
+  } else {  // all strands, one split of each at a time
+    float acc[W][V];
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[w][e] = 0.0f;
+    for (int j0 = 0; j0 < sr.n; j0 += W) {
+      float x[W][V];
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (j0 + w < sr.n) load(j0 + w, x[w]);
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (j0 + w < sr.n) {
+          const float f = s_f[j0 + w];
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[w][e] = __fmaf_rn(x[w][e], f, acc[w][e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      float a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        a = __fadd_rn(a, acc[w][e]);
+        b = __fadd_rn(b, acc[w][e + 1]);
+      }
+      *reinterpret_cast<uint32_t*>(out + lane * V + e) = none ? 0u : pack_bf16x2(__fdiv_rn(a, l), __fdiv_rn(b, l));
+    }
   }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(size_t)r * p.n_q_heads + hq] =
-        none ? -INFINITY : __fmul_rn(__fadd_rn(M, log2f(l)), 0.6931471805599453f);
+  if (p.lse && lane == 0 && (!kWide || warp == 0))
+    p.lse[unit] = none ? -INFINITY : __fmul_rn(__fadd_rn(M, log2f(l)), 0.6931471805599453f);
   asm volatile("fence.proxy.async.global;" ::: "memory");  // a context reads it next by bulk copies
 }
 
@@ -906,11 +1032,20 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   cfg.numAttrs = pdl ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, k_attend<D, FMT, N>, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((int64_t)p.rows.n_rows * p.n_q_heads));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
+  const int64_t units = (int64_t)p.rows.n_rows * p.n_q_heads;
+  const size_t words = (size_t)((p.max_splits + 31) / 32) * 33;
+  cfg.blockDim = dim3(256);
   cfg.numAttrs = 1;  // the merge may be resident before the partials are complete: it waits for them
-  return cudaLaunchKernelEx(&cfg, k_attend_merge<D>, p);
+  // A warp for each result where there are enough of them to fill the device,
+  // or few splits to be had in parallel.
+  if ((units >= 8 * num_sms || p.max_splits <= 8) && words * 4 * kStrands <= kMergeMaxSmem) {
+    cfg.gridDim = dim3((unsigned)((units + kStrands - 1) / kStrands));
+    cfg.dynamicSmemBytes = words * 4 * kStrands;
+    return cudaLaunchKernelEx(&cfg, k_attend_merge<D, false>, p);
+  }
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.dynamicSmemBytes = words * 4;
+  return cudaLaunchKernelEx(&cfg, k_attend_merge<D, true>, p);
 }
 
 // Query tiles of 8, 16 or 32 rows (16 at most for heads of 256): the smallest
@@ -936,6 +1071,12 @@ template <int D, int FMT>
 cudaError_t attend_prepare() {
   cudaError_t e;
   if ((e = attend_prepare_t<D, FMT, 1>()) != cudaSuccess || (e = attend_prepare_t<D, FMT, 2>()) != cudaSuccess) return e;
+  // the factors of as many splits as a table reaches positions
+  if ((e = cudaFuncSetAttribute(k_attend_merge<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMergeMaxSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(k_attend_merge<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMergeMaxSmem)) != cudaSuccess)
+    return e;
   return attend_prepare_t<D, FMT, D == 256 ? 2 : 4>();
 }
 

@@ -42,18 +42,12 @@ cudaError_t launch_kv_fetch(const KvPool& c, const RowBatch& b, bf16* k, int64_t
 // sequence in shared memory.
 constexpr int kAttendMaxSeq = 1024;
 
-// Splits of the attention's work: ranges of absolute positions, 256 each below
-// position 4096 and 512 beyond.
-constexpr int kAttendSplitA = 256, kAttendRegionA = 4096, kAttendSplitB = 512;
-__host__ __device__ inline int attend_split_of(int pos) {
-  return pos < kAttendRegionA ? pos / kAttendSplitA
-                              : kAttendRegionA / kAttendSplitA + (pos - kAttendRegionA) / kAttendSplitB;
-}
-
-__host__ __device__ inline int attend_split_end(int split) {  // first position behind it
-  constexpr int n = kAttendRegionA / kAttendSplitA;
-  return split < n ? (split + 1) * kAttendSplitA : kAttendRegionA + (split + 1 - n) * kAttendSplitB;
-}
+// Splits of the attention's work: ranges of 256 absolute positions.
+constexpr int kAttendSplit = 256;
+__host__ __device__ inline int attend_split_of(int pos) { return pos / kAttendSplit; }
+// The merge keeps a factor for each split in shared memory: 160 KB hold those
+// of the 2^23 positions that a table may reach.
+constexpr int kMergeMaxSmem = 160 * 1024;
 
 struct AttendParams {
   RowBatch rows;

@@ -83,8 +83,9 @@ bool read_pool(const sv_kv_pool* a, KvPool& c) {
 
 bool read_rows(const sv_row_batch* a, RowBatch& b) {
   if (!a || a->n_seq < 1 || a->n_rows < 1 || a->table_stride < 1 || !a->block_table || !a->first) return false;
-  // positions and rows stay below 2^30 and 2^28: their sums fit 32 bits
-  if (a->table_stride > (1 << 30) / kPage || a->n_rows > (1 << 28)) return false;
+  // positions stay below 2^23 (the attention's merge keeps a word for each
+  // split) and rows below 2^28: their sums fit 32 bits
+  if (a->table_stride > (1 << 23) / kPage || a->n_rows > (1 << 28)) return false;
   b = {};
   b.n_seq = a->n_seq;
   b.n_rows = a->n_rows;
@@ -167,10 +168,10 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
   if (sv_attend_workspace(pool, rows, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
   if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev) return SV_E_INVAL;
   if (workspace_bytes < need) return SV_E_NOMEM;
-  // 32-bit counts on the device: query rows, and chunks of 64 positions for
+  // 32-bit counts on the device: query rows, and chunks of 16 positions for
   // every kv head and tile of at least 8 query rows
   const int64_t f = (int64_t)b.n_rows * n_q_heads;
-  if (f > INT32_MAX || (f / 8 + (int64_t)b.n_seq * c.n_kv_heads) * (b.limit() / 64 + 1) > INT32_MAX)
+  if (f > INT32_MAX || (f / 8 + (int64_t)b.n_seq * c.n_kv_heads) * (b.limit() / 16 + 1) > INT32_MAX)
     return SV_E_INVAL;
   int num_sms = 0;
   const int rc = device_setup(&num_sms);

@@ -365,7 +365,7 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  * (device int32 [n_seq + 1], not decreasing; NULL: n_rows / n_seq rows each),
  * which stand at positions first[s], first[s] + 1, ... (device int32 [n_seq]).
  * Position p lies in page block_table[s * table_stride + p / 16] at slot p % 16
- * (device int32 [n_seq, table_stride]).  n_rows: rows of the buffers; those
+ * (device int32 [n_seq, table_stride], at most 2^23 positions).  n_rows: rows of the buffers; those
  * behind the last sequence's are not touched.  max_rows: the most rows of a
  * sequence where the caller knows it (0: n_rows); only speed depends on it.
  * The device arrays are read when the kernels run: a captured graph may be
