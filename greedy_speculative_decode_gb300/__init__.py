@@ -32,7 +32,7 @@ class SvConfig(ctypes.Structure):
                                    "ffn", "vocab")] + [
         ("rms_eps", ctypes.c_float), ("rope_theta", ctypes.c_float)] + [
         (n, _i32) for n in ("qk_norm", "act", "tie_embeddings", "page_size", "max_pages", "max_k",
-                            "max_seq", "kv_delayed")]
+                            "max_seq", "kv_delayed", "kv_format", "window", "sinks")]
 
 
 LAYER_KEYS = ("attn_norm", "wqkv", "q_norm", "k_norm", "wo", "ffn_norm", "w_gate_up", "w_down")
@@ -422,16 +422,22 @@ class Context:
     layout of include/sv.h; the tensors must outlive the context.
     kv_delayed: commit a verify window's K/V only after acceptance (sv_config
     kv_delayed = 1) instead of writing it and zeroing the rejected rows.
+    kv_format: "bf16", or "e4m3" for a cache in 8 bits (sv_config kv_format).
+    window, sinks: attend only to the last `window` positions and the first
+    `sinks` (0: to all).
     """
 
     def __init__(self, cfg, weights, *, max_k: int, max_seq: int, max_pages: int | None = None,
-                 stream=None, kv_delayed: bool = False):
+                 stream=None, kv_delayed: bool = False, kv_format: str = "bf16", window: int = 0, sinks: int = 0):
+        if kv_format not in ("bf16", "e4m3"):
+            raise ValueError(f"kv_format {kv_format!r}, expected 'bf16' or 'e4m3'")
         self.cfg = cfg
         self.max_k, self.max_seq = max_k, max_seq
         pages = max_pages if max_pages is not None else (max_seq + PAGE_SIZE - 1) // PAGE_SIZE
         self._c = SvConfig(cfg.n_layers, cfg.hidden, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim,
                            cfg.ffn, cfg.vocab, cfg.rms_eps, cfg.rope_theta, cfg.qk_norm, cfg.act,
-                           cfg.tie_embeddings, PAGE_SIZE, pages, max_k, max_seq, int(bool(kv_delayed)))
+                           cfg.tie_embeddings, PAGE_SIZE, pages, max_k, max_seq, int(bool(kv_delayed)),
+                           SV_KV_E4M3 if kv_format == "e4m3" else SV_KV_BF16, int(window), int(sinks))
         self._weights = weights  # keep the tensors alive
         w = SvWeights()
         w.embed = _ptr(weights[("embed", -1)])

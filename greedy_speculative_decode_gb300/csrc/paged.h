@@ -21,6 +21,7 @@ struct RowBatch {
   const int* table;      // [n_seq, table_stride]
   const int* first;      // [n_seq]
   const int* row_start;  // [n_seq + 1] or null
+  const int* cap;        // positions from *cap on have no pages (a context's table may be stale there), or null
   __host__ __device__ int limit() const { return table_stride * kPage; }  // positions the table reaches
 };
 

@@ -89,7 +89,7 @@ __device__ __forceinline__ int first_of(const RowBatch& b, int seq) {
 __device__ __forceinline__ int find_page(const RowBatch& b, int n_pages, int seq, int pos, int* status) {
   const int lp = pos / kPage;
   int page = -1;
-  if (lp < b.table_stride) page = __ldg(&b.table[(size_t)seq * b.table_stride + lp]);
+  if (lp < b.table_stride && (b.cap == nullptr || pos < __ldcg(b.cap))) page = __ldg(&b.table[(size_t)seq * b.table_stride + lp]);
   if (page < 0 || page >= n_pages) {
     if (status) atomicOr(status, ST_BAD_PAGE);
     return -1;

@@ -13,6 +13,7 @@
 
 #include "sv_internal.h"
 #include "linear_tc.h"
+#include "paged.h"
 
 using namespace sv;
 
@@ -48,7 +49,13 @@ struct sv_ctx {
   // device memory owned by the context
   std::vector<void*> allocs;
   bf16 *kpool = nullptr, *vpool = nullptr;
-  size_t layer_stride = 0;  // elements per layer in each pool
+  size_t layer_stride = 0;  // elements per layer in each pool (an 8-bit pool: pairs of codes)
+  // 8-bit cache: the pools hold codes, kexp and vexp their exponents; a step's
+  // new rows go through the staging pages (bf16), which kv_write reads
+  uint8_t *kexp = nullptr, *vexp = nullptr;
+  bf16 *kstage = nullptr, *vstage = nullptr;
+  int* bt_stage = nullptr;  // logical page -> staging page
+  int* kv_first = nullptr;  // kv_read's first position
   int pool_pages = 0;       // pages per layer: max_pages, plus kWinPages scratch pages when delayed
   int* block_table = nullptr;
   int* bt_shadow = nullptr;  // delayed write-through: block table with the window on scratch pages
@@ -216,6 +223,17 @@ bool step_delayed(const sv_ctx* ctx, int M, int mode) {
   return ctx->bt_shadow != nullptr && mode == MODE_VERIFY && M > 1;
 }
 
+// An 8-bit cache, and the steps that run the paged-cache attention (that of
+// sv_attend) instead of k_attention.
+bool kv8(const sv_ctx* ctx) { return ctx->cfg.kv_format == SV_KV_E4M3; }
+bool attends_paged(const sv_ctx* ctx) { return kv8(ctx) || ctx->cfg.window > 0; }
+// Staging pages: a block of up to kTcMaxRows rows spans one page more than it fills.
+constexpr int kStagePages = kTcMaxRows / kPage + 1;
+
+// Elements of a cached position's row per kv head, as the kernels that move
+// rows whole (zeroing) see it: an 8-bit row is half as many bf16 elements.
+int row_elems(const sv_ctx* ctx) { return kv8(ctx) ? ctx->cfg.head_dim / 2 : ctx->cfg.head_dim; }
+
 // The block table through which a step's kernels write and read K/V.
 const int* step_table(const sv_ctx* ctx, int M, int mode) {
   return step_delayed(ctx, M, mode) ? ctx->bt_shadow : ctx->block_table;
@@ -260,6 +278,11 @@ LinParams lin_params(sv_ctx* ctx, int which, int l, int M, int mode, float* logi
     p.out_stride = Hq * d;
     p.kcache = ctx->kpool + (size_t)l * ctx->layer_stride;
     p.vcache = ctx->vpool + (size_t)l * ctx->layer_stride;
+    if (kv8(ctx)) {  // the step's rows as bf16, for kv_write to round
+      p.kcache = ctx->kstage;
+      p.vcache = ctx->vstage;
+      p.block_table = ctx->bt_stage;
+    }
     p.q_gain = c.qk_norm ? ctx->q_norm[l] : nullptr;
     p.k_gain = c.qk_norm ? ctx->k_norm[l] : nullptr;
   } else if (which == LIN_O) {
@@ -328,6 +351,60 @@ AttnParams attn_params(sv_ctx* ctx, int l, int M, int mode) {
   return ap;
 }
 
+// One layer's cache and a step's M rows as the paged-cache operators take them.
+KvPool kv_pool(sv_ctx* ctx, int l) {
+  const sv_config& c = ctx->cfg;
+  KvPool k = {};
+  k.fmt = c.kv_format;
+  k.n_pages = ctx->pool_pages;
+  k.n_kv_heads = c.n_kv_heads;
+  k.head_dim = c.head_dim;
+  k.block = 1;
+  k.k = reinterpret_cast<uint8_t*>(ctx->kpool + (size_t)l * ctx->layer_stride);
+  k.v = reinterpret_cast<uint8_t*>(ctx->vpool + (size_t)l * ctx->layer_stride);
+  const size_t per_layer = (size_t)ctx->pool_pages * c.n_kv_heads * kPage;
+  k.k_exp = ctx->kexp ? ctx->kexp + l * per_layer : nullptr;
+  k.v_exp = ctx->vexp ? ctx->vexp + l * per_layer : nullptr;
+  return k;
+}
+
+RowBatch step_rows(sv_ctx* ctx, int M, int mode) {
+  RowBatch b = {};
+  b.n_seq = 1;
+  b.n_rows = b.rows_each = b.max_rows = M;
+  b.table_stride = ctx->bt_len;
+  b.table = step_table(ctx, M, mode);
+  b.first = &ctx->st->step_pos;
+  b.cap = &ctx->st->cap_len;
+  return b;
+}
+
+AttendParams attend_params(sv_ctx* ctx, int l, int M, int mode) {
+  const sv_config& c = ctx->cfg;
+  const KvPool k = kv_pool(ctx, l);
+  AttendParams p = {};
+  p.rows = step_rows(ctx, M, mode);
+  p.q = ctx->q;
+  p.out = ctx->o;
+  p.q_stride = p.out_stride = c.n_q_heads * c.head_dim;
+  p.k = k.k;
+  p.v = k.v;
+  p.k_exp = k.k_exp;
+  p.v_exp = k.v_exp;
+  p.n_q_heads = c.n_q_heads;
+  p.n_kv_heads = c.n_kv_heads;
+  p.n_pages = k.n_pages;
+  p.block = 1;
+  p.window = c.window;
+  p.sinks = c.sinks;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
+  p.max_splits = ctx->max_splits;
+  p.part_ml = ctx->part_ml;
+  p.part_o = ctx->part_o;
+  p.status = &ctx->st->status;
+  return p;
+}
+
 // Enqueue every kernel of one step of M rows on ctx->stream.
 int enqueue_step(sv_ctx* ctx, int M, int mode, float* logits, const StepIo& io) {
   const sv_config& c = ctx->cfg;
@@ -393,9 +470,17 @@ int enqueue_step(sv_ctx* ctx, int M, int mode, float* logits, const StepIo& io) 
     if (l == 0) p.withhold_cta1 = ctx->withhold_cta1;
     CK(prenorm(p, norm));
     CK(run_linear(ctx, *ld, p, epi, norm, s, pdl, next_of(LIN_QKV, l)));
-    AttnParams ap = attn_params(ctx, l, M, mode);
-    CK(launch_attention(ctx->kmap, ctx->vmap, ap, d, attn_grid, attn_multi, s, pdl));
-    CK(launch_attn_combine(ap, d, s, pdl));
+    if (kv8(ctx)) {
+      const KvSource src = {ctx->kstage, ctx->vstage, 0, 0, kStagePages};
+      CK(launch_kv_write(kv_pool(ctx, l), step_rows(ctx, M, mode), src, &ctx->st->status, s, pdl));
+    }
+    if (attends_paged(ctx)) {
+      CK(launch_attend(attend_params(ctx, l, M, mode), c.kv_format, d, ctx->num_sms, s, pdl));
+    } else {
+      AttnParams ap = attn_params(ctx, l, M, mode);
+      CK(launch_attention(ctx->kmap, ctx->vmap, ap, d, attn_grid, attn_multi, s, pdl));
+      CK(launch_attn_combine(ap, d, s, pdl));
+    }
     for (int w : {LIN_O, LIN_GU, LIN_DOWN}) {
       p = lin_params(ctx, w, l, M, mode, logits, &epi, &norm, &ld);
       CK(prenorm(p, norm));
@@ -409,7 +494,7 @@ int enqueue_step(sv_ctx* ctx, int M, int mode, float* logits, const StepIo& io) 
     CK(run_linear(ctx, *ld, p, epi, norm, s, pdl, next_of(LIN_HEAD, 0)));
   }
   CK(launch_accept(ctx->st, ctx->am_val, ctx->am_idx, ctx->lin_head.n_tiles, M, mode, ctx->kpool,
-                   ctx->vpool, ctx->layer_stride, ctx->block_table, c.n_layers, Hkv, d, dl, s, pdl, io));
+                   ctx->vpool, ctx->layer_stride, ctx->block_table, c.n_layers, Hkv, row_elems(ctx), dl, s, pdl, io));
   return SV_OK;
 }
 
@@ -630,6 +715,9 @@ int validate(const sv_config* c) {
   if (c->page_size != kPage || c->max_k < 1 || c->max_k > kMaxK) return 0;
   if (c->max_seq < c->max_k || c->max_seq > kMaxSeq || c->max_pages < 1) return 0;
   if (c->kv_delayed != 0 && c->kv_delayed != 1) return 0;
+  if (c->kv_format != SV_KV_BF16 && c->kv_format != SV_KV_E4M3) return 0;
+  if (c->kv_format == SV_KV_E4M3 && c->kv_delayed) return 0;
+  if (c->window < 0 || c->sinks < 0) return 0;
   return 1;
 }
 
@@ -680,7 +768,7 @@ int sv_create(const sv_config* cfg, const sv_weights* w, void* cuda_stream, sv_c
   const char* wh = getenv("SV_TEST_WITHHOLD_PARTIAL");
   ctx->withhold_cta1 = wh ? atoi(wh) + 1 : 0;
   if (prepare_linear_kernels() != cudaSuccess || prepare_linear_tc_kernels() != cudaSuccess ||
-      prepare_attention_kernels() != cudaSuccess)
+      prepare_attention_kernels() != cudaSuccess || (attends_paged(ctx) && prepare_attend_kernels() != cudaSuccess))
     return bail(SV_E_CUDA);
   // the weights are read below (the tiled copies) on the library's stream:
   // let every stream's earlier work, which may still be writing them, finish
@@ -722,12 +810,12 @@ int sv_create(const sv_config* cfg, const sv_weights* w, void* cuda_stream, sv_c
   const int MP = mp_of(kMaxK);  // prefill blocks take kMaxK rows whatever max_k is
   ctx->bt_len = pages_for(c.max_seq);
   ctx->pool_pages = c.max_pages + (c.kv_delayed ? kWinPages : 0);
-  ctx->layer_stride = (size_t)ctx->pool_pages * Hkv * kPage * d;
+  ctx->layer_stride = (size_t)ctx->pool_pages * Hkv * kPage * row_elems(ctx);
   // kernels address the pools' rows of head_dim elements with 32-bit indices
   if ((size_t)ctx->pool_pages * Hkv * kPage * (L > 0 ? L : 1) >= (size_t)INT32_MAX)
     return bail(SV_E_INVAL);
   const size_t pool = ctx->layer_stride * (L > 0 ? L : 1);
-  ctx->max_splits = attn_n_splits(c.max_seq, d);
+  ctx->max_splits = attends_paged(ctx) ? attend_split_of(ctx->bt_len * kPage - 1) + 1 : attn_n_splits(c.max_seq, d);
   size_t ws_words = 0;
   auto acc_ws = [&](const LinearDesc& ld) {
     if (ld.max_seg > 1) ws_words = std::max(ws_words, (size_t)ld.grid * kLinRows * MP);
@@ -758,11 +846,23 @@ int sv_create(const sv_config* cfg, const sv_weights* w, void* cuda_stream, sv_c
       (rc = dalloc(ctx, &ctx->am_idx, (size_t)kMaxK * ctx->lin_head.n_tiles)))
     return bail(rc);
   if (c.kv_delayed && (rc = dalloc(ctx, &ctx->bt_shadow, (size_t)ctx->bt_len))) return bail(rc);
+  if (kv8(ctx)) {
+    const size_t exps = (size_t)ctx->pool_pages * Hkv * kPage * (L > 0 ? L : 1);
+    const size_t stage = (size_t)kStagePages * Hkv * kPage * d;
+    if ((rc = dalloc(ctx, &ctx->kexp, exps)) || (rc = dalloc(ctx, &ctx->vexp, exps)) ||
+        (rc = dalloc(ctx, &ctx->kstage, stage)) || (rc = dalloc(ctx, &ctx->vstage, stage)) ||
+        (rc = dalloc(ctx, &ctx->bt_stage, (size_t)ctx->bt_len)) || (rc = dalloc(ctx, &ctx->kv_first, 1)))
+      return bail(rc);
+    std::vector<int> table(ctx->bt_len);
+    for (int i = 0; i < ctx->bt_len; ++i) table[i] = i % kStagePages;
+    if (cudaMemcpy(ctx->bt_stage, table.data(), sizeof(int) * ctx->bt_len, cudaMemcpyHostToDevice) != cudaSuccess)
+      return bail(SV_E_CUDA);
+  }
   if (cudaMemset(ctx->ws, 0xff, ws_words * sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(ctx->ws_tc, 0xff, ws_tc_words * sizeof(uint32_t)) != cudaSuccess)
     return bail(SV_E_CUDA);
-  if (!make_bf16_map(&ctx->kmap, ctx->kpool, pool / d, d, kPage) ||
-      !make_bf16_map(&ctx->vmap, ctx->vpool, pool / d, d, kPage) ||
+  if ((!kv8(ctx) && (!make_bf16_map(&ctx->kmap, ctx->kpool, pool / d, d, kPage) ||
+                     !make_bf16_map(&ctx->vmap, ctx->vpool, pool / d, d, kPage))) ||
       !make_bf16_map(&ctx->xmap_x, ctx->x, kRows, H, kMaxK) || !make_bf16_map(&ctx->xmap_o, ctx->o, kRows, Hq * d, kMaxK) ||
       !make_bf16_map(&ctx->xmap_a, ctx->a, kRows, c.ffn, kMaxK) ||
       !make_bf16_map(&ctx->xmap128_x, ctx->x, kRows, H, kTcMaxRows) ||
@@ -980,7 +1080,7 @@ int sv_truncate(sv_ctx* ctx, int new_len) {
   if ((rc = begin_call(ctx))) return rc;
   const sv_config& c = ctx->cfg;
   CK(launch_kv_zero(ctx->kpool, ctx->vpool, ctx->layer_stride, ctx->block_table, c.n_layers,
-                    c.n_kv_heads, c.head_dim, new_len, ctx->seq_len, ctx->stream));
+                    c.n_kv_heads, row_elems(ctx), new_len, ctx->seq_len, ctx->stream));
   // a shorter sequence has no known greedy token until the next commit
   const int pending = new_len == ctx->seq_len ? kKeepPending : -1;
   if (pending == -1) ctx->pending = -1;
@@ -1003,6 +1103,21 @@ int sv_kv_read(sv_ctx* ctx, int layer, int first, int count, void* k_dst_dev, vo
       first + count > ctx->n_alloc * kPage || !k_dst_dev || !v_dst_dev)
     return fail(ctx, SV_E_INVAL, "kv_read(layer %d, %d, %d) outside the allocated pages (%d positions)",
                 layer, first, count, ctx->n_alloc * kPage);
+  if (kv8(ctx)) {
+    const int width = c.n_kv_heads * c.head_dim;
+    const int n = std::max(0, std::min(count, ctx->seq_len - first));  // the rest is past the length
+    bf16 *kd = static_cast<bf16*>(k_dst_dev), *vd = static_cast<bf16*>(v_dst_dev);
+    if (n > 0) {
+      RowBatch b = step_rows(ctx, n, MODE_BODY);
+      b.first = ctx->kv_first;
+      CK(cudaMemcpyAsync(ctx->kv_first, &first, sizeof(int), cudaMemcpyHostToDevice, ctx->stream));
+      CK(launch_kv_fetch(kv_pool(ctx, layer), b, kd, width, vd, width, nullptr, ctx->stream));
+    }
+    CK(cudaMemsetAsync(kd + (size_t)n * width, 0, (size_t)(count - n) * width * sizeof(bf16), ctx->stream));
+    CK(cudaMemsetAsync(vd + (size_t)n * width, 0, (size_t)(count - n) * width * sizeof(bf16), ctx->stream));
+    CK(cudaStreamSynchronize(ctx->stream));
+    return end_call(ctx);
+  }
   CK(launch_kv_gather(ctx->kpool, ctx->vpool, ctx->layer_stride, ctx->block_table, layer, c.n_kv_heads,
                       c.head_dim, first, count, static_cast<bf16*>(k_dst_dev), static_cast<bf16*>(v_dst_dev),
                       ctx->stream));
@@ -1097,7 +1212,7 @@ int sv_step_kernel_count(const sv_ctx* ctx, int K, int with_head) {
   // (enqueue_step's prenorm): before QKV and gate|up, and before the LM head
   const bool prenorm = K > 8 && ctx->use_tc;
   const int embeds = (K + kMaxK - 1) / kMaxK;  // larger blocks are embedded kMaxK rows a launch
-  const int per_layer = 6 + (prenorm ? 2 : 0);
+  const int per_layer = 6 + (prenorm ? 2 : 0) + (kv8(ctx) ? 1 : 0);
   const int tail = with_head ? 2 + (prenorm ? 1 : 0) : 1;  // [norm,] LM head, accept; or accept
   const int window = with_head && step_delayed(ctx, K, MODE_VERIFY) ? 1 : 0;
   return embeds + per_layer * ctx->cfg.n_layers + tail + window;

@@ -64,6 +64,8 @@ extern "C" {
 #define SV_PAGE_SIZE 16       /* positions per KV page */
 #define SV_MAX_K 32           /* most rows in one verify step */
 #define SV_MAX_PREFILL_ROWS 128 /* most rows in one prefill block (tcgen05 linears) */
+#define SV_KV_BF16 0          /* cache formats: bf16 values */
+#define SV_KV_E4M3 1          /* e4m3 codes with power-of-two scales */
 
 typedef struct sv_ctx sv_ctx;
 
@@ -94,6 +96,17 @@ typedef struct {
    *   1 costs 3 more pages per layer and one copy kernel per verify step.
    *   Prefill and decode steps commit every row and take path 0 either way. */
   int32_t kv_delayed;
+  /* kv_format: SV_KV_BF16 (0), or SV_KV_E4M3 (1) for a cache in 8 bits with one
+   * exponent for each kv head and position (scale_block 1 of the paged caches
+   * below): half the cache's bytes and traffic, one kernel more a layer, which
+   * rounds the step's rows as it writes them.  Not together with kv_delayed.
+   * window, sinks: with window > 0 the row at position t attends only to the
+   * positions p > t - window and p < sinks (a model trained so; the cache
+   * keeps every position).
+   *   Either runs the attention of sv_attend below, with the same batch
+   * invariance: a verify row is bit-identical to single-token decode, and
+   * results do not depend on how the cache was built. */
+  int32_t kv_format, window, sinks;
 } sv_config;
 
 /* Device pointers to bf16 weights, row-major, borrowed for the context's
@@ -244,7 +257,9 @@ int sv_seq_len(const sv_ctx* ctx);
  * layer into two device buffers k_dst_dev, v_dst_dev, each bf16 [count,
  * n_kv_heads, head_dim].  Positions may run to the end of the last page the
  * sequence holds, past its length: every slot there is zero (rejected rows
- * and truncated positions are zeroed), which tests check.  Synchronous. */
+ * and truncated positions are zeroed), which tests check.  An 8-bit cache is
+ * read as the values its codes stand for, and past the length as zeros.
+ * Synchronous. */
 int sv_kv_read(sv_ctx* ctx, int layer, int first, int count, void* k_dst_dev, void* v_dst_dev);
 
 /* Shuffle the order in which free pages are handed out (seeded).  Results
@@ -264,7 +279,7 @@ int sv_trace_hidden(sv_ctx* ctx, void* hidden_dev, int max_rows);
 
 /* Number of kernel launches in one step of K rows: with_head = 1 counts a
  * verify step (LM head and acceptance, and for kv_delayed with K > 1 the
- * window copy), 0 a prefill block without the LM head (a block of more than
+ * window copy; an 8-bit cache's write is counted in each layer), 0 a prefill block without the LM head (a block of more than
  * 32 rows is embedded 32 rows a launch).  Steps of more than 8 rows on the
  * tcgen05 form add one row normalisation before each QKV, gate|up and LM
  * head linear. */
@@ -386,8 +401,6 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  * sv_attend of a process on a device sets kernel attributes).  Returns SV_OK,
  * SV_E_INVAL (nothing launched), SV_E_NOMEM (workspace too small, nothing
  * launched) or SV_E_CUDA. */
-#define SV_KV_BF16 0
-#define SV_KV_E4M3 1
 typedef struct {
   int32_t format, n_pages, n_kv_heads, head_dim, scale_block;
   void *k, *v;
