@@ -64,7 +64,7 @@ struct AttendTile {
 // accumulators a lane leave room for.
 __host__ __device__ constexpr int attend_per_sm(int d, bool bf16, int n) {
   const int rb = d * (bf16 ? 2 : 1);
-  return rb == 512 ? 1 : n * d >= 256 ? (rb == 256 ? 1 : 2) : rb == 256 ? 2 : n * d <= 64 ? 4 : 3;
+  return rb == 512 ? 1 : n * d >= 512 ? (rb == 256 ? 1 : 2) : rb == 256 ? 2 : n * d <= 64 ? 4 : 3;
 }
 
 template <int D_, int FMT_, int N_>
@@ -82,7 +82,7 @@ struct AttendCfg {
   static constexpr int NK = D / 16;               // k16 steps of a score
   static constexpr int U = D / 16;                // 16-column units of the output
   static constexpr int QR = 8 * N;                // query rows of a tile
-  static constexpr bool kQRegs = N * NK <= 16;    // query fragments stay in registers
+  static constexpr bool kQRegs = N * NK <= 8;     // query fragments stay in registers
   // the warps' meeting: each leaves its accumulators in the stage it has done
   // with, all columns or a part of them at a time
   static constexpr int kRounds = QR * D * 4 > kStageBytes ? QR * D * 4 / kStageBytes : 1;
@@ -92,11 +92,11 @@ struct AttendCfg {
   static constexpr int kScaleBytes = kBf16 ? 0 : 2 * PW * kPage;   // exponents of a stage (one a position)
   static constexpr int kRing = kAttendWarps * kStages;             // stages of all warps
   static constexpr int kOffScale = kRing * kStageBytes;
-  static constexpr int kOffQ = kOffScale + kRing * kScaleBytes;    // query fragments of a warp [N][NK][32 lanes][2 words]
+  static constexpr int kOffQ = kOffScale + kRing * kScaleBytes;    // query fragments [N][NK][32 lanes][2 words]
   static constexpr int kQBytes = kQRegs ? 0 : N * NK * 256;
-  static constexpr int kOffMl = kOffQ + kAttendWarps * kQBytes;    // [QR][4 warps] (reference, sum)
-  static constexpr int kOffSlot = kOffMl + QR * 32;                // [QR] places of the query rows in the output
-  static constexpr int kOffSeq = kOffSlot + QR * 4;                // [n_seq + 1] chunks before, first, row start
+  static constexpr int kOffMl = kOffQ + kQBytes;                   // [QR][4 warps] (reference, sum)
+  static constexpr int kOffRow = kOffMl + QR * 32;                 // [QR] score factors, positions, places in the output
+  static constexpr int kOffSeq = kOffRow + 3 * QR * 4;             // [n_seq + 1] chunks before, first, row start
   static constexpr int smem_bytes(int n_seq) { return 128 + kOffSeq + 4 * (3 * n_seq + 2); }
   static_assert(128 + kOffSeq + 4 * (3 * kAttendMaxSeq + 2) <= 227 * 1024, "shared memory of a CTA");
 };
@@ -363,8 +363,7 @@ struct AttendRows {
   uint2* s_q;  // query fragments in shared memory, where they do not stay in registers
   uint8_t* smem;
   int warp, lane, g, q4;
-  float o[U][N][4], m_run[N][2], l_run[N][2], fac[N][2];
-  int tpos[N][2];  // positions of the lane's query rows
+  float o[U][N][4], m_run[N][2], l_run[N][2];
   uint32_t qr[C::kQRegs ? N * C::NK : 1][2];
 
   __device__ __forceinline__ AttendRows(const AttendParams& p_, uint8_t* smem_) : p(p_), smem(smem_) {
@@ -372,15 +371,20 @@ struct AttendRows {
     lane = threadIdx.x & 31;
     g = lane >> 2;
     q4 = lane & 3;
-    s_q = reinterpret_cast<uint2*>(smem + C::kOffQ + warp * C::kQBytes) + lane;
+    s_q = reinterpret_cast<uint2*>(smem + C::kOffQ) + lane;
   }
+  __device__ __forceinline__ float* s_fac() const { return reinterpret_cast<float*>(smem + C::kOffRow); }
+  __device__ __forceinline__ int* s_t() const { return reinterpret_cast<int*>(smem + C::kOffRow) + C::QR; }
+  __device__ __forceinline__ int* s_slot() const { return reinterpret_cast<int*>(smem + C::kOffRow) + 2 * C::QR; }
   __device__ __forceinline__ bool sees(int t, int pos) const {
     return pos <= t && (p.window <= 0 || pos > t - p.window || pos < p.sinks);
   }
 
   // A tile's queries as B fragments.  Lane (g, q4) takes row g of each query
   // tile, the elements it meets in K: its 16-byte units of a key row, four
-  // elements a k16 step.
+  // elements a k16 step.  (Every warp writes the same to shared memory, and
+  // reads back its own; the last tile's was last read before the warps' last
+  // meeting.)
   __device__ __forceinline__ void queries(const AttendTile& it, int G) {
     constexpr int kUnits = C::RB / 64, kV = kBf16 ? 1 : 2, kSteps = C::NK / kUnits;  // kV: 16-byte loads a unit
 #pragma unroll
@@ -431,20 +435,14 @@ struct AttendRows {
             s_q[at * 32] = make_uint2(b0, b1);
           }
         }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        fac[n][c] = __shfl_sync(0xffffffffu, up, (2 * q4 + c) * 4);
-        const int fq = it.f0 + n * 8 + 2 * q4 + c;
-        tpos[n][c] = it.first + fq / G;
+      // the rows' score factors, positions and places in the output (-1: no row)
+      if (q4 == 0) {
+        s_fac()[n * 8 + g] = up;
+        s_t()[n * 8 + g] = it.first + f / G;
+        s_slot()[n * 8 + g] = f < it.nf ? (it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G : -1;
       }
     }
-    // (fragments in shared memory: a lane reads its own)
-    // places in the output, -1: no row (a barrier comes before they are read, at the warps' meeting)
-    if (threadIdx.x < C::QR) {
-      const int fq = it.f0 + threadIdx.x;
-      reinterpret_cast<int*>(smem + C::kOffSlot)[threadIdx.x] =
-          fq < it.nf ? (it.row0 + fq / G) * p.n_q_heads + it.kvh * G + fq % G : -1;
-    }
+    __syncwarp();
   }
 
   __device__ __forceinline__ void open() {
@@ -477,7 +475,7 @@ struct AttendRows {
           for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              if (have && sees(tpos[n][c], pos)) {
+              if (have && sees(s_t()[n * 8 + 2 * q4 + c], pos)) {
                 float& x = o[u][n][2 * (k & 1) + c];
                 x = __fadd_rn(x, __uint_as_float(b));
               }
@@ -497,54 +495,7 @@ struct AttendRows {
   __device__ __forceinline__ void pages(uint32_t kp, const uint8_t* sc, int base, uint32_t have, const uint32_t (&ke)[PW],
                                         const uint32_t (&ve)[PW]) {
     const uint32_t vp = kp + PW * C::kPageBytes;
-    float s[PW][N][4];
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int j = 0; j < PW; ++j) s[j][n][e] = 0.0f;
     const int pos = pos_of_row<kBf16>(g), pos8 = pos_of_row<kBf16>(g + 8);
-    constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
-    constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      uint32_t x[PW][2][4];
-      const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
-#pragma unroll
-      for (int j = 0; j < PW; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[j][h][0]), "=r"(x[j][h][1]), "=r"(x[j][h][2]), "=r"(x[j][h][3])
-                       : "r"(kp + j * C::kPageBytes + page_off<C::RB>(h ? pos8 : pos, c)));
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        uint32_t a[PW][4];
-#pragma unroll
-        for (int j = 0; j < PW; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            a[j][h] = kBf16 ? x[j][h][(2 * k) & 3] : f16x2_of_lo(x[j][h][k & 3]);
-            a[j][2 + h] = kBf16 ? x[j][h][(2 * k + 1) & 3] : f16x2_of_hi(x[j][h][k & 3]);
-          }
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const int f = n * C::NK + u * kSteps + k;
-          uint32_t b0, b1;
-          if constexpr (C::kQRegs) {
-            b0 = qr[f][0];
-            b1 = qr[f][1];
-          } else {
-            const uint2 b = s_q[f * 32];
-            b0 = b.x;
-            b1 = b.y;
-          }
-#pragma unroll
-          for (int j = 0; j < PW; ++j) mma_16<kBf16>(s[j][n], a[j], b0, b1);
-        }
-      }
-    }
     // The lane's positions, two a page: key scale, value exponent ev and 2^-ev.  A byte
     // of 255 makes the score 0 * inf and ev inf * 0: NaN.
     float ks[PW][2], ev[PW][2], iv[PW][2];
@@ -573,65 +524,120 @@ struct AttendRows {
     uint32_t hi[PW][N][2], lo[kBf16 ? PW : 1][N][2];
     bool moved = false;
     float alpha[N][2];
+    // two query tiles' scores at a time: K is widened anew for the next two, which
+    // costs less than holding all scores beside the accumulators
+    constexpr int NG = N < 2 ? N : 2;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
+    for (int n0 = 0; n0 < N; n0 += NG) {
+      float s[PW][NG][4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float fc = fac[n][c];
-        float m = -INFINITY;
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < PW; ++j) s[j][n][e] = 0.0f;
+      constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
+      constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        uint32_t x[PW][2][4];
+        const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
 #pragma unroll
         for (int j = 0; j < PW; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float& x = s[j][n][2 * h + c];
-            x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[j][h]), ev[j][h]);
-            if (kEdge)
-              x = ((have >> j) & 1u) && sees(tpos[n][c], base + j * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
-            m = fmaxf(m, x);
+          for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[j][h][0]), "=r"(x[j][h][1]), "=r"(x[j][h][2]), "=r"(x[j][h][3])
+                         : "r"(kp + j * C::kPageBytes + page_off<C::RB>(h ? pos8 : pos, c)));
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[PW][4];
+#pragma unroll
+          for (int j = 0; j < PW; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              a[j][h] = kBf16 ? x[j][h][(2 * k) & 3] : f16x2_of_lo(x[j][h][k & 3]);
+              a[j][2 + h] = kBf16 ? x[j][h][(2 * k + 1) & 3] : f16x2_of_hi(x[j][h][k & 3]);
+            }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            const int f = (n0 + n) * C::NK + u * kSteps + k;
+            uint32_t b0, b1;
+            if constexpr (C::kQRegs) {
+              b0 = qr[f][0];
+              b1 = qr[f][1];
+            } else {
+              const uint2 b = s_q[f * 32];
+              b0 = b.x;
+              b1 = b.y;
+            }
+#pragma unroll
+            for (int j = 0; j < PW; ++j) mma_16<kBf16>(s[j][n], a[j], b0, b1);
           }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        float a = 1.0f;
-        if (m > __fadd_rn(m_run[n][c], kAttendSlack)) {  // (of a row's first pages: -inf, and nothing to scale)
-          if (m_run[n][c] != -INFINITY) {
-            a = ex2(__fsub_rn(m_run[n][c], m));
-            moved = true;
-          }
-          m_run[n][c] = m;
         }
-        // a row that has seen nothing yet: every weight is 2^-inf = 0
-        const float ref = m_run[n][c] == -INFINITY ? 0.0f : m_run[n][c];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < PW; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float& x = s[j][n][2 * h + c];
-            const float e = ex2(__fsub_rn(x, ref));
-            if (kBf16)
-              sum = __fadd_rn(sum, e);
-            else if (kEdge)  // (the exponent of a masked place may be anything)
-              sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[j][h], sum);
-            else
-              sum = __fmaf_rn(e, iv[j][h], sum);
-            x = e;
-          }
-        l_run[n][c] = __fmaf_rn(l_run[n][c], a, sum);
-        alpha[n][c] = a;
       }
 #pragma unroll
-      for (int j = 0; j < PW; ++j)
+      for (int n = 0; n < NG; ++n) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = s[j][n][2 * h], y = s[j][n][2 * h + 1];
-          if (kBf16) {
-            hi[j][n][h] = transposed(pack_bf16x2(x, y));
-            lo[kBf16 ? j : 0][n][h] = transposed(pack_bf16x2(__fsub_rn(x, bf16r(x)), __fsub_rn(y, bf16r(y))));
-          } else {
-            hi[j][n][h] = transposed(pack_f16x2(x, y));
+        for (int c = 0; c < 2; ++c) {
+          const float fc = s_fac()[(n0 + n) * 8 + 2 * q4 + c];
+          const int t = kEdge ? s_t()[(n0 + n) * 8 + 2 * q4 + c] : 0;
+          float m = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < PW; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& x = s[j][n][2 * h + c];
+              x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[j][h]), ev[j][h]);
+              if (kEdge)
+                x = ((have >> j) & 1u) && sees(t, base + j * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
+              m = fmaxf(m, x);
+            }
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          float a = 1.0f;
+          if (m > __fadd_rn(m_run[n0 + n][c], kAttendSlack)) {  // (of a row's first pages: -inf, and nothing to scale)
+            if (m_run[n0 + n][c] != -INFINITY) {
+              a = ex2(__fsub_rn(m_run[n0 + n][c], m));
+              moved = true;
+            }
+            m_run[n0 + n][c] = m;
           }
+          // a row that has seen nothing yet: every weight is 2^-inf = 0
+          const float ref = m_run[n0 + n][c] == -INFINITY ? 0.0f : m_run[n0 + n][c];
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < PW; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& x = s[j][n][2 * h + c];
+              const float e = ex2(__fsub_rn(x, ref));
+              if (kBf16)
+                sum = __fadd_rn(sum, e);
+              else if (kEdge)  // (the exponent of a masked place may be anything)
+                sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[j][h], sum);
+              else
+                sum = __fmaf_rn(e, iv[j][h], sum);
+              x = e;
+            }
+          l_run[n0 + n][c] = __fmaf_rn(l_run[n0 + n][c], a, sum);
+          alpha[n0 + n][c] = a;
         }
+#pragma unroll
+        for (int j = 0; j < PW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = s[j][n][2 * h], y = s[j][n][2 * h + 1];
+            if (kBf16) {
+              hi[j][n0 + n][h] = transposed(pack_bf16x2(x, y));
+              lo[kBf16 ? j : 0][n0 + n][h] = transposed(pack_bf16x2(__fsub_rn(x, bf16r(x)), __fsub_rn(y, bf16r(y))));
+            } else {
+              hi[j][n0 + n][h] = transposed(pack_f16x2(x, y));
+            }
+          }
+      }
+      if (n0 + NG < N) __syncwarp();  // (keeps the compiler from mixing the groups, and their registers)
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -683,7 +689,6 @@ struct AttendRows {
   __device__ __forceinline__ void partial(int split, uint8_t* left) {
     constexpr int W = kAttendWarps, T = kAttendThreads, kStride = C::kStages * C::kStageBytes;
     float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
-    const int* s_slot = reinterpret_cast<const int*>(smem + C::kOffSlot);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -711,7 +716,7 @@ struct AttendRows {
           }
       named_sync(2, T);
       for (int e = threadIdx.x; e < C::QR * kV; e += T) {
-        const int qi = e / kV, v = e % kV, slot = s_slot[qi];
+        const int qi = e / kV, v = e % kV, slot = s_slot()[qi];
         if (slot < 0) continue;
         float2 ml[W];
         float M = -INFINITY, l = 0.0f;
