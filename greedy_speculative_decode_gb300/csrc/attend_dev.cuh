@@ -524,9 +524,7 @@ struct AttendRows {
     uint32_t hi[PW][N][2], lo[kBf16 ? PW : 1][N][2];
     bool moved = false;
     float alpha[N][2];
-    // two query tiles' scores at a time: K is widened anew for the next two, which
-    // costs less than holding all scores beside the accumulators
-    constexpr int NG = N < 2 ? N : 2;
+    constexpr int NG = N;
 #pragma unroll
     for (int n0 = 0; n0 < N; n0 += NG) {
       float s[PW][NG][4];
@@ -752,7 +750,11 @@ template <class C>
 __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8_t* smem) {
   constexpr int S = C::kStages, PW = C::PW;
   AttendPlace<C> at;
-  if (!at.start(wk)) return;
+  bool waited = !p.early;
+  if (!at.start(wk)) {
+    if (!waited) pdl_wait();  // so that the grid completes in order
+    return;
+  }
   AttendRows<C> rows(p, smem);
   const int warp = rows.warp, lane = rows.lane;
   const uint32_t ring = smem_u32(smem) + warp * S * C::kStageBytes;
@@ -802,9 +804,15 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
       seen = pages_of(at.i + k, ahead);
+      if (!waited && (at.i + k >= run || (at.list.at(at.i + k) + 1) * C::kChunk > at.tile.first)) {
+        pdl_wait();  // the call's own rows are among these positions
+        waited = true;
+      }
       request(k, seen, ahead, have[k], ke[k], ve[k]);
     }
     seen = pages_of(at.i + S - 1, ahead);
+    if (!waited) pdl_wait();
+    waited = true;
     rows.queries(at.tile, wk.G);
     rows.open();
     bool any = false;  // the item has a chunk that the tile sees
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) 
   uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 127u);
   int* before = reinterpret_cast<int*>(smem + C::kOffSeq);
   pdl_trigger();
-  pdl_wait();
+  if (!p.early) pdl_wait();
   const int S = p.rows.n_seq, G = p.n_q_heads / p.n_kv_heads;
   int *first = before + S + 1, *start = first + S;  // (S + 1 starts)
   AttendWork<C> wk{p, before, first, start, 0, G};
@@ -1053,17 +1061,15 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   return cudaLaunchKernelEx(&cfg, k_attend_merge<D, true>, p);
 }
 
-// Query tiles of 8, 16 or 32 rows (16 at most for heads of 256): the smallest
-// that hold a sequence's rows at once, so that its pages are read and widened
-// as seldom as accumulators in registers allow.  A row's result is the same in
-// each (the columns of an mma do not meet).
+// Query tiles of 8 rows where they hold a sequence's rows, else of 16.  (Tiles
+// of 32 read and widened a page half as often, but at 128 accumulators a lane
+// eight warps an SM were too few: 8 x 16 rows at 4k took 46 us, with tiles of
+// 16 and twelve warps 38; a prefill block of 128 rows 74 and 70.)  A row's
+// result is the same in either (the columns of an mma do not meet).
 template <int D, int FMT>
-cudaError_t attend_launch(const AttendParams& p, int num_sms,
-                          cudaStream_t s, bool pdl) {
+cudaError_t attend_launch(const AttendParams& p, int num_sms, cudaStream_t s, bool pdl) {
   const int64_t f = (int64_t)p.rows.max_rows * (p.n_q_heads / p.n_kv_heads);
-  if (f <= 8) return attend_launch_t<D, FMT, 1>(p, num_sms, s, pdl);
-  if (f <= 16 || D == 256) return attend_launch_t<D, FMT, 2>(p, num_sms, s, pdl);
-  return attend_launch_t<D, FMT, D == 256 ? 2 : 4>(p, num_sms, s, pdl);
+  return f <= 8 ? attend_launch_t<D, FMT, 1>(p, num_sms, s, pdl) : attend_launch_t<D, FMT, 2>(p, num_sms, s, pdl);
 }
 
 template <int D, int FMT, int N>
@@ -1075,14 +1081,14 @@ cudaError_t attend_prepare_t() {
 template <int D, int FMT>
 cudaError_t attend_prepare() {
   cudaError_t e;
-  if ((e = attend_prepare_t<D, FMT, 1>()) != cudaSuccess || (e = attend_prepare_t<D, FMT, 2>()) != cudaSuccess) return e;
+  if ((e = attend_prepare_t<D, FMT, 1>()) != cudaSuccess) return e;
   // the factors of as many splits as a table reaches positions
   if ((e = cudaFuncSetAttribute(k_attend_merge<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kMergeMaxSmem)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(k_attend_merge<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kMergeMaxSmem)) != cudaSuccess)
     return e;
-  return attend_prepare_t<D, FMT, D == 256 ? 2 : 4>();
+  return attend_prepare_t<D, FMT, 2>();
 }
 
 }  // namespace

@@ -43,9 +43,13 @@ cudaError_t launch_kv_fetch(const KvPool& c, const RowBatch& b, bf16* k, int64_t
 // sequence in shared memory.
 constexpr int kAttendMaxSeq = 1024;
 
-// Splits of the attention's work: ranges of 256 absolute positions.
-constexpr int kAttendSplit = 256;
-__host__ __device__ inline int attend_split_of(int pos) { return pos / kAttendSplit; }
+// Splits of the attention's work: ranges of absolute positions, 128 each below
+// position 1024 (a short context has many CTAs at work), 256 beyond.
+constexpr int kAttendSplitA = 128, kAttendRegionA = 1024, kAttendSplitB = 256;
+__host__ __device__ inline int attend_split_of(int pos) {
+  return pos < kAttendRegionA ? pos / kAttendSplitA
+                              : kAttendRegionA / kAttendSplitA + (pos - kAttendRegionA) / kAttendSplitB;
+}
 // The merge keeps a factor for each split in shared memory: 160 KB hold those
 // of the 2^23 positions that a table may reach.
 constexpr int kMergeMaxSmem = 160 * 1024;
@@ -63,6 +67,10 @@ struct AttendParams {
   float2* part_ml;  // [n_rows, n_q_heads, max_splits] (running max in log2 units, sum)
   float* part_o;    // [n_rows, n_q_heads, max_splits, head_dim]
   int* status;      // or null
+  // Whether first, the tables and what the cache holds below first were there
+  // before the kernel ahead of this one began (a context's steps): they are then
+  // read, and the first pages requested, before the wait for that kernel.
+  bool early;
 };
 
 cudaError_t prepare_attend_kernels();

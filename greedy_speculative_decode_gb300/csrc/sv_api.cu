@@ -374,12 +374,12 @@ RowBatch step_rows(sv_ctx* ctx, int M, int mode) {
   b.n_rows = b.rows_each = b.max_rows = M;
   b.table_stride = ctx->bt_len;
   b.table = step_table(ctx, M, mode);
-  b.first = &ctx->st->step_pos;
+  b.first = &ctx->st->seq_len;  // final for the whole step: only its last kernel changes it
   b.cap = &ctx->st->cap_len;
   return b;
 }
 
-AttendParams attend_params(sv_ctx* ctx, int l, int M, int mode) {
+AttendParams attend_params(sv_ctx* ctx, int l, int M, int mode, bool pdl) {
   const sv_config& c = ctx->cfg;
   const KvPool k = kv_pool(ctx, l);
   AttendParams p = {};
@@ -402,6 +402,7 @@ AttendParams attend_params(sv_ctx* ctx, int l, int M, int mode) {
   p.part_ml = ctx->part_ml;
   p.part_o = ctx->part_o;
   p.status = &ctx->st->status;
+  p.early = pdl && !step_delayed(ctx, M, mode);  // (the shadow table is made inside the step)
   return p;
 }
 
@@ -475,7 +476,7 @@ int enqueue_step(sv_ctx* ctx, int M, int mode, float* logits, const StepIo& io) 
       CK(launch_kv_write(kv_pool(ctx, l), step_rows(ctx, M, mode), src, &ctx->st->status, s, pdl));
     }
     if (attends_paged(ctx)) {
-      CK(launch_attend(attend_params(ctx, l, M, mode), c.kv_format, d, ctx->num_sms, s, pdl));
+      CK(launch_attend(attend_params(ctx, l, M, mode, pdl), c.kv_format, d, ctx->num_sms, s, pdl));
     } else {
       AttnParams ap = attn_params(ctx, l, M, mode);
       CK(launch_attention(ctx->kmap, ctx->vmap, ap, d, attn_grid, attn_multi, s, pdl));

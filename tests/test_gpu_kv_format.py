@@ -166,6 +166,29 @@ def test_window_longer_than_the_sequence_is_no_window():
 
 
 @pytest.mark.gpu
+def test_window_with_delayed_write_through():
+    """kv_delayed with a window: the same bits as write-then-truncate, queued
+    without a pause between steps, over windows that straddle pages."""
+    cfg = QWEN
+    _, dw = gh.make(cfg)
+    prompt = inputs.prefix_tokens(7, 45, cfg.vocab)
+    runs = []
+    for delayed in (False, True):
+        ctx = context(cfg, dw, "bf16", 40, 3, kv_delayed=delayed, shuffle=2)
+        pending = ctx.prefill(prompt)
+        out = []
+        for s in range(12):
+            w = [pending] + [(pending + 3 * j + s) % cfg.vocab for j in range(1, 14)]
+            lg = gh.logits_buf(14, cfg.vocab)
+            n, pending = ctx.verify(w, logits=lg)
+            out.append((n, pending, lg))
+        runs.append((out, cache_of(ctx, cfg, len(ctx))))
+    for (n, p, lg), (n2, p2, lg2) in zip(runs[0][0], runs[1][0]):
+        assert (n, p) == (n2, p2) and torch.equal(lg, lg2)
+    assert same(runs[0][1], runs[1][1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt,window,sinks", FORMS[:3])
 def test_asynchronous_verify_and_graphs(fmt, window, sinks, monkeypatch):
     """Queued windows against the synchronous call, and against steps launched
