@@ -713,9 +713,10 @@ struct AttendRows {
             dst[(16 * u + 8 + g) ^ (8 * q4)] = o[rd * kUR + u][n][2 + c];
           }
       named_sync(2, T);
-      for (int e = threadIdx.x; e < C::QR * kV; e += T) {
-        const int qi = e / kV, v = e % kV, slot = s_slot()[qi];
-        if (slot < 0) continue;
+      // T / QR threads a query row, each every (T / QR)-th float4 of it
+      constexpr int kPer = T / C::QR;
+      const int qi = threadIdx.x / kPer, slot = s_slot()[qi];
+      if (slot >= 0) {
         float2 ml[W];
         float M = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -724,21 +725,28 @@ struct AttendRows {
           M = fmaxf(M, ml[w].x);
         }
         const float ref = M == -INFINITY ? 0.0f : M;
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float f = ex2(__fsub_rn(ml[w].x, ref));
-          const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(left + w * kStride) +
-                                                            qi * C::kCols + ((4 * v) ^ (8 * ((qi >> 1) & 3))));
-          l = __fmaf_rn(ml[w].y, f, l);
-          a.x = __fmaf_rn(x.x, f, a.x);
-          a.y = __fmaf_rn(x.y, f, a.y);
-          a.z = __fmaf_rn(x.z, f, a.z);
-          a.w = __fmaf_rn(x.w, f, a.w);
+          ml[w].x = ex2(__fsub_rn(ml[w].x, ref));
+          l = __fmaf_rn(ml[w].y, ml[w].x, l);
         }
         const size_t at = (size_t)slot * p.max_splits + split;
-        if (rd == 0 && v == 0) p.part_ml[at] = make_float2(M, l);
-        *reinterpret_cast<float4*>(p.part_o + at * C::D + rd * C::kCols + 4 * v) = a;
+        if (rd == 0 && threadIdx.x % kPer == 0) p.part_ml[at] = make_float2(M, l);
+        float* dst = p.part_o + at * C::D + rd * C::kCols;
+#pragma unroll
+        for (int v = threadIdx.x % kPer; v < kV; v += kPer) {
+          float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(left + w * kStride) +
+                                                              qi * C::kCols + ((4 * v) ^ (8 * ((qi >> 1) & 3))));
+            a.x = __fmaf_rn(x.x, ml[w].x, a.x);
+            a.y = __fmaf_rn(x.y, ml[w].x, a.y);
+            a.z = __fmaf_rn(x.z, ml[w].x, a.z);
+            a.w = __fmaf_rn(x.w, ml[w].x, a.w);
+          }
+          *reinterpret_cast<float4*>(dst + 4 * v) = a;
+        }
       }
       named_sync(2, T);  // the stages, and s_ml, are free again
     }
