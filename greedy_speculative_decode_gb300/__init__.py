@@ -262,6 +262,7 @@ class RowBatch:
         self.n_seq, self.n_rows, self.device = n_seq, int(n_rows), block_table.device
         self.tensors = (block_table, first, row_start)
         self._workspace = {}  # bytes by (query heads, head_dim): the sizes of a batch do not change
+        self._scratch = {}    # workspaces of attend by stream (see there)
         self._c = SvRowBatch(n_seq, int(n_rows), int(max_rows), pages, _ptr(block_table), _ptr(first),
                              _ptr(row_start))
         self._p = ctypes.byref(self._c)
@@ -343,15 +344,35 @@ def attend_workspace(cache: PagedKv, rows: RowBatch, n_q_heads: int) -> int:
     return need
 
 
+def _own_workspace(cache, rows, need, stream):
+    """The batch's workspace on the call's stream. Work on one stream runs in
+    order, so its calls may share one; allocated under that stream, its memory
+    goes back to that stream's pool."""
+    import torch
+    dev = cache.device.index
+    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return _own_workspace(cache, rows, need, None)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=cache.device)
+    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+    ws = rows._scratch.get(key)
+    if ws is None or ws.numel() < need:
+        ws = rows._scratch[key] = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    return ws
+
+
 def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: int = 0, scale=None, lse=None,
            workspace=None, status=None, stream=None):
     """sv_attend: attention of the rows over the cache. q, out: bf16 [n_rows,
     n_q_heads, head_dim] (rows may lie apart); the row at position t sees p <=
     t, or with a window only p > t - window or p < sinks. scale: None for
     1 / sqrt(head_dim). lse: fp32 [n_rows, n_q_heads] for the log-sum-exp, or
-    None. workspace: uint8 tensor of attend_workspace bytes; None takes one
-    from torch's allocator for this call, on torch's current stream (then
-    `stream`, if given, must be that one). Asynchronous."""
+    None. workspace: uint8 tensor of attend_workspace bytes; None takes one of
+    the batch's own, kept for each stream (a call that is being captured into
+    a graph takes a new one from the graph's memory, so that graphs share
+    none). Calls with a workspace of the caller's that may run at the same
+    time need one each. Asynchronous."""
     if getattr(q, "dim", lambda: 0)() != 3:
         raise ValueError("q: must be a 3-D tensor [n_rows, n_q_heads, head_dim]")
     heads = q.shape[1]
@@ -370,20 +391,15 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
             raise ValueError(f"lse: on {lse.device}, the cache on {cache.device}")
     need = attend_workspace(cache, rows, heads)
     if workspace is None:
-        import torch
-        if stream is not None and stream != torch.cuda.current_stream(cache.device):
-            raise ValueError("a stream that is not torch's current one needs a workspace of the caller's")
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-        given = need
+        workspace = _own_workspace(cache, rows, need, stream)
     else:
         _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
         if workspace.device != cache.device:
             raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
-        given = workspace.numel()
     if scale is None:
         scale = cache.head_dim ** -0.5
     _launch(cache, stream, _lib.sv_attend, cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse),
-            window, sinks, scale, workspace.data_ptr(), given, _ptr(status))
+            window, sinks, scale, workspace.data_ptr(), workspace.numel(), _ptr(status))
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):

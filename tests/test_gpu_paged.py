@@ -507,6 +507,55 @@ def test_captured_and_replayed_with_other_lengths():
         assert all(torch.equal(x, y) for x, y in zip(twin.tensors, c.cache.tensors))
 
 
+def test_two_graphs_of_one_batch_replayed_at_once():
+    """Graphs captured without a workspace of the caller's share none, so they
+    may be replayed beside one another."""
+    import torch
+    sv = _sv()
+    c = Case(32, 32, 8, 128, [4] * 8, [3000] * 8)
+    qs, want, outs, graphs = [c.queries() for _ in range(2)], [], [], []
+    for q in qs:
+        want.append(c.attend(q)[0])
+    streams = [torch.cuda.Stream() for _ in qs]
+    for q, s in zip(qs, streams):
+        out = torch.empty_like(q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(5):
+                sv.attend(c.cache, c.rows, q, out)
+        outs.append(out)
+        graphs.append(g)
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_one_batch_on_two_streams_at_once():
+    import torch
+    sv = _sv()
+    c = Case(33, 32, 8, 128, [4] * 8, [3000] * 8)
+    qs = [c.queries() for _ in range(2)]
+    want = [c.attend(q)[0] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for q, o, s in zip(qs, outs, streams):
+            if i % 2:
+                sv.attend(c.cache, c.rows, q, o, stream=s)
+            else:
+                with torch.cuda.stream(s):
+                    sv.attend(c.cache, c.rows, q, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
 def test_calls_on_two_streams_at_once():
     import torch
     a, b = Case(29, 32, 8, 128, [4] * 8, [3000] * 8), Case(30, 32, 8, 128, [1] * 20, [1500] * 20)
