@@ -53,6 +53,7 @@ namespace {
 constexpr int kAttendWarps = 4;  // of a CTA
 constexpr int kAttendThreads = kAttendWarps * 32;
 constexpr float kAttendSlack = 8.0f;  // log2 of what a row's maximum may exceed its reference by
+constexpr float kAttendFar = -126.0f;  // 2^x is a normal fp32 number from here on
 
 // A tile of query rows.
 struct AttendTile {
@@ -134,6 +135,13 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// l 2^d for d <= 0, also where 2^d by itself is below fp32's range (a
+// denominator of values near 2^-100 is large, one of values near 2^100 small).
+__device__ __forceinline__ float times_ex2(float l, float d) {
+  const float h = __fmul_rn(d, 0.5f);
+  return d < kAttendFar ? __fmul_rn(__fmul_rn(l, ex2(h)), ex2(h)) : __fmul_rn(l, ex2(d));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -521,106 +529,122 @@ struct AttendRows {
         }
       }
     }
-    uint32_t hi[PW][N][2], lo[kBf16 ? PW : 1][N][2];
-    bool moved = false;
-    float alpha[N][2];
-    constexpr int NG = N;
+    float s[PW][N][4];
 #pragma unroll
-    for (int n0 = 0; n0 < N; n0 += NG) {
-      float s[PW][NG][4];
+    for (int j = 0; j < PW; ++j)
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < N; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.0f;
+    constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
+    constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+    for (int u = 0; u < kUnits; ++u) {
+      uint32_t x[PW][2][4];
+      const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
 #pragma unroll
-          for (int j = 0; j < PW; ++j) s[j][n][e] = 0.0f;
-      constexpr int kUnits = C::RB / 64;      // 16-byte units of a key row per lane
-      constexpr int kSteps = C::NK / kUnits;  // k16 steps per unit
+      for (int j = 0; j < PW; ++j)
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        uint32_t x[PW][2][4];
-        const int c = C::RB == 64 ? q4 : (u >> 1) * 8 + 2 * q4 + (u & 1);
+        for (int h = 0; h < 2; ++h)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[j][h][0]), "=r"(x[j][h][1]), "=r"(x[j][h][2]), "=r"(x[j][h][3])
+                       : "r"(kp + j * C::kPageBytes + page_off<C::RB>(h ? pos8 : pos, c)));
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t a[PW][4];
 #pragma unroll
         for (int j = 0; j < PW; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[j][h][0]), "=r"(x[j][h][1]), "=r"(x[j][h][2]), "=r"(x[j][h][3])
-                         : "r"(kp + j * C::kPageBytes + page_off<C::RB>(h ? pos8 : pos, c)));
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[PW][4];
-#pragma unroll
-          for (int j = 0; j < PW; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              a[j][h] = kBf16 ? x[j][h][(2 * k) & 3] : f16x2_of_lo(x[j][h][k & 3]);
-              a[j][2 + h] = kBf16 ? x[j][h][(2 * k + 1) & 3] : f16x2_of_hi(x[j][h][k & 3]);
-            }
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            const int f = (n0 + n) * C::NK + u * kSteps + k;
-            uint32_t b0, b1;
-            if constexpr (C::kQRegs) {
-              b0 = qr[f][0];
-              b1 = qr[f][1];
-            } else {
-              const uint2 b = s_q[f * 32];
-              b0 = b.x;
-              b1 = b.y;
-            }
-#pragma unroll
-            for (int j = 0; j < PW; ++j) mma_16<kBf16>(s[j][n], a[j], b0, b1);
+          for (int h = 0; h < 2; ++h) {
+            a[j][h] = kBf16 ? x[j][h][(2 * k) & 3] : f16x2_of_lo(x[j][h][k & 3]);
+            a[j][2 + h] = kBf16 ? x[j][h][(2 * k + 1) & 3] : f16x2_of_hi(x[j][h][k & 3]);
           }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int f = n * C::NK + u * kSteps + k;
+          uint32_t b0, b1;
+          if constexpr (C::kQRegs) {
+            b0 = qr[f][0];
+            b1 = qr[f][1];
+          } else {
+            const uint2 b = s_q[f * 32];
+            b0 = b.x;
+            b1 = b.y;
+          }
+#pragma unroll
+          for (int j = 0; j < PW; ++j) mma_16<kBf16>(s[j][n], a[j], b0, b1);
         }
       }
+    }
+    bool moved = false;
+    float alpha[N][2], low = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float fc = s_fac()[n * 8 + 2 * q4 + c];
+        const int t = kEdge ? s_t()[n * 8 + 2 * q4 + c] : 0;
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < PW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[j][n][2 * h + c];
+            x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[j][h]), ev[j][h]);
+            if (kEdge)
+              x = ((have >> j) & 1u) && sees(t, base + j * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
+            m = fmaxf(m, x);
+          }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        alpha[n][c] = 1.0f;
+        if (m > __fadd_rn(m_run[n][c], kAttendSlack)) {  // (of a row's first pages: -inf, and nothing to scale)
+          if (m_run[n][c] != -INFINITY) {
+            const float d = __fsub_rn(m_run[n][c], m);
+            alpha[n][c] = ex2(d);
+            l_run[n][c] = times_ex2(l_run[n][c], d);
+            moved = true;
+          }
+          m_run[n][c] = m;
+        }
+        // a row that has seen nothing yet: every weight is 2^-inf = 0
+        const float ref = m_run[n][c] == -INFINITY ? 0.0f : m_run[n][c];
+#pragma unroll
+        for (int j = 0; j < PW; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[j][n][2 * h + c];
+            x = __fsub_rn(x, ref);
+            if (!kBf16) low = fminf(low, kEdge && x == -INFINITY ? 0.0f : x);
+          }
+      }
+    // The weights and, in the denominators, p' 2^-ev.  Where p' itself is below
+    // fp32's range the latter need not be (a block of zeros has ev = -100): it
+    // is then 2^(log2(e) s - ref) directly.
+    uint32_t hi[PW][N][2], lo[kBf16 ? PW : 1][N][2];
+    auto weights = [&](auto far) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float fc = s_fac()[(n0 + n) * 8 + 2 * q4 + c];
-          const int t = kEdge ? s_t()[(n0 + n) * 8 + 2 * q4 + c] : 0;
-          float m = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < PW; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float& x = s[j][n][2 * h + c];
-              x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[j][h]), ev[j][h]);
-              if (kEdge)
-                x = ((have >> j) & 1u) && sees(t, base + j * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
-              m = fmaxf(m, x);
-            }
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          float a = 1.0f;
-          if (m > __fadd_rn(m_run[n0 + n][c], kAttendSlack)) {  // (of a row's first pages: -inf, and nothing to scale)
-            if (m_run[n0 + n][c] != -INFINITY) {
-              a = ex2(__fsub_rn(m_run[n0 + n][c], m));
-              moved = true;
-            }
-            m_run[n0 + n][c] = m;
-          }
-          // a row that has seen nothing yet: every weight is 2^-inf = 0
-          const float ref = m_run[n0 + n][c] == -INFINITY ? 0.0f : m_run[n0 + n][c];
           float sum = 0.0f;
 #pragma unroll
           for (int j = 0; j < PW; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& x = s[j][n][2 * h + c];
-              const float e = ex2(__fsub_rn(x, ref));
+              const float e = ex2(x);
+              float y;
               if (kBf16)
-                sum = __fadd_rn(sum, e);
-              else if (kEdge)  // (the exponent of a masked place may be anything)
-                sum = x == -INFINITY ? sum : __fmaf_rn(e, iv[j][h], sum);
+                y = __fadd_rn(sum, e);
+              else if (far.value && x < kAttendFar)
+                y = __fadd_rn(sum, ex2(__fsub_rn(x, ev[j][h])));
               else
-                sum = __fmaf_rn(e, iv[j][h], sum);
+                y = __fmaf_rn(e, iv[j][h], sum);
+              // (the exponent of a masked place may be anything)
+              sum = kEdge && !kBf16 && x == -INFINITY ? sum : y;
               x = e;
             }
-          l_run[n0 + n][c] = __fmaf_rn(l_run[n0 + n][c], a, sum);
-          alpha[n0 + n][c] = a;
+          l_run[n][c] = __fadd_rn(l_run[n][c], sum);
         }
 #pragma unroll
         for (int j = 0; j < PW; ++j)
@@ -628,15 +652,16 @@ struct AttendRows {
           for (int h = 0; h < 2; ++h) {
             const float x = s[j][n][2 * h], y = s[j][n][2 * h + 1];
             if (kBf16) {
-              hi[j][n0 + n][h] = transposed(pack_bf16x2(x, y));
-              lo[kBf16 ? j : 0][n0 + n][h] = transposed(pack_bf16x2(__fsub_rn(x, bf16r(x)), __fsub_rn(y, bf16r(y))));
+              hi[j][n][h] = transposed(pack_bf16x2(x, y));
+              lo[kBf16 ? j : 0][n][h] = transposed(pack_bf16x2(__fsub_rn(x, bf16r(x)), __fsub_rn(y, bf16r(y))));
             } else {
-              hi[j][n0 + n][h] = transposed(pack_f16x2(x, y));
+              hi[j][n][h] = transposed(pack_f16x2(x, y));
             }
           }
       }
-      if (n0 + NG < N) __syncwarp();  // (keeps the compiler from mixing the groups, and their registers)
-    }
+    };
+    if (!kBf16 && __any_sync(0xffffffffu, low < kAttendFar)) weights(std::true_type());
+    else weights(std::false_type());
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -727,8 +752,9 @@ struct AttendRows {
         const float ref = M == -INFINITY ? 0.0f : M;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          ml[w].x = ex2(__fsub_rn(ml[w].x, ref));
-          l = __fmaf_rn(ml[w].y, ml[w].x, l);
+          const float d = __fsub_rn(ml[w].x, ref);
+          ml[w].x = ex2(d);
+          l = __fadd_rn(l, times_ex2(ml[w].y, d));
         }
         const size_t at = (size_t)slot * p.max_splits + split;
         if (rd == 0 && threadIdx.x % kPer == 0) p.part_ml[at] = make_float2(M, l);
@@ -931,8 +957,9 @@ __global__ void __launch_bounds__(256) k_attend_merge(const AttendParams p) {
     float l = 0.0f, f = 0.0f;
     if (j < sr.n) {
       const float2 ml = __ldcg(&p.part_ml[base + sr.at(j)]);
-      f = ex2(__fsub_rn(ml.x, ref));
-      l = __fmul_rn(ml.y, f);
+      const float d = __fsub_rn(ml.x, ref);
+      f = ex2(d);
+      l = times_ex2(ml.y, d);
     }
     s_f[j] = f;
 #pragma unroll

@@ -364,6 +364,28 @@ def test_queries_and_values_of_extreme_size(size):
     assert (np.abs(f64(out) - o) <= tol).all() and (np.abs(f64(lse) - l) <= tol_l).all()
 
 
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 9])
+def test_values_of_every_size_beside_one_another(block, d, rows):
+    """Blocks of zeros, tiny, ordinary and huge values under scores of like size:
+    each position counts in full in the denominator, whatever its values' scale."""
+    import torch
+    sv = _sv()
+    c = Case(23, 2, 1, d, [rows], [700], "e4m3", block)
+    n = 700 + rows
+    every = sv.RowBatch(c.table, torch.zeros(1, dtype=torch.int32, device="cuda"), n)
+    k, v = c.randn(n, 1, d, spread=0.0), c.randn(n, 1, d, spread=0.0)
+    sizes = torch.tensor([0.0, 2.0 ** -98, 2.0 ** -30, 1.0, 2.0 ** 50, 2.0 ** 110])
+    pick = torch.randint(0, 6, ((n + 15) // 16,), generator=c.g).repeat_interleave(16)[:n] if block == 16 else \
+        torch.randint(0, 6, (n,), generator=c.g)
+    pick[:130] = 0  # (the first split sees zeros alone, later ones small values first)
+    v = (v.float() * sizes[pick].cuda()[:, None, None]).bfloat16()
+    sv.kv_write(c.cache, every, k, v)
+    for window, sinks in ((0, 0), (300, 40)):
+        c.check_attend(window, sinks)
+
+
 # ------------------------------------------------------------------ a row's result is its own
 @pytest.mark.parametrize("fmt,block", FORMS)
 @pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 64), (8, 2, 128), (14, 2, 128), (8, 1, 256)])
