@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsv.so")
@@ -19,6 +20,7 @@ MAX_K = 32
 MAX_PREFILL_ROWS = 128
 SV_KV_BF16, SV_KV_E4M3 = 0, 1
 ATTEND_MAX_SEQ = 1024
+_INT_MAX = 2 ** 31 - 1
 _ERRNAMES = {SV_E_INVAL: "SV_E_INVAL", SV_E_NOMEM: "SV_E_NOMEM", SV_E_CUDA: "SV_E_CUDA",
              SV_E_STATE: "SV_E_STATE"}
 
@@ -253,16 +255,18 @@ class RowBatch:
         _check_tensor(block_table, "block_table", "torch.int32", (n_seq, pages))
         _check_tensor(first, "first", "torch.int32", (n_seq,))
         _check_tensor(row_start, "row_start", "torch.int32", (n_seq + 1,))
-        if n_rows < 1 or (row_start is None and n_rows % n_seq):
-            raise ValueError(f"n_rows {n_rows}: must be positive, and a multiple of {n_seq} without row_start")
-        if max_rows < 0:
-            raise ValueError(f"max_rows {max_rows}: must not be negative")
+        if not 1 <= n_rows <= 1 << 28 or (row_start is None and n_rows % n_seq):
+            raise ValueError(f"n_rows {n_rows}: must be positive (at most 2^28), and a multiple of {n_seq} without "
+                             "row_start")
+        if not 0 <= max_rows <= _INT_MAX:
+            raise ValueError(f"max_rows {max_rows}: must not be negative, nor above {_INT_MAX}")
         if first.device != block_table.device or (row_start is not None and row_start.device != first.device):
             raise ValueError("the batch's tensors lie on different devices")
         self.n_seq, self.n_rows, self.device = n_seq, int(n_rows), block_table.device
         self.tensors = (block_table, first, row_start)
         self._workspace = {}  # bytes by (query heads, head_dim): the sizes of a batch do not change
         self._scratch = {}    # workspaces of attend by stream (see there)
+        self._lock = threading.Lock()  # held while a call that uses one of them is issued
         self._c = SvRowBatch(n_seq, int(n_rows), int(max_rows), pages, _ptr(block_table), _ptr(first),
                              _ptr(row_start))
         self._p = ctypes.byref(self._c)
@@ -372,7 +376,7 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     the batch's own, kept for each stream (a call that is being captured into
     a graph takes a new one from the graph's memory, so that graphs share
     none). Calls with a workspace of the caller's that may run at the same
-    time need one each. Asynchronous."""
+    time, or that two threads issue on one stream, need one each. Asynchronous."""
     if getattr(q, "dim", lambda: 0)() != 3:
         raise ValueError("q: must be a 3-D tensor [n_rows, n_q_heads, head_dim]")
     heads = q.shape[1]
@@ -381,8 +385,8 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     qs = _check_rows(q, "q", cache, rows.n_rows, heads)
     os_ = _check_rows(out, "out", cache, rows.n_rows, heads)
     _check_call(cache, rows, status)
-    if window < 0 or sinks < 0:
-        raise ValueError(f"window {window}, sinks {sinks}: must not be negative")
+    if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
+        raise ValueError(f"window {window}, sinks {sinks}: must not be negative, nor above {_INT_MAX}")
     if rows.n_seq > ATTEND_MAX_SEQ:
         raise ValueError(f"{rows.n_seq} sequences, at most {ATTEND_MAX_SEQ}")
     if lse is not None:
@@ -390,16 +394,21 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
         if lse.device != cache.device:
             raise ValueError(f"lse: on {lse.device}, the cache on {cache.device}")
     need = attend_workspace(cache, rows, heads)
-    if workspace is None:
-        workspace = _own_workspace(cache, rows, need, stream)
-    else:
-        _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
-        if workspace.device != cache.device:
-            raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
     if scale is None:
         scale = cache.head_dim ** -0.5
-    _launch(cache, stream, _lib.sv_attend, cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse),
-            window, sinks, scale, workspace.data_ptr(), workspace.numel(), _ptr(status))
+
+    def issue(ws):
+        _launch(cache, stream, _lib.sv_attend, cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_,
+                _ptr(lse), window, sinks, scale, ws.data_ptr(), ws.numel(), _ptr(status))
+
+    if workspace is None:
+        with rows._lock:  # (the call is two launches: another thread's must not come between them)
+            issue(_own_workspace(cache, rows, need, stream))
+        return
+    _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
+    if workspace.device != cache.device:
+        raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
+    issue(workspace)
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):
@@ -447,6 +456,8 @@ class Context:
                  stream=None, kv_delayed: bool = False, kv_format: str = "bf16", window: int = 0, sinks: int = 0):
         if kv_format not in ("bf16", "e4m3"):
             raise ValueError(f"kv_format {kv_format!r}, expected 'bf16' or 'e4m3'")
+        if max(window, sinks) > _INT_MAX:
+            raise ValueError(f"window {window}, sinks {sinks}: at most {_INT_MAX}")
         self.cfg = cfg
         self.max_k, self.max_seq = max_k, max_seq
         pages = max_pages if max_pages is not None else (max_seq + PAGE_SIZE - 1) // PAGE_SIZE

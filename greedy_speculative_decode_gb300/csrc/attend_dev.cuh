@@ -263,7 +263,7 @@ struct AttendPlace {
     tile.f0 = x % tiles * C::QR;
     t0 = tile.first + tile.f0 / wk.G;
     t1 = tile.first + (min(tile.f0 + C::QR, tile.nf) - 1) / wk.G;
-    vis_lo = wk.p.window > 0 ? max(t0 - wk.p.window + 1, 0) : 0;
+    vis_lo = wk.p.window > 0 ? (int)max((int64_t)t0 - wk.p.window + 1, (int64_t)0) : 0;
     vis_end = min(t1 + 1, wk.p.rows.limit());
   }
   // The list's last place of this CTA's run + 1: the items that begin before `end`.
@@ -305,14 +305,19 @@ __device__ int attend_plan(const AttendParams& p, int G, int* before, int* first
     start[s] = p.rows.row_start ? min(max(p.rows.row_start[s], 0), p.rows.n_rows) : s * p.rows.rows_each;
   for (int s = tid; s < S; s += kAttendThreads) first[s] = first_of(p.rows, s);
   __syncthreads();
+  bool back = false;  // row starts that decrease: the counts below would not hold
   for (int s = tid; s < S; s += kAttendThreads) {
     const int n = max(0, start[s + 1] - start[s]);
+    back |= start[s + 1] < start[s];
     const int tiles = (n * G + C::QR - 1) / C::QR;
     const ChunkList l = chunks_seen<C>(first[s], first[s] + n - 1, p.window, p.sinks, p.rows.limit());
     before[s] = n > 0 ? tiles * p.n_kv_heads * l.n : 0;
     if (n > 0 && first[s] + n > p.rows.limit() && p.status) atomicOr(p.status, ST_BAD_PAGE);
   }
-  __syncthreads();
+  if (__syncthreads_or(back)) {
+    if (tid == 0 && p.status) atomicOr(p.status, ST_BAD_PAGE);
+    return 0;
+  }
   if (tid < 32) {  // exclusive running total
     int carry = 0;
     for (int s0 = 0; s0 < S; s0 += 32) {
@@ -521,7 +526,9 @@ struct AttendRows {
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t bk = (kw >> (16 * h)) & 255u, bv = (vw >> (16 * h)) & 255u;
+          // (bytes below the writer's smallest, as a zeroed cache has, count as that one:
+          // 2^-ev of a block of zeros stays in range)
+          const uint32_t bk = (kw >> (16 * h)) & 255u, bv = max((vw >> (16 * h)) & 255u, (uint32_t)kExpMinByte);
           ks[j][h] = __uint_as_float(bk << 23);
           iv[j][h] = __uint_as_float((254u - bv) << 23);
           // 2^23 + bv as a float, less 2^23 + 127

@@ -372,25 +372,29 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  *     keeps the page's exponent or raises it; when it rises the page's
  *     earlier codes are rounded again.  A page whose first position is
  *     written starts anew.
- * The NaN codes 0x7f, 0xff are not written; where a caller's own pool holds
- * them at positions a row sees, that row's result is not defined (NaN or a
- * number), other rows' are not affected.
+ * The NaN codes 0x7f, 0xff and the exponent bytes 248 to 254 are not written;
+ * where a caller's own pool holds them at positions a row sees, that row's
+ * result is not defined (NaN or a number), other rows' are not affected.
+ * Zeroed exponents and codes are zeros, as written zeros are.
  *
  * The rows of a call: sequence s brings rows row_start[s] .. row_start[s+1] - 1
- * (device int32 [n_seq + 1], not decreasing; NULL: n_rows / n_seq rows each),
+ * (device int32 [n_seq + 1], not decreasing (sv_attend raises status bit 2 and
+ * leaves the outputs undefined where it does); NULL: n_rows / n_seq rows each),
  * which stand at positions first[s], first[s] + 1, ... (device int32 [n_seq]).
  * Position p lies in page block_table[s * table_stride + p / 16] at slot p % 16
- * (device int32 [n_seq, table_stride], at most 2^23 positions).  n_rows: rows of the buffers; those
- * behind the last sequence's are not touched.  max_rows: the most rows of a
- * sequence where the caller knows it (0: n_rows); only speed depends on it.
+ * (device int32 [n_seq, table_stride], at most 2^23 positions).  n_rows: rows
+ * of the buffers (at most 2^28); those behind the last sequence's are not
+ * touched.  max_rows: the most rows of a sequence where the caller knows it
+ * (0: n_rows); only speed depends on it.
  * The device arrays are read when the kernels run: a captured graph may be
  * replayed with other lengths, tables and rows.
  *   Rows at negative positions are padding: not written, fetched as zeros,
  * and attending to nothing.  A page that the table does not reach or that is
  * not of the pool is passed over (nothing written, zeros fetched, its
  * positions unseen) and status bit 2 raised.
- *   In one sv_kv_write call no two rows may lie at the same place of the pool.
- * Pages may be shared between sequences otherwise (a common prefix).
+ *   In one sv_kv_write call no two rows may lie at the same place of the pool,
+ * with scale_block 16 no rows of two sequences in the same page (its exponent
+ * is one). Pages may be shared between sequences otherwise (a common prefix).
  *
  * Conventions: device pointers of the current device; strides in elements,
  * multiples of 8, between rows whose heads lie side by side (rows of a fused
@@ -427,13 +431,16 @@ int sv_kv_fetch(const sv_kv_pool* pool, const sv_row_batch* rows, void* k_dev, i
  *   h / (n_q_heads / n_kv_heads) (n_q_heads a multiple of n_kv_heads);
  *   lse_dev: fp32 [n_rows, n_q_heads] or NULL.  A row that sees nothing gives
  *   zeros and -infinity.  What lies in places a row does not see has no effect on it.
- * Softmax sums and accumulators are fp32.  A row's result depends on its own
+ * Softmax sums and accumulators are fp32.  Over an 8-bit cache a weight times
+ * its value block's scale is rounded to f16 relative to the row's largest such
+ * product (2^-11 of itself, at least 2^-25 of the largest).  A row's result depends on its own
  * query, position, window and cache alone, bit for bit: not on the other
  * rows or sequences of the call, nor on the pages that hold the cache.
  * n_seq is at most 1024.
  *   workspace_dev: sv_attend_workspace bytes (256-byte aligned) that the call
  *   may overwrite; calls that may run at the same time (other streams,
- *   captured graphs replayed beside one another) need one each. */
+ *   captured graphs replayed beside one another), or that two threads issue
+ *   on one stream, need one each. */
 int sv_attend_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, int64_t* bytes);
 int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, const void* q_dev, int64_t q_stride,
               void* out_dev, int64_t out_stride, float* lse_dev, int window, int sinks, float scale,

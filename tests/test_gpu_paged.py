@@ -269,6 +269,41 @@ def test_padding_rows_see_nothing(fmt, block):
     assert not np.isneginf(f64(lse)[5:9]).any()
 
 
+@pytest.mark.parametrize("fmt,block", FORMS)
+def test_the_widest_window_beside_padding_is_no_window(fmt, block):
+    import torch
+    c = Case(34, 4, 2, 128, [3, 4, 2], [-1, -2, 300], fmt, block)
+    q = c.queries()
+    want = c.attend(q)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
+        got = c.attend(q, window, sinks)
+        assert c.status == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("back", [1, 400])
+def test_positions_of_a_zeroed_cache_are_zeros(block, back):
+    """Nothing written to the last `back` positions: zero keys and values, of score 0 and weight 1."""
+    import torch
+    c = Case(35, 4, 2, 128, [2, 1], [410, 420], "e4m3", block)
+    for s, last in enumerate((411, 420)):
+        for p in range(last + 1 - back, last + 1):
+            pg, sl = int(c.table_h[s, p // PAGE]), p % PAGE
+            for t in c.cache.tensors[:2]:
+                t[pg, :, sl] = 0
+            if block == 1 or sl == 0:
+                for t in c.cache.tensors[2:]:
+                    t[pg, :, sl // block] = 0
+    c.check_attend()
+    for t in c.cache.tensors:
+        t.zero_()
+    q = c.queries()
+    out, lse = c.attend(q)
+    assert (out == 0).all()
+    seen = torch.tensor([411.0, 412.0, 421.0], dtype=torch.float64)
+    assert (lse.double().cpu() - seen.log()[:, None]).abs().max() <= 2.0 ** -22 * 140  # ln of sums near 2^127
+
+
 def _unseen(c, window=0, sinks=0):
     """Masks [pages, 16] of the places that no row of their sequence sees."""
     import torch
@@ -492,6 +527,20 @@ def test_row_starts_outside_the_buffers_touch_nothing_outside():
     assert (out[:2] == 5).all() and (out[7:] == 5).all()
 
 
+@pytest.mark.parametrize("starts", [[0, 5, 2, 5], [3, 0, 5, 5], [5, 4, 3, 0], [0, 2, 1, 5]])
+def test_row_starts_that_decrease_touch_nothing_outside(starts):
+    import torch
+    sv = _sv()
+    for fmt, block in FORMS:
+        c = Case(36, 4, 2, 64, [2, 2, 1], [20, 30, 3], fmt, block)
+        out = torch.full((9, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        rows = sv.RowBatch(c.table, c.first, 5, row_start=torch.tensor(starts, dtype=torch.int32, device="cuda"))
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sv.attend(c.cache, rows, c.queries(), out[2:7], status=st)
+        torch.cuda.synchronize()
+        assert (out[:2] == 5).all() and (out[7:] == 5).all() and int(st.item()) == 2
+
+
 def test_captured_and_replayed_with_other_lengths():
     """A graph of write and attend, replayed while the program advances the
     lengths on the device: each replay as the eager calls."""
@@ -576,6 +625,42 @@ def test_one_batch_on_two_streams_at_once():
                     sv.attend(c.cache, c.rows, q, o)
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_one_batch_of_two_threads_on_one_stream():
+    import threading
+    import torch
+    sv = _sv()
+    c = Case(37, 8, 2, 128, [2] * 4, [500] * 4)
+    qs = [c.queries() for _ in range(2)]
+    want = [c.attend(q)[0] for q in qs]
+    outs = [[torch.empty_like(q) for _ in range(300)] for q in qs]
+    meet = threading.Barrier(2)
+
+    def work(q, o):
+        meet.wait()
+        for x in o:
+            sv.attend(c.cache, c.rows, q, x)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(qs, outs)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for o, w in zip(outs, want) for x in o)
+
+
+def test_numbers_beyond_the_library_integers_are_refused():
+    """ctypes would drop their upper bits."""
+    sv = _sv()
+    c = Case(38, 2, 1, 64, [1], [3])
+    q = c.queries()
+    for kw in (dict(window=2 ** 32), dict(sinks=2 ** 32 + 4), dict(window=2 ** 31), dict(sinks=-2 ** 32)):
+        with pytest.raises(ValueError, match="must not be negative, nor above"):
+            c.attend(q, **kw)
+    with pytest.raises(ValueError, match="n_rows"):
+        sv.RowBatch(c.table, c.first, 2 ** 32 + 1)
+    with pytest.raises(ValueError, match="max_rows"):
+        sv.RowBatch(c.table, c.first, 1, max_rows=2 ** 32)
 
 
 def test_calls_on_two_streams_at_once():

@@ -97,3 +97,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         sv.PagedKv.empty(4, 2, 64, fmt="int8", device="cpu")
     with pytest.raises(ValueError, match="scale_block"):
         sv.PagedKv.empty(4, 2, 64, scale_block=8, device="cpu")
+
+
+@pytest.mark.parametrize("kw", [dict(window=2 ** 31), dict(sinks=2 ** 32 + 1)], ids=str)
+def test_a_context_refuses_numbers_beyond_the_library_integers(kw):
+    with pytest.raises(ValueError, match="at most"):
+        sv.Context(None, {}, max_k=4, max_seq=64, **kw)
