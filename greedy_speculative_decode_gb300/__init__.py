@@ -214,7 +214,7 @@ class PagedKv:
             if t.data_ptr() % 16:
                 raise ValueError("the cache's tensors must be aligned to 16 bytes")
         import torch
-        self._bf16 = torch.bfloat16
+        self._bf16, self._torch = torch.bfloat16, torch._C  # (at hand: looked up on every call)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, d, k.device
         self._c = SvKvPool(self.format, n_pages, n_kv, d, self.scale_block, _ptr(k), _ptr(v), _ptr(k_exp),
@@ -302,13 +302,13 @@ def _check_call(cache, rows, status):
 
 def _launch(cache, stream, call, *args):
     """call(*args, stream handle) on the cache's device; stream None: torch's current one there."""
-    import torch
     dev = cache.device.index
     # (the current stream's handle without the Stream object around it: 2 us less a call)
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    handle = cache._torch._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if cache._torch._cuda_getDevice() == dev:
         rc = call(*args, handle)
     else:
+        import torch
         with torch.cuda.device(dev):
             rc = call(*args, handle)
     if rc != SV_OK:
@@ -352,17 +352,23 @@ def _own_workspace(cache, rows, need, stream):
     """The batch's workspace on the call's stream. Work on one stream runs in
     order, so its calls may share one; allocated under that stream, its memory
     goes back to that stream's pool."""
-    import torch
     dev = cache.device.index
-    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
+    if cache._torch._cuda_getDevice() != dev:
+        import torch
+        with torch.cuda.device(dev):
+            return _own_workspace(cache, rows, need, stream)
+    key = cache._torch._cuda_getCurrentRawStream(dev)
+    if stream is not None and stream.cuda_stream != key:
+        import torch
+        with torch.cuda.stream(stream):
             return _own_workspace(cache, rows, need, None)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=torch.uint8, device=cache.device)
-    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
-    ws = rows._scratch.get(key)
+    capturing = cache._torch._cuda_isCurrentStreamCapturing()
+    ws = None if capturing else rows._scratch.get(key)
     if ws is None or ws.numel() < need:
-        ws = rows._scratch[key] = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        import torch
+        ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        if not capturing:
+            rows._scratch[key] = ws
     return ws
 
 
@@ -397,18 +403,16 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     if scale is None:
         scale = cache.head_dim ** -0.5
 
-    def issue(ws):
-        _launch(cache, stream, _lib.sv_attend, cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_,
-                _ptr(lse), window, sinks, scale, ws.data_ptr(), ws.numel(), _ptr(status))
-
+    args = (cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse), window, sinks, scale)
     if workspace is None:
         with rows._lock:  # (the call is two launches: another thread's must not come between them)
-            issue(_own_workspace(cache, rows, need, stream))
+            ws = _own_workspace(cache, rows, need, stream)
+            _launch(cache, stream, _lib.sv_attend, *args, ws.data_ptr(), need, _ptr(status))
         return
     _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
     if workspace.device != cache.device:
         raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
-    issue(workspace)
+    _launch(cache, stream, _lib.sv_attend, *args, workspace.data_ptr(), workspace.numel(), _ptr(status))
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):
