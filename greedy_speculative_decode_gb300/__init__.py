@@ -217,6 +217,7 @@ class PagedKv:
         self._bf16, self._torch = torch.bfloat16, torch._C  # (at hand: looked up on every call)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, d, k.device
+        self._index = k.device.index
         self._c = SvKvPool(self.format, n_pages, n_kv, d, self.scale_block, _ptr(k), _ptr(v), _ptr(k_exp),
                            _ptr(v_exp))
         self._p = ctypes.byref(self._c)
@@ -274,7 +275,7 @@ class RowBatch:
 
 def _check_rows(t, name, cache, n_rows, heads):
     """Rows of heads side by side: [n_rows, heads, head_dim] bf16 whose rows may
-    lie apart (a slice of a fused projection). Returns the row stride."""
+    lie apart (a slice of a fused projection). Returns the address and the row stride."""
     d = cache.head_dim
     if t.dtype is not cache._bf16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
@@ -282,13 +283,16 @@ def _check_rows(t, name, cache, n_rows, heads):
         raise ValueError(f"{name}: on {t.device}, the cache on {cache.device}")
     if t.shape != (n_rows, heads, d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n_rows, heads, d)}")
+    at = t.data_ptr()
+    if t.is_contiguous() and at % 16 == 0:
+        return at, heads * d
     row, head, one = t.stride()
     if n_rows == 1:  # a lone row's stride says nothing
         row = heads * d
-    if one != 1 or (head != d and heads > 1) or row < heads * d or row % 8 or t.data_ptr() % 16:
+    if one != 1 or (head != d and heads > 1) or row < heads * d or row % 8 or at % 16:
         raise ValueError(f"{name}: needs heads side by side in rows a multiple of 8 elements apart, 16-byte "
                          f"aligned; strides {t.stride()}")
-    return row
+    return at, row
 
 
 def _check_call(cache, rows, status):
@@ -302,10 +306,10 @@ def _check_call(cache, rows, status):
 
 def _launch(cache, stream, call, *args):
     """call(*args, stream handle) on the cache's device; stream None: torch's current one there."""
-    dev = cache.device.index
+    dev, torch_c = cache._index, cache._torch
     # (the current stream's handle without the Stream object around it: 2 us less a call)
-    handle = cache._torch._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if cache._torch._cuda_getDevice() == dev:
+    handle = torch_c._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch_c._cuda_getDevice() == dev:
         rc = call(*args, handle)
     else:
         import torch
@@ -319,20 +323,21 @@ def kv_write(cache: PagedKv, rows: RowBatch, k, v, *, status=None, stream=None):
     """sv_kv_write: put the rows' K and V (bf16 [n_rows, n_kv_heads, head_dim],
     rows may lie apart) into the cache. status: int32 [1], failure bits are
     ORed into it. stream: None for torch's current one. Asynchronous."""
-    ks = _check_rows(k, "k", cache, rows.n_rows, cache.n_kv_heads)
-    vs = _check_rows(v, "v", cache, rows.n_rows, cache.n_kv_heads)
+    n, heads = rows.n_rows, cache.n_kv_heads
+    kp, ks = _check_rows(k, "k", cache, n, heads)
+    vp, vs = _check_rows(v, "v", cache, n, heads)
     _check_call(cache, rows, status)
-    _launch(cache, stream, _lib.sv_kv_write, cache._p, rows._p, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(status))
+    _launch(cache, stream, _lib.sv_kv_write, cache._p, rows._p, kp, ks, vp, vs, _ptr(status))
 
 
 def kv_fetch(cache: PagedKv, rows: RowBatch, k_out, v_out, *, status=None, stream=None):
     """sv_kv_fetch: K and V of the rows' positions, as bf16, into k_out, v_out
     ([n_rows, n_kv_heads, head_dim]). Asynchronous."""
-    ks = _check_rows(k_out, "k_out", cache, rows.n_rows, cache.n_kv_heads)
-    vs = _check_rows(v_out, "v_out", cache, rows.n_rows, cache.n_kv_heads)
+    n, heads = rows.n_rows, cache.n_kv_heads
+    kp, ks = _check_rows(k_out, "k_out", cache, n, heads)
+    vp, vs = _check_rows(v_out, "v_out", cache, n, heads)
     _check_call(cache, rows, status)
-    _launch(cache, stream, _lib.sv_kv_fetch, cache._p, rows._p, k_out.data_ptr(), ks, v_out.data_ptr(), vs,
-            _ptr(status))
+    _launch(cache, stream, _lib.sv_kv_fetch, cache._p, rows._p, kp, ks, vp, vs, _ptr(status))
 
 
 def attend_workspace(cache: PagedKv, rows: RowBatch, n_q_heads: int) -> int:
@@ -352,7 +357,7 @@ def _own_workspace(cache, rows, need, stream):
     """The batch's workspace on the call's stream. Work on one stream runs in
     order, so its calls may share one; allocated under that stream, its memory
     goes back to that stream's pool."""
-    dev = cache.device.index
+    dev = cache._index
     if cache._torch._cuda_getDevice() != dev:
         import torch
         with torch.cuda.device(dev):
@@ -388,8 +393,8 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     heads = q.shape[1]
     if heads < 1 or heads % cache.n_kv_heads:
         raise ValueError(f"q: {heads} heads, not a multiple of the cache's {cache.n_kv_heads}")
-    qs = _check_rows(q, "q", cache, rows.n_rows, heads)
-    os_ = _check_rows(out, "out", cache, rows.n_rows, heads)
+    qp, qs = _check_rows(q, "q", cache, rows.n_rows, heads)
+    op, os_ = _check_rows(out, "out", cache, rows.n_rows, heads)
     _check_call(cache, rows, status)
     if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
         raise ValueError(f"window {window}, sinks {sinks}: must not be negative, nor above {_INT_MAX}")
@@ -403,7 +408,7 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     if scale is None:
         scale = cache.head_dim ** -0.5
 
-    args = (cache._p, rows._p, heads, q.data_ptr(), qs, out.data_ptr(), os_, _ptr(lse), window, sinks, scale)
+    args = (cache._p, rows._p, heads, qp, qs, op, os_, _ptr(lse), window, sinks, scale)
     if workspace is None:
         with rows._lock:  # (the call is two launches: another thread's must not come between them)
             ws = _own_workspace(cache, rows, need, stream)
