@@ -23,6 +23,13 @@
 // At the split's end the warps' results meet in shared memory and go out as its
 // partial; a second kernel merges the splits.
 //
+// What bounds it (32 query over 8 kv heads of 128, 8 bits; the call with its
+// merge): single-token decode of 32 sequences up to 8192 long 84 us, the
+// cache's 432 MB read at 5.7 TB/s; more query rows are bound by the
+// instructions around the products and the latency between them (half an
+// instruction a cycle and scheduler): 4 rows at 32768 31 us, 16 sequences of 4
+// rows in windows of 4096 45 us, a block of 128 rows at 4096 73 us.
+//
 // An 8-bit cache's exponents cost an addition each.  The key's scales its
 // score; the value's, ev, is added to the score in log2 units, t' = log2(e) s +
 // ev, and the weights are p' = 2^(t' - ref): they already carry the value's
@@ -45,6 +52,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstring>
 #include <type_traits>
 
 namespace sv {
@@ -53,6 +61,7 @@ namespace {
 constexpr int kAttendWarps = 4;  // of a CTA
 constexpr int kAttendThreads = kAttendWarps * 32;
 constexpr float kAttendSlack = 8.0f;  // log2 of what a row's maximum may exceed its reference by
+constexpr float kAttendNone = -3.0e38f;  // reference of a row that has seen nothing (finite: a weight is 2^(-inf) = 0)
 constexpr float kAttendFar = -126.0f;  // 2^x is a normal fp32 number from here on
 
 // A tile of query rows.
@@ -61,8 +70,8 @@ struct AttendTile {
   int first;              // position of the sequence's first row
 };
 
-// CTAs per SM: what the rings (64 KB at rows of 128 bytes) and N D / 4
-// accumulators a lane leave room for.
+// CTAs per SM: what the rings (64 KB at rows of 128 bytes, two stages of two
+// pages of K and V for each warp) and N D / 4 accumulators a lane leave room for.
 __host__ __device__ constexpr int attend_per_sm(int d, bool bf16, int n) {
   const int rb = d * (bf16 ? 2 : 1);
   return rb == 512 ? 1 : n * d >= 512 ? (rb == 256 ? 1 : 2) : rb == 256 ? 2 : n * d <= 64 ? 4 : 3;
@@ -97,7 +106,8 @@ struct AttendCfg {
   static constexpr int kQBytes = kQRegs ? 0 : N * NK * 256;
   static constexpr int kOffMl = kOffQ + kQBytes;                   // [QR][4 warps] (reference, sum)
   static constexpr int kOffRow = kOffMl + QR * 32;                 // [QR] score factors, positions, places in the output
-  static constexpr int kOffSeq = kOffRow + 3 * QR * 4;             // [n_seq + 1] chunks before, first, row start
+  static constexpr int kOffPlace = kOffRow + 3 * QR * 4;           // [4 warps] the CTA's place in its run
+  static constexpr int kOffSeq = kOffPlace + kAttendWarps * 80;    // [n_seq + 1] chunks before, first, row start
   static constexpr int smem_bytes(int n_seq) { return 128 + kOffSeq + 4 * (3 * n_seq + 2); }
   static_assert(128 + kOffSeq + 4 * (3 * kAttendMaxSeq + 2) <= 227 * 1024, "shared memory of a CTA");
 };
@@ -380,7 +390,7 @@ struct AttendRows {
   uint32_t qr[C::kQRegs ? N * C::NK : 1][2];
 
   __device__ __forceinline__ AttendRows(const AttendParams& p_, uint8_t* smem_) : p(p_), smem(smem_) {
-    warp = threadIdx.x >> 5;
+    warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     lane = threadIdx.x & 31;
     g = lane >> 2;
     q4 = lane & 3;
@@ -461,7 +471,7 @@ struct AttendRows {
   __device__ __forceinline__ void open() {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      m_run[n][0] = m_run[n][1] = -INFINITY;
+      m_run[n][0] = m_run[n][1] = kAttendNone;
       l_run[n][0] = l_run[n][1] = 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) o[u][n][0] = o[u][n][1] = o[u][n][2] = o[u][n][3] = 0.0f;
@@ -581,8 +591,8 @@ struct AttendRows {
         }
       }
     }
-    bool moved = false;
-    float alpha[N][2], low = 0.0f;
+    float top[N][2], low = 0.0f;
+    bool rise = false;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -603,27 +613,44 @@ struct AttendRows {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        alpha[n][c] = 1.0f;
-        if (m > __fadd_rn(m_run[n][c], kAttendSlack)) {  // (of a row's first pages: -inf, and nothing to scale)
-          if (m_run[n][c] != -INFINITY) {
-            const float d = __fsub_rn(m_run[n][c], m);
-            alpha[n][c] = ex2(d);
-            l_run[n][c] = times_ex2(l_run[n][c], d);
-            moved = true;
-          }
-          m_run[n][c] = m;
+        top[n][c] = m;
+        rise |= m > __fadd_rn(m_run[n][c], kAttendSlack);
+      }
+    if (__any_sync(0xffffffffu, rise)) {
+      float alpha[N][2];
+      bool scaled = false;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const bool up = top[n][c] > __fadd_rn(m_run[n][c], kAttendSlack);
+          const float d = up ? __fsub_rn(m_run[n][c], top[n][c]) : 0.0f;
+          alpha[n][c] = ex2(d);
+          l_run[n][c] = times_ex2(l_run[n][c], d);
+          scaled |= up && m_run[n][c] != kAttendNone;  // (behind a row's first pages there is nothing to scale)
+          m_run[n][c] = up ? top[n][c] : m_run[n][c];
         }
-        // a row that has seen nothing yet: every weight is 2^-inf = 0
-        const float ref = m_run[n][c] == -INFINITY ? 0.0f : m_run[n][c];
+      if (__any_sync(0xffffffffu, scaled)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[u][n][e] = __fmul_rn(o[u][n][e], alpha[n][e & 1]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int j = 0; j < PW; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float& x = s[j][n][2 * h + c];
-            x = __fsub_rn(x, ref);
+            x = __fsub_rn(x, m_run[n][c]);
             if (!kBf16) low = fminf(low, kEdge && x == -INFINITY ? 0.0f : x);
           }
-      }
     // The weights and, in the denominators, p' 2^-ev.  Where p' itself is below
     // fp32's range the latter need not be (a block of zeros has ev = -100): it
     // is then 2^(log2(e) s - ref) directly.
@@ -669,14 +696,6 @@ struct AttendRows {
     };
     if (!kBf16 && __any_sync(0xffffffffu, low < kAttendFar)) weights(std::true_type());
     else weights(std::false_type());
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[u][n][e] = __fmul_rn(o[u][n][e], alpha[n][e & 1]);
-    }
 #pragma unroll
     for (int u = 0; u < U; u += 2) {
 #pragma unroll
@@ -750,16 +769,15 @@ struct AttendRows {
       const int qi = threadIdx.x / kPer, slot = s_slot()[qi];
       if (slot >= 0) {
         float2 ml[W];
-        float M = -INFINITY, l = 0.0f;
+        float M = kAttendNone, l = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           ml[w] = s_ml[qi * W + w];
           M = fmaxf(M, ml[w].x);
         }
-        const float ref = M == -INFINITY ? 0.0f : M;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float d = __fsub_rn(ml[w].x, ref);
+          const float d = __fsub_rn(ml[w].x, M);
           ml[w].x = ex2(d);
           l = __fadd_rn(l, times_ex2(ml[w].y, d));
         }
@@ -801,6 +819,11 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
   const uint32_t ring = smem_u32(smem) + warp * S * C::kStageBytes;
   const uint8_t* scales = smem + C::kOffScale + warp * S * C::kScaleBytes;
   const uint32_t scales_at = smem_u32(scales);
+  // (What only the next list needs of the place waits in shared memory, so that
+  // the loop over a list has the registers.)
+  static_assert(sizeof(AttendPlace<C>) <= 80, "a warp's place");
+  volatile int* kept = reinterpret_cast<int*>(smem + C::kOffPlace + warp * 80);
+  constexpr int kWords = sizeof(AttendPlace<C>) / 4;
   for (;;) {
     const int run = at.run_end();
     const int* table = p.rows.table + (size_t)at.seq * p.rows.table_stride;
@@ -856,6 +879,12 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
     waited = true;
     rows.queries(at.tile, wk.G);
     rows.open();
+    {
+      int w[kWords];
+      memcpy(w, &at, sizeof w);
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) kept[k] = w[k];  // (every lane the same)
+    }
     bool any = false;  // the item has a chunk that the tile sees
     int st = 0;
     for (int i = at.i; i < run; ++i) {
@@ -898,6 +927,12 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    {
+      int w[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) w[k] = kept[k];
+      memcpy(&at, w, sizeof w);
+    }
     if (!at.past(wk, run)) return;
     __syncwarp();  // every lane is done with this tile's stages (and the CTA, by its last meeting, with the slots)
   }
@@ -1091,9 +1126,10 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   const size_t words = (size_t)((p.max_splits + 31) / 32) * 33;
   cfg.blockDim = dim3(256);
   cfg.numAttrs = 1;  // the merge may be resident before the partials are complete: it waits for them
-  // A warp for each result where there are enough of them to fill the device,
-  // or few splits to be had in parallel.
-  if ((units >= 8 * num_sms || p.max_splits <= 8) && words * 4 * kStrands <= kMergeMaxSmem) {
+  // A warp for each result where there are enough of them to fill the device, or
+  // few splits to be had in parallel.  (128 rows of 32 heads over 4k: the call
+  // 77 us with a warp each, 89 with a block each; 32 rows over 8k 83.5 and 84.3.)
+  if ((units >= 4 * num_sms || p.max_splits <= 8) && words * 4 * kStrands <= kMergeMaxSmem) {
     cfg.gridDim = dim3((unsigned)((units + kStrands - 1) / kStrands));
     cfg.dynamicSmemBytes = words * 4 * kStrands;
     return cudaLaunchKernelEx(&cfg, k_attend_merge<D, false>, p);

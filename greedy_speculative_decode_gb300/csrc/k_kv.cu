@@ -2,7 +2,10 @@
 //
 // Both directions are bound by memory: per row and kv head they move 2 D
 // bf16 values on one side and 2 D codes (and exponents) on the other, with a
-// handful of instructions per value.
+// handful of instructions per value.  8 kv heads of 128, 8 bits: 8191 rows
+// written in 11.8 us (50 MB moved, 4.3 TB/s), 48 runs of up to 61 rows with an
+// exponent a page in 9.5 us, 24 runs of up to 700 fetched in 13.7 us (62 MB,
+// 4.5 TB/s); a few rows in 2.6 us, a launch and one wait for memory.
 #include "paged.h"
 #include "paged_dev.cuh"
 
@@ -44,7 +47,8 @@ __device__ __forceinline__ const uint4* src_row(const bf16* x, int64_t stride, c
 
 // Where a row's K and V of one kv head lie: D / 8 lanes move a (row, kv head),
 // 16 bytes of bf16 each, and take HB heads of their row at once, so that the row
-// is looked up once and 2 HB loads are in flight before the first is used.
+// is looked up once and 2 HB loads are in flight before the first is used.  (One
+// head at a time wrote the 8191 rows in 20.6 us and fetched the 24 runs in 18.4.)
 template <int D, int HB>
 struct RowUnit {
   static constexpr int L = D / 8;
