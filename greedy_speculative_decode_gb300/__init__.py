@@ -322,7 +322,8 @@ def _launch(cache, stream, call, *args):
 def kv_write(cache: PagedKv, rows: RowBatch, k, v, *, status=None, stream=None):
     """sv_kv_write: put the rows' K and V (bf16 [n_rows, n_kv_heads, head_dim],
     rows may lie apart) into the cache. status: int32 [1], failure bits are
-    ORed into it. stream: None for torch's current one. Asynchronous."""
+    ORed into it. stream: None for torch's current one. Asynchronous: tensors
+    of another stream's than the call's must be kept until it has run."""
     n, heads = rows.n_rows, cache.n_kv_heads
     kp, ks = _check_rows(k, "k", cache, n, heads)
     vp, vs = _check_rows(v, "v", cache, n, heads)
