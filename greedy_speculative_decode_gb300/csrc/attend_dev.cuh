@@ -605,7 +605,7 @@ struct AttendRows {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float& x = s[j][n][2 * h + c];
-            x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(x, __fmul_rn(fc, ks[j][h]), ev[j][h]);
+            x = kBf16 ? __fmul_rn(x, fc) : __fmaf_rn(__fmul_rn(x, fc), ks[j][h], ev[j][h]);
             if (kEdge)
               x = ((have >> j) & 1u) && sees(t, base + j * kPage + (h ? pos8 : pos)) ? x : -INFINITY;
             m = fmaxf(m, x);

@@ -421,6 +421,26 @@ def test_values_of_every_size_beside_one_another(block, d, rows):
         c.check_attend(window, sinks)
 
 
+@pytest.mark.parametrize("fmt,block", FORMS)
+def test_huge_keys_across_huge_queries(fmt, block):
+    """Products that are zero while the scales' product is beyond fp32: scores of zero, not NaN."""
+    import torch
+    sv = _sv()
+    c = Case(39, 2, 1, 64, [2], [40], fmt, block)
+    every = sv.RowBatch(c.table, torch.zeros(1, dtype=torch.int32, device="cuda"), 42)
+    k, v = c.randn(42, 1, 64, spread=0.0), c.randn(42, 1, 64, spread=0.0)
+    k[:, :, :32] = 0
+    k *= 2.0 ** 80
+    sv.kv_write(c.cache, every, k, v)
+    q = c.queries() * 2.0 ** 80
+    q[:, :, 32:] = 0
+    out, lse = c.attend(q)
+    o, l, tol, tol_l = ref.attend(c.pool_np(), c.table_h.numpy(), c.where, f64(q), 0, 0, 0.125)
+    # scores are exactly zero: an output is off by half a bf16 step, 2^-11 for each
+    # weight of a mean magnitude below two, and fp32 sums of 42 terms; ln 42 by 2^-18
+    assert (np.abs(f64(out) - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -9).all() and (np.abs(f64(lse) - l) <= 2.0 ** -18).all()
+
+
 # ------------------------------------------------------------------ a row's result is its own
 @pytest.mark.parametrize("fmt,block", FORMS)
 @pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 64), (8, 2, 128), (14, 2, 128), (8, 1, 256)])
