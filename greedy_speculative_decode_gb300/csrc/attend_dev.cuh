@@ -406,8 +406,8 @@ struct AttendRows {
   // A tile's queries as B fragments.  Lane (g, q4) takes row g of each query
   // tile, the elements it meets in K: its 16-byte units of a key row, four
   // elements a k16 step.  (Every warp writes the same to shared memory, and
-  // reads back its own; the last tile's was last read before the warps' last
-  // meeting.)
+  // reads back its own.  The warps meet between two tiles' queries, see
+  // attend_cta, so none finds another tile's.)
   __device__ __forceinline__ void queries(const AttendTile& it, int G) {
     constexpr int kUnits = C::RB / 64, kV = kBf16 ? 1 : 2, kSteps = C::NK / kUnits;  // kV: 16-byte loads a unit
 #pragma unroll
@@ -886,6 +886,7 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
       for (int k = 0; k < kWords; ++k) kept[k] = w[k];  // (every lane the same)
     }
     bool any = false;  // the item has a chunk that the tile sees
+    bool met = false;  // the warps have met since they wrote the queries
     int st = 0;
     for (int i = at.i; i < run; ++i) {
       // the pages S - 1 places on, into the stage that place i - 1 had (every lane has done with it)
@@ -922,6 +923,7 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
         if (any) {
           rows.partial(split, left);
           rows.open();
+          met = true;
         }
         any = false;
       }
@@ -934,7 +936,12 @@ __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8
       memcpy(&at, w, sizeof w);
     }
     if (!at.past(wk, run)) return;
-    __syncwarp();  // every lane is done with this tile's stages (and the CTA, by its last meeting, with the slots)
+    // Every lane is done with this tile's stages.  A run that held nothing the
+    // tile sees (the later chunks of an early tile, those before a late tile's
+    // window, rows of padding) had no meeting: without one a warp still at its
+    // queries would write them over the next tile's.
+    __syncwarp();
+    if (!met) named_sync(2, kAttendThreads);
   }
 }
 

@@ -770,3 +770,21 @@ def test_a_decode_loop_written_read_and_attended():
             o, _, tol, _ = ref.attend(pool, table_h.numpy(), where, f64(q), 0, 0, d ** -0.5)
             assert (np.abs(f64(out) - o) <= tol).all()
             length += keep
+
+
+@pytest.mark.parametrize("fmt,d", [("e4m3", 128), ("bf16", 64), ("bf16", 256)])
+@pytest.mark.parametrize("lens,firsts,window,sinks", [([300], [0], 0, 0), ([150, 150, 150], [500, 0, 700], 60, 2),
+                                                      ([140] * 6, [-100, -137, -90, -50, -120, -139], 0, 0)],
+                         ids=["prompt", "window", "padding"])
+def test_runs_of_ctas_that_begin_in_places_their_tile_does_not_see(fmt, d, lens, firsts, window, sinks):
+    """More chunks than there are CTAs, so that runs of work begin in the middle
+    of a tile's list: among chunks behind an early tile's rows, in front of a
+    late tile's window, or in a tile of padding alone.  The tiles that follow in
+    the same run keep their own queries, call after call."""
+    import torch
+    n_q, n_kv = (32, 8) if d < 256 else (16, 4)
+    c = Case(40, n_q, n_kv, d, lens, firsts, fmt)
+    q, out, lse = c.check_attend(window, sinks)
+    for _ in range(60):
+        o2, l2 = c.attend(q, window, sinks)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
