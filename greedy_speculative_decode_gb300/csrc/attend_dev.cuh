@@ -480,7 +480,9 @@ struct AttendRows {
 
   // An infinity or NaN of a bf16 page in a place that some row does not see
   // must not meet that row's weight of zero: it is taken out here and added to
-  // the rows that see it.  (a: columns g, g + 8 of unit u, positions 2 q4, 2 q4
+  // the rows that see it, whose accumulators it makes infinite or NaN.  On a
+  // page that all rows see the products do that; which of the two comes out
+  // is decided at the end (infinite_value).  (a: columns g, g + 8 of unit u, positions 2 q4, 2 q4
   // + 1 and 8 more of the page; the accumulators of these columns are held by
   // the same quad of lanes.)
   __device__ __forceinline__ void set_apart(int base, bool have, int u, uint32_t (&a)[4]) {
@@ -961,6 +963,34 @@ __global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) 
   attend_cta<C>(p, wk, smem);
 }
 
+// What column c of a row's output over a bf16 cache is when the products made
+// it an infinity or a NaN: hi x + lo x of an infinite x is a NaN where a
+// weight's second term is zero or negative, and so is an infinity rescaled by a
+// factor too small for fp32.  Weights are positive, so the sum of the row's
+// infinite values (a NaN, if there is one or if they have both signs) is the
+// row's output, whatever tile it was part of.  Returns 0 where the row sees
+// none (finite values whose sum is beyond fp32).  Splits with a finite partial
+// hold none.
+template <int D>
+__device__ __noinline__ float infinite_value(const AttendParams& p, const SplitRange& sr, size_t base, int seq, int t,
+                                             int kvh, int c) {
+  const int* table = p.rows.table + (size_t)seq * p.rows.table_stride;
+  const bf16* v = reinterpret_cast<const bf16*>(p.v);
+  float sum = 0.0f;
+  for (int j = 0; j < sr.n; ++j) {
+    const int s = sr.at(j), end = min(min(attend_split_start(s + 1), t + 1), p.rows.limit());
+    if (fabsf(__ldcg(p.part_o + (base + s) * D + c)) < INFINITY) continue;
+    for (int pos = attend_split_start(s); pos < end; ++pos) {
+      if (p.window > 0 && pos <= t - p.window && pos >= p.sinks) continue;
+      const int page = __ldg(table + pos / kPage);
+      if ((uint32_t)page >= (uint32_t)p.n_pages) continue;
+      const float x = __bfloat162float(v[(((size_t)page * p.n_kv_heads + kvh) * kPage + pos % kPage) * D + c]);
+      if (!(fabsf(x) < INFINITY)) sum = __fadd_rn(sum, x);
+    }
+  }
+  return sum;
+}
+
 // The splits of one (row, query head) merged: out = sum_s o_s 2^(m_s - M) /
 // sum_s l_s 2^(m_s - M), in a fixed order for the splits that the row sees,
 // whatever else is in the call: the j-th of them belongs to strand j mod 8, each
@@ -970,7 +1000,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) 
 // partials are requested side by side).  Else a warp does all of it.
 constexpr int kStrands = 8;
 template <int D, bool kWide>
-__global__ void __launch_bounds__(256) k_attend_merge(const AttendParams p) {
+__global__ void __launch_bounds__(256) k_attend_merge(const __grid_constant__ AttendParams p) {
   constexpr int V = D / 32, W = kStrands, B = 8;  // V: elements a lane, columns V * lane ..
   extern __shared__ float s_dyn[];                // factors [max_splits], denominators [max_splits / 32] of a unit
   __shared__ float s_red[W], s_o[kWide ? W : 1][D];
@@ -1033,6 +1063,7 @@ __global__ void __launch_bounds__(256) k_attend_merge(const AttendParams p) {
   for (int k = 0; k < (sr.n + 31) / 32; ++k) l = __fadd_rn(l, s_l[k]);
   const bool none = l == 0.0f;  // a row that sees nothing: zeros
   bf16* out = p.out + (int64_t)r * p.out_stride + hq * D;
+  float zero = 0.0f;  // a NaN when a sum is not finite
   if constexpr (kWide) {  // this warp's strand, eight of its splits at a time
     float acc[V];
 #pragma unroll
@@ -1057,6 +1088,7 @@ __global__ void __launch_bounds__(256) k_attend_merge(const AttendParams p) {
       float a = 0.0f;
 #pragma unroll
       for (int w = 0; w < W; ++w) a = __fadd_rn(a, s_o[w][c]);
+      zero = __fmaf_rn(a, 0.0f, zero);
       out[c] = __float2bfloat16_rn(none ? 0.0f : __fdiv_rn(a, l));
     }
   } else {  // all strands, one split of each at a time
@@ -1086,7 +1118,18 @@ __global__ void __launch_bounds__(256) k_attend_merge(const AttendParams p) {
         a = __fadd_rn(a, acc[w][e]);
         b = __fadd_rn(b, acc[w][e + 1]);
       }
+      zero = __fmaf_rn(a, 0.0f, __fmaf_rn(b, 0.0f, zero));
       *reinterpret_cast<uint32_t*>(out + lane * V + e) = none ? 0u : pack_bf16x2(__fdiv_rn(a, l), __fdiv_rn(b, l));
+    }
+  }
+  if (zero != 0.0f && l == l && p.k_exp == nullptr) {
+    const int kvh = hq / (p.n_q_heads / p.n_kv_heads);
+    asm volatile("" ::: "memory");  // (the thread's own stores above, of pairs)
+#pragma unroll 1
+    for (int c = kWide ? threadIdx.x : lane * V; c < (kWide ? D : (lane + 1) * V); c += kWide ? 256 : 1) {
+      if (fabsf(__bfloat162float(out[c])) < INFINITY) continue;
+      const float a = infinite_value<D>(p, sr, base, seq, t, kvh, c);
+      if (a != 0.0f) out[c] = __float2bfloat16_rn(a);
     }
   }
   if (p.lse && lane == 0 && (!kWide || warp == 0))

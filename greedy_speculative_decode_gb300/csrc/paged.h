@@ -50,6 +50,10 @@ __host__ __device__ inline int attend_split_of(int pos) {
   return pos < kAttendRegionA ? pos / kAttendSplitA
                               : kAttendRegionA / kAttendSplitA + (pos - kAttendRegionA) / kAttendSplitB;
 }
+__host__ __device__ inline int attend_split_start(int split) {
+  const int n = kAttendRegionA / kAttendSplitA;
+  return split < n ? split * kAttendSplitA : kAttendRegionA + (split - n) * kAttendSplitB;
+}
 // The merge keeps a factor for each split in shared memory: 160 KB hold those
 // of the 2^23 positions that a table may reach.
 constexpr int kMergeMaxSmem = 160 * 1024;

@@ -431,6 +431,8 @@ int sv_kv_fetch(const sv_kv_pool* pool, const sv_row_batch* rows, void* k_dev, i
  *   h / (n_q_heads / n_kv_heads) (n_q_heads a multiple of n_kv_heads);
  *   lse_dev: fp32 [n_rows, n_q_heads] or NULL.  A row that sees nothing gives
  *   zeros and -infinity.  What lies in places a row does not see has no effect on it.
+ * An infinity among the values of a bf16 cache that a row sees is the row's
+ * output in that column; a NaN, or infinities of both signs, make it NaN.
  * Softmax sums and accumulators are fp32.  Over an 8-bit cache a weight times
  * its value block's scale is rounded to f16 relative to the row's largest such
  * product (2^-11 of itself, at least 2^-25 of the largest).  A row's result depends on its own

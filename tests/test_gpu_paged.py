@@ -788,3 +788,30 @@ def test_runs_of_ctas_that_begin_in_places_their_tile_does_not_see(fmt, d, lens,
     for _ in range(60):
         o2, l2 = c.attend(q, window, sinks)
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 64), (4, 2, 128), (4, 1, 256)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_an_infinite_value_is_the_same_in_every_batch(n_q, n_kv, d, value):
+    """Position 5 lies in a page that the row at 20 sees whole, and that a tile
+    which begins at 2 does not.  Weights are like in size, so that the weighted
+    sum of an infinity is that infinity."""
+    import torch
+    sv = _sv()
+    c = Case(41, n_q, n_kv, d, [25, 3, 2], [2, 300, 1500], "bf16")
+    for s, p in ((0, 5), (1, 281), (2, 130), (2, 700), (2, 1100), (2, 1101), (2, 1490)):  # several splits of one run
+        c.cache.v[int(c.table_h[s, p // PAGE]), 0, p % PAGE, 7] = value
+    q = c.queries()
+    out, lse = c.attend(q, scale=0.02)
+    hit = out[:, :n_q // n_kv, 7]
+    assert torch.isfinite(hit[:3]).all()  # positions 2 .. 4
+    same = torch.isnan(hit[3:]) if value != value else hit[3:] == value
+    assert same.all()
+    rest = out.clone()
+    rest[3:, :n_q // n_kv, 7] = 0
+    assert torch.isfinite(rest).all()
+    for s, r, t in c.where:
+        o1, l1 = torch.empty_like(q[:1]), torch.empty((1, n_q), device="cuda")
+        rows = sv.RowBatch(c.table[s:s + 1], torch.tensor([t], dtype=torch.int32, device="cuda"), 1)
+        sv.attend(c.cache, rows, q[r:r + 1], o1, scale=0.02, lse=l1)
+        assert torch.equal(o1[0].view(torch.int16), out[r].view(torch.int16)) and torch.equal(l1[0], lse[r]), t
