@@ -18,6 +18,10 @@
 //     reference that weights are taken against moves only when a row's maximum
 //     has risen by more than 2^8 over it (weights reach 2^8, which f16 and fp32
 //     hold as exactly as those below one), so accumulators are seldom rescaled.
+//     A warp sums at most 64 positions of a split, four warps meet: bf16 values
+//     of up to 2^112 stay within fp32 whatever the weights.  (Weights taken
+//     times 2^-16 would keep all of them in range, but the tensor cores flush
+//     sums below 2^-126: values below 2^-108 would be lost instead.)
 //   O^T += V^T P^T, all columns.  A transposing load of bytes makes V's operand
 //     (four consecutive positions of a column in a word).
 // At the split's end the warps' results meet in shared memory and go out as its
@@ -482,7 +486,7 @@ struct AttendRows {
   // must not meet that row's weight of zero: it is taken out here and added to
   // the rows that see it, whose accumulators it makes infinite or NaN.  On a
   // page that all rows see the products do that; which of the two comes out
-  // is decided at the end (infinite_value).  (a: columns g, g + 8 of unit u, positions 2 q4, 2 q4
+  // is decided at the end (far_value).  (a: columns g, g + 8 of unit u, positions 2 q4, 2 q4
   // + 1 and 8 more of the page; the accumulators of these columns are held by
   // the same quad of lanes.)
   __device__ __forceinline__ void set_apart(int base, bool have, int u, uint32_t (&a)[4]) {
@@ -963,32 +967,37 @@ __global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) 
   attend_cta<C>(p, wk, smem);
 }
 
-// What column c of a row's output over a bf16 cache is when the products made
-// it an infinity or a NaN: hi x + lo x of an infinite x is a NaN where a
-// weight's second term is zero or negative, and so is an infinity rescaled by a
-// factor too small for fp32.  Weights are positive, so the sum of the row's
-// infinite values (a NaN, if there is one or if they have both signs) is the
-// row's output, whatever tile it was part of.  Returns 0 where the row sees
-// none (finite values whose sum is beyond fp32).  Splits with a finite partial
-// hold none.
+// Column c of a row's output over a bf16 cache where the sum of its splits came
+// out as an infinity or a NaN.
+//   The row sees an infinity: hi x + lo x is a NaN where a weight's second term
+// is zero or negative, and so is an infinity rescaled by a factor too small for
+// fp32.  Weights are positive, so the output is the sum of the row's infinite
+// values (a NaN, if there is one or if they have both signs), whatever tile the
+// row was part of.  Splits with a finite partial hold none.
+//   It sees none: finite partials have a sum beyond fp32.  It is taken again of
+// their 2^-24-fold (2^8 for a weight, 2^16 for the splits), and the mean is
+// finite.
+// M: the largest reference, l: the sum of the weights.
 template <int D>
-__device__ __noinline__ float infinite_value(const AttendParams& p, const SplitRange& sr, size_t base, int seq, int t,
-                                             int kvh, int c) {
+__device__ __noinline__ float far_value(const AttendParams& p, const SplitRange& sr, size_t base, int seq, int t, int kvh,
+                                        int c, float M, float l) {
   const int* table = p.rows.table + (size_t)seq * p.rows.table_stride;
   const bf16* v = reinterpret_cast<const bf16*>(p.v);
-  float sum = 0.0f;
+  float infinite = 0.0f, sum = 0.0f;
   for (int j = 0; j < sr.n; ++j) {
     const int s = sr.at(j), end = min(min(attend_split_start(s + 1), t + 1), p.rows.limit());
-    if (fabsf(__ldcg(p.part_o + (base + s) * D + c)) < INFINITY) continue;
+    const float o = __ldcg(p.part_o + (base + s) * D + c);
+    sum = __fmaf_rn(o, __fmul_rn(ex2(__fsub_rn(__ldcg(&p.part_ml[base + s].x), M)), 0x1p-24f), sum);
+    if (fabsf(o) < INFINITY) continue;
     for (int pos = attend_split_start(s); pos < end; ++pos) {
       if (p.window > 0 && pos <= t - p.window && pos >= p.sinks) continue;
       const int page = __ldg(table + pos / kPage);
       if ((uint32_t)page >= (uint32_t)p.n_pages) continue;
       const float x = __bfloat162float(v[(((size_t)page * p.n_kv_heads + kvh) * kPage + pos % kPage) * D + c]);
-      if (!(fabsf(x) < INFINITY)) sum = __fadd_rn(sum, x);
+      if (!(fabsf(x) < INFINITY)) infinite = __fadd_rn(infinite, x);
     }
   }
-  return sum;
+  return infinite != 0.0f ? infinite : __fdiv_rn(sum, __fmul_rn(l, 0x1p-24f));
 }
 
 // The splits of one (row, query head) merged: out = sum_s o_s 2^(m_s - M) /
@@ -1128,8 +1137,7 @@ __global__ void __launch_bounds__(256) k_attend_merge(const __grid_constant__ At
 #pragma unroll 1
     for (int c = kWide ? threadIdx.x : lane * V; c < (kWide ? D : (lane + 1) * V); c += kWide ? 256 : 1) {
       if (fabsf(__bfloat162float(out[c])) < INFINITY) continue;
-      const float a = infinite_value<D>(p, sr, base, seq, t, kvh, c);
-      if (a != 0.0f) out[c] = __float2bfloat16_rn(a);
+      out[c] = __float2bfloat16_rn(far_value<D>(p, sr, base, seq, t, kvh, c, M, l));
     }
   }
   if (p.lse && lane == 0 && (!kWide || warp == 0))

@@ -433,7 +433,9 @@ int sv_kv_fetch(const sv_kv_pool* pool, const sv_row_batch* rows, void* k_dev, i
  *   zeros and -infinity.  What lies in places a row does not see has no effect on it.
  * An infinity among the values of a bf16 cache that a row sees is the row's
  * output in that column; a NaN, or infinities of both signs, make it NaN.
- * Softmax sums and accumulators are fp32.  Over an 8-bit cache a weight times
+ * Softmax sums and accumulators are fp32.  Over a bf16 cache the sum of up to
+ * 256 positions is taken with weights of up to 2^8: values beyond 2^112 may
+ * come out as infinities.  Over an 8-bit cache a weight times
  * its value block's scale is rounded to f16 relative to the row's largest such
  * product (2^-11 of itself, at least 2^-25 of the largest).  A row's result depends on its own
  * query, position, window and cache alone, bit for bit: not on the other

@@ -815,3 +815,17 @@ def test_an_infinite_value_is_the_same_in_every_batch(n_q, n_kv, d, value):
         rows = sv.RowBatch(c.table[s:s + 1], torch.tensor([t], dtype=torch.int32, device="cuda"), 1)
         sv.attend(c.cache, rows, q[r:r + 1], o1, scale=0.02, lse=l1)
         assert torch.equal(o1[0].view(torch.int16), out[r].view(torch.int16)) and torch.equal(l1[0], lse[r]), t
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 9, 40])
+@pytest.mark.parametrize("size", [2.0 ** 117, 2.0 ** -100])
+def test_bf16_values_near_the_ends_of_their_range(d, rows, size):
+    """A mean of finite values is finite, where the sum of thousands of them is not."""
+    n_q = 32 if rows == 40 else 2  # (the merge's other form)
+    c = Case(42, n_q, 2, d, [rows, 1], [3500, 40], "bf16")
+    x = c.randn(c.cache.n_pages, 2, PAGE, d, spread=0.0).float().clamp(-3.9, 3.9)
+    c.cache.v.copy_((x.abs() * size).bfloat16())
+    c.check_attend(scale=1e-4)
+    c.cache.v.copy_((x * size).bfloat16())
+    c.check_attend(scale=1e-4)
