@@ -342,7 +342,9 @@ def kv_fetch(cache: PagedKv, rows: RowBatch, k_out, v_out, *, status=None, strea
 
 
 def attend_workspace(cache: PagedKv, rows: RowBatch, n_q_heads: int) -> int:
-    """sv_attend_workspace: bytes that attend needs besides its arguments."""
+    """sv_attend_workspace: bytes that attend needs besides its arguments. They grow
+    with the rows and with the width of the block table, to about 512 MB (4 GB
+    for the widest tables); calls of more rows run in blocks."""
     key = (n_q_heads, cache.head_dim)
     need = rows._workspace.get(key)
     if need is None:
@@ -411,7 +413,7 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
 
     args = (cache._p, rows._p, heads, qp, qs, op, os_, _ptr(lse), window, sinks, scale)
     if workspace is None:
-        with rows._lock:  # (the call is two launches: another thread's must not come between them)
+        with rows._lock:  # (the call is several launches: another thread's must not come between them)
             ws = _own_workspace(cache, rows, need, stream)
             _launch(cache, stream, _lib.sv_attend, *args, ws.data_ptr(), need, _ptr(status))
         return

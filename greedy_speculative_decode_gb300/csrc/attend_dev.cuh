@@ -109,7 +109,7 @@ struct AttendCfg {
   static constexpr int kOffQ = kOffScale + kRing * kScaleBytes;    // query fragments [N][NK][32 lanes][2 words]
   static constexpr int kQBytes = kQRegs ? 0 : N * NK * 256;
   static constexpr int kOffMl = kOffQ + kQBytes;                   // [QR][4 warps] (reference, sum)
-  static constexpr int kOffRow = kOffMl + QR * 32;                 // [QR] score factors, positions, places in the output
+  static constexpr int kOffRow = kOffMl + QR * 32;                 // [QR] score factors, positions, places among the partials
   static constexpr int kOffPlace = kOffRow + 3 * QR * 4;           // [4 warps] the CTA's place in its run
   static constexpr int kOffSeq = kOffPlace + kAttendWarps * 80;    // [n_seq + 1] chunks before, first, row start
   static constexpr int smem_bytes(int n_seq) { return 128 + kOffSeq + 4 * (3 * n_seq + 2); }
@@ -314,10 +314,12 @@ struct AttendPlace {
 template <class C>
 __device__ int attend_plan(const AttendParams& p, int G, int* before, int* first, int* start) {
   const int tid = threadIdx.x, S = p.rows.n_seq;
-  // (rows outside the call's buffers are left out)
-  for (int s = tid; s <= S; s += kAttendThreads)
-    start[s] = p.rows.row_start ? min(max(p.rows.row_start[s], 0), p.rows.n_rows) : s * p.rows.rows_each;
-  for (int s = tid; s < S; s += kAttendThreads) first[s] = first_of(p.rows, s);
+  // (rows outside this launch's are left out: a sequence cut by row_lo begins with the position of that row)
+  for (int s = tid; s <= S; s += kAttendThreads) {
+    const int at = p.rows.row_start ? p.rows.row_start[s] : s * p.rows.rows_each;
+    start[s] = min(max(at, p.row_lo), p.row_hi);
+    if (s < S) first[s] = (int)min((int64_t)first_of(p.rows, s) + max((int64_t)p.row_lo - at, (int64_t)0), (int64_t)1 << 30);
+  }
   __syncthreads();
   bool back = false;  // row starts that decrease: the counts below would not hold
   for (int s = tid; s < S; s += kAttendThreads) {
@@ -462,11 +464,11 @@ struct AttendRows {
             s_q[at * 32] = make_uint2(b0, b1);
           }
         }
-      // the rows' score factors, positions and places in the output (-1: no row)
+      // the rows' score factors, positions and places among the partials (-1: no row)
       if (q4 == 0) {
         s_fac()[n * 8 + g] = up;
         s_t()[n * 8 + g] = it.first + f / G;
-        s_slot()[n * 8 + g] = f < it.nf ? (it.row0 + f / G) * p.n_q_heads + it.kvh * G + f % G : -1;
+        s_slot()[n * 8 + g] = f < it.nf ? (it.row0 - p.row_lo + f / G) * p.n_q_heads + it.kvh * G + f % G : -1;
       }
     }
     __syncwarp();
@@ -1014,14 +1016,14 @@ __global__ void __launch_bounds__(256) k_attend_merge(const __grid_constant__ At
   extern __shared__ float s_dyn[];                // factors [max_splits], denominators [max_splits / 32] of a unit
   __shared__ float s_red[W], s_o[kWide ? W : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = kWide ? blockIdx.x : blockIdx.x * W + warp;  // row * n_q_heads + head
+  const int unit = kWide ? blockIdx.x : blockIdx.x * W + warp;  // (row - row_lo) * n_q_heads + head
   const int groups = (p.max_splits + 31) / 32;
   float* s_f = s_dyn + (kWide ? 0 : warp * groups * 33);
   float* s_l = s_f + groups * 32;
-  const int r = unit / p.n_q_heads, hq = unit % p.n_q_heads;
+  const int r = p.row_lo + unit / p.n_q_heads, hq = unit % p.n_q_heads;
   pdl_trigger();
   int seq, i, t = 0;
-  const bool row = r < p.rows.n_rows && find_row(p.rows, r, seq, i);
+  const bool row = r < p.row_hi && find_row(p.rows, r, seq, i);
   if (row) t = first_of(p.rows, seq) + i;
   const SplitRange sr = splits_seen(t, t, p.window, p.sinks, p.rows.limit());
   pdl_wait();
@@ -1141,7 +1143,7 @@ __global__ void __launch_bounds__(256) k_attend_merge(const __grid_constant__ At
     }
   }
   if (p.lse && lane == 0 && (!kWide || warp == 0))
-    p.lse[unit] = none ? -INFINITY : __fmul_rn(__fadd_rn(M, log2f(l)), 0.6931471805599453f);
+    p.lse[(size_t)r * p.n_q_heads + hq] = none ? -INFINITY : __fmul_rn(__fadd_rn(M, log2f(l)), 0.6931471805599453f);
   asm volatile("fence.proxy.async.global;" ::: "memory");  // a context reads it next by bulk copies
 }
 
@@ -1165,7 +1167,7 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   // a bound on the call's chunks (the lengths are known on the device only)
   const int G = p.n_q_heads / p.n_kv_heads;
-  const int64_t tiles = (int64_t)p.rows.n_rows * G / C::QR + p.rows.n_seq;
+  const int64_t n_rows = p.row_hi - p.row_lo, tiles = n_rows * G / C::QR + p.rows.n_seq;
   const int64_t items = tiles * p.n_kv_heads * (p.rows.limit() / C::kChunk + 1);
   const int64_t grid = std::min<int64_t>(items, (int64_t)num_sms * per_sm);
   cudaLaunchConfig_t cfg = {};
@@ -1180,7 +1182,7 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   cfg.numAttrs = pdl ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, k_attend<D, FMT, N>, p);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)p.rows.n_rows * p.n_q_heads;
+  const int64_t units = n_rows * p.n_q_heads;
   const size_t words = (size_t)((p.max_splits + 31) / 32) * 33;
   cfg.blockDim = dim3(256);
   cfg.numAttrs = 1;  // the merge may be resident before the partials are complete: it waits for them

@@ -65,11 +65,12 @@ struct AttendParams {
   int64_t q_stride, out_stride;
   float* lse;  // [n_rows, n_q_heads] natural-log sum of exponentials, or null
   const uint8_t *k, *v, *k_exp, *v_exp;
+  int row_lo, row_hi;  // the batch's rows that this launch takes (partials count from row_lo)
   int n_q_heads, n_kv_heads, n_pages, block, window, sinks;
   float scale_log2;  // softmax scale * log2(e)
   int max_splits;
-  float2* part_ml;  // [n_rows, n_q_heads, max_splits] (running max in log2 units, sum)
-  float* part_o;    // [n_rows, n_q_heads, max_splits, head_dim]
+  float2* part_ml;  // [row_hi - row_lo, n_q_heads, max_splits] (running max in log2 units, sum)
+  float* part_o;    // [row_hi - row_lo, n_q_heads, max_splits, head_dim]
   int* status;      // or null
   // Whether first, the tables and what the cache holds below first were there
   // before the kernel ahead of this one began (a context's steps): they are then

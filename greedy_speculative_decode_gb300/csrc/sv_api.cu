@@ -384,6 +384,7 @@ AttendParams attend_params(sv_ctx* ctx, int l, int M, int mode, bool pdl) {
   const KvPool k = kv_pool(ctx, l);
   AttendParams p = {};
   p.rows = step_rows(ctx, M, mode);
+  p.row_hi = M;
   p.q = ctx->q;
   p.out = ctx->o;
   p.q_stride = p.out_stride = c.n_q_heads * c.head_dim;

@@ -444,7 +444,11 @@ int sv_kv_fetch(const sv_kv_pool* pool, const sv_row_batch* rows, void* k_dev, i
  *   workspace_dev: sv_attend_workspace bytes (256-byte aligned) that the call
  *   may overwrite; calls that may run at the same time (other streams,
  *   captured graphs replayed beside one another), or that two threads issue
- *   on one stream, need one each. */
+ *   on one stream, need one each.  It holds n_q_heads * (4 head_dim + 8) bytes
+ *   for every row and every 256 positions that the block table reaches (128 of
+ *   the first 1024).  Calls that would need more than 512 MB run in blocks of
+ *   rows, one behind the other, and need that much (64 rows are kept together
+ *   as far as 4 GB: decode with a table cut for the longest context). */
 int sv_attend_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, int64_t* bytes);
 int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, const void* q_dev, int64_t q_stride,
               void* out_dev, int64_t out_stride, float* lse_dev, int window, int sinks, float scale,

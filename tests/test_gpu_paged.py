@@ -829,3 +829,75 @@ def test_bf16_values_near_the_ends_of_their_range(d, rows, size):
     c.check_attend(scale=1e-4)
     c.cache.v.copy_((x * size).bfloat16())
     c.check_attend(scale=1e-4)
+
+
+def _pieces(c, q, lens, firsts, window, sinks, k_rows):
+    """Every sequence by itself, k_rows rows a call, on a table cut to what they need."""
+    import torch
+    sv = _sv()
+    out, lse = torch.zeros_like(q), torch.zeros((q.shape[0], q.shape[1]), device="cuda")
+    at = 0
+    for s, (n, f) in enumerate(zip(lens, firsts)):
+        for i in range(0, n, k_rows):
+            m = min(k_rows, n - i)
+            pages = max(1, (f + i + m + PAGE - 1) // PAGE)
+            first = torch.tensor([f + i], dtype=torch.int32, device="cuda")
+            rows = sv.RowBatch(c.table[s:s + 1, :pages].contiguous(), first, m)
+            sl = slice(at + i, at + i + m)
+            o, l = torch.empty_like(q[sl]), torch.empty_like(lse[sl])
+            sv.attend(c.cache, rows, q[sl], o, window=window, sinks=sinks, lse=l)
+            out[sl], lse[sl] = o, l
+        at += n
+    return out, lse
+
+
+@pytest.mark.parametrize("fmt,window,sinks", [("e4m3", 0, 0), ("bf16", 70, 3)])
+def test_calls_of_many_rows_are_taken_in_blocks(fmt, window, sinks):
+    """A table for 65536 positions: 300 rows of 32 heads would have 1.3 GB of
+    partials.  The blocks' borders fall inside sequences; nothing behind the
+    workspace is written; captured and replayed the same."""
+    import torch
+    sv = _sv()
+    lens, firsts = [90, 0, 1, 100, 3, 104], [200, 9, 700, -20, 31, 0]
+    c = Case(43, 32, 2, 128, lens, firsts, fmt, back=2)
+    table = torch.full((len(lens), 4096), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    rows = sv.RowBatch(table, c.first, c.n_rows, row_start=c.row_start)
+    q = c.queries()
+    need = sv.attend_workspace(c.cache, rows, 32)
+    assert need <= 512 << 20
+    ws = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((c.n_rows, 32), 7.0, device="cuda")
+    kw = dict(window=window, sinks=sinks, lse=lse, status=st)
+    sv.attend(c.cache, rows, q, out, workspace=ws[:need], **kw)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and (ws[need:] == 0x5a).all()
+    n = sum(lens)
+    assert (out[n:] == 7).all() and (lse[n:] == 7).all()
+    want, want_l = _pieces(c, q, lens, firsts, window, sinks, 16)
+    assert torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], want_l[:n])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.attend(c.cache, rows, q, out, **kw)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[:n], want[:n])
+    # in the place of the queries
+    sv.attend(c.cache, rows, q, q, **kw)
+    assert torch.equal(q[:n], want[:n])
+
+
+@pytest.mark.parametrize("ragged", [True, False])
+def test_long_prompts_in_blocks(ragged):
+    """2000 rows of two sequences, three blocks, against calls of 64 rows."""
+    import torch
+    sv = _sv()
+    lens, firsts = [1000, 1000], [0, 37]
+    c = Case(44, 32, 8, 128, lens, firsts, "e4m3", pages=1100, ragged=ragged)
+    assert sv.attend_workspace(c.cache, c.rows, 32) <= 512 << 20
+    q = c.queries()
+    out, lse = c.attend(q)
+    want, want_l = _pieces(c, q, lens, firsts, 0, 0, 64)
+    assert torch.equal(out, want) and torch.equal(lse, want_l)

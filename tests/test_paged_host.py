@@ -103,3 +103,33 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
 def test_a_context_refuses_numbers_beyond_the_library_integers(kw):
     with pytest.raises(ValueError, match="at most"):
         sv.Context(None, {}, max_k=4, max_seq=64, **kw)
+
+
+def test_the_workspace_does_not_grow_without_bound():
+    """Long prompts: at most 512 MB; wide tables: what 64 rows need, at most 4 GB
+    (or what one row does)."""
+    n = ctypes.c_int64()
+
+    def need(heads, head_dim, **kw):
+        p, r = pool(head_dim=head_dim), rows(**kw)
+        assert sv.lib().sv_attend_workspace(ctypes.byref(p), ctypes.byref(r), heads, ctypes.byref(n)) == 0
+        return n.value
+
+    def row(heads, head_dim, positions):  # one row's partials
+        splits = min(positions, 1024) // 128 + max(0, positions - 1024) // 256
+        return heads * splits * (4 * head_dim + 8)
+
+    # small calls take what they always did
+    assert need(32, 128, n_seq=32, n_rows=32, table_stride=512) == 32 * row(32, 128, 8192)
+    assert need(32, 128, n_seq=32, n_rows=32, table_stride=1 << 16) == 32 * row(32, 128, 1 << 20)
+    for d, stride, n_rows in ((128, 512, 8192), (128, 2048, 32768), (64, 64, 1 << 22), (256, 1 << 14, 4096), (128, 1 << 19, 77)):
+        one = row(32, d, stride * 16)
+        got = need(32, d, n_seq=1, n_rows=n_rows, table_stride=stride)
+        assert one <= got <= max(512 << 20, min(64 * one, 4 << 30)) + 256, (d, stride, n_rows)
+
+
+def test_more_query_rows_than_a_word_counts_are_refused():
+    n = ctypes.c_int64()
+    p, r = pool(), rows(n_seq=1, n_rows=1 << 28)
+    assert sv.lib().sv_attend_workspace(ctypes.byref(p), ctypes.byref(r), 1 << 30, ctypes.byref(n)) == INVAL
+    assert attend(p, r, heads=32, qs=4096, os=4096) == INVAL
