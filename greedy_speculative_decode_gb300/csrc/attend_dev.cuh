@@ -1152,10 +1152,14 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
                             cudaStream_t s, bool pdl) {
   using C = AttendCfg<D, FMT, N>;
   const int smem = C::smem_bytes(p.rows.n_seq);
-  // CTAs per SM at this much shared memory: asked once for each size
-  static std::atomic<int64_t> known{0};
+  // CTAs per SM at this much shared memory: asked once for each device and size
+  static std::atomic<int64_t> of_device[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::atomic<int64_t>& known = of_device[dev];
   int64_t k = known.load(std::memory_order_relaxed);
-  cudaError_t e = cudaSuccess;
   if ((int)(k >> 8) != smem) {
     int n = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attend<D, FMT, N>, kAttendThreads, smem);

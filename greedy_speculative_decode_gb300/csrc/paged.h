@@ -39,6 +39,8 @@ cudaError_t launch_kv_write(const KvPool& c, const RowBatch& b, const KvSource& 
 cudaError_t launch_kv_fetch(const KvPool& c, const RowBatch& b, bf16* k, int64_t k_stride, bf16* v,
                             int64_t v_stride, int* status, cudaStream_t s);
 
+constexpr int kMaxDevices = 64;  // that the attention keeps settings of
+
 // Most sequences of an attention call: each CTA keeps three words per
 // sequence in shared memory.
 constexpr int kAttendMaxSeq = 1024;

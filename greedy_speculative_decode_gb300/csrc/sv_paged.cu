@@ -32,8 +32,6 @@ cudaError_t launch_attend(const AttendParams& p, int fmt, int head_dim, int num_
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 // Per-device set-up of the attention kernels, and the device's SM count.
 struct DeviceSetup {
   int num_sms = 0;
