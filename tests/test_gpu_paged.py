@@ -901,3 +901,32 @@ def test_long_prompts_in_blocks(ragged):
     out, lse = c.attend(q)
     want, want_l = _pieces(c, q, lens, firsts, 0, 0, 64)
     assert torch.equal(out, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("n_q,n_kv,d", [(4, 1, 64), (8, 2, 128), (4, 1, 256)])
+def test_attend_where_the_splits_get_longer(fmt, block, n_q, n_kv, d):
+    """Rows, window edges and sinks on both sides of position 1024, one by one."""
+    for first, lens in ((1020, 9), (1023, 1), (1024, 1), (1278, 4)):
+        c = Case(45, n_q, n_kv, d, [lens, 2], [first, 1022], fmt, block)
+        c.check_attend()
+        for window, sinks in ((1, 0), (2, 1024), (3, 1025), (257, 1023), (900, 2)):
+            c.check_attend(window, sinks)
+    for t in (1030, 1500):  # windows that begin at 1022 .. 1026
+        c = Case(46, n_q, n_kv, d, [1, 1, 1], [t, t + 1, t - 1], fmt, block)
+        for lo in (1022, 1023, 1024, 1025, 1026):
+            c.check_attend(t - lo + 1, 3)
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 4), (300, 200)])
+def test_attend_more_chunks_than_ctas(fmt, block, window, sinks):
+    """CTAs begin in the middle of a tile's list and go on into other tiles, kv
+    heads and sequences, empty ones among them."""
+    c = Case(47, 32, 16, 64, [70, 0, 33, 1, 0, 90, 41], [300, 5, 0, 1100, 77, 150, -30], fmt, block, back=3)
+    q, out, lse = c.check_attend(window, sinks)
+    import torch
+    for _ in range(20):
+        o2, l2 = c.attend(q, window, sinks)
+        n = c.start[-1]
+        assert torch.equal(out[:n], o2[:n]) and torch.equal(lse[:n], l2[:n])
