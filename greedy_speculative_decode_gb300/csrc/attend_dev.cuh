@@ -318,7 +318,8 @@ __device__ int attend_plan(const AttendParams& p, int G, int* before, int* first
   for (int s = tid; s <= S; s += kAttendThreads) {
     const int at = p.rows.row_start ? p.rows.row_start[s] : s * p.rows.rows_each;
     start[s] = min(max(at, p.row_lo), p.row_hi);
-    if (s < S) first[s] = (int)min((int64_t)first_of(p.rows, s) + max((int64_t)p.row_lo - at, (int64_t)0), (int64_t)1 << 30);
+    if (s < S)  // (2^30 and up to 2^28 rows; more is a row start below zero)
+      first[s] = first_of(p.rows, s) + (int)min(max((int64_t)p.row_lo - at, (int64_t)0), (int64_t)1 << 28);
   }
   __syncthreads();
   bool back = false;  // row starts that decrease: the counts below would not hold

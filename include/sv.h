@@ -380,7 +380,8 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  * The rows of a call: sequence s brings rows row_start[s] .. row_start[s+1] - 1
  * (device int32 [n_seq + 1], not decreasing (sv_attend raises status bit 2 and
  * leaves the outputs undefined where it does); NULL: n_rows / n_seq rows each),
- * which stand at positions first[s], first[s] + 1, ... (device int32 [n_seq]).
+ * which stand at positions first[s], first[s] + 1, ... (device int32 [n_seq],
+ * read as within -2^30 .. 2^30).
  * Position p lies in page block_table[s * table_stride + p / 16] at slot p % 16
  * (device int32 [n_seq, table_stride], at most 2^23 positions).  n_rows: rows
  * of the buffers (at most 2^28); those behind the last sequence's are not

@@ -889,6 +889,29 @@ def test_calls_of_many_rows_are_taken_in_blocks(fmt, window, sinks):
     assert torch.equal(q[:n], want[:n])
 
 
+def test_blocks_of_rows_far_beyond_the_table():
+    """Rows at 2^30 and more, whose windows reach back to positions that differ
+    from row to row: the blocks' border elsewhere."""
+    import torch
+    sv = _sv()
+    c = Case(48, 32, 1, 128, [300], [0], "e4m3")
+    table = torch.full((1, 4096), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    far = torch.tensor([1 << 30], dtype=torch.int32, device="cuda")
+    q = c.queries()
+    window = (1 << 30) + 40  # row i sees the positions above i - 40
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    sv.attend(c.cache, sv.RowBatch(table, far, 300), q, out, window=window, status=st)
+    assert int(st.item()) == 2  # the table does not reach them
+    # (a sequence begins at 2^30 at most, so fewer rows instead of later ones)
+    some = sv.RowBatch(table, far, 124)
+    assert sv.attend_workspace(c.cache, some, 32) > sv.attend_workspace(c.cache, sv.RowBatch(table, far, 300), 32)
+    o = torch.empty_like(q[:124])
+    sv.attend(c.cache, some, q[:124], o, window=window)
+    assert torch.equal(o, out[:124])
+
+
 @pytest.mark.parametrize("ragged", [True, False])
 def test_long_prompts_in_blocks(ragged):
     """2000 rows of two sequences, three blocks, against calls of 64 rows."""
