@@ -60,7 +60,7 @@ bool read_pool(const sv_kv_pool* a, KvPool& c) {
   if (!a || (a->format != SV_KV_BF16 && a->format != SV_KV_E4M3)) return false;
   if (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256) return false;
   if (a->n_pages < 1 || a->n_kv_heads < 1 || bad16(a->k) || bad16(a->v)) return false;
-  // the kernels' 32-bit coordinates count positions of a head, or 128-byte rows
+  // the interface's limit: positions of all heads count in 32 bits
   if ((int64_t)a->n_pages * a->n_kv_heads * kPage >= INT32_MAX) return false;
   c = {};
   c.fmt = a->format;

@@ -105,7 +105,9 @@ typedef struct {
    * keeps every position).
    *   Either runs the attention of sv_attend below, with the same batch
    * invariance: a verify row is bit-identical to single-token decode, and
-   * results do not depend on how the cache was built. */
+   * results do not depend on how the cache was built.  The context holds that
+   * attention's workspace for 128 rows over max_seq, whatever the window (281
+   * MB for 32768 positions and 32 query heads of 128). */
   int32_t kv_format, window, sinks;
 } sv_config;
 
@@ -354,7 +356,8 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  * above run the same kernels on their own pools (sv_config.kv_format, window).
  *
  * A pool holds codes k, v [n_pages, n_kv_heads, 16, head_dim], device memory
- * aligned to 16 bytes.  head_dim is 64, 128 or 256.  format:
+ * aligned to 16 bytes.  head_dim is 64, 128 or 256; n_pages * n_kv_heads * 16
+ * is below 2^31 - 1.  format:
  *   SV_KV_BF16  the codes are the bf16 values (k_exp, v_exp, scale_block unused);
  *   SV_KV_E4M3  8 bits: e4m3 codes, and for each kv head and block of
  *     scale_block = 1 or 16 positions one e8m0 exponent byte b, the value
@@ -372,9 +375,10 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  *     keeps the page's exponent or raises it; when it rises the page's
  *     earlier codes are rounded again.  A page whose first position is
  *     written starts anew.
- * The NaN codes 0x7f, 0xff and the exponent bytes 248 to 254 are not written;
- * where a caller's own pool holds them at positions a row sees, that row's
- * result is not defined (NaN or a number), other rows' are not affected.
+ * The NaN codes 0x7f, 0xff, the exponent bytes 248 to 254, and 0 to 26 beside
+ * codes that are not zero, are not written; where a caller's own pool holds them
+ * at positions a row sees, that row's result is not defined (NaN or a number),
+ * other rows' are not affected.
  * Zeroed exponents and codes are zeros, as written zeros are.
  *
  * The rows of a call: sequence s brings rows row_start[s] .. row_start[s+1] - 1
