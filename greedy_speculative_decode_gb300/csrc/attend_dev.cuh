@@ -29,10 +29,10 @@
 //
 // What bounds it (32 query over 8 kv heads of 128, 8 bits; the call with its
 // merge): single-token decode of 32 sequences up to 8192 long 84 us, the
-// cache's 432 MB read at 5.7 TB/s; more query rows are bound by the
-// instructions around the products and the latency between them (half an
-// instruction a cycle and scheduler): 4 rows at 32768 31 us, 16 sequences of 4
-// rows in windows of 4096 45 us, a block of 128 rows at 4096 73 us.
+// cache's 432 MB read at 5.6 TB/s; more query rows are bound by the
+// instructions around the products and the latency between them (0.45
+// instructions a cycle and scheduler): 4 rows at 32768 29 us, 16 sequences of 4
+// rows in windows of 4096 45 us, a block of 128 rows at 4096 74 us.
 //
 // An 8-bit cache's exponents cost an addition each.  The key's scales its
 // score; the value's, ev, is added to the score in log2 units, t' = log2(e) s +
@@ -1193,7 +1193,8 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   cfg.numAttrs = 1;  // the merge may be resident before the partials are complete: it waits for them
   // A warp for each result where there are enough of them to fill the device, or
   // few splits to be had in parallel.  (128 rows of 32 heads over 4k: the call
-  // 77 us with a warp each, 89 with a block each; 32 rows over 8k 83.5 and 84.3.)
+  // 73.6 us with a warp each, 84.7 with a block each; 8 x 16 rows 39.3 and 44.5,
+  // 16 x 4 in windows of 4096 44.7 and 49.0, 32 rows over 8k 83.6 and 83.2.)
   if ((units >= 4 * num_sms || p.max_splits <= 8) && words * 4 * kStrands <= kMergeMaxSmem) {
     cfg.gridDim = dim3((unsigned)((units + kStrands - 1) / kStrands));
     cfg.dynamicSmemBytes = words * 4 * kStrands;
@@ -1206,8 +1207,8 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
 
 // Query tiles of 8 rows where they hold a sequence's rows, else of 16.  (Tiles
 // of 32 read and widened a page half as often, but at 128 accumulators a lane
-// eight warps an SM were too few: 8 x 16 rows at 4k took 46 us, with tiles of
-// 16 and twelve warps 38; a prefill block of 128 rows 74 and 70.)  A row's
+// eight warps an SM were too few: 8 x 16 rows at 4k took 49 us, with tiles of
+// 16 and twelve warps 39; a prefill block of 128 rows 78 and 74.)  A row's
 // result is the same in either (the columns of an mma do not meet).
 template <int D, int FMT>
 cudaError_t attend_launch(const AttendParams& p, int num_sms, cudaStream_t s, bool pdl) {
