@@ -992,12 +992,19 @@ __device__ __noinline__ float far_value(const AttendParams& p, const SplitRange&
     const float o = __ldcg(p.part_o + (base + s) * D + c);
     sum = __fmaf_rn(o, __fmul_rn(ex2(__fsub_rn(__ldcg(&p.part_ml[base + s].x), M)), 0x1p-24f), sum);
     if (fabsf(o) < INFINITY) continue;
-    for (int pos = attend_split_start(s); pos < end; ++pos) {
-      if (p.window > 0 && pos <= t - p.window && pos >= p.sinks) continue;
+    for (int pos = attend_split_start(s); pos < end; pos += 4) {
       const int page = __ldg(table + pos / kPage);
       if ((uint32_t)page >= (uint32_t)p.n_pages) continue;
-      const float x = __bfloat162float(v[(((size_t)page * p.n_kv_heads + kvh) * kPage + pos % kPage) * D + c]);
-      if (!(fabsf(x) < INFINITY)) infinite = __fadd_rn(infinite, x);
+      const bf16* column = v + (((size_t)page * p.n_kv_heads + kvh) * kPage + pos % kPage) * D + c;
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __bfloat162float(column[i * D]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool seen = pos + i < end && (p.window <= 0 || pos + i > t - p.window || pos + i < p.sinks);
+        if (seen && !(fabsf(x[i]) < INFINITY)) infinite = __fadd_rn(infinite, x[i]);
+      }
+      if (infinite != infinite) return infinite;
     }
   }
   return infinite != 0.0f ? infinite : __fdiv_rn(sum, __fmul_rn(l, 0x1p-24f));
