@@ -20,6 +20,10 @@ MAX_K = 32
 MAX_PREFILL_ROWS = 128
 SV_KV_BF16, SV_KV_E4M3 = 0, 1
 ATTEND_MAX_SEQ = 1024
+PAGES_MAX_SEQ = 1024
+LOGPROBS_MAX_TOP = 32
+SV_LOGITS_F32, SV_LOGITS_BF16 = 0, 1
+ST_BAD_PAGE, ST_BAD_TOKEN, ST_NO_PAGES = 2, 4, 16  # bits of an operator's status
 _INT_MAX = 2 ** 31 - 1
 _ERRNAMES = {SV_E_INVAL: "SV_E_INVAL", SV_E_NOMEM: "SV_E_NOMEM", SV_E_CUDA: "SV_E_CUDA",
              SV_E_STATE: "SV_E_STATE"}
@@ -52,6 +56,11 @@ class SvKvPool(ctypes.Structure):
 class SvRowBatch(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("n_seq", "n_rows", "max_rows", "table_stride")] + [
         (n, _P) for n in ("block_table", "first", "row_start")]
+
+
+class SvKvPages(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("n_seq", "table_stride", "n_pages")] + [
+        (n, _P) for n in ("block_table", "length", "held", "refs")]
 
 
 class SvError(RuntimeError):
@@ -88,13 +97,19 @@ def _load():
     L.sv_kv_write.argtypes = L.sv_kv_fetch.argtypes = [_P, _P, _P, i64, _P, i64, _P, _P]
     L.sv_attend_workspace.argtypes = [_P, _P, _i32, ctypes.POINTER(i64)]
     L.sv_attend.argtypes = [_P, _P, _i32, _P, i64, _P, i64, _P, _i32, _i32, ctypes.c_float, _P, i64, _P, _P]
+    L.sv_kv_fork_workspace.argtypes = [_P, ctypes.POINTER(i64)]
+    L.sv_kv_fork.argtypes = [_P, _P, _P, _P, _P, _P, _P, i64, _P, _P]
+    L.sv_kv_compact.argtypes = [_P, _P, _P, _i32, _P, _P, _P]
+    L.sv_kv_copy.argtypes = [_P, _P, _i32, _P, _i32, _P, _P]
+    L.sv_logprobs.argtypes = [_P, _i32, i64, _i32, _i32, ctypes.c_float, _P, _i32, _P, _P, _P, _i32, _P, _P, _P, _P]
     L.sv_last_error.argtypes = [_P]
     L.sv_last_error.restype = ctypes.c_char_p
     for name in ("sv_create", "sv_prefill", "sv_decode", "sv_verify", "sv_verify_async",
                  "sv_reserve", "sv_sync", "sv_truncate", "sv_seq_len", "sv_kv_read",
                  "sv_shuffle_pages", "sv_trace_hidden", "sv_step_kernel_count", "sv_time_linear",
                  "sv_lm_head_noalloc", "sv_prefill_blocks", "sv_kv_write", "sv_kv_fetch",
-                 "sv_attend_workspace", "sv_attend"):
+                 "sv_attend_workspace", "sv_attend", "sv_kv_fork_workspace", "sv_kv_fork", "sv_kv_compact",
+                 "sv_kv_copy", "sv_logprobs"):
         getattr(L, name).restype = _i32
     return L
 
@@ -214,7 +229,7 @@ class PagedKv:
             if t.data_ptr() % 16:
                 raise ValueError("the cache's tensors must be aligned to 16 bytes")
         import torch
-        self._bf16, self._torch = torch.bfloat16, torch._C  # (at hand: looked up on every call)
+        self._bf16, self._int32, self._torch = torch.bfloat16, torch.int32, torch._C  # (at hand: looked up on every call)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, d, k.device
         self._index = k.device.index
@@ -421,6 +436,236 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     if workspace.device != cache.device:
         raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
     _launch(cache, stream, _lib.sv_attend, *args, workspace.data_ptr(), workspace.numel(), _ptr(status))
+
+
+class KvPages:
+    """Which sequence holds which page of a cache (sv_kv_pages in include/sv.h).
+
+    block_table: int32 [n_seq, width], a row's pages, -1 behind them; length,
+    held: int32 [n_seq], a row's positions and the pages it holds; refs: int32
+    [n_pages], the rows that hold a page (and holds of the program's own). All
+    contiguous on one CUDA device, kept alive by this object; KvPages.empty
+    allocates them, all pages free. block_table and length serve as a
+    RowBatch's block_table and first."""
+
+    def __init__(self, block_table, length, held, refs):
+        if getattr(block_table, "dim", lambda: 0)() != 2 or min(block_table.shape) < 1:
+            raise ValueError("block_table: must be a 2-D tensor [n_seq, pages]")
+        if getattr(refs, "dim", lambda: 0)() != 1 or not 1 <= refs.shape[0] < 1 << 27:
+            raise ValueError("refs: must be a 1-D tensor [n_pages] of fewer than 2^27 pages")
+        n_seq, width = (int(x) for x in block_table.shape)
+        if n_seq > PAGES_MAX_SEQ or width > (1 << 23) // PAGE_SIZE:
+            raise ValueError(f"block_table: shape {tuple(block_table.shape)}, at most {PAGES_MAX_SEQ} sequences of "
+                             f"{(1 << 23) // PAGE_SIZE} pages")
+        _check_tensor(block_table, "block_table", "torch.int32", (n_seq, width))
+        _check_tensor(length, "length", "torch.int32", (n_seq,))
+        _check_tensor(held, "held", "torch.int32", (n_seq,))
+        _check_tensor(refs, "refs", "torch.int32", refs.shape)
+        if not block_table.device == length.device == held.device == refs.device:
+            raise ValueError("the tensors lie on different devices")
+        import torch
+        self._torch, self._int32 = torch._C, torch.int32
+        self.block_table, self.length, self.held, self.refs = block_table, length, held, refs
+        self.n_seq, self.width, self.n_pages, self.device = n_seq, width, int(refs.shape[0]), refs.device
+        self._index = refs.device.index
+        self._scratch = {}
+        self._lock = threading.Lock()
+        self._c = SvKvPages(n_seq, width, self.n_pages, _ptr(block_table), _ptr(length), _ptr(held), _ptr(refs))
+        self._p = ctypes.byref(self._c)
+        self._fork_bytes = 4 * (self.n_pages + n_seq * width)
+
+    @classmethod
+    def empty(cls, n_seq: int, width: int, n_pages: int, *, device="cuda"):
+        """n_seq rows without pages, all of n_pages pages free."""
+        import torch
+        return cls(torch.full((n_seq, width), -1, dtype=torch.int32, device=device),
+                   *(torch.zeros(n, dtype=torch.int32, device=device) for n in (n_seq, n_seq, n_pages)))
+
+
+def _check_pages_call(pages, out, moves, status):
+    if moves.dtype is not pages._int32 or moves.dim() != 2 or moves.shape[1] != 2 or moves.shape[0] < 1:
+        raise ValueError(f"moves: {moves.dtype} of shape {tuple(moves.shape)}, expected torch.int32 [n, 2]")
+    if moves.device != pages.device or not moves.is_contiguous() or moves.data_ptr() % 8:
+        raise ValueError("moves: must be contiguous on the tables' device, aligned to 8 bytes")
+    if out is not None:
+        if (out.n_seq, out.width, out.n_pages, out.device) != (pages.n_seq, pages.width, pages.n_pages, pages.device):
+            raise ValueError("out: must have the sizes and the device of pages")
+        if out is not pages:
+            mine = {pages._c.block_table, pages._c.length, pages._c.held, pages._c.refs}
+            if mine & {out._c.block_table, out._c.length, out._c.held, out._c.refs}:
+                raise ValueError("out: shares memory with pages")
+    if status is not None:
+        _check_tensor(status, "status", "torch.int32", (1,))
+        if status.device != pages.device:
+            raise ValueError(f"status: on {status.device}, the tables on {pages.device}")
+
+
+def kv_fork(pages: KvPages, moves, *, source=None, keep=None, room=None, out=None, workspace=None, status=None,
+            stream=None):
+    """sv_kv_fork: new rows from old ones, all at once. Row s becomes the first
+    min(keep[s], length[source[s]]) positions of what row source[s] was, with
+    pages for room[s] positions; source[s] = -1 frees it. source, keep, room:
+    int32 [n_seq] (None: itself, all, none beyond). Full pages are shared; a
+    last page in which another row's positions lie too is copied: moves (int32
+    [n_seq, 2]) says from where to where, for kv_copy. out: a KvPages of the
+    same sizes for the result, None: in place. All or nothing: status bit 16
+    (too few free pages) or 2 (a source or a row that cannot be). workspace:
+    uint8, 4 (n_pages + n_seq * width) bytes; None takes one of the object's
+    own, kept for each stream (in a capture, one of the graph's). Asynchronous."""
+    _check_pages_call(pages, out, moves, status)
+    n = pages.n_seq
+    if moves.shape[0] != n:
+        raise ValueError(f"moves: {moves.shape[0]} rows, expected {n}")
+    ptrs = []
+    for t, name in ((source, "source"), (keep, "keep"), (room, "room")):
+        if t is None:
+            ptrs.append(0)
+            continue
+        if t.dtype is not pages._int32 or t.shape != (n,) or t.device != pages.device or not t.is_contiguous():
+            raise ValueError(f"{name}: must be a contiguous torch.int32 tensor [{n}] on {pages.device}")
+        ptrs.append(t.data_ptr())
+    op = None if out is None else out._p
+    need = pages._fork_bytes
+    if workspace is None:
+        with pages._lock:
+            ws = _own_workspace(pages, pages, need, stream)
+            _launch(pages, stream, _lib.sv_kv_fork, pages._p, *ptrs, op, moves.data_ptr(), ws.data_ptr(), need, _ptr(status))
+        return
+    _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
+    if workspace.device != pages.device:
+        raise ValueError(f"workspace: on {workspace.device}, the tables on {pages.device}")
+    _launch(pages, stream, _lib.sv_kv_fork, pages._p, *ptrs, op, moves.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _ptr(status))
+
+
+def kv_compact(pages: KvPages, moves, *, where=None, out=None, status=None, stream=None):
+    """sv_kv_compact: the highest pages in use change to the lowest free numbers,
+    as many as moves (int32 [n, 2]) has room for; pass it to kv_copy. where:
+    int32 [n_pages], each page's number after the call (-1: free), or None. out:
+    a KvPages of the same sizes, None: in place. Asynchronous."""
+    _check_pages_call(pages, out, moves, status)
+    if where is not None:
+        _check_tensor(where, "where", "torch.int32", (pages.n_pages,))
+        if where.device != pages.device:
+            raise ValueError(f"where: on {where.device}, the tables on {pages.device}")
+    op = None if out is None else out._p
+    if where is not None:
+        _launch(pages, stream, _lib.sv_kv_compact, pages._p, op, moves.data_ptr(), moves.shape[0], where.data_ptr(),
+                _ptr(status))
+        return
+    with pages._lock:
+        ws = _own_workspace(pages, pages, pages._fork_bytes, stream)
+        _launch(pages, stream, _lib.sv_kv_compact, pages._p, op, moves.data_ptr(), moves.shape[0], ws.data_ptr(), _ptr(status))
+
+
+class KvLayers:
+    """The caches of a model's layers, for kv_copy: PagedKv of one format and shape."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        if not self.caches:
+            raise ValueError("no caches")
+        first = self.caches[0]
+        for c in self.caches:
+            if _kind(c) != _kind(first) or c.n_pages != first.n_pages:
+                raise ValueError("the caches differ in format, shape or device")
+        self.n_pages, self.device, self._index, self._torch = first.n_pages, first.device, first._index, first._torch
+        self._c = (SvKvPool * len(self.caches))(*(c._c for c in self.caches))
+        self._int32 = first._int32
+
+
+def _kind(c):
+    return c.format, c.n_kv_heads, c.head_dim, c.scale_block, c.device
+
+
+def kv_copy(cache, moves, *, into=None, status=None, stream=None):
+    """sv_kv_copy: pages moves[i, 0] of cache (a PagedKv, or KvLayers) to pages
+    moves[i, 1] of `into` (None: of the same). moves: int32 [n, 2]; (-1, -1) is
+    passed over. No page may be written by two moves, nor read by one and
+    written by another. Asynchronous."""
+    if isinstance(cache, PagedKv):
+        pools, n, kind = cache._p, 1, _kind(cache)
+    else:
+        pools, n, kind = cache._c, len(cache.caches), _kind(cache.caches[0])
+    to = None
+    if into is not None:
+        if isinstance(into, PagedKv):
+            to, n_to, kind_to = into._p, 1, _kind(into)
+        else:
+            to, n_to, kind_to = into._c, len(into.caches), _kind(into.caches[0])
+        if n_to != n or kind_to != kind:
+            raise ValueError("into: differs from cache in the number of layers, format, shape or device")
+    if moves.dtype is not cache._int32 or moves.dim() != 2 or moves.shape[1] != 2 or moves.shape[0] < 1:
+        raise ValueError(f"moves: {moves.dtype} of shape {tuple(moves.shape)}, expected torch.int32 [n, 2]")
+    if moves.device != cache.device or not moves.is_contiguous() or moves.data_ptr() % 8:
+        raise ValueError("moves: must be contiguous on the cache's device, aligned to 8 bytes")
+    if status is not None:
+        _check_tensor(status, "status", "torch.int32", (1,))
+        if status.device != cache.device:
+            raise ValueError(f"status: on {status.device}, the cache on {cache.device}")
+    _launch(cache, stream, _lib.sv_kv_copy, pools, to, n, moves.data_ptr(), moves.shape[0], _ptr(status))
+
+
+class _Device:  # what _launch needs of a device that no cache names
+    def __init__(self, device, torch):
+        self._index, self._torch = device.index, torch._C
+
+
+_devices = {}
+
+
+def logprobs(logits, tokens, out, *, scale: float = 1.0, lse=None, entropy=None, top_values=None, top_ids=None,
+             status=None, stream=None):
+    """sv_logprobs: log probabilities of given tokens, softmax over each row of
+    scale * logits (fp32 or bf16 [n_rows, vocab], rows may lie apart). tokens:
+    int32 [n_rows] or [n_rows, n], -1 for an unused place (0 comes out); out:
+    fp32 of the same shape. lse, entropy: fp32 [n_rows]; top_values (fp32),
+    top_ids (int32) [n_rows, k], k at most 32: the most probable tokens, ties
+    to the lowest id. Each of these or None. Asynchronous."""
+    import torch
+    if getattr(logits, "dim", lambda: 0)() != 2 or min(logits.shape) < 1:
+        raise ValueError("logits: must be a 2-D tensor [n_rows, vocab]")
+    n, vocab = logits.shape
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits: must be a CUDA tensor")
+    if logits.dtype is torch.float32:
+        kind = SV_LOGITS_F32
+    elif logits.dtype is torch.bfloat16:
+        kind = SV_LOGITS_BF16
+    else:
+        raise ValueError(f"logits: dtype {logits.dtype}, expected torch.float32 or torch.bfloat16")
+    row, one = logits.stride()
+    if (one != 1 and vocab > 1) or (row < vocab and n > 1):
+        raise ValueError(f"logits: strides {logits.stride()}, expected rows of consecutive elements")
+    if n == 1:  # a lone row's stride says nothing
+        row = vocab
+    if tokens.dtype is not torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != n:
+        raise ValueError(f"tokens: {tokens.dtype} of shape {tuple(tokens.shape)}, expected torch.int32 [{n}] or [{n}, k]")
+    n_tok = 1 if tokens.dim() == 1 else tokens.shape[1]
+    k = 0
+    for t, name in ((top_values, "top_values"), (top_ids, "top_ids")):
+        if t is None:
+            continue
+        if t.dim() != 2 or t.shape[0] != n or not 1 <= t.shape[1] <= LOGPROBS_MAX_TOP:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{n}, 1 .. {LOGPROBS_MAX_TOP}]")
+        if k and t.shape[1] != k:
+            raise ValueError("top_values and top_ids differ in shape")
+        k = t.shape[1]
+    for t, name, kind_of, shape in ((tokens, "tokens", torch.int32, tokens.shape), (out, "out", torch.float32, tokens.shape),
+                                    (lse, "lse", torch.float32, (n,)), (entropy, "entropy", torch.float32, (n,)),
+                                    (top_values, "top_values", torch.float32, (n, k)), (top_ids, "top_ids", torch.int32, (n, k)),
+                                    (status, "status", torch.int32, (1,))):
+        if t is None and name != "out":
+            continue
+        if t.dtype is not kind_of or t.shape != shape or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: must be a contiguous {kind_of} tensor {tuple(shape)} on {dev}, not {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    at = _devices.get(dev)
+    if at is None:
+        at = _devices[dev] = _Device(dev, torch)
+    _launch(at, stream, _lib.sv_logprobs, logits.data_ptr(), kind, row, n, vocab, scale, tokens.data_ptr(), n_tok,
+            out.data_ptr(), _ptr(lse), _ptr(entropy), k, _ptr(top_values), _ptr(top_ids), _ptr(status))
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):

@@ -87,7 +87,7 @@ enum StepMode : int { MODE_VERIFY = 0, MODE_PREFILL = 1, MODE_BODY = 2 };
 // the context is unusable after them.  ST_BAD_STATE is reported only in the
 // result of the step it concerns: tokens[0] of a verify step was not the
 // pending greedy token, so the step committed nothing.
-enum Status : int { ST_TIMEOUT = 1, ST_BAD_PAGE = 2, ST_BAD_TOKEN = 4, ST_BAD_STATE = 8 };
+enum Status : int { ST_TIMEOUT = 1, ST_BAD_PAGE = 2, ST_BAD_TOKEN = 4, ST_BAD_STATE = 8, ST_NO_PAGES = 16 };
 
 // Device-resident state of the sequence and of the current step.
 // cap_len and tokens are adjacent so the host sets both with one copy.

@@ -404,7 +404,8 @@ int sv_lm_head_noalloc(const void* x_dev, const void* gain_dev, const void* w_de
  * Conventions: device pointers of the current device; strides in elements,
  * multiples of 8, between rows whose heads lie side by side (rows of a fused
  * projection will do); row buffers 16-byte aligned.  status_dev: int32 the
- * kernels OR their failure bits into (1 timeout, 2 bad page), or NULL.
+ * kernels OR their failure bits into (1 timeout, 2 bad page; further ones where a
+ * call names them), or NULL.
  * cuda_stream: the stream to run on (NULL = legacy stream).  Asynchronous, no
  * allocation, no synchronisation: may be captured into a graph (the first
  * sv_attend of a process on a device sets kernel attributes).  Returns SV_OK,
@@ -458,6 +459,90 @@ int sv_attend_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, int n_
 int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, const void* q_dev, int64_t q_stride,
               void* out_dev, int64_t out_stride, float* lse_dev, int window, int sinks, float scale,
               void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/* ------------------------------------------------- pages of sequences, shared
+ * Who holds which page of a cache, on the device: pages handed out, shared
+ * between sequences, given back, packed and copied.  The same table and lengths
+ * serve as sv_row_batch's block_table and first.  With conventions as above
+ * (asynchronous, no allocation, may be captured into a graph).
+ *
+ * Row s of block_table (int32 [n_seq, table_stride]) holds the pages of a
+ * sequence, -1 behind them: held[s] pages for its length[s] positions (int32
+ * [n_seq]; pages may be held ahead of positions).  refs[page] (int32 [n_pages])
+ * counts the rows that hold a page; a program may count holds of its own there
+ * too.  A page with a count of zero is free.  n_seq is at most 1024, table_stride
+ * at most 2^19, n_pages below 2^27. */
+typedef struct {
+  int32_t n_seq, table_stride, n_pages;
+  int32_t *block_table, *length, *held, *refs;
+} sv_kv_pages;
+
+/* New rows from old ones, all at once: row s becomes the first
+ *   L = min(keep[s], length[source[s]])
+ * positions of what row source[s] was before the call, with pages for
+ * max(L, room[s]) positions.  source[s] = -1 leaves row s with nothing (its pages
+ * are given back).  source, keep, room: device int32 [n_seq]; NULL: itself, all,
+ * none beyond L.
+ *   Whole pages are shared and counted.  A last page that is not full is the
+ * row's own, so that it can be written: where others hold it too (another row, or
+ * a count of the program's) the row gets a copy of it; but where all hold it as
+ * such a page the lowest row goes on in it.  New pages are the lowest free ones,
+ * in the order of the rows and of their positions; pages that this call gives
+ * back are free to it.  Pages held ahead of L are given back.
+ *   moves_dev: int32 [n_seq, 2], (page, its copy) of each row, or (-1, -1): pass
+ * them to sv_kv_copy for every layer's pool before the rows are written.
+ *   out: where the new rows, lengths and counts go, of the same sizes as pages and
+ * with no memory of theirs; NULL (or the same arrays): in place.
+ * All or nothing: with too few free pages (status bit 16), a source outside -1 ..
+ * n_seq - 1 or a row of more pages than the table is wide (bit 2) the tables stay
+ * as they were and all moves are -1.  An entry that is no page of the pool is
+ * carried along and raises bit 2.
+ *   workspace_dev: sv_kv_fork_workspace bytes, 16-byte aligned, as for sv_attend. */
+int sv_kv_fork_workspace(const sv_kv_pages* pages, int64_t* bytes);
+int sv_kv_fork(const sv_kv_pages* pages, const int32_t* source, const int32_t* keep, const int32_t* room,
+               const sv_kv_pages* out, int32_t* moves_dev, void* workspace_dev, int64_t workspace_bytes,
+               int32_t* status_dev, void* cuda_stream);
+
+/* Pack the pages in use: while a page in use lies above a free one, the highest
+ * goes to the lowest.  With n_moves >= half the pages, those in use end up in 0 ..
+ * U - 1; with fewer, that many moves are made (the next call goes on).
+ *   moves_dev: int32 [n_moves, 2], (from, to), (-1, -1) behind the last: pass them
+ * to sv_kv_copy for every layer's pool.
+ *   where_dev: int32 [n_pages], the number that each page in use before the call has
+ * after it, -1 for a free one (for what a program keeps by page number).
+ *   out: as for sv_kv_fork. */
+int sv_kv_compact(const sv_kv_pages* pages, const sv_kv_pages* out, int32_t* moves_dev, int32_t n_moves,
+                  int32_t* where_dev, int32_t* status_dev, void* cuda_stream);
+
+/* Copy pages: K, V and exponents of page moves[i][0] of pool from[j] to page
+ * moves[i][1] of pool into[j], for n_pools pools (a model's layers; into NULL: the
+ * same pools).  All of one format and of one shape but for the number of pages,
+ * which is the same among from, and among into.  Moves of (-1, -1) are passed over,
+ * others that name no page of the pools too, raising status bit 2.  No page
+ * may be written by two moves, nor read by one and written by another. */
+int sv_kv_copy(const sv_kv_pool* from, const sv_kv_pool* into, int n_pools, const int32_t* moves_dev, int32_t n_moves,
+               int32_t* status_dev, void* cuda_stream);
+
+/* ---------------------------------------------------------- log probabilities
+ * Of rows of logits x (dtype SV_LOGITS_F32 or SV_LOGITS_BF16, [n_rows, vocab], rows
+ * `stride` elements apart, no alignment needed), with y = scale x, scale > 0:
+ *   lse[r] = ln sum_i exp(y_i)
+ *   out[r, t] = y[tokens[r, t]] - lse[r]   (tokens, out: [n_rows, n_tokens])
+ *   entropy[r] = -sum_i p_i ln p_i, p_i = exp(y_i - lse[r])
+ *   top_ids[r], top_values[r] ([n_rows, top]): the `top` (at most 32) most probable
+ *     tokens and their log probabilities, falling; ties to the lowest id.
+ * lse, entropy, top_values, top_ids: fp32 (ids int32) or NULL.  A logit of -infinity
+ * is a token of probability zero: log probability -infinity, never among the most
+ * probable (places left over: id -1, -infinity).  A row with a NaN or +infinity, or
+ * of -infinities alone, has no distribution: its results are NaN, its ids -1.  (So
+ * has one with a |scale x| beyond 2^127.)  A token of -1 gives 0 (an unused place),
+ * any other outside 0 .. vocab - 1 a NaN and status bit 4.  Sums are fp32.  A
+ * row's results do not depend on the other rows' values. */
+#define SV_LOGITS_F32 0
+#define SV_LOGITS_BF16 1
+int sv_logprobs(const void* logits_dev, int dtype, int64_t stride, int n_rows, int vocab, float scale,
+                const int32_t* tokens_dev, int n_tokens, float* out_dev, float* lse_dev, float* entropy_dev, int top,
+                float* top_values_dev, int32_t* top_ids_dev, int32_t* status_dev, void* cuda_stream);
 
 const char* sv_last_error(const sv_ctx* ctx);
 

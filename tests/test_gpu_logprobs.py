@@ -1,0 +1,222 @@
+"""logprobs against the 64-bit form of pages_ref.py.
+
+Tolerances.  With y = scale x (an fp32 constant scale log2(e), off by 2^-23 of
+itself: once rounded in scale, once in the product), z = y - m is one fused
+operation, off by 2^-23 |z| for the constant and half a step of the result, 2^-24
+|z|; the reference m by 2^-24 |m|, the same for a whole row, so that it cancels
+from every log probability but the lse itself.  2^z is off by 2^-22 and by ln2
+times z's error.  With w the weights, an error of e_i = 2^-22 + 2^-22 |z_i| of each
+gives
+  delta = sum w_i e_i / sum w_i = 2^-22 (1 + sum p |z|)
+of the sum, and adding n values along chains of at most c additions (a thread's
+share, then a tree) another c 2^-24, c = 8 ceil(vocab / 4096) + 64.  In log2 units
+log2 of the sum is off by 1.45 (delta + c 2^-24) and its own 2^-23 (|log2 l| + 1).  A log
+probability adds 2^-22 |y - m| + 2^-23 of itself; the entropy the error of sum p z:
+2 delta-like terms with |z|."""
+import numpy as np
+import pytest
+
+from . import pages_ref as ref
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def _sv():
+    import greedy_speculative_decode_gb300 as sv
+    return sv
+
+
+def tolerances(x, scale, tokens):
+    y = x * np.float64(np.float32(scale)) * np.log2(np.e)
+    n, vocab = x.shape
+    c = 8 * -(-vocab // 4096) + 64
+    tol_l, tol_e, tol_t = np.zeros(n), np.zeros(n), np.zeros(tokens.shape)
+    zs = []
+    with np.errstate(all="ignore"):
+        for r in range(n):
+            z = np.maximum(y[r] - y[r].max(), -1000)
+            w = np.exp2(z)
+            p = w / w.sum()
+            az = np.abs(z)
+            delta = 2.0 ** -22 * (1 + (p * az).sum()) + c * 2.0 ** -24
+            l2 = np.log2(w.sum())
+            err = 1.45 * delta + 2.0 ** -23 * (abs(l2) + 1)
+            tol_l[r] = err + 2.0 ** -22 * np.abs(y[r].max()) + 2.0 ** -23 * abs(y[r].max() + l2)
+            tol_e[r] = err + 2 * (p * az * (2.0 ** -22 * (2 + az))).sum() + 2 * c * 2.0 ** -24 * (p * az).sum() + delta * (p * az).sum()
+            zs.append((err, y[r].max()))
+            for i, t in enumerate(tokens[r]):
+                if 0 <= t < vocab and np.isfinite(y[r, t]):
+                    d = abs(y[r, t] - y[r].max())
+                    tol_t[r, i] = err + 2.0 ** -22 * d + 2.0 ** -22 * (d + abs(l2))
+    return tol_t, tol_l, tol_e, zs
+
+
+def run(x, tokens, scale=1.0, top=0, stream=None):
+    sv = _sv()
+    n = x.shape[0]
+    out = torch.full(tokens.shape, 7.0, device="cuda")
+    lse, ent = (torch.full((n,), 7.0, device="cuda") for _ in range(2))
+    tv = torch.full((n, top), 7.0, device="cuda") if top else None
+    ti = torch.full((n, top), 7, dtype=torch.int32, device="cuda") if top else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sv.logprobs(x, tokens, out, scale=scale, lse=lse, entropy=ent, top_values=tv, top_ids=ti, status=st, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse, ent, tv, ti, int(st.item())
+
+
+def check(x, tokens, scale=1.0, top=0):
+    out, lse, ent, tv, ti, st = run(x, tokens, scale, top)
+    xn, tn = x.double().cpu().numpy(), tokens.cpu().numpy()
+    if tn.ndim == 1:
+        tn = tn[:, None]
+    o, l, e, v, i = ref.logprobs(xn, tn, scale, top)
+    tt, tl, te, zs = tolerances(xn, scale, tn)
+
+    def near(got, want, tol):
+        got = got.double().cpu().numpy().reshape(want.shape)
+        fine = np.isfinite(want)
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert np.array_equal(got[~fine & ~np.isnan(want)], want[~fine & ~np.isnan(want)])
+        over = np.abs(got[fine] - want[fine]) - np.broadcast_to(tol, want.shape)[fine]
+        assert not over.size or over.max() <= 0, over.max()
+
+    near(out, o, tt)
+    near(lse, l, tl)
+    near(ent, e, te)
+    if top:
+        assert np.array_equal(ti.cpu().numpy(), i)
+        err = np.array([z[0] for z in zs])[:, None]
+        near(tv, v, err + 2.0 ** -21 * (np.abs(np.where(np.isfinite(v), v, 0)) * 1.45 + 1 + np.abs(np.where(np.isfinite(l), l, 0))[:, None]))
+    assert st == (4 if ((tn < -1) | (tn >= xn.shape[1])).any() else 0)
+
+
+def logits(seed, n, vocab, dtype, spread=3.0, stride=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    buf = torch.full((n, stride or vocab), 3.0e38, device="cuda").to(dtype)
+    x = buf[:, :vocab]
+    x.copy_((spread * torch.randn((n, vocab), generator=g, device="cuda")).bfloat16())  # (ties, as a model's bf16 logits have)
+    return x
+
+
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(1, 1), (3, 2), (1, 31), (5, 129), (2, 1024), (1, 4097), (3, 32003), (1, 151936),
+                                     (40, 9001), (2, 262144), (700, 513), (1, 600001)])
+def test_logprobs(dtype, n, vocab):
+    x = logits(n + vocab, n, vocab, dtype)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    tokens = torch.randint(0, vocab, (n, 3), generator=g, device="cuda", dtype=torch.int32)
+    for top in (0, 1, 20, 32):
+        check(x, tokens, top=top)
+    check(x, tokens[:, 0].contiguous(), scale=0.37, top=5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("stride,begin", [(1001, 0), (1007, 3), (1024, 1), (1000, 5)])
+def test_rows_of_any_alignment(dtype, stride, begin):
+    """Odd strides and beginnings: no row lies on a boundary, and what lies beside a row has no effect."""
+    n, vocab = 9, 997
+    buf = logits(3, n, stride, dtype)
+    buf[:, begin + vocab:] = 1.0e30
+    buf[:, :begin] = 1.0e30
+    x = buf.reshape(-1)[begin:].as_strided((n - 1, vocab), (stride, 1))
+    tokens = torch.arange(n - 1, dtype=torch.int32, device="cuda") * 100
+    if begin + vocab > stride:
+        buf.clamp_(max=9.0)
+    check(x, tokens, top=7)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+def test_rows_without_a_distribution_and_impossible_tokens(dtype):
+    vocab = 5000
+    x = logits(5, 9, vocab, dtype)
+    inf, nan = float("inf"), float("nan")
+    x[0] = -inf
+    x[1, 77] = inf
+    x[2, 4999] = nan
+    x[3, :] = -inf
+    x[3, 123] = -2.5  # certain
+    x[4, 5:] = -inf  # fewer possible tokens than alternatives
+    x[5, ::2] = -inf
+    x[6] = nan
+    x[7, :] = 0.0  # all alike: ties to the lowest id
+    tokens = torch.tensor([[0, -1], [77, 3], [1, 2], [123, 4], [4, 5], [1, 2], [0, 0], [4999, -1], [-2, vocab]],
+                          dtype=torch.int32, device="cuda")
+    for top in (1, 8, 32):
+        check(x, tokens, top=top)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["rising", "falling", "steps", "alike", "few", "last"])
+@pytest.mark.parametrize("n", [1, 400])
+def test_alternatives_of_rows_in_an_unkind_order(dtype, kind, n):
+    """Values in order (every chunk's largest above all before it), long runs of
+    equal ones, and all large ones in one chunk."""
+    vocab = 40001
+    i = torch.arange(vocab, device="cuda").float()
+    row = {"rising": i / 4096, "falling": -i / 4096, "steps": torch.floor(i / 1000) * 0.25, "alike": 0 * i + 1.5,
+           "few": torch.where(i % 997 == 5, 3.0, -1.0), "last": torch.where(i >= vocab - 64, 2.0 + (i % 7), 0.0)}[kind]
+    x = row.to(dtype).expand(n, vocab).contiguous()
+    if n > 1:
+        x[1:] = x[:1] + 0.0
+        x = x[:3] if vocab * n > 1 << 22 else x
+        x = x.repeat(140, 1)[:400]
+    tokens = torch.full((x.shape[0],), vocab - 1, dtype=torch.int32, device="cuda")
+    out, lse, ent, tv, ti, _ = run(x, tokens, top=32)
+    check(x[:1].contiguous(), tokens[:1], top=32)
+    one = run(x[:1].contiguous(), tokens[:1], top=32)
+    assert (ti == one[4]).all()  # ids do not depend on the rows beside (cut into more CTAs or fewer)
+
+
+def test_large_and_far_apart_logits():
+    x = torch.zeros((4, 3000), device="cuda")
+    x[0] = torch.linspace(-1.0e4, 1.0e4, 3000)
+    x[1, 5], x[1, 6] = 2.0 ** 100, -2.0 ** 100
+    x[2] = -3.0e4
+    x[3, 100] = 60.0
+    tokens = torch.tensor([2999, 5, 7, 100], dtype=torch.int32, device="cuda")
+    check(x, tokens, top=4)
+    check(x, tokens, scale=2.0, top=4)
+
+
+def test_the_same_bits_every_time_and_in_graphs_and_streams():
+    sv = _sv()
+    x = logits(9, 6, 151936, torch.bfloat16)
+    tokens = torch.randint(0, 151936, (6,), device="cuda", dtype=torch.int32)
+    a = run(x, tokens, top=20)
+    for _ in range(20):
+        b = run(x, tokens, top=20)
+        assert all(torch.equal(p, q) for p, q in zip(a[:5], b[:5]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b = run(x, tokens, top=20, stream=side)
+    assert all(torch.equal(p, q) for p, q in zip(a[:5], b[:5]))
+    out, ids = torch.empty(6, device="cuda"), torch.empty((6, 20), dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.logprobs(x, tokens, out, top_ids=ids)
+    x.copy_(logits(10, 6, 151936, torch.bfloat16))
+    g.replay()
+    torch.cuda.synchronize()
+    want = run(x, tokens, top=20)
+    assert torch.equal(out, want[0]) and torch.equal(ids, want[4])
+
+
+def test_a_steps_logits():
+    """The rows of a verify step: its logits in, the greedy token among the alternatives."""
+    import inputs
+    from . import gpu_helpers as gh
+    cfg = inputs.TINY
+    dw = inputs.device_weights(cfg, seed=0, gain_std=0.1)
+    ctx = gh.context(cfg, dw, max_k=8, max_seq=64)
+    pending = ctx.prefill(inputs.prefix_tokens(0, 20, cfg.vocab))
+    lg = gh.logits_buf(3, cfg.vocab)
+    toks = [pending, 5, 9]
+    _, corr = ctx.verify(toks, logits=lg)
+    tokens = torch.tensor([5, 9, -1], dtype=torch.int32, device="cuda")
+    check(lg, tokens, top=10)
+    _, _, _, _, ti, _ = run(lg, tokens, top=10)
+    assert torch.equal(ti[:, 0].long(), lg.argmax(1)) and corr in ti[:, 0].tolist()
