@@ -58,6 +58,10 @@ class SvRowBatch(ctypes.Structure):
         (n, _P) for n in ("block_table", "first", "row_start")]
 
 
+class SvSharedPrefix(ctypes.Structure):
+    _fields_ = [("n_groups", _i32), ("length", _P), ("group_start", _P)]
+
+
 class SvKvPages(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("n_seq", "table_stride", "n_pages")] + [
         (n, _P) for n in ("block_table", "length", "held", "refs")]
@@ -97,6 +101,8 @@ def _load():
     L.sv_kv_write.argtypes = L.sv_kv_fetch.argtypes = [_P, _P, _P, i64, _P, i64, _P, _P]
     L.sv_attend_workspace.argtypes = [_P, _P, _i32, ctypes.POINTER(i64)]
     L.sv_attend.argtypes = [_P, _P, _i32, _P, i64, _P, i64, _P, _i32, _i32, ctypes.c_float, _P, i64, _P, _P]
+    L.sv_attend_shared_workspace.argtypes = [_P, _P, _P, _i32, ctypes.POINTER(i64)]
+    L.sv_attend_shared.argtypes = [_P, _P, _P, _i32, _P, i64, _P, i64, _P, ctypes.c_float, _P, i64, _P, _P]
     L.sv_kv_fork_workspace.argtypes = [_P, ctypes.POINTER(i64)]
     L.sv_kv_fork.argtypes = [_P, _P, _P, _P, _P, _P, _P, i64, _P, _P]
     L.sv_kv_compact.argtypes = [_P, _P, _P, _i32, _P, _P, _P]
@@ -108,7 +114,8 @@ def _load():
                  "sv_reserve", "sv_sync", "sv_truncate", "sv_seq_len", "sv_kv_read",
                  "sv_shuffle_pages", "sv_trace_hidden", "sv_step_kernel_count", "sv_time_linear",
                  "sv_lm_head_noalloc", "sv_prefill_blocks", "sv_kv_write", "sv_kv_fetch",
-                 "sv_attend_workspace", "sv_attend", "sv_kv_fork_workspace", "sv_kv_fork", "sv_kv_compact",
+                 "sv_attend_workspace", "sv_attend", "sv_attend_shared_workspace",
+                 "sv_attend_shared", "sv_kv_fork_workspace", "sv_kv_fork", "sv_kv_compact",
                  "sv_kv_copy", "sv_logprobs"):
         getattr(L, name).restype = _i32
     return L
@@ -436,6 +443,85 @@ def attend(cache: PagedKv, rows: RowBatch, q, out, *, window: int = 0, sinks: in
     if workspace.device != cache.device:
         raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
     _launch(cache, stream, _lib.sv_attend, *args, workspace.data_ptr(), workspace.numel(), _ptr(status))
+
+
+class SharedPrefix:
+    """Groups of sequences whose first pages are the same (sv_shared_prefix in
+    include/sv.h). length: int32 [n_groups], the positions that each group
+    shares; group_start: int32 [n_groups + 1], group g being the sequences
+    group_start[g] .. group_start[g + 1] - 1, or None for groups of equal size
+    one behind the other. CUDA tensors, read when the kernels run."""
+
+    def __init__(self, length, group_start=None):
+        if getattr(length, "dim", lambda: 0)() != 1 or length.shape[0] < 1:
+            raise ValueError("length: must be a 1-D tensor [n_groups]")
+        n = int(length.shape[0])
+        _check_tensor(length, "length", "torch.int32", (n,))
+        _check_tensor(group_start, "group_start", "torch.int32", (n + 1,))
+        if group_start is not None and group_start.device != length.device:
+            raise ValueError("the prefix's tensors lie on different devices")
+        self.n_groups, self.device, self.uniform = n, length.device, group_start is None
+        self.tensors = (length, group_start)
+        self._c = SvSharedPrefix(n, _ptr(length), _ptr(group_start))
+        self._p = ctypes.byref(self._c)
+
+
+def _check_prefix(rows, prefix):
+    if prefix.device != rows.device:
+        raise ValueError(f"prefix: on {prefix.device}, the rows' tables on {rows.device}")
+    if prefix.n_groups > rows.n_seq or (prefix.uniform and rows.n_seq % prefix.n_groups):
+        raise ValueError(f"prefix: {prefix.n_groups} groups of {rows.n_seq} sequences")
+
+
+def attend_shared_workspace(cache: PagedKv, rows: RowBatch, prefix: SharedPrefix, n_q_heads: int) -> int:
+    """sv_attend_shared_workspace: bytes that attend_shared needs besides its arguments."""
+    key = (n_q_heads, cache.head_dim, prefix.n_groups)
+    need = rows._workspace.get(key)
+    if need is None:
+        _check_prefix(rows, prefix)
+        n = ctypes.c_int64(0)
+        rc = _lib.sv_attend_shared_workspace(cache._p, rows._p, prefix._p, int(n_q_heads), ctypes.byref(n))
+        if rc != SV_OK:
+            raise SvError(rc, f"attend_shared_workspace({n_q_heads} query heads)")
+        need = rows._workspace[key] = n.value
+    return need
+
+
+def attend_shared(cache: PagedKv, rows: RowBatch, prefix: SharedPrefix, q, out, *, scale=None, lse=None, workspace=None,
+                  status=None, stream=None):
+    """sv_attend_shared: the result of attend (without a window), reading what the
+    sequences of a group share once for all of the group's rows. The tables of
+    a group's sequences must agree on the pages of its first prefix.length
+    positions (as kv_fork leaves them). Arguments as attend's; workspace:
+    attend_shared_workspace bytes. Asynchronous."""
+    if getattr(q, "dim", lambda: 0)() != 3:
+        raise ValueError("q: must be a 3-D tensor [n_rows, n_q_heads, head_dim]")
+    heads = q.shape[1]
+    if heads < 1 or heads % cache.n_kv_heads:
+        raise ValueError(f"q: {heads} heads, not a multiple of the cache's {cache.n_kv_heads}")
+    qp, qs = _check_rows(q, "q", cache, rows.n_rows, heads)
+    op, os_ = _check_rows(out, "out", cache, rows.n_rows, heads)
+    _check_call(cache, rows, status)
+    _check_prefix(rows, prefix)
+    if rows.n_seq > ATTEND_MAX_SEQ:
+        raise ValueError(f"{rows.n_seq} sequences, at most {ATTEND_MAX_SEQ}")
+    if lse is not None:
+        _check_tensor(lse, "lse", "torch.float32", (rows.n_rows, heads))
+        if lse.device != cache.device:
+            raise ValueError(f"lse: on {lse.device}, the cache on {cache.device}")
+    need = attend_shared_workspace(cache, rows, prefix, heads)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    args = (cache._p, rows._p, prefix._p, heads, qp, qs, op, os_, _ptr(lse), scale)
+    if workspace is None:
+        with rows._lock:  # (the call is several launches: another thread's must not come between them)
+            ws = _own_workspace(cache, rows, need, stream)
+            _launch(cache, stream, _lib.sv_attend_shared, *args, ws.data_ptr(), need, _ptr(status))
+        return
+    _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
+    if workspace.device != cache.device:
+        raise ValueError(f"workspace: on {workspace.device}, the cache on {cache.device}")
+    _launch(cache, stream, _lib.sv_attend_shared, *args, workspace.data_ptr(), workspace.numel(), _ptr(status))
 
 
 class KvPages:

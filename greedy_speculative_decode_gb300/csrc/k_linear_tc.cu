@@ -26,6 +26,7 @@
 // (bounded) for its own copies and multiplies, and frees its tensor memory.
 #include "lin_dev.cuh"
 #include "linear_tc.h"
+#include "tc_dev.cuh"
 
 namespace sv {
 namespace {
@@ -44,57 +45,6 @@ struct TcGeom {
   static constexpr int kCR = MP <= 32 ? MP : 32;     // token rows per read-back / epilogue chunk
   static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 };
-
-// ---------------------------------------------------------------- tcgen05
-// Shared-memory operand descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (the TMA box layout); start address >> 4 in bits 0-13,
-// leading offset 1 (unused by swizzled K-major operands), stride 1024 >> 4 in
-// bits 32-45, descriptor version 1 at bit 46, layout 2 (128B swizzle) at 61.
-__device__ __forceinline__ uint64_t tc_sdesc(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-// Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, both
-// K-major; N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t tc_idesc(int M, int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum)
-      : "memory");
-}
-
-// Arrive once on `bar` when every tcgen05 operation this thread issued so far
-// has completed.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// Eight consecutive accumulator columns of the warp's 32 lanes.
-__device__ __forceinline__ void tc_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                 "=r"(r[7])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 // ---------------------------------------------------------------- layout
 struct TcSmem {

@@ -132,6 +132,57 @@ int block_rows(const RowBatch& b, int n_q_heads, int head_dim) {
   return (int)std::min(most, (each + 15) / 16 * 16);
 }
 
+// What both attention calls check and fill in: all but the window and the rows of a launch.
+int read_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, const void* q_dev, int64_t q_stride,
+                void* out_dev, int64_t out_stride, float* lse_dev, float scale, void* workspace_dev,
+                int64_t workspace_bytes, int32_t* status_dev, KvPool& c, AttendParams& p, int& each, int& num_sms) {
+  RowBatch b;
+  if (!read_pool(pool, c) || !read_rows(rows, b)) return SV_E_INVAL;
+  if (n_q_heads < 1 || n_q_heads % c.n_kv_heads || !std::isfinite(scale)) return SV_E_INVAL;
+  if (b.n_seq > kAttendMaxSeq) return SV_E_INVAL;
+  const int width = n_q_heads * c.head_dim;
+  if (bad16(q_dev) || bad16(out_dev) || bad_stride(q_stride, width) || bad_stride(out_stride, width)) return SV_E_INVAL;
+  int64_t need = 0;
+  if (sv_attend_workspace(pool, rows, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
+  if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev) return SV_E_INVAL;
+  if (workspace_bytes < need) return SV_E_NOMEM;
+  // 32-bit counts on the device, of a block of rows: chunks of 16 positions for
+  // every kv head and tile of at least 8 query rows
+  each = block_rows(b, n_q_heads, c.head_dim);
+  const int64_t f = (int64_t)each * n_q_heads;
+  if ((f / 8 + (int64_t)b.n_seq * c.n_kv_heads) * (b.limit() / 16 + 1) > INT32_MAX) return SV_E_INVAL;
+  const int rc = device_setup(&num_sms);
+  if (rc != SV_OK) return rc;
+  p = {};
+  p.rows = b;
+  p.q = static_cast<const bf16*>(q_dev);
+  p.out = static_cast<bf16*>(out_dev);
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.lse = lse_dev;
+  p.k = c.k;
+  p.v = c.v;
+  p.k_exp = c.k_exp;
+  p.v_exp = c.v_exp;
+  p.n_q_heads = n_q_heads;
+  p.n_kv_heads = c.n_kv_heads;
+  p.n_pages = c.n_pages;
+  p.block = c.block;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.max_splits = max_splits(b);
+  p.part_ml = static_cast<float2*>(workspace_dev);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) +
+                                      round256(f * p.max_splits * (int64_t)sizeof(float2)));
+  p.status = status_dev;
+  return SV_OK;
+}
+
+// Groups of sequences: as many as there are sequences at most.
+bool read_prefix(const sv_shared_prefix* a, const RowBatch& b) {
+  if (!a || a->n_groups < 1 || a->n_groups > b.n_seq || !a->length) return false;
+  return a->group_start != nullptr || b.n_seq % a->n_groups == 0;
+}
+
 }  // namespace
 
 }  // namespace sv
@@ -182,50 +233,49 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
               void* out_dev, int64_t out_stride, float* lse_dev, int window, int sinks, float scale,
               void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream) {
   KvPool c;
-  RowBatch b;
-  if (!read_pool(pool, c) || !read_rows(rows, b)) return SV_E_INVAL;
-  if (n_q_heads < 1 || n_q_heads % c.n_kv_heads || window < 0 || sinks < 0 || !std::isfinite(scale)) return SV_E_INVAL;
-  if (b.n_seq > kAttendMaxSeq) return SV_E_INVAL;
-  const int width = n_q_heads * c.head_dim;
-  if (bad16(q_dev) || bad16(out_dev) || bad_stride(q_stride, width) || bad_stride(out_stride, width)) return SV_E_INVAL;
-  int64_t need = 0;
-  if (sv_attend_workspace(pool, rows, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
-  if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev) return SV_E_INVAL;
-  if (workspace_bytes < need) return SV_E_NOMEM;
-  // 32-bit counts on the device, of a block of rows: chunks of 16 positions for
-  // every kv head and tile of at least 8 query rows
-  const int each = block_rows(b, n_q_heads, c.head_dim);
-  const int64_t f = (int64_t)each * n_q_heads;
-  if ((f / 8 + (int64_t)b.n_seq * c.n_kv_heads) * (b.limit() / 16 + 1) > INT32_MAX) return SV_E_INVAL;
-  int num_sms = 0;
-  const int rc = device_setup(&num_sms);
+  AttendParams p;
+  int each, num_sms;
+  if (window < 0 || sinks < 0) return SV_E_INVAL;
+  const int rc = read_attend(pool, rows, n_q_heads, q_dev, q_stride, out_dev, out_stride, lse_dev, scale, workspace_dev,
+                             workspace_bytes, status_dev, c, p, each, num_sms);
   if (rc != SV_OK) return rc;
-  AttendParams p = {};
-  p.rows = b;
-  p.q = static_cast<const bf16*>(q_dev);
-  p.out = static_cast<bf16*>(out_dev);
-  p.q_stride = q_stride;
-  p.out_stride = out_stride;
-  p.lse = lse_dev;
-  p.k = c.k;
-  p.v = c.v;
-  p.k_exp = c.k_exp;
-  p.v_exp = c.v_exp;
-  p.n_q_heads = n_q_heads;
-  p.n_kv_heads = c.n_kv_heads;
-  p.n_pages = c.n_pages;
-  p.block = c.block;
   p.window = window;
   p.sinks = sinks;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.max_splits = max_splits(b);
-  p.part_ml = static_cast<float2*>(workspace_dev);
-  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) +
-                                      round256(f * p.max_splits * (int64_t)sizeof(float2)));
-  p.status = status_dev;
-  for (int lo = 0; lo < b.n_rows; lo += each) {
+  for (int lo = 0; lo < p.rows.n_rows; lo += each) {
     p.row_lo = lo;
-    p.row_hi = std::min(lo + each, b.n_rows);
+    p.row_hi = std::min(lo + each, p.rows.n_rows);
+    if (launch_attend(p, c.fmt, c.head_dim, num_sms, static_cast<cudaStream_t>(cuda_stream), false) != cudaSuccess)
+      return SV_E_CUDA;
+  }
+  return SV_OK;
+}
+
+int sv_attend_shared_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_shared_prefix* prefix,
+                               int n_q_heads, int64_t* bytes) {
+  RowBatch b;
+  int64_t own = 0;
+  if (sv_attend_workspace(pool, rows, n_q_heads, &own) != SV_OK || !read_rows(rows, b) || !bytes) return SV_E_INVAL;
+  if (b.n_seq > kAttendMaxSeq || !read_prefix(prefix, b)) return SV_E_INVAL;
+  *bytes = own;
+  return SV_OK;
+}
+
+int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_shared_prefix* prefix, int n_q_heads,
+                     const void* q_dev, int64_t q_stride, void* out_dev, int64_t out_stride, float* lse_dev,
+                     float scale, void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev,
+                     void* cuda_stream) {
+  KvPool c;
+  AttendParams p;
+  int each, num_sms;
+  int64_t need = 0;
+  if (sv_attend_shared_workspace(pool, rows, prefix, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
+  const int rc = read_attend(pool, rows, n_q_heads, q_dev, q_stride, out_dev, out_stride, lse_dev, scale, workspace_dev,
+                             workspace_bytes, status_dev, c, p, each, num_sms);
+  if (rc != SV_OK) return rc;
+  if (workspace_bytes < need) return SV_E_NOMEM;
+  for (int lo = 0; lo < p.rows.n_rows; lo += each) {
+    p.row_lo = lo;
+    p.row_hi = std::min(lo + each, p.rows.n_rows);
     if (launch_attend(p, c.fmt, c.head_dim, num_sms, static_cast<cudaStream_t>(cuda_stream), false) != cudaSuccess)
       return SV_E_CUDA;
   }

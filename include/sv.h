@@ -460,6 +460,33 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
               void* out_dev, int64_t out_stride, float* lse_dev, int window, int sinks, float scale,
               void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
 
+/* The same result for sequences of which groups share the pages of a long prefix
+ * (several continuations of a prompt, many requests behind one system prompt): the
+ * shared pages are read once for all rows of a group instead of once a sequence.
+ *   Group g is the sequences group_start[g] .. group_start[g + 1] - 1 (device int32
+ * [n_groups + 1], not decreasing, or NULL: n_seq / n_groups each; at most n_seq
+ * groups).  All of them have the same pages for positions 0 .. length[g] - 1 (device
+ * int32 [n_groups]): the table row of the group's first sequence is read for them.
+ * Only whole pages that every row of the group sees count as shared (a row within
+ * the prefix limits it for its group); the rest, and sequences in no group, are
+ * attended to as by sv_attend.  No window.
+ *   A row's result may differ from sv_attend's in the last bits, and with the
+ * number of rows and groups of the call and their lengths, since the prefix is cut
+ * between CTAs by the call's whole work.  The same call gives the same bits.
+ * Over a bf16 cache values beyond 2^96 may come out as infinities.
+ *   workspace_dev: sv_attend_shared_workspace bytes, as for sv_attend: that call's,
+ * and n_q_heads * (8 head_dim + 16) bytes a row. */
+typedef struct {
+  int32_t n_groups;
+  const int32_t *length, *group_start;
+} sv_shared_prefix;
+int sv_attend_shared_workspace(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_shared_prefix* prefix,
+                               int n_q_heads, int64_t* bytes);
+int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_shared_prefix* prefix, int n_q_heads,
+                     const void* q_dev, int64_t q_stride, void* out_dev, int64_t out_stride, float* lse_dev,
+                     float scale, void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev,
+                     void* cuda_stream);
+
 /* ------------------------------------------------- pages of sequences, shared
  * Who holds which page of a cache, on the device: pages handed out, shared
  * between sequences, given back, packed and copied.  The same table and lengths

@@ -1,0 +1,322 @@
+"""attend_shared against the 64-bit form of paged_ref.py (its tolerances hold here
+too: the operands, sums and roundings are of the same kinds; a bf16 weight's first
+term is cut off, not rounded, and the second, of the rest, is within 2^-17), and
+against attend on the same batch."""
+import numpy as np
+import pytest
+
+from . import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+PAGE = 16
+
+
+def _sv():
+    import greedy_speculative_decode_gb300 as sv
+    return sv
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+class Case:
+    """Groups of sequences: groups = [(shared positions, [(first, rows), ...]), ...]."""
+
+    def __init__(self, seed, n_q, n_kv, d, groups, fmt="e4m3", block=1, back=0, spread=2.0, slack=0, alone=()):
+        sv = _sv()
+        g = self.g = torch.Generator().manual_seed(seed)
+        self.n_q, self.n_kv, self.d, self.fmt = n_q, n_kv, d, fmt
+        seqs = [(f, m, k) for k, (_, members) in enumerate(groups) for f, m in members] + [(f, m, -1) for f, m in alone]
+        n_seq = len(seqs)
+        self.firsts, self.lens = [s[0] for s in seqs], [s[1] for s in seqs]
+        width = max(1, max((max(f, 0) + m + PAGE - 1) // PAGE for f, m, _ in seqs), max(-(-p // PAGE) for p, _ in groups)) + slack
+        total = n_seq * width + sum(-(-p // PAGE) for p, _ in groups) + 3
+        order = torch.randperm(total, generator=g)
+        table = order[: n_seq * width].reshape(n_seq, width).int()
+        at = n_seq * width
+        self.start_of = [0]
+        i = 0
+        for p, members in groups:
+            n = p // PAGE
+            table[i:i + len(members), :n] = order[at:at + n].int()
+            at += n
+            i += len(members)
+            self.start_of.append(i)
+        self.table_h = table
+        n = sum(self.lens)
+        self.n_rows = n + back
+        x = torch.randn((2, total, n_kv, PAGE, d), generator=g) * torch.exp2(spread * torch.randn((2, total, n_kv, PAGE, 1), generator=g))
+        if fmt == "bf16":
+            pool = [x[0].bfloat16(), x[1].bfloat16()]
+        else:
+            e = torch.randint(118, 128, (2, total, n_kv, PAGE // block), generator=g)
+            c = torch.randint(0, 127, (2, total, n_kv, PAGE, d), generator=g) + 128 * torch.randint(0, 2, (2, total, n_kv, PAGE, d), generator=g)
+            pool = [c[0].to(torch.uint8), c[1].to(torch.uint8), e[0].to(torch.uint8), e[1].to(torch.uint8)]
+        self.cache = sv.PagedKv(*[t.cuda() for t in pool])
+        self.start = np.concatenate([[0], np.cumsum(self.lens)]).astype(np.int32).tolist()
+        self.where = ref.rows_of(self.firsts, self.start, self.n_rows, n_seq)
+        self.table, self.first = table.cuda(), torch.tensor(self.firsts, dtype=torch.int32).cuda()
+        self.rows = sv.RowBatch(self.table, self.first, self.n_rows, row_start=torch.tensor(self.start, dtype=torch.int32).cuda(),
+                                max_rows=max(max(self.lens), 1))
+        self.length = torch.tensor([p for p, _ in groups], dtype=torch.int32).cuda()
+        self.prefix = sv.SharedPrefix(self.length, torch.tensor(self.start_of, dtype=torch.int32).cuda())
+
+    def queries(self, spread=1.0):
+        x = torch.randn((self.n_rows, self.n_q, self.d), generator=self.g)
+        return (x * torch.exp2(spread * torch.randn((self.n_rows, self.n_q, 1), generator=self.g))).bfloat16().cuda()
+
+    def pool_np(self):
+        c = self.cache
+        if self.fmt == "bf16":
+            return (f64(c.k), None), (f64(c.v), None)
+        return (c.k.cpu().numpy(), c.k_exp.cpu().numpy()), (c.v.cpu().numpy(), c.v_exp.cpu().numpy())
+
+    def call(self, q, scale=None, **kw):
+        out = torch.full((self.n_rows, self.n_q, self.d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((self.n_rows, self.n_q), float("nan"), device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        _sv().attend_shared(self.cache, self.rows, self.prefix, q, out, scale=scale, lse=lse, status=st, **kw)
+        torch.cuda.synchronize()
+        self.status = int(st.item())
+        return out, lse
+
+    def plain(self, q, scale=None):
+        out = torch.full((self.n_rows, self.n_q, self.d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((self.n_rows, self.n_q), float("nan"), device="cuda")
+        _sv().attend(self.cache, self.rows, q, out, scale=scale, lse=lse)
+        torch.cuda.synchronize()
+        return out, lse
+
+    def check(self, scale=None, q=None):
+        q = self.queries() if q is None else q
+        out, lse = self.call(q, scale)
+        assert self.status == 0
+        o, l, tol, tol_l = ref.attend(self.pool_np(), self.table_h.numpy(), self.where, f64(q), 0, 0, self.d ** -0.5 if scale is None else scale)
+        n = self.start[-1]
+        got, gl = f64(out)[:n], f64(lse)[:n]
+        assert np.isfinite(got).all()
+        over = np.abs(got - o[:n]) - tol[:n]
+        assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+        empty = np.isinf(l[:n])
+        assert np.array_equal(np.isinf(gl), empty) and (gl[empty] < 0).all()
+        assert (np.abs(gl[~empty] - l[:n][~empty]) <= tol_l[:n][~empty]).all()
+        assert np.isnan(f64(out)[n:]).all() and np.isnan(f64(lse)[n:]).all()  # rows behind the last sequence
+        return q, out, lse
+
+
+SHAPES = [(4, 2, 64), (32, 8, 128), (8, 1, 256), (7, 1, 128), (20, 1, 64)]
+FORMS = [("bf16", 1), ("e4m3", 1), ("e4m3", 16)]
+BATCHES = {
+    "one page": [(16, [(16, 1), (17, 1)])],
+    "a chunk": [(128, [(128, 1), (131, 2), (140, 1)])],
+    "ends inside": [(208, [(208, 1), (230, 3), (209, 1), (290, 2)])],
+    "long": [(1104, [(1110, 1), (1104, 1), (1190, 1)])],
+    "groups": [(64, [(70, 1)] * 3), (0, [(5, 2), (9, 1)]), (320, [(330, 2), (321, 1)]), (32, [(32, 1)])],
+    "not whole pages": [(75, [(75, 1), (80, 2)]), (15, [(20, 1), (16, 1)])],
+    "rows within the prefix": [(256, [(300, 1), (100, 2), (260, 1)])],
+    "padding": [(48, [(50, 2), (-3, 2), (-2, 4)]), (64, [(66, 1), (-9, 1)])],
+    "sequences without rows": [(48, [(50, 0), (50, 2), (60, 0)]), (32, [(40, 0)])],
+    "wide": [(144, [(144, 90), (150, 1)])],
+}
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("n_q,n_kv,d", SHAPES)
+@pytest.mark.parametrize("batch", sorted(BATCHES))
+def test_shared(fmt, block, n_q, n_kv, d, batch):
+    if batch in ("long", "wide") and (n_q, n_kv, d) not in ((4, 2, 64), (7, 1, 128), (8, 1, 256)):
+        pytest.skip("the 64-bit form of the wider ones takes long")
+    Case(3, n_q, n_kv, d, BATCHES[batch], fmt, block, back=2, alone=((37, 1),)).check()
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("scale", [1.0, -0.11, 0.0])
+def test_scales(fmt, block, scale):
+    Case(5, 6, 2, 128, [(160, [(170, 1), (163, 2)])], fmt, block, spread=1.0).check(scale=scale)
+
+
+def near_attend(c, q, out, lse):
+    """Both are within a bf16 step (of the value, or of the mean's terms) of the exact result."""
+    o, l = c.plain(q)
+    n = c.start[-1]
+    a, b = f64(out)[:n], f64(o)[:n]
+    big = np.abs(b).max() + 1e-30
+    assert (np.abs(a - b) <= 2.0 ** -7 * np.abs(b) + 2.0 ** -9 * big).all()
+    gl, wl = f64(lse)[:n], f64(l)[:n]
+    fine = np.isfinite(wl)
+    assert np.array_equal(fine, np.isfinite(gl)) and (np.abs(gl[fine] - wl[fine]) <= 2.0 ** -12 * (np.abs(wl[fine]) + 8)).all()
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("n_q,n_kv,d,seqs,rows,prefix", [
+    (32, 8, 128, 64, 1, 4096), (32, 8, 128, 33, 1, 1000), (28, 4, 128, 9, 5, 3333), (8, 1, 256, 40, 2, 2048),
+    (4, 2, 64, 200, 1, 5000), (16, 8, 128, 3, 128, 1500), (32, 8, 128, 1, 200, 700), (8, 1, 256, 1, 1, 20000), (2, 2, 64, 700, 3, 640)])
+def test_larger_batches(fmt, block, n_q, n_kv, d, seqs, rows, prefix):
+    """Many tiles, many segments, and one; against attend."""
+    c = Case(11, n_q, n_kv, d, [(prefix, [(prefix + (s * 7) % 60, rows) for s in range(seqs)])], fmt, block, spread=0.5)
+    q = c.queries(0.5)
+    near_attend(c, q, *c.call(q))
+    assert c.status == 0
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+def test_many_groups(fmt, block):
+    groups = [(16 * (k % 9) + 100 * (k % 3), [(450 + k + s, 1 + (k + s) % 3) for s in range(1 + k % 4)]) for k in range(40)]
+    c = Case(12, 8, 2, 128, groups, fmt, block, spread=0.5)
+    q = c.queries(0.5)
+    near_attend(c, q, *c.call(q))
+    c2 = Case(12, 8, 2, 64, groups, fmt, block, spread=0.5)
+    q = c2.queries(0.5)
+    near_attend(c2, q, *c2.call(q))
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scores_that_rise_and_fall(fmt, block, d):
+    """References that move on every chunk, by little and by much."""
+    c = Case(13, 4, 1, d, [(1024, [(1030, 1), (1040, 2)])], fmt, block, spread=0.2)
+    q = c.queries(0.0)
+    for grow in (1.0, 6.0, -6.0):
+        p = torch.arange(1024 // PAGE).float()
+        f = torch.exp2(grow * (p / p[-1]) - (grow if grow > 0 else 0))
+        pages = c.table_h[0, :1024 // PAGE].long().cuda()
+        if fmt == "bf16":
+            c.cache.k[pages] = (torch.randn((len(p), 1, PAGE, d), generator=c.g) * 8 * f[:, None, None, None]).bfloat16().cuda()
+        else:
+            c.cache.k_exp[pages] = (120 + torch.log2(f).round()).to(torch.uint8).cuda()[:, None, None]
+        c.check(q=q)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_blocks_of_zeros_beside_large_values(d):
+    """Exponents of values 2^120 apart: denominators hold (an 8-bit cache)."""
+    c = Case(14, 4, 1, d, [(320, [(320, 1), (330, 1)])], "e4m3", 1)
+    pages = c.table_h[0, :20].long().cuda()
+    c.cache.v_exp[pages[::2]] = 27
+    c.cache.v[pages[::2]] = 0
+    c.cache.v_exp[pages[1::2]] = 150
+    c.check()
+    c.cache.v_exp[pages] = 0
+    c.cache.k_exp[pages[3]] = 0
+    c.cache.k[pages[3]] = 0
+    c.cache.v[pages] = 0
+    out, _ = c.call(c.queries())
+    assert np.isfinite(f64(out)[:2]).all()
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_values_that_are_not_finite(fmt, block, d):
+    c = Case(15, 4, 2, d, [(272, [(280, 1), (272, 2)]), (32, [(40, 1)])], fmt, block)
+    q = c.queries()
+    out0, lse0 = c.call(q)
+    page = int(c.table_h[0, 9])
+    if fmt == "bf16":
+        c.cache.v[page, 1, 5, 7] = float("inf")
+        c.cache.v[page, 1, 6, 9] = float("-inf")
+        c.cache.v[page, 1, 6, 10] = float("nan")
+        c.cache.v[page, 1, 0, 11] = float("inf")
+        c.cache.v[page, 1, 3, 11] = float("-inf")
+    else:
+        c.cache.v_exp[page, 1] = 255
+        c.cache.v[page, 1] = 0
+    out, lse = c.call(q)
+    a, b = f64(out), f64(out0)
+    rows, same = slice(0, 3), np.ones((c.n_rows, 4, d), bool)
+    if fmt == "bf16":
+        assert (a[rows, 2:, 7] == np.inf).all() and (a[rows, 2:, 9] == -np.inf).all() and np.isnan(a[rows, 2:, 10:12]).all()
+        same[rows, 2:, [7, 9, 10, 11]] = False
+        same = np.moveaxis(same, 0, 0)
+        for k in (7, 9, 10, 11):
+            same[rows, 2:, k] = False
+    else:
+        assert np.isnan(a[rows, 2:]).all()
+        same[rows, 2:] = False
+    n = c.start[-1]
+    assert np.array_equal(a[:n][same[:n]], b[:n][same[:n]])
+    # large finite values have a finite mean
+    if fmt == "bf16":
+        c.cache.v[page] = 2.0 ** 90
+        c.check(q=q)
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_pages_that_are_not_there(fmt, block, d):
+    """A bad entry among the shared pages: its positions are unseen, and bit 2 is raised."""
+    c = Case(16, 4, 2, d, [(400, [(400, 1), (410, 2)])], fmt, block)
+    q = c.queries()
+    good = c.table.clone()
+    for entry in (-1, 1 << 30, c.cache.n_pages):
+        c.table.copy_(good)
+        c.table[:, 8:13] = entry
+        c.table[:, 24] = entry
+        out, lse = c.call(q)
+        assert c.status == 2
+        want, wl = c.plain(q)
+        near_attend(c, q, out, lse)
+    c.table.fill_(-1)
+    out, lse = c.call(q)
+    assert (f64(out)[:3] == 0).all() and (f64(lse)[:3] == -np.inf).all()
+
+
+def test_queries_that_are_not_finite_and_very_uneven():
+    for fmt in ("bf16", "e4m3"):
+        c = Case(17, 4, 2, 128, [(144, [(150, 1), (150, 1), (150, 1)])], fmt)
+        q = c.queries()
+        base, _ = c.call(q)
+        q2 = q.clone()
+        q2[1, 2, 5] = float("nan")
+        q2[1, 0] = float("inf")
+        out, lse = c.call(q2)
+        a, b = f64(out), f64(base)
+        assert np.isnan(a[1, 2]).all() and np.isnan(a[1, 0]).all()
+        keep = np.ones((3, 4), bool)
+        keep[1, [0, 2]] = False
+        assert np.array_equal(a[keep], b[keep])
+        q[0] *= 2.0 ** 20
+        q[1] *= 2.0 ** -30
+        c.check(q=q, scale=2.0 ** -22)
+
+
+def test_strided_rows_a_workspace_of_ones_own_and_streams():
+    sv = _sv()
+    c = Case(18, 8, 2, 128, [(512, [(512 + s, 1) for s in range(20)])])
+    q = c.queries()
+    want, wl = c.call(q)
+    wide = torch.full((c.n_rows, 30, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:11] = q
+    out = torch.full((c.n_rows, 12, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    need = sv.attend_shared_workspace(c.cache, c.rows, c.prefix, 8)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    sv.attend_shared(c.cache, c.rows, c.prefix, wide[:, 3:11], out[:, 2:10], workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(out[:, 2:10], want) and (out[:, :2] == 5).all() and (out[:, 10:] == 5).all()
+    for _ in range(10):
+        again, gl = c.call(q)
+        assert torch.equal(again, want) and torch.equal(gl, wl)
+
+
+def test_captured_and_replayed_with_other_lengths():
+    sv = _sv()
+    c = Case(19, 8, 2, 128, [(512, [(530 + s, 1) for s in range(6)])], slack=3)
+    q = c.queries()
+    out = torch.empty_like(q)
+    sv.attend_shared(c.cache, c.rows, c.prefix, q, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.attend_shared(c.cache, c.rows, c.prefix, q, out)
+    for shared, first in ((512, 530), (80, 97), (0, 3), (496, 540)):
+        c.length.fill_(shared)
+        c.first.copy_(torch.arange(6, dtype=torch.int32).cuda() + first)
+        q.copy_(c.queries())
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, c.call(q)[0])
+        _, lse = c.call(q)
+        near_attend(c, q, out, lse)
