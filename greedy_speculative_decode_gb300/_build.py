@@ -10,7 +10,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsv.so")
 SOURCES = ["k_linear.cu", "k_linear_tc.cu", "k_attn.cu", "k_misc.cu", "sv_api.cu", "sv_noalloc.cu",
-           "sv_paged.cu", "sv_pages.cu", "k_pages.cu", "k_logprobs.cu", "k_kv.cu", "k_attend_64.cu", "k_attend_128.cu", "k_attend_256.cu"]
+           "sv_paged.cu", "sv_pages.cu", "k_pages.cu", "k_logprobs.cu", "k_shared.cu",
+           "k_kv.cu", "k_attend_64.cu", "k_attend_128.cu", "k_attend_256.cu"]
 
 # --fmad=false: every fused multiply-add in the kernels is written out, so
 # the rounding of each element never depends on what the compiler contracts.

@@ -204,6 +204,11 @@ __device__ __forceinline__ SplitRange splits_seen(int t0, int t1, int window, in
 struct ChunkList {
   int n_sink, lo, n;
   __device__ __forceinline__ int at(int i) const { return i < n_sink ? i : lo + i - n_sink; }
+  // without the chunks before the first (no window, so no sinks)
+  __device__ __forceinline__ void skip(int first) {
+    n = max(0, n - max(0, first - lo));
+    lo = max(lo, first);
+  }
 };
 template <class C>
 __device__ __forceinline__ ChunkList chunks_seen(int t0, int t1, int window, int sinks, int limit) {
@@ -271,6 +276,7 @@ struct AttendPlace {
     tile.nf = n * wk.G;
     tiles = (tile.nf + C::QR - 1) / C::QR;
     list = chunks_seen<C>(tile.first, tile.first + n - 1, wk.p.window, wk.p.sinks, wk.p.rows.limit());
+    if (wk.p.from) list.skip(__ldcg(wk.p.from + seq) / C::kChunk);
   }
   __device__ __forceinline__ void open_tile(const AttendWork<C>& wk) {
     tile.kvh = x / tiles;
@@ -278,6 +284,7 @@ struct AttendPlace {
     t0 = tile.first + tile.f0 / wk.G;
     t1 = tile.first + (min(tile.f0 + C::QR, tile.nf) - 1) / wk.G;
     vis_lo = wk.p.window > 0 ? (int)max((int64_t)t0 - wk.p.window + 1, (int64_t)0) : 0;
+    if (wk.p.from) vis_lo = __ldcg(wk.p.from + seq);
     vis_end = min(t1 + 1, wk.p.rows.limit());
   }
   // The list's last place of this CTA's run + 1: the items that begin before `end`.
@@ -327,7 +334,8 @@ __device__ int attend_plan(const AttendParams& p, int G, int* before, int* first
     const int n = max(0, start[s + 1] - start[s]);
     back |= start[s + 1] < start[s];
     const int tiles = (n * G + C::QR - 1) / C::QR;
-    const ChunkList l = chunks_seen<C>(first[s], first[s] + n - 1, p.window, p.sinks, p.rows.limit());
+    ChunkList l = chunks_seen<C>(first[s], first[s] + n - 1, p.window, p.sinks, p.rows.limit());
+    if (p.from) l.skip(__ldcg(p.from + s) / C::kChunk);
     before[s] = n > 0 ? tiles * p.n_kv_heads * l.n : 0;
     if (n > 0 && first[s] + n > p.rows.limit() && p.status) atomicOr(p.status, ST_BAD_PAGE);
   }
@@ -1194,6 +1202,7 @@ cudaError_t attend_launch_t(const AttendParams& p, int num_sms,
   cfg.numAttrs = pdl ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, k_attend<D, FMT, N>, p);
   if (e != cudaSuccess) return e;
+  if (p.from) return cudaSuccess;  // (merged with the rest by the caller)
   const int64_t units = n_rows * p.n_q_heads;
   const size_t words = (size_t)((p.max_splits + 31) / 32) * 33;
   cfg.blockDim = dim3(256);

@@ -1,0 +1,125 @@
+// k_shared.cu -- the plan of attention to shared prefixes, and the launches of its
+// kernels (shared_dev.cuh).
+#include "shared_dev.cuh"
+
+#include <algorithm>
+
+namespace sv {
+namespace {
+
+// What the groups share: eff, the positions that lie in shared pages and that all
+// rows of the group see (whole pages of them), and the work this makes.  One
+// thread a sequence, then one a group.
+__global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ SharedParams p, int chunk, int streams) {
+  __shared__ int s_eff[1024], s_start[1025];
+  __shared__ long long s_sum[32];
+  const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
+  pdl_trigger();
+  for (int g = tid; g <= N; g += 1024)
+    s_start[g] = p.group_start ? min(max(__ldg(p.group_start + g), 0), S) : (int)((long long)S * g / N);
+  if (tid < N) {
+    const int most = min(max(__ldg(p.length + tid), 0), p.a.rows.limit());
+    s_eff[tid] = most;
+  }
+  __syncthreads();
+  const bool back = __syncthreads_or(tid < N && s_start[tid + 1] < s_start[tid]);
+  if (back && tid == 0 && p.a.status) atomicOr(p.a.status, ST_BAD_PAGE);
+  auto start_of = [&](int s) { return p.a.rows.row_start ? __ldg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
+  auto clip = [&](int r) { return min(max(r, 0), p.a.rows.n_rows); };
+  int gi = -1;
+  if (tid < S) {
+    if (!back && tid >= s_start[0] && tid < s_start[N]) {
+      int lo = 0, hi = N;  // the last group that begins at or before the sequence
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= tid) lo = mid; else hi = mid;
+      }
+      gi = lo;
+      const int first = first_of(p.a.rows, tid), n = start_of(tid + 1) - start_of(tid);
+      if (n > 0 && first + n > 0) atomicMin(&s_eff[gi], max(first, 0) + 1);  // (rows of padding alone see nothing)
+    }
+    p.group[tid] = gi;
+  }
+  __syncthreads();
+  SharedGroup g = {};
+  long long units = 0;
+  if (tid < N) {
+    g.s0 = s_start[tid];
+    if (!back && s_start[tid + 1] > g.s0) {
+      g.row0 = clip(start_of(g.s0));
+      const int rows = clip(start_of(s_start[tid + 1])) - g.row0;
+      if (rows > 0) {
+        g.eff = s_eff[tid] / kPage * kPage;
+        g.R = rows * G;
+        g.chunks = (g.eff + chunk - 1) / chunk;
+        g.tiles = (g.R + kSharedTile - 1) / kSharedTile;
+      }
+    }
+    s_eff[tid] = g.eff;
+    units = (long long)p.a.n_kv_heads * g.chunks * g.tiles;
+  }
+  // A CTA has whole chunks: two units, where a list has two tiles.
+  const int least = __syncthreads_or(units > 0 && g.tiles > 1) ? streams : 1;
+  // units before each group
+  const int lane = tid & 31, warp = tid >> 5;
+  long long x = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    before += w < warp ? s_sum[w] : 0;
+    all += s_sum[w];
+  }
+  if (tid < N) {
+    g.unit0 = before + x - units;
+    p.plan[tid] = g;
+  }
+  if (tid == 0) {
+    SharedGroup end = {};
+    end.unit0 = all;
+    end.eff = (int)min((long long)p.grid, max(all / least, 1LL));
+    p.plan[N] = end;
+  }
+  if (tid < S) p.from[tid] = gi >= 0 ? s_eff[gi] : 0;
+}
+
+}  // namespace
+
+cudaError_t prepare_shared_kernels() {
+  cudaError_t e;
+  if ((e = shared_prepare<64, SV_KV_BF16>()) != cudaSuccess || (e = shared_prepare<64, SV_KV_E4M3>()) != cudaSuccess ||
+      (e = shared_prepare<128, SV_KV_BF16>()) != cudaSuccess || (e = shared_prepare<128, SV_KV_E4M3>()) != cudaSuccess ||
+      (e = shared_prepare<256, SV_KV_BF16>()) != cudaSuccess)
+    return e;
+  return shared_prepare<256, SV_KV_E4M3>();
+}
+
+cudaError_t launch_shared_prefix(const SharedParams& p, int fmt, int head_dim, cudaStream_t s) {
+  k_shared_plan<<<1, 1024, 0, s>>>(p, shared_chunk(head_dim), shared_streams(head_dim));
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool b = fmt == SV_KV_BF16;
+  switch (head_dim) {
+    case 64: return b ? shared_launch<64, SV_KV_BF16>(p, s) : shared_launch<64, SV_KV_E4M3>(p, s);
+    case 128: return b ? shared_launch<128, SV_KV_BF16>(p, s) : shared_launch<128, SV_KV_E4M3>(p, s);
+    case 256: return b ? shared_launch<256, SV_KV_BF16>(p, s) : shared_launch<256, SV_KV_E4M3>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_shared_merge(const SharedParams& p, int head_dim, int num_sms, cudaStream_t s) {
+  switch (head_dim) {
+    case 64: return shared_merge_launch<64>(p, s);
+    case 128: return shared_merge_launch<128>(p, s);
+    case 256: return shared_merge_launch<256>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sv

@@ -78,6 +78,9 @@ struct AttendParams {
   // before the kernel ahead of this one began (a context's steps): they are then
   // read, and the first pages requested, before the wait for that kernel.
   bool early;
+  // First position of each sequence that this launch takes ([n_seq], multiples of
+  // the page), or null: those before are another kernel's, which merges too.
+  const int* from;
 };
 
 cudaError_t prepare_attend_kernels();

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "paged.h"
+#include "shared.h"
 
 namespace sv {
 
@@ -46,7 +47,7 @@ int device_setup(int* num_sms) {
   if (g_dev[dev].num_sms == 0) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return SV_E_CUDA;
-    if (prepare_attend_kernels() != cudaSuccess) return SV_E_CUDA;
+    if (prepare_attend_kernels() != cudaSuccess || prepare_shared_kernels() != cudaSuccess) return SV_E_CUDA;
     g_dev[dev].num_sms = n;
   }
   *num_sms = g_dev[dev].num_sms;
@@ -177,6 +178,18 @@ int read_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads,
   return SV_OK;
 }
 
+// Most CTAs of the prefix kernel (one an SM): the workspace has a tile for each, whatever the device.
+constexpr int kSharedMostCtas = 192;
+
+// The workspace of a call with shared prefixes, behind attend's: the plan, then the
+// prefix kernel's partials.
+int64_t shared_bytes(const RowBatch& b, int n_groups, int n_q_heads, int head_dim, int64_t* plane) {
+  *plane = (int64_t)b.n_rows * n_q_heads + (int64_t)kSharedMostCtas * kSharedTile;
+  const int64_t rows = *plane * shared_streams(head_dim);
+  return round256((n_groups + 1) * (int64_t)sizeof(SharedGroup)) + round256(2 * 4 * (int64_t)b.n_seq) +
+         round256(rows * (int64_t)sizeof(float2)) + rows * head_dim * (int64_t)sizeof(float);
+}
+
 // Groups of sequences: as many as there are sequences at most.
 bool read_prefix(const sv_shared_prefix* a, const RowBatch& b) {
   if (!a || a->n_groups < 1 || a->n_groups > b.n_seq || !a->length) return false;
@@ -256,7 +269,8 @@ int sv_attend_shared_workspace(const sv_kv_pool* pool, const sv_row_batch* rows,
   int64_t own = 0;
   if (sv_attend_workspace(pool, rows, n_q_heads, &own) != SV_OK || !read_rows(rows, b) || !bytes) return SV_E_INVAL;
   if (b.n_seq > kAttendMaxSeq || !read_prefix(prefix, b)) return SV_E_INVAL;
-  *bytes = own;
+  int64_t plane;
+  *bytes = round256(own) + shared_bytes(b, prefix->n_groups, n_q_heads, pool->head_dim, &plane);
   return SV_OK;
 }
 
@@ -273,10 +287,34 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
                              workspace_bytes, status_dev, c, p, each, num_sms);
   if (rc != SV_OK) return rc;
   if (workspace_bytes < need) return SV_E_NOMEM;
+  SharedParams sp = {};
+  uint8_t* at = static_cast<uint8_t*>(workspace_dev) +
+                round256(partial_bytes(each, n_q_heads, p.max_splits, c.head_dim));
+  auto take = [&](int64_t bytes) {
+    uint8_t* r = at;
+    at += round256(bytes);
+    return r;
+  };
+  sp.n_groups = prefix->n_groups;
+  sp.group_start = prefix->group_start;
+  sp.length = prefix->length;
+  shared_bytes(p.rows, sp.n_groups, n_q_heads, c.head_dim, &sp.plane);
+  sp.plan = reinterpret_cast<SharedGroup*>(take((sp.n_groups + 1) * (int64_t)sizeof(SharedGroup)));
+  sp.from = reinterpret_cast<int*>(take(2 * 4 * (int64_t)p.rows.n_seq));
+  sp.group = sp.from + p.rows.n_seq;
+  sp.ml = reinterpret_cast<float2*>(take(sp.plane * shared_streams(c.head_dim) * (int64_t)sizeof(float2)));
+  sp.o = reinterpret_cast<float*>(at);
+  sp.grid = std::min(num_sms, kSharedMostCtas);
+  p.from = sp.from;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  sp.a = p;
+  if (launch_shared_prefix(sp, c.fmt, c.head_dim, s) != cudaSuccess) return SV_E_CUDA;
   for (int lo = 0; lo < p.rows.n_rows; lo += each) {
     p.row_lo = lo;
     p.row_hi = std::min(lo + each, p.rows.n_rows);
-    if (launch_attend(p, c.fmt, c.head_dim, num_sms, static_cast<cudaStream_t>(cuda_stream), false) != cudaSuccess)
+    sp.a = p;
+    if (launch_attend(p, c.fmt, c.head_dim, num_sms, s, true) != cudaSuccess ||
+        launch_shared_merge(sp, c.head_dim, num_sms, s) != cudaSuccess)
       return SV_E_CUDA;
   }
   return SV_OK;

@@ -320,3 +320,12 @@ def test_captured_and_replayed_with_other_lengths():
         assert torch.equal(out, c.call(q)[0])
         _, lse = c.call(q)
         near_attend(c, q, out, lse)
+
+
+def test_groups_that_run_backwards_share_nothing():
+    c = Case(20, 4, 2, 64, [(64, [(70, 1), (71, 1)]), (32, [(40, 1)])])
+    q = c.queries()
+    c.prefix.tensors[1].copy_(torch.tensor([0, 3, 2], dtype=torch.int32))
+    out, lse = c.call(q)
+    assert c.status == 2
+    near_attend(c, q, out, lse)
