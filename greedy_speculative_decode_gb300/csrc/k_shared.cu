@@ -12,7 +12,7 @@ namespace {
 // thread a sequence, then one a group.
 __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ SharedParams p, int chunk, int streams) {
   __shared__ int s_eff[1024], s_start[1025];
-  __shared__ long long s_sum[32];
+  __shared__ int s_sum[32], s_unit[1025];
   const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
   pdl_trigger();
   for (int g = tid; g <= N; g += 1024)
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   }
   __syncthreads();
   SharedGroup g = {};
-  long long units = 0;
+  int units = 0;
   if (tid < N) {
     g.s0 = s_start[tid];
     if (!back && s_start[tid + 1] > g.s0) {
@@ -56,40 +56,58 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
       }
     }
     s_eff[tid] = g.eff;
-    units = (long long)p.a.n_kv_heads * g.chunks * g.tiles;
+    units = p.a.n_kv_heads * g.chunks * g.tiles;
   }
   // A CTA has whole chunks: two units, where a list has two tiles.
   const int least = __syncthreads_or(units > 0 && g.tiles > 1) ? streams : 1;
   // units before each group
   const int lane = tid & 31, warp = tid >> 5;
-  long long x = units;
+  int x = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) s_sum[warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
+  int before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < 32; ++w) {
     before += w < warp ? s_sum[w] : 0;
     all += s_sum[w];
   }
+  const int ctas = min(p.grid, max(all / least, 1));
   if (tid < N) {
     g.unit0 = before + x - units;
+    s_unit[tid] = g.unit0;
     p.plan[tid] = g;
   }
   if (tid == 0) {
     SharedGroup end = {};
     end.unit0 = all;
-    end.eff = (int)min((long long)p.grid, max(all / least, 1LL));
+    end.eff = ctas;
     p.plan[N] = end;
+  }
+  __syncthreads();
+  if (tid <= p.grid) {  // where each CTA's run begins
+    const int u = tid < ctas ? (int)((unsigned long long)all * tid / ctas) : all;
+    int lo = 0, hi = N;  // the last group that begins at or before it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_unit[mid] <= u) lo = mid; else hi = mid;
+    }
+    p.begin[tid] = make_int2(u, lo);
   }
   if (tid < S) p.from[tid] = gi >= 0 ? s_eff[gi] : 0;
 }
 
 }  // namespace
+
+bool shared_units_fit(const RowBatch& b, int n_groups, int n_q_heads, int n_kv_heads, int head_dim) {
+  const int64_t chunks = b.limit() / shared_chunk(head_dim) + 1;
+  const int64_t tiles = (int64_t)b.n_rows * (n_q_heads / n_kv_heads) / kSharedTile + n_groups;
+  return chunks * tiles <= INT32_MAX / 2 / n_kv_heads;
+}
 
 cudaError_t prepare_shared_kernels() {
   cudaError_t e;
@@ -115,9 +133,9 @@ cudaError_t launch_shared_prefix(const SharedParams& p, int fmt, int head_dim, c
 
 cudaError_t launch_shared_merge(const SharedParams& p, int head_dim, int num_sms, cudaStream_t s) {
   switch (head_dim) {
-    case 64: return shared_merge_launch<64>(p, s);
-    case 128: return shared_merge_launch<128>(p, s);
-    case 256: return shared_merge_launch<256>(p, s);
+    case 64: return shared_merge_launch<64>(p, num_sms, s);
+    case 128: return shared_merge_launch<128>(p, num_sms, s);
+    case 256: return shared_merge_launch<256>(p, num_sms, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -13,11 +13,12 @@ __host__ __device__ constexpr int shared_chunk(int d) { return d <= 128 ? 128 : 
 
 // A group of sequences, as k_shared_plan leaves it.
 struct SharedGroup {
-  long long unit0;  // units of work before it (a unit: a chunk for a tile); behind the last group the total
-  int eff;          // positions that all its rows see and share; behind the last group the CTAs that take part
-  int s0;           // its first sequence, whose table is read
-  int row0, R;      // its first row, and its query rows for a kv head
+  int unit0;     // units of work before it (a unit: a chunk for a tile); behind the last group the total
+  int eff;       // positions that all its rows see and share; behind the last group the CTAs that take part
+  int s0;        // its first sequence, whose table is read
+  int row0, R;   // its first row, and its query rows for a kv head
   int chunks, tiles;
+  int unused;
 };
 
 struct SharedParams {
@@ -29,6 +30,7 @@ struct SharedParams {
   SharedGroup* plan;  // [n_groups + 1]
   int* from;          // [n_seq] first position of a sequence that is not shared
   int* group;         // [n_seq] its group, or -1
+  int2* begin;        // [grid + 1] the unit that a CTA's run begins with, and its group
   float2* ml;         // [streams][plane] a segment's references and sums
   float* o;           // [streams][plane][head_dim]
   int64_t plane;      // rows of a stream's
@@ -36,6 +38,8 @@ struct SharedParams {
 };
 
 cudaError_t prepare_shared_kernels();
+// Whether the units of a call count in 32 bits.
+bool shared_units_fit(const RowBatch& b, int n_groups, int n_q_heads, int n_kv_heads, int head_dim);
 // The plan and the prefix, for all rows.
 cudaError_t launch_shared_prefix(const SharedParams& p, int fmt, int head_dim, cudaStream_t s);
 // Rows a.row_lo .. a.row_hi - 1: the prefix's partials and the own positions' merged.

@@ -17,7 +17,7 @@
 //     tensor memory, the weights go back there over them as the A operand of P V.
 //     The reference of a row moves only when its maximum rises by more than 2^8
 //     over it, so the accumulators are seldom read back and rescaled.
-//   Warp 8: one thread issues the multiplies.  Warp 9: loads.
+//   Warp 8: one thread issues the multiplies.  Warps 9, 10: loads of K and V.
 //   Warps 12-15 (8-bit caches): codes to f16, once for all query rows of the CTA.
 //
 // Types, as in attend_dev.cuh: a bf16 cache's weights are the sum of two bf16
@@ -41,7 +41,12 @@ bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols
 
 namespace {
 
-constexpr float kShSlack = 8.0f;     // log2 of what a row's maximum may exceed its reference by
+constexpr float kShSlack = 8.0f;     // log2 of what a row's maximum may rise by before its reference follows
+// log2 of a row's largest weight when its reference is set.  f16 weights lie as high
+// in their range as the slack lets them: their steps below 2^-14 are then 2^-32 of
+// the largest, which leaves 2^-25 where a chunk's values are scaled by up to 2^-7.
+__host__ __device__ constexpr float sh_bias(bool bf16) { return bf16 ? 0.0f : 7.0f; }
+constexpr int kShKeySpread = 15, kShValueSpread = 7;  // of the exponents of an even chunk
 constexpr float kShNone = -3.0e38f;  // reference of a row that has seen nothing
 constexpr float kShFar = -126.0f;    // 2^x is a normal fp32 number from here on
 
@@ -58,7 +63,7 @@ struct ShCfg {
   static constexpr int kRings = 4;  // chunks whose scales and page masks are kept
   static constexpr int kThreads = kBf16 ? 384 : 512;
   // registers: of the launch, of a softmax thread, of the others (their sum must not be above the launch's)
-  static constexpr int kRegs = kBf16 ? 168 : 128, kRegsSoft = kBf16 ? 232 : 200, kRegsOther = kBf16 ? 40 : 56;
+  static constexpr int kRegs = kBf16 ? 168 : 128, kRegsSoft = kBf16 ? 224 : 192, kRegsOther = kBf16 ? 56 : 64;
   static_assert(2 * kRegsSoft + (kThreads / 128 - 2) * kRegsOther <= kThreads / 128 * kRegs, "registers of the warpgroups");
   // tensor memory: scores (and weights over them) of two steps, accumulators of each stream
   static constexpr uint32_t kScoreCol = CP, kOutCol = 512 - NS * D;
@@ -70,9 +75,10 @@ struct ShCfg {
   static constexpr int kOffLow = kOffScale + (kBf16 ? 0 : kRings * 3 * CP * 4);
   static constexpr int kOffBar = kOffLow;
   static constexpr int kBars = 2 * kOps + 2 * kRaws + kRings + 2 /*s_full*/ + 2 /*p_full*/ + 2 /*pv*/ + 2 /*q*/ + 1 /*drain*/;
-  static constexpr int kOffMask = kOffBar + kBars * 8;  // [8] pages of a chunk that are there
-  static constexpr int kOffRawMask = kOffMask + 32;     // [8] the same for an item of codes
-  static constexpr int kOffTmem = kOffRawMask + 32;
+  static constexpr int kOffMeta = kOffBar + kBars * 8;  // [8] what a chunk holds (sh_meta)
+  static constexpr int kOffRawMeta = kOffMeta + 32;     // [8] the same for an item of codes
+  static constexpr int kOffFac = kOffRawMeta + 32;      // [NS][128] the query rows' factors
+  static constexpr int kOffTmem = kOffFac + NS * kSharedTile * 4;
   static constexpr int kSmem = 1024 + kOffTmem + 16;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -82,6 +88,13 @@ template <class C>
 __device__ __forceinline__ constexpr uint32_t sh_idesc(int N, bool b_mn) {
   return (1u << 4) | (C::kBf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(kSharedTile >> 4) << 24);
+}
+
+// A whole warp's wait.  Its lanes go on together: one that fell behind, and that
+// nothing else waits for, could otherwise look for a phase when the next but one
+// has already come, which has the same parity.
+__device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
 __device__ __forceinline__ float sh_ex2(float x) {
@@ -105,58 +118,53 @@ struct ShSegment {
   SharedGroup g;
   int kvh, pair, w;  // w: tiles of the list
   int i0, i1;
-  long long unit;  // of the list's first chunk
 };
 
 __device__ __forceinline__ SharedGroup sh_group(const SharedGroup* plan, int g) {
   SharedGroup r;
   const int4* src = reinterpret_cast<const int4*>(plan + g);
   const int4 a = __ldcg(src), b = __ldcg(src + 1);
-  r.unit0 = (long long)(uint32_t)a.x | ((long long)a.y << 32);
-  r.eff = a.z; r.s0 = a.w; r.row0 = b.x; r.R = b.y; r.chunks = b.z; r.tiles = b.w;
+  r.unit0 = a.x; r.eff = a.y; r.s0 = a.z; r.row0 = a.w; r.R = b.x; r.chunks = b.y; r.tiles = b.z;
   return r;
 }
 
-// CTA that has unit u of U, of G CTAs.
-__device__ __forceinline__ int sh_owner(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
+// CTA that has unit u of U, of G CTAs: the run of CTA c begins with unit U c / G.
+__device__ __forceinline__ int sh_owner(int u, int U, int G) {
+  return (int)((((unsigned long long)u + 1) * G - 1) / (unsigned)U);
+}
 
 template <int NS>
 struct ShRun {
   const SharedGroup* plan;
-  int n_groups, n_kv;
-  long long u, hi;  // the next unit, the end of the CTA's
-  int gi;           // group that u is in
-  __device__ __forceinline__ ShRun(const SharedParams& p, int cta) : plan(p.plan), n_groups(p.n_groups), n_kv(p.a.n_kv_heads) {
-    const SharedGroup end = sh_group(plan, n_groups);
-    u = hi = 0;
-    gi = -1;
-    if (cta >= end.eff || end.unit0 == 0) return;
-    u = end.unit0 * cta / end.eff;
-    hi = end.unit0 * (cta + 1) / end.eff;
-    int lo = 0, top = n_groups;
-    while (top - lo > 1) {
-      const int mid = (lo + top) >> 1;
-      if (__ldcg(&plan[mid].unit0) <= u) lo = mid; else top = mid;
-    }
-    gi = lo;
+  int n_kv;
+  int u, hi;  // the next unit, the end of the CTA's
+  int gi;     // group that u is in
+  SharedGroup g;
+  __device__ __forceinline__ ShRun(const SharedParams& p, int cta) : plan(p.plan), n_kv(p.a.n_kv_heads) {
+    const int2 a = __ldcg(p.begin + cta), b = __ldcg(p.begin + cta + 1);
+    u = a.x;
+    gi = a.y;
+    hi = b.x;
+    if (u < hi) g = sh_group(plan, gi);
   }
   __device__ __forceinline__ bool next(ShSegment& s) {
     while (u < hi) {
-      s.g = sh_group(plan, gi);
-      const long long per = (long long)s.g.chunks * s.g.tiles, at = u - s.g.unit0;
+      const int per = g.chunks * g.tiles, at = u - g.unit0;
       if (at >= per * n_kv) {
-        ++gi;
+        g = sh_group(plan, ++gi);
         continue;
       }
-      s.kvh = (int)(at / per);
-      const long long in = at - s.kvh * per;
-      s.pair = (int)(in / ((long long)s.g.chunks * NS));
-      s.w = min(NS, s.g.tiles - s.pair * NS);
-      s.unit = s.g.unit0 + s.kvh * per + (long long)s.pair * NS * s.g.chunks;
-      s.i0 = (int)((u - s.unit + s.w - 1) / s.w);
-      s.i1 = (int)min((long long)s.g.chunks, (hi - s.unit + s.w - 1) / s.w);
-      const bool rest = s.i1 == s.g.chunks;
-      u = rest ? s.unit + (long long)s.g.chunks * s.w : hi;
+      s.g = g;
+      s.kvh = at / per;
+      const int in = at - s.kvh * per;
+      s.pair = in / (g.chunks * NS);
+      s.w = min(NS, g.tiles - s.pair * NS);
+      const int unit = g.unit0 + s.kvh * per + s.pair * NS * g.chunks;
+      const bool two = s.w == 2;
+      s.i0 = two ? (u - unit + 1) >> 1 : u - unit;
+      s.i1 = min(g.chunks, two ? (hi - unit + 1) >> 1 : hi - unit);
+      const bool rest = s.i1 == g.chunks;
+      u = rest ? unit + g.chunks * s.w : hi;
       if (s.i1 > s.i0) return true;
     }
     return false;
@@ -202,8 +210,9 @@ struct ShSmem {
   __device__ __forceinline__ uint8_t* raw(int s) const { return base + C::kOffRaw + s * C::kRawBytes; }
   __device__ __forceinline__ uint8_t* exps(int s) const { return base + C::kOffExp + s * 2 * C::CP; }
   __device__ __forceinline__ float* scale(int s) const { return reinterpret_cast<float*>(base + C::kOffScale) + s * 3 * C::CP; }
-  __device__ __forceinline__ volatile int* mask() const { return reinterpret_cast<int*>(base + C::kOffMask); }
-  __device__ __forceinline__ volatile int* raw_mask() const { return reinterpret_cast<int*>(base + C::kOffRawMask); }
+  __device__ __forceinline__ volatile uint32_t* meta() const { return reinterpret_cast<uint32_t*>(base + C::kOffMeta); }
+  __device__ __forceinline__ volatile uint32_t* raw_meta() const { return reinterpret_cast<uint32_t*>(base + C::kOffRawMeta); }
+  __device__ __forceinline__ float* fac(int x) const { return reinterpret_cast<float*>(base + C::kOffFac) + x * kSharedTile; }
   __device__ __forceinline__ uint32_t* tmem() const { return reinterpret_cast<uint32_t*>(base + C::kOffTmem); }
   // barriers
   __device__ __forceinline__ uint64_t* op_full(int s) const { return bar + s; }
@@ -219,202 +228,303 @@ struct ShSmem {
   __device__ __forceinline__ uint64_t* drain() const { return rest(8); }
 };
 
+// What a chunk holds: the pages that are there (bits 0-7); whether it is even (bit
+// 8): over an 8-bit cache the exponents of its keys lie within 15 of one another,
+// and those of its values within 7, so that f16 holds the codes exactly times
+// 2^(exponent - largest); whether it is plain: even, and all pages there; then the largest
+// exponents (bytes, bits 16 and 24).
+constexpr uint32_t kShEven = 256u, kShPlain = 512u;
+__device__ __forceinline__ float sh_meta_key(uint32_t m) { return __uint_as_float(((m >> 16) & 255u) << 23); }
+__device__ __forceinline__ float sh_meta_value(uint32_t m) { return (float)((int)(m >> 24) - 127); }
+
 // ------------------------------------------------------------------ loads
-// One warp.  Lane l < kPages looks up page l of a chunk and asks for its part of
-// the operand: boxes of a bf16 page straight into the operand's layout (a page that is not there reads as
-// zeros: a row beyond the tensor), or an 8-bit page's codes and exponents.
+// The operands of a CTA's run in the order of their loads.
 template <class C>
-__device__ bool sh_load(const SharedParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap, const ShSmem<C>& sm) {
-  const int lane = threadIdx.x & 31;
-  ShRun<C::NS> run(p, blockIdx.x);
+struct ShItems {
+  ShRun<C::NS> run;
   ShSegment s;
-  uint32_t at = 0, chunk_no = 0;  // operands, and chunks, so far
-  bool ok = true;
-  while (ok && run.next(s)) {
-    const int* table = p.a.rows.table + (size_t)s.g.s0 * p.a.rows.table_stride;
-    const ShOrder ord{s.i1 - s.i0, s.w == 2};
-    for (int i = 0; i < 2 * ord.n && ok; ++i, ++at) {
-      bool is_v;
-      const int c = ord.item(i, is_v);
-      const int pos = (s.i0 + c) * C::CP + lane * kPage;
-      int page = -1;
-      if (lane < C::kPages && pos < s.g.eff) {
-        page = __ldg(table + pos / kPage);
-        if ((uint32_t)page >= (uint32_t)p.a.n_pages) {
-          if (p.a.status && !is_v) atomicOr(p.a.status, ST_BAD_PAGE);
-          page = -1;
-        }
-      }
-      const int there = (int)__ballot_sync(0xffffffffu, page >= 0);
-      if constexpr (C::kBf16) {
-        const int st = at % C::kOps;
-        if (at >= C::kOps && !mbar_wait(sm.op_empty(st), ((at / C::kOps) & 1u) ^ 1u)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          if (!is_v) sm.mask()[(chunk_no + c) & 7] = there;
-          mbar_arrive_expect_tx(sm.op_full(st), C::kOpBytes);
-        }
-        __syncwarp();
-        if (lane < C::kPages) {
-          const int64_t row = page >= 0 ? ((int64_t)page * p.a.n_kv_heads + s.kvh) * kPage : (int64_t)p.a.n_pages * p.a.n_kv_heads * kPage;
-          const uint64_t pol = policy_evict_last();
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_2d(sm.op(st) + h * C::CP * 128 + lane * kPage * 128, is_v ? vmap : kmap, h * 64, (int)row, sm.op_full(st), pol);
-        }
-      } else {
-        const int st = at % C::kRaws;
-        uint4 ke = make_uint4(0u, 0u, 0u, 0u), ve = ke;
-        const size_t ph = page >= 0 ? (size_t)page * p.a.n_kv_heads + s.kvh : 0;
-        if (page >= 0 && !is_v) {  // (the scores need both)
-          if (p.a.block == 1) {
-            ke = __ldg(reinterpret_cast<const uint4*>(p.a.k_exp) + ph);
-            ve = __ldg(reinterpret_cast<const uint4*>(p.a.v_exp) + ph);
-          } else {
-            const uint32_t a = __ldg(p.a.k_exp + ph) * 0x01010101u, b = __ldg(p.a.v_exp + ph) * 0x01010101u;
-            ke = make_uint4(a, a, a, a);
-            ve = make_uint4(b, b, b, b);
-          }
-        }
-        if (at >= C::kRaws && !mbar_wait(sm.raw_empty(st), ((at / C::kRaws) & 1u) ^ 1u)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (!is_v && lane < C::kPages) {
-          reinterpret_cast<uint4*>(sm.exps(st))[lane] = ke;
-          reinterpret_cast<uint4*>(sm.exps(st) + C::CP)[lane] = ve;
-        }
-        if (lane == 0) sm.raw_mask()[st] = there;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(sm.raw_full(st), (uint32_t)__popc(there) * kPage * C::D);
-        __syncwarp();
-        if (page >= 0)
-          bulk_load(sm.raw(st) + lane * kPage * C::D, (is_v ? p.a.v : p.a.k) + ph * kPage * C::D, kPage * C::D, sm.raw_full(st));
-      }
-    }
-    chunk_no += ord.n;
+  ShOrder ord;
+  int i;
+  uint32_t at;                // the item's number
+  uint32_t chunk_no, chunk0;  // chunks before the segment; number of the item's chunk
+  int c;                      // the item's chunk within its segment
+  bool is_v, more;
+  __device__ __forceinline__ ShItems(const SharedParams& p) : run(p, blockIdx.x), ord{0, false}, i(0), at(0), chunk_no(0) {
+    more = run.next(s);
+    if (more) ord = {s.i1 - s.i0, s.w == 2};
+    look();
   }
-  // copies in flight have landed before the CTA goes on
-  __syncwarp();
-  constexpr uint32_t kRing = C::kBf16 ? C::kOps : C::kRaws;
-  if (lane == 0)
-    for (uint32_t k = at > kRing ? at - kRing : 0; k < at; ++k) {
-      if (!mbar_wait(C::kBf16 ? sm.op_full(k % kRing) : sm.raw_full(k % kRing), (k / kRing) & 1u)) break;
+  __device__ __forceinline__ void look() {
+    if (!more) return;
+    c = ord.item(i, is_v);
+    chunk0 = chunk_no + c;
+  }
+  __device__ __forceinline__ void step() {
+    ++at;
+    if (++i == 2 * ord.n) {
+      chunk_no += ord.n;
+      i = 0;
+      more = run.next(s);
+      if (more) ord = {s.i1 - s.i0, s.w == 2};
     }
+    look();
+  }
+};
+
+// A warp for K and one for V.  Lane l < kPages looks up page l of a chunk; its part
+// of the operand: boxes of a bf16 page straight into the operand's layout (a page
+// that is not there reads as zeros: a row beyond the tensor), or an 8-bit page's
+// codes.  Page numbers are looked up two operands ahead, exponents one.
+template <class C, bool kValues>
+__device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShSmem<C>& sm, uint32_t& end) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t lead = tc_elect();
+  ShItems<C> it(p);
+  struct Item {
+    int page, kvh;
+    bool there, wanted;  // there: an item at all; wanted: with a page for this lane
+    uint32_t at, chunk;
+  };
+  auto look = [&]() {
+    while (it.more && it.is_v != kValues) it.step();
+    Item r = {-1, 0, it.more, false, it.at, 0};
+    if (!it.more) return r;
+    const int pos = (it.s.i0 + it.c) * C::CP + lane * kPage;
+    r.wanted = lane < C::kPages && pos < it.s.g.eff;
+    if (r.wanted) r.page = __ldg(p.a.rows.table + (size_t)it.s.g.s0 * p.a.rows.table_stride + pos / kPage);
+    r.kvh = it.s.kvh;
+    r.chunk = it.chunk0;
+    it.step();
+    return r;
+  };
+  uint4 ke = make_uint4(0u, 0u, 0u, 0u), ve = ke;
+  auto exponents = [&](const Item& x, uint4& k, uint4& v) {
+    k = v = make_uint4(0u, 0u, 0u, 0u);
+    if (C::kBf16 || (uint32_t)x.page >= (uint32_t)p.a.n_pages) return;
+    const size_t ph = (size_t)x.page * p.a.n_kv_heads + x.kvh;
+    if (p.a.block == 1) {
+      k = __ldg(reinterpret_cast<const uint4*>(p.a.k_exp) + ph);
+      v = __ldg(reinterpret_cast<const uint4*>(p.a.v_exp) + ph);
+    } else {
+      const uint32_t a = __ldg(p.a.k_exp + ph) * 0x01010101u, b = __ldg(p.a.v_exp + ph) * 0x01010101u;
+      k = make_uint4(a, a, a, a);
+      v = make_uint4(b, b, b, b);
+    }
+  };
+  Item now = look(), next = look();
+  exponents(now, ke, ve);
+  bool ok = true;
+  constexpr uint32_t kRing = C::kBf16 ? C::kOps : C::kRaws;
+  const uint64_t pol = policy_evict_last();
+  end = 0;  // behind the last operand asked for
+  while (now.there) {
+    const Item far = look();
+    uint4 ke1, ve1;
+    exponents(next, ke1, ve1);
+    const uint32_t at = now.at;
+    const int st = at % kRing;
+    ok = at < kRing || sh_wait(C::kBf16 ? sm.op_empty(st) : sm.raw_empty(st), ((at / kRing) & 1u) ^ 1u);
+    if (!ok) break;
+    end = at + 1;
+    const bool have = (uint32_t)now.page < (uint32_t)p.a.n_pages;
+    if (!kValues && !have && now.wanted && p.a.status) atomicOr(p.a.status, ST_BAD_PAGE);
+    const uint32_t there = __ballot_sync(0xffffffffu, have);
+    uint32_t meta = there | kShEven;
+    const uint32_t plain = there == (1u << C::kPages) - 1u ? kShPlain : 0u;
+    // (row of the pool's positions; none beyond the last)
+    const int row = have ? (now.page * p.a.n_kv_heads + now.kvh) * kPage : p.a.n_pages * p.a.n_kv_heads * kPage;
+    if constexpr (C::kBf16) {
+      if (lead) {
+        if (!kValues) sm.meta()[now.chunk & 7] = meta | plain;
+        mbar_arrive_expect_tx(sm.op_full(st), C::kOpBytes);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int pg = 0; pg < C::kPages; ++pg) {
+        const int r = __shfl_sync(0xffffffffu, row, pg);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          if (lead) tma_load_2d(sm.op(st) + h * C::CP * 128 + pg * kPage * 128, map, h * 64, r, sm.op_full(st), pol);
+      }
+    } else {
+      // (bytes below the writer's smallest, as a zeroed cache has, count as that one for values)
+      const uint32_t least = kExpMinByte * 0x01010101u;
+      ve = make_uint4(__vmaxu4(ve.x, least), __vmaxu4(ve.y, least), __vmaxu4(ve.z, least), __vmaxu4(ve.w, least));
+      auto top = [](const uint4& e) {
+        const uint32_t m = __vmaxu4(__vmaxu4(e.x, e.y), __vmaxu4(e.z, e.w)), h = __vmaxu4(m, m >> 16);
+        return max(h & 255u, (h >> 8) & 255u);
+      };
+      auto low = [](const uint4& e) {
+        const uint32_t m = __vminu4(__vminu4(e.x, e.y), __vminu4(e.z, e.w)), h = __vminu4(m, (m >> 16) | (m << 16));
+        return min(h & 255u, (h >> 8) & 255u);
+      };
+      const uint32_t kt = __reduce_max_sync(0xffffffffu, have ? top(ke) : 0u), kl = __reduce_min_sync(0xffffffffu, have ? low(ke) : 255u);
+      const uint32_t vt = __reduce_max_sync(0xffffffffu, have ? top(ve) : 0u), vl = __reduce_min_sync(0xffffffffu, have ? low(ve) : 255u);
+      if (kt == kExpNaN || vt == kExpNaN || kt > kl + kShKeySpread || vt > vl + kShValueSpread) meta &= ~kShEven;
+      meta |= (kt << 16) | (vt << 24) | (meta & kShEven ? plain : 0u);
+      if (lane < C::kPages) {
+        if (!kValues) reinterpret_cast<uint4*>(sm.exps(st))[lane] = ke;
+        reinterpret_cast<uint4*>(sm.exps(st) + C::CP)[lane] = ve;
+      }
+      if (lead) sm.raw_meta()[st] = meta;
+      __syncwarp();
+      if (lead) mbar_arrive_expect_tx(sm.raw_full(st), (uint32_t)__popc(there) * kPage * C::D);
+      __syncwarp();
+      const uint8_t* pool = kValues ? p.a.v : p.a.k;
+#pragma unroll 1
+      for (int pg = 0; pg < C::kPages; ++pg) {
+        const int r = __shfl_sync(0xffffffffu, row, pg);
+        if (lead && (there >> pg & 1u))
+          bulk_load(sm.raw(st) + pg * kPage * C::D, pool + (size_t)r * C::D, kPage * C::D, sm.raw_full(st));
+      }
+    }
+    now = next;
+    next = far;
+    ke = ke1;
+    ve = ve1;
+  }
   return ok;
 }
 
+// After a failure: the last copies asked for have landed, or the waits for them run
+// out.  (A place that the other warp has used again since is waited for in vain.)
+template <class C>
+__device__ void sh_load_drain(const ShSmem<C>& sm, uint32_t end) {
+  constexpr uint32_t kRing = C::kBf16 ? C::kOps : C::kRaws;
+  for (uint32_t k = end > kRing ? end - kRing : 0; k < end; ++k)
+    sh_wait(C::kBf16 ? sm.op_full(k % kRing) : sm.raw_full(k % kRing), (k / kRing) & 1u);
+}
+
 // ------------------------------------------------------------------ 8-bit codes to f16 operands
+// Four warps.  An even chunk's codes are scaled to its largest exponents; of
+// another the codes go as they are, and the scores take the exponents (sm.scale).
 template <class C>
 __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
   const int tid = threadIdx.x & 127;
-  ShRun<C::NS> run(p, blockIdx.x);
-  ShSegment s;
-  uint32_t at = 0, chunk_no = 0;
-  while (run.next(s)) {
-    const ShOrder ord{s.i1 - s.i0, s.w == 2};
-    for (int i = 0; i < 2 * ord.n; ++i, ++at) {
-      bool is_v;
-      const uint32_t c = chunk_no + ord.item(i, is_v);
-      const int st = at % C::kRaws, os = at % C::kOps;
-      if (!mbar_wait(sm.raw_full(st), (at / C::kRaws) & 1u)) return false;
-      if (at >= C::kOps && !mbar_wait(sm.op_empty(os), ((at / C::kOps) & 1u) ^ 1u)) return false;
-      const int there = sm.raw_mask()[st];
-      if (!is_v) {
-        const int ring = c % C::kRings;
-        if (c >= C::kRings && !mbar_wait(sm.sc_empty(ring), ((c / C::kRings) & 1u) ^ 1u)) return false;
-        if (tid < C::CP) {
-          // (bytes below the writer's smallest, as a zeroed cache has, count as that one; 255: NaN)
-          const uint32_t bk = sm.exps(st)[tid], bv = max((uint32_t)sm.exps(st)[C::CP + tid], (uint32_t)kExpMinByte);
-          float* f = sm.scale(ring);
-          f[tid] = exp_byte_value(bk);
-          f[C::CP + tid] = bv == kExpNaN ? exp_byte_value(bv) : (float)((int)bv - 127);
-          f[2 * C::CP + tid] = __uint_as_float((254u - min(bv, 254u)) << 23);
-        }
-        if (tid == 0) sm.mask()[c & 7] = there;
+  for (ShItems<C> it(p); it.more; it.step()) {
+    const uint32_t c = it.chunk0, at = it.at;
+    const int st = at % C::kRaws, os = at % C::kOps;
+    if (!sh_wait(sm.raw_full(st), (at / C::kRaws) & 1u)) return false;
+    if (at >= C::kOps && !sh_wait(sm.op_empty(os), ((at / C::kOps) & 1u) ^ 1u)) return false;
+    const uint32_t meta = sm.raw_meta()[st];
+    const bool even = meta & kShEven;
+    const uint8_t* exps = sm.exps(st) + (it.is_v ? C::CP : 0);
+    const int most = it.is_v ? meta >> 24 : (meta >> 16) & 255;
+    if (!it.is_v) {
+      const int ring = c % C::kRings;
+      if (c >= C::kRings && !sh_wait(sm.sc_empty(ring), ((c / C::kRings) & 1u) ^ 1u)) return false;
+      if (!even && tid < C::CP) {
+        const uint32_t bk = sm.exps(st)[tid], bv = sm.exps(st)[C::CP + tid];
+        float* f = sm.scale(ring);
+        f[tid] = exp_byte_value(bk);
+        f[C::CP + tid] = bv == kExpNaN ? exp_byte_value(bv) : (float)((int)bv - 127);
+        f[2 * C::CP + tid] = __uint_as_float((254u - min(bv, 254u)) << 23);
       }
-      const uint8_t* raw = sm.raw(st);
-      const uint32_t dst = smem_u32(sm.op(os));
-      constexpr int kUnits = C::CP * C::D / 16, kRow = C::D / 16;  // 16 codes each; of a position
-#pragma unroll
-      for (int k = 0; k < kUnits / 128; ++k) {
-        const int u = tid + k * 128, pos = u / kRow, c16 = u % kRow;
-        uint4 w = *reinterpret_cast<const uint4*>(raw + u * 16);
-        if (!((there >> (pos / kPage)) & 1)) w = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        const uint32_t half = dst + (c16 >> 2) * C::CP * 128 + pos * 128;
-        // a quarter warp's lanes write eight different 16-byte places of a 128-byte row
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int second = C::D == 64 ? e : e ^ ((c16 >> 2) & 1), unit = 2 * (c16 & 3) + second;
-          const uint32_t a = second ? x[2] : x[0], b = second ? x[3] : x[1];
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + ((unit ^ (pos & 7)) << 4)), "r"(f16x2_of_lo(a)),
-                       "r"(f16x2_of_hi(a)), "r"(f16x2_of_lo(b)), "r"(f16x2_of_hi(b))
-                       : "memory");
-        }
-      }
-      fence_proxy_async_smem();  // the multiplies read the operand through the async proxy, and copies overwrite the codes
-      mbar_arrive(sm.op_full(os));
-      mbar_arrive(sm.raw_empty(st));
+      if (tid == 0) sm.meta()[c & 7] = meta;
     }
-    chunk_no += ord.n;
+    // A thread has a position (half of one, two of them), which has one exponent, in
+    // units of 16 codes.  Lanes begin with different units: the eight of a quarter
+    // warp then read eight different 16-byte columns and (128 codes) write eight.
+    constexpr int kThreadsRow = 128 / C::CP > 1 ? 128 / C::CP : 1, kRowUnits = C::D / 16, kMine = kRowUnits / kThreadsRow;
+    const int pos = tid / kThreadsRow, u0 = tid % kThreadsRow * kMine;
+    const uint8_t* raw = sm.raw(st) + pos * C::D;
+    const uint32_t dst = smem_u32(sm.op(os)) + pos * 128;
+    const bool have = (meta >> (pos / kPage)) & 1u;
+    uint32_t by = 0x3c003c00u;  // 1, or 2^(the position's exponent - the largest): at least 2^-15
+    if (have && even) {
+      const int e = exps[pos] - most;
+      by = (e > -15 ? (uint32_t)(15 + e) << 10 : 0x0200u) * 0x00010001u;
+    }
+    auto scaled = [&](uint32_t h) {
+      uint32_t r;
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(by));
+      return r;
+    };
+#pragma unroll
+    for (int k0 = 0; k0 < kMine; k0 += 4) {
+      uint4 w[4];
+      int unit[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        unit[k] = u0 + ((k0 + k + (C::D == 64 ? tid >> 1 : tid)) & (kMine - 1));
+        w[k] = *reinterpret_cast<const uint4*>(raw + unit[k] * 16);
+        if (!have) w[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t half = dst + (unit[k] >> 2) * C::CP * 128, col = 2 * (unit[k] & 3);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + ((col ^ (pos & 7)) << 4)), "r"(scaled(f16x2_of_lo(w[k].x))),
+                     "r"(scaled(f16x2_of_hi(w[k].x))), "r"(scaled(f16x2_of_lo(w[k].y))), "r"(scaled(f16x2_of_hi(w[k].y)))
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + (((col + 1) ^ (pos & 7)) << 4)), "r"(scaled(f16x2_of_lo(w[k].z))),
+                     "r"(scaled(f16x2_of_hi(w[k].z))), "r"(scaled(f16x2_of_lo(w[k].w))), "r"(scaled(f16x2_of_hi(w[k].w)))
+                     : "memory");
+      }
+    }
+    fence_proxy_async_smem();  // the multiplies read the operand through the async proxy, and copies overwrite the codes
+    mbar_arrive(sm.op_full(os));
+    mbar_arrive(sm.raw_empty(st));
   }
   return true;
 }
 
 // ------------------------------------------------------------------ multiplies
+// One warp, of which one lane issues.
 template <class C>
 __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t tmem) {
   constexpr int CP = C::CP, D = C::D;
   constexpr uint32_t kScores = sh_idesc<C>(CP, false), kValues = sh_idesc<C>(D, true);
+  const uint32_t lead = tc_elect();
+  tmem = __shfl_sync(0xffffffffu, tmem, 0);
   ShRun<C::NS> run(p, blockIdx.x);
   ShSegment s;
-  uint32_t at0 = 0, step0 = 0, seg = 0;
+  uint32_t at0 = 0, seg = 0;
   bool ok = true;
   uint32_t used[2] = {0, 0};  // uses of each score place so far
+  const uint32_t q_base = smem_u32(sm.q(0)), op_base = smem_u32(sm.op(0));
   while (ok && run.next(s)) {
     const ShOrder ord{s.i1 - s.i0, s.w == 2};
     const int n = ord.steps();
     auto scores = [&](int j) {
       const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
       const uint32_t at = at0 + ord.k_at(c);
-      if (j < C::NS && !mbar_wait(sm.q_full(stream), seg & 1u)) return false;
-      if (!mbar_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u)) return false;
+      if (j < C::NS && !sh_wait(sm.q_full(stream), seg & 1u)) return false;
+      if (!sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u)) return false;
       tc_fence_after();
-      const uint32_t a = smem_u32(sm.q(stream)), b = smem_u32(sm.op(at % C::kOps));
+      const uint64_t a = tc_sdesc(q_base + stream * C::kQBytes), b = tc_sdesc(op_base + at % C::kOps * C::kOpBytes);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        tc_mma(tmem + x * C::kScoreCol, tc_sdesc(a + (k / 4) * kSharedTile * 128 + (k % 4) * 32),
-               tc_sdesc(b + (k / 4) * CP * 128 + (k % 4) * 32), kScores, k > 0);
-      tc_commit(sm.s_full(x));
-      if (!ord.both || x == 1) tc_commit(sm.op_empty(at % C::kOps));
+        tc_mma_if(lead, tmem + x * C::kScoreCol, a + (((k / 4) * kSharedTile * 128 + (k % 4) * 32) >> 4),
+                  b + (((k / 4) * CP * 128 + (k % 4) * 32) >> 4), kScores, k > 0);
+      tc_commit_if(lead, sm.s_full(x));
+      if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
       return true;
     };
     ok = scores(0) && (n < 2 || scores(1));
     for (int j = 0; j < n && ok; ++j) {
       const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
       const uint32_t at = at0 + ord.v_at(c);
-      ok = mbar_wait(sm.p_full(x), used[x] & 1u) && mbar_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u);
+      ok = sh_wait(sm.p_full(x), used[x] & 1u) && sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u);
       if (!ok) break;
       ++used[x];
       tc_fence_after();
-      const uint32_t b = smem_u32(sm.op(at % C::kOps)), o = tmem + C::kOutCol + stream * D, w = tmem + x * C::kScoreCol;
+      const uint64_t b = tc_sdesc_mn(op_base + at % C::kOps * C::kOpBytes, CP * 128);
+      const uint32_t o = tmem + C::kOutCol + stream * D, w = tmem + x * C::kScoreCol;
 #pragma unroll
       for (int t = 0; t < (C::kBf16 ? 2 : 1); ++t)
 #pragma unroll
         for (int k = 0; k < CP / 16; ++k)
-          tc_mma_ts(o, w + t * (CP / 2) + k * 8, tc_sdesc_mn(b + k * 16 * 128, CP * 128), kValues, j >= C::NS || t > 0 || k > 0);
-      tc_commit(sm.pv_done(x));
-      if (!ord.both || x == 1) tc_commit(sm.op_empty(at % C::kOps));
+          tc_mma_ts_if(lead, o, w + t * (CP / 2) + k * 8, b + (k * 16 * 128 >> 4), kValues, j >= C::NS || t > 0 || k > 0);
+      tc_commit_if(lead, sm.pv_done(x));
+      if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
       if (j + 2 < n) ok = scores(j + 2);
     }
     at0 += 2 * ord.n;
-    step0 += n;
     ++seg;
   }
   // every multiply has completed before tensor memory is freed
-  tc_commit(sm.drain());
-  if (!mbar_wait(sm.drain(), 0)) ok = false;
+  tc_commit_if(lead, sm.drain());
+  if (!sh_wait(sm.drain(), 0)) ok = false;
   return ok;
 }
 
@@ -429,170 +539,211 @@ struct ShSoft {
   const uint32_t lane_off;  // the warp's lanes of tensor memory
   const uint32_t tmem;
   float ref, l, fac;
+  uint32_t most;               // largest value exponent (byte) of the segment's plain chunks so far
   uint32_t steps[2] = {0, 0};  // steps of each score place so far
 
   __device__ __forceinline__ ShSoft(const SharedParams& p_, const ShSmem<C>& sm_, uint32_t tm)
       : p(p_), sm(sm_), x(threadIdx.x >> 7), r(threadIdx.x & 127), lane_off((uint32_t)(threadIdx.x & 96) << 16), tmem(tm) {}
 
-  // The row's queries, as an operand of 64-column halves with 128-byte swizzled rows.
+  __device__ __forceinline__ void open() {
+    ref = kShNone;
+    l = 0.0f;
+    most = 0;
+  }
+
+  // The tile's queries, as an operand of 64-column halves with 128-byte swizzled
+  // rows; D / 8 lanes load a row.  Their factor is positive (the sign goes to the
+  // queries), so that the largest product is the largest score.
   __device__ __forceinline__ void queries(const ShSegment& s, int tile, int G) {
-    const int f = tile * kSharedTile + r;
-    const bool there = f < s.g.R;
-    const bf16* row = there ? p.a.q + (int64_t)(s.g.row0 + f / G) * p.a.q_stride + (s.kvh * G + f % G) * D : p.a.q;
-    const uint32_t dst = smem_u32(sm.q(x)) + r * 128;
-    const uint32_t zero = 0u;
-    float down = 1.0f;
-    fac = p.a.scale_log2;
-    uint32_t flip = 0u;
-    if (C::kBf16) {  // (a positive factor, so that the largest score is the largest product)
-      if (fac < 0.0f) flip = 0x80008000u;
-      fac = fmaxf(fabsf(fac), 0x1p-126f);  // (and not zero: a score of -infinity stays one)
-    } else {
-      uint32_t m = 0;
-#pragma unroll 4
-      for (int u = 0; u < D / 8; ++u) {
-        const uint4 w = there ? __ldg(reinterpret_cast<const uint4*>(row) + u) : make_uint4(zero, zero, zero, zero);
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+    constexpr int U = D / 8, kLoads = U < 16 ? U : 16;  // lanes of a row; loads at a time
+    const uint32_t flip = p.a.scale_log2 < 0.0f ? 0x80008000u : 0u, dst = smem_u32(sm.q(x));
+    const float scale = fmaxf(fabsf(p.a.scale_log2), 0x1p-126f);  // (and not zero: a score of -infinity stays one)
+#pragma unroll 1
+    for (int i0 = 0; i0 < U; i0 += kLoads) {
+      uint4 w[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int idx = (i0 + i) * 128 + r, f = tile * kSharedTile + idx / U;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (f < s.g.R)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(p.a.q + (int64_t)(s.g.row0 + f / G) * p.a.q_stride + (s.kvh * G + f % G) * D) + idx % U);
       }
-      m = max(m & 0xffffu, m >> 16);
-      // the row's largest exponent E: q / 2^(E - 127) is below 2 (an infinity or NaN makes the row NaN)
-      const int E = min(max((int)(m >> 7), 1), 253);
-      down = __uint_as_float((uint32_t)(254 - E) << 23);
-      fac = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __fmul_rn(fac, __uint_as_float((uint32_t)E << 23));
-    }
-#pragma unroll 4
-    for (int u = 0; u < D / 8; ++u) {
-      uint4 w = there ? __ldg(reinterpret_cast<const uint4*>(row) + u) : make_uint4(zero, zero, zero, zero);
-      if (C::kBf16) {
-        w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
-      } else {
-        auto two = [&](uint32_t v) {
-          return sh_f16x2(__fmul_rn(__uint_as_float(v << 16), down), __fmul_rn(__uint_as_float(v & 0xffff0000u), down));
-        };
-        w = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int idx = (i0 + i) * 128 + r, row = idx / U, u = idx % U;
+        uint4 v = w[i];
+        float fr = scale;
+        if (!C::kBf16) {
+          uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+          for (int o = 1; o < U; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // the row's largest exponent E: q / 2^(E - 127) is below 2 (an infinity or NaN makes the row NaN)
+          const int E = min(max((int)(m >> 7), 1), 253);
+          const float down = __uint_as_float((uint32_t)(254 - E) << 23);
+          fr = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __fmul_rn(scale, __uint_as_float((uint32_t)E << 23));
+          auto two = [&](uint32_t a) {
+            return sh_f16x2(__fmul_rn(__uint_as_float(a << 16), down), __fmul_rn(__uint_as_float(a & 0xffff0000u), down));
+          };
+          v = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+        }
+        if (u == 0) sm.fac(x)[row] = fr;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (u >> 3) * kSharedTile * 128 + row * 128 + (((u & 7) ^ (row & 7)) << 4)),
+                     "r"(v.x ^ flip), "r"(v.y ^ flip), "r"(v.z ^ flip), "r"(v.w ^ flip)
+                     : "memory");
       }
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (u >> 3) * kSharedTile * 128 + (((u & 7) ^ (r & 7)) << 4)),
-                   "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                   : "memory");
     }
     fence_proxy_async_smem();
     mbar_arrive(sm.q_full(x));
-    ref = kShNone;
-    l = 0.0f;
+    named_sync(1 + x, 128);  // the factors
+    fac = sm.fac(x)[r];
+    open();
   }
 
-  // Step j of the segment, on score place y: scores to weights.  no: the chunk's number in the call.
-  __device__ __forceinline__ bool step(int j, int y, uint32_t no, bool both) {
-    if (!mbar_wait(sm.s_full(y), steps[y] & 1u)) return false;
+  __device__ __forceinline__ uint32_t scores_at(int y) const { return tmem + lane_off + y * C::kScoreCol; }
+
+  // The reference follows a row's largest score `top` of step j where it has risen by more than the slack.
+  __device__ __forceinline__ bool follow(float top, int j, int y) {
+    constexpr float kBias = sh_bias(C::kBf16);
+    const bool up = top > __fadd_rn(ref, kShSlack + kBias);
+    if (!__any_sync(0xffffffffu, up)) return true;
+    top = __fsub_rn(top, kBias);
+    const float d = up ? __fsub_rn(ref, top) : 0.0f, a = sh_ex2(d);
+    const bool scaled = up && ref != kShNone;
+    l = sh_times_ex2(l, d);
+    ref = up ? top : ref;
+    if (!__any_sync(0xffffffffu, scaled)) return true;  // (behind a row's first chunk there is nothing to scale)
+    // the product before this step (with two streams it ran before these scores did)
+    if (C::NS == 1 && j > 0 && !sh_wait(sm.pv_done(y ^ 1), (steps[y ^ 1] - 1u) & 1u)) return false;
     tc_fence_after();
-    const uint32_t place = tmem + lane_off + y * C::kScoreCol;
+    const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t v[32];
+      tc_ld32(o + c, v);
+      tc_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a));
+      tc_st32(o + c, v);
+    }
+    tc_wait_st();
+    return true;
+  }
+
+  // Weights of columns c .. c + 31 to where the product reads them.
+  __device__ __forceinline__ void put(uint32_t place, int c, const uint32_t* w) {
+    uint32_t hi[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)  // (a bf16 weight's first term: its upper half)
+      hi[e] = C::kBf16 ? __byte_perm(w[2 * e], w[2 * e + 1], 0x7632)
+                       : sh_f16x2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+    tc_st16(place + c / 2, hi);
+    if (C::kBf16) {  // the second: the rest, rounded
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        hi[e] = pack_bf16x2(__fsub_rn(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e] & 0xffff0000u)),
+                            __fsub_rn(__uint_as_float(w[2 * e + 1]), __uint_as_float(w[2 * e + 1] & 0xffff0000u)));
+      tc_st16(place + CP / 2 + c / 2, hi);
+    }
+  }
+
+  // A plain chunk: t' = s f + ev for all of it.  Weights 2^(t' - ref); the
+  // denominator takes them times 2^-ev, or where values of the segment have
+  // exponents so much larger that a weight may be below fp32's range although its
+  // share of the denominator counts, 2^(s f - ref).
+  __device__ __forceinline__ bool plain(int j, int y, uint32_t meta) {
+    const uint32_t place = scores_at(y);
     uint32_t w[CP / 32][32];
 #pragma unroll
     for (int c = 0; c < CP / 32; ++c) tc_ld32(place + 32 * c, w[c]);
     tc_wait_ld();
-    auto at = [&](int c) -> uint32_t& { return w[c / 32][c % 32]; };
-    const int there = sm.mask()[no & 7];
-    const float* sc = sm.scale(no % C::kRings);
-    // scores in log2 units (a bf16 cache: before the factor), with the value's exponent
-    float top = -INFINITY;
-    if constexpr (!C::kBf16) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < CP; c += 4) {
-        const float4 ks = *reinterpret_cast<const float4*>(sc + c), ev = *reinterpret_cast<const float4*>(sc + CP + c);
-        at(c) = __float_as_uint(__fmaf_rn(__fmul_rn(__uint_as_float(at(c)), fac), ks.x, ev.x));
-        at(c + 1) = __float_as_uint(__fmaf_rn(__fmul_rn(__uint_as_float(at(c + 1)), fac), ks.y, ev.y));
-        at(c + 2) = __float_as_uint(__fmaf_rn(__fmul_rn(__uint_as_float(at(c + 2)), fac), ks.z, ev.z));
-        at(c + 3) = __float_as_uint(__fmaf_rn(__fmul_rn(__uint_as_float(at(c + 3)), fac), ks.w, ev.w));
-      }
-    }
-    if (there != (1 << C::kPages) - 1) {  // pages that are not there
-#pragma unroll
-      for (int c = 0; c < CP; ++c)
-        if (!((there >> (c / kPage)) & 1)) at(c) = 0xff800000u;
-    }
-#pragma unroll
-    for (int c = 0; c < CP; ++c) top = fmaxf(top, __uint_as_float(at(c)));
-    if (C::kBf16) top = __fmul_rn(top, fac);
-    if (__any_sync(0xffffffffu, top > __fadd_rn(ref, kShSlack))) {
-      const bool up = top > __fadd_rn(ref, kShSlack);
-      const float d = up ? __fsub_rn(ref, top) : 0.0f, a = sh_ex2(d);
-      const bool scaled = up && ref != kShNone;
-      l = sh_times_ex2(l, d);
-      ref = up ? top : ref;
-      if (__any_sync(0xffffffffu, scaled)) {
-        // (the product before this step: with two streams it ran before these scores did)
-        if (C::NS == 1 && j > 0 && !mbar_wait(sm.pv_done(y ^ 1), (steps[y ^ 1] - 1u) & 1u)) return false;
-        tc_fence_after();
-        const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
+    for (int c = 0; c < CP; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(w[c / 32][c % 32]));
+    const float f = C::kBf16 ? fac : __fmul_rn(fac, sh_meta_key(meta)), ev = C::kBf16 ? 0.0f : sh_meta_value(meta);
+    if (!follow(__fmaf_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), f, ev), j, y)) return false;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    bool far = false;
+    if (!C::kBf16) {
+      const uint32_t e = meta >> 24;
+      most = max(most, e);
+      far = e + 60u < most;
+      if (far) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < CP; c += 32) {
           uint32_t v[32];
-          tc_ld32(o + c, v);
+          tc_ld32(place + c, v);
           tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), a));
-          tc_st32(o + c, v);
+          for (int i = 0; i < 32; ++i) sum[i & 3] = __fadd_rn(sum[i & 3], sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, -ref)));
         }
-        tc_wait_st();
+        l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])));
       }
     }
-    // weights and their sum
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (C::kBf16) {
+    const float off = __fsub_rn(ev, ref);
 #pragma unroll
-      for (int c = 0; c < CP; ++c) {
-        const float e = sh_ex2(__fmaf_rn(__uint_as_float(at(c)), fac, -ref));
-        sum[c & 3] = __fadd_rn(sum[c & 3], e);
-        at(c) = __float_as_uint(e);
+    for (int c = 0; c < CP / 32; ++c) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float e = sh_ex2(__fmaf_rn(__uint_as_float(w[c][i]), f, off));
+        sum[i & 3] = __fadd_rn(sum[i & 3], e);
+        w[c][i] = __float_as_uint(e);
       }
-#pragma unroll
-      for (int c = 0; c < CP; c += 32) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t a = at(c + 2 * e), b = at(c + 2 * e + 1);
-          // the first term: the value's upper half; the second: the rest, rounded
-          hi[e] = __byte_perm(a, b, 0x7632);
-          lo[e] = pack_bf16x2(__fsub_rn(__uint_as_float(a), __uint_as_float(a & 0xffff0000u)),
-                              __fsub_rn(__uint_as_float(b), __uint_as_float(b & 0xffff0000u)));
-        }
-        tc_st16(place + c / 2, hi);
-        tc_st16(place + CP / 2 + c / 2, lo);
-      }
-    } else {
-      float low = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CP; ++c) {
-        const float z = __fsub_rn(__uint_as_float(at(c)), ref);
-        at(c) = __float_as_uint(z);
-        low = fminf(low, z);
-      }
-      const bool far = __any_sync(0xffffffffu, low < kShFar);
-#pragma unroll
-      for (int c = 0; c < CP; c += 4) {
-        const float4 iv = *reinterpret_cast<const float4*>(sc + 2 * CP + c);
-        const float f[4] = {iv.x, iv.y, iv.z, iv.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float z = __uint_as_float(at(c + e)), v = sh_ex2(z);
-          at(c + e) = __float_as_uint(v);
-          if (far && z < kShFar) {  // p' is below fp32's range, p need not be
-            const float ev = sc[CP + c + e];
-            if (z != -INFINITY) sum[e] = __fadd_rn(sum[e], sh_ex2(__fsub_rn(z, ev)));
-          } else {
-            sum[e] = __fmaf_rn(v, f[e], sum[e]);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < CP; c += 64) {
-        uint32_t h[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) h[e] = sh_f16x2(__uint_as_float(at(c + 2 * e)), __uint_as_float(at(c + 2 * e + 1)));
-        tc_st32(place + c / 2, h);
-      }
+      put(place, 32 * c, w[c]);
     }
-    l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])));
+    const float all = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
+    if (C::kBf16) l = __fadd_rn(l, all);
+    else if (!far) l = __fmaf_rn(all, __uint_as_float((254u - (meta >> 24)) << 23), l);
+    return true;
+  }
+
+  // Any chunk: pages may be missing, exponents differ by position (sc: 2^ek, ev, 2^-ev of each).
+  __device__ __forceinline__ bool uneven(int j, int y, uint32_t meta, const float* sc) {
+    const uint32_t place = scores_at(y);
+    const bool even = C::kBf16 || meta & kShEven;
+    const float ks = C::kBf16 ? 1.0f : sh_meta_key(meta), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
+    const float iv = __uint_as_float((254u - (meta >> 24)) << 23);
+    uint32_t w[CP / 32][32];
+#pragma unroll
+    for (int c = 0; c < CP / 32; ++c) tc_ld32(place + 32 * c, w[c]);
+    tc_wait_ld();
+    // scores in log2 units, with the value's exponent
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {
+      float t = __fmul_rn(__uint_as_float(w[c / 32][c % 32]), fac);
+      if (!C::kBf16) t = even ? __fmaf_rn(t, ks, vs) : __fmaf_rn(t, sc[c], sc[CP + c]);
+      t = (meta >> (c / kPage)) & 1u ? t : -INFINITY;
+      top = fmaxf(top, t);
+      w[c / 32][c % 32] = __float_as_uint(t);
+    }
+    if (!follow(top, j, y)) return false;
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CP / 32; ++c) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float z = __fsub_rn(__uint_as_float(w[c][i]), ref), e = sh_ex2(z);
+        if (C::kBf16)
+          sum = __fadd_rn(sum, e);
+        else if (z < kShFar)  // 2^z is below fp32's range, the position's share of the denominator need not be
+          sum = __fadd_rn(sum, z == -INFINITY ? 0.0f : sh_ex2(__fsub_rn(z, even ? vs : sc[CP + 32 * c + i])));
+        else
+          sum = __fmaf_rn(e, even ? iv : sc[2 * CP + 32 * c + i], sum);
+        w[c][i] = __float_as_uint(e);
+      }
+      put(place, 32 * c, w[c]);
+    }
+    l = __fadd_rn(l, sum);
+    return true;
+  }
+
+  // Step j of the segment, on score place y: scores to weights.  no: the chunk's number in the call.
+  __device__ __forceinline__ bool step(int j, int y, uint32_t no, bool both) {
+    if (!sh_wait(sm.s_full(y), steps[y] & 1u)) return false;
+    tc_fence_after();
+    const uint32_t meta = sm.meta()[no & 7];
+    if (!(meta & kShPlain ? plain(j, y, meta) : uneven(j, y, meta, sm.scale(no % C::kRings)))) return false;
     tc_wait_st();
     tc_fence_before();
     mbar_arrive(sm.p_full(y));
@@ -610,7 +761,7 @@ struct ShSoft {
     const int f = tile * kSharedTile + r;
     const long long at = (long long)x * p.plane + sh_slot(p, s.g, s.kvh, s.pair, C::NS, cta) + r;
     if (n > 0) {
-      if (!mbar_wait(sm.pv_done(y), (steps[y] - 1u) & 1u)) return false;
+      if (!sh_wait(sm.pv_done(y), (steps[y] - 1u) & 1u)) return false;
       tc_fence_after();
       const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
 #pragma unroll 1
@@ -639,7 +790,7 @@ struct ShSoft {
       const ShOrder ord{s.i1 - s.i0, s.w == 2};
       const int n = ord.steps(), tile = s.pair * C::NS + (ord.both ? x : 0);
       if (C::NS == 1 || x < n) queries(s, tile, G);
-      else { ref = kShNone; l = 0.0f; mbar_arrive(sm.q_full(x)); }
+      else { open(); mbar_arrive(sm.q_full(x)); }
       int mine = 0, y = 0;
       for (int j = C::NS == 2 ? x : 0; j < n; j += C::NS) {
         y = j & 1;
@@ -661,7 +812,11 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const ShSmem<C> sm(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  if (C::kBf16 && threadIdx.x == 288) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kOps; ++i) {
       mbar_init(sm.op_full(i), C::kBf16 ? 1 : 128);
@@ -692,22 +847,28 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
   pdl_wait();  // the plan
   pdl_trigger();
   bool ok = true;
+  uint32_t end = 0;  // of a loading warp's operands
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
     if (C::NS == 2 || warp < 4) ok = ShSoft<C>(p, sm, tmem).run();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == 8) {
-      if (lane == 0) ok = sh_multiply<C>(p, sm, tmem);
+      ok = sh_multiply<C>(p, sm, tmem);
     } else if (warp == 9) {
-      ok = sh_load<C>(p, &kmap, &vmap, sm);
+      ok = sh_load<C, false>(p, &kmap, sm, end);
+    } else if (warp == 10) {
+      ok = sh_load<C, true>(p, &vmap, sm, end);
     } else if (warp >= 12) {
       if constexpr (!C::kBf16) ok = sh_widen<C>(p, sm);
     }
   }
   if (!ok && p.a.status) atomicOr(p.a.status, ST_TIMEOUT);
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {  // (without a failure every copy has been waited for by what reads it)
+    sh_load_drain<C>(sm, end);
+    __syncthreads();
+  }
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -742,28 +903,32 @@ __device__ __noinline__ float sh_far_value(const SharedParams& p, const int* tab
 }
 
 // The partials of one (row, query head): segments of the prefix, then splits of the
-// row's own positions, added up in that order.  A warp for each result.
-template <int D, bool kBf16>
+// row's own positions.  kWide: a block for each, its warps take every eighth partial
+// and add up in order; else a warp does all.
+template <int D, bool kBf16, bool kWide>
 __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ SharedParams p) {
-  constexpr int V = D / 32, NS = shared_streams(D), CP = shared_chunk(D), B = 8;
+  constexpr int V = D / 32, NS = shared_streams(D), W = kWide ? 8 : 1, B = V == 8 ? 4 : 8;
+  __shared__ float s_o[W][D], s_m[W], s_l[W];
+  __shared__ int s_bad[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * 8 + warp;
+  const int unit = kWide ? blockIdx.x : blockIdx.x * 8 + warp;
   const int H = p.a.n_q_heads, r = p.a.row_lo + unit / H, hq = unit % H, G = H / p.a.n_kv_heads;
-  int seq, i;
+  int seq, i, t = 0;
   const bool row = r < p.a.row_hi && find_row(p.a.rows, r, seq, i);
+  if (row) t = first_of(p.a.rows, seq) + i;
   pdl_trigger();
   pdl_wait();
-  if (!row) return;
-  const int t = first_of(p.a.rows, seq) + i, from = __ldcg(p.from + seq), gi = __ldcg(p.group + seq), kvh = hq / G;
+  if (!row) return;  // (a whole block, or a warp that meets no other)
+  const int from = __ldcg(p.from + seq), gi = __ldcg(p.group + seq), kvh = hq / G;
   // the prefix: CTAs c0 .. c1 - 1, one or two partials each
   int c0 = 0, c1 = 0, planes = 1, plane = 0;
   long long slot = 0;
   if (t >= 0 && from > 0 && gi >= 0) {
     const SharedGroup g = sh_group(p.plan, gi), end = sh_group(p.plan, p.n_groups);
     const int f = (r - g.row0) * G + hq % G, pair = f / (NS * kSharedTile), w = min(NS, g.tiles - pair * NS);
-    const long long first = g.unit0 + (long long)kvh * g.chunks * g.tiles + (long long)pair * NS * g.chunks;
+    const int first = g.unit0 + kvh * g.chunks * g.tiles + pair * NS * g.chunks;
     c0 = sh_owner(first, end.unit0, end.eff);
-    c1 = sh_owner(first + (long long)(g.chunks - 1) * w, end.unit0, end.eff) + 1;
+    c1 = sh_owner(first + (g.chunks - 1) * w, end.unit0, end.eff) + 1;
     planes = w == 2 ? 1 : NS;
     plane = w == 2 ? f / kSharedTile & 1 : 0;
     slot = sh_slot(p, g, kvh, pair, NS, 0) + f % kSharedTile;
@@ -776,41 +941,52 @@ __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ Sh
   auto place = [&](int j) {  // of partial j < n1
     return (long long)(planes == 2 ? j & 1 : plane) * p.plane + slot + (long long)(c0 + (planes == 2 ? j >> 1 : j)) * kSharedTile;
   };
-  auto ml_of = [&](int j) { return j < n1 ? __ldcg(p.ml + place(j)) : __ldcg(p.a.part_ml + own + (j - n1)); };
-  float M = kShNone;
-  for (int j = lane; j < n; j += 32) M = fmaxf(M, ml_of(j).x);
+  float M = kShNone, l = 0.0f, acc[V];
+  bool bad = false;  // a partial that is not finite
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float l = 0.0f, acc[V], bad = 0.0f, small[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = small[e] = 0.0f;
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const float2 ml = j0 + lane < n ? ml_of(j0 + lane) : make_float2(kShNone, 0.0f);
+  for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+  // this warp's partials, warp + W k: 32 references and sums at a time, then B accumulators
+  for (int k0 = 0; (kWide ? warp : 0) + W * k0 < n; k0 += 32) {
+    const int first = (kWide ? warp : 0) + W * k0, j = first + W * lane, cnt = min(32, (n - first + W - 1) / W);
+    float2 ml = make_float2(kShNone, 0.0f);
+    if (lane < cnt) ml = j < n1 ? __ldcg(p.ml + place(j)) : __ldcg(p.a.part_ml + own + (j - n1));
     // (a partial that has seen nothing has no accumulators; one of NaN scores has a NaN sum)
     const bool saw = !(ml.y == 0.0f);
+    const uint32_t some = __ballot_sync(0xffffffffu, saw);
+    float top = M;
+    float mine = saw ? ml.x : kShNone;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    top = fmaxf(top, mine);
+    {
+      const float d = __fsub_rn(M, top), f = sh_ex2(d);
+      l = sh_times_ex2(l, d);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = d < 0.0f ? __fmul_rn(acc[e], f) : acc[e];
+      M = top;
+    }
     const float d = __fsub_rn(ml.x, M), f = saw ? sh_ex2(d) : 0.0f;
     float part = saw ? sh_times_ex2(ml.y, d) : 0.0f;
-    const uint32_t some = __ballot_sync(0xffffffffu, saw);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part = __fadd_rn(part, __shfl_xor_sync(0xffffffffu, part, o));
     l = __fadd_rn(l, part);
-    for (int k0 = 0; k0 < min(32, n - j0); k0 += B) {
+    for (int b0 = 0; b0 < cnt; b0 += B) {
       float x[B][V];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int j = j0 + k0 + b;
-        const bool have = (some >> (k0 + b)) & 1u;  // (bits behind the last partial are clear)
-        const float* src = !have ? nullptr : j < n1 ? p.o + place(j) * D : p.a.part_o + (own + (j - n1)) * D;
+        const int jb = first + W * (b0 + b);
+        const bool have = b0 + b < 32 && (some >> (b0 + b)) & 1u;
 #pragma unroll
         for (int e = 0; e < V; ++e) x[b][e] = 0.0f;
         if (have) {
+          const float* src = (jb < n1 ? p.o + place(jb) * D : p.a.part_o + (own + (jb - n1)) * D) + lane * V;
           if constexpr (V == 2) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src + lane * V));
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
             x[b][0] = v.x; x[b][1] = v.y;
           } else {
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + lane * V + e));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + e));
               x[b][e] = v.x; x[b][e + 1] = v.y; x[b][e + 2] = v.z; x[b][e + 3] = v.w;
             }
           }
@@ -818,33 +994,85 @@ __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ Sh
       }
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const float fb = __shfl_sync(0xffffffffu, f, k0 + b);
+        const float fb = __shfl_sync(0xffffffffu, f, b0 + b);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+          if (kBf16) bad |= !(fabsf(x[b][e]) < INFINITY);
           acc[e] = __fmaf_rn(x[b][e], fb, acc[e]);
-          if (kBf16) {
-            small[e] = __fmaf_rn(x[b][e], __fmul_rn(fb, 0x1p-24f), small[e]);
-            bad = __fmaf_rn(x[b][e], 0.0f, bad);
-          }
         }
       }
     }
   }
-  const bool none = l == 0.0f;
-  bf16* out = p.a.out + (int64_t)r * p.a.out_stride + hq * D + lane * V;
   float y[V];
+  bool none;
+  if constexpr (kWide) {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = l;
+    }
+    const int any = __any_sync(0xffffffffu, bad);
+    if (lane == 0) s_bad[warp] = any;
 #pragma unroll
-  for (int e = 0; e < V; ++e) y[e] = none ? 0.0f : __fdiv_rn(acc[e], l);
-  if (kBf16 && l == l && !none) {
-    const int* table = p.a.rows.table + (size_t)seq * p.a.rows.table_stride;
+    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+    __syncthreads();
+    M = kShNone;
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (!(fabsf(acc[e]) < INFINITY))
-        y[e] = sh_far_value<D>(p, table, t, kvh, lane * V + e, bad == 0.0f, __fdiv_rn(small[e], __fmul_rn(l, 0x1p-24f)));
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w]);
+    l = 0.0f;
+    bad = false;
+    float f[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float d = __fsub_rn(s_m[w], M);
+      f[w] = sh_ex2(d);
+      l = __fadd_rn(l, sh_times_ex2(s_l[w], d));
+      bad |= s_bad[w] != 0;
+    }
+    if (warp * 32 >= D) return;
+    // a warp's 32 columns
+    const int c = warp * 32 + lane;
+    float a = 0.0f, small = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      if (!(s_l[w] == 0.0f)) {
+        a = __fmaf_rn(s_o[w][c], f[w], a);
+        small = __fmaf_rn(s_o[w][c], __fmul_rn(f[w], 0x1p-24f), small);
+      }
+    none = l == 0.0f;
+    float v = none ? 0.0f : __fdiv_rn(a, l);
+    if (kBf16 && l == l && !none && !(fabsf(a) < INFINITY))
+      v = sh_far_value<D>(p, p.a.rows.table + (size_t)seq * p.a.rows.table_stride, t, kvh, c, !bad, __fdiv_rn(small, __fmul_rn(l, 0x1p-24f)));
+    p.a.out[(int64_t)r * p.a.out_stride + hq * D + c] = __float2bfloat16_rn(v);
+  } else {
+    none = l == 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = none ? 0.0f : __fdiv_rn(acc[e], l);
+    if (kBf16 && l == l && !none) {
+#pragma unroll 1
+      for (int e = 0; e < V; ++e) {
+        float a = 0.0f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) a = k == e ? acc[k] : a;
+        if (fabsf(a) < INFINITY) continue;
+        // the sum again, of the partials times 2^-24
+        float small = 0.0f;
+        for (int j = 0; j < n; ++j) {
+          const float2 ml = j < n1 ? __ldcg(p.ml + place(j)) : __ldcg(p.a.part_ml + own + (j - n1));
+          if (ml.y == 0.0f) continue;
+          const float* src = j < n1 ? p.o + place(j) * D : p.a.part_o + (own + (j - n1)) * D;
+          small = __fmaf_rn(__ldcg(src + lane * V + e), __fmul_rn(sh_ex2(__fsub_rn(ml.x, M)), 0x1p-24f), small);
+        }
+        const float v = sh_far_value<D>(p, p.a.rows.table + (size_t)seq * p.a.rows.table_stride, t, kvh, lane * V + e, !bad,
+                                        __fdiv_rn(small, __fmul_rn(l, 0x1p-24f)));
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[k] = k == e ? v : y[k];
+      }
+    }
+    bf16* out = p.a.out + (int64_t)r * p.a.out_stride + hq * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
   }
-#pragma unroll
-  for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
-  if (p.a.lse && lane == 0)
+  if (p.a.lse && lane == 0 && warp == (kWide ? 0 : warp))
     p.a.lse[(size_t)r * H + hq] = none ? -INFINITY : __fmul_rn(__fadd_rn(M, log2f(l)), 0.6931471805599453f);
 }
 
@@ -881,10 +1109,11 @@ cudaError_t shared_launch(const SharedParams& p, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t shared_merge_launch(const SharedParams& p, cudaStream_t s) {
+cudaError_t shared_merge_launch(const SharedParams& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const int64_t units = (int64_t)(p.a.row_hi - p.a.row_lo) * p.a.n_q_heads;
-  cfg.gridDim = dim3((unsigned)((units + 7) / 8));
+  const bool wide = units <= 32 * (int64_t)num_sms;
+  cfg.gridDim = dim3((unsigned)(wide ? units : (units + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -892,7 +1121,11 @@ cudaError_t shared_merge_launch(const SharedParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.a.k_exp ? cudaLaunchKernelEx(&cfg, k_shared_merge<D, false>, p) : cudaLaunchKernelEx(&cfg, k_shared_merge<D, true>, p);
+  if (wide)
+    return p.a.k_exp ? cudaLaunchKernelEx(&cfg, k_shared_merge<D, false, true>, p)
+                     : cudaLaunchKernelEx(&cfg, k_shared_merge<D, true, true>, p);
+  return p.a.k_exp ? cudaLaunchKernelEx(&cfg, k_shared_merge<D, false, false>, p)
+                   : cudaLaunchKernelEx(&cfg, k_shared_merge<D, true, false>, p);
 }
 
 }  // namespace

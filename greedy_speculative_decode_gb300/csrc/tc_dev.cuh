@@ -63,12 +63,37 @@ __device__ __forceinline__ uint64_t tc_sdesc_mn(uint32_t addr, uint32_t next) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// A from tensor memory (two 16-bit values a column, M lanes), B from shared memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accum) {
+// One lane of a warp whose lanes all run the code around it.  What issues many
+// multiplies runs as a whole warp, and only the instruction itself is for one
+// lane: descriptors and addresses then stay in uniform registers.  (In a branch
+// for one lane they are moved there for each multiply, 125 cycles instead of the
+// 64 that 128 x 128 x 16 takes.)
+__device__ __forceinline__ uint32_t tc_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void tc_mma_if(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accum)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum), "r"(lead)
+      : "memory");
+}
+// A from tensor memory (two 16-bit values a column, M lanes), B from shared memory.
+__device__ __forceinline__ void tc_mma_ts_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                             bool accum) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accum), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 
