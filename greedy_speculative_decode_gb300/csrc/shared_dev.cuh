@@ -62,9 +62,6 @@ struct ShCfg {
   static constexpr int kRaws = kBf16 ? 0 : D == 64 ? 4 : 3;
   static constexpr int kRings = 4;  // chunks whose scales and page masks are kept
   static constexpr int kThreads = kBf16 ? 384 : 512;
-  // registers: of the launch, of a softmax thread, of the others (their sum must not be above the launch's)
-  static constexpr int kRegs = kBf16 ? 168 : 128, kRegsSoft = kBf16 ? 224 : 192, kRegsOther = kBf16 ? 56 : 64;
-  static_assert(2 * kRegsSoft + (kThreads / 128 - 2) * kRegsOther <= kThreads / 128 * kRegs, "registers of the warpgroups");
   // tensor memory: scores (and weights over them) of two steps, accumulators of each stream
   static constexpr uint32_t kScoreCol = CP, kOutCol = 512 - NS * D;
   static_assert(2 * kScoreCol <= kOutCol, "columns of tensor memory");
@@ -77,8 +74,8 @@ struct ShCfg {
   static constexpr int kBars = 2 * kOps + 2 * kRaws + kRings + 2 /*s_full*/ + 2 /*p_full*/ + 2 /*pv*/ + 2 /*q*/ + 1 /*drain*/;
   static constexpr int kOffMeta = kOffBar + kBars * 8;  // [8] what a chunk holds (sh_meta)
   static constexpr int kOffRawMeta = kOffMeta + 32;     // [8] the same for an item of codes
-  static constexpr int kOffFac = kOffRawMeta + 32;      // [NS][128] the query rows' factors
-  static constexpr int kOffTmem = kOffFac + NS * kSharedTile * 4;
+  static constexpr int kOffRow = kOffRawMeta + 32;      // [NS][128] token rows of the query rows (-1: none)
+  static constexpr int kOffTmem = kOffRow + NS * kSharedTile * 4;
   static constexpr int kSmem = 1024 + kOffTmem + 16;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -88,6 +85,12 @@ template <class C>
 __device__ __forceinline__ constexpr uint32_t sh_idesc(int N, bool b_mn) {
   return (1u << 4) | (C::kBf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(kSharedTile >> 4) << 24);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // A whole warp's wait.  Its lanes go on together: one that fell behind, and that
@@ -212,7 +215,7 @@ struct ShSmem {
   __device__ __forceinline__ float* scale(int s) const { return reinterpret_cast<float*>(base + C::kOffScale) + s * 3 * C::CP; }
   __device__ __forceinline__ volatile uint32_t* meta() const { return reinterpret_cast<uint32_t*>(base + C::kOffMeta); }
   __device__ __forceinline__ volatile uint32_t* raw_meta() const { return reinterpret_cast<uint32_t*>(base + C::kOffRawMeta); }
-  __device__ __forceinline__ float* fac(int x) const { return reinterpret_cast<float*>(base + C::kOffFac) + x * kSharedTile; }
+  __device__ __forceinline__ int* rows(int x) const { return reinterpret_cast<int*>(base + C::kOffRow) + x * kSharedTile; }
   __device__ __forceinline__ uint32_t* tmem() const { return reinterpret_cast<uint32_t*>(base + C::kOffTmem); }
   // barriers
   __device__ __forceinline__ uint64_t* op_full(int s) const { return bar + s; }
@@ -440,7 +443,7 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
       asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(by));
       return r;
     };
-#pragma unroll
+#pragma unroll 1
     for (int k0 = 0; k0 < kMine; k0 += 4) {
       uint4 w[4];
       int unit[4];
@@ -481,9 +484,9 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
   uint32_t at0 = 0, seg = 0;
   bool ok = true;
   uint32_t used[2] = {0, 0};  // uses of each score place so far
-  const uint32_t q_base = smem_u32(sm.q(0)), op_base = smem_u32(sm.op(0));
+  const uint32_t q_base = __shfl_sync(0xffffffffu, smem_u32(sm.q(0)), 0), op_base = __shfl_sync(0xffffffffu, smem_u32(sm.op(0)), 0);
   while (ok && run.next(s)) {
-    const ShOrder ord{s.i1 - s.i0, s.w == 2};
+    const ShOrder ord{__shfl_sync(0xffffffffu, s.i1 - s.i0, 0), __shfl_sync(0xffffffffu, s.w, 0) == 2};
     const int n = ord.steps();
     auto scores = [&](int j) {
       const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
@@ -514,7 +517,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
       for (int t = 0; t < (C::kBf16 ? 2 : 1); ++t)
 #pragma unroll
         for (int k = 0; k < CP / 16; ++k)
-          tc_mma_ts_if(lead, o, w + t * (CP / 2) + k * 8, b + (k * 16 * 128 >> 4), kValues, j >= C::NS || t > 0 || k > 0);
+          tc_mma_ts_if(lead, o, w + (k / 2) * 32 + t * 16 + (k % 2) * 8, b + (k * 16 * 128 >> 4), kValues, j >= C::NS || t > 0 || k > 0);
       tc_commit_if(lead, sm.pv_done(x));
       if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
       if (j + 2 < n) ok = scores(j + 2);
@@ -552,51 +555,64 @@ struct ShSoft {
   }
 
   // The tile's queries, as an operand of 64-column halves with 128-byte swizzled
-  // rows; D / 8 lanes load a row.  Their factor is positive (the sign goes to the
-  // queries), so that the largest product is the largest score.
+  // rows: copied there as they are, then scaled in place, a row a thread.  Their
+  // factor is positive (the sign goes to the queries), so that the largest product is
+  // the largest score.
   __device__ __forceinline__ void queries(const ShSegment& s, int tile, int G) {
-    constexpr int U = D / 8, kLoads = U < 16 ? U : 16;  // lanes of a row; loads at a time
-    const uint32_t flip = p.a.scale_log2 < 0.0f ? 0x80008000u : 0u, dst = smem_u32(sm.q(x));
-    const float scale = fmaxf(fabsf(p.a.scale_log2), 0x1p-126f);  // (and not zero: a score of -infinity stays one)
-#pragma unroll 1
-    for (int i0 = 0; i0 < U; i0 += kLoads) {
-      uint4 w[kLoads];
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int idx = (i0 + i) * 128 + r, f = tile * kSharedTile + idx / U;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (f < s.g.R)
-          w[i] = __ldg(reinterpret_cast<const uint4*>(p.a.q + (int64_t)(s.g.row0 + f / G) * p.a.q_stride + (s.kvh * G + f % G) * D) + idx % U);
+    constexpr int U = D / 8;  // 16-byte units of a row
+    const uint32_t dst = smem_u32(sm.q(x));
+    const int f0 = tile * kSharedTile;
+    sm.rows(x)[r] = f0 + r < s.g.R ? (f0 + r) / G : -1;
+    named_sync(1 + x, 128);
+    const bf16* q = p.a.q + (int64_t)s.g.row0 * p.a.q_stride + s.kvh * G * D;
+#pragma unroll 4
+    for (int i = 0; i < U; ++i) {
+      const int idx = i * 128 + r, row = idx / U, u = idx % U;
+      const int token = sm.rows(x)[row], head = f0 + row - token * G;
+      const uint32_t to = dst + (u >> 3) * kSharedTile * 128 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+      if (token >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(q + token * p.a.q_stride + head * D + u * 8) : "memory");
+      else
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    named_sync(1 + x, 128);
+    const uint32_t flip = p.a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    fac = fmaxf(fabsf(p.a.scale_log2), 0x1p-126f);  // (and not zero: a score of -infinity stays one)
+    auto unit = [&](int u) { return dst + (u >> 3) * kSharedTile * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4); };
+    auto load = [&](int u) {
+      uint4 w;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(unit(u)));
+      return w;
+    };
+    float down = 1.0f;
+    if (!C::kBf16) {
+      uint32_t m = 0;
+#pragma unroll 4
+      for (int u = 0; u < U; ++u) {
+        const uint4 w = load(u);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
       }
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int idx = (i0 + i) * 128 + r, row = idx / U, u = idx % U;
-        uint4 v = w[i];
-        float fr = scale;
-        if (!C::kBf16) {
-          uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-          m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-          for (int o = 1; o < U; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // the row's largest exponent E: q / 2^(E - 127) is below 2 (an infinity or NaN makes the row NaN)
-          const int E = min(max((int)(m >> 7), 1), 253);
-          const float down = __uint_as_float((uint32_t)(254 - E) << 23);
-          fr = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __fmul_rn(scale, __uint_as_float((uint32_t)E << 23));
-          auto two = [&](uint32_t a) {
-            return sh_f16x2(__fmul_rn(__uint_as_float(a << 16), down), __fmul_rn(__uint_as_float(a & 0xffff0000u), down));
-          };
-          v = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
-        }
-        if (u == 0) sm.fac(x)[row] = fr;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (u >> 3) * kSharedTile * 128 + row * 128 + (((u & 7) ^ (row & 7)) << 4)),
-                     "r"(v.x ^ flip), "r"(v.y ^ flip), "r"(v.z ^ flip), "r"(v.w ^ flip)
+      m = max(m & 0xffffu, m >> 16);
+      // the row's largest exponent E: q / 2^(E - 127) is below 2 (an infinity or NaN makes the row NaN)
+      const int E = min(max((int)(m >> 7), 1), 253);
+      down = __uint_as_float((uint32_t)(254 - E) << 23);
+      fac = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __fmul_rn(fac, __uint_as_float((uint32_t)E << 23));
+    }
+    if (!C::kBf16 || flip) {
+#pragma unroll 2
+      for (int u = 0; u < U; ++u) {
+        uint4 w = load(u);
+        auto two = [&](uint32_t v) {
+          if (!C::kBf16) v = sh_f16x2(__fmul_rn(__uint_as_float(v << 16), down), __fmul_rn(__uint_as_float(v & 0xffff0000u), down));
+          return v ^ flip;
+        };
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit(u)), "r"(two(w.x)), "r"(two(w.y)), "r"(two(w.z)), "r"(two(w.w))
                      : "memory");
       }
     }
     fence_proxy_async_smem();
     mbar_arrive(sm.q_full(x));
-    named_sync(1 + x, 128);  // the factors
-    fac = sm.fac(x)[r];
     open();
   }
 
@@ -630,20 +646,21 @@ struct ShSoft {
     return true;
   }
 
-  // Weights of columns c .. c + 31 to where the product reads them.
-  __device__ __forceinline__ void put(uint32_t place, int c, const uint32_t* w) {
+  // 32 columns' weights over their scores, where the product reads them: two 16-bit
+  // values a column, 16 columns; of a bf16 cache the second terms in the other 16.
+  __device__ __forceinline__ void put(uint32_t place, const uint32_t (&w)[32]) {
     uint32_t hi[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e)  // (a bf16 weight's first term: its upper half)
       hi[e] = C::kBf16 ? __byte_perm(w[2 * e], w[2 * e + 1], 0x7632)
                        : sh_f16x2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
-    tc_st16(place + c / 2, hi);
+    tc_st16(place, hi);
     if (C::kBf16) {  // the second: the rest, rounded
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         hi[e] = pack_bf16x2(__fsub_rn(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e] & 0xffff0000u)),
                             __fsub_rn(__uint_as_float(w[2 * e + 1]), __uint_as_float(w[2 * e + 1] & 0xffff0000u)));
-      tc_st16(place + CP / 2 + c / 2, hi);
+      tc_st16(place + 16, hi);
     }
   }
 
@@ -651,49 +668,62 @@ struct ShSoft {
   // denominator takes them times 2^-ev, or where values of the segment have
   // exponents so much larger that a weight may be below fp32's range although its
   // share of the denominator counts, 2^(s f - ref).
+  //   Scores are read twice, 32 columns at a time in loops that are not unrolled
+  // further: with all 128 in registers and unrolled the code of the warps came to
+  // more than the instruction caches feed (8 cycles an instruction).
   __device__ __forceinline__ bool plain(int j, int y, uint32_t meta) {
     const uint32_t place = scores_at(y);
-    uint32_t w[CP / 32][32];
+    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < CP; c += 64) {
+      uint32_t v[32], w[32];
+      tc_ld32(place + c, v);
+      tc_ld32(place + c + 32, w);
+      tc_wait_ld();
 #pragma unroll
-    for (int c = 0; c < CP / 32; ++c) tc_ld32(place + 32 * c, w[c]);
-    tc_wait_ld();
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int c = 0; c < CP; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(w[c / 32][c % 32]));
+      for (int i = 0; i < 32; i += 2) {
+        m0 = max3(m0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        m1 = max3(m1, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+      }
+    }
     const float f = C::kBf16 ? fac : __fmul_rn(fac, sh_meta_key(meta)), ev = C::kBf16 ? 0.0f : sh_meta_value(meta);
-    if (!follow(__fmaf_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), f, ev), j, y)) return false;
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!follow(__fmaf_rn(fmaxf(m0, m1), f, ev), j, y)) return false;
     bool far = false;
     if (!C::kBf16) {
       const uint32_t e = meta >> 24;
       most = max(most, e);
       far = e + 60u < most;
-      if (far) {
-#pragma unroll 1
-        for (int c = 0; c < CP; c += 32) {
-          uint32_t v[32];
-          tc_ld32(place + c, v);
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sum[i & 3] = __fadd_rn(sum[i & 3], sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, -ref)));
-        }
-        l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])));
-      }
     }
     const float off = __fsub_rn(ev, ref);
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, direct = 0.0f;
+    uint32_t v[32], w[32];
+    auto weigh = [&](uint32_t (&a)[32]) {
+      if (!C::kBf16 && far) {
 #pragma unroll
-    for (int c = 0; c < CP / 32; ++c) {
+        for (int i = 0; i < 32; ++i) direct = __fadd_rn(direct, sh_ex2(__fmaf_rn(__uint_as_float(a[i]), f, -ref)));
+      }
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float e = sh_ex2(__fmaf_rn(__uint_as_float(w[c][i]), f, off));
+        const float e = sh_ex2(__fmaf_rn(__uint_as_float(a[i]), f, off));
         sum[i & 3] = __fadd_rn(sum[i & 3], e);
-        w[c][i] = __float_as_uint(e);
+        a[i] = __float_as_uint(e);
       }
-      put(place, 32 * c, w[c]);
+    };
+    tc_ld32(place, v);
+#pragma unroll 1
+    for (int c = 0; c < CP; c += 64) {  // (the next 32 columns are on their way while these are worked on)
+      tc_wait_ld();
+      tc_ld32(place + c + 32, w);
+      weigh(v);
+      put(place + c, v);
+      tc_wait_ld();
+      if (c + 64 < CP) tc_ld32(place + c + 64, v);
+      weigh(w);
+      put(place + c + 32, w);
     }
     const float all = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
     if (C::kBf16) l = __fadd_rn(l, all);
-    else if (!far) l = __fmaf_rn(all, __uint_as_float((254u - (meta >> 24)) << 23), l);
+    else l = far ? __fadd_rn(l, direct) : __fmaf_rn(all, __uint_as_float((254u - (meta >> 24)) << 23), l);
     return true;
   }
 
@@ -703,36 +733,41 @@ struct ShSoft {
     const bool even = C::kBf16 || meta & kShEven;
     const float ks = C::kBf16 ? 1.0f : sh_meta_key(meta), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
     const float iv = __uint_as_float((254u - (meta >> 24)) << 23);
-    uint32_t w[CP / 32][32];
+    uint32_t w[32];
+    auto scores = [&](int c) {  // in log2 units, with the value's exponent
+      tc_ld32(place + c, w);
+      tc_wait_ld();
 #pragma unroll
-    for (int c = 0; c < CP / 32; ++c) tc_ld32(place + 32 * c, w[c]);
-    tc_wait_ld();
-    // scores in log2 units, with the value's exponent
+      for (int i = 0; i < 32; ++i) {
+        float t = __fmul_rn(__uint_as_float(w[i]), fac);
+        if (!C::kBf16) t = even ? __fmaf_rn(t, ks, vs) : __fmaf_rn(t, sc[c + i], sc[CP + c + i]);
+        w[i] = (meta >> ((c + i) / kPage)) & 1u ? __float_as_uint(t) : 0xff800000u;
+      }
+    };
     float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < CP; c += 32) {
+      scores(c);
 #pragma unroll
-    for (int c = 0; c < CP; ++c) {
-      float t = __fmul_rn(__uint_as_float(w[c / 32][c % 32]), fac);
-      if (!C::kBf16) t = even ? __fmaf_rn(t, ks, vs) : __fmaf_rn(t, sc[c], sc[CP + c]);
-      t = (meta >> (c / kPage)) & 1u ? t : -INFINITY;
-      top = fmaxf(top, t);
-      w[c / 32][c % 32] = __float_as_uint(t);
+      for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
     }
     if (!follow(top, j, y)) return false;
     float sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CP / 32; ++c) {
+#pragma unroll 1
+    for (int c = 0; c < CP; c += 32) {
+      scores(c);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float z = __fsub_rn(__uint_as_float(w[c][i]), ref), e = sh_ex2(z);
+        const float z = __fsub_rn(__uint_as_float(w[i]), ref), e = sh_ex2(z);
         if (C::kBf16)
           sum = __fadd_rn(sum, e);
         else if (z < kShFar)  // 2^z is below fp32's range, the position's share of the denominator need not be
-          sum = __fadd_rn(sum, z == -INFINITY ? 0.0f : sh_ex2(__fsub_rn(z, even ? vs : sc[CP + 32 * c + i])));
+          sum = __fadd_rn(sum, z == -INFINITY ? 0.0f : sh_ex2(__fsub_rn(z, even ? vs : sc[CP + c + i])));
         else
-          sum = __fmaf_rn(e, even ? iv : sc[2 * CP + 32 * c + i], sum);
-        w[c][i] = __float_as_uint(e);
+          sum = __fmaf_rn(e, even ? iv : sc[2 * CP + c + i], sum);
+        w[i] = __float_as_uint(e);
       }
-      put(place, 32 * c, w[c]);
+      put(place + c, w);
     }
     l = __fadd_rn(l, sum);
     return true;
@@ -849,10 +884,8 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
   bool ok = true;
   uint32_t end = 0;  // of a loading warp's operands
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
     if (C::NS == 2 || warp < 4) ok = ShSoft<C>(p, sm, tmem).run();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == 8) {
       ok = sh_multiply<C>(p, sm, tmem);
     } else if (warp == 9) {
@@ -1079,12 +1112,7 @@ __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ Sh
 template <int D, int FMT>
 cudaError_t shared_prepare() {
   using C = ShCfg<D, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(k_shared_prefix<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  // The warpgroups' registers come out of what the launch got: with fewer the kernel would wait for ever.
-  cudaFuncAttributes at;
-  if ((e = cudaFuncGetAttributes(&at, k_shared_prefix<D, FMT>)) != cudaSuccess) return e;
-  return at.numRegs >= C::kRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(k_shared_prefix<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
 }
 
 template <int D, int FMT>
