@@ -61,7 +61,9 @@ struct ShCfg {
   static constexpr int kRawBytes = kBf16 ? 0 : CP * D;  // its codes
   static constexpr int kRaws = kBf16 ? 0 : D == 64 ? 4 : 3;
   static constexpr int kRings = 4;  // chunks whose scales and page masks are kept
-  static constexpr int kThreads = kBf16 ? 384 : 512;
+  static constexpr int kSoftWarps = 8 * NS;  // two warpgroups a stream
+  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1, kWidenWarp = kSoftWarps + 4;
+  static constexpr int kThreads = (kWidenWarp + (kBf16 ? 0 : 4)) * 32;
   // tensor memory: scores (and weights over them) of two steps, accumulators of each stream
   static constexpr uint32_t kScoreCol = CP, kOutCol = 512 - NS * D;
   static_assert(2 * kScoreCol <= kOutCol, "columns of tensor memory");
@@ -74,9 +76,11 @@ struct ShCfg {
   static constexpr int kBars = 2 * kOps + 2 * kRaws + kRings + 2 /*s_full*/ + 2 /*p_full*/ + 2 /*pv*/ + 2 /*q*/ + 1 /*drain*/;
   static constexpr int kOffMeta = kOffBar + kBars * 8;  // [8] what a chunk holds (sh_meta)
   static constexpr int kOffRawMeta = kOffMeta + 32;     // [8] the same for an item of codes
-  static constexpr int kOffRow = kOffRawMeta + 32;      // [NS][128] token rows of the query rows (-1: none)
-  static constexpr int kOffTmem = kOffRow + NS * kSharedTile * 4;
-  static constexpr int kSmem = 1024 + kOffTmem + 16;
+  // [2 score places][2 halves][128 rows] largest scores and sums; before a segment's first
+  // step [places][128] token rows of the query rows (-1: none)
+  static constexpr int kOffRow = kOffRawMeta + 32;
+  static constexpr int kOffTmem = kOffRow + 4 * kSharedTile * 4;
+  static constexpr int kSmem = kOffTmem + 16;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -215,7 +219,8 @@ struct ShSmem {
   __device__ __forceinline__ float* scale(int s) const { return reinterpret_cast<float*>(base + C::kOffScale) + s * 3 * C::CP; }
   __device__ __forceinline__ volatile uint32_t* meta() const { return reinterpret_cast<uint32_t*>(base + C::kOffMeta); }
   __device__ __forceinline__ volatile uint32_t* raw_meta() const { return reinterpret_cast<uint32_t*>(base + C::kOffRawMeta); }
-  __device__ __forceinline__ int* rows(int x) const { return reinterpret_cast<int*>(base + C::kOffRow) + x * kSharedTile; }
+  __device__ __forceinline__ float* meet(int y) const { return reinterpret_cast<float*>(base + C::kOffRow) + y * 2 * kSharedTile; }
+  __device__ __forceinline__ int* rows(int x) const { return reinterpret_cast<int*>(meet(x)); }  // (the stream's own place)
   __device__ __forceinline__ uint32_t* tmem() const { return reinterpret_cast<uint32_t*>(base + C::kOffTmem); }
   // barriers
   __device__ __forceinline__ uint64_t* op_full(int s) const { return bar + s; }
@@ -443,18 +448,19 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
       asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(by));
       return r;
     };
+    constexpr int kAtOnce = kMine < 8 ? kMine : 8;
 #pragma unroll 1
-    for (int k0 = 0; k0 < kMine; k0 += 4) {
-      uint4 w[4];
-      int unit[4];
+    for (int k0 = 0; k0 < kMine; k0 += kAtOnce) {
+      uint4 w[kAtOnce];
+      int unit[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         unit[k] = u0 + ((k0 + k + (C::D == 64 ? tid >> 1 : tid)) & (kMine - 1));
         w[k] = *reinterpret_cast<const uint4*>(raw + unit[k] * 16);
         if (!have) w[k] = make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         const uint32_t half = dst + (unit[k] >> 2) * C::CP * 128, col = 2 * (unit[k] & 3);
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + ((col ^ (pos & 7)) << 4)), "r"(scaled(f16x2_of_lo(w[k].x))),
                      "r"(scaled(f16x2_of_hi(w[k].x))), "r"(scaled(f16x2_of_lo(w[k].y))), "r"(scaled(f16x2_of_hi(w[k].y)))
@@ -483,7 +489,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
   ShSegment s;
   uint32_t at0 = 0, seg = 0;
   bool ok = true;
-  uint32_t used[2] = {0, 0};  // uses of each score place so far
+  uint32_t used0 = 0, used1 = 0;  // uses of each score place so far
   const uint32_t q_base = __shfl_sync(0xffffffffu, smem_u32(sm.q(0)), 0), op_base = __shfl_sync(0xffffffffu, smem_u32(sm.op(0)), 0);
   while (ok && run.next(s)) {
     const ShOrder ord{__shfl_sync(0xffffffffu, s.i1 - s.i0, 0), __shfl_sync(0xffffffffu, s.w, 0) == 2};
@@ -507,9 +513,10 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
     for (int j = 0; j < n && ok; ++j) {
       const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
       const uint32_t at = at0 + ord.v_at(c);
-      ok = sh_wait(sm.p_full(x), used[x] & 1u) && sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u);
+      ok = sh_wait(sm.p_full(x), (x ? used1 : used0) & 1u) && sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u);
       if (!ok) break;
-      ++used[x];
+      used0 += x ^ 1;
+      used1 += x;
       tc_fence_after();
       const uint64_t b = tc_sdesc_mn(op_base + at % C::kOps * C::kOpBytes, CP * 128);
       const uint32_t o = tmem + C::kOutCol + stream * D, w = tmem + x * C::kScoreCol;
@@ -532,22 +539,24 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
 }
 
 // ------------------------------------------------------------------ softmax
-// A warpgroup's stream: thread r has query row r of the tile.
+// A stream: two warpgroups, thread r of each has query row r of the tile, the first
+// the lower half of a chunk's positions, the second the upper one.
 template <class C>
 struct ShSoft {
-  static constexpr int CP = C::CP, D = C::D;
+  static constexpr int CP = C::CP, D = C::D, W = CP / 2;  // W: a thread's positions of a chunk
   const SharedParams& p;
   const ShSmem<C>& sm;
-  const int x, r;           // stream, row of the tile
+  const int x, h, r;        // stream, half, row of the tile
   const uint32_t lane_off;  // the warp's lanes of tensor memory
   const uint32_t tmem;
   float ref, l, fac;
   uint32_t most;               // largest value exponent (byte) of the segment's plain chunks so far
-  uint32_t steps[2] = {0, 0};  // steps of each score place so far
+  uint32_t steps0 = 0, steps1 = 0;  // steps of each score place so far
 
   __device__ __forceinline__ ShSoft(const SharedParams& p_, const ShSmem<C>& sm_, uint32_t tm)
-      : p(p_), sm(sm_), x(threadIdx.x >> 7), r(threadIdx.x & 127), lane_off((uint32_t)(threadIdx.x & 96) << 16), tmem(tm) {}
+      : p(p_), sm(sm_), x(threadIdx.x >> 8), h((threadIdx.x >> 7) & 1), r(threadIdx.x & 127), lane_off((uint32_t)(threadIdx.x & 96) << 16), tmem(tm) {}
 
+  __device__ __forceinline__ uint32_t steps(int y) const { return y ? steps1 : steps0; }
   __device__ __forceinline__ void open() {
     ref = kShNone;
     l = 0.0f;
@@ -562,12 +571,12 @@ struct ShSoft {
     constexpr int U = D / 8;  // 16-byte units of a row
     const uint32_t dst = smem_u32(sm.q(x));
     const int f0 = tile * kSharedTile;
-    sm.rows(x)[r] = f0 + r < s.g.R ? (f0 + r) / G : -1;
-    named_sync(1 + x, 128);
+    if (h == 0) sm.rows(x)[r] = f0 + r < s.g.R ? (f0 + r) / G : -1;
+    meet();
     const bf16* q = p.a.q + (int64_t)s.g.row0 * p.a.q_stride + s.kvh * G * D;
 #pragma unroll 4
-    for (int i = 0; i < U; ++i) {
-      const int idx = i * 128 + r, row = idx / U, u = idx % U;
+    for (int i = 0; i < U / 2; ++i) {
+      const int idx = (2 * i + h) * 128 + r, row = idx / U, u = idx % U;
       const int token = sm.rows(x)[row], head = f0 + row - token * G;
       const uint32_t to = dst + (u >> 3) * kSharedTile * 128 + row * 128 + (((u & 7) ^ (row & 7)) << 4);
       if (token >= 0)
@@ -576,7 +585,7 @@ struct ShSoft {
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0u) : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    named_sync(1 + x, 128);
+    meet();
     const uint32_t flip = p.a.scale_log2 < 0.0f ? 0x80008000u : 0u;
     fac = fmaxf(fabsf(p.a.scale_log2), 0x1p-126f);  // (and not zero: a score of -infinity stays one)
     auto unit = [&](int u) { return dst + (u >> 3) * kSharedTile * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4); };
@@ -598,10 +607,11 @@ struct ShSoft {
       const int E = min(max((int)(m >> 7), 1), 253);
       down = __uint_as_float((uint32_t)(254 - E) << 23);
       fac = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __fmul_rn(fac, __uint_as_float((uint32_t)E << 23));
+      meet();  // (both halves have looked)
     }
     if (!C::kBf16 || flip) {
 #pragma unroll 2
-      for (int u = 0; u < U; ++u) {
+      for (int u = h * U / 2; u < (h + 1) * U / 2; ++u) {
         uint4 w = load(u);
         auto two = [&](uint32_t v) {
           if (!C::kBf16) v = sh_f16x2(__fmul_rn(__uint_as_float(v << 16), down), __fmul_rn(__uint_as_float(v & 0xffff0000u), down));
@@ -616,7 +626,16 @@ struct ShSoft {
     open();
   }
 
-  __device__ __forceinline__ uint32_t scores_at(int y) const { return tmem + lane_off + y * C::kScoreCol; }
+  __device__ __forceinline__ uint32_t scores_at(int y) const { return tmem + lane_off + y * C::kScoreCol + h * W; }
+  __device__ __forceinline__ void meet() const { named_sync(1 + x, 256); }
+  // The larger of both halves' numbers of the row (on score place y).  The next ones
+  // are written when this step's weights, which both give, have been used.
+  __device__ __forceinline__ float larger(float v, int y) const {
+    float* s = sm.meet(y);
+    s[h * kSharedTile + r] = v;
+    meet();
+    return fmaxf(v, s[(h ^ 1) * kSharedTile + r]);
+  }
 
   // The reference follows a row's largest score `top` of step j where it has risen by more than the slack.
   __device__ __forceinline__ bool follow(float top, int j, int y) {
@@ -630,11 +649,11 @@ struct ShSoft {
     ref = up ? top : ref;
     if (!__any_sync(0xffffffffu, scaled)) return true;  // (behind a row's first chunk there is nothing to scale)
     // the product before this step (with two streams it ran before these scores did)
-    if (C::NS == 1 && j > 0 && !sh_wait(sm.pv_done(y ^ 1), (steps[y ^ 1] - 1u) & 1u)) return false;
+    if (C::NS == 1 && j > 0 && !sh_wait(sm.pv_done(y ^ 1), (steps(y ^ 1) - 1u) & 1u)) return false;
     tc_fence_after();
     const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c = h * D / 2; c < (h + 1) * D / 2; c += 32) {
       uint32_t v[32];
       tc_ld32(o + c, v);
       tc_wait_ld();
@@ -668,26 +687,23 @@ struct ShSoft {
   // denominator takes them times 2^-ev, or where values of the segment have
   // exponents so much larger that a weight may be below fp32's range although its
   // share of the denominator counts, 2^(s f - ref).
-  //   Scores are read twice, 32 columns at a time in loops that are not unrolled
-  // further: with all 128 in registers and unrolled the code of the warps came to
-  // more than the instruction caches feed (8 cycles an instruction).
+  //   Scores are read twice, 32 columns at a time, in loops that are not unrolled
+  // further: the warps' code then fits the instruction caches and their registers the
+  // file.  (Nearly all of an SM's L1 is shared memory here: what a register spills
+  // comes back from L2.)
   __device__ __forceinline__ bool plain(int j, int y, uint32_t meta) {
     const uint32_t place = scores_at(y);
-    float m0 = -INFINITY, m1 = -INFINITY;
+    uint32_t v[32];
+    float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-    for (int c = 0; c < CP; c += 64) {
-      uint32_t v[32], w[32];
+    for (int c = 0; c < W; c += 32) {
       tc_ld32(place + c, v);
-      tc_ld32(place + c + 32, w);
       tc_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        m0 = max3(m0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-        m1 = max3(m1, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-      }
+      for (int i = 0; i < 32; i += 2) m[i / 2 & 1] = max3(m[i / 2 & 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
     }
     const float f = C::kBf16 ? fac : __fmul_rn(fac, sh_meta_key(meta)), ev = C::kBf16 ? 0.0f : sh_meta_value(meta);
-    if (!follow(__fmaf_rn(fmaxf(m0, m1), f, ev), j, y)) return false;
+    if (!follow(__fmaf_rn(larger(fmaxf(m[0], m[1]), y), f, ev), j, y)) return false;
     bool far = false;
     if (!C::kBf16) {
       const uint32_t e = meta >> 24;
@@ -695,33 +711,24 @@ struct ShSoft {
       far = e + 60u < most;
     }
     const float off = __fsub_rn(ev, ref);
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, direct = 0.0f;
-    uint32_t v[32], w[32];
-    auto weigh = [&](uint32_t (&a)[32]) {
+    float sum[2] = {0.0f, 0.0f}, direct = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < W; c += 32) {
+      tc_ld32(place + c, v);
+      tc_wait_ld();
       if (!C::kBf16 && far) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) direct = __fadd_rn(direct, sh_ex2(__fmaf_rn(__uint_as_float(a[i]), f, -ref)));
+        for (int i = 0; i < 32; ++i) direct = __fadd_rn(direct, sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, -ref)));
       }
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float e = sh_ex2(__fmaf_rn(__uint_as_float(a[i]), f, off));
-        sum[i & 3] = __fadd_rn(sum[i & 3], e);
-        a[i] = __float_as_uint(e);
+        const float e = sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, off));
+        sum[i & 1] = __fadd_rn(sum[i & 1], e);
+        v[i] = __float_as_uint(e);
       }
-    };
-    tc_ld32(place, v);
-#pragma unroll 1
-    for (int c = 0; c < CP; c += 64) {  // (the next 32 columns are on their way while these are worked on)
-      tc_wait_ld();
-      tc_ld32(place + c + 32, w);
-      weigh(v);
       put(place + c, v);
-      tc_wait_ld();
-      if (c + 64 < CP) tc_ld32(place + c + 64, v);
-      weigh(w);
-      put(place + c + 32, w);
     }
-    const float all = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
+    const float all = __fadd_rn(sum[0], sum[1]);
     if (C::kBf16) l = __fadd_rn(l, all);
     else l = far ? __fadd_rn(l, direct) : __fmaf_rn(all, __uint_as_float((254u - (meta >> 24)) << 23), l);
     return true;
@@ -733,6 +740,8 @@ struct ShSoft {
     const bool even = C::kBf16 || meta & kShEven;
     const float ks = C::kBf16 ? 1.0f : sh_meta_key(meta), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
     const float iv = __uint_as_float((254u - (meta >> 24)) << 23);
+    const uint32_t there = meta >> (h * (W / kPage));
+    sc += h * W;
     uint32_t w[32];
     auto scores = [&](int c) {  // in log2 units, with the value's exponent
       tc_ld32(place + c, w);
@@ -741,20 +750,20 @@ struct ShSoft {
       for (int i = 0; i < 32; ++i) {
         float t = __fmul_rn(__uint_as_float(w[i]), fac);
         if (!C::kBf16) t = even ? __fmaf_rn(t, ks, vs) : __fmaf_rn(t, sc[c + i], sc[CP + c + i]);
-        w[i] = (meta >> ((c + i) / kPage)) & 1u ? __float_as_uint(t) : 0xff800000u;
+        w[i] = (there >> ((c + i) / kPage)) & 1u ? __float_as_uint(t) : 0xff800000u;
       }
     };
     float top = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < CP; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       scores(c);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
     }
-    if (!follow(top, j, y)) return false;
+    if (!follow(larger(top, y), j, y)) return false;
     float sum = 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < CP; c += 32) {
+    for (int c = 0; c < W; c += 32) {
       scores(c);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -775,7 +784,7 @@ struct ShSoft {
 
   // Step j of the segment, on score place y: scores to weights.  no: the chunk's number in the call.
   __device__ __forceinline__ bool step(int j, int y, uint32_t no, bool both) {
-    if (!sh_wait(sm.s_full(y), steps[y] & 1u)) return false;
+    if (!sh_wait(sm.s_full(y), steps(y) & 1u)) return false;
     tc_fence_after();
     const uint32_t meta = sm.meta()[no & 7];
     if (!(meta & kShPlain ? plain(j, y, meta) : uneven(j, y, meta, sm.scale(no % C::kRings)))) return false;
@@ -787,7 +796,8 @@ struct ShSoft {
       mbar_arrive(sm.sc_empty(no % C::kRings));
       if (C::NS == 2 && !both) mbar_arrive(sm.sc_empty(no % C::kRings));  // (a chunk that one stream alone has)
     }
-    ++steps[y];
+    steps0 += y ^ 1;
+    steps1 += y;
     return true;
   }
 
@@ -796,11 +806,11 @@ struct ShSoft {
     const int f = tile * kSharedTile + r;
     const long long at = (long long)x * p.plane + sh_slot(p, s.g, s.kvh, s.pair, C::NS, cta) + r;
     if (n > 0) {
-      if (!sh_wait(sm.pv_done(y), (steps[y] - 1u) & 1u)) return false;
+      if (!sh_wait(sm.pv_done(y), (steps(y) - 1u) & 1u)) return false;
       tc_fence_after();
       const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = h * D / 2; c < (h + 1) * D / 2; c += 32) {
         uint32_t v[32];
         tc_ld32(o + c, v);
         tc_wait_ld();
@@ -812,7 +822,11 @@ struct ShSoft {
       }
       tc_fence_before();
     }
-    if (f < s.g.R) p.ml[at] = make_float2(ref, l);
+    float* sum = sm.meet(y);
+    if (h == 1) sum[r] = l;
+    meet();
+    if (h == 0 && f < s.g.R) p.ml[at] = make_float2(ref, __fadd_rn(l, sum[r]));
+    meet();  // (the place is free again)
     return true;
   }
 
@@ -824,9 +838,9 @@ struct ShSoft {
     while (run.next(s)) {
       const ShOrder ord{s.i1 - s.i0, s.w == 2};
       const int n = ord.steps(), tile = s.pair * C::NS + (ord.both ? x : 0);
-      if (C::NS == 1 || x < n) queries(s, tile, G);
+      if (x < n) queries(s, tile, G);
       else { open(); mbar_arrive(sm.q_full(x)); }
-      int mine = 0, y = 0;
+      int mine = 0, y = C::NS == 2 ? x : 0;
       for (int j = C::NS == 2 ? x : 0; j < n; j += C::NS) {
         y = j & 1;
         if (!step(j, y, chunk_no + ord.chunk(j), ord.both)) return false;
@@ -844,11 +858,10 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
     k_shared_prefix(const __grid_constant__ SharedParams p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap) {
   using C = ShCfg<D, FMT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   const ShSmem<C> sm(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  if (C::kBf16 && threadIdx.x == 288) {
+  if (C::kBf16 && threadIdx.x == C::kLoadWarp * 32) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
@@ -861,12 +874,12 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
       mbar_init(sm.raw_full(i), 1);
       mbar_init(sm.raw_empty(i), 128);
     }
-    for (int i = 0; i < C::kRings; ++i) mbar_init(sm.sc_empty(i), C::NS == 2 ? 8 : 4);
+    for (int i = 0; i < C::kRings; ++i) mbar_init(sm.sc_empty(i), C::kSoftWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(sm.s_full(i), 1);
-      mbar_init(sm.p_full(i), 128);
+      mbar_init(sm.p_full(i), 256);
       mbar_init(sm.pv_done(i), 1);
-      mbar_init(sm.q_full(i), 128);
+      mbar_init(sm.q_full(i), 256);
     }
     mbar_init(sm.drain(), 1);
     fence_barrier_init();
@@ -883,18 +896,16 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
   pdl_trigger();
   bool ok = true;
   uint32_t end = 0;  // of a loading warp's operands
-  if (warp < 8) {
-    if (C::NS == 2 || warp < 4) ok = ShSoft<C>(p, sm, tmem).run();
-  } else {
-    if (warp == 8) {
-      ok = sh_multiply<C>(p, sm, tmem);
-    } else if (warp == 9) {
-      ok = sh_load<C, false>(p, &kmap, sm, end);
-    } else if (warp == 10) {
-      ok = sh_load<C, true>(p, &vmap, sm, end);
-    } else if (warp >= 12) {
-      if constexpr (!C::kBf16) ok = sh_widen<C>(p, sm);
-    }
+  if (warp < C::kSoftWarps) {
+    ok = ShSoft<C>(p, sm, tmem).run();
+  } else if (warp == C::kMmaWarp) {
+    ok = sh_multiply<C>(p, sm, tmem);
+  } else if (warp == C::kLoadWarp) {
+    ok = sh_load<C, false>(p, &kmap, sm, end);
+  } else if (warp == C::kLoadWarp + 1) {
+    ok = sh_load<C, true>(p, &vmap, sm, end);
+  } else if (warp >= C::kWidenWarp) {
+    if constexpr (!C::kBf16) ok = sh_widen<C>(p, sm);
   }
   if (!ok && p.a.status) atomicOr(p.a.status, ST_TIMEOUT);
   tc_fence_before();
