@@ -15,7 +15,15 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   __shared__ int s_sum[32], s_unit[1025];
   const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
   pdl_trigger();
-  for (int g = tid; g <= N; g += 1024)
+  auto start_of = [&](int s) { return p.a.rows.row_start ? __ldg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
+  auto clip = [&](int r) { return min(max(r, 0), p.a.rows.n_rows); };
+  int first = 0, n = 0;
+  if (tid < S) {
+    first = first_of(p.a.rows, tid);
+    n = start_of(tid + 1) - start_of(tid);
+  }
+  if (tid < 32) s_sum[tid] = 0;
+  for (int g = tid; g <= N; g += blockDim.x)
     s_start[g] = p.group_start ? min(max(__ldg(p.group_start + g), 0), S) : (int)((long long)S * g / N);
   if (tid < N) {
     const int most = min(max(__ldg(p.length + tid), 0), p.a.rows.limit());
@@ -24,8 +32,6 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   __syncthreads();
   const bool back = __syncthreads_or(tid < N && s_start[tid + 1] < s_start[tid]);
   if (back && tid == 0 && p.a.status) atomicOr(p.a.status, ST_BAD_PAGE);
-  auto start_of = [&](int s) { return p.a.rows.row_start ? __ldg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
-  auto clip = [&](int r) { return min(max(r, 0), p.a.rows.n_rows); };
   int gi = -1;
   if (tid < S) {
     if (!back && tid >= s_start[0] && tid < s_start[N]) {
@@ -35,7 +41,6 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
         if (s_start[mid] <= tid) lo = mid; else hi = mid;
       }
       gi = lo;
-      const int first = first_of(p.a.rows, tid), n = start_of(tid + 1) - start_of(tid);
       if (n > 0 && first + n > 0) atomicMin(&s_eff[gi], max(first, 0) + 1);  // (rows of padding alone see nothing)
     }
     p.group[tid] = gi;
@@ -119,7 +124,8 @@ cudaError_t prepare_shared_kernels() {
 }
 
 cudaError_t launch_shared_prefix(const SharedParams& p, int fmt, int head_dim, cudaStream_t s) {
-  k_shared_plan<<<1, 1024, 0, s>>>(p, shared_chunk(head_dim), shared_streams(head_dim));
+  const int most = std::max(p.a.rows.n_seq, p.grid + 1);  // (a thread each)
+  k_shared_plan<<<1, std::min(1024, (most + 31) / 32 * 32), 0, s>>>(p, shared_chunk(head_dim), shared_streams(head_dim));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const bool b = fmt == SV_KV_BF16;

@@ -947,35 +947,38 @@ __device__ __noinline__ float sh_far_value(const SharedParams& p, const int* tab
 }
 
 // The partials of one (row, query head): segments of the prefix, then splits of the
-// row's own positions.  kWide: a block for each, its warps take every eighth partial
-// and add up in order; else a warp does all.
-template <int D, bool kBf16, bool kWide>
+// row's own positions.  W warps (of a block of eight) take every W-th of them each and
+// add up in order.
+template <int D, bool kBf16, int W>
 __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ SharedParams p) {
-  constexpr int V = D / 32, NS = shared_streams(D), W = kWide ? 8 : 1, B = V == 8 ? 4 : 8;
-  __shared__ float s_o[W][D], s_m[W], s_l[W];
-  __shared__ int s_bad[W];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = kWide ? blockIdx.x : blockIdx.x * 8 + warp;
-  const int H = p.a.n_q_heads, r = p.a.row_lo + unit / H, hq = unit % H, G = H / p.a.n_kv_heads;
-  int seq, i, t = 0;
+  constexpr int V = D / 32, NS = shared_streams(D), B = V == 8 ? 4 : 8, kUnits = 8 / W;
+  __shared__ float s_o[8][D], s_m[8], s_l[8];
+  __shared__ int s_bad[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp % W, w0 = warp - mine;
+  const int unit = blockIdx.x * kUnits + warp / W;
+  const int H = p.a.n_q_heads, r = p.a.row_lo + unit / H, hq = unit % H, G = H / p.a.n_kv_heads, kvh = hq / G;
+  int seq = 0, i = 0, t = -1, from = 0, gi = -1;
   const bool row = r < p.a.row_hi && find_row(p.a.rows, r, seq, i);
-  if (row) t = first_of(p.a.rows, seq) + i;
   pdl_trigger();
-  pdl_wait();
-  if (!row) return;  // (a whole block, or a warp that meets no other)
-  const int from = __ldcg(p.from + seq), gi = __ldcg(p.group + seq), kvh = hq / G;
-  // the prefix: CTAs c0 .. c1 - 1, one or two partials each
-  int c0 = 0, c1 = 0, planes = 1, plane = 0;
+  // (the plan was complete before the prefix's kernel began its work, and that before
+  // this one could start: only the partials are waited for)
+  int c0 = 0, c1 = 0, planes = 1, plane = 0;  // the prefix: CTAs c0 .. c1 - 1, one or two partials each
   long long slot = 0;
-  if (t >= 0 && from > 0 && gi >= 0) {
-    const SharedGroup g = sh_group(p.plan, gi), end = sh_group(p.plan, p.n_groups);
-    const int f = (r - g.row0) * G + hq % G, pair = f / (NS * kSharedTile), w = min(NS, g.tiles - pair * NS);
-    const int first = g.unit0 + kvh * g.chunks * g.tiles + pair * NS * g.chunks;
-    c0 = sh_owner(first, end.unit0, end.eff);
-    c1 = sh_owner(first + (g.chunks - 1) * w, end.unit0, end.eff) + 1;
-    planes = w == 2 ? 1 : NS;
-    plane = w == 2 ? f / kSharedTile & 1 : 0;
-    slot = sh_slot(p, g, kvh, pair, NS, 0) + f % kSharedTile;
+  if (row) {
+    from = __ldcg(p.from + seq);
+    gi = __ldcg(p.group + seq);
+    const SharedGroup end = sh_group(p.plan, p.n_groups);
+    t = first_of(p.a.rows, seq) + i;
+    if (t >= 0 && from > 0 && gi >= 0) {
+      const SharedGroup g = sh_group(p.plan, gi);
+      const int f = (r - g.row0) * G + hq % G, pair = f / (NS * kSharedTile), w = min(NS, g.tiles - pair * NS);
+      const int first = g.unit0 + kvh * g.chunks * g.tiles + pair * NS * g.chunks;
+      c0 = sh_owner(first, end.unit0, end.eff);
+      c1 = sh_owner(first + (g.chunks - 1) * w, end.unit0, end.eff) + 1;
+      planes = w == 2 ? 1 : NS;
+      plane = w == 2 ? f / kSharedTile & 1 : 0;
+      slot = sh_slot(p, g, kvh, pair, NS, 0) + f % kSharedTile;
+    }
   }
   const int n1 = (c1 - c0) * planes;
   // its own positions: the splits from `from` on
@@ -985,138 +988,137 @@ __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ Sh
   auto place = [&](int j) {  // of partial j < n1
     return (long long)(planes == 2 ? j & 1 : plane) * p.plane + slot + (long long)(c0 + (planes == 2 ? j >> 1 : j)) * kSharedTile;
   };
+  auto sums_of = [&](int j) { return j < n1 ? p.ml + place(j) : p.a.part_ml + own + (j - n1); };
+  auto out_of = [&](int j) { return j < n1 ? p.o + place(j) * D : p.a.part_o + (own + (j - n1)) * D; };
+  pdl_wait();
   float M = kShNone, l = 0.0f, acc[V];
   bool bad = false;  // a partial that is not finite
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.0f;
-  // this warp's partials, warp + W k: 32 references and sums at a time, then B accumulators
-  for (int k0 = 0; (kWide ? warp : 0) + W * k0 < n; k0 += 32) {
-    const int first = (kWide ? warp : 0) + W * k0, j = first + W * lane, cnt = min(32, (n - first + W - 1) / W);
+  // this warp's partials, 32 references and sums at a time, then B accumulators (whose
+  // loads need not wait for the sums: what has seen nothing is left out afterwards)
+  for (int first = mine; first < n; first += 32 * W) {
+    const int cnt = min(32, (n - first + W - 1) / W);
     float2 ml = make_float2(kShNone, 0.0f);
-    if (lane < cnt) ml = j < n1 ? __ldcg(p.ml + place(j)) : __ldcg(p.a.part_ml + own + (j - n1));
-    // (a partial that has seen nothing has no accumulators; one of NaN scores has a NaN sum)
-    const bool saw = !(ml.y == 0.0f);
-    const uint32_t some = __ballot_sync(0xffffffffu, saw);
-    float top = M;
-    float mine = saw ? ml.x : kShNone;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, o));
-    top = fmaxf(top, mine);
-    {
-      const float d = __fsub_rn(M, top), f = sh_ex2(d);
-      l = sh_times_ex2(l, d);
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = d < 0.0f ? __fmul_rn(acc[e], f) : acc[e];
-      M = top;
-    }
-    const float d = __fsub_rn(ml.x, M), f = saw ? sh_ex2(d) : 0.0f;
-    float part = saw ? sh_times_ex2(ml.y, d) : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part = __fadd_rn(part, __shfl_xor_sync(0xffffffffu, part, o));
-    l = __fadd_rn(l, part);
+    if (lane < cnt) ml = __ldcg(sums_of(first + W * lane));
+    float f = 0.0f;
+    uint32_t some = 0;
     for (int b0 = 0; b0 < cnt; b0 += B) {
       float x[B][V];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int jb = first + W * (b0 + b);
-        const bool have = b0 + b < 32 && (some >> (b0 + b)) & 1u;
 #pragma unroll
         for (int e = 0; e < V; ++e) x[b][e] = 0.0f;
-        if (have) {
-          const float* src = (jb < n1 ? p.o + place(jb) * D : p.a.part_o + (own + (jb - n1)) * D) + lane * V;
-          if constexpr (V == 2) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-            x[b][0] = v.x; x[b][1] = v.y;
-          } else {
+        if (b0 + b >= cnt) continue;
+        const float* src = out_of(first + W * (b0 + b)) + lane * V;
+        if constexpr (V == 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+          x[b][0] = v.x; x[b][1] = v.y;
+        } else {
 #pragma unroll
-            for (int e = 0; e < V; e += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + e));
-              x[b][e] = v.x; x[b][e + 1] = v.y; x[b][e + 2] = v.z; x[b][e + 3] = v.w;
-            }
+          for (int e = 0; e < V; e += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + e));
+            x[b][e] = v.x; x[b][e + 1] = v.y; x[b][e + 2] = v.z; x[b][e + 3] = v.w;
           }
         }
+      }
+      if (b0 == 0) {
+        // (a partial that has seen nothing has no accumulators; one of NaN scores has a NaN sum)
+        const bool saw = !(ml.y == 0.0f);
+        some = __ballot_sync(0xffffffffu, saw);
+        float top = saw ? ml.x : kShNone;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, M);
+        const float d0 = __fsub_rn(M, top), f0 = sh_ex2(d0), d = __fsub_rn(ml.x, top);
+        f = saw ? sh_ex2(d) : 0.0f;
+        float part = saw ? sh_times_ex2(ml.y, d) : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) part = __fadd_rn(part, __shfl_xor_sync(0xffffffffu, part, o));
+        l = __fadd_rn(sh_times_ex2(l, d0), part);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = d0 < 0.0f ? __fmul_rn(acc[e], f0) : acc[e];
+        M = top;
       }
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const float fb = __shfl_sync(0xffffffffu, f, b0 + b);
+        if (b0 + b < 32 && (some >> (b0 + b)) & 1u) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (kBf16) bad |= !(fabsf(x[b][e]) < INFINITY);
-          acc[e] = __fmaf_rn(x[b][e], fb, acc[e]);
+          for (int e = 0; e < V; ++e) {
+            if (kBf16) bad |= !(fabsf(x[b][e]) < INFINITY);
+            acc[e] = __fmaf_rn(x[b][e], fb, acc[e]);
+          }
         }
       }
     }
   }
-  float y[V];
-  bool none;
-  if constexpr (kWide) {
+  if (W > 1) {
+    const int any = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
       s_m[warp] = M;
       s_l[warp] = l;
+      s_bad[warp] = any;
     }
-    const int any = __any_sync(0xffffffffu, bad);
-    if (lane == 0) s_bad[warp] = any;
 #pragma unroll
     for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
     __syncthreads();
+  }
+  if (!row) return;
+  // the unit's warps take D / W columns each: lane's column c, c + 32, ...
+  float f[W];
+  if (W > 1) {
     M = kShNone;
 #pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w]);
+    for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w0 + w]);
     l = 0.0f;
     bad = false;
-    float f[W];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float d = __fsub_rn(s_m[w], M);
+      const float d = __fsub_rn(s_m[w0 + w], M);
       f[w] = sh_ex2(d);
-      l = __fadd_rn(l, sh_times_ex2(s_l[w], d));
-      bad |= s_bad[w] != 0;
+      l = __fadd_rn(l, sh_times_ex2(s_l[w0 + w], d));
+      bad |= s_bad[w0 + w] != 0;
     }
-    if (warp * 32 >= D) return;
-    // a warp's 32 columns
-    const int c = warp * 32 + lane;
-    float a = 0.0f, small = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-      if (!(s_l[w] == 0.0f)) {
-        a = __fmaf_rn(s_o[w][c], f[w], a);
-        small = __fmaf_rn(s_o[w][c], __fmul_rn(f[w], 0x1p-24f), small);
-      }
-    none = l == 0.0f;
-    float v = none ? 0.0f : __fdiv_rn(a, l);
-    if (kBf16 && l == l && !none && !(fabsf(a) < INFINITY))
-      v = sh_far_value<D>(p, p.a.rows.table + (size_t)seq * p.a.rows.table_stride, t, kvh, c, !bad, __fdiv_rn(small, __fmul_rn(l, 0x1p-24f)));
-    p.a.out[(int64_t)r * p.a.out_stride + hq * D + c] = __float2bfloat16_rn(v);
   } else {
-    none = l == 0.0f;
+    bad = __any_sync(0xffffffffu, bad);
+  }
+  const bool none = l == 0.0f;
+  constexpr int kCols = D / W >= 32 ? D / W / 32 : 1;
+  bf16* out = p.a.out + (int64_t)r * p.a.out_stride + hq * D;
 #pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = none ? 0.0f : __fdiv_rn(acc[e], l);
-    if (kBf16 && l == l && !none) {
-#pragma unroll 1
-      for (int e = 0; e < V; ++e) {
-        float a = 0.0f;
+  for (int k = 0; k < (W > 1 ? kCols : V / 2); ++k) {
+    float y[2];
+    int c[2];
 #pragma unroll
-        for (int k = 0; k < V; ++k) a = k == e ? acc[k] : a;
-        if (fabsf(a) < INFINITY) continue;
+    for (int e = 0; e < (W > 1 ? 1 : 2); ++e) {
+      float a = 0.0f;
+      if (W > 1) {
+        c[e] = (mine * kCols + k) * 32 + lane;
+        if (c[e] >= D) break;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (!(s_l[w0 + w] == 0.0f)) a = __fmaf_rn(s_o[w0 + w][c[e]], f[w], a);
+      } else {
+        c[e] = lane * V + 2 * k + e;
+        a = acc[2 * k + e];
+      }
+      y[e] = none ? 0.0f : __fdiv_rn(a, l);
+      if (kBf16 && l == l && !none && !(fabsf(a) < INFINITY)) {
         // the sum again, of the partials times 2^-24
         float small = 0.0f;
         for (int j = 0; j < n; ++j) {
-          const float2 ml = j < n1 ? __ldcg(p.ml + place(j)) : __ldcg(p.a.part_ml + own + (j - n1));
-          if (ml.y == 0.0f) continue;
-          const float* src = j < n1 ? p.o + place(j) * D : p.a.part_o + (own + (j - n1)) * D;
-          small = __fmaf_rn(__ldcg(src + lane * V + e), __fmul_rn(sh_ex2(__fsub_rn(ml.x, M)), 0x1p-24f), small);
+          const float2 ml = __ldcg(sums_of(j));
+          if (!(ml.y == 0.0f)) small = __fmaf_rn(__ldcg(out_of(j) + c[e]), __fmul_rn(sh_ex2(__fsub_rn(ml.x, M)), 0x1p-24f), small);
         }
-        const float v = sh_far_value<D>(p, p.a.rows.table + (size_t)seq * p.a.rows.table_stride, t, kvh, lane * V + e, !bad,
-                                        __fdiv_rn(small, __fmul_rn(l, 0x1p-24f)));
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[k] = k == e ? v : y[k];
+        y[e] = sh_far_value<D>(p, p.a.rows.table + (size_t)seq * p.a.rows.table_stride, t, kvh, c[e], !bad,
+                               __fdiv_rn(small, __fmul_rn(l, 0x1p-24f)));
       }
+      if (W > 1) out[c[e]] = __float2bfloat16_rn(y[e]);
     }
-    bf16* out = p.a.out + (int64_t)r * p.a.out_stride + hq * D + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
+    if (W == 1) *reinterpret_cast<uint32_t*>(out + c[0]) = pack_bf16x2(y[0], y[1]);
   }
-  if (p.a.lse && lane == 0 && warp == (kWide ? 0 : warp))
+  if (p.a.lse && lane == 0 && mine == 0)
     p.a.lse[(size_t)r * H + hq] = none ? -INFINITY : __fmul_rn(__fadd_rn(M, log2f(l)), 0.6931471805599453f);
 }
 
@@ -1147,12 +1149,10 @@ cudaError_t shared_launch(const SharedParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_shared_prefix<D, FMT>, p, km, vm);
 }
 
-template <int D>
-cudaError_t shared_merge_launch(const SharedParams& p, int num_sms, cudaStream_t s) {
+template <int D, int W>
+cudaError_t shared_merge_t(const SharedParams& p, int64_t units, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t units = (int64_t)(p.a.row_hi - p.a.row_lo) * p.a.n_q_heads;
-  const bool wide = units <= 32 * (int64_t)num_sms;
-  cfg.gridDim = dim3((unsigned)(wide ? units : (units + 7) / 8));
+  cfg.gridDim = dim3((unsigned)((units * W + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1160,11 +1160,17 @@ cudaError_t shared_merge_launch(const SharedParams& p, int num_sms, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (wide)
-    return p.a.k_exp ? cudaLaunchKernelEx(&cfg, k_shared_merge<D, false, true>, p)
-                     : cudaLaunchKernelEx(&cfg, k_shared_merge<D, true, true>, p);
-  return p.a.k_exp ? cudaLaunchKernelEx(&cfg, k_shared_merge<D, false, false>, p)
-                   : cudaLaunchKernelEx(&cfg, k_shared_merge<D, true, false>, p);
+  return p.a.k_exp ? cudaLaunchKernelEx(&cfg, k_shared_merge<D, false, W>, p) : cudaLaunchKernelEx(&cfg, k_shared_merge<D, true, W>, p);
+}
+
+// Warps for a result: as many as the device holds at once, at most eight.
+template <int D>
+cudaError_t shared_merge_launch(const SharedParams& p, int num_sms, cudaStream_t s) {
+  const int64_t units = (int64_t)(p.a.row_hi - p.a.row_lo) * p.a.n_q_heads, most = 16 * (int64_t)num_sms;
+  if (units * 8 <= most) return shared_merge_t<D, 8>(p, units, s);
+  if (units * 4 <= most) return shared_merge_t<D, 4>(p, units, s);
+  if (units * 2 <= most) return shared_merge_t<D, 2>(p, units, s);
+  return shared_merge_t<D, 1>(p, units, s);
 }
 
 }  // namespace

@@ -191,6 +191,14 @@ int64_t shared_bytes(const RowBatch& b, int n_groups, int n_q_heads, int head_di
          round256(rows * (int64_t)sizeof(float2)) + rows * head_dim * (int64_t)sizeof(float);
 }
 
+// Whether a call is so small that attending to each sequence by itself is faster
+// than the four launches of a shared prefix: by what k_attend has to do at most,
+// tiles of 16 query rows times positions that the tables reach.
+bool attend_alone(const RowBatch& b, int group, int n_kv_heads) {
+  const int64_t tiles = b.n_seq * (((int64_t)b.max_rows * group + 15) / 16) * n_kv_heads;
+  return tiles <= (int64_t(1) << 18) / b.limit();
+}
+
 // Groups of sequences: as many as there are sequences at most.
 bool read_prefix(const sv_shared_prefix* a, const RowBatch& b) {
   if (!a || a->n_groups < 1 || a->n_groups > b.n_seq || !a->length) return false;
@@ -307,7 +315,8 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
   sp.ml = reinterpret_cast<float2*>(take(sp.plane * shared_streams(c.head_dim) * (int64_t)sizeof(float2)));
   sp.o = reinterpret_cast<float*>(at);
   sp.grid = std::min(num_sms, kSharedMostCtas);
-  const bool share = shared_units_fit(p.rows, sp.n_groups, n_q_heads, c.n_kv_heads, c.head_dim);
+  const bool share = !attend_alone(p.rows, n_q_heads / c.n_kv_heads, c.n_kv_heads) &&
+                     shared_units_fit(p.rows, sp.n_groups, n_q_heads, c.n_kv_heads, c.head_dim);
   if (share) p.from = sp.from;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   sp.a = p;

@@ -23,9 +23,13 @@ def f64(t):
 
 
 class Case:
-    """Groups of sequences: groups = [(shared positions, [(first, rows), ...]), ...]."""
+    """Groups of sequences: groups = [(shared positions, [(first, rows), ...]), ...].
 
-    def __init__(self, seed, n_q, n_kv, d, groups, fmt="e4m3", block=1, back=0, spread=2.0, slack=0, alone=()):
+    wide: the tables are made wide enough that the call goes through the kernels of
+    shared prefixes (by what the tables reach, see attend_alone in sv_paged.cu);
+    else they end with the longest sequence, and small calls are attend's."""
+
+    def __init__(self, seed, n_q, n_kv, d, groups, fmt="e4m3", block=1, back=0, spread=2.0, slack=0, alone=(), wide=True):
         sv = _sv()
         g = self.g = torch.Generator().manual_seed(seed)
         self.n_q, self.n_kv, self.d, self.fmt = n_q, n_kv, d, fmt
@@ -45,6 +49,11 @@ class Case:
             at += n
             i += len(members)
             self.start_of.append(i)
+        if wide:
+            tiles = n_seq * n_kv * -(-max(max(self.lens), 1) * (n_q // n_kv) // 16)
+            more = (1 << 18) // tiles // PAGE + 1 - width
+            if more > 0:
+                table = torch.cat([table, torch.full((n_seq, more), -1, dtype=torch.int32)], 1)
         self.table_h = table
         n = sum(self.lens)
         self.n_rows = n + back
@@ -130,6 +139,16 @@ def test_shared(fmt, block, n_q, n_kv, d, batch):
     if batch in ("long", "wide") and (n_q, n_kv, d) not in ((4, 2, 64), (7, 1, 128), (8, 1, 256)):
         pytest.skip("the 64-bit form of the wider ones takes long")
     Case(3, n_q, n_kv, d, BATCHES[batch], fmt, block, back=2, alone=((37, 1),)).check()
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("batch", ["ends inside", "groups", "padding", "rows within the prefix"])
+def test_small_calls(fmt, block, batch):
+    c = Case(4, 8, 2, 128, BATCHES[batch], fmt, block, back=1, wide=False)
+    q, out, lse = c.check()
+    o, l = c.plain(q)
+    n = c.start[-1]
+    assert torch.equal(out[:n], o[:n]) and torch.equal(lse[:n], l[:n])
 
 
 @pytest.mark.parametrize("fmt,block", FORMS)
