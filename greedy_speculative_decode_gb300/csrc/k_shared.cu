@@ -101,7 +101,9 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
       const int mid = (lo + hi) >> 1;
       if (s_unit[mid] <= u) lo = mid; else hi = mid;
     }
-    p.begin[tid] = make_int2(u, lo);
+    p.begin[tid].unit = u;
+    p.begin[tid].group = lo;
+    p.begin[tid].g = p.plan[lo];  // (written by this block before the barrier)
   }
   if (tid < S) p.from[tid] = gi >= 0 ? s_eff[gi] : 0;
 }

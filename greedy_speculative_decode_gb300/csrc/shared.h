@@ -21,6 +21,12 @@ struct SharedGroup {
   int unused;
 };
 
+// Where a CTA's run begins: the unit, its group, and a copy of that.
+struct SharedBegin {
+  int unit, group, unused[2];
+  SharedGroup g;
+};
+
 struct SharedParams {
   AttendParams a;  // q, out, lse, the pool, and the partials of the rows' own positions
   int n_groups;
@@ -30,7 +36,7 @@ struct SharedParams {
   SharedGroup* plan;  // [n_groups + 1]
   int* from;          // [n_seq] first position of a sequence that is not shared
   int* group;         // [n_seq] its group, or -1
-  int2* begin;        // [grid + 1] the unit that a CTA's run begins with, and its group
+  SharedBegin* begin; // [grid + 1]
   float2* ml;         // [streams][plane] a segment's references and sums
   float* o;           // [streams][plane][head_dim]
   int64_t plane;      // rows of a stream's

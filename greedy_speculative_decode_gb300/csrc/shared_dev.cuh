@@ -97,6 +97,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// A value that all lanes of a warp have, in a uniform register (a reduction's result
+// is one): descriptors worked out from such values cost the multiplying warp a few
+// instructions, not a move for each operand of each multiply.
+__device__ __forceinline__ uint32_t sh_uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // A whole warp's wait.  Its lanes go on together: one that fell behind, and that
 // nothing else waits for, could otherwise look for a phase when the next but one
 // has already come, which has the same parity.
@@ -148,11 +153,11 @@ struct ShRun {
   int gi;     // group that u is in
   SharedGroup g;
   __device__ __forceinline__ ShRun(const SharedParams& p, int cta) : plan(p.plan), n_kv(p.a.n_kv_heads) {
-    const int2 a = __ldcg(p.begin + cta), b = __ldcg(p.begin + cta + 1);
+    const int2 a = __ldcg(reinterpret_cast<const int2*>(p.begin + cta));
+    hi = __ldcg(&p.begin[cta + 1].unit);
+    g = sh_group(&p.begin[cta].g, 0);
     u = a.x;
     gi = a.y;
-    hi = b.x;
-    if (u < hi) g = sh_group(plan, gi);
   }
   __device__ __forceinline__ bool next(ShSegment& s) {
     while (u < hi) {
@@ -257,32 +262,27 @@ struct ShItems {
   uint32_t chunk_no, chunk0;  // chunks before the segment; number of the item's chunk
   int c;                      // the item's chunk within its segment
   bool is_v, more;
-  __device__ __forceinline__ ShItems(const SharedParams& p) : run(p, blockIdx.x), ord{0, false}, i(0), at(0), chunk_no(0) {
-    more = run.next(s);
-    if (more) ord = {s.i1 - s.i0, s.w == 2};
-    look();
-  }
-  __device__ __forceinline__ void look() {
-    if (!more) return;
-    c = ord.item(i, is_v);
-    chunk0 = chunk_no + c;
-  }
+  __device__ __forceinline__ ShItems(const SharedParams& p)
+      : run(p, blockIdx.x), ord{0, false}, i(-1), at(0xffffffffu), chunk_no(0), more(true) {}
+  // To the next item (the first one at first); more: there is one.
   __device__ __forceinline__ void step() {
     ++at;
     if (++i == 2 * ord.n) {
       chunk_no += ord.n;
       i = 0;
       more = run.next(s);
-      if (more) ord = {s.i1 - s.i0, s.w == 2};
+      if (!more) return;
+      ord = {s.i1 - s.i0, s.w == 2};
     }
-    look();
+    c = ord.item(i, is_v);
+    chunk0 = chunk_no + c;
   }
 };
 
 // A warp for K and one for V.  Lane l < kPages looks up page l of a chunk; its part
 // of the operand: boxes of a bf16 page straight into the operand's layout (a page
 // that is not there reads as zeros: a row beyond the tensor), or an 8-bit page's
-// codes.  Page numbers are looked up two operands ahead, exponents one.
+// codes.  Page numbers are looked up two operands ahead.
 template <class C, bool kValues>
 __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShSmem<C>& sm, uint32_t& end) {
   const int lane = threadIdx.x & 31;
@@ -293,48 +293,50 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
     bool there, wanted;  // there: an item at all; wanted: with a page for this lane
     uint32_t at, chunk;
   };
-  auto look = [&]() {
-    while (it.more && it.is_v != kValues) it.step();
-    Item r = {-1, 0, it.more, false, it.at, 0};
-    if (!it.more) return r;
-    const int pos = (it.s.i0 + it.c) * C::CP + lane * kPage;
-    r.wanted = lane < C::kPages && pos < it.s.g.eff;
-    if (r.wanted) r.page = __ldg(p.a.rows.table + (size_t)it.s.g.s0 * p.a.rows.table_stride + pos / kPage);
-    r.kvh = it.s.kvh;
-    r.chunk = it.chunk0;
-    it.step();
-    return r;
-  };
-  uint4 ke = make_uint4(0u, 0u, 0u, 0u), ve = ke;
-  auto exponents = [&](const Item& x, uint4& k, uint4& v) {
-    k = v = make_uint4(0u, 0u, 0u, 0u);
-    if (C::kBf16 || (uint32_t)x.page >= (uint32_t)p.a.n_pages) return;
-    const size_t ph = (size_t)x.page * p.a.n_kv_heads + x.kvh;
-    if (p.a.block == 1) {
-      k = __ldg(reinterpret_cast<const uint4*>(p.a.k_exp) + ph);
-      v = __ldg(reinterpret_cast<const uint4*>(p.a.v_exp) + ph);
-    } else {
-      const uint32_t a = __ldg(p.a.k_exp + ph) * 0x01010101u, b = __ldg(p.a.v_exp + ph) * 0x01010101u;
-      k = make_uint4(a, a, a, a);
-      v = make_uint4(b, b, b, b);
-    }
-  };
-  Item now = look(), next = look();
-  exponents(now, ke, ve);
+  Item now = {-1, 0, false, false, 0, 0}, next = now;
   bool ok = true;
   constexpr uint32_t kRing = C::kBf16 ? C::kOps : C::kRaws;
   const uint64_t pol = policy_evict_last();
   end = 0;  // behind the last operand asked for
-  while (now.there) {
-    const Item far = look();
-    uint4 ke1, ve1;
-    exponents(next, ke1, ve1);
+  for (int k = 0;; ++k) {
+    // the operand two on: its page numbers
+    Item far = {-1, 0, false, false, 0, 0};
+    do {
+      if (it.more) it.step();
+    } while (it.more && it.is_v != kValues);
+    if (it.more) {
+      const int pos = (it.s.i0 + it.c) * C::CP + lane * kPage;
+      far.there = true;
+      far.wanted = lane < C::kPages && pos < it.s.g.eff;
+      if (far.wanted) far.page = __ldg(p.a.rows.table + (size_t)it.s.g.s0 * p.a.rows.table_stride + pos / kPage);
+      far.kvh = it.s.kvh;
+      far.at = it.at;
+      far.chunk = it.chunk0;
+    }
+    if (!now.there) {  // (the first two rounds, or the end)
+      if (k >= 2) break;
+      now = next;
+      next = far;
+      continue;
+    }
     const uint32_t at = now.at;
     const int st = at % kRing;
     ok = at < kRing || sh_wait(C::kBf16 ? sm.op_empty(st) : sm.raw_empty(st), ((at / kRing) & 1u) ^ 1u);
     if (!ok) break;
     end = at + 1;
     const bool have = (uint32_t)now.page < (uint32_t)p.a.n_pages;
+    uint4 ke = make_uint4(0u, 0u, 0u, 0u), ve = ke;
+    if (!C::kBf16 && have) {
+      const size_t ph = (size_t)now.page * p.a.n_kv_heads + now.kvh;
+      if (p.a.block == 1) {
+        ke = __ldg(reinterpret_cast<const uint4*>(p.a.k_exp) + ph);
+        ve = __ldg(reinterpret_cast<const uint4*>(p.a.v_exp) + ph);
+      } else {
+        const uint32_t a = __ldg(p.a.k_exp + ph) * 0x01010101u, b = __ldg(p.a.v_exp + ph) * 0x01010101u;
+        ke = make_uint4(a, a, a, a);
+        ve = make_uint4(b, b, b, b);
+      }
+    }
     if (!kValues && !have && now.wanted && p.a.status) atomicOr(p.a.status, ST_BAD_PAGE);
     const uint32_t there = __ballot_sync(0xffffffffu, have);
     uint32_t meta = there | kShEven;
@@ -355,6 +357,16 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
           if (lead) tma_load_2d(sm.op(st) + h * C::CP * 128 + pg * kPage * 128, map, h * 64, r, sm.op_full(st), pol);
       }
     } else {
+      if (lead) mbar_arrive_expect_tx(sm.raw_full(st), (uint32_t)__popc(there) * kPage * C::D);
+      __syncwarp();
+      const uint8_t* pool = kValues ? p.a.v : p.a.k;
+#pragma unroll 1
+      for (int pg = 0; pg < C::kPages; ++pg) {
+        const int r = __shfl_sync(0xffffffffu, row, pg);
+        if (lead && (there >> pg & 1u))
+          bulk_load(sm.raw(st) + pg * kPage * C::D, pool + (size_t)r * C::D, kPage * C::D, sm.raw_full(st));
+      }
+      // the exponents, while the codes are on their way
       // (bytes below the writer's smallest, as a zeroed cache has, count as that one for values)
       const uint32_t least = kExpMinByte * 0x01010101u;
       ve = make_uint4(__vmaxu4(ve.x, least), __vmaxu4(ve.y, least), __vmaxu4(ve.z, least), __vmaxu4(ve.w, least));
@@ -376,20 +388,10 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
       }
       if (lead) sm.raw_meta()[st] = meta;
       __syncwarp();
-      if (lead) mbar_arrive_expect_tx(sm.raw_full(st), (uint32_t)__popc(there) * kPage * C::D);
-      __syncwarp();
-      const uint8_t* pool = kValues ? p.a.v : p.a.k;
-#pragma unroll 1
-      for (int pg = 0; pg < C::kPages; ++pg) {
-        const int r = __shfl_sync(0xffffffffu, row, pg);
-        if (lead && (there >> pg & 1u))
-          bulk_load(sm.raw(st) + pg * kPage * C::D, pool + (size_t)r * C::D, kPage * C::D, sm.raw_full(st));
-      }
+      if (lead) mbar_arrive(sm.raw_full(st));
     }
     now = next;
     next = far;
-    ke = ke1;
-    ve = ve1;
   }
   return ok;
 }
@@ -409,7 +411,10 @@ __device__ void sh_load_drain(const ShSmem<C>& sm, uint32_t end) {
 template <class C>
 __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
   const int tid = threadIdx.x & 127;
-  for (ShItems<C> it(p); it.more; it.step()) {
+  ShItems<C> it(p);
+  for (;;) {
+    it.step();
+    if (!it.more) break;
     const uint32_t c = it.chunk0, at = it.at;
     const int st = at % C::kRaws, os = at % C::kOps;
     if (!sh_wait(sm.raw_full(st), (at / C::kRaws) & 1u)) return false;
@@ -484,15 +489,15 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
   constexpr int CP = C::CP, D = C::D;
   constexpr uint32_t kScores = sh_idesc<C>(CP, false), kValues = sh_idesc<C>(D, true);
   const uint32_t lead = tc_elect();
-  tmem = __shfl_sync(0xffffffffu, tmem, 0);
+  tmem = sh_uniform(tmem);
   ShRun<C::NS> run(p, blockIdx.x);
   ShSegment s;
   uint32_t at0 = 0, seg = 0;
   bool ok = true;
   uint32_t used0 = 0, used1 = 0;  // uses of each score place so far
-  const uint32_t q_base = __shfl_sync(0xffffffffu, smem_u32(sm.q(0)), 0), op_base = __shfl_sync(0xffffffffu, smem_u32(sm.op(0)), 0);
+  const uint32_t q_base = sh_uniform(smem_u32(sm.q(0))), op_base = sh_uniform(smem_u32(sm.op(0)));
   while (ok && run.next(s)) {
-    const ShOrder ord{__shfl_sync(0xffffffffu, s.i1 - s.i0, 0), __shfl_sync(0xffffffffu, s.w, 0) == 2};
+    const ShOrder ord{(int)sh_uniform(s.i1 - s.i0), sh_uniform(s.w) == 2u};
     const int n = ord.steps();
     auto scores = [&](int j) {
       const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
@@ -509,8 +514,8 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
       if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
       return true;
     };
-    ok = scores(0) && (n < 2 || scores(1));
-    for (int j = 0; j < n && ok; ++j) {
+    for (int j = -2; j < n && ok; ++j) {
+      if (j >= 0) {
       const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
       const uint32_t at = at0 + ord.v_at(c);
       ok = sh_wait(sm.p_full(x), (x ? used1 : used0) & 1u) && sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u);
@@ -527,6 +532,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
           tc_mma_ts_if(lead, o, w + (k / 2) * 32 + t * 16 + (k % 2) * 8, b + (k * 16 * 128 >> 4), kValues, j >= C::NS || t > 0 || k > 0);
       tc_commit_if(lead, sm.pv_done(x));
       if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
+      }
       if (j + 2 < n) ok = scores(j + 2);
     }
     at0 += 2 * ord.n;
@@ -809,15 +815,34 @@ struct ShSoft {
       if (!sh_wait(sm.pv_done(y), (steps(y) - 1u) & 1u)) return false;
       tc_fence_after();
       const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
+      // through the warp's part of the stream's queries, which have done their work: 16
+      // columns of its 32 rows at a time, so that a store writes 64 bytes of eight rows
+      const int lane = threadIdx.x & 31;
+      const uint32_t stage = smem_u32(sm.q(x)) + ((threadIdx.x >> 5) & 7) * (C::kQBytes / 8);
+      const int rows = s.g.R - (f - lane);  // of the warp's that are there
+      float* out = p.o + (at - lane) * D;
 #pragma unroll 1
       for (int c = h * D / 2; c < (h + 1) * D / 2; c += 32) {
         uint32_t v[32];
         tc_ld32(o + c, v);
         tc_wait_ld();
-        if (f < s.g.R) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)), "r"(v[16 * k + 4 * e]),
+                         "r"(v[16 * k + 4 * e + 1]), "r"(v[16 * k + 4 * e + 2]), "r"(v[16 * k + 4 * e + 3])
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = e * 8 + lane / 4, u = lane & 3;
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(stage + row * 64 + ((u ^ ((row >> 1) & 3)) << 4)));
+            if (row < rows) *reinterpret_cast<uint4*>(out + row * D + c + 16 * k + 4 * u) = w;
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -871,7 +896,7 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
       mbar_init(sm.op_empty(i), 1);
     }
     for (int i = 0; i < C::kRaws; ++i) {
-      mbar_init(sm.raw_full(i), 1);
+      mbar_init(sm.raw_full(i), 2);  // (the codes are asked for, the exponents are there)
       mbar_init(sm.raw_empty(i), 128);
     }
     for (int i = 0; i < C::kRings; ++i) mbar_init(sm.sc_empty(i), C::kSoftWarps);

@@ -187,7 +187,7 @@ int64_t shared_bytes(const RowBatch& b, int n_groups, int n_q_heads, int head_di
   *plane = (int64_t)b.n_rows * n_q_heads + (int64_t)kSharedMostCtas * kSharedTile;
   const int64_t rows = *plane * shared_streams(head_dim);
   return round256((n_groups + 1) * (int64_t)sizeof(SharedGroup)) + round256(2 * 4 * (int64_t)b.n_seq) +
-         round256((kSharedMostCtas + 1) * (int64_t)sizeof(int2)) +
+         round256((kSharedMostCtas + 1) * (int64_t)sizeof(SharedBegin)) +
          round256(rows * (int64_t)sizeof(float2)) + rows * head_dim * (int64_t)sizeof(float);
 }
 
@@ -311,7 +311,7 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
   sp.plan = reinterpret_cast<SharedGroup*>(take((sp.n_groups + 1) * (int64_t)sizeof(SharedGroup)));
   sp.from = reinterpret_cast<int*>(take(2 * 4 * (int64_t)p.rows.n_seq));
   sp.group = sp.from + p.rows.n_seq;
-  sp.begin = reinterpret_cast<int2*>(take((kSharedMostCtas + 1) * (int64_t)sizeof(int2)));
+  sp.begin = reinterpret_cast<SharedBegin*>(take((kSharedMostCtas + 1) * (int64_t)sizeof(SharedBegin)));
   sp.ml = reinterpret_cast<float2*>(take(sp.plane * shared_streams(c.head_dim) * (int64_t)sizeof(float2)));
   sp.o = reinterpret_cast<float*>(at);
   sp.grid = std::min(num_sms, kSharedMostCtas);
