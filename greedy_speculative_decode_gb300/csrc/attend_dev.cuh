@@ -826,7 +826,7 @@ template <class C>
 __device__ void attend_cta(const AttendParams& p, const AttendWork<C>& wk, uint8_t* smem) {
   constexpr int S = C::kStages, PW = C::PW;
   AttendPlace<C> at;
-  bool waited = !p.early;
+  bool waited = !p.early || p.free;
   if (!at.start(wk)) {
     if (!waited) pdl_wait();  // so that the grid completes in order
     return;
@@ -970,12 +970,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendCfg<D, FMT, N>::kPerSm) 
   uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 127u);
   int* before = reinterpret_cast<int*>(smem + C::kOffSeq);
   pdl_trigger();
-  if (!p.early) pdl_wait();
+  if (!p.early && !p.free) pdl_wait();
   const int S = p.rows.n_seq, G = p.n_q_heads / p.n_kv_heads;
   int *first = before + S + 1, *start = first + S;  // (S + 1 starts)
   AttendWork<C> wk{p, before, first, start, 0, G};
   wk.total = attend_plan<C>(p, G, before, first, start);
   attend_cta<C>(p, wk, smem);
+  if (p.free) pdl_wait();  // (grids complete in order)
 }
 
 // Column c of a row's output over a bf16 cache where the sum of its splits came

@@ -12,7 +12,8 @@ namespace {
 // thread a sequence, then one a group.
 __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ SharedParams p, int chunk, int streams) {
   __shared__ int s_eff[1024], s_start[1025];
-  __shared__ int s_sum[32], s_unit[1025];
+  __shared__ int s_sum[32], s_sum2[32], s_unit[1025], s_list[1025];  // units and lists before each group
+  __shared__ int2 s_first[256];  // of each list, where CTAs' runs end with lists: its first unit, and CTA
   const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
   pdl_trigger();
   auto start_of = [&](int s) { return p.a.rows.row_start ? __ldg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
@@ -22,7 +23,7 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
     first = first_of(p.a.rows, tid);
     n = start_of(tid + 1) - start_of(tid);
   }
-  if (tid < 32) s_sum[tid] = 0;
+  if (tid < 32) s_sum[tid] = s_sum2[tid] = 0;
   for (int g = tid; g <= N; g += blockDim.x)
     s_start[g] = p.group_start ? min(max(__ldg(p.group_start + g), 0), S) : (int)((long long)S * g / N);
   if (tid < N) {
@@ -65,45 +66,85 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   }
   // A CTA has whole chunks: two units, where a list has two tiles.
   const int least = __syncthreads_or(units > 0 && g.tiles > 1) ? streams : 1;
-  // units before each group
+  // units and lists before each group
   const int lane = tid & 31, warp = tid >> 5;
-  int x = units;
+  const int lists = units > 0 ? p.a.n_kv_heads * ((g.tiles + streams - 1) / streams) : 0;
+  int x = units, y = lists;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
   }
-  if (lane == 31) s_sum[warp] = x;
+  if (lane == 31) {
+    s_sum[warp] = x;
+    s_sum2[warp] = y;
+  }
   __syncthreads();
-  int before = 0, all = 0;
+  int before = 0, all = 0, before2 = 0, all2 = 0;
 #pragma unroll
   for (int w = 0; w < 32; ++w) {
     before += w < warp ? s_sum[w] : 0;
+    before2 += w < warp ? s_sum2[w] : 0;
     all += s_sum[w];
+    all2 += s_sum2[w];
   }
   const int ctas = min(p.grid, max(all / least, 1));
+  // Lists of at least a CTA's share each: then a CTA works on one alone.
+  const int small = g.chunks * (g.tiles % streams ? g.tiles % streams : streams);
+  const int aligned = __syncthreads_and(units == 0 || (long long)small * ctas >= all) && all2 <= ctas;
   if (tid < N) {
     g.unit0 = before + x - units;
     s_unit[tid] = g.unit0;
+    s_list[tid] = before2 + y - lists;
     p.plan[tid] = g;
   }
   if (tid == 0) {
     SharedGroup end = {};
     end.unit0 = all;
     end.eff = ctas;
+    end.aligned = aligned;
     p.plan[N] = end;
   }
   __syncthreads();
-  if (tid <= p.grid) {  // where each CTA's run begins
-    const int u = tid < ctas ? (int)((unsigned long long)all * tid / ctas) : all;
-    int lo = 0, hi = N;  // the last group that begins at or before it
+  auto last_at = [](const int* v, int n, int u) {  // the last of n that is at most u
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_unit[mid] <= u) lo = mid; else hi = mid;
+      if (v[mid] <= u) lo = mid; else hi = mid;
     }
+    return lo;
+  };
+  if (aligned && tid < all2) {
+    const int gi = last_at(s_list, N, tid);
+    const SharedGroup q = p.plan[gi];  // (written by this block before the barrier)
+    const int pairs = (q.tiles + streams - 1) / streams, i = tid - s_list[gi];
+    const int u = q.unit0 + i / pairs * q.chunks * q.tiles + i % pairs * streams * q.chunks;
+    s_first[tid] = make_int2(u, sh_first(u, all, ctas));
+  }
+  __syncthreads();
+  if (tid <= p.grid) {  // where each CTA's run begins
+    int u = all;
+    if (tid < ctas && all > 0) {
+      u = (int)((unsigned long long)all * tid / ctas);
+      if (aligned) {
+        int lo = 0, hi = all2;  // its list
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_first[mid].y <= tid) lo = mid; else hi = mid;
+        }
+        const int2 a = s_first[lo], b = lo + 1 < all2 ? s_first[lo + 1] : make_int2(all, ctas);
+        const SharedGroup q = p.plan[last_at(s_unit, N, a.x)];
+        const int w = (b.x - a.x) / q.chunks;  // its tiles
+        u = a.x + (int)((long long)q.chunks * (tid - a.y) / (b.y - a.y)) * w;
+      }
+    }
+    const int lo = last_at(s_unit, N, u);
     p.begin[tid].unit = u;
     p.begin[tid].group = lo;
-    p.begin[tid].g = p.plan[lo];  // (written by this block before the barrier)
+    p.begin[tid].g = p.plan[lo];
   }
   if (tid < S) p.from[tid] = gi >= 0 ? s_eff[gi] : 0;
 }

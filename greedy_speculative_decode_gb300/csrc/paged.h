@@ -81,6 +81,7 @@ struct AttendParams {
   // First position of each sequence that this launch takes ([n_seq], multiples of
   // the page), or null: those before are another kernel's, which merges too.
   const int* from;
+  bool free;  // nothing of the kernel ahead of this one is read or overwritten: it is waited for at the end
 };
 
 cudaError_t prepare_attend_kernels();

@@ -18,7 +18,7 @@ struct SharedGroup {
   int s0;        // its first sequence, whose table is read
   int row0, R;   // its first row, and its query rows for a kv head
   int chunks, tiles;
-  int unused;
+  int aligned;   // behind the last group: whether CTAs' runs end with lists (sh_first)
 };
 
 // Where a CTA's run begins: the unit, its group, and a copy of that.

@@ -26,8 +26,11 @@
 // their row's largest value; sums, references and accumulators are fp32.
 //
 // Work is divided as chunks of all (group, kv head, tiles) lists one behind the
-// other, in equal runs for the CTAs; each CTA leaves a partial (reference, sum,
+// other.  Where every list is enough for a CTA each has a number of them for itself,
+// else all lists are cut into equal runs.  Each CTA leaves a partial (reference, sum,
 // accumulators) for each list its run touches, and the merge adds them in order.
+// (A new list costs a CTA some 5 us: queries, and a partial.  Equal runs throughout:
+// 71 us for 128 x 1 behind 16384, now XX; XX and XX for 64 x 4 behind 4096.)
 #pragma once
 #include "paged_dev.cuh"
 #include "shared.h"
@@ -136,13 +139,18 @@ __device__ __forceinline__ SharedGroup sh_group(const SharedGroup* plan, int g) 
   SharedGroup r;
   const int4* src = reinterpret_cast<const int4*>(plan + g);
   const int4 a = __ldcg(src), b = __ldcg(src + 1);
-  r.unit0 = a.x; r.eff = a.y; r.s0 = a.z; r.row0 = a.w; r.R = b.x; r.chunks = b.y; r.tiles = b.z;
+  r.unit0 = a.x; r.eff = a.y; r.s0 = a.z; r.row0 = a.w; r.R = b.x; r.chunks = b.y; r.tiles = b.z; r.aligned = b.w;
   return r;
 }
 
-// CTA that has unit u of U, of G CTAs: the run of CTA c begins with unit U c / G.
+// Of G CTAs and U units: the CTA that has unit u where runs are equal (that of CTA c
+// begins with unit U c / G), and the first CTA of a list that begins with unit u where
+// they end with lists.
 __device__ __forceinline__ int sh_owner(int u, int U, int G) {
   return (int)((((unsigned long long)u + 1) * G - 1) / (unsigned)U);
+}
+__device__ __forceinline__ int sh_first(int u, int U, int G) {
+  return (int)((2ull * u * G + U) / (2ull * U));
 }
 
 template <int NS>
@@ -998,8 +1006,13 @@ __global__ void __launch_bounds__(256) k_shared_merge(const __grid_constant__ Sh
       const SharedGroup g = sh_group(p.plan, gi);
       const int f = (r - g.row0) * G + hq % G, pair = f / (NS * kSharedTile), w = min(NS, g.tiles - pair * NS);
       const int first = g.unit0 + kvh * g.chunks * g.tiles + pair * NS * g.chunks;
-      c0 = sh_owner(first, end.unit0, end.eff);
-      c1 = sh_owner(first + (g.chunks - 1) * w, end.unit0, end.eff) + 1;
+      if (end.aligned) {
+        c0 = sh_first(first, end.unit0, end.eff);
+        c1 = sh_first(first + g.chunks * w, end.unit0, end.eff);
+      } else {
+        c0 = sh_owner(first, end.unit0, end.eff);
+        c1 = sh_owner(first + (g.chunks - 1) * w, end.unit0, end.eff) + 1;
+      }
       planes = w == 2 ? 1 : NS;
       plane = w == 2 ? f / kSharedTile & 1 : 0;
       slot = sh_slot(p, g, kvh, pair, NS, 0) + f % kSharedTile;

@@ -324,6 +324,7 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
   for (int lo = 0; lo < p.rows.n_rows; lo += each) {
     p.row_lo = lo;
     p.row_hi = std::min(lo + each, p.rows.n_rows);
+    p.free = share && lo == 0;  // (behind the prefix's kernel; later blocks overwrite what a merge reads)
     sp.a = p;
     if (launch_attend(p, c.fmt, c.head_dim, num_sms, s, share) != cudaSuccess ||
         (share && launch_shared_merge(sp, c.head_dim, num_sms, s) != cudaSuccess))
