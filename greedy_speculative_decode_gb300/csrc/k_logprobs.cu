@@ -10,14 +10,14 @@
 // lanes, warps and CTAs are added up in a fixed order.
 //
 // The k most probable tokens come from the same pass: it leaves the largest
-// logit of each of at most 512 chunks of the row (consecutive ids) in shared
+// logit of each of at most 512 chunks (128 of a short row) (consecutive ids) in shared
 // memory.  The k-th largest of those is a bound that every one of the k reaches;
 // at most k chunks have to be read again (from L2), those above the bound and,
 // of those equal to it, the first: k tokens of theirs are at least as probable
 // as any of a later one, with lower ids.
 //
 // What bounds it: memory for many rows, the chain of load, meeting and second
-// look for a few.  A row is a cluster of 1 to 16 CTAs, so that few rows fill the
+// look for a few.  A row is a cluster of 1 to 8 CTAs, so that few rows fill the
 // device too; they meet over distributed shared memory.
 #include "sv_internal.h"
 #include "sv_ptx.cuh"
@@ -32,10 +32,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
-constexpr int kLpChunks = kLpThreads;  // of a row: a thread looks at one each
+// Threads of a CTA: 128 for short rows, of which an SM then holds more.
+constexpr int kLpWide = 512, kLpNarrow = 128;
 constexpr int kLpMost = kLogprobsMaxTop;
 constexpr float kLpNone = -3.0e38f;  // reference of what has seen nothing
+constexpr float kLpSlack = 4.0f;    // log2 of what a weight may be before the reference follows
 static_assert(kLpMost == 32, "a lane holds one of a warp's best");
 
 __device__ __forceinline__ float lp_ex2(float x) {
@@ -71,6 +72,13 @@ struct LpVec<float> {
     x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ float largest(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  // word i of the 16 bytes from element v, where only lo .. hi - 1 are there
+  static __device__ __forceinline__ uint32_t part(const float* p, int v, int i, int lo, int hi) {
+    return v + i >= lo && v + i < hi ? __float_as_uint(__ldg(p + v + i)) : 0xff800000u;
+  }
 };
 template <>
 struct LpVec<bf16> {
@@ -84,36 +92,49 @@ struct LpVec<bf16> {
     }
   }
   static __device__ __forceinline__ float one(const bf16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ float largest(const uint4& w) {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t part(const bf16* p, int v, int i, int lo, int hi) {
+    uint32_t w = 0;
+    for (int e = 0; e < 2; ++e) {
+      const int at = v + 2 * i + e;
+      w |= (at >= lo && at < hi ? (uint32_t)__bfloat16_as_ushort(p[at]) : 0xff80u) << (16 * e);
+    }
+    return w;
+  }
 };
 
 // A row in blocks of 32 N elements from the 16-byte boundary at or before its
 // first one: element v of that count is token v - lead.
-template <class T>
+template <class T, int TH>
 struct LpRow {
   static constexpr int N = LpVec<T>::N, kBlock = 32 * N;
   const T* base;
-  int lead, vocab, blocks, per, chunks;  // per: blocks of a chunk
+  int lead, vocab, blocks, shift, chunks;  // 2^shift: blocks of a chunk; a thread looks at one chunk
   __device__ __forceinline__ LpRow(const T* row, int vocab_) : vocab(vocab_) {
     lead = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
     base = row - lead;
     blocks = (int)(((int64_t)lead + vocab + kBlock - 1) / kBlock);
-    per = (blocks + kLpChunks - 1) / kLpChunks;
-    chunks = (blocks + per - 1) / per;
+    shift = 0;
+    while (blocks > TH << shift) ++shift;
+    chunks = (blocks + (1 << shift) - 1) >> shift;
   }
-  // This lane's part of block b is whole, to be loaded as 16 bytes; else element by element.
-  __device__ __forceinline__ bool whole(int b, int lane) const {
-    const int64_t v = (int64_t)b * kBlock + lane * N;
-    return v >= lead && v + N <= (int64_t)lead + vocab;
-  }
+  // This lane's 16 bytes of block b, which lies within the row.  (Element numbers are at
+  // most vocab + 8 and a block: below 2^31.)
   __device__ __forceinline__ uint4 load(int b, int lane) const {
-    return __ldg(reinterpret_cast<const uint4*>(base + (int64_t)b * kBlock + lane * N));
+    return __ldg(reinterpret_cast<const uint4*>(base + b * kBlock + lane * N));
   }
-  __device__ __forceinline__ void edge(int b, int lane, float (&x)[N]) const {
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int64_t v = (int64_t)b * kBlock + lane * N + e;
-      x[e] = v >= lead && v < (int64_t)lead + vocab ? LpVec<T>::one(base + v) : -INFINITY;
-    }
+  // Of one that may not: -infinity outside the row, of which no byte is read.
+  __device__ __forceinline__ uint4 edge(int b, int lane) const {
+    const int v = b * kBlock + lane * N;
+    if (v >= lead && v + N <= lead + vocab) return load(b, lane);
+    auto part = [&](int i) { return LpVec<T>::part(base, v, i, lead, lead + vocab); };
+    return make_uint4(part(0), part(1), part(2), part(3));
   }
 };
 
@@ -133,27 +154,30 @@ struct LpBest {
   }
 };
 
+template <int TH>
 struct LpShared {
-  float m[kLpWarps], l[kLpWarps], t[kLpWarps];
+  static constexpr int kWarps = TH / 32;
+  float m[kWarps], l[kWarps], t[kWarps];
   float cta[3];                  // the CTA's (m, l, t)
-  uint32_t chunk[kLpChunks];     // largest logit of each of this CTA's chunks
+  uint32_t chunk[TH];            // largest logit of each of this CTA's chunks
   int chosen[kLpMost], n_chosen;
-  uint32_t key[kLpThreads];      // candidates
-  int id[kLpThreads];
-  int warp_n[kLpWarps];
-  uint32_t best_key[kLpMost];    // the CTA's best
-  int best_id[kLpMost], n_best;
+  uint32_t key[TH];              // candidates
+  int id[TH];
+  int warp_n[kWarps];
+  uint2 best[kLpMost];           // the CTA's best: order and id (-1: none)
 };
 
-// The best `most` of the threads' candidates (have: this thread has one), in order, into s.best_*.
-__device__ __forceinline__ void lp_rank(LpShared& s, bool have, uint32_t key, int id, int most) {
+// The best `most` of the threads' candidates (have: this thread has one), in order, into s.best.
+template <int TH>
+__device__ __forceinline__ void lp_rank(LpShared<TH>& s, bool have, uint32_t key, int id, int most) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t mask = __ballot_sync(0xffffffffu, have);
   if (lane == 0) s.warp_n[warp] = __popc(mask);
+  if (tid < kLpMost) s.best[tid] = make_uint2(0u, 0xffffffffu);
   __syncthreads();
   int before = 0, n = 0;
 #pragma unroll
-  for (int w = 0; w < kLpWarps; ++w) {
+  for (int w = 0; w < TH / 32; ++w) {
     before += w < warp ? s.warp_n[w] : 0;
     n += s.warp_n[w];
   }
@@ -168,65 +192,89 @@ __device__ __forceinline__ void lp_rank(LpShared& s, bool have, uint32_t key, in
     id = s.id[tid];
     int rank = 0;
     for (int i = 0; i < n; ++i) rank += LpBest::better(s.key[i], s.id[i], key, id);
-    if (rank < most) {
-      s.best_key[rank] = key;
-      s.best_id[rank] = id;
-    }
+    if (rank < most) s.best[rank] = make_uint2(key, (uint32_t)id);
   }
-  if (tid == 0) s.n_best = min(n, most);
   __syncthreads();
 }
 
-template <class T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsParams p) {
+template <class T, int TH, bool kTop, bool kEntropy>
+__global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   using V = LpVec<T>;
-  constexpr int N = V::N, kBatch = 4;
-  __shared__ LpShared s;
+  constexpr int N = V::N, kAhead = 4;
+  constexpr int kLpThreads = TH, kLpWarps = TH / 32;
+  using Row = LpRow<T, TH>;
+  __shared__ LpShared<TH> s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / CS;
   const T* logits = static_cast<const T*>(p.logits) + (int64_t)r * p.stride;
-  const LpRow<T> row(logits, p.vocab);
+  const Row row(logits, p.vocab);
   const float c = p.scale_log2;
   const int c0 = (int)((int64_t)rank * row.chunks / CS), c1 = (int)((int64_t)(rank + 1) * row.chunks / CS);
-  const int b0 = c0 * row.per, b1 = min(c1 * row.per, row.blocks);
+  const int b0 = c0 << row.shift, b1 = min(c1 << row.shift, row.blocks);
   if (kTop) {
     s.chunk[tid] = 0;
     __syncthreads();
   }
   float m = kLpNone, l = 0.0f, t = 0.0f;
-  for (int b = b0 + warp; b < b1; b += kBatch * kLpWarps) {
-    uint4 w[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (b + i * kLpWarps < b1 && row.whole(b + i * kLpWarps, lane)) w[i] = row.load(b + i * kLpWarps, lane);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int bi = b + i * kLpWarps;
-      if (bi >= b1) break;
-      float x[N];
-      if (row.whole(bi, lane)) V::open(w[i], x);
-      else row.edge(bi, lane, x);
-      float top = x[0];
-#pragma unroll
-      for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
+  auto add = [&](const uint4& w, int b) {
+    float x[N];
+    V::open(w, x);
+    float top = V::largest(w);
+    // (the reference follows when it falls behind by 2^4)
+    const bool far = __fmaf_rn(top, c, -m) > kLpSlack;
+    if (kTop || __any_sync(0xffffffffu, far)) {
       top = warp_max(top);
-      if (kTop && lane == 0) atomicMax(&s.chunk[bi / row.per], order_of(top));
+      if (kTop && lane == 0) atomicMax(&s.chunk[b >> row.shift], order_of(top));
       const float y = __fmul_rn(top, c);
-      if (y > m) {
+      if (__fsub_rn(y, m) > kLpSlack) {
         const float d = __fsub_rn(m, y), f = lp_ex2(d);
         t = f > 0.0f ? __fmul_rn(f, __fmaf_rn(d, l, t)) : 0.0f;
         l = __fmul_rn(f, l);
         m = y;
       }
+    }
+    const float before = t;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float z = __fmaf_rn(x[e], c, -m), q = lp_ex2(z);
+      l = __fadd_rn(l, q);
+      if (kEntropy) t = __fmaf_rn(q, z, t);
+      x[e] = z;
+    }
+    if (kEntropy && t != t) {  // an impossible token's 0 * inf is zero (a NaN among the logits has made l one)
+      t = before;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        // (2^z (z) of an impossible token is zero, not 0 * inf; a NaN stays one)
-        const float z = max_nan(__fmaf_rn(x[e], c, -m), -1000.0f), q = lp_ex2(z);
-        l = __fadd_rn(l, q);
-        t = __fmaf_rn(q, z, t);
+        const float z = fmaxf(x[e], -1000.0f);
+        t = __fmaf_rn(lp_ex2(z), z, t);
       }
+    }
+  };
+  // Blocks that lie within the row, each warp's next three on their way while one is
+  // worked on; the row's ends by themselves.
+  const int whole0 = max(b0, row.lead > 0 ? 1 : 0), whole1 = min(b1, (row.lead + row.vocab) / Row::kBlock);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int b = i ? row.blocks - 1 : 0;
+    if (warp == i && b >= b0 && b < b1 && (b < whole0 || b >= whole1) && !(i && b == 0)) add(row.edge(b, lane), b);
+  }
+  uint4 w[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (whole0 + warp + i * kLpWarps < whole1) w[i] = row.load(whole0 + warp + i * kLpWarps, lane);
+  }
+#pragma unroll 1
+  for (int b = whole0 + warp; b < whole1; b += kAhead * kLpWarps) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int bi = b + i * kLpWarps;
+      if (bi >= whole1) break;
+      const uint4 now = w[i];
+      if (bi + kAhead * kLpWarps < whole1) w[i] = row.load(bi + kAhead * kLpWarps, lane);
+      add(now, bi);
     }
   }
 #pragma unroll
@@ -301,10 +349,14 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsParams p)
     key = CS > 1 ? cluster.map_shared_rank(s.chunk, at)[tid] : s.chunk[tid];
   }
   if (!good) key = 0;  // (no tokens to name)
-  // The largest bound that k chunks reach, bit by bit.
+  // The largest bound that k chunks reach, bit by bit (of bf16 values the upper 16 say all).
+  constexpr int kLow = sizeof(T) == 2 ? 16 : 0;
+  key >>= kLow;
+  const uint32_t none = kOrderNegInf >> kLow;
   uint32_t bound = 0;
   bool exact = false;
-  for (uint32_t bit = 0x80000000u; bit && !exact; bit >>= 1) {
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u >> kLow; bit && !exact; bit >>= 1) {
     const int n = __syncthreads_count(key >= (bound | bit));
     if (n >= k) {
       bound |= bit;
@@ -312,7 +364,7 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsParams p)
     }
   }
   // Chunks above the bound, and the first of those equal to it (all that reach it, where they are k).
-  bool take = key > kOrderNegInf && key >= bound;
+  bool take = key > none && key >= bound;
   if (!exact && bound > 0) {
     const int above = __syncthreads_count(key > bound);
     const uint32_t eq = __ballot_sync(0xffffffffu, key == bound);
@@ -322,22 +374,23 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsParams p)
     for (int w = 0; w < warp; ++w) before += s.warp_n[w];
     if (key == bound && before >= k - above) take = false;
   }
+  bound <<= kLow;
   if (tid == 0) s.n_chosen = 0;
   __syncthreads();
   if (take && tid >= c0 && tid < c1) s.chosen[atomicAdd(&s.n_chosen, 1)] = tid;
   __syncthreads();
   LpBest best = {0u, -1};
-  const int items = s.n_chosen * row.per;
+  const int items = s.n_chosen << row.shift;
+#pragma unroll 1
   for (int i = warp; i < items; i += kLpWarps) {
-    const int b = s.chosen[i / row.per] * row.per + i % row.per;
+    const int b = (s.chosen[i >> row.shift] << row.shift) + (i & ((1 << row.shift) - 1));
     if (b >= row.blocks) continue;
     float x[N];
-    if (row.whole(b, lane)) V::open(row.load(b, lane), x);
-    else row.edge(b, lane, x);
+    V::open(row.edge(b, lane), x);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const uint32_t ke = order_of(x[e]);
-      const int id = (int)((int64_t)b * LpRow<T>::kBlock + lane * N + e - row.lead);
+      const int id = (int)((int64_t)b * Row::kBlock + lane * N + e - row.lead);
       uint32_t left = __ballot_sync(0xffffffffu, ke > kOrderNegInf && ke >= bound);
       while (left) {
         const int from = __ffs(left) - 1;
@@ -351,63 +404,60 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsParams p)
     cluster.sync();
     if (rank == 0) {  // thread (CTA i, place j) takes that one's j-th
       const int i = tid / kLpMost, j = tid % kLpMost;
-      bool have = false;
-      if (i < CS) {
-        have = j < *cluster.map_shared_rank(&s.n_best, i);
-        if (have) {
-          key = cluster.map_shared_rank(s.best_key, i)[j];
-          best.id = cluster.map_shared_rank(s.best_id, i)[j];
-        }
-      }
+      uint2 other = make_uint2(0u, 0xffffffffu);
+      if (i < CS) other = cluster.map_shared_rank(s.best, i)[j];
       __syncthreads();  // this CTA's own are in registers now
-      lp_rank(s, have, key, best.id, k);
+      lp_rank(s, (int)other.y >= 0, other.x, (int)other.y, k);
     }
   }
   if (rank == 0 && tid < k) {
-    const bool there = tid < s.n_best;
-    const uint32_t o = there ? s.best_key[tid] : 0;
-    const float x = __uint_as_float((o >> 31) ? o ^ 0x80000000u : ~o);
+    const uint2 o = s.best[tid];
+    const bool there = (int)o.y >= 0;
+    const float x = __uint_as_float((o.x >> 31) ? o.x ^ 0x80000000u : ~o.x);
     if (p.top_values) p.top_values[(int64_t)r * k + tid] = !good ? NaN : there ? log_prob(x) : -INFINITY;
-    if (p.top_ids) p.top_ids[(int64_t)r * k + tid] = there ? s.best_id[tid] : -1;
+    if (p.top_ids) p.top_ids[(int64_t)r * k + tid] = (int)o.y;
   }
   if (CS > 1) cluster.sync();
 }
 
-template <class T, bool kTop>
+template <class T, int TH, bool kTop, bool kEntropy>
 cudaError_t launch_t(const LogprobsParams& p, int n_rows, int cs, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_rows * cs);
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(TH);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cs;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_logprobs<T, kTop>, p);
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_logprobs<T, TH, kTop, kEntropy>, p);
+}
+
+template <class T, int TH>
+cudaError_t launch_e(const LogprobsParams& p, int n_rows, int cs, cudaStream_t s) {
+  if (p.entropy) return p.top ? launch_t<T, TH, true, true>(p, n_rows, cs, s) : launch_t<T, TH, false, true>(p, n_rows, cs, s);
+  return p.top ? launch_t<T, TH, true, false>(p, n_rows, cs, s) : launch_t<T, TH, false, false>(p, n_rows, cs, s);
 }
 
 template <class T>
-cudaError_t prepare_t() {
-  cudaError_t e = cudaFuncSetAttribute(k_logprobs<T, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_logprobs<T, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t launch_d(const LogprobsParams& p, int n_rows, int num_sms, cudaStream_t s) {
+  constexpr int kBlock = 32 * LpVec<T>::N;
+  // Rows of up to 16 blocks for each of a narrow CTA's warps.
+  if (p.vocab <= kLpNarrow / 32 * 16 * kBlock) return launch_e<T, kLpNarrow>(p, n_rows, 1, s);
+  // CTAs of a row: up to one an SM in all, while each warp has a block of its own.
+  // (1 row of 151936 fp32 with 20 alternatives: 12.9 us with 16, 11.9 with 8, 13.9 with
+  // 4, 26 with 1; 24 rows of 262144 bf16 with 5: 17.9 with 8, 16.2 with 4, 22.7 with 2.)
+  int cs = 1;
+  while (cs < 8 && (int64_t)n_rows * cs * 2 <= num_sms && p.vocab / kBlock >= 2 * cs * (kLpWide / 32)) cs *= 2;
+  return launch_e<T, kLpWide>(p, n_rows, cs, s);
 }
 
 }  // namespace
 
-cudaError_t prepare_logprobs() {
-  cudaError_t e = prepare_t<float>();
-  return e != cudaSuccess ? e : prepare_t<bf16>();
-}
-
 cudaError_t launch_logprobs(const LogprobsParams& p, int n_rows, bool is_bf16, int num_sms, cudaStream_t s) {
-  // CTAs of a row: as many as keep two on an SM busy, while each warp has a block of its own.
-  const int blocks = p.vocab / (32 * (is_bf16 ? LpVec<bf16>::N : LpVec<float>::N));
-  int cs = 1;
-  while (cs < 16 && (int64_t)n_rows * cs * 2 <= 2 * num_sms && blocks >= 2 * cs * kLpWarps) cs *= 2;
-  if (is_bf16) return p.top ? launch_t<bf16, true>(p, n_rows, cs, s) : launch_t<bf16, false>(p, n_rows, cs, s);
-  return p.top ? launch_t<float, true>(p, n_rows, cs, s) : launch_t<float, false>(p, n_rows, cs, s);
+  return is_bf16 ? launch_d<bf16>(p, n_rows, num_sms, s) : launch_d<float>(p, n_rows, num_sms, s);
 }
 
 }  // namespace sv
