@@ -240,6 +240,7 @@ class PagedKv:
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, d, k.device
         self._index = k.device.index
+        self._n, self._kind = 1, (self.format, n_kv, d, self.scale_block, k.device)  # (as KvLayers has them)
         self._c = SvKvPool(self.format, n_pages, n_kv, d, self.scale_block, _ptr(k), _ptr(v), _ptr(k_exp),
                            _ptr(v_exp))
         self._p = ctypes.byref(self._c)
@@ -559,6 +560,7 @@ class KvPages:
         self._c = SvKvPages(n_seq, width, self.n_pages, _ptr(block_table), _ptr(length), _ptr(held), _ptr(refs))
         self._p = ctypes.byref(self._c)
         self._fork_bytes = 4 * (self.n_pages + n_seq * width)
+        self._tables = frozenset((_ptr(block_table), _ptr(length), _ptr(held), _ptr(refs)))
 
     @classmethod
     def empty(cls, n_seq: int, width: int, n_pages: int, *, device="cuda"):
@@ -568,22 +570,36 @@ class KvPages:
                    *(torch.zeros(n, dtype=torch.int32, device=device) for n in (n_seq, n_seq, n_pages)))
 
 
-def _check_pages_call(pages, out, moves, status):
-    if moves.dtype is not pages._int32 or moves.dim() != 2 or moves.shape[1] != 2 or moves.shape[0] < 1:
-        raise ValueError(f"moves: {moves.dtype} of shape {tuple(moves.shape)}, expected torch.int32 [n, 2]")
-    if moves.device != pages.device or not moves.is_contiguous() or moves.data_ptr() % 8:
-        raise ValueError("moves: must be contiguous on the tables' device, aligned to 8 bytes")
-    if out is not None:
-        if (out.n_seq, out.width, out.n_pages, out.device) != (pages.n_seq, pages.width, pages.n_pages, pages.device):
-            raise ValueError("out: must have the sizes and the device of pages")
-        if out is not pages:
-            mine = {pages._c.block_table, pages._c.length, pages._c.held, pages._c.refs}
-            if mine & {out._c.block_table, out._c.length, out._c.held, out._c.refs}:
-                raise ValueError("out: shares memory with pages")
-    if status is not None:
-        _check_tensor(status, "status", "torch.int32", (1,))
-        if status.device != pages.device:
-            raise ValueError(f"status: on {status.device}, the tables on {pages.device}")
+def _check_moves(moves, of):
+    """The address of moves and their number.  (Checks of every call: what asks a tensor
+    little, in little time.)"""
+    n = moves.numel() >> 1
+    if moves.dtype is not of._int32 or not n or moves.shape != (n, 2) or not moves.is_contiguous():
+        raise ValueError(f"moves: {moves.dtype} of shape {tuple(moves.shape)}, expected a contiguous torch.int32 [n, 2]")
+    at = moves.data_ptr()
+    if moves.get_device() != of._index or at % 8:
+        raise ValueError(f"moves: must be on {of.device}, aligned to 8 bytes")
+    return at, n
+
+
+def _check_out(pages, out):
+    """The address of the result's tables, None for in place."""
+    if out is None or out is pages:
+        return None
+    if (out.n_seq, out.width, out.n_pages, out._index) != (pages.n_seq, pages.width, pages.n_pages, pages._index):
+        raise ValueError("out: must have the sizes and the device of pages")
+    if not pages._tables.isdisjoint(out._tables):
+        raise ValueError("out: shares memory with pages")
+    return out._p
+
+
+def _check_status(status, of):
+    if status is None:
+        return 0
+    _check_tensor(status, "status", "torch.int32", (1,))
+    if status.get_device() != of._index:
+        raise ValueError(f"status: on {status.device}, expected {of.device}")
+    return status.data_ptr()
 
 
 def kv_fork(pages: KvPages, moves, *, source=None, keep=None, room=None, out=None, workspace=None, status=None,
@@ -598,30 +614,28 @@ def kv_fork(pages: KvPages, moves, *, source=None, keep=None, room=None, out=Non
     (too few free pages) or 2 (a source or a row that cannot be). workspace:
     uint8, 4 (n_pages + n_seq * width) bytes; None takes one of the object's
     own, kept for each stream (in a capture, one of the graph's). Asynchronous."""
-    _check_pages_call(pages, out, moves, status)
-    n = pages.n_seq
-    if moves.shape[0] != n:
-        raise ValueError(f"moves: {moves.shape[0]} rows, expected {n}")
+    (mp, rows), n, index = _check_moves(moves, pages), pages.n_seq, pages._index
+    if rows != n:
+        raise ValueError(f"moves: {rows} rows, expected {n}")
     ptrs = []
-    for t, name in ((source, "source"), (keep, "keep"), (room, "room")):
+    for t in (source, keep, room):
         if t is None:
             ptrs.append(0)
             continue
-        if t.dtype is not pages._int32 or t.shape != (n,) or t.device != pages.device or not t.is_contiguous():
+        if t.dtype is not pages._int32 or t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+            name = "source" if t is source else "keep" if t is keep else "room"
             raise ValueError(f"{name}: must be a contiguous torch.int32 tensor [{n}] on {pages.device}")
         ptrs.append(t.data_ptr())
-    op = None if out is None else out._p
-    need = pages._fork_bytes
+    op, sp, need = _check_out(pages, out), _check_status(status, pages), pages._fork_bytes
     if workspace is None:
         with pages._lock:
             ws = _own_workspace(pages, pages, need, stream)
-            _launch(pages, stream, _lib.sv_kv_fork, pages._p, *ptrs, op, moves.data_ptr(), ws.data_ptr(), need, _ptr(status))
+            _launch(pages, stream, _lib.sv_kv_fork, pages._p, *ptrs, op, mp, ws.data_ptr(), need, sp)
         return
     _check_buf(workspace, "workspace", "torch.uint8", need, cuda=True)
     if workspace.device != pages.device:
         raise ValueError(f"workspace: on {workspace.device}, the tables on {pages.device}")
-    _launch(pages, stream, _lib.sv_kv_fork, pages._p, *ptrs, op, moves.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _ptr(status))
+    _launch(pages, stream, _lib.sv_kv_fork, pages._p, *ptrs, op, mp, workspace.data_ptr(), workspace.numel(), sp)
 
 
 def kv_compact(pages: KvPages, moves, *, where=None, out=None, status=None, stream=None):
@@ -629,19 +643,16 @@ def kv_compact(pages: KvPages, moves, *, where=None, out=None, status=None, stre
     as many as moves (int32 [n, 2]) has room for; pass it to kv_copy. where:
     int32 [n_pages], each page's number after the call (-1: free), or None. out:
     a KvPages of the same sizes, None: in place. Asynchronous."""
-    _check_pages_call(pages, out, moves, status)
+    (mp, n), op, sp = _check_moves(moves, pages), _check_out(pages, out), _check_status(status, pages)
     if where is not None:
         _check_tensor(where, "where", "torch.int32", (pages.n_pages,))
         if where.device != pages.device:
             raise ValueError(f"where: on {where.device}, the tables on {pages.device}")
-    op = None if out is None else out._p
-    if where is not None:
-        _launch(pages, stream, _lib.sv_kv_compact, pages._p, op, moves.data_ptr(), moves.shape[0], where.data_ptr(),
-                _ptr(status))
+        _launch(pages, stream, _lib.sv_kv_compact, pages._p, op, mp, n, where.data_ptr(), sp)
         return
     with pages._lock:
         ws = _own_workspace(pages, pages, pages._fork_bytes, stream)
-        _launch(pages, stream, _lib.sv_kv_compact, pages._p, op, moves.data_ptr(), moves.shape[0], ws.data_ptr(), _ptr(status))
+        _launch(pages, stream, _lib.sv_kv_compact, pages._p, op, mp, n, ws.data_ptr(), sp)
 
 
 class KvLayers:
@@ -653,15 +664,11 @@ class KvLayers:
             raise ValueError("no caches")
         first = self.caches[0]
         for c in self.caches:
-            if _kind(c) != _kind(first) or c.n_pages != first.n_pages:
+            if c._kind != first._kind or c.n_pages != first.n_pages:
                 raise ValueError("the caches differ in format, shape or device")
         self.n_pages, self.device, self._index, self._torch = first.n_pages, first.device, first._index, first._torch
         self._c = (SvKvPool * len(self.caches))(*(c._c for c in self.caches))
-        self._int32 = first._int32
-
-
-def _kind(c):
-    return c.format, c.n_kv_heads, c.head_dim, c.scale_block, c.device
+        self._p, self._n, self._kind, self._int32 = ctypes.byref(self._c), len(self.caches), first._kind, first._int32
 
 
 def kv_copy(cache, moves, *, into=None, status=None, stream=None):
@@ -669,35 +676,34 @@ def kv_copy(cache, moves, *, into=None, status=None, stream=None):
     moves[i, 1] of `into` (None: of the same). moves: int32 [n, 2]; (-1, -1) is
     passed over. No page may be written by two moves, nor read by one and
     written by another. Asynchronous."""
-    if isinstance(cache, PagedKv):
-        pools, n, kind = cache._p, 1, _kind(cache)
-    else:
-        pools, n, kind = cache._c, len(cache.caches), _kind(cache.caches[0])
     to = None
     if into is not None:
-        if isinstance(into, PagedKv):
-            to, n_to, kind_to = into._p, 1, _kind(into)
-        else:
-            to, n_to, kind_to = into._c, len(into.caches), _kind(into.caches[0])
-        if n_to != n or kind_to != kind:
+        if into._n != cache._n or into._kind != cache._kind:
             raise ValueError("into: differs from cache in the number of layers, format, shape or device")
-    if moves.dtype is not cache._int32 or moves.dim() != 2 or moves.shape[1] != 2 or moves.shape[0] < 1:
-        raise ValueError(f"moves: {moves.dtype} of shape {tuple(moves.shape)}, expected torch.int32 [n, 2]")
-    if moves.device != cache.device or not moves.is_contiguous() or moves.data_ptr() % 8:
-        raise ValueError("moves: must be contiguous on the cache's device, aligned to 8 bytes")
-    if status is not None:
-        _check_tensor(status, "status", "torch.int32", (1,))
-        if status.device != cache.device:
-            raise ValueError(f"status: on {status.device}, the cache on {cache.device}")
-    _launch(cache, stream, _lib.sv_kv_copy, pools, to, n, moves.data_ptr(), moves.shape[0], _ptr(status))
+        to = into._p
+    mp, n = _check_moves(moves, cache)
+    _launch(cache, stream, _lib.sv_kv_copy, cache._p, to, cache._n, mp, n, _check_status(status, cache))
 
 
-class _Device:  # what _launch needs of a device that no cache names
-    def __init__(self, device, torch):
-        self._index, self._torch = device.index, torch._C
+class _Device:
+    """What a call needs of a device that no cache names, and torch's types at hand."""
+
+    def __init__(self, index):
+        import torch
+        self._index, self._torch, self.device = index, torch._C, torch.device("cuda", index)
+        self.fp32, self.int32 = torch.float32, torch.int32
+        self.kinds = {torch.float32: SV_LOGITS_F32, torch.bfloat16: SV_LOGITS_BF16}
 
 
 _devices = {}
+
+
+def _check_result(t, name, dtype, shape, index):
+    """The address of a contiguous tensor of one type and shape on device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{index}, not {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def logprobs(logits, tokens, out, *, scale: float = 1.0, lse=None, entropy=None, top_values=None, top_ids=None,
@@ -708,50 +714,43 @@ def logprobs(logits, tokens, out, *, scale: float = 1.0, lse=None, entropy=None,
     fp32 of the same shape. lse, entropy: fp32 [n_rows]; top_values (fp32),
     top_ids (int32) [n_rows, k], k at most 32: the most probable tokens, ties
     to the lowest id. Each of these or None. Asynchronous."""
-    import torch
-    if getattr(logits, "dim", lambda: 0)() != 2 or min(logits.shape) < 1:
+    if getattr(logits, "ndim", 0) != 2 or not logits.numel():
         raise ValueError("logits: must be a 2-D tensor [n_rows, vocab]")
-    n, vocab = logits.shape
-    dev = logits.device
     if not logits.is_cuda:
         raise ValueError("logits: must be a CUDA tensor")
-    if logits.dtype is torch.float32:
-        kind = SV_LOGITS_F32
-    elif logits.dtype is torch.bfloat16:
-        kind = SV_LOGITS_BF16
-    else:
+    index = logits.get_device()
+    at = _devices.get(index)
+    if at is None:
+        at = _devices[index] = _Device(index)
+    n, vocab = logits.shape
+    kind = at.kinds.get(logits.dtype)
+    if kind is None:
         raise ValueError(f"logits: dtype {logits.dtype}, expected torch.float32 or torch.bfloat16")
     row, one = logits.stride()
     if (one != 1 and vocab > 1) or (row < vocab and n > 1):
         raise ValueError(f"logits: strides {logits.stride()}, expected rows of consecutive elements")
     if n == 1:  # a lone row's stride says nothing
         row = vocab
-    if tokens.dtype is not torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != n:
-        raise ValueError(f"tokens: {tokens.dtype} of shape {tuple(tokens.shape)}, expected torch.int32 [{n}] or [{n}, k]")
-    n_tok = 1 if tokens.dim() == 1 else tokens.shape[1]
-    k = 0
-    for t, name in ((top_values, "top_values"), (top_ids, "top_ids")):
-        if t is None:
-            continue
-        if t.dim() != 2 or t.shape[0] != n or not 1 <= t.shape[1] <= LOGPROBS_MAX_TOP:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{n}, 1 .. {LOGPROBS_MAX_TOP}]")
-        if k and t.shape[1] != k:
-            raise ValueError("top_values and top_ids differ in shape")
-        k = t.shape[1]
-    for t, name, kind_of, shape in ((tokens, "tokens", torch.int32, tokens.shape), (out, "out", torch.float32, tokens.shape),
-                                    (lse, "lse", torch.float32, (n,)), (entropy, "entropy", torch.float32, (n,)),
-                                    (top_values, "top_values", torch.float32, (n, k)), (top_ids, "top_ids", torch.int32, (n, k)),
-                                    (status, "status", torch.int32, (1,))):
-        if t is None and name != "out":
-            continue
-        if t.dtype is not kind_of or t.shape != shape or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: must be a contiguous {kind_of} tensor {tuple(shape)} on {dev}, not {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-    at = _devices.get(dev)
-    if at is None:
-        at = _devices[dev] = _Device(dev, torch)
-    _launch(at, stream, _lib.sv_logprobs, logits.data_ptr(), kind, row, n, vocab, scale, tokens.data_ptr(), n_tok,
-            out.data_ptr(), _ptr(lse), _ptr(entropy), k, _ptr(top_values), _ptr(top_ids), _ptr(status))
+    shape = tokens.shape
+    if len(shape) not in (1, 2) or shape[0] != n:
+        raise ValueError(f"tokens: shape {tuple(shape)}, expected [{n}] or [{n}, k]")
+    per = (n,)
+    k = vp = ip = lp = ep = 0
+    if top_values is not None or top_ids is not None:
+        top = (top_ids if top_values is None else top_values).shape
+        k = top[-1] if len(top) == 2 else 0
+        if not 1 <= k <= LOGPROBS_MAX_TOP:
+            raise ValueError(f"alternatives of shape {tuple(top)}, expected [{n}, 1 .. {LOGPROBS_MAX_TOP}]")
+        top = (n, k)
+        vp = 0 if top_values is None else _check_result(top_values, "top_values", at.fp32, top, index)
+        ip = 0 if top_ids is None else _check_result(top_ids, "top_ids", at.int32, top, index)
+    if lse is not None:
+        lp = _check_result(lse, "lse", at.fp32, per, index)
+    if entropy is not None:
+        ep = _check_result(entropy, "entropy", at.fp32, per, index)
+    _launch(at, stream, _lib.sv_logprobs, logits.data_ptr(), kind, row, n, vocab, scale,
+            _check_result(tokens, "tokens", at.int32, shape, index), 1 if len(shape) == 1 else shape[1],
+            _check_result(out, "out", at.fp32, shape, index), lp, ep, k, vp, ip, _check_status(status, at))
 
 
 def spec_generate(target: "Context", draft: "Context", pending: int, K: int, n_new: int):

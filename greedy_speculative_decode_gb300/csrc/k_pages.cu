@@ -5,7 +5,7 @@
 // the rows that hold a page, and whatever else a program counts there.  Both
 // plans (fork, compact) are functions of the table and the counts alone: sums
 // over rows and pages, no order of arrival.  Each is one launch of one cluster
-// of eight CTAs, which meet at the cluster's barriers: a table's numbers are few
+// of up to eight CTAs, which meet at the cluster's barriers: a table's numbers are few
 // (64 rows of 256 pages and 20 thousand pages are 200 KB, in L2), so what bounds
 // them is the chain of dependent loads and barriers, not bytes.
 //
@@ -25,7 +25,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPgThreads = 1024, kPgWarps = 32, kPgCtas = 8;
+constexpr int kPgThreads = 1024, kPgWarps = 32;
+// CTAs of a plan's cluster: one where there is little to look through.
+constexpr int kPgWide = 8;
 static_assert(kPagesMaxSeq == kPgThreads, "a thread a row");
 
 // Exclusive sums over the block's threads; total in `sum`.  (s: 33 words; two barriers.)
@@ -51,20 +53,31 @@ __device__ __forceinline__ int block_scan(int v, int* s, int& sum) {
   return before + x - v;
 }
 
+// All of the plan's threads meet; what they wrote is seen.
+template <int CTAS>
+__device__ __forceinline__ void meet() {
+  if (CTAS == 1) __syncthreads();
+  else cg::this_cluster().sync();
+}
+
 // The pages of a warp: 32-page steps a .. b - 1 of the pool, in order of (CTA, warp).
+template <int CTAS>
 struct PageRange {
   int a, b;
   __device__ __forceinline__ PageRange(int n_pages, int rank) {
-    const int64_t steps = (n_pages + 31) / 32, w = rank * kPgWarps + (threadIdx.x >> 5), all = kPgCtas * kPgWarps;
-    a = (int)(steps * w / all);
-    b = (int)(steps * (w + 1) / all);
+    const unsigned steps = (n_pages + 31) / 32, w = rank * kPgWarps + (threadIdx.x >> 5);
+    constexpr unsigned kAll = CTAS * kPgWarps;  // (a power of two; below 2^22 steps)
+    a = (int)(steps * w / kAll);
+    b = (int)(steps * (w + 1) / kAll);
   }
 };
 
 // Pages of the range with a count of zero.
-__device__ __forceinline__ int count_free(const PageRange& g, const int* refs, int n_pages) {
+template <int CTAS>
+__device__ __forceinline__ int count_free(const PageRange<CTAS>& g, const int* refs, int n_pages) {
   const int lane = threadIdx.x & 31;
   int n = 0;
+#pragma unroll 1
   for (int s = g.a; s < g.b; s += 4) {
     int x[4];
 #pragma unroll
@@ -79,17 +92,22 @@ __device__ __forceinline__ int count_free(const PageRange& g, const int* refs, i
 }
 
 // Free pages before this warp's range, and of the whole pool (`all`); a cluster barrier.
+template <int CTAS>
 __device__ __forceinline__ int free_before(int mine, int* s_scan, int* s_total, int& all) {
   cg::cluster_group cluster = cg::this_cluster();
   int sum;
   const int before = block_scan((threadIdx.x & 31) == 0 ? mine : 0, s_scan, sum);
+  if (CTAS == 1) {
+    all = sum;
+    return __shfl_sync(0xffffffffu, before, 0);
+  }
   if (threadIdx.x == 0) *s_total = sum;
   cluster.sync();
   int base = 0;
   all = 0;
   const int rank = (int)cluster.block_rank();
 #pragma unroll
-  for (int c = 0; c < kPgCtas; ++c) {
+  for (int c = 0; c < CTAS; ++c) {
     const int n = *cluster.map_shared_rank(s_total, c);
     base += c < rank ? n : 0;
     all += n;
@@ -107,12 +125,13 @@ struct ForkShared {
 
 // New rows.  Every CTA works out the rows' numbers by itself; entries and pages
 // are divided among them.
-__global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) k_fork(const ForkParams p) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPgThreads, 1) k_fork(const ForkParams p) {
   extern __shared__ int s_raw[];
   ForkShared& s = *reinterpret_cast<ForkShared*>(s_raw);
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
-  const int S = p.in.n_seq, W = p.in.width, all_threads = kPgCtas * kPgThreads, me = rank * kPgThreads + tid;
+  const int tid = threadIdx.x, lane = tid & 31, rank = CTAS == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  pdl_trigger();
+  const int S = p.in.n_seq, W = p.in.width, all_threads = CTAS * kPgThreads, me = rank * kPgThreads + tid;
   // ---- the rows: what they keep and need
   int wrong = 0, keep = 0, kept = 0, need = 0, src = -1, held = 0, last = -1;
   if (tid < S) {
@@ -139,13 +158,13 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   }
   // ---- the counts: those of before, ...
   for (int i = me; i < p.in.n_pages; i += all_threads) p.count[i] = __ldcg(p.in.refs + i);
-  cluster.sync();
+  meet<CTAS>();
   wrong = __syncthreads_or(wrong) ? ST_BAD_PAGE : 0;
   // ... less the old rows' entries, with the new rows'
-  const int64_t entries = (int64_t)S * W;
+  const int entries = S * W;  // (at most 2^29)
   if (!wrong) {
-    for (int64_t e = me; e < entries; e += all_threads) {
-      const int row = (int)(e / W), j = (int)(e - (int64_t)row * W);
+    for (int e = me; e < entries; e += all_threads) {
+      const int row = (unsigned)e / (unsigned)W, j = e - row * W;
       if (j >= max(s.held[row], s.kept[row])) continue;
       const int old = j < s.held[row] ? __ldcg(p.in.table + e) : -1;
       int now = -1;
@@ -159,7 +178,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
       if ((uint32_t)now < (uint32_t)p.in.n_pages) atomicAdd(p.count + now, 1);
     }
   }
-  cluster.sync();
+  meet<CTAS>();
   // ---- last pages that are not full: one row may go on in the page itself
   int copy = 0;
   if (!wrong && last >= 0) {
@@ -183,15 +202,15 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   // (page counts of copied pages stay above zero: whether a page is free does not change)
   if (rank == 0 && copy) atomicSub(p.count + last, 1);
   // ---- free pages, lowest first
-  const PageRange range(p.in.n_pages, rank);
+  const PageRange<CTAS> range(p.in.n_pages, rank);
   const int mine = count_free(range, p.count, p.in.n_pages);
   int free_all;
-  int at = free_before(mine, s.scan, &s.total, free_all);
+  int at = free_before<CTAS>(mine, s.scan, &s.total, free_all);
   if (!wrong && free_all < wanted) wrong = ST_NO_PAGES;
   if (wrong) {  // nothing changes
     if (me < S) p.moves[me] = make_int2(-1, -1);
     if (me == 0 && p.status) atomicOr(p.status, wrong);
-    cluster.sync();  // the others read this CTA's total
+    meet<CTAS>();  // the others read this CTA's total
     return;
   }
   for (int st = range.a; st < range.b; ++st) {
@@ -215,8 +234,8 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     if (from < -1 && i == 0) p.moves[lo] = make_int2(-2 - from, page);
   }
   // ---- the rows' entries and numbers
-  for (int64_t e = me; e < entries; e += all_threads) {
-    const int row = (int)(e / W), j = (int)(e - (int64_t)row * W);
+  for (int e = me; e < entries; e += all_threads) {
+    const int row = (unsigned)e / (unsigned)W, j = e - row * W;
     const int kept_here = s.kept[row] - (s.last[row] < -1);
     if (j < kept_here) {
       if (!p.in_place) p.out.table[e] = __ldcg(p.in.table + (int64_t)s.src[row] * W + j);
@@ -230,7 +249,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     p.out.held[tid] = need;
     if (!copy) p.moves[tid] = make_int2(-1, -1);
   }
-  cluster.sync();
+  meet<CTAS>();
 }
 
 struct CompactShared {
@@ -240,18 +259,19 @@ struct CompactShared {
 
 // With U pages in use, the used ones at U and above go to the free ones below:
 // the k-th highest to the k-th lowest.
-__global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) k_compact(const CompactParams p) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPgThreads, 1) k_compact(const CompactParams p) {
   __shared__ CompactShared s;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
-  const int N = p.in.n_pages, W = p.in.width, all_threads = kPgCtas * kPgThreads, me = rank * kPgThreads + tid;
-  const PageRange range(N, rank);
+  const int tid = threadIdx.x, lane = tid & 31, rank = CTAS == 1 ? 0 : (int)cg::this_cluster().block_rank();
+  pdl_trigger();
+  const int N = p.in.n_pages, W = p.in.width, all_threads = CTAS * kPgThreads, me = rank * kPgThreads + tid;
+  const PageRange<CTAS> range(N, rank);
   const int mine = count_free(range, p.in.refs, N);
   int free_all;
-  const int free_at = free_before(mine, s.scan, &s.total, free_all);
+  const int free_at = free_before<CTAS>(mine, s.scan, &s.total, free_all);
   const int used = N - free_all;
   for (int k = me; k < p.n_moves; k += all_threads) p.moves[k] = make_int2(-1, -1);
-  cluster.sync();
+  meet<CTAS>();
   int at = free_at;
   for (int st = range.a; st < range.b; ++st) {
     const int page = st * 32 + lane;
@@ -268,7 +288,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     if (n != 0 && page >= used && k < p.n_moves) p.moves[k].x = page;
     if (!p.in_place) p.out.refs[page] = n;
   }
-  cluster.sync();
+  meet<CTAS>();
   // (free pages below `used` and used ones from there on are as many)
   for (int k = me; k < p.n_moves; k += all_threads) {
     const int2 m = __ldcg(p.moves + k);
@@ -277,10 +297,10 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     p.out.refs[m.y] = __ldcg(p.in.refs + m.x);
     p.out.refs[m.x] = 0;
   }
-  cluster.sync();
-  const int64_t entries = (int64_t)p.in.n_seq * W;
-  for (int64_t e = me; e < entries; e += all_threads) {
-    const int row = (int)(e / W), j = (int)(e - (int64_t)row * W);
+  meet<CTAS>();
+  const int entries = p.in.n_seq * W;
+  for (int e = me; e < entries; e += all_threads) {
+    const int row = (unsigned)e / (unsigned)W, j = e - row * W;
     if (j >= __ldcg(p.in.held + row)) {
       if (!p.in_place) p.out.table[e] = -1;
       continue;
@@ -305,6 +325,8 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 // time, 16 bytes a thread, four of them on their way before the first is stored.
 __global__ void __launch_bounds__(256) k_copy_pages(const __grid_constant__ CopyParams p) {
   const int tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();  // the moves, and whoever wrote the pages
   const int64_t units = (int64_t)p.n_moves * p.n_pools * 2;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int mv = (int)(u / (2 * p.n_pools)), w = (int)(u - (int64_t)mv * 2 * p.n_pools), at = w >> 1;
@@ -337,23 +359,38 @@ __global__ void __launch_bounds__(256) k_copy_pages(const __grid_constant__ Copy
 }  // namespace
 
 cudaError_t prepare_pages() {
-  return cudaFuncSetAttribute(k_fork, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ForkShared));
+  const cudaError_t e = cudaFuncSetAttribute(k_fork<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ForkShared));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_fork<kPgWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ForkShared));
 }
 
+// Whether one CTA is enough: it looks through entries and pages 1024 at a time.
+static bool small_plan(const PageTable& t) { return (int64_t)t.n_seq * t.width + t.n_pages <= 4 * kPgThreads; }
+
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t s) {
-  k_fork<<<kPgCtas, kPgThreads, sizeof(ForkShared), s>>>(p);
+  if (small_plan(p.in)) k_fork<1><<<1, kPgThreads, sizeof(ForkShared), s>>>(p);
+  else k_fork<kPgWide><<<kPgWide, kPgThreads, sizeof(ForkShared), s>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
-  k_compact<<<kPgCtas, kPgThreads, 0, s>>>(p);
+  if (small_plan(p.in)) k_compact<1><<<1, kPgThreads, 0, s>>>(p);
+  else k_compact<kPgWide><<<kPgWide, kPgThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s) {
   const int64_t units = (int64_t)p.n_moves * p.n_pools * 2;
-  k_copy_pages<<<(unsigned)std::min<int64_t>(units, 8 * (int64_t)num_sms), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, 8 * (int64_t)num_sms));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_copy_pages, p);
 }
 
 }  // namespace sv

@@ -152,7 +152,7 @@ int sv_kv_copy(const sv_kv_pool* from, const sv_kv_pool* into, int n_pools, cons
   int num_sms = 0;
   const int rc = device_setup(&num_sms);
   if (rc != SV_OK) return rc;
-  CopyParams p = {};
+  CopyParams p;  // (pools beyond n_pools are not read)
   p.moves = reinterpret_cast<const int2*>(moves_dev);
   p.n_moves = n_moves;
   p.n_from = f0.n_pages;
