@@ -208,6 +208,8 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / CS;
+  pdl_trigger();
+  pdl_wait();
   const T* logits = static_cast<const T*>(p.logits) + (int64_t)r * p.stride;
   const Row row(logits, p.vocab);
   const float c = p.scale_log2;
@@ -426,12 +428,14 @@ cudaError_t launch_t(const LogprobsParams& p, int n_rows, int cs, cudaStream_t s
   cfg.gridDim = dim3((unsigned)n_rows * cs);
   cfg.blockDim = dim3(TH);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_logprobs<T, TH, kTop, kEntropy>, p);
 }
 

@@ -131,6 +131,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPgThreads, 1) k_
   ForkShared& s = *reinterpret_cast<ForkShared*>(s_raw);
   const int tid = threadIdx.x, lane = tid & 31, rank = CTAS == 1 ? 0 : (int)cg::this_cluster().block_rank();
   pdl_trigger();
+  pdl_wait();
   const int S = p.in.n_seq, W = p.in.width, all_threads = CTAS * kPgThreads, me = rank * kPgThreads + tid;
   // ---- the rows: what they keep and need
   int wrong = 0, keep = 0, kept = 0, need = 0, src = -1, held = 0, last = -1;
@@ -264,6 +265,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPgThreads, 1) k_
   __shared__ CompactShared s;
   const int tid = threadIdx.x, lane = tid & 31, rank = CTAS == 1 ? 0 : (int)cg::this_cluster().block_rank();
   pdl_trigger();
+  pdl_wait();
   const int N = p.in.n_pages, W = p.in.width, all_threads = CTAS * kPgThreads, me = rank * kPgThreads + tid;
   const PageRange<CTAS> range(N, rank);
   const int mine = count_free(range, p.in.refs, N);
@@ -367,30 +369,36 @@ cudaError_t prepare_pages() {
 // Whether one CTA is enough: it looks through entries and pages 1024 at a time.
 static bool small_plan(const PageTable& t) { return (int64_t)t.n_seq * t.width + t.n_pages <= 4 * kPgThreads; }
 
-cudaError_t launch_fork(const ForkParams& p, cudaStream_t s) {
-  if (small_plan(p.in)) k_fork<1><<<1, kPgThreads, sizeof(ForkShared), s>>>(p);
-  else k_fork<kPgWide><<<kPgWide, kPgThreads, sizeof(ForkShared), s>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
-  if (small_plan(p.in)) k_compact<1><<<1, kPgThreads, 0, s>>>(p);
-  else k_compact<kPgWide><<<kPgWide, kPgThreads, 0, s>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s) {
-  const int64_t units = (int64_t)p.n_moves * p.n_pools * 2;
+// A kernel that may be launched while the one ahead of it ends (it waits for that
+// before it reads anything).
+template <class P>
+static cudaError_t launch_behind(void (*kernel)(P), const P& p, unsigned grid, unsigned block, size_t smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, 8 * (int64_t)num_sms));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_copy_pages, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t s) {
+  return small_plan(p.in) ? launch_behind(k_fork<1>, p, 1, kPgThreads, sizeof(ForkShared), s)
+                          : launch_behind(k_fork<kPgWide>, p, kPgWide, kPgThreads, sizeof(ForkShared), s);
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
+  return small_plan(p.in) ? launch_behind(k_compact<1>, p, 1, kPgThreads, 0, s)
+                          : launch_behind(k_compact<kPgWide>, p, kPgWide, kPgThreads, 0, s);
+}
+
+cudaError_t launch_copy(const CopyParams& p, int num_sms, cudaStream_t s) {
+  const int64_t units = (int64_t)p.n_moves * p.n_pools * 2;
+  return launch_behind(k_copy_pages, p, (unsigned)std::min<int64_t>(units, 8 * (int64_t)num_sms), 256, 0, s);
 }
 
 }  // namespace sv

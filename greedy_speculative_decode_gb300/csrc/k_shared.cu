@@ -16,6 +16,7 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   __shared__ int2 s_first[256];  // of each list, where CTAs' runs end with lists: its first unit, and CTA
   const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
   pdl_trigger();
+  pdl_wait();
   auto start_of = [&](int s) { return p.a.rows.row_start ? __ldg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
   auto clip = [&](int r) { return min(max(r, 0), p.a.rows.n_rows); };
   int first = 0, n = 0;
@@ -168,8 +169,16 @@ cudaError_t prepare_shared_kernels() {
 
 cudaError_t launch_shared_prefix(const SharedParams& p, int fmt, int head_dim, cudaStream_t s) {
   const int most = std::max(p.a.rows.n_seq, p.grid + 1);  // (a thread each)
-  k_shared_plan<<<1, std::min(1024, (most + 31) / 32 * 32), 0, s>>>(p, shared_chunk(head_dim), shared_streams(head_dim));
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(std::min(1024, (most + 31) / 32 * 32));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_shared_plan, p, shared_chunk(head_dim), shared_streams(head_dim));
   if (e != cudaSuccess) return e;
   const bool b = fmt == SV_KV_BF16;
   switch (head_dim) {
