@@ -414,11 +414,12 @@ __device__ void sh_load_drain(const ShSmem<C>& sm, uint32_t end) {
 }
 
 // ------------------------------------------------------------------ 8-bit codes to f16 operands
-// Four warps.  An even chunk's codes are scaled to its largest exponents; of
+// Four warps.  (Eight: 75 us for 128 x 1 behind 16384, with four 72.)  An even chunk's codes are scaled to its largest exponents; of
 // another the codes go as they are, and the scores take the exponents (sm.scale).
 template <class C>
 __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
-  const int tid = threadIdx.x & 127;
+  constexpr int kWidth = 128;
+  const int tid = threadIdx.x - C::kWidenWarp * 32;
   ShItems<C> it(p);
   for (;;) {
     it.step();
@@ -443,10 +444,10 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
       }
       if (tid == 0) sm.meta()[c & 7] = meta;
     }
-    // A thread has a position (half of one, two of them), which has one exponent, in
-    // units of 16 codes.  Lanes begin with different units: the eight of a quarter
-    // warp then read eight different 16-byte columns and (128 codes) write eight.
-    constexpr int kThreadsRow = 128 / C::CP > 1 ? 128 / C::CP : 1, kRowUnits = C::D / 16, kMine = kRowUnits / kThreadsRow;
+    // A thread has a position (half of one of 256 codes), which has one exponent, in
+    // units of 16 codes.  Lanes begin with different units: the eight of a quarter warp
+    // then read eight different 16-byte columns and (128 codes a position) write eight.
+    constexpr int kThreadsRow = kWidth / C::CP, kRowUnits = C::D / 16, kMine = kRowUnits / kThreadsRow;
     const int pos = tid / kThreadsRow, u0 = tid % kThreadsRow * kMine;
     const uint8_t* raw = sm.raw(st) + pos * C::D;
     const uint32_t dst = smem_u32(sm.op(os)) + pos * 128;
@@ -461,25 +462,23 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
       asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(by));
       return r;
     };
-    constexpr int kAtOnce = kMine < 8 ? kMine : 8;
-#pragma unroll 1
-    for (int k0 = 0; k0 < kMine; k0 += kAtOnce) {
-      uint4 w[kAtOnce];
-      int unit[kAtOnce];
+    uint4 w[kMine];
+    int unit[kMine];
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        unit[k] = u0 + ((k0 + k + (C::D == 64 ? tid >> 1 : tid)) & (kMine - 1));
-        w[k] = *reinterpret_cast<const uint4*>(raw + unit[k] * 16);
-        if (!have) w[k] = make_uint4(0u, 0u, 0u, 0u);
-      }
+    for (int k = 0; k < kMine; ++k) {
+      unit[k] = u0 + ((k + (C::D == 64 ? pos >> 1 : pos)) & (kMine - 1));
+      w[k] = *reinterpret_cast<const uint4*>(raw + unit[k] * 16);
+      if (!have) w[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const uint32_t half = dst + (unit[k] >> 2) * C::CP * 128, col = 2 * (unit[k] & 3);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + ((col ^ (pos & 7)) << 4)), "r"(scaled(f16x2_of_lo(w[k].x))),
-                     "r"(scaled(f16x2_of_hi(w[k].x))), "r"(scaled(f16x2_of_lo(w[k].y))), "r"(scaled(f16x2_of_hi(w[k].y)))
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + (((col + 1) ^ (pos & 7)) << 4)), "r"(scaled(f16x2_of_lo(w[k].z))),
-                     "r"(scaled(f16x2_of_hi(w[k].z))), "r"(scaled(f16x2_of_lo(w[k].w))), "r"(scaled(f16x2_of_hi(w[k].w)))
+    for (int k = 0; k < kMine; ++k) {
+      const uint32_t half = dst + (unit[k] >> 2) * C::CP * 128, col = 2 * (unit[k] & 3);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool second = (kThreadsRow == 1 ? e : e ^ (tid & 1)) != 0;
+        const uint32_t a = second ? w[k].z : w[k].x, b = second ? w[k].w : w[k].y;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half + (((col + second) ^ (pos & 7)) << 4)), "r"(scaled(f16x2_of_lo(a))),
+                     "r"(scaled(f16x2_of_hi(a))), "r"(scaled(f16x2_of_lo(b))), "r"(scaled(f16x2_of_hi(b)))
                      : "memory");
       }
     }
@@ -797,11 +796,13 @@ struct ShSoft {
   }
 
   // Step j of the segment, on score place y: scores to weights.  no: the chunk's number in the call.
-  __device__ __forceinline__ bool step(int j, int y, uint32_t no, bool both) {
+  // idle: the warp's rows are behind the tile's last.
+  __device__ __forceinline__ bool step(int j, int y, uint32_t no, bool both, bool idle) {
     if (!sh_wait(sm.s_full(y), steps(y) & 1u)) return false;
     tc_fence_after();
     const uint32_t meta = sm.meta()[no & 7];
-    if (!(meta & kShPlain ? plain(j, y, meta) : uneven(j, y, meta, sm.scale(no % C::kRings)))) return false;
+    if (idle) meet();  // (the weights of its rows may be anything: no product of another row's meets them)
+    else if (!(meta & kShPlain ? plain(j, y, meta) : uneven(j, y, meta, sm.scale(no % C::kRings)))) return false;
     tc_wait_st();
     tc_fence_before();
     mbar_arrive(sm.p_full(y));
@@ -873,10 +874,11 @@ struct ShSoft {
       const int n = ord.steps(), tile = s.pair * C::NS + (ord.both ? x : 0);
       if (x < n) queries(s, tile, G);
       else { open(); mbar_arrive(sm.q_full(x)); }
+      const bool idle = tile * kSharedTile + (r & 96) >= s.g.R;
       int mine = 0, y = C::NS == 2 ? x : 0;
       for (int j = C::NS == 2 ? x : 0; j < n; j += C::NS) {
         y = j & 1;
-        if (!step(j, y, chunk_no + ord.chunk(j), ord.both)) return false;
+        if (!step(j, y, chunk_no + ord.chunk(j), ord.both, idle)) return false;
         ++mine;
       }
       if (!partial(s, tile, mine, y, blockIdx.x)) return false;

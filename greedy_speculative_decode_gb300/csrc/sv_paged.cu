@@ -192,11 +192,16 @@ int64_t shared_bytes(const RowBatch& b, int n_groups, int n_q_heads, int head_di
 }
 
 // Whether a call is so small that attending to each sequence by itself is faster
-// than the four launches of a shared prefix: by what k_attend has to do at most,
-// tiles of 16 query rows times positions that the tables reach.
-bool attend_alone(const RowBatch& b, int group, int n_kv_heads) {
-  const int64_t tiles = b.n_seq * (((int64_t)b.max_rows * group + 15) / 16) * n_kv_heads;
-  return tiles <= (int64_t(1) << 18) / b.limit();
+// than the four launches of a shared prefix: by what k_attend may have to read, rows
+// of K for every tile of 16 query rows over all positions that the tables reach.
+//   us alone and shared, one layer in a graph (8b: 32 / 8 heads of 128; d256: 8 / 1):
+// 8b, 8 x 1 behind 2048, 17 MB: 15 and 24; 8 x 1 behind 8192, 66 MB: 27 and 28; 16 x 8
+// behind 2048, 69 MB: 49 and 34; 8b bf16, 32 x 1 behind 512, 40 MB: 21 and 26; 1 x 64
+// behind 2048, 71 MB: 37 and 31; d256 bf16, 32 x 1 behind 2048, 34 MB: 22 and 29; 4 x 8
+// behind 8192, 66 MB: 38 and 36.
+bool attend_alone(const RowBatch& b, const KvPool& c, int group) {
+  const int64_t tiles = b.n_seq * (((int64_t)b.max_rows * group + 15) / 16) * c.n_kv_heads;
+  return tiles <= (int64_t(56) << 20) / b.limit() / c.row_bytes();
 }
 
 // Groups of sequences: as many as there are sequences at most.
@@ -315,7 +320,7 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
   sp.ml = reinterpret_cast<float2*>(take(sp.plane * shared_streams(c.head_dim) * (int64_t)sizeof(float2)));
   sp.o = reinterpret_cast<float*>(at);
   sp.grid = std::min(num_sms, kSharedMostCtas);
-  const bool share = !attend_alone(p.rows, n_q_heads / c.n_kv_heads, c.n_kv_heads) &&
+  const bool share = !attend_alone(p.rows, c, n_q_heads / c.n_kv_heads) &&
                      shared_units_fit(p.rows, sp.n_groups, n_q_heads, c.n_kv_heads, c.head_dim);
   if (share) p.from = sp.from;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);

@@ -51,7 +51,7 @@ class Case:
             self.start_of.append(i)
         if wide:
             tiles = n_seq * n_kv * -(-max(max(self.lens), 1) * (n_q // n_kv) // 16)
-            more = (1 << 18) // tiles // PAGE + 1 - width
+            more = (56 << 20) // (tiles * d * (2 if fmt == "bf16" else 1)) // PAGE + 1 - width
             if more > 0:
                 table = torch.cat([table, torch.full((n_seq, more), -1, dtype=torch.int32)], 1)
         self.table_h = table
