@@ -94,6 +94,23 @@ __device__ __forceinline__ constexpr uint32_t sh_idesc(int N, bool b_mn) {
          ((uint32_t)(kSharedTile >> 4) << 24);
 }
 
+// Two fp32 values in one instruction's operands.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t x, uint32_t& lo, uint32_t& hi) { asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -490,7 +507,22 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
 }
 
 // ------------------------------------------------------------------ multiplies
-// One warp, of which one lane issues.
+// A place in the ring of operands, and the parity of its phase.
+template <int N>
+struct ShPlace {
+  uint32_t slot, phase;
+  __device__ __forceinline__ void go(uint32_t n) {  // (n <= N)
+    slot += n;
+    if (slot >= N) {
+      slot -= N;
+      phase ^= 1u;
+    }
+  }
+};
+
+// One warp, of which one lane issues.  The tensor cores take a multiply of 128 x 128 x
+// 16 every 64 cycles and hold some eight of them ahead: what the warp does between two
+// batches is kept to a few instructions.
 template <class C>
 __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t tmem) {
   constexpr int CP = C::CP, D = C::D;
@@ -499,51 +531,59 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
   tmem = sh_uniform(tmem);
   ShRun<C::NS> run(p, blockIdx.x);
   ShSegment s;
-  uint32_t at0 = 0, seg = 0;
+  uint32_t seg = 0, steps = 0;  // parities: of the segment, of the two score places
   bool ok = true;
-  uint32_t used0 = 0, used1 = 0;  // uses of each score place so far
-  const uint32_t q_base = sh_uniform(smem_u32(sm.q(0))), op_base = sh_uniform(smem_u32(sm.op(0)));
+  ShPlace<C::kOps> k = {0, 0};
+  const uint64_t q_desc = tc_sdesc(sh_uniform(smem_u32(sm.q(0))));
+  const uint32_t op_base = sh_uniform(smem_u32(sm.op(0)));
+  const uint64_t k_desc = tc_sdesc(op_base), v_desc = tc_sdesc_mn(op_base, CP * 128);
   while (ok && run.next(s)) {
-    const ShOrder ord{(int)sh_uniform(s.i1 - s.i0), sh_uniform(s.w) == 2u};
-    const int n = ord.steps();
-    auto scores = [&](int j) {
-      const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
-      const uint32_t at = at0 + ord.k_at(c);
-      if (j < C::NS && !sh_wait(sm.q_full(stream), seg & 1u)) return false;
-      if (!sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u)) return false;
-      tc_fence_after();
-      const uint64_t a = tc_sdesc(q_base + stream * C::kQBytes), b = tc_sdesc(op_base + at % C::kOps * C::kOpBytes);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc_mma_if(lead, tmem + x * C::kScoreCol, a + (((k / 4) * kSharedTile * 128 + (k % 4) * 32) >> 4),
-                  b + (((k / 4) * CP * 128 + (k % 4) * 32) >> 4), kScores, k > 0);
-      tc_commit_if(lead, sm.s_full(x));
-      if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
-      return true;
-    };
-    for (int j = -2; j < n && ok; ++j) {
+    const int chunks = (int)sh_uniform(s.i1 - s.i0);
+    const bool both = sh_uniform(s.w) == 2u;
+    const int n = both ? 2 * chunks : chunks;
+    ShPlace<C::kOps> v = k;
+    v.go(both || n == 1 ? 1 : 2);
+    for (int j = -2; j < n; ++j) {
+      const uint32_t x = j & 1, stream = C::NS == 2 ? x : 0;
+      const bool last = !both || x;  // of the steps with these operands
       if (j >= 0) {
-      const int x = j & 1, stream = C::NS == 2 ? x : 0, c = ord.chunk(j);
-      const uint32_t at = at0 + ord.v_at(c);
-      ok = sh_wait(sm.p_full(x), (x ? used1 : used0) & 1u) && sh_wait(sm.op_full(at % C::kOps), (at / C::kOps) & 1u);
-      if (!ok) break;
-      used0 += x ^ 1;
-      used1 += x;
-      tc_fence_after();
-      const uint64_t b = tc_sdesc_mn(op_base + at % C::kOps * C::kOpBytes, CP * 128);
-      const uint32_t o = tmem + C::kOutCol + stream * D, w = tmem + x * C::kScoreCol;
+        ok = sh_wait(sm.p_full(x), steps >> x & 1u) && sh_wait(sm.op_full(v.slot), v.phase);
+        if (!ok) break;
+        steps ^= 1u << x;
+        tc_fence_after();
+        const uint64_t b = v_desc + v.slot * (C::kOpBytes >> 4);
+        const uint32_t o = tmem + C::kOutCol + stream * D, w = tmem + x * C::kScoreCol;
 #pragma unroll
-      for (int t = 0; t < (C::kBf16 ? 2 : 1); ++t)
+        for (int t = 0; t < (C::kBf16 ? 2 : 1); ++t)
 #pragma unroll
-        for (int k = 0; k < CP / 16; ++k)
-          tc_mma_ts_if(lead, o, w + (k / 2) * 32 + t * 16 + (k % 2) * 8, b + (k * 16 * 128 >> 4), kValues, j >= C::NS || t > 0 || k > 0);
-      tc_commit_if(lead, sm.pv_done(x));
-      if (!ord.both || x == 1) tc_commit_if(lead, sm.op_empty(at % C::kOps));
+          for (int i = 0; i < CP / 16; ++i)
+            tc_mma_ts_if(lead, o, w + (i / 2) * 32 + t * 16 + (i % 2) * 8, b + (i * 16 * 128 >> 4), kValues, j >= C::NS || t > 0 || i > 0);
+        tc_commit_if(lead, sm.pv_done(x));
+        if (last) {
+          tc_commit_if(lead, sm.op_empty(v.slot));
+          v.go(!both && j == n - 2 ? 1 : 2);
+        }
       }
-      if (j + 2 < n) ok = scores(j + 2);
+      if (j + 2 < n) {
+        ok = (j + 2 >= C::NS || sh_wait(sm.q_full(stream), seg)) && sh_wait(sm.op_full(k.slot), k.phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a = q_desc + stream * (C::kQBytes >> 4), b = k_desc + k.slot * (C::kOpBytes >> 4);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          tc_mma_if(lead, tmem + x * C::kScoreCol, a + (((i / 4) * kSharedTile * 128 + (i % 4) * 32) >> 4),
+                    b + (((i / 4) * CP * 128 + (i % 4) * 32) >> 4), kScores, i > 0);
+        tc_commit_if(lead, sm.s_full(x));
+        if (last) {
+          tc_commit_if(lead, sm.op_empty(k.slot));
+          k.go(!both && j == -2 ? 1 : 2);
+        }
+      }
     }
-    at0 += 2 * ord.n;
-    ++seg;
+    // the next segment's first operand is behind the last of V: v went by two from there
+    k.slot = v.slot == 0 ? C::kOps - 1 : v.slot - 1;
+    k.phase = v.slot == 0 ? v.phase ^ 1u : v.phase;
+    seg ^= 1u;
   }
   // every multiply has completed before tensor memory is freed
   tc_commit_if(lead, sm.drain());
@@ -689,9 +729,11 @@ struct ShSoft {
     tc_st16(place, hi);
     if (C::kBf16) {  // the second: the rest, rounded
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        hi[e] = pack_bf16x2(__fsub_rn(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e] & 0xffff0000u)),
-                            __fsub_rn(__uint_as_float(w[2 * e + 1]), __uint_as_float(w[2 * e + 1] & 0xffff0000u)));
+      for (int e = 0; e < 16; ++e) {
+        uint32_t a, b;  // (a weight is not negative: its upper half with the sign set is what is taken off)
+        split(add2(pair_of(w[2 * e], w[2 * e + 1]), pair_of((w[2 * e] & 0xffff0000u) | 0x80000000u, (w[2 * e + 1] & 0xffff0000u) | 0x80000000u)), a, b);
+        hi[e] = pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
+      }
       tc_st16(place + 16, hi);
     }
   }
@@ -724,7 +766,9 @@ struct ShSoft {
       far = e + 60u < most;
     }
     const float off = __fsub_rn(ev, ref);
-    float sum[2] = {0.0f, 0.0f}, direct = 0.0f;
+    const uint64_t f2 = pair_of(__float_as_uint(f), __float_as_uint(f)), off2 = pair_of(__float_as_uint(off), __float_as_uint(off));
+    uint64_t sum2 = 0;
+    float direct = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < W; c += 32) {
       tc_ld32(place + c, v);
@@ -734,14 +778,18 @@ struct ShSoft {
         for (int i = 0; i < 32; ++i) direct = __fadd_rn(direct, sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, -ref)));
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float e = sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, off));
-        sum[i & 1] = __fadd_rn(sum[i & 1], e);
-        v[i] = __float_as_uint(e);
+      for (int i = 0; i < 32; i += 2) {
+        uint32_t a, b;
+        split(fma2(pair_of(v[i], v[i + 1]), f2, off2), a, b);
+        v[i] = __float_as_uint(sh_ex2(__uint_as_float(a)));
+        v[i + 1] = __float_as_uint(sh_ex2(__uint_as_float(b)));
+        sum2 = add2(sum2, pair_of(v[i], v[i + 1]));
       }
       put(place + c, v);
     }
-    const float all = __fadd_rn(sum[0], sum[1]);
+    uint32_t even_sum, odd_sum;
+    split(sum2, even_sum, odd_sum);
+    const float all = __fadd_rn(__uint_as_float(even_sum), __uint_as_float(odd_sum));
     if (C::kBf16) l = __fadd_rn(l, all);
     else l = far ? __fadd_rn(l, direct) : __fmaf_rn(all, __uint_as_float((254u - (meta >> 24)) << 23), l);
     return true;
