@@ -133,18 +133,18 @@ int block_rows(const RowBatch& b, int n_q_heads, int head_dim) {
   return (int)std::min(most, (each + 15) / 16 * 16);
 }
 
-// What both attention calls check and fill in: all but the window and the rows of a launch.
+// What both attention calls check and fill in: all but the window and the rows of a
+// launch.  need: the call's workspace.
 int read_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, const void* q_dev, int64_t q_stride,
                 void* out_dev, int64_t out_stride, float* lse_dev, float scale, void* workspace_dev,
-                int64_t workspace_bytes, int32_t* status_dev, KvPool& c, AttendParams& p, int& each, int& num_sms) {
+                int64_t workspace_bytes, int64_t need, int32_t* status_dev, KvPool& c, AttendParams& p, int& each,
+                int& num_sms) {
   RowBatch b;
   if (!read_pool(pool, c) || !read_rows(rows, b)) return SV_E_INVAL;
   if (n_q_heads < 1 || n_q_heads % c.n_kv_heads || !std::isfinite(scale)) return SV_E_INVAL;
   if (b.n_seq > kAttendMaxSeq) return SV_E_INVAL;
   const int width = n_q_heads * c.head_dim;
   if (bad16(q_dev) || bad16(out_dev) || bad_stride(q_stride, width) || bad_stride(out_stride, width)) return SV_E_INVAL;
-  int64_t need = 0;
-  if (sv_attend_workspace(pool, rows, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
   if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev) return SV_E_INVAL;
   if (workspace_bytes < need) return SV_E_NOMEM;
   // 32-bit counts on the device, of a block of rows: chunks of 16 positions for
@@ -262,9 +262,10 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
   KvPool c;
   AttendParams p;
   int each, num_sms;
-  if (window < 0 || sinks < 0) return SV_E_INVAL;
+  int64_t need = 0;
+  if (window < 0 || sinks < 0 || sv_attend_workspace(pool, rows, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
   const int rc = read_attend(pool, rows, n_q_heads, q_dev, q_stride, out_dev, out_stride, lse_dev, scale, workspace_dev,
-                             workspace_bytes, status_dev, c, p, each, num_sms);
+                             workspace_bytes, need, status_dev, c, p, each, num_sms);
   if (rc != SV_OK) return rc;
   p.window = window;
   p.sinks = sinks;
@@ -298,9 +299,8 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
   int64_t need = 0;
   if (sv_attend_shared_workspace(pool, rows, prefix, n_q_heads, &need) != SV_OK) return SV_E_INVAL;
   const int rc = read_attend(pool, rows, n_q_heads, q_dev, q_stride, out_dev, out_stride, lse_dev, scale, workspace_dev,
-                             workspace_bytes, status_dev, c, p, each, num_sms);
+                             workspace_bytes, need, status_dev, c, p, each, num_sms);
   if (rc != SV_OK) return rc;
-  if (workspace_bytes < need) return SV_E_NOMEM;
   SharedParams sp = {};
   uint8_t* at = static_cast<uint8_t*>(workspace_dev) +
                 round256(partial_bytes(each, n_q_heads, p.max_splits, c.head_dim));
