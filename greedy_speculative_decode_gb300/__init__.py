@@ -559,7 +559,10 @@ class KvPages:
         self._lock = threading.Lock()
         self._c = SvKvPages(n_seq, width, self.n_pages, _ptr(block_table), _ptr(length), _ptr(held), _ptr(refs))
         self._p = ctypes.byref(self._c)
-        self._fork_bytes = 4 * (self.n_pages + n_seq * width)
+        n = ctypes.c_int64(0)
+        if _lib.sv_kv_fork_workspace(self._p, ctypes.byref(n)) != SV_OK:
+            raise SvError(SV_E_INVAL, "sv_kv_fork_workspace rejected the tables")
+        self._fork_bytes = n.value
         self._tables = frozenset((_ptr(block_table), _ptr(length), _ptr(held), _ptr(refs)))
 
     @classmethod

@@ -71,13 +71,13 @@ struct LpVec<float> {
   static __device__ __forceinline__ void open(const uint4& w, float (&x)[4]) {
     x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
   }
-  static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ float one(const float* p) { return __ldcg(p); }
   static __device__ __forceinline__ float largest(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
   }
   // word i of the 16 bytes from element v, where only lo .. hi - 1 are there
   static __device__ __forceinline__ uint32_t part(const float* p, int v, int i, int lo, int hi) {
-    return v + i >= lo && v + i < hi ? __float_as_uint(__ldg(p + v + i)) : 0xff800000u;
+    return v + i >= lo && v + i < hi ? __float_as_uint(__ldcg(p + v + i)) : 0xff800000u;
   }
 };
 template <>
@@ -91,7 +91,7 @@ struct LpVec<bf16> {
       x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ float one(const bf16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ float one(const bf16* p) { return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p)) << 16); }
   static __device__ __forceinline__ float largest(const uint4& w) {
     uint32_t a, b;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
@@ -103,7 +103,7 @@ struct LpVec<bf16> {
     uint32_t w = 0;
     for (int e = 0; e < 2; ++e) {
       const int at = v + 2 * i + e;
-      w |= (at >= lo && at < hi ? (uint32_t)__bfloat16_as_ushort(p[at]) : 0xff80u) << (16 * e);
+      w |= (at >= lo && at < hi ? (uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p + at)) : 0xff80u) << (16 * e);
     }
     return w;
   }
@@ -127,7 +127,7 @@ struct LpRow {
   // This lane's 16 bytes of block b, which lies within the row.  (Element numbers are at
   // most vocab + 8 and a block: below 2^31.)
   __device__ __forceinline__ uint4 load(int b, int lane) const {
-    return __ldg(reinterpret_cast<const uint4*>(base + b * kBlock + lane * N));
+    return __ldcg(reinterpret_cast<const uint4*>(base + b * kBlock + lane * N));
   }
   // Of one that may not: -infinity outside the row, of which no byte is read.
   __device__ __forceinline__ uint4 edge(int b, int lane) const {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / CS;
   pdl_trigger();
-  pdl_wait();
+  pdl_wait();  // (what the kernels ahead wrote is read past L1, which this one may have shared with them)
   const T* logits = static_cast<const T*>(p.logits) + (int64_t)r * p.stride;
   const Row row(logits, p.vocab);
   const float c = p.scale_log2;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   auto log_prob = [&](float x) { return __fmul_rn(__fsub_rn(__fmaf_rn(x, c, -M), l2), ln2); };
   if (rank == 0) {
     for (int i = tid; i < p.n_tokens; i += kLpThreads) {
-      const int tok = __ldg(p.tokens + (int64_t)r * p.n_tokens + i);
+      const int tok = __ldcg(p.tokens + (int64_t)r * p.n_tokens + i);
       float v = 0.0f;  // a token of -1: an unused place
       if (tok >= 0 && tok < p.vocab) v = log_prob(V::one(logits + tok));
       else if (tok != -1) {

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(256) k_copy_pages(const __grid_constant__ Copy
   const int64_t units = (int64_t)p.n_moves * p.n_pools * 2;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int mv = (int)(u / (2 * p.n_pools)), w = (int)(u - (int64_t)mv * 2 * p.n_pools), at = w >> 1;
-    const int2 m = __ldg(p.moves + mv);
+    const int2 m = __ldcg(p.moves + mv);
     if (m.x == -1 && m.y == -1) continue;
     if ((uint32_t)m.x >= (uint32_t)p.n_from || (uint32_t)m.y >= (uint32_t)p.n_to) {
       if (tid == 0 && p.status) atomicOr(p.status, ST_BAD_PAGE);
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(256) k_copy_pages(const __grid_constant__ Copy
       uint4 x[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (i + k * 4096 < p.page_bytes) x[k] = __ldcs(reinterpret_cast<const uint4*>(src + i + k * 4096));
+        if (i + k * 4096 < p.page_bytes) x[k] = __ldcg(reinterpret_cast<const uint4*>(src + i + k * 4096));
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (i + k * 4096 < p.page_bytes) __stcs(reinterpret_cast<uint4*>(dst + i + k * 4096), x[k]);
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(256) k_copy_pages(const __grid_constant__ Copy
     if (p.exp_bytes) {
       const uint8_t* es = (w & 1 ? pool.v_exp : pool.k_exp) + (int64_t)m.x * p.exp_bytes;
       uint8_t* ed = (w & 1 ? pool.v_exp_to : pool.k_exp_to) + (int64_t)m.y * p.exp_bytes;
-      for (int i = tid; i < p.exp_bytes; i += 256) ed[i] = __ldcs(es + i);
+      for (int i = tid; i < p.exp_bytes; i += 256) ed[i] = __ldcg(es + i);
     }
   }
 }

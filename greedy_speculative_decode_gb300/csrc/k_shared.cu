@@ -11,13 +11,13 @@ namespace {
 // rows of the group see (whole pages of them), and the work this makes.  One
 // thread a sequence, then one a group.
 __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ SharedParams p, int chunk, int streams) {
-  __shared__ int s_eff[1024], s_start[1025];
+  __shared__ int s_eff[1024], s_lead[1024], s_start[1025];  // s_lead: a group's first sequence with rows that see something
   __shared__ int s_sum[32], s_sum2[32], s_unit[1025], s_list[1025];  // units and lists before each group
   __shared__ int2 s_first[256];  // of each list, where CTAs' runs end with lists: its first unit, and CTA
   const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
   pdl_trigger();
   pdl_wait();
-  auto start_of = [&](int s) { return p.a.rows.row_start ? __ldg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
+  auto start_of = [&](int s) { return p.a.rows.row_start ? __ldcg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
   auto clip = [&](int r) { return min(max(r, 0), p.a.rows.n_rows); };
   int first = 0, n = 0;
   if (tid < S) {
@@ -26,10 +26,11 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   }
   if (tid < 32) s_sum[tid] = s_sum2[tid] = 0;
   for (int g = tid; g <= N; g += blockDim.x)
-    s_start[g] = p.group_start ? min(max(__ldg(p.group_start + g), 0), S) : (int)((long long)S * g / N);
+    s_start[g] = p.group_start ? min(max(__ldcg(p.group_start + g), 0), S) : (int)((long long)S * g / N);
   if (tid < N) {
-    const int most = min(max(__ldg(p.length + tid), 0), p.a.rows.limit());
+    const int most = min(max(__ldcg(p.length + tid), 0), p.a.rows.limit());
     s_eff[tid] = most;
+    s_lead[tid] = S;
   }
   __syncthreads();
   const bool back = __syncthreads_or(tid < N && s_start[tid + 1] < s_start[tid]);
@@ -43,7 +44,10 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
         if (s_start[mid] <= tid) lo = mid; else hi = mid;
       }
       gi = lo;
-      if (n > 0 && first + n > 0) atomicMin(&s_eff[gi], max(first, 0) + 1);  // (rows of padding alone see nothing)
+      if (n > 0 && first + n > 0) {  // (rows of padding alone see nothing)
+        atomicMin(&s_eff[gi], max(first, 0) + 1);
+        atomicMin(&s_lead[gi], tid);
+      }
     }
     p.group[tid] = gi;
   }
@@ -51,9 +55,9 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   SharedGroup g = {};
   int units = 0;
   if (tid < N) {
-    g.s0 = s_start[tid];
-    if (!back && s_start[tid + 1] > g.s0) {
-      g.row0 = clip(start_of(g.s0));
+    g.s0 = s_lead[tid];
+    if (!back && g.s0 < S) {
+      g.row0 = clip(start_of(s_start[tid]));
       const int rows = clip(start_of(s_start[tid + 1])) - g.row0;
       if (rows > 0) {
         g.eff = s_eff[tid] / kPage * kPage;

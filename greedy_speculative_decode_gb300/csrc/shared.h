@@ -15,7 +15,7 @@ __host__ __device__ constexpr int shared_chunk(int d) { return d <= 128 ? 128 : 
 struct SharedGroup {
   int unit0;     // units of work before it (a unit: a chunk for a tile); behind the last group the total
   int eff;       // positions that all its rows see and share; behind the last group the CTAs that take part
-  int s0;        // its first sequence, whose table is read
+  int s0;        // its first sequence with rows that see something, whose table is read
   int row0, R;   // its first row, and its query rows for a kv head
   int chunks, tiles;
   int aligned;   // behind the last group: whether CTAs' runs end with lists (sh_first)

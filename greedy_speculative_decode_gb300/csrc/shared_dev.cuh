@@ -333,7 +333,7 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
       const int pos = (it.s.i0 + it.c) * C::CP + lane * kPage;
       far.there = true;
       far.wanted = lane < C::kPages && pos < it.s.g.eff;
-      if (far.wanted) far.page = __ldg(p.a.rows.table + (size_t)it.s.g.s0 * p.a.rows.table_stride + pos / kPage);
+      if (far.wanted) far.page = __ldcg(p.a.rows.table + (size_t)it.s.g.s0 * p.a.rows.table_stride + pos / kPage);
       far.kvh = it.s.kvh;
       far.at = it.at;
       far.chunk = it.chunk0;
@@ -354,10 +354,10 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
     if (!C::kBf16 && have) {
       const size_t ph = (size_t)now.page * p.a.n_kv_heads + now.kvh;
       if (p.a.block == 1) {
-        ke = __ldg(reinterpret_cast<const uint4*>(p.a.k_exp) + ph);
-        ve = __ldg(reinterpret_cast<const uint4*>(p.a.v_exp) + ph);
+        ke = __ldcg(reinterpret_cast<const uint4*>(p.a.k_exp) + ph);
+        ve = __ldcg(reinterpret_cast<const uint4*>(p.a.v_exp) + ph);
       } else {
-        const uint32_t a = __ldg(p.a.k_exp + ph) * 0x01010101u, b = __ldg(p.a.v_exp + ph) * 0x01010101u;
+        const uint32_t a = __ldcg(p.a.k_exp + ph) * 0x01010101u, b = __ldcg(p.a.v_exp + ph) * 0x01010101u;
         ke = make_uint4(a, a, a, a);
         ve = make_uint4(b, b, b, b);
       }
@@ -603,7 +603,7 @@ struct ShSoft {
   const uint32_t lane_off;  // the warp's lanes of tensor memory
   const uint32_t tmem;
   float ref, l, fac;
-  uint32_t most;               // largest value exponent (byte) of the segment's plain chunks so far
+  uint32_t most;               // largest value exponent (byte) of the segment's chunks so far
   uint32_t steps0 = 0, steps1 = 0;  // steps of each score place so far
 
   __device__ __forceinline__ ShSoft(const SharedParams& p_, const ShSmem<C>& sm_, uint32_t tm)
@@ -822,6 +822,7 @@ struct ShSoft {
       for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
     }
     if (!follow(larger(top, y), j, y)) return false;
+    if (!C::kBf16) most = max(most, meta >> 24);
     float sum = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < W; c += 32) {

@@ -466,7 +466,8 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
  *   Group g is the sequences group_start[g] .. group_start[g + 1] - 1 (device int32
  * [n_groups + 1], not decreasing, or NULL: n_seq / n_groups each; at most n_seq
  * groups).  All of them have the same pages for positions 0 .. length[g] - 1 (device
- * int32 [n_groups]): the table row of the group's first sequence is read for them.
+ * int32 [n_groups]): the table row of the group's first sequence with rows that see
+ * something is read for them.
  * Only whole pages that every row of the group sees count as shared (a row within
  * the prefix limits it for its group); the rest, and sequences in no group, are
  * attended to as by sv_attend.  No window.

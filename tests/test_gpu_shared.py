@@ -282,6 +282,26 @@ def test_pages_that_are_not_there(fmt, block, d):
     assert (f64(out)[:3] == 0).all() and (f64(lse)[:3] == -np.inf).all()
 
 
+@pytest.mark.parametrize("fmt,block", FORMS)
+def test_a_group_whose_first_sequences_have_ended(fmt, block):
+    """Sequences without rows, or with padding alone, may have any table."""
+    c = Case(21, 4, 2, 128, [(256, [(256, 0), (-2, 2), (260, 1), (300, 2)]), (64, [(-5, 1), (70, 1)]), (32, [(-1, 1)])], fmt, block)
+    c.table[0] = c.table[1] = c.table[4] = c.table[6] = -1
+    c.check()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_even_chunks_beside_uneven_ones(d):
+    """Values whose exponents are far apart, in one chunk and between chunks (an 8-bit cache)."""
+    c = Case(22, 4, 1, d, [(512, [(520, 1), (512, 2)])], "e4m3", 1, spread=1.0)
+    pages = c.table_h[0, :32].long().cuda()
+    for chunk, e in enumerate((60, 150, 40, 110)):
+        c.cache.v_exp[pages[8 * chunk:8 * chunk + 8]] = e
+    for odd in ((), (3,), (9, 12), (17,), (3, 9, 17, 30)):
+        c.cache.v_exp[pages[list(odd)], :, 5] = 100
+        c.check()
+
+
 def test_queries_that_are_not_finite_and_very_uneven():
     for fmt in ("bf16", "e4m3"):
         c = Case(17, 4, 2, 128, [(144, [(150, 1), (150, 1), (150, 1)])], fmt)
