@@ -7,7 +7,12 @@
 // over rows and pages, no order of arrival.  Each is one launch of one cluster
 // of up to eight CTAs, which meet at the cluster's barriers: a table's numbers are few
 // (64 rows of 256 pages and 20 thousand pages are 200 KB, in L2), so what bounds
-// them is the chain of dependent loads and barriers, not bytes.
+// them is the chain of dependent loads and barriers, not bytes: with the copy of
+// its pages a fork of 1 row to 8 takes 7.9 us in a graph (one CTA; 14 with eight),
+// of 64 rows of up to 4096 positions 15.4 (eight CTAs).  The copy of the pages is a
+// kernel of its own behind the plan, queued before that has ended; it is bound by
+// memory: 64 x 4096 positions of two layers compacted, 180 MB read and as many
+// written, in 72-76 us, 0.71 of the copy rate.
 //
 // Free pages are found by rank: a warp counts those of its range of pages with
 // ballots, the counts are summed over warps and CTAs, and a second look at the

@@ -9,28 +9,43 @@
 // behind the prefix goes through k_attend; a merge adds both.
 //
 // A CTA has two streams of steps, each with its scores, accumulators and softmax
-// warpgroup, so that one's products run beside the other's exponentials: two
+// warpgroups, so that one's products run beside the other's exponentials: two
 // tiles of 128 query rows that share the chunks of K and V they load, or, of a
 // single tile, the even and the odd chunks.  (Rows of 256 elements leave tensor
 // memory for one stream only; its scores alternate between two places.)
-//   Warps 0-3, 4-7: softmax of a stream, a query row a thread.  Scores are read from
-//     tensor memory, the weights go back there over them as the A operand of P V.
-//     The reference of a row moves only when its maximum rises by more than 2^8
-//     over it, so the accumulators are seldom read back and rescaled.
-//   Warp 8: one thread issues the multiplies.  Warps 9, 10: loads of K and V.
-//   Warps 12-15 (8-bit caches): codes to f16, once for all query rows of the CTA.
+//   Warps 0-7, 8-15: softmax of a stream.  Each of its two warpgroups takes half of a
+//     chunk's positions, a query row a thread; the halves exchange their largest score
+//     in shared memory.  Scores are read from tensor memory, the weights go back there
+//     over them as the A operand of P V.  The reference of a row moves only when its
+//     maximum rises by more than 2^8 over it, so the accumulators are seldom read back
+//     and rescaled.  (A warpgroup a stream, a whole row a thread: 132 us for 128 x 1 behind
+//     16384 where two took 120, 92 and 81 for 64 x 4 behind 4096.)
+//   Warp 16: its elected thread issues the multiplies.  Warps 17, 18: loads of K and V.
+//   Warps 20-23 (8-bit caches): codes to f16, once for all query rows of the CTA.
+// (One stream, D = 256: softmax warps 0-7, then 8, 9 and 10, 12-15.)
 //
 // Types, as in attend_dev.cuh: a bf16 cache's weights are the sum of two bf16
 // values (2^-16); over an 8-bit cache weights are f16 and carry the value's
 // exponent, t' = log2(e) s + ev, queries go to f16 divided by a power of two near
-// their row's largest value; sums, references and accumulators are fp32.
+// their row's largest value; sums, references and accumulators are fp32.  Where the
+// exponents of a chunk's keys lie within 2^15 of one another and its values' within
+// 2^7 they are folded into the f16 operands instead (exact: a code has 4 bits), and
+// its scores and sums need no factor a position; other chunks ("uneven") do.
 //
 // Work is divided as chunks of all (group, kv head, tiles) lists one behind the
 // other.  Where every list is enough for a CTA each has a number of them for itself,
 // else all lists are cut into equal runs.  Each CTA leaves a partial (reference, sum,
 // accumulators) for each list its run touches, and the merge adds them in order.
 // (A new list costs a CTA some 5 us: queries, and a partial.  Equal runs throughout:
-// 71 us for 128 x 1 behind 16384, now XX; XX and XX for 64 x 4 behind 4096.)
+// 78 us for 128 x 1 behind 16384, now 72; 71 and 59 for 64 x 4 behind 4096.)
+//
+// Measured (32 / 8 heads of 128 unless noted; the whole call, then this kernel): bf16,
+// 64 x 1 behind 32768: 78 and 45 us, 134 MB of prefix, of which the products alone are
+// 24 us of a tensor pipe (three of 64 cycles for each 16 columns: S, P's two terms);
+// e4m3, 32 x 1 behind 8192: 38 and 17; 64 x 4 behind 4096, 28 / 4 heads: 59; bf16, d 256,
+// 13 x 2, 8 / 1 heads: 34.  Neither memory nor the pipe is full (52 % for bf16, 37 % for
+// e4m3): a stream's step is a chain, S, softmax, P V, and two of them overlap; the
+// softmax's warps issue an instruction every other cycle.
 #pragma once
 #include "paged_dev.cuh"
 #include "shared.h"
