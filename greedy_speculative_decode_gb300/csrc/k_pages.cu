@@ -75,6 +75,11 @@ struct PageRange {
     a = (int)(steps * w / kAll);
     b = (int)(steps * (w + 1) / kAll);
   }
+  // Whether a page is in the range of one of a CTA's warps.
+  static __device__ __forceinline__ bool has(int n_pages, int rank, int page) {
+    const unsigned steps = (n_pages + 31) / 32, step = (unsigned)page / 32;
+    return step >= steps * rank / CTAS && step < steps * (rank + 1) / CTAS;
+  }
 };
 
 // Pages of the range with a count of zero.
@@ -205,8 +210,6 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPgThreads, 1) k_
     s.offset[tid] = offset;
     if (copy) s.last[tid] = -2 - last;  // (every thread has compared: block_scan's barriers)
   }
-  // (page counts of copied pages stay above zero: whether a page is free does not change)
-  if (rank == 0 && copy) atomicSub(p.count + last, 1);
   // ---- free pages, lowest first
   const PageRange<CTAS> range(p.in.n_pages, rank);
   const int mine = count_free(range, p.count, p.in.n_pages);
@@ -219,6 +222,11 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kPgThreads, 1) k_
     meet<CTAS>();  // the others read this CTA's total
     return;
   }
+  // A copied page has a holder less.  Behind the barrier, for until then the other CTAs
+  // may have `holders` still to read; each CTA for the pages that it has below.  (The
+  // counts stay above zero: whether a page is free does not change.)
+  if (copy && PageRange<CTAS>::has(p.in.n_pages, rank, last)) atomicSub(p.count + last, 1);
+  __syncthreads();
   for (int st = range.a; st < range.b; ++st) {
     const int page = st * 32 + lane;
     const int n = page < p.in.n_pages ? __ldcg(p.count + page) : 1;
