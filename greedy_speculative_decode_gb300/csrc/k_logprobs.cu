@@ -29,6 +29,7 @@
 #include "sv_ptx.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <cooperative_groups.h>
 
 #include "logprobs.h"
@@ -41,7 +42,10 @@ namespace cg = cooperative_groups;
 // Threads of a CTA: 128 for short rows, of which an SM then holds more.
 constexpr int kLpWide = 512, kLpNarrow = 128;
 constexpr int kLpMost = kLogprobsMaxTop;
-constexpr float kLpNone = -3.0e38f;  // reference of what has seen nothing
+constexpr float kLpFar = 536870912.0f;  // 2^29: half a step of a reference below it is at most 16
+// Reference of what has seen nothing: logits below it (masks of -1e30 or the type's lowest
+// value) weigh nothing, where a reference of their own would be off by more than 2^127.
+constexpr float kLpNone = -kLpFar;
 constexpr float kLpSlack = 4.0f;    // log2 of what a weight may be before the reference follows
 static_assert(kLpMost == 32, "a lane holds one of a warp's best");
 
@@ -203,6 +207,46 @@ __device__ __forceinline__ void lp_rank(LpShared<TH>& s, bool have, uint32_t key
   __syncthreads();
 }
 
+// A row whose largest y = x c is beyond kLpFar: a reference rounded to fp32 would lie too
+// far from it for 2^(y - m), and c x may be beyond fp32's range (rows masked with -1e30 or
+// the type's lowest value throughout).  Its largest logit X (-infinity: none is
+// finite) and the sums of z = (x - X) c.  Each CTA reads the whole row, plainly: such rows
+// are rare.
+template <class T, int TH>
+__device__ __noinline__ void lp_far_row(LpShared<TH>& s, const T* logits, int vocab, float c, float& X, float& L, float& E) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  X = -INFINITY;
+#pragma unroll 1
+  for (int i = tid; i < vocab; i += TH) X = fmaxf(X, LpVec<T>::one(logits + i));
+  X = warp_max(X);
+  __syncthreads();  // (the warps' numbers have been read)
+  if (lane == 0) s.m[warp] = X;
+  __syncthreads();
+  for (int i = 0; i < TH / 32; ++i) X = fmaxf(X, s.m[i]);
+  L = E = 0.0f;
+#pragma unroll 1
+  for (int i = tid; X > -INFINITY && i < vocab; i += TH) {
+    const float z = __fmul_rn(__fsub_rn(LpVec<T>::one(logits + i), X), c), q = lp_ex2(z);
+    L = __fadd_rn(L, q);
+    E = __fmaf_rn(q, fmaxf(z, -1000.0f), E);  // (an impossible token's 0 * inf is zero)
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    L = __fadd_rn(L, __shfl_xor_sync(0xffffffffu, L, o));
+    E = __fadd_rn(E, __shfl_xor_sync(0xffffffffu, E, o));
+  }
+  if (lane == 0) {
+    s.l[warp] = L;
+    s.t[warp] = E;
+  }
+  __syncthreads();
+  L = E = 0.0f;
+  for (int i = 0; i < TH / 32; ++i) {
+    L = __fadd_rn(L, s.l[i]);
+    E = __fadd_rn(E, s.t[i]);
+  }
+}
+
 template <class T, int TH, bool kTop, bool kEntropy>
 __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   using V = LpVec<T>;
@@ -324,11 +368,21 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
     }
     meet(CS, [&](int i, int k) { return __shfl_sync(0xffffffffu, all[k], i); }, M, L, E);
   }
+  float X = 0.0f;
+  const bool is_far = !(fabsf(M) < kLpFar);  // (the same for all CTAs of the row)
+  if (is_far) {
+    lp_far_row<T, TH>(s, logits, p.vocab, c, X, L, E);
+    M = X;
+  }
   // A row with a NaN or an infinity, or of nothing but -infinity, has no distribution.
   const float NaN = __uint_as_float(0x7fffffffu), ln2 = 0.6931471805599453f;
   const bool good = L > 0.0f && L < INFINITY && fabsf(M) < INFINITY;
   const float l2 = good ? log2f(L) : NaN;
-  auto log_prob = [&](float x) { return __fmul_rn(__fsub_rn(__fmaf_rn(x, c, -M), l2), ln2); };
+  auto log_prob = [&](float x) {
+    const float z = is_far ? __fmul_rn(__fsub_rn(x, X), c) : __fmaf_rn(x, c, -M), v = __fmul_rn(__fsub_rn(z, l2), ln2);
+    // (a finite logit's is finite: beyond fp32's range the rest of z is nothing beside x c)
+    return v == -INFINITY && x > -INFINITY ? fmaxf(__fmul_rn(x, __fmul_rn(c, ln2)), -FLT_MAX) : v;
+  };
   if (rank == 0) {
     for (int i = tid; i < p.n_tokens; i += kLpThreads) {
       const int tok = __ldcg(p.tokens + (int64_t)r * p.n_tokens + i);
@@ -341,7 +395,10 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
       p.out[(int64_t)r * p.n_tokens + i] = v;
     }
     if (tid == 0) {
-      if (p.lse) p.lse[r] = __fmul_rn(__fadd_rn(M, l2), ln2);
+      if (p.lse) {
+        const float far_lse = fminf(fmaxf(__fmaf_rn(X, __fmul_rn(c, ln2), __fmul_rn(l2, ln2)), -FLT_MAX), FLT_MAX);
+        p.lse[r] = is_far && good ? far_lse : __fmul_rn(__fadd_rn(M, l2), ln2);
+      }
       if (p.entropy) p.entropy[r] = max_nan(__fmul_rn(__fsub_rn(l2, __fdiv_rn(E, L)), ln2), 0.0f);
     }
   }

@@ -562,10 +562,12 @@ int sv_kv_copy(const sv_kv_pool* from, const sv_kv_pool* into, int n_pools, cons
  * lse, entropy, top_values, top_ids: fp32 (ids int32) or NULL.  A logit of -infinity
  * is a token of probability zero: log probability -infinity, never among the most
  * probable (places left over: id -1, -infinity).  A row with a NaN or +infinity, or
- * of -infinities alone, has no distribution: its results are NaN, its ids -1.  (So
- * has one with a |scale x| beyond 2^127.)  A token of -1 gives 0 (an unused place),
- * any other outside 0 .. vocab - 1 a NaN and status bit 4.  Sums are fp32.  A
- * row's results do not depend on the other rows' values. */
+ * of -infinities alone, has no distribution: its results are NaN, its ids -1.
+ * Finite logits are logits whatever their size: a row of nothing but a mask's
+ * -1e30 or the type's lowest value is a uniform distribution, and a log probability
+ * or lse beyond fp32's range is the finite value nearest to it.  A token of -1
+ * gives 0 (an unused place), any other outside 0 .. vocab - 1 a NaN and status bit 4.
+ * Sums are fp32.  A row's results do not depend on the other rows' values. */
 #define SV_LOGITS_F32 0
 #define SV_LOGITS_BF16 1
 int sv_logprobs(const void* logits_dev, int dtype, int64_t stride, int n_rows, int vocab, float scale,

@@ -96,7 +96,7 @@ def logprobs(x, tokens, scale, top):
             w = np.exp(y[r] - m)
             lse[r] = m + np.log(w.sum())
             p = w / w.sum()
-            lp = y[r] - lse[r]
+            lp = (y[r] - m) - np.log(w.sum())  # (y - lse would lose the sum beside logits of 1e17 and more)
             ent[r] = -(p[p > 0] * lp[p > 0]).sum()
             order = np.lexsort((np.arange(vocab), -x[r]))[:top]
             order = order[x[r][order] > -np.inf]

@@ -171,6 +171,48 @@ def test_alternatives_of_rows_in_an_unkind_order(dtype, kind, n):
     assert (ti == one[4]).all()  # ids do not depend on the rows beside (cut into more CTAs or fewer)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [700, 5001, 151936])
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+def test_masks_of_the_lowest_value(dtype, vocab, scale):
+    # the largest finite x of row 4 is itself below what x log2(e) leaves of fp32's range
+    low = torch.finfo(dtype).min
+    x = torch.full((5, vocab), low, dtype=dtype, device="cuda")
+    x[1, ::3] = -float("inf")
+    x[2, vocab // 2] = 1.5
+    x[3, 5:] = logits(9, 1, vocab - 5, dtype)[0]
+    x[4, 7], x[4, 300] = low * 0.75, low * 0.75
+    tokens = torch.tensor([[0, vocab - 1], [1, 3], [vocab // 2, 4], [4, 5], [7, 8]], dtype=torch.int32, device="cuda")
+    for top in (0, 4, 32):
+        check(x, tokens, scale=scale, top=top)
+    # scale x below fp32's range
+    out, lse, ent, tv, ti, st = run(x, tokens, 2.0, 4)
+    most = torch.finfo(torch.float32).min
+    assert out[2, 1] == most and out[3, 0] == most and lse[0] == most and lse[1] == most
+    assert abs(out[0, 0].item() + np.log(vocab)) < 1e-4 and abs(ent[0].item() - np.log(vocab)) < 1e-3
+    assert ti[0].tolist() == [0, 1, 2, 3] and ti[4, :2].tolist() == [7, 300] and st == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [700, 151936])
+def test_rows_far_from_zero(dtype, vocab):
+    # differences beside logits that have few bits left for them
+    bases = (-1.0e5, 1.0e8, -1.0e9, -1.0e10, 3.0e10, -1.0e30, 1.7e38, -2.2e38)
+    x = torch.stack([torch.full((vocab,), b, dtype=dtype, device="cuda") for b in bases])
+    x[:, 5:9] *= 1.0 + 2.0 * torch.finfo(dtype).eps
+    x[:, 600] = -float("inf")
+    tokens = torch.tensor([[5, 0, 600, vocab - 1]] * len(bases), dtype=torch.int32, device="cuda")
+    for top in (0, 8):
+        check(x, tokens, top=top)
+    x[3, 9], x[4, 9], x[5, 9] = float("nan"), float("inf"), 2.0
+    check(x, tokens, top=8)
+    # the same as masks: most of a row, and what stands before and behind the rest
+    x[:, 300:420] = logits(3, 8, 120, dtype)
+    x[3, 9], x[4, 9] = bases[3], bases[3]
+    tokens[:, 1] = 333
+    check(x, tokens, top=8)
+
+
 def test_large_and_far_apart_logits():
     x = torch.zeros((4, 3000), device="cuda")
     x[0] = torch.linspace(-1.0e4, 1.0e4, 3000)
