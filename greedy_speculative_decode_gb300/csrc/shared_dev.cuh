@@ -66,6 +66,7 @@ constexpr float kShSlack = 8.0f;     // log2 of what a row's maximum may rise by
 __host__ __device__ constexpr float sh_bias(bool bf16) { return bf16 ? 0.0f : 7.0f; }
 constexpr int kShKeySpread = 15, kShValueSpread = 7;  // of the exponents of an even chunk
 constexpr float kShNone = -3.0e38f;  // reference of a row that has seen nothing
+constexpr float kShBig = 1048576.0f;  // 2^20: half a step of a reference is 1 / 32 of log2
 constexpr float kShFar = -126.0f;    // 2^x is a normal fp32 number from here on
 
 template <int D_, int FMT_>
@@ -708,7 +709,7 @@ struct ShSoft {
   // The reference follows a row's largest score `top` of step j where it has risen by more than the slack.
   __device__ __forceinline__ bool follow(float top, int j, int y) {
     constexpr float kBias = sh_bias(C::kBf16);
-    const bool up = top > __fadd_rn(ref, kShSlack + kBias);
+    const bool up = __fsub_rn(top, ref) > kShSlack + kBias;  // (the difference is exact, a sum need not be)
     if (!__any_sync(0xffffffffu, up)) return true;
     top = __fsub_rn(top, kBias);
     const float d = up ? __fsub_rn(ref, top) : 0.0f, a = sh_ex2(d);
@@ -780,17 +781,24 @@ struct ShSoft {
       most = max(most, e);
       far = e + 60u < most;
     }
-    const float off = __fsub_rn(ev, ref);
-    const uint64_t f2 = pair_of(__float_as_uint(f), __float_as_uint(f)), off2 = pair_of(__float_as_uint(off), __float_as_uint(off));
+    // Large scores: a reference is rounded, so the product less it, which is rounded once,
+    // would not be what `follow` compared; take the rounded score less the reference.
+    const bool big = __any_sync(0xffffffffu, fabsf(ref) > kShBig && ref != kShNone);
+    const float fac1 = big ? 1.0f : f, off = big ? 0.0f : __fsub_rn(ev, ref), off_key = big ? -ev : -ref;
+    const uint64_t f2 = pair_of(__float_as_uint(fac1), __float_as_uint(fac1)), off2 = pair_of(__float_as_uint(off), __float_as_uint(off));
     uint64_t sum2 = 0;
     float direct = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < W; c += 32) {
       tc_ld32(place + c, v);
       tc_wait_ld();
+      if (big) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__fsub_rn(__fmaf_rn(__uint_as_float(v[i]), f, ev), ref));
+      }
       if (!C::kBf16 && far) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) direct = __fadd_rn(direct, sh_ex2(__fmaf_rn(__uint_as_float(v[i]), f, -ref)));
+        for (int i = 0; i < 32; ++i) direct = __fadd_rn(direct, sh_ex2(__fmaf_rn(__uint_as_float(v[i]), fac1, off_key)));
       }
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
@@ -814,7 +822,7 @@ struct ShSoft {
   __device__ __forceinline__ bool uneven(int j, int y, uint32_t meta, const float* sc) {
     const uint32_t place = scores_at(y);
     const bool even = C::kBf16 || meta & kShEven;
-    const float ks = C::kBf16 ? 1.0f : sh_meta_key(meta), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
+    const float kf = C::kBf16 ? fac : __fmul_rn(fac, sh_meta_key(meta)), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
     const float iv = __uint_as_float((254u - (meta >> 24)) << 23);
     const uint32_t there = meta >> (h * (W / kPage));
     sc += h * W;
@@ -824,8 +832,10 @@ struct ShSoft {
       tc_wait_ld();
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        float t = __fmul_rn(__uint_as_float(w[i]), fac);
-        if (!C::kBf16) t = even ? __fmaf_rn(t, ks, vs) : __fmaf_rn(t, sc[c + i], sc[CP + c + i]);
+        // (rounded once, as a plain chunk's)
+        const float t = C::kBf16 ? __fmul_rn(__uint_as_float(w[i]), fac)
+                        : even   ? __fmaf_rn(__uint_as_float(w[i]), kf, vs)
+                                 : __fmaf_rn(__uint_as_float(w[i]), __fmul_rn(fac, sc[c + i]), sc[CP + c + i]);
         w[i] = (there >> ((c + i) / kPage)) & 1u ? __float_as_uint(t) : 0xff800000u;
       }
     };

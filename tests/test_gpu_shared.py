@@ -209,6 +209,60 @@ def test_scores_that_rise_and_fall(fmt, block, d):
         c.check(q=q)
 
 
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_scores(fmt, block, d):
+    """All keys alike: whatever a score's size and sign, the result is a mean of the values.
+
+    The shared positions have one score, the row's own another: their kernels add the d
+    products in different orders, each sum off by at most d 2^-23 sum |q k| (fp32
+    accumulation, truncating), and round the score (2^-23 |s|, twice).  In log2 units
+    that is E below, and the own positions weigh 2^-E to 2^E times as much as the
+    shared ones; the result moves from one end to the other of an interval."""
+    c = Case(23, 4, 1, d, [(640, [(640, 1), (655, 2)])], fmt, block, spread=0.0)
+    c.cache.k[:] = c.cache.k[:1, :, :1].clone()
+    if fmt != "bf16":
+        c.cache.k_exp[:], c.cache.v_exp[:] = 127, 120
+    q = c.queries(0.0)
+    v = f64(c.cache.v) if fmt == "bf16" else f64(c.cache.v.view(torch.float8_e4m3fn)) * 2.0 ** -7
+    k = (f64(c.cache.k) if fmt == "bf16" else f64(c.cache.k.view(torch.float8_e4m3fn)))[0, 0, 0]
+    size = np.abs(f64(q) * k).sum(-1)
+    for scale in (0.0, 1.0e3, -1.0e5, 1.0e7, 3.3e9, -1.0e12, 2.0e20):
+        out, lse = c.call(q, scale=scale)
+        got = f64(out)
+        for r, (s, t) in enumerate(((0, 640), (1, 655), (1, 656))):
+            x = np.concatenate([v[int(c.table_h[s, p]), 0] for p in range(t // PAGE + 1)])[:t + 1]
+            E = abs(scale) * np.log2(np.e) * size[r] * (2 * d * 2.0 ** -23 + 2.0 ** -22)
+            ends = []
+            for w in (-E, E):
+                a, b = np.exp2(np.minimum(-w, 0))[:, None], np.exp2(np.minimum(w, 0))[:, None]
+                ends.append((a * x[:640].sum(0) + b * x[640:].sum(0)) / (640 * a + (t - 639) * b))
+            # weights alike within 2^-11 (f16; bf16 in two terms closer), sums in fp32, a bf16 result
+            big = np.maximum(np.abs(x[:640]).mean(0), np.abs(x[640:]).mean(0))
+            lo, hi = np.minimum(*ends), np.maximum(*ends)
+            tol = 2.0 ** -10 * big + 2.0 ** -8 * np.maximum(np.abs(lo), np.abs(hi))
+            assert (got[r] >= lo - tol).all() and (got[r] <= hi + tol).all(), (scale, r)
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_scores_of_shared_positions_alone(fmt, block, d):
+    c = Case(24, 4, 1, d, [(640, [(639, 1), (639, 1)])], fmt, block, spread=0.0)
+    c.cache.k[:] = c.cache.k[:1, :, :1].clone()
+    if fmt != "bf16":
+        c.cache.k_exp[:], c.cache.v_exp[:] = 127, 120
+    q = c.queries(0.0)
+    v = f64(c.cache.v) if fmt == "bf16" else f64(c.cache.v.view(torch.float8_e4m3fn)) * 2.0 ** -7
+    x = np.concatenate([v[int(c.table_h[0, p]), 0] for p in range(40)])
+    for uneven in (False, True):
+        if uneven:  # (a page that is not there, in one chunk)
+            c.table[:, 3] = -1
+            x = np.concatenate([x[:48], x[64:]])
+        for scale in (0.0, 1.0e3, -1.0e5, 1.0e7, 3.3e9, -1.0e12, 2.0e20):
+            got = f64(c.call(q, scale=scale)[0])
+            assert (np.abs(got - x.mean(0)) <= 2.0 ** -10 * np.abs(x).mean(0) + 2.0 ** -8 * np.abs(x.mean(0))).all(), scale
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_blocks_of_zeros_beside_large_values(d):
     """Exponents of values 2^120 apart: denominators hold (an 8-bit cache)."""
