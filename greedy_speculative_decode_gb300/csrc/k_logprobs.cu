@@ -18,13 +18,15 @@
 //
 // What bounds it: for many rows instructions, then memory (some 12 an element of
 // bf16: widen, maximum, scale, subtract, exponential, two sums; 2048 x 151936, 622
-// MB, in 129 us, 0.71 of the copy rate at 0.77 instructions a cycle and scheduler);
+// MB, in 122 us, 0.75 of the copy rate at 0.77 instructions a cycle and scheduler);
 // for a few the chain of load, meeting and second look (1 x 151936 fp32 with 20
-// alternatives 10.6 us in a graph, 6.6 without any; 24 x 262144 bf16 with 5 14.8).  A
+// alternatives 10.8 us in a graph, 6.0 without any; 24 x 262144 bf16 with 5 15).  A
 // row is a cluster of 1 to 8 CTAs, so that few rows fill the device too; they meet
 // over distributed shared memory.  (Up to 16 CTAs a row: 13.0 us for the first,
 // 17.9 for the last.  Sums of pairs in one instruction, fma.f32x2: 148 us for 2048
-// x 151936; the packing costs more than it saves.)
+// x 151936; the packing costs more than it saves.  Two blocks at a time: 117 to 125,
+// by what the compiler makes of it, and 100 instead of 75 for 500 x 151936 fp32 with
+// 20 alternatives, whose CTAs then take the registers of a third of an SM.)
 #include "sv_internal.h"
 #include "sv_ptx.cuh"
 
