@@ -51,6 +51,7 @@
 #include "shared.h"
 #include "tc_dev.cuh"
 
+#include <cfloat>
 #include <cuda_fp16.h>
 
 namespace sv {
@@ -754,6 +755,15 @@ struct ShSoft {
     }
   }
 
+  // From a product to a score.  Not infinite, so that a product of zero is a score of
+  // zero; a NaN where the query row has one, or an infinity.
+  __device__ __forceinline__ float factor(float key) const {
+    if (C::kBf16) return fac;
+    float f;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(__fmul_rn(fac, key)), "f"(FLT_MAX));
+    return f;
+  }
+
   // A plain chunk: t' = s f + ev for all of it.  Weights 2^(t' - ref); the
   // denominator takes them times 2^-ev, or where values of the segment have
   // exponents so much larger that a weight may be below fp32's range although its
@@ -773,7 +783,7 @@ struct ShSoft {
 #pragma unroll
       for (int i = 0; i < 32; i += 2) m[i / 2 & 1] = max3(m[i / 2 & 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
     }
-    const float f = C::kBf16 ? fac : __fmul_rn(fac, sh_meta_key(meta)), ev = C::kBf16 ? 0.0f : sh_meta_value(meta);
+    const float f = factor(sh_meta_key(meta)), ev = C::kBf16 ? 0.0f : sh_meta_value(meta);
     if (!follow(__fmaf_rn(larger(fmaxf(m[0], m[1]), y), f, ev), j, y)) return false;
     bool far = false;
     if (!C::kBf16) {
@@ -822,7 +832,7 @@ struct ShSoft {
   __device__ __forceinline__ bool uneven(int j, int y, uint32_t meta, const float* sc) {
     const uint32_t place = scores_at(y);
     const bool even = C::kBf16 || meta & kShEven;
-    const float kf = C::kBf16 ? fac : __fmul_rn(fac, sh_meta_key(meta)), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
+    const float kf = factor(sh_meta_key(meta)), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
     const float iv = __uint_as_float((254u - (meta >> 24)) << 23);
     const uint32_t there = meta >> (h * (W / kPage));
     sc += h * W;
@@ -835,7 +845,7 @@ struct ShSoft {
         // (rounded once, as a plain chunk's)
         const float t = C::kBf16 ? __fmul_rn(__uint_as_float(w[i]), fac)
                         : even   ? __fmaf_rn(__uint_as_float(w[i]), kf, vs)
-                                 : __fmaf_rn(__uint_as_float(w[i]), __fmul_rn(fac, sc[c + i]), sc[CP + c + i]);
+                                 : __fmaf_rn(__uint_as_float(w[i]), factor(sc[c + i]), sc[CP + c + i]);
         w[i] = (there >> ((c + i) / kPage)) & 1u ? __float_as_uint(t) : 0xff800000u;
       }
     };

@@ -567,7 +567,8 @@ int sv_kv_copy(const sv_kv_pool* from, const sv_kv_pool* into, int n_pools, cons
  * -1e30 or the type's lowest value is a uniform distribution, and a log probability
  * or lse beyond fp32's range is the finite value nearest to it.  A token of -1
  * gives 0 (an unused place), any other outside 0 .. vocab - 1 a NaN and status bit 4.
- * Sums are fp32.  A row's results do not depend on the other rows' values. */
+ * Sums are fp32, in an order that depends on the call's sizes and a row's alignment
+ * alone: a row's results do not depend on the other rows' values. */
 #define SV_LOGITS_F32 0
 #define SV_LOGITS_BF16 1
 int sv_logprobs(const void* logits_dev, int dtype, int64_t stride, int n_rows, int vocab, float scale,

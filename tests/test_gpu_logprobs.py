@@ -262,3 +262,13 @@ def test_a_steps_logits():
     check(lg, tokens, top=10)
     _, _, _, _, ti, _ = run(lg, tokens, top=10)
     assert torch.equal(ti[:, 0].long(), lg.argmax(1)) and corr in ti[:, 0].tolist()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+def test_rows_beyond_2_to_31_elements(dtype):
+    vocab, stride = 5000, (1 << 30) + 5
+    flat = torch.empty(2 * stride + vocab, dtype=dtype, device="cuda")
+    x = torch.as_strided(flat, (3, vocab), (stride, 1))
+    x.copy_(logits(31, 3, vocab, dtype))
+    tokens = torch.tensor([[0, 4999], [17, -1], [4998, 2]], dtype=torch.int32, device="cuda")
+    check(x, tokens, top=5)

@@ -422,3 +422,64 @@ def test_groups_that_run_backwards_share_nothing():
     out, lse = c.call(q)
     assert c.status == 2
     near_attend(c, q, out, lse)
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+def test_pools_beyond_4_gigabytes(fmt, block):
+    """The same pages, of a small pool and at the end of a large one: the same bits; copied there by kv_copy."""
+    sv = _sv()
+    c = Case(25, 8, 8, 128, [(640, [(640 + 7 * s, 1 + s % 2) for s in range(5)])], fmt, block)
+    q = c.queries()
+    want = c.call(q)
+    n = c.cache.n_pages
+    many = (9 << 29) // (8 * PAGE * 128 * (2 if fmt == "bf16" else 1)) + n  # (4.5 GB of K)
+    large = sv.PagedKv.empty(many, 8, 128, fmt=fmt, scale_block=block)
+    moves = torch.stack([torch.arange(n), torch.arange(many - n, many)], 1).int().cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sv.kv_copy(c.cache, moves, into=large, status=st)
+    at = torch.where(c.table >= 0, c.table + (many - n), c.table)
+    c.table.copy_(at)
+    c.cache = large
+    got = c.call(q)
+    assert c.status == 0 and st.item() == 0
+    k = c.start[-1]
+    assert torch.equal(got[0][:k], want[0][:k]) and torch.equal(got[1][:k], want[1][:k])
+    back = sv.PagedKv.empty(n, 8, 128, fmt=fmt, scale_block=block)
+    sv.kv_copy(large, moves.flip(1).contiguous(), into=back)
+    again = torch.full_like(back.k, 1)
+    again.copy_(large.k[many - n:])
+    assert torch.equal(back.k.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("uneven", [False, True])
+def test_huge_keys_across_huge_queries(fmt, block, d, uneven):
+    """Products that are zero while the scales' product is beyond fp32: scores of zero, not NaN."""
+    c = Case(26, 4, 1, d, [(320, [(330, 1), (321, 2)])], fmt, block, spread=0.0)
+    c.cache.k[..., : d // 2] = 0
+    if fmt == "bf16":
+        c.cache.k.mul_(2.0 ** 80)
+    else:
+        c.cache.k_exp[:], c.cache.v_exp[:] = 127 + 74, 120
+        if uneven:
+            c.cache.k_exp[::3], c.cache.v_exp[::5] = 127 + 50, 140
+            c.cache.v[::5] = 0
+    q = c.queries(0.0) * 2.0 ** 80
+    q[..., d // 2:] = 0
+    c.check(q=q, scale=0.125)
+
+
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_an_infinite_query_across_negative_keys(block, d):
+    """Scores of -infinity alone, from a query that is not finite: NaN, as attend has it (an 8-bit cache)."""
+    c = Case(27, 4, 2, d, [(320, [(330, 1), (321, 2)])], "e4m3", block)
+    q = c.queries()
+    c.cache.k[..., 5] = 0x80 | 0x38
+    q[1, 2, 5] = float("inf")
+    for _ in range(2):
+        out, lse = c.call(q)
+        o, l = c.plain(q)
+        assert torch.isnan(out[1, 2]).all() and torch.equal(torch.isnan(out), torch.isnan(o)) and torch.equal(torch.isnan(lse), torch.isnan(l))
+        c.cache.v_exp[::7] = 90  # (exponents far apart)
