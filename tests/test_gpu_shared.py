@@ -483,3 +483,134 @@ def test_an_infinite_query_across_negative_keys(block, d):
         o, l = c.plain(q)
         assert torch.isnan(out[1, 2]).all() and torch.equal(torch.isnan(out), torch.isnan(o)) and torch.equal(torch.isnan(lse), torch.isnan(l))
         c.cache.v_exp[::7] = 90  # (exponents far apart)
+
+
+def test_calls_of_many_rows_are_taken_in_blocks():
+    """A table for 65536 positions: 300 rows of 32 heads are taken in blocks of rows whose
+    borders fall inside groups; nothing behind the workspace is written; in a graph,
+    and in the place of the queries, the same."""
+    sv = _sv()
+    groups = [(208, [(208, 90), (300, 1), (230, 100)]), (32, [(40, 3), (-20, 22), (33, 84)])]
+    c = Case(28, 32, 2, 128, groups, "e4m3", 1, back=2, wide=False)
+    table = torch.full((6, 4096), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    c.table, c.table_h = table, table.cpu()
+    c.rows = sv.RowBatch(table, c.first, c.n_rows, row_start=torch.tensor(c.start, dtype=torch.int32).cuda(), max_rows=100)
+    q, out, lse = c.check()
+    need = sv.attend_shared_workspace(c.cache, c.rows, c.prefix, 32)
+    ws = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    again, again_l = c.call(q, workspace=ws[:need])
+    n = c.start[-1]
+    assert (ws[need:] == 0x5a).all() and torch.equal(again[:n], out[:n]) and torch.equal(again_l[:n], lse[:n])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.attend_shared(c.cache, c.rows, c.prefix, q, again)
+    again.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again[:n], out[:n])
+    sv.attend_shared(c.cache, c.rows, c.prefix, q, q)
+    assert torch.equal(q[:n], out[:n])
+
+
+def test_graphs_streams_and_threads_at_once():
+    import threading
+    sv = _sv()
+    c = Case(29, 32, 8, 128, [(2000, [(2000 + 9 * s, 2) for s in range(8)])])
+    qs = [c.queries() for _ in range(2)]
+    want = [c.call(q)[0] for q in qs]
+    streams, outs, graphs = [torch.cuda.Stream() for _ in qs], [torch.empty_like(q) for q in qs], []
+    for q, o, s in zip(qs, outs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(5):
+                sv.attend_shared(c.cache, c.rows, c.prefix, q, o)
+        graphs.append(g)
+    for i in range(8):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for q, o, s, g in zip(qs, outs, streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay() if i % 2 else sv.attend_shared(c.cache, c.rows, c.prefix, q, o)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    many = [[torch.empty_like(q) for _ in range(100)] for q in qs]
+    meet = threading.Barrier(2)
+
+    def work(q, o):
+        meet.wait()
+        for x in o:
+            sv.attend_shared(c.cache, c.rows, c.prefix, q, x)
+            sv.attend(c.cache, c.rows, q, x) if x is o[50] else None
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(qs, many)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for o, w in zip(many, want) for k, x in enumerate(o) if k != 50)
+
+
+@pytest.mark.parametrize("starts", [[-4, 2, 3, 4000], [0, 5, 2, 5], [3, 0, 5, 5], [5, 4, 3, 0], [0, 2, 1, 5]])
+@pytest.mark.parametrize("fmt,block", FORMS)
+def test_row_starts_outside_touch_nothing_outside(fmt, block, starts):
+    sv = _sv()
+    c = Case(30, 4, 2, 64, [(64, [(64, 2), (70, 2), (90, 1)])], fmt, block)
+    out = torch.full((9, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((9, 4), 5.0, device="cuda")
+    rows = sv.RowBatch(c.table, c.first, 5, row_start=torch.tensor(starts, dtype=torch.int32, device="cuda"), max_rows=5)
+    sv.attend_shared(c.cache, rows, c.prefix, c.queries(), out[2:7], lse=lse[2:7])
+    torch.cuda.synchronize()
+    assert all((t[:2] == 5).all() and (t[7:] == 5).all() for t in (out, lse))
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_keys_that_are_not_finite(fmt, block, d):
+    """A NaN among a head's keys is in the row's sum; the other heads' rows stay as they were."""
+    c = Case(31, 4, 2, d, [(272, [(280, 1), (272, 2)])], fmt, block)
+    q = c.queries()
+    out0, lse0 = c.call(q)
+    page = int(c.table_h[0, 9])
+    if fmt == "bf16":
+        c.cache.k[page, 1, 5, 7] = float("nan")
+    else:
+        c.cache.k_exp[page, 1, 0] = 255
+    out, lse = c.call(q)
+    n = c.start[-1]
+    assert torch.isnan(out[:n, 2:]).all() and torch.isnan(lse[:n, 2:]).all()
+    assert torch.equal(out[:n, :2], out0[:n, :2]) and torch.equal(lse[:n, :2], lse0[:n, :2])
+    if fmt == "bf16":  # an infinite score is all of the softmax's weight: no finite result
+        c.cache.k[page, 1, 5, 7] = float("inf")
+        out, lse = c.call(q)
+        o, l = c.plain(q)
+        assert torch.equal(torch.isnan(out[:n]), torch.isnan(o[:n])) and torch.equal(torch.isnan(lse[:n]), torch.isnan(l[:n]))
+        assert torch.equal(out[:n, :2], out0[:n, :2])
+
+
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_zeroed_cache(block, d):
+    """Keys and values of zero, exponent byte 0, some or all: of score 0 and weight 1."""
+    c = Case(32, 4, 2, d, [(400, [(410, 1), (400, 2)])], "e4m3", block)
+    pages = c.table_h[0, 12:20].long().cuda()
+    for t in c.cache.tensors:
+        t[pages] = 0
+    c.check()
+    for t in c.cache.tensors:
+        t.zero_()
+    out, lse = c.call(c.queries())
+    n = c.start[-1]
+    seen = torch.tensor([411.0, 401.0, 402.0], device="cuda")
+    assert (out[:n] == 0).all() and ((lse[:n] - seen.log()[:, None]).abs() <= 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 60])
+def test_queries_and_values_of_extreme_size(block, size):
+    """Scores of ordinary size from tiny queries and huge keys, and values far from one."""
+    c = Case(33, 4, 2, 128, [(320, [(330, 1), (321, 2)])], "e4m3", block)
+    e = int(np.log2(size))
+    c.cache.k_exp += e
+    c.cache.v_exp -= e
+    c.check(q=c.queries() * (0.5 / size))
