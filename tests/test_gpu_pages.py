@@ -276,3 +276,36 @@ def test_captured_on_a_stream_and_replayed():
         got = state(pages)
         assert np.array_equal(got[0], c[0]) and np.array_equal(got[3], c[1]) and np.array_equal(got[2], f[2])
         pages.length.copy_(dev(ln))
+
+
+@pytest.mark.parametrize("n_seq,sources", [(1024, 32), (1024, 1), (500, 125)])
+def test_many_rows_of_one_unfinished_page_each_time_alike(n_seq, sources):
+    """All but one row of each source's copies its last page: counts that CTAs read while
+    they are to be lowered."""
+    sv = _sv()
+    pages, out = (sv.KvPages.empty(n_seq, 6, 9000) for _ in range(2))
+    moves = torch.empty((n_seq, 2), dtype=torch.int32, device="cuda")
+    sv.kv_fork(pages, moves, room=dev([70 if s < sources else 0 for s in range(n_seq)]))
+    pages.length.copy_(dev([70 if s < sources else 0 for s in range(n_seq)]))
+    pages.held.copy_(dev([5 if s < sources else 0 for s in range(n_seq)]))
+    source, keep = [s % sources for s in range(n_seq)], [65 + s // sources % 5 for s in range(n_seq)]
+    want = step(pages, out=out, source=source, keep=keep)
+    first = [t.clone() for t in (out.block_table, out.length, out.held, out.refs)]
+    source, keep = dev(source), dev(keep)
+    for _ in range(100):
+        for t in (out.block_table, out.length, out.held, out.refs):
+            t.fill_(-7)
+        sv.kv_fork(pages, moves, source=source, keep=keep, out=out)
+        assert np.array_equal(moves.cpu().numpy(), want)
+        assert all(torch.equal(a, b) for a, b in zip(first, (out.block_table, out.length, out.held, out.refs)))
+
+
+def test_the_widest_table_and_a_large_pool():
+    sv = _sv()
+    pages = sv.KvPages.empty(40, 4096, 400000)
+    rng = random.Random(8)
+    step(pages, source=[-1] * 40)
+    load(pages, ref.fork(*state(pages), None, None, [rng.randrange(1, 60000) for _ in range(40)])[:4])
+    pages.length.copy_(dev([min(int(h) * 16, rng.randrange(1, 60000)) for h in pages.held.tolist()]))
+    step(pages, source=[rng.randrange(-1, 40) for _ in range(40)], keep=[rng.randrange(0, 65000) for _ in range(40)],
+         room=[rng.randrange(0, 65536) for _ in range(40)])
