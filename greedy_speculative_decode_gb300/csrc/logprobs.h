@@ -17,6 +17,7 @@ struct LogprobsParams {
   int* status;
 };
 
+cudaError_t prepare_logprobs();
 cudaError_t launch_logprobs(const LogprobsParams& p, int n_rows, bool is_bf16, int num_sms, cudaStream_t s);
 
 }  // namespace sv

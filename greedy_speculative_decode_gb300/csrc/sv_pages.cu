@@ -20,7 +20,7 @@ int device_setup(int* num_sms) {
   if (g_sms[dev] == 0) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return SV_E_CUDA;
-    if (prepare_pages() != cudaSuccess) return SV_E_CUDA;
+    if (prepare_pages() != cudaSuccess || prepare_logprobs() != cudaSuccess) return SV_E_CUDA;
     g_sms[dev] = n;
   }
   *num_sms = g_sms[dev];
