@@ -16,17 +16,14 @@
 // of those equal to it, the first: k tokens of theirs are at least as probable
 // as any of a later one, with lower ids.
 //
-// What bounds it: for many rows instructions, then memory (some 12 an element of
-// bf16: widen, maximum, scale, subtract, exponential, two sums; 2048 x 151936, 622
-// MB, in 122 us, 0.75 of the copy rate at 0.77 instructions a cycle and scheduler);
+// What bounds it: for many rows instructions, then memory (of bf16: widen, maximum, scale, subtract, exponential, two sums; 2048 x 151936, 622
+// MB, in 109 us, 0.84 of the copy rate);
 // for a few the chain of load, meeting and second look (1 x 151936 fp32 with 20
-// alternatives 10.8 us in a graph, 6.0 without any; 24 x 262144 bf16 with 5 15).  A
+// alternatives 10.8 us in a graph, 6.0 without any; 24 x 262144 bf16 with 5 12.9).  A
 // row is a cluster of 1 to 8 CTAs, so that few rows fill the device too; they meet
 // over distributed shared memory.  (Up to 16 CTAs a row: 13.0 us for the first,
 // 17.9 for the last.  Sums of pairs in one instruction, fma.f32x2: 148 us for 2048
-// x 151936; the packing costs more than it saves.  Two blocks at a time: 117 to 125,
-// by what the compiler makes of it, and 100 instead of 75 for 500 x 151936 fp32 with
-// 20 alternatives, whose CTAs then take the registers of a third of an SM.)
+// x 151936 where the form without took 122; the packing costs more than it saves.)
 #include "sv_internal.h"
 #include "sv_ptx.cuh"
 
@@ -84,6 +81,7 @@ struct LpVec<float> {
     x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return __ldcg(p); }
+  static __device__ __forceinline__ uint4 finite(const uint4& w) { return w; }
   static __device__ __forceinline__ float largest(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
   }
@@ -104,6 +102,15 @@ struct LpVec<bf16> {
     }
   }
   static __device__ __forceinline__ float one(const bf16* p) { return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p)) << 16); }
+  // The same with finite values for infinities (an impossible token's 0 * inf is zero then); a NaN stays one.
+  static __device__ __forceinline__ uint4 finite(const uint4& w) {
+    uint4 r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(w.x), "r"(0xf14af14au));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(w.y), "r"(0xf14af14au));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.z) : "r"(w.z), "r"(0xf14af14au));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.w) : "r"(w.w), "r"(0xf14af14au));
+    return r;
+  }
   static __device__ __forceinline__ float largest(const uint4& w) {
     uint32_t a, b;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
@@ -252,7 +259,8 @@ __device__ __noinline__ void lp_far_row(LpShared<TH>& s, const T* logits, int vo
 template <class T, int TH, bool kTop, bool kEntropy>
 __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   using V = LpVec<T>;
-  constexpr int N = V::N, kAhead = 4;
+  // (two blocks at once: a check of the reference for both; 2048 x 151936 bf16 109 us, one by one 127)
+  constexpr int N = V::N, kAhead = 4, kAtOnce = N == 8 && !kTop ? 2 : 1;
   constexpr int kLpThreads = TH, kLpWarps = TH / 32;
   using Row = LpRow<T, TH>;
   __shared__ LpShared<TH> s;
@@ -272,10 +280,16 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
     __syncthreads();
   }
   float m = kLpNone, l = 0.0f, t = 0.0f;
-  auto add = [&](const uint4& w, int b) {
-    float x[N];
-    V::open(w, x);
+  // A lane's 16 bytes of block b, and of another one (of rows without alternatives).
+  auto add = [&](const uint4& w, int b, const auto&... other) {
+    constexpr int NV = 1 + sizeof...(other);
+    float x[NV][N];
+    V::open(kEntropy ? V::finite(w) : w, x[0]);  // (of bf16 values all finite, four instructions for eight)
     float top = V::largest(w);
+    if constexpr (NV == 2) {
+      V::open(kEntropy ? V::finite(other...) : (other, ...), x[1]);
+      top = fmaxf(top, V::largest(other...));
+    }
     // (the reference follows when it falls behind by 2^4)
     const bool far = __fmaf_rn(top, c, -m) > kLpSlack;
     if (kTop || __any_sync(0xffffffffu, far)) {
@@ -291,19 +305,23 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
     }
     const float before = t;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float z = __fmaf_rn(x[e], c, -m), q = lp_ex2(z);
-      l = __fadd_rn(l, q);
-      if (kEntropy) t = __fmaf_rn(q, z, t);
-      x[e] = z;
-    }
-    if (kEntropy && t != t) {  // an impossible token's 0 * inf is zero (a NaN among the logits has made l one)
-      t = before;
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float z = fmaxf(x[e], -1000.0f);
-        t = __fmaf_rn(lp_ex2(z), z, t);
+        const float z = __fmaf_rn(x[v][e], c, -m), q = lp_ex2(z);
+        l = __fadd_rn(l, q);
+        if (kEntropy) t = __fmaf_rn(q, z, t);
+        x[v][e] = z;
       }
+    if (kEntropy && N == 4 && t != t) {  // an impossible token's 0 * inf is zero (a NaN among the logits has made l one)
+      t = before;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float z = fmaxf(x[v][e], -1000.0f);
+          t = __fmaf_rn(lp_ex2(z), z, t);
+        }
     }
   };
   // Blocks that lie within the row, each warp's next three on their way while one is
@@ -323,12 +341,23 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
 #pragma unroll 1
   for (int b = whole0 + warp; b < whole1; b += kAhead * kLpWarps) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kAhead; i += kAtOnce) {
       const int bi = b + i * kLpWarps;
       if (bi >= whole1) break;
       const uint4 now = w[i];
-      if (bi + kAhead * kLpWarps < whole1) w[i] = row.load(bi + kAhead * kLpWarps, lane);
-      add(now, bi);
+      if constexpr (kAtOnce == 2) {
+        const uint4 then = w[i + 1];
+        if (bi + kLpWarps >= whole1) {  // a last one alone
+          add(now, bi);
+          break;
+        }
+        if (bi + kAhead * kLpWarps < whole1) w[i] = row.load(bi + kAhead * kLpWarps, lane);
+        if (bi + (kAhead + 1) * kLpWarps < whole1) w[i + 1] = row.load(bi + (kAhead + 1) * kLpWarps, lane);
+        add(now, bi, then);
+      } else {
+        if (bi + kAhead * kLpWarps < whole1) w[i] = row.load(bi + kAhead * kLpWarps, lane);
+        add(now, bi);
+      }
     }
   }
 #pragma unroll
