@@ -292,10 +292,10 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
     }
     // (the reference follows when it falls behind by 2^4)
     const bool far = __fmaf_rn(top, c, -m) > kLpSlack;
-    if (kTop || __any_sync(0xffffffffu, far)) {
-      top = warp_max(top);
-      if (kTop && lane == 0) atomicMax(&s.chunk[b >> row.shift], order_of(top));
-      const float y = __fmul_rn(top, c);
+    float chunk = 0.0f;
+    if (kTop) chunk = warp_max(top);  // (used at the end: nothing here waits for it)
+    if (__any_sync(0xffffffffu, far)) {
+      const float y = __fmul_rn(kTop ? chunk : warp_max(top), c);
       if (__fsub_rn(y, m) > kLpSlack) {
         const float d = __fsub_rn(m, y), f = lp_ex2(d);
         t = f > 0.0f ? __fmul_rn(f, __fmaf_rn(d, l, t)) : 0.0f;
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
           t = __fmaf_rn(lp_ex2(z), z, t);
         }
     }
+    if (kTop && lane == 0) atomicMax(&s.chunk[b >> row.shift], order_of(chunk));
   };
   // Blocks that lie within the row, each warp's next three on their way while one is
   // worked on; the row's ends by themselves.
