@@ -260,7 +260,7 @@ template <class T, int TH, bool kTop, bool kEntropy>
 __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   using V = LpVec<T>;
   // (two blocks at once: a check of the reference for both; 2048 x 151936 bf16 109 us, one by one 127)
-  constexpr int N = V::N, kAhead = 4, kAtOnce = N == 8 && !kTop ? 2 : 1;
+  constexpr int N = V::N, kAhead = 4, kAtOnce = N == 8 ? 2 : 1;
   constexpr int kLpThreads = TH, kLpWarps = TH / 32;
   using Row = LpRow<T, TH>;
   __shared__ LpShared<TH> s;
@@ -285,17 +285,22 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
     constexpr int NV = 1 + sizeof...(other);
     float x[NV][N];
     V::open(kEntropy ? V::finite(w) : w, x[0]);  // (of bf16 values all finite, four instructions for eight)
-    float top = V::largest(w);
+    const float one = V::largest(w);
+    float top = one, next = 0.0f;
     if constexpr (NV == 2) {
       V::open(kEntropy ? V::finite(other...) : (other, ...), x[1]);
-      top = fmaxf(top, V::largest(other...));
+      next = V::largest(other...);
+      top = fmaxf(top, next);
     }
     // (the reference follows when it falls behind by 2^4)
     const bool far = __fmaf_rn(top, c, -m) > kLpSlack;
-    float chunk = 0.0f;
-    if (kTop) chunk = warp_max(top);  // (used at the end: nothing here waits for it)
+    float chunk = 0.0f;  // (used at the end: nothing here waits for it)
+    if (kTop) {
+      chunk = warp_max(one);
+      if (NV == 2) next = warp_max(next);
+    }
     if (__any_sync(0xffffffffu, far)) {
-      const float y = __fmul_rn(kTop ? chunk : warp_max(top), c);
+      const float y = __fmul_rn(kTop ? NV == 2 ? fmaxf(chunk, next) : chunk : warp_max(top), c);
       if (__fsub_rn(y, m) > kLpSlack) {
         const float d = __fsub_rn(m, y), f = lp_ex2(d);
         t = f > 0.0f ? __fmul_rn(f, __fmaf_rn(d, l, t)) : 0.0f;
@@ -323,7 +328,10 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
           t = __fmaf_rn(lp_ex2(z), z, t);
         }
     }
-    if (kTop && lane == 0) atomicMax(&s.chunk[b >> row.shift], order_of(chunk));
+    if (kTop && lane == 0) {
+      atomicMax(&s.chunk[b >> row.shift], order_of(chunk));
+      if (NV == 2) atomicMax(&s.chunk[(b + kLpWarps) >> row.shift], order_of(next));
+    }
   };
   // Blocks that lie within the row, each warp's next three on their way while one is
   // worked on; the row's ends by themselves.
