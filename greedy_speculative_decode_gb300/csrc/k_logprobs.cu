@@ -16,14 +16,17 @@
 // of those equal to it, the first: k tokens of theirs are at least as probable
 // as any of a later one, with lower ids.
 //
-// What bounds it: for many rows instructions, then memory (of bf16: widen, maximum, scale, subtract, exponential, two sums; 2048 x 151936, 622
-// MB, in 109 us, 0.84 of the copy rate);
-// for a few the chain of load, meeting and second look (1 x 151936 fp32 with 20
-// alternatives 10.8 us in a graph, 6.0 without any; 24 x 262144 bf16 with 5 12.9).  A
-// row is a cluster of 1 to 8 CTAs, so that few rows fill the device too; they meet
-// over distributed shared memory.  (Up to 16 CTAs a row: 13.0 us for the first,
-// 17.9 for the last.  Sums of pairs in one instruction, fma.f32x2: 148 us for 2048
-// x 151936 where the form without took 122; the packing costs more than it saves.)
+// What bounds it: for many rows memory, and instructions nearly as much (of bf16: widen,
+// maximum, scale and subtract, exponential, two sums; 2048 x 151936, 622 MB, in 109 us,
+// 0.84 of the copy rate; 1000 x 151936 with 5 alternatives, 304 MB, 79 us, of which a
+// third is the second look, when an SM has few loads on their way); for a few rows the
+// chain of load, meeting and second look (1 x 151936 fp32 with 20 alternatives 10.6 us in
+// a graph, 6.0 without any; 24 x 262144 bf16 with 5 12.4).  A row is a cluster of 1 to 8
+// CTAs, so that few rows fill the device too; they meet over distributed shared memory.
+// (Up to 16 CTAs a row: 13.0 and 17.9 us for these two, when 8 took 10.5 and 13.8.  Two CTAs
+// a row where there are rows for every SM: 500 x 151936 fp32 with 20 91 us, one 75.  Sums
+// of pairs in one instruction, fma.f32x2: 148 us for the first case, when the form
+// without took 129.)
 #include "sv_internal.h"
 #include "sv_ptx.cuh"
 
@@ -259,7 +262,8 @@ __device__ __noinline__ void lp_far_row(LpShared<TH>& s, const T* logits, int vo
 template <class T, int TH, bool kTop, bool kEntropy>
 __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   using V = LpVec<T>;
-  // (two blocks at once: a check of the reference for both; 2048 x 151936 bf16 109 us, one by one 127)
+  // (bf16 blocks by twos, with one check of the reference: 2048 x 151936 109 us, one by one
+  // 127; of fp32 500 x 151936 with 20 alternatives would take 80, one by one 73)
   constexpr int N = V::N, kAhead = 4, kAtOnce = N == 8 ? 2 : 1;
   constexpr int kLpThreads = TH, kLpWarps = TH / 32;
   using Row = LpRow<T, TH>;
