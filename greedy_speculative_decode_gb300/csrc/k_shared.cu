@@ -17,11 +17,12 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   const int tid = threadIdx.x, S = p.a.rows.n_seq, N = p.n_groups, G = p.a.n_q_heads / p.a.n_kv_heads;
   pdl_trigger();
   pdl_wait();
-  auto start_of = [&](int s) { return p.a.rows.row_start ? __ldcg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
-  auto clip = [&](int r) { return min(max(r, 0), p.a.rows.n_rows); };
+  auto given_start = [&](int s) { return p.a.rows.row_start ? __ldcg(p.a.rows.row_start + s) : s * p.a.rows.rows_each; };
+  auto start_of = [&](int s) { return min(max(given_start(s), 0), p.a.rows.n_rows); };  // (as k_attend reads them)
   int first = 0, n = 0;
   if (tid < S) {
-    first = first_of(p.a.rows, tid);
+    const int at = given_start(tid);
+    first = first_of(p.a.rows, tid) + (at < 0 ? (int)min(-(int64_t)at, (int64_t)1 << 28) : 0);
     n = start_of(tid + 1) - start_of(tid);
   }
   if (tid < 32) s_sum[tid] = s_sum2[tid] = 0;
@@ -33,7 +34,9 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
     s_lead[tid] = S;
   }
   __syncthreads();
-  const bool back = __syncthreads_or(tid < N && s_start[tid + 1] < s_start[tid]);
+  // Groups or rows that run backwards: nothing is shared.  (Of rows that do, the merge's
+  // search could find one below its group's first, whose partials are elsewhere.)
+  const bool back = __syncthreads_or((tid < N && s_start[tid + 1] < s_start[tid]) || n < 0);
   if (back && tid == 0 && p.a.status) atomicOr(p.a.status, ST_BAD_PAGE);
   int gi = -1;
   if (tid < S) {
@@ -57,8 +60,8 @@ __global__ void __launch_bounds__(1024) k_shared_plan(const __grid_constant__ Sh
   if (tid < N) {
     g.s0 = s_lead[tid];
     if (!back && g.s0 < S) {
-      g.row0 = clip(start_of(s_start[tid]));
-      const int rows = clip(start_of(s_start[tid + 1])) - g.row0;
+      g.row0 = start_of(s_start[tid]);
+      const int rows = start_of(s_start[tid + 1]) - g.row0;
       if (rows > 0) {
         g.eff = s_eff[tid] / kPage * kPage;
         g.R = rows * G;

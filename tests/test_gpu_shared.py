@@ -614,3 +614,27 @@ def test_queries_and_values_of_extreme_size(block, size):
     c.cache.k_exp += e
     c.cache.v_exp -= e
     c.check(q=c.queries() * (0.5 / size))
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("starts", [
+    [0, 30, 60, 20, 50, 80], [0, 60, 10, 70, 40, 80], [80, 60, 40, 20, 10, 0], [0, 80, 0, 80, 0, 80],
+    [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 50, 2 ** 31 - 1, 80], [0, 10, 20, 30, 79, 78]])
+def test_row_starts_that_run_backwards_share_nothing(fmt, block, starts):
+    """Several groups, whose rows then overlap: bit 2 is raised, nothing outside the call's
+    rows is written, nothing behind the workspace, and the next call is right."""
+    sv = _sv()
+    c = Case(34, 4, 2, 128, [(256, [(256, 16), (270, 16)]), (128, [(140, 16)]), (320, [(320, 16), (400, 16)])], fmt, block)
+    q, want, wl = c.check()
+    rows = sv.RowBatch(c.table, c.first, 80, row_start=torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    need = sv.attend_shared_workspace(c.cache, rows, c.prefix, 4)
+    ws = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.full((84, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((84, 4), 5.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sv.attend_shared(c.cache, rows, c.prefix, q, out[2:82], lse=lse[2:82], workspace=ws[:need], status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 2 and (ws[need:] == 0x5a).all()
+    assert all((t[:2] == 5).all() and (t[82:] == 5).all() for t in (out, lse))
+    got, gl = c.call(q)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
