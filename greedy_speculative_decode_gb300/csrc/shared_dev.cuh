@@ -548,7 +548,10 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
   tmem = sh_uniform(tmem);
   ShRun<C::NS> run(p, blockIdx.x);
   ShSegment s;
-  uint32_t seg = 0, steps = 0;  // parities: of the segment, of the two score places
+  // parities: of the streams' queries, of the two score places (a bit each).  A segment of a
+  // single step has none for the second stream, which does not arrive for it either: it
+  // may be several such segments ahead, or one behind.
+  uint32_t seg = 0, steps = 0;
   bool ok = true;
   ShPlace<C::kOps> k = {0, 0};
   const uint64_t q_desc = tc_sdesc(sh_uniform(smem_u32(sm.q(0))));
@@ -582,7 +585,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
         }
       }
       if (j + 2 < n) {
-        ok = (j + 2 >= C::NS || sh_wait(sm.q_full(stream), seg)) && sh_wait(sm.op_full(k.slot), k.phase);
+        ok = (j + 2 >= C::NS || sh_wait(sm.q_full(stream), seg >> stream & 1u)) && sh_wait(sm.op_full(k.slot), k.phase);
         if (!ok) break;
         tc_fence_after();
         const uint64_t a = q_desc + stream * (C::kQBytes >> 4), b = k_desc + k.slot * (C::kOpBytes >> 4);
@@ -600,7 +603,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
     // the next segment's first operand is behind the last of V: v went by two from there
     k.slot = v.slot == 0 ? C::kOps - 1 : v.slot - 1;
     k.phase = v.slot == 0 ? v.phase ^ 1u : v.phase;
-    seg ^= 1u;
+    seg ^= C::NS == 2 && n > 1 ? 3u : 1u;
   }
   // every multiply has completed before tensor memory is freed
   tc_commit_if(lead, sm.drain());
@@ -957,7 +960,7 @@ struct ShSoft {
       const ShOrder ord{s.i1 - s.i0, s.w == 2};
       const int n = ord.steps(), tile = s.pair * C::NS + (ord.both ? x : 0);
       if (x < n) queries(s, tile, G);
-      else { open(); mbar_arrive(sm.q_full(x)); }
+      else open();
       const bool idle = tile * kSharedTile + (r & 96) >= s.g.R;
       int mine = 0, y = C::NS == 2 ? x : 0;
       for (int j = C::NS == 2 ? x : 0; j < n; j += C::NS) {

@@ -638,3 +638,21 @@ def test_row_starts_that_run_backwards_share_nothing(fmt, block, starts):
     assert all((t[:2] == 5).all() and (t[82:] == 5).all() for t in (out, lse))
     got, gl = c.call(q)
     assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("fmt,block", FORMS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prefixes_of_a_chunk_before_longer_ones(fmt, block, d):
+    """More lists than CTAs: a CTA has segments of one step, of which its second stream has
+    no part, and then longer ones; the same bits every time."""
+    groups = []
+    for k in range(60):
+        groups += [(112, [(112 + k % 7, 1)]), (64, [(70, 2)]), (128, [(128, 1)]), (512, [(512 + k % 5, 1), (530, 2)])]
+    c = Case(35, 4, 1, d, groups, fmt, block, spread=0.5)
+    q = c.queries(0.5)
+    out, lse = c.call(q)
+    assert c.status == 0
+    near_attend(c, q, out, lse)
+    for _ in range(20):
+        again, gl = c.call(q)
+        assert torch.equal(again, out) and torch.equal(gl, lse)
