@@ -41,6 +41,7 @@ struct SharedParams {
   float* o;           // [streams][plane][head_dim]
   int64_t plane;      // rows of a stream's
   int grid;           // CTAs of the prefix kernel
+  uint32_t wait_ns;   // how long one of its waits may last
 };
 
 cudaError_t prepare_shared_kernels();

@@ -100,7 +100,9 @@ struct ShCfg {
   // step [places][128] token rows of the query rows (-1: none)
   static constexpr int kOffRow = kOffRawMeta + 32;
   static constexpr int kOffTmem = kOffRow + 4 * kSharedTile * 4;
-  static constexpr int kSmem = kOffTmem + 16;
+  static constexpr int kOffFailed = kOffTmem + 4;     // whether a wait of the CTA has given up
+  static constexpr int kOffLast = kOffTmem + 16;      // [8] the last copy into each place of the ring that is loaded, + 1
+  static constexpr int kSmem = kOffLast + 32;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -138,13 +140,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // is one): descriptors worked out from such values cost the multiplying warp a few
 // instructions, not a move for each operand of each multiply.
 __device__ __forceinline__ uint32_t sh_uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-
-// A whole warp's wait.  Its lanes go on together: one that fell behind, and that
-// nothing else waits for, could otherwise look for a phase when the next but one
-// has already come, which has the same parity.
-__device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
 
 __device__ __forceinline__ float sh_ex2(float x) {
   float r;
@@ -258,7 +253,8 @@ template <class C>
 struct ShSmem {
   uint8_t* base;
   uint64_t* bar;
-  __device__ __forceinline__ ShSmem(uint8_t* b) : base(b), bar(reinterpret_cast<uint64_t*>(b + C::kOffBar)) {}
+  uint32_t limit_ns;  // of a wait
+  __device__ __forceinline__ ShSmem(uint8_t* b, uint32_t ns) : base(b), bar(reinterpret_cast<uint64_t*>(b + C::kOffBar)), limit_ns(ns) {}
   __device__ __forceinline__ uint8_t* q(int x) const { return base + C::kOffQ + x * C::kQBytes; }
   __device__ __forceinline__ uint8_t* op(int s) const { return base + C::kOffOp + s * C::kOpBytes; }
   __device__ __forceinline__ uint8_t* raw(int s) const { return base + C::kOffRaw + s * C::kRawBytes; }
@@ -281,6 +277,32 @@ struct ShSmem {
   __device__ __forceinline__ uint64_t* pv_done(int x) const { return rest(4 + x); }  // its product P V is
   __device__ __forceinline__ uint64_t* q_full(int x) const { return rest(6 + x); }   // a stream's queries are
   __device__ __forceinline__ uint64_t* drain() const { return rest(8); }
+  __device__ __forceinline__ volatile uint32_t* failed() const { return reinterpret_cast<uint32_t*>(base + C::kOffFailed); }
+  __device__ __forceinline__ volatile uint32_t* last() const { return reinterpret_cast<uint32_t*>(base + C::kOffLast); }
+
+  // A whole warp's wait.  Its lanes go on together: one that fell behind, and that
+  // nothing else waits for, could otherwise look for a phase when the next but one
+  // has already come, which has the same parity.
+  //   False: it gave up, or another warp of the CTA has; from then on no wait of the CTA
+  // lasts.  Loads, widening and multiplies then end.  The softmax's warps go on, over
+  // scores that mean nothing, to the end of the run: they meet at named barriers,
+  // which have no limit, so one of them that left would hold up those that did not
+  // fail.  What they write lies in the CTA's own partials.
+  __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity) const {
+    bool ok = mbar_try_wait(b, parity);
+    if (!ok) {
+      const unsigned long long t0 = globaltimer_ns();
+      for (uint32_t i = 1;; ++i) {
+        ok = mbar_try_wait(b, parity);
+        if (ok || *failed()) break;
+        if (((i & 255u) == 0u || limit_ns < 1000000u) && globaltimer_ns() - t0 > limit_ns) {
+          *failed() = 1u;
+          break;
+        }
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  }
 };
 
 // What a chunk holds: the pages that are there (bits 0-7); whether it is even (bit
@@ -326,7 +348,7 @@ struct ShItems {
 // that is not there reads as zeros: a row beyond the tensor), or an 8-bit page's
 // codes.  Page numbers are looked up two operands ahead.
 template <class C, bool kValues>
-__device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShSmem<C>& sm, uint32_t& end) {
+__device__ void sh_load(const SharedParams& p, const CUtensorMap* map, const ShSmem<C>& sm) {
   const int lane = threadIdx.x & 31;
   const uint32_t lead = tc_elect();
   ShItems<C> it(p);
@@ -336,10 +358,8 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
     uint32_t at, chunk;
   };
   Item now = {-1, 0, false, false, 0, 0}, next = now;
-  bool ok = true;
   constexpr uint32_t kRing = C::kBf16 ? C::kOps : C::kRaws;
   const uint64_t pol = policy_evict_last();
-  end = 0;  // behind the last operand asked for
   for (int k = 0;; ++k) {
     // the operand two on: its page numbers
     Item far = {-1, 0, false, false, 0, 0};
@@ -363,9 +383,8 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
     }
     const uint32_t at = now.at;
     const int st = at % kRing;
-    ok = at < kRing || sh_wait(C::kBf16 ? sm.op_empty(st) : sm.raw_empty(st), ((at / kRing) & 1u) ^ 1u);
-    if (!ok) break;
-    end = at + 1;
+    if (at >= kRing && !sm.wait(C::kBf16 ? sm.op_empty(st) : sm.raw_empty(st), ((at / kRing) & 1u) ^ 1u)) return;
+    if (lead) sm.last()[st] = at + 1;
     const bool have = (uint32_t)now.page < (uint32_t)p.a.n_pages;
     uint4 ke = make_uint4(0u, 0u, 0u, 0u), ve = ke;
     if (!C::kBf16 && have) {
@@ -435,23 +454,23 @@ __device__ bool sh_load(const SharedParams& p, const CUtensorMap* map, const ShS
     now = next;
     next = far;
   }
-  return ok;
 }
 
-// After a failure: the last copies asked for have landed, or the waits for them run
-// out.  (A place that the other warp has used again since is waited for in vain.)
+// After a failure: the last copy into each place has landed, or the wait for it runs out.
 template <class C>
-__device__ void sh_load_drain(const ShSmem<C>& sm, uint32_t end) {
+__device__ void sh_load_drain(const ShSmem<C>& sm) {
   constexpr uint32_t kRing = C::kBf16 ? C::kOps : C::kRaws;
-  for (uint32_t k = end > kRing ? end - kRing : 0; k < end; ++k)
-    sh_wait(C::kBf16 ? sm.op_full(k % kRing) : sm.raw_full(k % kRing), (k / kRing) & 1u);
+  for (uint32_t st = 0; st < kRing; ++st) {
+    const uint32_t n = sm.last()[st];
+    if (n > 0) mbar_wait(C::kBf16 ? sm.op_full(st) : sm.raw_full(st), ((n - 1) / kRing) & 1u);
+  }
 }
 
 // ------------------------------------------------------------------ 8-bit codes to f16 operands
 // Four warps.  (Eight: 75 us for 128 x 1 behind 16384, with four 72.)  An even chunk's codes are scaled to its largest exponents; of
 // another the codes go as they are, and the scores take the exponents (sm.scale).
 template <class C>
-__device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
+__device__ void sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
   constexpr int kWidth = 128;
   const int tid = threadIdx.x - C::kWidenWarp * 32;
   ShItems<C> it(p);
@@ -460,15 +479,15 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
     if (!it.more) break;
     const uint32_t c = it.chunk0, at = it.at;
     const int st = at % C::kRaws, os = at % C::kOps;
-    if (!sh_wait(sm.raw_full(st), (at / C::kRaws) & 1u)) return false;
-    if (at >= C::kOps && !sh_wait(sm.op_empty(os), ((at / C::kOps) & 1u) ^ 1u)) return false;
+    if (!sm.wait(sm.raw_full(st), (at / C::kRaws) & 1u)) return;
+    if (at >= C::kOps && !sm.wait(sm.op_empty(os), ((at / C::kOps) & 1u) ^ 1u)) return;
     const uint32_t meta = sm.raw_meta()[st];
     const bool even = meta & kShEven;
     const uint8_t* exps = sm.exps(st) + (it.is_v ? C::CP : 0);
     const int most = it.is_v ? meta >> 24 : (meta >> 16) & 255;
     if (!it.is_v) {
       const int ring = c % C::kRings;
-      if (c >= C::kRings && !sh_wait(sm.sc_empty(ring), ((c / C::kRings) & 1u) ^ 1u)) return false;
+      if (c >= C::kRings && !sm.wait(sm.sc_empty(ring), ((c / C::kRings) & 1u) ^ 1u)) return;
       if (!even && tid < C::CP) {
         const uint32_t bk = sm.exps(st)[tid], bv = sm.exps(st)[C::CP + tid];
         float* f = sm.scale(ring);
@@ -520,7 +539,6 @@ __device__ bool sh_widen(const SharedParams& p, const ShSmem<C>& sm) {
     mbar_arrive(sm.op_full(os));
     mbar_arrive(sm.raw_empty(st));
   }
-  return true;
 }
 
 // ------------------------------------------------------------------ multiplies
@@ -541,7 +559,7 @@ struct ShPlace {
 // 16 every 64 cycles and hold some eight of them ahead: what the warp does between two
 // batches is kept to a few instructions.
 template <class C>
-__device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t tmem) {
+__device__ void sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t tmem) {
   constexpr int CP = C::CP, D = C::D;
   constexpr uint32_t kScores = sh_idesc<C>(CP, false), kValues = sh_idesc<C>(D, true);
   const uint32_t lead = tc_elect();
@@ -567,7 +585,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
       const uint32_t x = j & 1, stream = C::NS == 2 ? x : 0;
       const bool last = !both || x;  // of the steps with these operands
       if (j >= 0) {
-        ok = sh_wait(sm.p_full(x), steps >> x & 1u) && sh_wait(sm.op_full(v.slot), v.phase);
+        ok = sm.wait(sm.p_full(x), steps >> x & 1u) && sm.wait(sm.op_full(v.slot), v.phase);
         if (!ok) break;
         steps ^= 1u << x;
         tc_fence_after();
@@ -585,7 +603,7 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
         }
       }
       if (j + 2 < n) {
-        ok = (j + 2 >= C::NS || sh_wait(sm.q_full(stream), seg >> stream & 1u)) && sh_wait(sm.op_full(k.slot), k.phase);
+        ok = (j + 2 >= C::NS || sm.wait(sm.q_full(stream), seg >> stream & 1u)) && sm.wait(sm.op_full(k.slot), k.phase);
         if (!ok) break;
         tc_fence_after();
         const uint64_t a = q_desc + stream * (C::kQBytes >> 4), b = k_desc + k.slot * (C::kOpBytes >> 4);
@@ -607,8 +625,8 @@ __device__ bool sh_multiply(const SharedParams& p, const ShSmem<C>& sm, uint32_t
   }
   // every multiply has completed before tensor memory is freed
   tc_commit_if(lead, sm.drain());
-  if (!sh_wait(sm.drain(), 0)) ok = false;
-  return ok;
+  if (!mbar_wait(sm.drain(), 0)) *sm.failed() = 1u;
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax
@@ -711,18 +729,18 @@ struct ShSoft {
   }
 
   // The reference follows a row's largest score `top` of step j where it has risen by more than the slack.
-  __device__ __forceinline__ bool follow(float top, int j, int y) {
+  __device__ __forceinline__ void follow(float top, int j, int y) {
     constexpr float kBias = sh_bias(C::kBf16);
     const bool up = __fsub_rn(top, ref) > kShSlack + kBias;  // (the difference is exact, a sum need not be)
-    if (!__any_sync(0xffffffffu, up)) return true;
+    if (!__any_sync(0xffffffffu, up)) return;
     top = __fsub_rn(top, kBias);
     const float d = up ? __fsub_rn(ref, top) : 0.0f, a = sh_ex2(d);
     const bool scaled = up && ref != kShNone;
     l = sh_times_ex2(l, d);
     ref = up ? top : ref;
-    if (!__any_sync(0xffffffffu, scaled)) return true;  // (behind a row's first chunk there is nothing to scale)
+    if (!__any_sync(0xffffffffu, scaled)) return;  // (behind a row's first chunk there is nothing to scale)
     // the product before this step (with two streams it ran before these scores did)
-    if (C::NS == 1 && j > 0 && !sh_wait(sm.pv_done(y ^ 1), (steps(y ^ 1) - 1u) & 1u)) return false;
+    if (C::NS == 1 && j > 0) sm.wait(sm.pv_done(y ^ 1), (steps(y ^ 1) - 1u) & 1u);
     tc_fence_after();
     const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
 #pragma unroll 1
@@ -735,7 +753,6 @@ struct ShSoft {
       tc_st32(o + c, v);
     }
     tc_wait_st();
-    return true;
   }
 
   // 32 columns' weights over their scores, where the product reads them: two 16-bit
@@ -775,7 +792,7 @@ struct ShSoft {
   // further: the warps' code then fits the instruction caches and their registers the
   // file.  (Nearly all of an SM's L1 is shared memory here: what a register spills
   // comes back from L2.)
-  __device__ __forceinline__ bool plain(int j, int y, uint32_t meta) {
+  __device__ __forceinline__ void plain(int j, int y, uint32_t meta) {
     const uint32_t place = scores_at(y);
     uint32_t v[32];
     float m[2] = {-INFINITY, -INFINITY};
@@ -787,7 +804,7 @@ struct ShSoft {
       for (int i = 0; i < 32; i += 2) m[i / 2 & 1] = max3(m[i / 2 & 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
     }
     const float f = factor(sh_meta_key(meta)), ev = C::kBf16 ? 0.0f : sh_meta_value(meta);
-    if (!follow(__fmaf_rn(larger(fmaxf(m[0], m[1]), y), f, ev), j, y)) return false;
+    follow(__fmaf_rn(larger(fmaxf(m[0], m[1]), y), f, ev), j, y);
     bool far = false;
     if (!C::kBf16) {
       const uint32_t e = meta >> 24;
@@ -828,11 +845,10 @@ struct ShSoft {
     const float all = __fadd_rn(__uint_as_float(even_sum), __uint_as_float(odd_sum));
     if (C::kBf16) l = __fadd_rn(l, all);
     else l = far ? __fadd_rn(l, direct) : __fmaf_rn(all, __uint_as_float((254u - (meta >> 24)) << 23), l);
-    return true;
   }
 
   // Any chunk: pages may be missing, exponents differ by position (sc: 2^ek, ev, 2^-ev of each).
-  __device__ __forceinline__ bool uneven(int j, int y, uint32_t meta, const float* sc) {
+  __device__ __forceinline__ void uneven(int j, int y, uint32_t meta, const float* sc) {
     const uint32_t place = scores_at(y);
     const bool even = C::kBf16 || meta & kShEven;
     const float kf = factor(sh_meta_key(meta)), vs = C::kBf16 ? 0.0f : sh_meta_value(meta);
@@ -859,7 +875,7 @@ struct ShSoft {
 #pragma unroll
       for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
     }
-    if (!follow(larger(top, y), j, y)) return false;
+    follow(larger(top, y), j, y);
     if (!C::kBf16) most = max(most, meta >> 24);
     float sum = 0.0f;
 #pragma unroll 1
@@ -879,17 +895,17 @@ struct ShSoft {
       put(place + c, w);
     }
     l = __fadd_rn(l, sum);
-    return true;
   }
 
   // Step j of the segment, on score place y: scores to weights.  no: the chunk's number in the call.
   // idle: the warp's rows are behind the tile's last.
-  __device__ __forceinline__ bool step(int j, int y, uint32_t no, bool both, bool idle) {
-    if (!sh_wait(sm.s_full(y), steps(y) & 1u)) return false;
+  __device__ __forceinline__ void step(int j, int y, uint32_t no, bool both, bool idle) {
+    sm.wait(sm.s_full(y), steps(y) & 1u);
     tc_fence_after();
     const uint32_t meta = sm.meta()[no & 7];
     if (idle) meet();  // (the weights of its rows may be anything: no product of another row's meets them)
-    else if (!(meta & kShPlain ? plain(j, y, meta) : uneven(j, y, meta, sm.scale(no % C::kRings)))) return false;
+    else if (meta & kShPlain) plain(j, y, meta);
+    else uneven(j, y, meta, sm.scale(no % C::kRings));
     tc_wait_st();
     tc_fence_before();
     mbar_arrive(sm.p_full(y));
@@ -900,15 +916,14 @@ struct ShSoft {
     }
     steps0 += y ^ 1;
     steps1 += y;
-    return true;
   }
 
   // The segment's partial.  n: steps of this stream; y: the last one's score place.
-  __device__ __forceinline__ bool partial(const ShSegment& s, int tile, int n, int y, int cta) {
+  __device__ __forceinline__ void partial(const ShSegment& s, int tile, int n, int y, int cta) {
     const int f = tile * kSharedTile + r;
     const long long at = (long long)x * p.plane + sh_slot(p, s.g, s.kvh, s.pair, C::NS, cta) + r;
     if (n > 0) {
-      if (!sh_wait(sm.pv_done(y), (steps(y) - 1u) & 1u)) return false;
+      sm.wait(sm.pv_done(y), (steps(y) - 1u) & 1u);
       tc_fence_after();
       const uint32_t o = tmem + lane_off + C::kOutCol + (C::NS == 2 ? x : 0) * D;
       // through the warp's part of the stream's queries, which have done their work: 16
@@ -948,10 +963,9 @@ struct ShSoft {
     meet();
     if (h == 0 && f < s.g.R) p.ml[at] = make_float2(ref, __fadd_rn(l, sum[r]));
     meet();  // (the place is free again)
-    return true;
   }
 
-  __device__ bool run() {
+  __device__ void run() {
     const int G = p.a.n_q_heads / p.a.n_kv_heads;
     ShRun<C::NS> run(p, blockIdx.x);
     ShSegment s;
@@ -965,13 +979,12 @@ struct ShSoft {
       int mine = 0, y = C::NS == 2 ? x : 0;
       for (int j = C::NS == 2 ? x : 0; j < n; j += C::NS) {
         y = j & 1;
-        if (!step(j, y, chunk_no + ord.chunk(j), ord.both, idle)) return false;
+        step(j, y, chunk_no + ord.chunk(j), ord.both, idle);
         ++mine;
       }
-      if (!partial(s, tile, mine, y, blockIdx.x)) return false;
+      partial(s, tile, mine, y, blockIdx.x);
       chunk_no += ord.n;
     }
-    return true;
   }
 };
 
@@ -981,7 +994,7 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
                     const __grid_constant__ CUtensorMap vmap) {
   using C = ShCfg<D, FMT>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const ShSmem<C> sm(smem);
+  const ShSmem<C> sm(smem, p.wait_ns);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   if (C::kBf16 && threadIdx.x == C::kLoadWarp * 32) {
     prefetch_tensormap(&kmap);
@@ -1005,6 +1018,8 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
     }
     mbar_init(sm.drain(), 1);
     fence_barrier_init();
+    *sm.failed() = 0u;
+    for (int i = 0; i < 8; ++i) sm.last()[i] = 0u;
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(sm.tmem())) : "memory");
@@ -1016,23 +1031,22 @@ __global__ void __launch_bounds__(ShCfg<D, FMT>::kThreads, 1)
   const uint32_t tmem = *sm.tmem();
   pdl_wait();  // the plan
   pdl_trigger();
-  bool ok = true;
-  uint32_t end = 0;  // of a loading warp's operands
   if (warp < C::kSoftWarps) {
-    ok = ShSoft<C>(p, sm, tmem).run();
+    ShSoft<C>(p, sm, tmem).run();
   } else if (warp == C::kMmaWarp) {
-    ok = sh_multiply<C>(p, sm, tmem);
+    sh_multiply<C>(p, sm, tmem);
   } else if (warp == C::kLoadWarp) {
-    ok = sh_load<C, false>(p, &kmap, sm, end);
+    sh_load<C, false>(p, &kmap, sm);
   } else if (warp == C::kLoadWarp + 1) {
-    ok = sh_load<C, true>(p, &vmap, sm, end);
+    sh_load<C, true>(p, &vmap, sm);
   } else if (warp >= C::kWidenWarp) {
-    if constexpr (!C::kBf16) ok = sh_widen<C>(p, sm);
+    if constexpr (!C::kBf16) sh_widen<C>(p, sm);
   }
-  if (!ok && p.a.status) atomicOr(p.a.status, ST_TIMEOUT);
   tc_fence_before();
-  if (__syncthreads_or(!ok)) {  // (without a failure every copy has been waited for by what reads it)
-    sh_load_drain<C>(sm, end);
+  __syncthreads();
+  if (*sm.failed()) {  // (without a failure every copy has been waited for by what reads it)
+    if (threadIdx.x == 0 && p.a.status) atomicOr(p.a.status, ST_TIMEOUT);
+    if (warp == C::kLoadWarp) sh_load_drain<C>(sm);
     __syncthreads();
   }
   if (warp == 0) {

@@ -1,11 +1,14 @@
 // sv_paged.cu -- C entry points of the paged-cache operators: argument
 // checks and the launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 
 #include "paged.h"
 #include "shared.h"
+#include "sv_ptx.cuh"
 
 namespace sv {
 
@@ -39,6 +42,8 @@ struct DeviceSetup {
 };
 std::mutex g_mu;
 DeviceSetup g_dev[kMaxDevices];
+// How long a wait of the prefix kernel may last (SV_TEST_SHARED_WAIT_NS: less, for a test of its failure).
+std::atomic<uint32_t> g_wait_ns{(uint32_t)kWaitLimitNs};
 
 int device_setup(int* num_sms) {
   int dev = 0;
@@ -48,6 +53,7 @@ int device_setup(int* num_sms) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return SV_E_CUDA;
     if (prepare_attend_kernels() != cudaSuccess || prepare_shared_kernels() != cudaSuccess) return SV_E_CUDA;
+    if (const char* ns = getenv("SV_TEST_SHARED_WAIT_NS")) g_wait_ns = (uint32_t)std::min<unsigned long>(strtoul(ns, nullptr, 10), kWaitLimitNs);
     g_dev[dev].num_sms = n;
   }
   *num_sms = g_dev[dev].num_sms;
@@ -320,6 +326,7 @@ int sv_attend_shared(const sv_kv_pool* pool, const sv_row_batch* rows, const sv_
   sp.ml = reinterpret_cast<float2*>(take(sp.plane * shared_streams(c.head_dim) * (int64_t)sizeof(float2)));
   sp.o = reinterpret_cast<float*>(at);
   sp.grid = std::min(num_sms, kSharedMostCtas);
+  sp.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   const bool share = !attend_alone(p.rows, c, n_q_heads / c.n_kv_heads) &&
                      shared_units_fit(p.rows, sp.n_groups, n_q_heads, c.n_kv_heads, c.head_dim);
   if (share) p.from = sp.from;

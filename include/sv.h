@@ -475,6 +475,9 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
  * number of rows and groups of the call and their lengths, since the prefix is cut
  * between CTAs by the call's whole work.  The same call gives the same bits.
  * Over a bf16 cache values beyond 2^96 may come out as infinities.
+ *   SV_TEST_SHARED_WAIT_NS=n (environment, read by the first call on a device):
+ * failure-detection test only.  A wait inside the kernel of the shared positions gives
+ * up after n ns instead of 2 s; status bit 1 is raised, and that call's results are wrong.
  *   workspace_dev: sv_attend_shared_workspace bytes, as for sv_attend: that call's,
  * and n_q_heads * (8 head_dim + 16) bytes a row. */
 typedef struct {

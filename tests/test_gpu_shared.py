@@ -656,3 +656,47 @@ def test_prefixes_of_a_chunk_before_longer_ones(fmt, block, d):
     for _ in range(20):
         again, gl = c.call(q)
         assert torch.equal(again, out) and torch.equal(gl, lse)
+
+
+_SHORT_WAITS = """
+import time, torch
+import greedy_speculative_decode_gb300 as sv
+from tests.test_gpu_shared import BATCHES, Case, near_attend
+raised = 0
+for fmt, block in (("bf16", 1), ("e4m3", 1), ("e4m3", 16)):
+    for n_q, n_kv, d in ((8, 2, 64), (32, 8, 128), (8, 1, 256)):
+        for groups in (BATCHES["long"], BATCHES["wide"], BATCHES["groups"],
+                       [(128, [(128 + k, 1)]) for k in range(30)] + [(500, [(500 + k, 2) for k in range(20)])]):
+            c = Case(36, n_q, n_kv, d, groups, fmt, block, back=2, spread=0.5)
+            q = c.queries(0.5)
+            want, wl = c.plain(q)
+            ws = torch.full((sv.attend_shared_workspace(c.cache, c.rows, c.prefix, n_q) + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+            for _ in range(5):
+                t = time.monotonic()
+                out, lse = c.call(q, workspace=ws[:-4096])
+                assert time.monotonic() - t < 5 and c.status in (0, 1), c.status
+                raised += c.status
+                assert (ws[-4096:] == 0x5a).all() and torch.isnan(out[c.start[-1]:]).all()
+                if not c.status:
+                    near_attend(c, q, out, lse)
+            again, gl = c.plain(q)
+            n = c.start[-1]
+            assert torch.equal(again[:n], want[:n]) and torch.equal(gl[:n], wl[:n])
+print("raised", raised)
+"""
+
+
+@pytest.mark.parametrize("ns", [0, 3000])
+def test_a_wait_that_gives_up_ends_the_call(ns):
+    """Failure detection without a fault: with waits of next to no time some of a CTA's warps
+    give up while others of the same stream do not.  Every call ends, raises bit 1 where a
+    wait gave up, writes nothing outside, and leaves the device as it was."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _SHORT_WAITS], cwd=root, env=dict(os.environ, SV_TEST_SHARED_WAIT_NS=str(ns)),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    raised = int(r.stdout.split("raised")[1])
+    assert raised > 0 if ns == 0 else raised >= 0
