@@ -219,6 +219,15 @@ __device__ __forceinline__ void lp_rank(LpShared<TH>& s, bool have, uint32_t key
   __syncthreads();
 }
 
+// (x - X) c, where x - X may be beyond fp32's range though the product is not (x of 3e38
+// and -3e38 with c = 1/4).
+__device__ __forceinline__ float lp_below(float x, float X, float c) {
+  const float d = __fsub_rn(x, X);
+  if (d > -INFINITY) return __fmul_rn(d, c);
+  const float h = __fmul_rn(__fsub_rn(__fmul_rn(0.5f, x), __fmul_rn(0.5f, X)), c);
+  return __fadd_rn(h, h);
+}
+
 // A row whose largest y = x c is beyond kLpFar: a reference rounded to fp32 would lie too
 // far from it for 2^(y - m), and c x may be beyond fp32's range (rows masked with -1e30 or
 // the type's lowest value throughout).  Its largest logit X (-infinity: none is
@@ -238,7 +247,7 @@ __device__ __noinline__ void lp_far_row(LpShared<TH>& s, const T* logits, int vo
   L = E = 0.0f;
 #pragma unroll 1
   for (int i = tid; X > -INFINITY && i < vocab; i += TH) {
-    const float z = __fmul_rn(__fsub_rn(LpVec<T>::one(logits + i), X), c), q = lp_ex2(z);
+    const float z = lp_below(LpVec<T>::one(logits + i), X, c), q = lp_ex2(z);
     L = __fadd_rn(L, q);
     E = __fmaf_rn(q, fmaxf(z, -1000.0f), E);  // (an impossible token's 0 * inf is zero)
   }
@@ -423,9 +432,10 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   const bool good = L > 0.0f && L < INFINITY && fabsf(M) < INFINITY;
   const float l2 = good ? log2f(L) : NaN;
   auto log_prob = [&](float x) {
-    const float z = is_far ? __fmul_rn(__fsub_rn(x, X), c) : __fmaf_rn(x, c, -M), v = __fmul_rn(__fsub_rn(z, l2), ln2);
-    // (a finite logit's is finite: beyond fp32's range the rest of z is nothing beside x c)
-    return v == -INFINITY && x > -INFINITY ? fmaxf(__fmul_rn(x, __fmul_rn(c, ln2)), -FLT_MAX) : v;
+    const float z = is_far ? lp_below(x, X, c) : __fmaf_rn(x, c, -M), v = __fmul_rn(__fsub_rn(z, l2), ln2);
+    // (a finite logit's is finite: where z is beyond fp32's range l2 is nothing beside it, nor is a
+    // row's M that is not far)
+    return v == -INFINITY && x > -INFINITY ? fmaxf(lp_below(x, is_far ? X : 0.0f, __fmul_rn(c, ln2)), -FLT_MAX) : v;
   };
   if (rank == 0) {
     for (int i = tid; i < p.n_tokens; i += kLpThreads) {

@@ -272,3 +272,34 @@ def test_rows_beyond_2_to_31_elements(dtype):
     x.copy_(logits(31, 3, vocab, dtype))
     tokens = torch.tensor([[0, 4999], [17, -1], [4998, 2]], dtype=torch.int32, device="cuda")
     check(x, tokens, top=5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [700, 151936])
+@pytest.mark.parametrize("scale", [3.0, 1.0, 0.5, 0.25, 1.0e-3, 1.0e-20, 3.0e-29, 1.0e-30])
+def test_logits_further_apart_than_fp32_reaches(dtype, vocab, scale):
+    """3e38 and -3e38 in one row: a log probability is -scale 6e38, or the nearest finite value.
+
+    The product with the scale's constant, rounded twice, and a difference, a product and a
+    sum of the result's: at most five half steps, 5 * 2^-24 of the value; an ordinary log
+    probability here is at most 1e2, off by less than 1e-4 (2048 steps of its size)."""
+    x = torch.zeros((3, vocab), device="cuda")
+    x[0, 5], x[0, 7], x[0, 9] = 3.0e38, -3.0e38, -float("inf")
+    x[1, 5], x[1, 7], x[1, 9] = 3.0e38, -3.0e38, 3.0e38
+    x[2], x[2, 7] = 3.0e38, -3.0e38
+    x = x.to(dtype)
+    tokens = torch.tensor([[5, 7, 8, 9]] * 3, dtype=torch.int32, device="cuda")
+    sv = _sv()
+    out, lse = torch.empty((3, 4), device="cuda"), torch.empty(3, device="cuda")
+    tv, ti = torch.empty((3, 32), device="cuda"), torch.empty((3, 32), dtype=torch.int32, device="cuda")
+    sv.logprobs(x, tokens, out, scale=scale, lse=lse, top_values=tv, top_ids=ti)
+    torch.cuda.synchronize()
+    most = np.float64(np.finfo(np.float32).max)
+    o, l, _, v, i = ref.logprobs(x.double().cpu().numpy(), tokens.cpu().numpy(), scale, 32)
+    for got, want in ((out, o), (lse, l), (tv, v)):
+        got = got.double().cpu().numpy()
+        want = np.where(np.isinf(want), want, np.clip(want, -most, most))
+        assert np.array_equal(np.isinf(got), np.isinf(want))
+        fine = np.isfinite(want)
+        assert (np.abs(got[fine] - want[fine]) <= 5 * 2.0 ** -24 * np.abs(want[fine]) + 1e-4).all(), (got, want)
+    assert np.array_equal(ti.cpu().numpy(), i)
