@@ -303,3 +303,52 @@ def test_logits_further_apart_than_fp32_reaches(dtype, vocab, scale):
         fine = np.isfinite(want)
         assert (np.abs(got[fine] - want[fine]) <= 5 * 2.0 ** -24 * np.abs(want[fine]) + 1e-4).all(), (got, want)
     assert np.array_equal(ti.cpu().numpy(), i)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [700, 40001])
+@pytest.mark.parametrize("scale", [1.0e-37, 1.0e-30, 2.0e-29, 5.0e-29, 1.0e-20, 1.0e-8, 3.0e8, 1.0e9, 1.0e12, 1.0e20, 1.0e30])
+def test_scales_of_any_size(dtype, vocab, scale):
+    """Impossible tokens, and masks, beside logits that the scale brings near one another or far
+    apart; the same with an entropy asked for and without."""
+    x = torch.full((6, vocab), -float("inf"), device="cuda")
+    size = min(1.0 / scale, 1.0e38)
+    row = logits(40, 1, vocab, torch.float32, spread=1.0)[0]
+    x[0, ::2] = row[::2] * size
+    x[1, ::3], x[1, 9] = -0.125, 0.0
+    x[2, 5:40], x[2, 6] = -0.125, 20.0
+    x[3] = torch.finfo(dtype).min
+    x[3, 50:90], x[3, ::7] = -0.125 * size, -float("inf")
+    x[4, 3], x[4, 4], x[4, 5] = -2.0e30, -1.0e30, -1.5e30
+    x[5] = -1.0e30
+    x[5, ::2] = -float("inf")
+    x = x.to(dtype)
+    tokens = torch.tensor([[0, 1, 6, 7]] * 6, dtype=torch.int32, device="cuda")
+    # (a log probability and the lse may be beyond fp32's range: the nearest finite value)
+    most = np.float64(np.finfo(np.float32).max)
+    xn, tn = x.double().cpu().numpy(), tokens.cpu().numpy()
+    o, l, e, v, i = ref.logprobs(xn, tn, scale, 8)
+    tt, tl, te, zs = tolerances(xn, scale, tn)
+    err = np.array([z[0] for z in zs])[:, None]
+    tv_tol = err + 2.0 ** -21 * (np.abs(np.where(np.isfinite(v), v, 0)) * 1.45 + 1)
+
+    def near(got, want, tol):
+        got, want = got.double().cpu().numpy(), np.where(np.isinf(want), want, np.clip(want, -most, most))
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isinf(got), np.isinf(want)), (got, want)
+        fine = np.isfinite(want)
+        tol = np.minimum(tol[fine], most) + 2.0 ** -22 * np.abs(want[fine])
+        assert (np.abs(got[fine] - want[fine]) <= tol).all(), (got, want)
+
+    for top in (0, 8):
+        out, lse, ent, tv, ti, st = run(x, tokens, scale, top)
+        assert st == 0
+        near(out, o, tt)
+        near(lse, l, tl)
+        near(ent, e, te)
+        if top:
+            assert np.array_equal(ti.cpu().numpy(), i)
+            near(tv, v, tv_tol)
+    _sv().logprobs(x, tokens, out, scale=scale, lse=lse)
+    torch.cuda.synchronize()
+    near(out, o, tt)
+    near(lse, l, tl)
