@@ -150,3 +150,76 @@ def test_beams(fmt, block, n_q, n_kv, d, prompt, wide):
     held_equals(alive)
     sv.kv_fork(pages, torch.empty((S, 2), dtype=torch.int32, device="cuda"), source=dev([-1] * S))
     assert int(pages.refs.abs().sum()) == 0 and int(pages.block_table.max()) == -1
+
+
+@pytest.mark.parametrize("fmt,block", [("bf16", 1), ("e4m3", 1), ("e4m3", 16)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_forks_copies_and_attention_with_no_kernel_between(fmt, block, d):
+    """Each of these kernels may start before the one ahead of it has ended.  Tables, pages and
+    exponents that the call before last has read change in between: the same bits as with
+    the device waited for after every call."""
+    import greedy_speculative_decode_gb300 as sv
+    g = torch.Generator().manual_seed(3)
+    S, n_q, n_kv, prefix, steps = 16, 32, 8, 256, 14
+    width, n_pages = (56 << 20) // (S * n_kv * d * (2 if fmt == "bf16" else 1)) // PAGE + 1, 256
+    shape = (n_pages, n_kv, PAGE, d)
+    if fmt == "bf16":
+        pool = [torch.randn(shape, generator=g).bfloat16() for _ in range(2)]
+    else:
+        codes = [torch.randint(0, 126, shape, generator=g) + 128 * torch.randint(0, 2, shape, generator=g) for _ in range(2)]
+        exps = [torch.randint(112, 122, (n_pages, n_kv, PAGE // block), generator=g) for _ in range(2)]
+        pool = [t.to(torch.uint8) for t in codes + exps]
+    begin = [t.cuda() for t in pool]
+    cache = sv.PagedKv(*[t.clone() for t in begin])
+    pages = sv.KvPages.empty(S, width, n_pages)
+    moves, status = torch.empty((S, 2), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    # rows of one prompt, of uneven lengths, whose last pages are partly filled
+    lengths = [prefix + 5 + 7 * s for s in range(S)]
+    room = dev([lengths[-1] + 9] * S)
+    sv.kv_fork(pages, moves, source=dev([0] + [-1] * (S - 1)), room=room, status=status)
+    pages.length[0] = prefix
+    sv.kv_fork(pages, moves, source=dev([0] * S), room=room, status=status)
+    pages.length.copy_(dev(lengths))
+    tables = [t.clone() for t in (pages.block_table, pages.length, pages.held, pages.refs)]
+    sources = [dev([int(x) for x in torch.randint(0, S, (S,), generator=g)]) for _ in range(steps)]
+    batch, share = sv.RowBatch(pages.block_table, pages.length, S), sv.SharedPrefix(dev([prefix]))
+    q = [torch.randn((S, n_q, d), generator=g).bfloat16().cuda() for _ in range(steps)]
+    outs = [torch.empty_like(x) for x in q]
+
+    def restore():
+        for t, b in zip(cache.tensors, begin):
+            t.copy_(b)
+        for t, b in zip((pages.block_table, pages.length, pages.held, pages.refs), tables):
+            t.copy_(b)
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+
+    def run(wait):
+        for k in range(steps):
+            sv.kv_fork(pages, moves, source=sources[k], room=room, status=status)
+            wait()
+            sv.kv_copy(cache, moves, status=status)
+            wait()
+            sv.attend_shared(cache, batch, share, q[k], outs[k], status=status)
+            wait()
+
+    restore()
+    run(torch.cuda.synchronize)
+    want = [o.clone() for o in outs]
+    assert int(status.item()) == 0 and all(torch.isfinite(w).all() for w in want)
+    # not all alike: the rows do change
+    assert not torch.equal(pages.length, tables[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(lambda: None)
+    for _ in range(5):
+        restore()
+        run(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        restore()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert int(status.item()) == 0
