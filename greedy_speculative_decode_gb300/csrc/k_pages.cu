@@ -35,7 +35,7 @@ constexpr int kPgThreads = 1024, kPgWarps = 32;
 constexpr int kPgWide = 8;
 static_assert(kPagesMaxSeq == kPgThreads, "a thread a row");
 
-// Exclusive sums over the block's threads; total in `sum`.  (s: 33 words; two barriers.)
+// Exclusive sums over the block's threads; total in `sum`.  (s: a word a warp; two barriers.)
 __device__ __forceinline__ int block_scan(int v, int* s, int& sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;

@@ -479,7 +479,9 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
  * failure-detection test only.  A wait inside the kernel of the shared positions gives
  * up after n ns instead of 2 s; status bit 1 is raised, and that call's results are wrong.
  *   workspace_dev: sv_attend_shared_workspace bytes, as for sv_attend: that call's,
- * and n_q_heads * (8 head_dim + 16) bytes a row. */
+ * n_q_heads * (8 head_dim + 16) bytes a row (with head_dim 256 half as many), as many
+ * as for another 24576 / n_q_heads rows whatever the batch (26 MB; with head_dim 64
+ * 13), and some 50 KB of plan. */
 typedef struct {
   int32_t n_groups;
   const int32_t *length, *group_start;

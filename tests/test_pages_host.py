@@ -186,3 +186,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         sv.logprobs(torch.zeros((2, 5)), torch.zeros(2, dtype=torch.int32), torch.zeros(2))
     with pytest.raises(ValueError, match="no caches"):
         sv.KvLayers([])
+
+
+# ------------------------------------------------------------------ what the header says of sizes and addresses
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads,n_seq,each", [(4, 4, 2), (32, 64, 1), (16, 1000, 7)])
+def test_attend_shared_workspace_is_as_documented(d, heads, n_seq, each):
+    r = rows(n_seq=n_seq, n_rows=n_seq * each)
+    own, n = ctypes.c_int64(), ctypes.c_int64()
+    assert L.sv_attend_workspace(ref(pool(head_dim=d)), ref(r), heads, ref(own)) == 0
+    assert L.sv_attend_shared_workspace(ref(pool(head_dim=d)), ref(r), ref(prefix(n_groups=1)), heads, ref(n)) == 0
+    row = heads * (8 * d + 16) // (2 if d == 256 else 1)
+    more = n.value - own.value - row * (n_seq * each) - row * 24576 // heads
+    assert 0 <= more <= 52000
