@@ -61,6 +61,7 @@ int device_setup(int* num_sms) {
 }
 
 bool bad16(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool odd4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }  // (null is fine)
 
 // The pool and the rows as the kernels take them; false: not valid.
 bool read_pool(const sv_kv_pool* a, KvPool& c) {
@@ -89,6 +90,7 @@ bool read_pool(const sv_kv_pool* a, KvPool& c) {
 
 bool read_rows(const sv_row_batch* a, RowBatch& b) {
   if (!a || a->n_seq < 1 || a->n_rows < 1 || a->table_stride < 1 || !a->block_table || !a->first) return false;
+  if (odd4(a->block_table) || odd4(a->first) || odd4(a->row_start)) return false;
   // positions stay below 2^23 (the attention's merge keeps a word for each
   // split) and rows below 2^28: their sums fit 32 bits
   if (a->table_stride > (1 << 23) / kPage || a->n_rows > (1 << 28)) return false;
@@ -151,7 +153,7 @@ int read_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads,
   if (b.n_seq > kAttendMaxSeq) return SV_E_INVAL;
   const int width = n_q_heads * c.head_dim;
   if (bad16(q_dev) || bad16(out_dev) || bad_stride(q_stride, width) || bad_stride(out_stride, width)) return SV_E_INVAL;
-  if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev) return SV_E_INVAL;
+  if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) || !workspace_dev || odd4(lse_dev) || odd4(status_dev)) return SV_E_INVAL;
   if (workspace_bytes < need) return SV_E_NOMEM;
   // 32-bit counts on the device, of a block of rows: chunks of 16 positions for
   // every kv head and tile of at least 8 query rows
@@ -212,7 +214,7 @@ bool attend_alone(const RowBatch& b, const KvPool& c, int group) {
 
 // Groups of sequences: as many as there are sequences at most.
 bool read_prefix(const sv_shared_prefix* a, const RowBatch& b) {
-  if (!a || a->n_groups < 1 || a->n_groups > b.n_seq || !a->length) return false;
+  if (!a || a->n_groups < 1 || a->n_groups > b.n_seq || !a->length || odd4(a->length) || odd4(a->group_start)) return false;
   return a->group_start != nullptr || b.n_seq % a->n_groups == 0;
 }
 
@@ -232,7 +234,7 @@ int sv_kv_write(const sv_kv_pool* pool, const sv_row_batch* rows, const void* k_
   const int width = c.n_kv_heads * c.head_dim;
   if (bad16(k_dev) || bad16(v_dev) || bad_stride(k_stride, width) || bad_stride(v_stride, width)) return SV_E_INVAL;
   if ((int64_t)b.n_rows * width / 8 > UINT32_MAX) return SV_E_INVAL;
-  if (c.n_kv_heads > 65535) return SV_E_INVAL;
+  if (c.n_kv_heads > 65535 || odd4(status_dev)) return SV_E_INVAL;
   KvSource src = {static_cast<const bf16*>(k_dev), static_cast<const bf16*>(v_dev), k_stride, v_stride, 0};
   return launch_kv_write(c, b, src, status_dev, static_cast<cudaStream_t>(cuda_stream), false) == cudaSuccess
              ? SV_OK
@@ -246,7 +248,7 @@ int sv_kv_fetch(const sv_kv_pool* pool, const sv_row_batch* rows, void* k_dev, i
   if (!read_pool(pool, c) || !read_rows(rows, b)) return SV_E_INVAL;
   const int width = c.n_kv_heads * c.head_dim;
   if (bad16(k_dev) || bad16(v_dev) || bad_stride(k_stride, width) || bad_stride(v_stride, width)) return SV_E_INVAL;
-  if ((int64_t)b.n_rows * width / 8 > UINT32_MAX) return SV_E_INVAL;
+  if ((int64_t)b.n_rows * width / 8 > UINT32_MAX || odd4(status_dev)) return SV_E_INVAL;
   return launch_kv_fetch(c, b, static_cast<bf16*>(k_dev), k_stride, static_cast<bf16*>(v_dev), v_stride, status_dev,
                          static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? SV_OK

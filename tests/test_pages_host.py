@@ -199,3 +199,16 @@ def test_attend_shared_workspace_is_as_documented(d, heads, n_seq, each):
     row = heads * (8 * d + 16) // (2 if d == 256 else 1)
     more = n.value - own.value - row * (n_seq * each) - row * 24576 // heads
     assert 0 <= more <= 52000
+
+
+@pytest.mark.parametrize("at", range(7))
+def test_addresses_that_no_int32_or_float_has_are_refused(at):
+    odd = [A + 2 if k == at else A for k in range(7)]
+    r = rows(block_table=odd[0], first=odd[1], row_start=odd[2])
+    x = prefix(length=odd[3], group_start=odd[4])
+    assert L.sv_attend_shared(ref(pool()), ref(r), ref(x), 4, A, 512, A, 512, odd[5], 1.0, A, 1 << 40, odd[6], None) == INVAL
+    if at not in (3, 4):
+        assert L.sv_attend(ref(pool()), ref(r), 4, A, 512, A, 512, odd[5], 0, 0, 1.0, A, 1 << 40, odd[6], None) == INVAL
+    if at in (0, 1, 2, 6):
+        for call in (L.sv_kv_write, L.sv_kv_fetch):
+            assert call(ref(pool()), ref(r), A, 512, A, 512, odd[6], None) == INVAL
