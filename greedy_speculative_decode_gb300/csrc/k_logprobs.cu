@@ -32,7 +32,6 @@
 
 #include <algorithm>
 #include <cfloat>
-#include <cmath>
 #include <cooperative_groups.h>
 
 #include "logprobs.h"
@@ -85,7 +84,7 @@ struct LpVec<float> {
     x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return __ldcg(p); }
-  static __device__ __forceinline__ uint4 finite(const uint4& w, uint32_t) { return w; }
+  static __device__ __forceinline__ uint4 finite(const uint4& w) { return w; }
   static __device__ __forceinline__ float largest(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
   }
@@ -106,14 +105,14 @@ struct LpVec<bf16> {
     }
   }
   static __device__ __forceinline__ float one(const bf16* p) { return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p)) << 16); }
-  // The same with finite values for infinities (an impossible token's 0 * inf is zero then); a
-  // NaN stays one.  lowest: see lp_lowest.
-  static __device__ __forceinline__ uint4 finite(const uint4& w, uint32_t lowest) {
+  // The same with finite values, of -1e30, for infinities (an impossible token's 0 * inf is zero
+  // then); a NaN stays one.
+  static __device__ __forceinline__ uint4 finite(const uint4& w) {
     uint4 r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(w.x), "r"(lowest));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(w.y), "r"(lowest));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.z) : "r"(w.z), "r"(lowest));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.w) : "r"(w.w), "r"(lowest));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(w.x), "r"(0xf14af14au));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(w.y), "r"(0xf14af14au));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.z) : "r"(w.z), "r"(0xf14af14au));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.w) : "r"(w.w), "r"(0xf14af14au));
     return r;
   }
   static __device__ __forceinline__ float largest(const uint4& w) {
@@ -232,9 +231,9 @@ __device__ __forceinline__ float lp_below(float x, float X, float c) {
 
 // A row whose largest y = x c is beyond kLpFar: a reference rounded to fp32 would lie too
 // far from it for 2^(y - m), and c x may be beyond fp32's range (rows masked with -1e30 or
-// the type's lowest value throughout).  Its largest logit X (-infinity: none is
-// finite) and the sums of z = (x - X) c.  Each CTA reads the whole row, plainly: such rows
-// are rare.
+// the type's lowest value throughout); or a row of a call that sums plainly (lp_plain).
+// Its largest logit X (-infinity: none is finite) and the sums of z = (x - X) c.  Each CTA
+// reads the whole row, plainly: such rows are rare.
 template <class T, int TH>
 __device__ __noinline__ void lp_far_row(LpShared<TH>& s, const T* logits, int vocab, float c, float& X, float& L, float& E) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -299,11 +298,11 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
   auto add = [&](const uint4& w, int b, const auto&... other) {
     constexpr int NV = 1 + sizeof...(other);
     float x[NV][N];
-    V::open(kEntropy ? V::finite(w, p.lowest) : w, x[0]);  // (of bf16 values all finite, four instructions for eight)
+    V::open(kEntropy ? V::finite(w) : w, x[0]);  // (of bf16 values all finite, four instructions for eight)
     const float one = V::largest(w);
     float top = one, next = 0.0f;
     if constexpr (NV == 2) {
-      V::open(kEntropy ? V::finite((other, ...), p.lowest) : (other, ...), x[1]);
+      V::open(kEntropy ? V::finite(other...) : (other, ...), x[1]);
       next = V::largest(other...);
       top = fmaxf(top, next);
     }
@@ -424,9 +423,7 @@ __global__ void __launch_bounds__(TH) k_logprobs(const LogprobsParams p) {
     meet(CS, [&](int i, int k) { return __shfl_sync(0xffffffffu, all[k], i); }, M, L, E);
   }
   float X = 0.0f;
-  // (the same for all CTAs of the row; an entropy that impossible tokens have made a NaN, see
-  // lp_lowest, is summed again too)
-  const bool is_far = !(fabsf(M) < kLpFar) || (kEntropy && E != E && L == L);
+  const bool is_far = !(fabsf(M) < (N == 8 ? p.far : kLpFar));  // (the same for all CTAs of the row)
   if (is_far) {
     lp_far_row<T, TH>(s, logits, p.vocab, c, X, L, E);
     M = X;
@@ -609,18 +606,14 @@ cudaError_t prepare_logprobs() {
   return prepare_e<bf16, kLpNarrow>();
 }
 
-// Two bf16 values below which y = x c is less than -2^32, so that a weight is zero beside
-// any reference, and at which it is finite, more than -2^33.  Scales below 2^-95 leave no
-// such value: -infinity, and impossible tokens then make the sum for the entropy a NaN.
-static uint32_t lp_lowest(float c) {
-  const int e = std::ilogb(c);  // (2^e <= c < 2^(e + 1); c is above zero and finite)
-  const uint32_t one = e >= -95 ? 0x8000u | ((uint32_t)(127 + 32 - e) << 7) : 0xff80u;
-  return one | (one << 16);
-}
+// Whether rows of bf16 logits are summed plainly for their entropy: where -1e30 times the scale
+// is beyond fp32's range, or not so far down that a weight of it is zero beside any
+// reference (below -2^32).
+static bool lp_plain(float c) { return c > 0x1p28f || c < 0x1p-67f; }
 
 cudaError_t launch_logprobs(const LogprobsParams& params, int n_rows, bool is_bf16, int num_sms, cudaStream_t s) {
   LogprobsParams p = params;
-  p.lowest = lp_lowest(p.scale_log2);
+  p.far = is_bf16 && p.entropy && lp_plain(p.scale_log2) ? 0.0f : kLpFar;
   return is_bf16 ? launch_d<bf16>(p, n_rows, num_sms, s) : launch_d<float>(p, n_rows, num_sms, s);
 }
 

@@ -15,7 +15,7 @@ struct LogprobsParams {
   float *out, *lse, *entropy, *top_values;  // out [n_rows, n_tokens]; the others [n_rows] and [n_rows, top], or null
   int* top_ids;
   int* status;
-  uint32_t lowest;  // of bf16 logits, two: smaller ones count as it (launch_logprobs works it out)
+  float far;  // bf16 rows whose largest scale_log2 x is as far from zero are summed plainly (launch_logprobs sets it)
 };
 
 cudaError_t prepare_logprobs();
