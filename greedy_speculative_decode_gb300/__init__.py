@@ -494,7 +494,9 @@ def attend_shared(cache: PagedKv, rows: RowBatch, prefix: SharedPrefix, q, out, 
     sequences of a group share once for all of the group's rows. The tables of
     a group's sequences must agree on the pages of its first prefix.length
     positions (as kv_fork leaves them). Arguments as attend's; workspace:
-    attend_shared_workspace bytes. Asynchronous."""
+    attend_shared_workspace bytes. Whether a call is small enough to be attend's
+    goes by its rows and the width of its tables (lengths are on the device):
+    cut them for the longest sequence. Asynchronous."""
     if getattr(q, "dim", lambda: 0)() != 3:
         raise ValueError("q: must be a 3-D tensor [n_rows, n_q_heads, head_dim]")
     heads = q.shape[1]

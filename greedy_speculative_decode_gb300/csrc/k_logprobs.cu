@@ -18,15 +18,16 @@
 //
 // What bounds it: for many rows memory, and instructions nearly as much (of bf16: widen,
 // maximum, scale and subtract, exponential, two sums; 2048 x 151936, 622 MB, in 109 us,
-// 0.84 of the copy rate; 1000 x 151936 with 5 alternatives, 304 MB, 79 us, of which a
+// 0.84 of the copy rate; 1000 x 151936 with 5 alternatives, 304 MB, 78 us, of which a
 // third is the second look, when an SM has few loads on their way); for a few rows the
-// chain of load, meeting and second look (1 x 151936 fp32 with 20 alternatives 10.6 us in
-// a graph, 6.0 without any; 24 x 262144 bf16 with 5 12.4).  A row is a cluster of 1 to 8
-// CTAs, so that few rows fill the device too; they meet over distributed shared memory.
-// (Up to 16 CTAs a row: 13.0 and 17.9 us for these two, when 8 took 10.5 and 13.8.  Two CTAs
-// a row where there are rows for every SM: 500 x 151936 fp32 with 20 91 us, one 75.  Sums
-// of pairs in one instruction, fma.f32x2: 148 us for the first case, when the form
-// without took 129.)
+// chain of load, meeting and second look (1 x 151936 fp32 with 20 alternatives 10.3 us in
+// a graph, 5.8 without any; 24 x 262144 bf16 with 5 12.0).  A row of fewer chunks than
+// alternatives has all its logits put in order, one by one: 2000 x 1024 bf16 9.8 us with
+// one alternative, 78 with 5.  A row is a cluster of 1 to 8 CTAs, so that few rows fill
+// the device too; they meet over distributed shared memory.
+// (Two CTAs a row where there are rows for every SM: 500 x 151936 fp32 with 20 91 us, when
+// one took 75.  Sums of pairs in one instruction, fma.f32x2: 148 us for the first case,
+// when the form without took 129.)
 #include "sv_internal.h"
 #include "sv_ptx.cuh"
 
@@ -589,8 +590,9 @@ cudaError_t launch_d(const LogprobsParams& p, int n_rows, int num_sms, cudaStrea
   // Rows of up to 16 blocks for each of a narrow CTA's warps.
   if (p.vocab <= kLpNarrow / 32 * 16 * kBlock) return launch_e<T, kLpNarrow>(p, n_rows, 1, num_sms, s);
   // CTAs of a row: up to one an SM in all, while each warp has a block of its own.
-  // (1 row of 151936 fp32 with 20 alternatives: 12.9 us with 16, 11.9 with 8, 13.9 with
-  // 4, 26 with 1; 24 rows of 262144 bf16 with 5: 17.9 with 8, 16.2 with 4, 22.7 with 2.)
+  // (1, 2, 4, 8 and 16 of them: 1 row of 151936 fp32 with 20 alternatives 20.3, 15.4, 11.9,
+  // 10.5 and 11.8 us, where the rule takes 8; 24 rows of 262144 bf16 with 5 19.4, 15.3,
+  // 12.2, 14.7 and 30.2, where it takes 4.)
   int cs = 1;
   while (cs < 8 && (int64_t)n_rows * cs * 2 <= num_sms && p.vocab / kBlock >= 2 * cs * (kLpWide / 32)) cs *= 2;
   return launch_e<T, kLpWide>(p, n_rows, cs, num_sms, s);

@@ -8,11 +8,11 @@
 // of up to eight CTAs, which meet at the cluster's barriers: a table's numbers are few
 // (64 rows of 256 pages and 20 thousand pages are 200 KB, in L2), so what bounds
 // them is the chain of dependent loads and barriers, not bytes: with the copy of
-// its pages a fork of 1 row to 8 takes 7.9 us in a graph (one CTA; 14 with eight),
+// its pages a fork of 1 row to 8 takes 8.2 us in a graph (one CTA),
 // of 64 rows of up to 4096 positions 15.4 (eight CTAs).  The copy of the pages is a
 // kernel of its own behind the plan, queued before that has ended; it is bound by
 // memory: 64 x 4096 positions of two layers compacted, 180 MB read and as many
-// written, in 74 us (76.5 with loads that stay in L2), 0.71 of the copy rate.
+// written, in 73 us (76.5 with loads that stay in L2), 0.71 of the copy rate.
 //
 // Free pages are found by rank: a warp counts those of its range of pages with
 // ballots, the counts are summed over warps and CTAs, and a second look at the
@@ -388,7 +388,10 @@ cudaError_t prepare_pages() {
   return cudaFuncSetAttribute(k_fork<kPgWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ForkShared));
 }
 
-// Whether one CTA is enough: it looks through entries and pages 1024 at a time.
+// Whether one CTA is enough: it looks through entries and pages 1024 at a time, where
+// eight have their barriers.  (Entries and pages, then us of a plan in a graph with one CTA
+// and with eight: fork 585 6.1 and 7.8, 3292 8.1 and 9.0, 6740 10.9 and 9.5, 14000 18.2
+// and 10.1; compact 567 4.7 and 6.3, 3274 5.8 and 7.2, 6706 7.6 and 7.4, 13934 11.2 and 8.1.)
 static bool small_plan(const PageTable& t) { return (int64_t)t.n_seq * t.width + t.n_pages <= 4 * kPgThreads; }
 
 // A kernel that may be launched while the one ahead of it ends (it waits for that

@@ -42,8 +42,9 @@
 // Measured (32 / 8 heads of 128 unless noted; the whole call, then this kernel): bf16,
 // 64 x 1 behind 32768: 78 and 45 us, 134 MB of prefix, of which the products alone are
 // 24 us of a tensor pipe (three of 64 cycles for each 16 columns: S, P's two terms);
-// e4m3, 32 x 1 behind 8192: 38 and 17; 64 x 4 behind 4096, 28 / 4 heads: 59; bf16, d 256,
-// 13 x 2, 8 / 1 heads: 34.  Neither memory nor the pipe is full (52 % for bf16, 37 % for
+// e4m3, 32 x 1 behind 8192: 38 and 17; 64 x 4 behind 4096, 28 / 4 heads: 58; bf16, d 256,
+// 13 x 2, 8 / 1 heads: 35; d 64, 64 x 1 behind 8192, 4 / 2 heads: 25, bf16 33.  Where every
+// chunk is uneven: e4m3, 32 x 1 behind 8192: 50; d 64: 32.  Neither memory nor the pipe is full (52 % for bf16, 37 % for
 // e4m3): a stream's step is a chain, S, softmax, P V, and two of them overlap; the
 // softmax's warps issue an instruction every other cycle.
 #pragma once
@@ -294,8 +295,8 @@ struct ShSmem {
   // A whole warp's wait.  Its lanes go on together: one that fell behind, and that
   // nothing else waits for, could otherwise look for a phase when the next but one
   // has already come, which has the same parity.
-  //   False: it gave up, or another warp of the CTA has; from then on no wait of the CTA
-  // lasts.  Loads, widening and multiplies then end.  The softmax's warps go on, over
+  //   False: it gave up, or another warp of the CTA has; from then on a wait of the CTA
+  // lasts two looks (4 us each).  Loads, widening and multiplies then end.  The softmax's warps go on, over
   // scores that mean nothing, to the end of the run: they meet at named barriers,
   // which have no limit, so one of them that left would hold up those that did not
   // fail.  What they write lies in the CTA's own partials.

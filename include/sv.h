@@ -472,8 +472,14 @@ int sv_attend(const sv_kv_pool* pool, const sv_row_batch* rows, int n_q_heads, c
  * the prefix limits it for its group); the rest, and sequences in no group, are
  * attended to as by sv_attend.  No window.
  *   A row's result may differ from sv_attend's in the last bits, and with the
- * number of rows and groups of the call and their lengths, since the prefix is cut
- * between CTAs by the call's whole work.  The same call gives the same bits.
+ * number of rows and groups of the call, their lengths and the width of the tables,
+ * since the prefix is cut between CTAs by the call's whole work.  The same call gives
+ * the same bits.
+ *   Calls for which sv_attend may have to read no more than 56 MB are sv_attend's, which
+ * is faster there, in its bits.  That goes by the rows and by the positions that the
+ * tables reach (the lengths are on the device): tables should be cut for the call's
+ * longest sequence.  8 sequences behind 512 positions take 10 us with tables of 39 pages
+ * and 24 with tables of 2048, where sv_attend takes 10 with either.
  * Over a bf16 cache values beyond 2^96 may come out as infinities.
  *   SV_TEST_SHARED_WAIT_NS=n (environment, read by the first call on a device):
  * failure-detection test only.  A wait inside the kernel of the shared positions gives
