@@ -44,9 +44,10 @@
 // 24 us of a tensor pipe (three of 64 cycles for each 16 columns: S, P's two terms);
 // e4m3, 32 x 1 behind 8192: 38 and 17; 64 x 4 behind 4096, 28 / 4 heads: 58; bf16, d 256,
 // 13 x 2, 8 / 1 heads: 35; d 64, 64 x 1 behind 8192, 4 / 2 heads: 25, bf16 33.  Where every
-// chunk is uneven: e4m3, 32 x 1 behind 8192: 50; d 64: 32.  Neither memory nor the pipe is full (52 % for bf16, 37 % for
-// e4m3): a stream's step is a chain, S, softmax, P V, and two of them overlap; the
-// softmax's warps issue an instruction every other cycle.
+// chunk is uneven: e4m3, 32 x 1 behind 8192: 50; d 64: 32.
+//   Neither memory nor the pipe is full (52 % for bf16, 37 % for e4m3): a stream's step
+// is a chain, S, softmax, P V, and two of them overlap; the softmax's warps issue an
+// instruction every other cycle.
 #pragma once
 #include "paged_dev.cuh"
 #include "shared.h"
@@ -296,10 +297,10 @@ struct ShSmem {
   // nothing else waits for, could otherwise look for a phase when the next but one
   // has already come, which has the same parity.
   //   False: it gave up, or another warp of the CTA has; from then on a wait of the CTA
-  // lasts two looks (4 us each).  Loads, widening and multiplies then end.  The softmax's warps go on, over
-  // scores that mean nothing, to the end of the run: they meet at named barriers,
-  // which have no limit, so one of them that left would hold up those that did not
-  // fail.  What they write lies in the CTA's own partials.
+  // lasts two looks (4 us each).  Loads, widening and multiplies then end.  The softmax's
+  // warps go on, over scores that mean nothing, to the end of the run: they meet at
+  // named barriers, which have no limit, so one of them that left would hold up those
+  // that did not fail.  What they write lies in the CTA's own partials.
   __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity) const {
     bool ok = mbar_try_wait(b, parity);
     if (!ok) {
